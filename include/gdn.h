@@ -71,7 +71,8 @@ typedef enum gdn_status {
     GDN_ERR_UNSUPPORTED = 5, /* valid request the library does not implement */
     GDN_ERR_CUDA = 6,        /* a CUDA runtime call failed (message has detail) */
     GDN_ERR_TIMEOUT = 7,     /* a bounded device-side wait gave up */
-    GDN_ERR_WORKSPACE = 8    /* workspace missing, misaligned or too small */
+    GDN_ERR_WORKSPACE = 8,   /* workspace missing, misaligned or too small */
+    GDN_ERR_CAPACITY = 9     /* a page pool or block table has too few entries */
 } gdn_status;
 
 typedef enum gdn_dtype { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype;
@@ -504,6 +505,140 @@ GDN_API int gdn_gated_delta_dense_ws(const void *q, const void *k, const void *v
                                      float *state_fin, int B, int S, int H, int n,
                                      int gate_per_channel, float scale, int dtype,
                                      void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Softmax-attention layers beside the delta layers
+ * ------------------------------------------------
+ * Stacks that use gated-delta layers interleave them with softmax-attention
+ * layers over the same packed tokens.  Four calls serve those layers, in the
+ * order of a serving step:
+ *   gdn_page_plan         pages, slots and positions of the step's new tokens
+ *   gdn_qk_norm_rope      q/k norm, position rotation, k and v into the cache
+ *   gdn_attention_varlen  causal attention of whole packed prompts
+ *   gdn_attention_paged   attention of new tokens over the paged cache
+ * (no counterpart on the source pages).  Shared conventions:
+ * - H query heads and HKV key-value heads of D channels (H % HKV == 0, 1 <= D
+ *   <= 256); query head h reads key-value head h / (H / HKV).
+ * - offsets [B+1] as above, except that offsets[B] may be less than N: rows
+ *   from offsets[B] on belong to no sequence and their outputs are not written
+ *   (a step of fixed size with fewer tokens).
+ * - A paged cache holds num_pages pages of page_size tokens, [num_pages,
+ *   page_size, HKV, D] T each for k and v.  Token t of sequence b is in slot
+ *   block_table[b, t / page_size] * page_size + t % page_size.
+ * - A malformed sequence (bad offsets, a negative length, more tokens than its
+ *   block table or max_q covers) is skipped: its outputs are not written.
+ */
+
+/*
+ * gdn_page_plan - block tables, slots and positions of a step's new tokens.
+ *
+ *   new_lens     [B] int32   new tokens of each request (>= 0)
+ *   cached_lens  [B] int32   tokens already in its pages (>= 0)
+ *   block_table  [B, max_pages] int32, updated in place: request b owns the
+ *                first ceil(cached/page_size) entries and receives pages for
+ *                the rest of its cached + new tokens
+ *   free_pages   [n_free] int32   pages to hand out, in this order
+ *   cursor       [1] int32   entries of free_pages already handed out
+ *   offsets      [B+1] int32 exclusive prefix sum of new_lens
+ *   kv_lens      [B] int32   cached + new; may equal cached_lens
+ *   positions    [N] int32   position of each new token in its sequence
+ *   slots        [N] int32   cache slot of each new token
+ *   cursor_out   [1] int32   cursor after this step; may equal cursor
+ *   status       [1] int32   GDN_OK, or GDN_ERR_SHAPE (a negative length or
+ *                cursor), GDN_ERR_OFFSETS (more than N new tokens), or
+ *                GDN_ERR_CAPACITY (block table or free pages too short)
+ * Requests receive pages in index order.  N is the capacity of positions and
+ * slots: entries past the last new token get position 0 and slot -1.  When
+ * status is not GDN_OK nothing is handed out: offsets are all 0, slots -1,
+ * kv_lens equals cached_lens, block_table and the cursor keep their values.
+ * Requires 1 <= B <= 8192, N >= 0, 1 <= page_size <= 65536, max_pages >= 1,
+ * n_free >= 0.
+ */
+GDN_API int gdn_page_plan(const int32_t *new_lens, const int32_t *cached_lens,
+                          int32_t *block_table, const int32_t *free_pages, const int32_t *cursor,
+                          int32_t *offsets, int32_t *kv_lens, int32_t *positions, int32_t *slots,
+                          int32_t *cursor_out, int32_t *status, int B, int N, int page_size,
+                          int max_pages, int n_free, void *stream);
+
+/* Which channels gdn_qk_norm_rope rotates together. */
+typedef enum gdn_rope_style {
+    GDN_ROPE_HALF = 0, /* channels (i, i + R/2), i < R/2 */
+    GDN_ROPE_PAIRS = 1 /* channels (2i, 2i + 1), i < R/2 */
+} gdn_rope_style;
+
+/*
+ * gdn_qk_norm_rope - per-head RMS norm of q and k, position rotation, and the
+ * write of k and v into a paged cache, in one pass over the projection's rows.
+ *
+ *   qkv        N rows of (H + 2 HKV) D channels T (q heads, k heads, v heads),
+ *              row_stride elements apart (row_stride >= (H + 2 HKV) D)
+ *   q_weight, k_weight [D] f32, or NULL for no norm of q / k
+ *   cos_sin    [max_pos, R] f32: row p holds the R/2 cosines, then the R/2
+ *              sines, of position p (NULL when R == 0)
+ *   positions  [N] int32 (NULL when R == 0)
+ *   slots      [N] int32 or NULL: with slots, k and v rows also go to slot
+ *              slots[t] of k_cache and v_cache [num_slots, HKV, D] T (a slot
+ *              outside [0, num_slots) writes nothing)
+ *   q_out      [N, H, D] T;  k_out [N, HKV, D] T or NULL (not written)
+ * Per head x: y = x w / sqrt(mean(x^2) + eps) (y = x without a weight), then
+ * the first R channels are rotated in pairs (a, b) -> (a c - b s, b c + a s).
+ * Computed in fp32 and rounded once to T.  A token whose position is outside
+ * [0, max_pos) is skipped.  Tokens with the same slot leave one of their rows.
+ * Requires R even, 0 <= R <= D.
+ */
+GDN_API int gdn_qk_norm_rope(const void *qkv, int64_t row_stride, const float *q_weight,
+                             const float *k_weight, float eps, const float *cos_sin,
+                             const int32_t *positions, int max_pos, const int32_t *slots,
+                             void *q_out, void *k_out, void *k_cache, void *v_cache,
+                             int num_slots, int N, int H, int HKV, int D, int R, int style,
+                             int dtype, void *stream);
+
+/*
+ * gdn_attention_varlen - causal softmax attention of packed sequences:
+ *   out_i = sum_{j <= i} p_ij v_j,  p_i = softmax_j(scale q_i . k_j)
+ * over the tokens j of i's own sequence.
+ *   q          N rows of H heads of D T, q_stride elements apart (>= H D)
+ *   k, v       N rows of HKV heads of D T, k_stride, v_stride apart (>= HKV D)
+ *              (so all three may be columns of one projection)
+ *   offsets    [B+1] int32
+ *   out        [N, H, D] T
+ *   scale      0 means 1/sqrt(D)
+ * Scores and sums in fp32; bf16 probabilities are rounded to bf16 before the
+ * product with v on the tensor-core path.  A non-finite v_j reaches only the
+ * queries that see token j.
+ */
+GDN_API int gdn_attention_varlen(const void *q, const void *k, const void *v,
+                                 const int32_t *offsets, void *out, int B, int N, int H, int HKV,
+                                 int D, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                 float scale, int dtype, void *stream);
+
+/*
+ * gdn_attention_paged - causal softmax attention of new tokens over a paged
+ * cache that already holds their keys and values.  Sequence b has the n =
+ * offsets[b+1] - offsets[b] rows of q and kv_lens[b] cached tokens, the new
+ * ones last: row i sees keys [0, kv_lens[b] - n + i].  A row that sees no key
+ * (kv_lens[b] < n) gives 0.
+ *   q            N rows of H heads of D T, q_stride elements apart (>= H D)
+ *   k_cache, v_cache [num_pages, page_size, HKV, D] T
+ *   block_table  [B, max_pages] int32; entries outside [0, num_pages) that a
+ *                sequence reaches are read as zero keys and values
+ *   kv_lens      [B] int32, offsets [B+1] int32
+ *   max_q        upper bound of n (1 for a decode step)
+ *   out          [N, H, D] T;  scale as above
+ *   workspace    device, 256-byte aligned, at least
+ *                gdn_attention_paged_workspace_bytes() bytes, not shared with a
+ *                concurrently running call; its contents need no initialisation
+ */
+GDN_API int gdn_attention_paged(const void *q, const void *k_cache, const void *v_cache,
+                                const int32_t *block_table, const int32_t *kv_lens,
+                                const int32_t *offsets, void *out, int B, int N, int H, int HKV,
+                                int D, int page_size, int max_pages, int num_pages, int max_q,
+                                int64_t q_stride, float scale, int dtype, void *workspace,
+                                size_t ws_bytes, void *stream);
+
+/* Workspace bytes of gdn_attention_paged (0 on bad input). */
+GDN_API size_t gdn_attention_paged_workspace_bytes(int B, int N, int H, int HKV, int D,
+                                                   int max_q);
 
 #ifdef __cplusplus
 }

@@ -33,7 +33,9 @@ __all__ = [
     "gdn_gated_delta_dense",
     "gdn_set_segment_min_len", "gdn_segment_min_len", "gdn_segment_plan",
     "gdn_selftest_wait_timeout", "gdn_dense_workspace_bytes", "gdn_workspace_bytes_ex",
-    "gdn_dense_workspace_bytes_ex",
+    "gdn_dense_workspace_bytes_ex", "gdn_page_plan", "gdn_qk_norm_rope", "gdn_attention_varlen",
+    "gdn_attention_paged", "gdn_attention_paged_workspace_bytes", "GDN_ROPE_HALF",
+    "GDN_ROPE_PAIRS",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -47,9 +49,10 @@ GDN_OPT_GATE_PER_CHANNEL = 64  # a [N, H, K]: one decay per key channel
 RULE_OPTS = {"gated_delta": 0, "delta": GDN_OPT_NO_DECAY, "gated": GDN_OPT_NO_RETRIEVE,
              "linear": GDN_OPT_NO_DECAY | GDN_OPT_NO_RETRIEVE}
 GDN_ACT_NONE, GDN_ACT_SILU = 0, 1
+GDN_ROPE_HALF, GDN_ROPE_PAIRS = 0, 1
 STATUS_NAMES = {0: "GDN_OK", 1: "GDN_ERR_NULL", 2: "GDN_ERR_SHAPE", 3: "GDN_ERR_OVERFLOW",
                 4: "GDN_ERR_OFFSETS", 5: "GDN_ERR_UNSUPPORTED", 6: "GDN_ERR_CUDA",
-                7: "GDN_ERR_TIMEOUT", 8: "GDN_ERR_WORKSPACE"}
+                7: "GDN_ERR_TIMEOUT", 8: "GDN_ERR_WORKSPACE", 9: "GDN_ERR_CAPACITY"}
 
 _lib = None
 
@@ -75,6 +78,7 @@ def load_library():
                           "`python -m varlen_gated_delta_gb300.build` (no CPU fallback exists)")
     lib = ctypes.CDLL(path)
     vp, i, f, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    i64 = ctypes.c_int64
     lib.gdn_version.restype = i
     lib.gdn_last_error.restype = ctypes.c_char_p
     lib.gdn_conv1d_varlen.argtypes = [vp] * 7 + [i] * 7 + [vp]
@@ -113,10 +117,17 @@ def load_library():
     lib.gdn_dense_workspace_bytes_ex.restype = ctypes.c_size_t
     lib.gdn_set_kernel_events.argtypes = [i, vp, vp]
     lib.gdn_set_kernel_events.restype = i
+    lib.gdn_page_plan.argtypes = [vp] * 11 + [i] * 5 + [vp]
+    lib.gdn_qk_norm_rope.argtypes = [vp, i64, vp, vp, f, vp, vp, i] + [vp] * 5 + [i] * 8 + [vp]
+    lib.gdn_attention_varlen.argtypes = [vp] * 5 + [i] * 5 + [i64] * 3 + [f, i, vp]
+    lib.gdn_attention_paged.argtypes = [vp] * 7 + [i] * 9 + [i64, f, i, vp, sz, vp]
+    lib.gdn_attention_paged_workspace_bytes.argtypes = [i] * 6
+    lib.gdn_attention_paged_workspace_bytes.restype = sz
     for name in ("gdn_conv1d_varlen", "gdn_prepare", "gdn_delta_varlen", "gdn_layer_varlen",
                  "gdn_workspace_status", "gdn_set_chunk_min_len", "gdn_conv1d_varlen_capture",
                  "gdn_delta_varlen_capture", "gdn_layer_varlen_capture", "gdn_prepare_ex",
-                 "gdn_delta_varlen_ex", "gdn_layer_varlen_ex", "gdn_gated_delta_dense"):
+                 "gdn_delta_varlen_ex", "gdn_layer_varlen_ex", "gdn_gated_delta_dense",
+                 "gdn_page_plan", "gdn_qk_norm_rope", "gdn_attention_varlen", "gdn_attention_paged"):
         getattr(lib, name).restype = i
     _lib = lib
     return lib
@@ -629,3 +640,141 @@ def gdn_segment_plan(offsets, H: int, V: int, sm_count: int) -> list:
     if rc < 0:
         _check(-rc)
     return [int(counts[i]) for i in range(B)]
+
+
+# ------------------------------------------------------------------ softmax-attention layers
+
+def _rows(t, name, dtype, shape, device):
+    """Pointer and token stride of a tensor of rows: contiguous but for the token stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or t.device != device:
+        raise GdnError(6, f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise GdnError(2, f"{name} has dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise GdnError(2, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    width = 1
+    for n, stride in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
+        if n != 1 and stride != width:
+            raise GdnError(2, f"{name} must be contiguous within a token")
+        width *= n
+    stride = t.stride(0) if shape[0] > 1 else width
+    if stride < width:
+        raise GdnError(2, f"{name} has token stride {stride}, below its row width {width}")
+    return (t.data_ptr() if t.numel() > 0 else None), stride
+
+
+def gdn_page_plan(new_lens, cached_lens, block_table, free_pages, *, page_size, N, cursor,
+                  offsets=None, kv_lens=None, positions=None, slots=None, cursor_out=None,
+                  status=None):
+    """Block tables, slots and positions of a step's new tokens, on the device.
+
+    Request b has ``cached_lens[b]`` tokens and gets ``new_lens[b]`` more; pages come
+    from ``free_pages`` at ``cursor`` [1] on and enter ``block_table`` [B, max_pages]
+    in place.  ``N`` is the capacity of ``positions`` and ``slots`` (slots past the last
+    new token are -1).  ``kv_lens`` may be ``cached_lens`` and ``cursor_out`` may be
+    ``cursor``.  Returns (offsets [B+1], kv_lens [B], positions [N], slots [N],
+    cursor_out [1], status [1]), all int32; when status[0] != 0 nothing was handed out."""
+    lib = load_library()
+    B, max_pages = block_table.shape
+    dev, i32 = block_table.device, torch.int32
+    new = lambda t, n: torch.empty((n,), dtype=i32, device=dev) if t is None else t
+    offsets, kv_lens, cursor_out = new(offsets, B + 1), new(kv_lens, B), new(cursor_out, 1)
+    positions, slots, status = new(positions, N), new(slots, N), new(status, 1)
+    args = [_ptr(new_lens, "new_lens", i32, (B,), dev), _ptr(cached_lens, "cached_lens", i32, (B,), dev),
+            _ptr(block_table, "block_table", i32, (B, max_pages), dev),
+            _ptr(free_pages, "free_pages", i32, (free_pages.numel(),), dev),
+            _ptr(cursor, "cursor", i32, (1,), dev), _ptr(offsets, "offsets", i32, (B + 1,), dev),
+            _ptr(kv_lens, "kv_lens", i32, (B,), dev), _ptr(positions, "positions", i32, (N,), dev),
+            _ptr(slots, "slots", i32, (N,), dev), _ptr(cursor_out, "cursor_out", i32, (1,), dev),
+            _ptr(status, "status", i32, (1,), dev)]
+    _check(lib.gdn_page_plan(*args, B, N, int(page_size), max_pages, free_pages.numel(),
+                             _stream(dev)))
+    return offsets, kv_lens, positions, slots, cursor_out, status
+
+
+def gdn_qk_norm_rope(qkv, cos_sin=None, positions=None, *, H, HKV, D, q_weight=None, k_weight=None,
+                     eps=1e-6, style=GDN_ROPE_HALF, q=None, k=None, slots=None, k_cache=None,
+                     v_cache=None):
+    """Per-head RMS norm of q and k, position rotation, k and v into the paged cache.
+
+    ``qkv`` [N, (H + 2 HKV) D] (any row stride); ``cos_sin`` [max_pos, R] f32 holds R/2
+    cosines then R/2 sines per position (None: no rotation).  With ``slots`` [N] the k and
+    v rows go to ``k_cache`` / ``v_cache`` [num_pages, page_size, HKV, D], and a packed k
+    is only written when a tensor ``k`` is given.  Returns (q [N,H,D], k [N,HKV,D] or None)."""
+    lib = load_library()
+    N = qkv.shape[0]
+    T, dev, f32, i32 = qkv.dtype, qkv.device, torch.float32, torch.int32
+    base, stride = _rows(qkv, "qkv", T, (N, (H + 2 * HKV) * D), dev)
+    q = torch.empty((N, H, D), dtype=T, device=dev) if q is None else q
+    if k is None and slots is None:
+        k = torch.empty((N, HKV, D), dtype=T, device=dev)
+    max_pos, R = (0, 0) if cos_sin is None else cos_sin.shape
+    num_slots = 0
+    kc = vc = None
+    if slots is not None:
+        if k_cache is None or v_cache is None:
+            raise GdnError(1, "slots need k_cache and v_cache")
+        cshape = (*k_cache.shape[:2], HKV, D)
+        num_slots = cshape[0] * cshape[1]
+        kc, vc = _ptr(k_cache, "k_cache", T, cshape, dev), _ptr(v_cache, "v_cache", T, cshape, dev)
+    _check(lib.gdn_qk_norm_rope(
+        base, stride, _ptr(q_weight, "q_weight", f32, (D,), dev), _ptr(k_weight, "k_weight", f32, (D,), dev),
+        float(eps), _ptr(cos_sin, "cos_sin", f32, (max_pos, R), dev),
+        _ptr(positions, "positions", i32, (N,), dev), max_pos, _ptr(slots, "slots", i32, (N,), dev),
+        _ptr(q, "q", T, (N, H, D), dev), _ptr(k, "k", T, (N, HKV, D), dev), kc, vc, num_slots, N, H,
+        HKV, D, R, int(style), _dtype_code(qkv), _stream(dev)))
+    return q, k
+
+
+def gdn_attention_varlen(q, k, v, offsets, *, scale=0.0, out=None):
+    """Causal softmax attention of packed sequences with grouped heads.
+
+    q [N, H, D], k and v [N, HKV, D] (any token stride), offsets [B+1] int32.
+    Returns out [N, H, D]; rows from offsets[B] on are not written."""
+    lib = load_library()
+    N, H, D = q.shape
+    HKV = k.shape[1]
+    T, dev = q.dtype, q.device
+    B = offsets.numel() - 1
+    out = torch.empty((N, H, D), dtype=T, device=dev) if out is None else out
+    (qp, qs), (kp, ks), (vp, vs) = (_rows(q, "q", T, (N, H, D), dev), _rows(k, "k", T, (N, HKV, D), dev),
+                                    _rows(v, "v", T, (N, HKV, D), dev))
+    _check(lib.gdn_attention_varlen(qp, kp, vp, _ptr(offsets, "offsets", torch.int32, (B + 1,), dev),
+                                    _ptr(out, "out", T, (N, H, D), dev), B, N, H, HKV, D, qs, ks, vs,
+                                    float(scale), _dtype_code(q), _stream(dev)))
+    return out
+
+
+def gdn_attention_paged_workspace_bytes(B, N, H, HKV, D, max_q) -> int:
+    return int(load_library().gdn_attention_paged_workspace_bytes(B, N, H, HKV, D, max_q))
+
+
+def gdn_attention_paged(q, k_cache, v_cache, block_table, kv_lens, offsets, *, max_q, scale=0.0,
+                        out=None, workspace=None):
+    """Causal softmax attention of new tokens over a paged cache that holds them.
+
+    q [N, H, D] (any token stride); k_cache, v_cache [num_pages, page_size, HKV, D];
+    block_table [B, max_pages], kv_lens [B], offsets [B+1] int32.  Row i of a sequence
+    with n rows sees its keys [0, kv_len - n + i].  ``max_q`` bounds n (1 for decode).
+    ``workspace`` is an optional uint8 tensor of gdn_attention_paged_workspace_bytes
+    bytes.  Returns out [N, H, D]; rows from offsets[B] on are not written."""
+    lib = load_library()
+    N, H, D = q.shape
+    pages, page_size, HKV, _ = k_cache.shape
+    B, max_pages = block_table.shape
+    T, dev, i32 = q.dtype, q.device, torch.int32
+    out = torch.empty((N, H, D), dtype=T, device=dev) if out is None else out
+    qp, qs = _rows(q, "q", T, (N, H, D), dev)
+    if workspace is None:
+        need = gdn_attention_paged_workspace_bytes(B, N, H, HKV, D, int(max_q))
+        workspace = torch.empty((max(need, 256),), dtype=torch.uint8, device=dev)
+    cshape = (pages, page_size, HKV, D)
+    _check(lib.gdn_attention_paged(
+        qp, _ptr(k_cache, "k_cache", T, cshape, dev), _ptr(v_cache, "v_cache", T, cshape, dev),
+        _ptr(block_table, "block_table", i32, (B, max_pages), dev), _ptr(kv_lens, "kv_lens", i32, (B,), dev),
+        _ptr(offsets, "offsets", i32, (B + 1,), dev), _ptr(out, "out", T, (N, H, D), dev), B, N, H, HKV, D,
+        page_size, max_pages, pages, int(max_q), qs, float(scale), _dtype_code(q),
+        _ptr(workspace, "workspace", torch.uint8, None, dev), workspace.numel(), _stream(dev)))
+    return out

@@ -1,0 +1,171 @@
+// page_plan.cu - gdn_page_plan: block tables, slots and positions of a step's
+// new tokens, built on the GPU from request lengths.
+//
+// With ps tokens to a page, request b owns ceil(cached_b / ps) pages and needs
+// ceil((cached_b + new_b) / ps); the difference comes from the free list at
+// cursor + (the needs of requests before b).  So the whole plan is two prefix
+// sums over the requests and one independent computation per new token and per
+// new page.  There is next to nothing to read or write: the call is bound by
+// its launch and by the latency of the scan.  One launch of one thread-block
+// cluster: every CTA computes both prefix sums for itself in shared memory (B
+// is small), and the CTAs share the tokens and pages.  The cluster barrier
+// between the last read and the first write is what lets cursor_out and
+// kv_lens be the inputs' own buffers.
+#include <cooperative_groups.h>
+
+#include "common.cuh"
+#include "serving.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 1024;
+
+// Exclusive sums of (a, c) over the block; returns the block's totals in ta, tc.
+__device__ __forceinline__ void block_scan2(long long &a, long long &c, long long &ta,
+                                            long long &tc, long long (*s_sum)[2]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long a0 = a, c0 = c;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long xa = __shfl_up_sync(0xffffffffu, a, d), xc = __shfl_up_sync(0xffffffffu, c, d);
+        if (lane >= d) a += xa, c += xc;
+    }
+    if (lane == 31) s_sum[warp][0] = a, s_sum[warp][1] = c;
+    __syncthreads();
+    if (warp == 0) {
+        long long wa = s_sum[lane][0], wc = s_sum[lane][1];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long xa = __shfl_up_sync(0xffffffffu, wa, d), xc = __shfl_up_sync(0xffffffffu, wc, d);
+            if (lane >= d) wa += xa, wc += xc;
+        }
+        s_sum[lane][0] = wa, s_sum[lane][1] = wc;
+    }
+    __syncthreads();
+    ta = s_sum[31][0], tc = s_sum[31][1];
+    a += (warp ? s_sum[warp - 1][0] : 0) - a0;
+    c += (warp ? s_sum[warp - 1][1] : 0) - c0;
+}
+
+// Largest b with ofs[b] <= x (ofs[0] = 0 <= x < ofs[B]).
+__device__ __forceinline__ int find(const int *ofs, int B, int x) {
+    int lo = 0, hi = B - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (ofs[mid] <= x) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kThreads) page_plan_kernel(const PagePlan p) {
+    extern __shared__ int s_plan[];
+    int *s_ofs = s_plan, *s_page = s_plan + p.B + 1, *s_cached = s_plan + 2 * (p.B + 1);
+    __shared__ long long s_sum[32][2];
+    __shared__ int s_bad;
+    const int tid = threadIdx.x;
+    const int rank = blockIdx.x, ranks = gridDim.x;  // the grid is one cluster
+    const int ps = p.page_size;
+    pdl_wait_primary();
+
+    if (tid == 0) s_bad = 0;
+    __syncthreads();
+    const int cursor = __ldg(p.cursor);
+    const int per = (p.B + kThreads - 1) / kThreads;
+    const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+    long long tok = 0, pages = 0;
+    int bad = 0;  // the most severe finding: shape, then capacity
+    for (int b = b0; b < b1; ++b) {
+        int n = __ldg(p.new_lens + b), c = __ldg(p.cached_lens + b);
+        if (n < 0 || c < 0) {
+            bad = GDN_ERR_SHAPE;
+            n = 0, c = max(c, 0);
+        }
+        if ((long long)c + n > (long long)p.max_pages * ps || (long long)c + n > INT32_MAX - ps)
+            bad = bad ? bad : GDN_ERR_CAPACITY;
+        s_cached[b] = c;
+        tok += n;
+        pages += ((long long)c + n + ps - 1) / ps - ((long long)c + ps - 1) / ps;
+    }
+    if (bad) atomicMax(&s_bad, bad == GDN_ERR_SHAPE ? 2 : 1);
+    long long all_tok, all_pages;
+    block_scan2(tok, pages, all_tok, all_pages, s_sum);
+    int status = s_bad == 2 || cursor < 0      ? GDN_ERR_SHAPE
+                 : all_tok > p.N               ? GDN_ERR_OFFSETS
+                 : s_bad || cursor + all_pages > p.n_free ? GDN_ERR_CAPACITY
+                                               : GDN_OK;
+    const bool ok = status == GDN_OK;
+    if (ok)
+        for (int b = b0; b < b1; ++b) {  // every sum fits: at most N tokens and n_free pages
+            const int n = __ldg(p.new_lens + b), c = s_cached[b];
+            s_ofs[b] = (int)tok;
+            s_page[b] = (int)pages;
+            tok += n;
+            pages += (c + n + ps - 1) / ps - (c + ps - 1) / ps;
+        }
+    const int total = ok ? (int)all_tok : 0, fresh = ok ? (int)all_pages : 0;
+    if (tid == 0) s_ofs[p.B] = total, s_page[p.B] = fresh;
+    // Every CTA has read what the outputs may overwrite (and this CTA's sums are in place).
+    cooperative_groups::this_cluster().sync();
+
+    const int t0 = rank * kThreads + tid, step = ranks * kThreads;
+    for (int b = t0; b <= p.B; b += step) {
+        p.offsets[b] = ok ? s_ofs[b] : 0;
+        if (b < p.B && (ok || p.kv_lens != p.cached_lens))
+            p.kv_lens[b] = ok ? s_cached[b] + s_ofs[b + 1] - s_ofs[b] : __ldg(p.cached_lens + b);
+    }
+    if (t0 == 0) {
+        *p.cursor_out = cursor + fresh;
+        *p.status = status;
+    }
+    for (int i = t0; i < fresh; i += step) {
+        const int b = find(s_page, p.B, i), old = (s_cached[b] + ps - 1) / ps;
+        p.block_table[(size_t)b * p.max_pages + old + i - s_page[b]] = __ldg(p.free_pages + cursor + i);
+    }
+    for (int t = t0; t < p.N; t += step) {
+        int pos = 0, slot = -1;
+        if (t < total) {
+            const int b = find(s_ofs, p.B, t);
+            const int c = s_cached[b], old = (c + ps - 1) / ps;
+            pos = c + t - s_ofs[b];
+            const int page = pos / ps;
+            // a page of before this step, or the one that the loop above hands out
+            const long long id = page < old ? p.block_table[(size_t)b * p.max_pages + page]
+                                            : __ldg(p.free_pages + cursor + s_page[b] + page - old);
+            const long long at = id * ps + pos % ps;
+            slot = id < 0 || at > INT32_MAX ? -1 : (int)at;
+        }
+        p.positions[t] = pos;
+        p.slots[t] = slot;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_page_plan(const PagePlan &p, cudaStream_t s) {
+    static std::atomic<uint64_t> attr_set{0};
+    const size_t smem = 3 * ((size_t)p.B + 1) * 4;
+    cudaError_t e = once_per_device(attr_set, [] {
+        return cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    3 * (kPagePlanMaxB + 1) * 4);
+    });
+    if (e != cudaSuccess) return e;
+    const int ctas = p.N + p.B > 2 * kThreads ? 8 : 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, page_plan_kernel, p);
+    note_launch();
+    return e;
+}
+
+}  // namespace gdn
