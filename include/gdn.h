@@ -636,6 +636,13 @@ GDN_API int gdn_attention_paged(const void *q, const void *k_cache, const void *
                                 int64_t q_stride, float scale, int dtype, void *workspace,
                                 size_t ws_bytes, void *stream);
 
+/*
+ * Synchronises `stream` and returns GDN_ERR_TIMEOUT when a bounded device-side
+ * wait of an attention call has given up on the current device since the last
+ * query (the outputs of that call are then incomplete), else GDN_OK.
+ */
+GDN_API int gdn_attention_status(void *stream);
+
 /* Workspace bytes of gdn_attention_paged (0 on bad input). */
 GDN_API size_t gdn_attention_paged_workspace_bytes(int B, int N, int H, int HKV, int D,
                                                    int max_q);

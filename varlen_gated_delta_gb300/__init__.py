@@ -34,7 +34,8 @@ __all__ = [
     "gdn_set_segment_min_len", "gdn_segment_min_len", "gdn_segment_plan",
     "gdn_selftest_wait_timeout", "gdn_dense_workspace_bytes", "gdn_workspace_bytes_ex",
     "gdn_dense_workspace_bytes_ex", "gdn_page_plan", "gdn_qk_norm_rope", "gdn_attention_varlen",
-    "gdn_attention_paged", "gdn_attention_paged_workspace_bytes", "GDN_ROPE_HALF",
+    "gdn_attention_paged", "gdn_attention_paged_workspace_bytes", "gdn_attention_status",
+    "GDN_ROPE_HALF",
     "GDN_ROPE_PAIRS",
 ]
 
@@ -121,6 +122,8 @@ def load_library():
     lib.gdn_qk_norm_rope.argtypes = [vp, i64, vp, vp, f, vp, vp, i] + [vp] * 5 + [i] * 8 + [vp]
     lib.gdn_attention_varlen.argtypes = [vp] * 5 + [i] * 5 + [i64] * 3 + [f, i, vp]
     lib.gdn_attention_paged.argtypes = [vp] * 7 + [i] * 9 + [i64, f, i, vp, sz, vp]
+    lib.gdn_attention_status.argtypes = [vp]
+    lib.gdn_attention_status.restype = i
     lib.gdn_attention_paged_workspace_bytes.argtypes = [i] * 6
     lib.gdn_attention_paged_workspace_bytes.restype = sz
     for name in ("gdn_conv1d_varlen", "gdn_prepare", "gdn_delta_varlen", "gdn_layer_varlen",
@@ -745,6 +748,13 @@ def gdn_attention_varlen(q, k, v, offsets, *, scale=0.0, out=None):
                                     _ptr(out, "out", T, (N, H, D), dev), B, N, H, HKV, D, qs, ks, vs,
                                     float(scale), _dtype_code(q), _stream(dev)))
     return out
+
+
+def gdn_attention_status(device=None) -> None:
+    """Synchronise the current stream; raise GdnError (GDN_ERR_TIMEOUT) when a wait inside an
+    attention kernel gave up since the last query."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    _check(load_library().gdn_attention_status(_stream(dev)))
 
 
 def gdn_attention_paged_workspace_bytes(B, N, H, HKV, D, max_q) -> int:

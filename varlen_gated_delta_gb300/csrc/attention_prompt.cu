@@ -1,0 +1,669 @@
+// attention_prompt.cu - causal softmax attention of prompts and prompt slices on
+// the tcgen05 tensor cores (bf16).
+//
+// For a tile of 128 queries of one head, over tiles of BN keys:
+//   S = Q K^T,  m' = max(m, rowmax S),  P = 2^(c (S - m')),  l' = l 2^(c (m - m')) + rowsum P,
+//   O' = O 2^(c (m - m')) + P V,   c = scale log2(e),   out = O / l.
+// 4 D operations for each visible (query, key): bound by the tensor cores, with
+// the exponentials (one a score, on the special-function units) close behind.
+//
+// A CTA holds a pair of query tiles (one for D > 128) and every key tile it
+// loads serves both.  Warp roles: one softmax warpgroup per query tile (a thread
+// owns a row, so row maxima and sums need no exchange), one TMA warp, one MMA
+// warp, two warps that mend V tiles.  S and O live in tensor memory; P replaces
+// S in place as bf16 (A operand of the second product, read from tensor
+// memory).  The MMA warp alternates the tiles, so one tile's softmax runs under
+// the other's products; with a single query tile S is double buffered instead
+// and the products of the next key tile run under the softmax.
+//
+// O is rescaled only when the row maximum has grown by more than 2^8 since the
+// last time: P then stays below 2^8, with the same relative precision, and
+// the division by l at the end uses the same reference.
+//
+// V rows that some query of the tile must not see (later tokens, other
+// sequences, stale cache slots) meet P = 0, and 0 * inf would be NaN: in the few
+// key tiles that have masked scores, warps 2 and 3 of the last warpgroup replace
+// non-finite V values by 0 before the product, and, if there were any, the
+// epilogue adds them to the rows that do see them.
+//
+// Persistent CTAs, one per SM, take (query tile pair, head) items in a fixed
+// interleaved order, longest first by the tile's place in its sequence; heads
+// are innermost, so that the heads of a group read the same keys out of L2.
+#include <cmath>
+
+#include "attention.cuh"
+#include "sm100.cuh"
+
+namespace gdn {
+namespace {
+
+using namespace sm100;
+
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr int kMaxBins = 4096;  // bins of the longest-first order
+constexpr float kLazy = 8.f;    // growth of the row maximum (log2) that O waits for
+
+// Set when a bounded wait of an attention kernel has given up.
+__device__ int g_attention_timeout;
+
+template <int DP>
+struct Cfg {
+    static constexpr int NQ = DP > 128 ? 1 : 2;    // query tiles of a CTA
+    static constexpr int BN = DP > 128 ? 64 : 128; // keys of a tile
+    static constexpr int TM = NQ * 128;            // queries of an item
+    static constexpr int NB = DP / 64;             // 64-channel blocks (128 swizzled bytes a row)
+    static constexpr int QBYTES = 128 * DP * 2, SLOT = BN * DP * 2;
+    static constexpr int SLOTS = 4;
+    static constexpr int THREADS = NQ * 128 + 128;
+    // tensor memory: two score buffers, then O of each query tile
+    static constexpr int COL_O = 2 * BN;
+};
+
+struct PromptParams {
+    Attn a;
+    int G;
+    int box_rows;   // key rows of a TMA box
+    int bins, bin_shift;
+    int min_rows;   // sequences with at most this many (query, head of a group) rows are not ours
+    float c;        // |scale| log2(e)
+    int negate;     // scale < 0
+};
+
+// Warp-wide mbarrier wait that gives up, for the whole warp, after kWaitLimitNs
+// or when another role has.
+__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    const uint32_t addr = smem_u32(bar);
+    bool ok = mbar_try_wait(addr, parity);
+    if (!ok) {
+        const uint64_t t0 = global_timer_ns();
+        bool stop = false;
+        while (!ok && !stop) {
+#pragma unroll 1
+            for (int i = 0; i < 32 && !ok; ++i) ok = mbar_try_wait(addr, parity);
+            if (!ok && *abort) stop = true;
+            if (!ok && !stop && global_timer_ns() - t0 > kWaitLimitNs) {
+                *abort = 1;
+                atomicExch(&g_attention_timeout, 1);
+                stop = true;
+            }
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int x,
+                                            int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+// D[tmem] (+)= A[tmem] B^T, issued by one thread.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// One item: TM queries from row0 on of one head of sequence b.
+struct Item {
+    int b, h, start, len, kv, row0;
+    int n[2];     // key tiles of each query tile (0: no rows, or none that sees a key)
+    int tiles;    // key tiles loaded
+    int fix;      // first key tile with masked scores
+};
+
+template <int DP>
+__device__ __forceinline__ int seq_tiles(const PromptParams &p, int b) {
+    int start, len, kv;
+    if (!attn_seq(p.a, b, start, len, kv) || (long)len * p.G <= p.min_rows) return 0;
+    return (len + Cfg<DP>::TM - 1) / Cfg<DP>::TM;
+}
+
+// Tiles of a sequence of n tiles that fall into bin.
+__device__ __forceinline__ int in_bin(int n, int bin, int shift) {
+    return max(0, min(n - (bin << shift), 1 << shift));
+}
+
+// Warp-wide: item `idx`; false past the last one.  suffix[i]: tiles in bins >= i.
+template <int DP>
+__device__ __forceinline__ bool get_item(const PromptParams &p, const int *suffix, long idx, Item &it) {
+    using C = Cfg<DP>;
+    const int lane = threadIdx.x & 31;
+    const long total = (long)suffix[0] * p.a.H;
+    if (idx >= total) return false;
+    int rank = (int)(idx / p.a.H);
+    it.h = (int)(idx % p.a.H);
+    int lo = 0, hi = p.bins - 1;  // the bin with suffix[bin + 1] <= rank < suffix[bin]
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (suffix[mid] > rank) lo = mid;
+        else hi = mid - 1;
+    }
+    rank -= suffix[lo + 1];
+    for (int b0 = 0; b0 < p.a.B; b0 += 32) {
+        const int n = b0 + lane < p.a.B ? in_bin(seq_tiles<DP>(p, b0 + lane), lo, p.bin_shift) : 0;
+        int sum = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, sum, d);
+            if (lane >= d) sum += x;
+        }
+        const int all = __shfl_sync(0xffffffffu, sum, 31);
+        if (rank >= all) {
+            rank -= all;
+            continue;
+        }
+        const int at = __ffs(__ballot_sync(0xffffffffu, rank < sum)) - 1;
+        const int before = __shfl_sync(0xffffffffu, sum - n, at), mine = __shfl_sync(0xffffffffu, n, at);
+        it.b = b0 + at;
+        const int level = (lo << p.bin_shift) + mine - 1 - (rank - before);
+        attn_seq(p.a, it.b, it.start, it.len, it.kv);
+        it.row0 = level * C::TM;
+        it.tiles = 0;
+        const int shift = it.kv - it.len;
+#pragma unroll
+        for (int t = 0; t < C::NQ; ++t) {
+            const int r = it.row0 + t * 128, rows = min(128, it.len - r);
+            const int most = rows > 0 ? min(it.kv, shift + r + rows) : 0;
+            it.n[t] = most > 0 ? (most + C::BN - 1) / C::BN : 0;
+            it.tiles = max(it.tiles, it.n[t]);
+        }
+        it.fix = max(0, shift + it.row0 + 1) / C::BN;
+        return true;
+    }
+    return false;
+}
+
+template <int DP>
+__global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
+    attn_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                       const __grid_constant__ CUtensorMap vmap, const PromptParams p) {
+    using C = Cfg<DP>;
+    constexpr int NQ = C::NQ, BN = C::BN, NB = C::NB, SLOTS = C::SLOTS;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    unsigned char *sq = smem, *ring = smem + NQ * C::QBYTES;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(ring + SLOTS * C::SLOT);
+    uint64_t *full = bars, *empty = full + SLOTS, *q_full = empty + SLOTS, *q_empty = q_full + 2,
+             *s_full = q_empty + 2, *p_full = s_full + 2, *o_done = p_full + 2, *v_fixed = o_done + 2;
+    int *s_bad = reinterpret_cast<int *>(v_fixed + SLOTS);  // item that had non-finite masked V values
+    int *s_abort = s_bad + 4;
+    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(s_abort + 1);
+    int *suffix = s_abort + 4;  // [bins + 1]
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int kTmaWarp = NQ * 4, kMmaWarp = NQ * 4 + 1;
+
+    if (tid == 0) {
+        for (int i = 0; i < SLOTS; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, i & 1 ? 3 : 1);  // V (odd) slots: the products and both mending warps
+            mbar_init(v_fixed + i, 64);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(q_full + i, 1), mbar_init(q_empty + i, 1);
+            mbar_init(s_full + i, 1), mbar_init(p_full + i, 128), mbar_init(o_done + i, 1);
+        }
+        fence_mbar_init();
+        for (int i = 0; i < 4; ++i) s_bad[i] = 0;
+        *s_abort = 0;
+        tma_prefetch_desc(&qmap), tma_prefetch_desc(&kmap), tma_prefetch_desc(&vmap);
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(s_tmem, 512);
+        tmem_relinquish();
+    }
+    pdl_wait_primary();
+    // tiles per bin of places in a sequence, then suffix sums
+    for (int i = tid; i <= p.bins; i += C::THREADS) suffix[i] = 0;
+    __syncthreads();
+    for (int b = tid; b < p.a.B; b += C::THREADS) {
+        const int n = seq_tiles<DP>(p, b);
+        for (int i = 0; (i << p.bin_shift) < n && i < p.bins; ++i) atomicAdd(suffix + i, in_bin(n, i, p.bin_shift));
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int carry = 0;
+        for (int i0 = (p.bins - 1) & ~31; i0 >= 0; i0 -= 32) {
+            int x = i0 + lane < p.bins ? suffix[i0 + lane] : 0;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int y = __shfl_down_sync(0xffffffffu, x, d);
+                if (lane + d < 32) x += y;
+            }
+            x += carry;
+            if (i0 + lane < p.bins) suffix[i0 + lane] = x;
+            carry = __shfl_sync(0xffffffffu, x, 0);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+    volatile int *abort = s_abort;
+    const long step = gridDim.x;
+    Item it;
+    it.n[1] = 0;
+
+    if (warp == kTmaWarp) {
+        // ---------------------------------------------------------------- loads
+        uint32_t slot = 0, phase = 0, q_phase = 0;
+        const int boxes = BN / p.box_rows;  // boxes of a 64-channel block of a key tile
+        auto next_slot = [&]() {
+            if (++slot == SLOTS) slot = 0, phase ^= 1;
+        };
+        for (long idx = blockIdx.x; get_item<DP>(p, suffix, idx, it); idx += step) {
+#pragma unroll
+            for (int t = 0; t < NQ; ++t) {
+                if (it.n[t] == 0) continue;
+                if (!wait_or_abort(q_empty + t, ((q_phase >> t) & 1) ^ 1, abort)) goto done;
+                q_phase ^= 1u << t;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(q_full + t, C::QBYTES);
+                    for (int c = 0; c < NB; ++c)
+                        tma_load_3d(sq + t * C::QBYTES + c * 128 * 128, &qmap, q_full + t, c * 64, it.h,
+                                    it.start + it.row0 + t * 128);
+                }
+            }
+            for (int j = 0; j < it.tiles; ++j) {
+                // the row of this lane's box (packed keys: one box, at its token)
+                int row = it.start + j * BN;
+                if (p.a.block_table != nullptr && lane < boxes) {
+                    const int key = j * BN + lane * p.box_rows;
+                    const int page = key < it.kv ? __ldg(p.a.block_table + (size_t)it.b * p.a.max_pages + key / p.a.page_size) : -1;
+                    // outside the cache: past its end, where the load gives zeros
+                    row = page < 0 || page >= p.a.num_pages ? p.a.num_pages * p.a.page_size
+                                                            : page * p.a.page_size + key % p.a.page_size;
+                }
+                for (int kv = 0; kv < 2; ++kv) {
+                    if (!wait_or_abort(empty + slot, phase ^ 1, abort)) goto done;
+                    if (lane == 0) mbar_arrive_expect_tx(full + slot, C::SLOT);
+                    __syncwarp();
+                    if (lane < boxes) {
+                        unsigned char *dst = ring + slot * C::SLOT + lane * p.box_rows * 128;
+                        for (int c = 0; c < NB; ++c)
+                            tma_load_3d(dst + c * BN * 128, kv ? &vmap : &kmap, full + slot, c * 64, it.h / p.G, row);
+                    }
+                    next_slot();
+                }
+            }
+        }
+    } else if (warp == kMmaWarp) {
+        // ---------------------------------------------------------------- products
+        const uint32_t id_s = idesc_bf16(128, BN, false, false) | (p.negate ? 1u << 13 : 0u);
+        const uint32_t id_o = idesc_bf16(128, DP, false, true);
+        const uint32_t q_addr = smem_u32(sq), r_addr = smem_u32(ring);
+        uint32_t q_phase = 0, p_phase = 0, fix_phase = 0;  // one bit a barrier
+        uint32_t seq = 0;  // loads before this item: K_j is load seq + 2 j, V_j the one after it
+        auto slot_of = [&](uint32_t s) { return s % SLOTS; };
+        auto phase_of = [&](uint32_t s) { return (s / SLOTS) & 1; };
+        for (long idx = blockIdx.x; get_item<DP>(p, suffix, idx, it); idx += step) {
+            // S[buf] = Q[t] K_j^T
+            auto scores = [&](int t, int buf, int j) {
+                if (lane == 0) {
+                    const uint32_t kb = r_addr + slot_of(seq + 2 * j) * C::SLOT, qb = q_addr + t * C::QBYTES;
+#pragma unroll
+                    for (int ks = 0; ks < DP / 16; ++ks)
+                        mma_bf16(tmem + buf * BN, sdesc_sw128(qb + (ks >> 2) * 128 * 128 + (ks & 3) * 32, 16, 1024),
+                                 sdesc_sw128(kb + (ks >> 2) * BN * 128 + (ks & 3) * 32, 16, 1024), id_s, ks > 0);
+                    mma_commit(s_full + buf);
+                }
+                __syncwarp();
+            };
+            auto wait_slot = [&](uint32_t s) {
+                const bool ok = wait_or_abort(full + slot_of(s), phase_of(s), abort);
+                tc_fence_after();
+                return ok;
+            };
+            auto free_slot = [&](uint32_t s) {
+                if (lane == 0) mma_commit(empty + slot_of(s));
+                __syncwarp();
+            };
+            auto free_q = [&](int t) {
+                if (lane == 0) mma_commit(q_empty + t);
+                __syncwarp();
+            };
+            // O[t] (+)= P[buf] V_j
+            auto values = [&](int t, int buf, int j) {
+                if (!wait_or_abort(p_full + buf, (p_phase >> buf) & 1, abort)) return false;
+                p_phase ^= 1u << buf;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t vb = r_addr + slot_of(seq + 2 * j + 1) * C::SLOT;
+#pragma unroll
+                    for (int ks = 0; ks < BN / 16; ++ks)
+                        mma_bf16_ts(tmem + C::COL_O + t * DP, tmem + buf * BN + ks * 8,
+                                    sdesc_sw128(vb + ks * 2048, BN * 128, 1024), id_o, j > 0 || ks > 0);
+                    mma_commit(o_done + t);
+                }
+                __syncwarp();
+                return true;
+            };
+            if (it.tiles > 0) {
+                if (!wait_slot(seq)) goto done;
+#pragma unroll
+                for (int t = 0; t < NQ; ++t) {
+                    if (it.n[t] == 0) continue;
+                    if (!wait_or_abort(q_full + t, (q_phase >> t) & 1, abort)) goto done;
+                    q_phase ^= 1u << t;
+                    tc_fence_after();
+                    scores(t, t, 0);
+                    if (it.n[t] == 1) free_q(t);
+                }
+                free_slot(seq);
+            }
+            for (int j = 0; j < it.tiles; ++j) {
+                const bool more = j + 1 < it.tiles;
+                if (NQ == 1 && more) {  // the next scores run under this tile's softmax
+                    if (!wait_slot(seq + 2 * (j + 1))) goto done;
+                    scores(0, (j + 1) & 1, j + 1);
+                    if (j + 2 == it.n[0]) free_q(0);
+                    free_slot(seq + 2 * (j + 1));
+                }
+                if (!wait_slot(seq + 2 * j + 1)) goto done;
+                if (j >= it.fix) {
+                    const uint32_t v = slot_of(seq + 2 * j + 1);
+                    if (!wait_or_abort(v_fixed + v, (fix_phase >> v) & 1, abort)) goto done;
+                    fix_phase ^= 1u << v;
+                    tc_fence_after();
+                }
+                if (NQ == 1) {
+                    if (!values(0, j & 1, j)) goto done;
+                } else {
+                    bool have_k = false;
+#pragma unroll
+                    for (int t = 0; t < NQ; ++t) {
+                        if (j >= it.n[t]) continue;
+                        if (!values(t, t, j)) goto done;
+                        if (j + 1 < it.n[t]) {
+                            if (!have_k && !wait_slot(seq + 2 * (j + 1))) goto done;
+                            have_k = true;
+                            scores(t, t, j + 1);
+                            if (j + 2 == it.n[t]) free_q(t);
+                        }
+                    }
+                    if (more) free_slot(seq + 2 * (j + 1));
+                }
+                free_slot(seq + 2 * j + 1);
+            }
+            seq += 2 * it.tiles;
+        }
+    } else if (warp > kMmaWarp) {
+        // ---------------------------------------------------------------- non-finite V values
+        uint32_t seq = 0, n_item = 0;
+        const int ft = (warp - kMmaWarp - 1) * 32 + lane;
+        for (long idx = blockIdx.x; get_item<DP>(p, suffix, idx, it); idx += step, ++n_item) {
+            for (int j = 0; j < it.tiles; ++j) {
+                // every V tile is waited for, so that no phase of its barrier goes by unseen
+                const uint32_t s = seq + 2 * j + 1;
+                if (!wait_or_abort(full + s % SLOTS, (s / SLOTS) & 1, abort)) goto done;
+                if (lane == 0) mbar_arrive(empty + s % SLOTS);
+                if (j < it.fix) continue;
+                uint4 *tile = reinterpret_cast<uint4 *>(ring + (s % SLOTS) * C::SLOT);
+                bool bad = false;
+#pragma unroll 4
+                for (int i = ft; i < C::SLOT / 16; i += 64) {
+                    uint4 x = tile[i];
+                    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                    bool hit = false;
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        const bool lo = (w[z] & 0x7f80u) == 0x7f80u, hi = (w[z] & 0x7f800000u) == 0x7f800000u;
+                        hit |= lo | hi;
+                        w[z] &= (lo ? 0xffff0000u : 0xffffffffu) & (hi ? 0x0000ffffu : 0xffffffffu);
+                    }
+                    if (hit) tile[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                    bad |= hit;
+                }
+                if (bad) s_bad[n_item & 3] = (int)n_item + 1;
+                fence_async_smem();
+                mbar_arrive(v_fixed + s % SLOTS);
+            }
+            seq += 2 * it.tiles;
+        }
+    } else {
+        // ---------------------------------------------------------------- softmax of query tile t
+        const int t = warp >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t o_col = lanes + C::COL_O + t * DP;
+        uint32_t s_phase = 0, o_count = 0, n_item = 0;
+        for (long idx = blockIdx.x; get_item<DP>(p, suffix, idx, it); idx += step, ++n_item) {
+            const int shift = it.kv - it.len, r = it.row0 + t * 128 + row;
+            const int n = NQ == 2 && t ? it.n[1] : it.n[0];
+            const int least = shift + it.row0 + t * 128 + 1;  // keys that the tile's first row sees
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; j < n; ++j) {
+                const int buf = NQ == 2 ? t : j & 1;
+                if (!wait_or_abort(s_full + buf, (s_phase >> buf) & 1, abort)) goto done;
+                s_phase ^= 1u << buf;
+                tc_fence_after();
+                const uint32_t s_col = lanes + buf * BN;
+                uint32_t x[BN / 32][32];
+#pragma unroll
+                for (int c = 0; c < BN / 32; ++c) tmem_ld32(s_col + c * 32, x[c]);
+                tmem_wait_ld();
+                if ((j + 1) * BN > least) {  // some row does not see all of these keys
+                    const int seen = shift + r + 1 - j * BN;
+#pragma unroll
+                    for (int c = 0; c < BN / 32; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (c * 32 + i >= seen) x[c][i] = 0xff800000u;
+                }
+                float mx[4] = {m, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < BN / 32; ++c)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(x[c][i]));
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                if (m == -INFINITY) m = top;  // nothing summed yet
+                // rescale O when the reference of some row of the warp has to move
+                const bool move = (top - m) * p.c > kLazy;
+                if (__any_sync(0xffffffffu, move)) {
+                    const float f = move ? exp2_fast((m - top) * p.c) : 1.f;
+                    if (move) m = top, l *= f;
+                    // (j > 0 here: a first tile sets m itself)
+                    if (!wait_or_abort(o_done + t, (o_count - 1) & 1, abort)) goto done;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < DP; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(o_col + c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tmem_st32(o_col + c, o);
+                    }
+                    tmem_wait_st();
+                }
+                const float mc = m == -INFINITY ? 0.f : -m * p.c;
+                float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int c = 0; c < BN / 64; ++c) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float2 s2 = make_float2(__uint_as_float(x[2 * c + (i >> 4)][(2 * i) & 31]),
+                                                      __uint_as_float(x[2 * c + (i >> 4)][(2 * i + 1) & 31]));
+                        float2 e = __ffma2_rn(s2, make_float2(p.c, p.c), make_float2(mc, mc));
+                        e.x = exp2_fast(e.x), e.y = exp2_fast(e.y);
+                        sum = __fadd2_rn(sum, e);
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(e.x, e.y);
+                        pk[i] = *reinterpret_cast<const uint32_t *>(&h);
+                    }
+                    tmem_st32(s_col + c * 32, pk);
+                }
+                l += sum.x + sum.y;
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(p_full + buf);
+                ++o_count;
+            }
+            // ---- out = O / l
+            // (the scores of the last key tile were committed after the products before the last
+            // one but, with a single query tile, not after that one: wait for both in turn)
+            if (n > 0) {
+                if (NQ == 1 && n > 1 && !wait_or_abort(o_done + t, o_count & 1, abort)) goto done;
+                if (!wait_or_abort(o_done + t, (o_count - 1) & 1, abort)) goto done;
+                tc_fence_after();
+            }
+            const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (NaN stays)
+            const bool bad = n > 0 && s_bad[n_item & 3] == (int)n_item + 1;
+            const int seen = min(it.kv, shift + r + 1);
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) +
+                                 ((size_t)(it.start + r) * p.a.H + it.h) * p.a.D;
+#pragma unroll 1
+            for (int c = 0; c < DP; c += 32) {
+                __syncwarp();
+                uint32_t o[32];
+                if (n > 0) {
+                    tmem_ld32(o_col + c, o);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = 0u;
+                }
+                float f[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) f[i] = l != 0.f ? __uint_as_float(o[i]) * inv : 0.f;
+                if (bad && r < it.len)
+                    for (int j = it.fix * BN; j < seen; ++j) {
+                        const long at = attn_key_row(p.a, it.b, it.start, j, p.a.vs);
+                        if (at < 0) continue;
+                        const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(p.a.v) + at + (long)(it.h / p.G) * p.a.D;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (c + i < p.a.D) {
+                                const float y = __bfloat162float(v[c + i]);
+                                if (!isfinite(y)) f[i] += y;
+                            }
+                    }
+                if (r < it.len)
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8)
+                        if (c + i < p.a.D) {
+                            Vec16<__nv_bfloat16> w;
+#pragma unroll
+                            for (int z = 0; z < 8; ++z) w.v[z] = __float2bfloat16_rn(f[i + z]);
+                            *reinterpret_cast<uint4 *>(out + c + i) = w.u;
+                        }
+            }
+            tc_fence_before();  // the next item's products follow this tile's next arrival
+        }
+    }
+done:
+    __syncwarp();
+    if (warp == kTmaWarp && *abort)  // copies in flight land before the CTA's memory goes
+        for (int i = 0; i < SLOTS; ++i) mbar_wait(full + i, 0, 1000000), mbar_wait(full + i, 1, 1000000);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static EncodeTiledFn fn = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            ptr = nullptr;
+        return reinterpret_cast<EncodeTiledFn>(ptr);
+    }();
+    return fn;
+}
+
+// [rows][heads][D] bf16 with `stride` elements a row, read in boxes of 64 channels
+// of one head and box_rows rows; channels past D and rows past the end read as 0.
+bool encode_rows(CUtensorMap *map, const void *base, long rows, int heads, int D, long stride, int box_rows) {
+    const EncodeTiledFn enc = encode_fn();
+    if (enc == nullptr) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows}, es[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DP>
+cudaError_t launch(const Attn &a, int min_rows, cudaStream_t s) {
+    using C = Cfg<DP>;
+    PromptParams p{};
+    p.a = a;
+    p.G = a.H / a.HKV;
+    p.min_rows = min_rows;
+    p.c = std::fmax(std::fabs(a.scale) * kLog2e, 1e-30f);
+    p.negate = a.scale < 0.f;
+    const bool paged = a.block_table != nullptr;
+    p.box_rows = C::BN;
+    if (paged) while (a.page_size % p.box_rows != 0) p.box_rows /= 2;
+    const long levels = ((long)a.max_q + C::TM - 1) / C::TM;
+    while (((levels + (1L << p.bin_shift) - 1) >> p.bin_shift) > kMaxBins) ++p.bin_shift;
+    p.bins = (int)((levels + (1L << p.bin_shift) - 1) >> p.bin_shift);
+    const long kv_rows = paged ? (long)a.num_pages * a.page_size : a.N;
+    CUtensorMap qm, km, vm;
+    if (!encode_rows(&qm, a.q, a.N, a.H, a.D, a.qs, 128) ||
+        !encode_rows(&km, a.k, kv_rows, a.HKV, a.D, a.ks, p.box_rows) ||
+        !encode_rows(&vm, a.v, kv_rows, a.HKV, a.D, a.vs, p.box_rows))
+        return cudaErrorInvalidValue;
+    static std::atomic<uint64_t> attr_set{0};
+    constexpr size_t kFixed = (size_t)C::NQ * C::QBYTES + C::SLOTS * C::SLOT + 256 + 1024;
+    cudaError_t e = once_per_device(attr_set, [] {
+        return cudaFuncSetAttribute(attn_prompt_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)(kFixed + (kMaxBins + 1) * 4));
+    });
+    if (e != cudaSuccess) return e;
+    int dev = 0, sms = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const long items = ((long)a.N / C::TM + a.B) * a.H;
+    const long grid = items < sms ? items : sms;
+    e = launch_kernel(attn_prompt_kernel<DP>, dim3((unsigned)grid), dim3(C::THREADS), kFixed + (p.bins + 1) * 4, s,
+                      false, qm, km, vm, p);
+    note_launch();
+    return e;
+}
+
+}  // namespace
+
+int attention_timeouts(cudaStream_t s, cudaError_t *e) {
+    int seen = 0;
+    const int none = 0;
+    *e = cudaMemcpyFromSymbolAsync(&seen, g_attention_timeout, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+    if (*e == cudaSuccess) *e = cudaStreamSynchronize(s);
+    if (*e == cudaSuccess && seen)
+        *e = cudaMemcpyToSymbolAsync(g_attention_timeout, &none, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+    if (*e == cudaSuccess && seen) *e = cudaStreamSynchronize(s);
+    return seen;
+}
+
+bool attention_prompt_supported(const Attn &a, int dtype) {
+    const bool paged = a.block_table != nullptr;
+    return dtype == GDN_BF16 && rows_aligned(a.q, a.qs, a.D, 2) && rows_aligned(a.k, a.ks, a.D, 2) &&
+           rows_aligned(a.v, a.vs, a.D, 2) && ((uintptr_t)a.out & 15) == 0 && (!paged || a.page_size % 8 == 0);
+}
+
+cudaError_t launch_attention_prompt(const Attn &a, int min_rows, cudaStream_t s) {
+    if (a.D <= 64) return launch<64>(a, min_rows, s);
+    if (a.D <= 128) return launch<128>(a, min_rows, s);
+    return launch<256>(a, min_rows, s);
+}
+
+}  // namespace gdn

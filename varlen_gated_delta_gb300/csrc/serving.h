@@ -57,4 +57,12 @@ inline bool rows_aligned(const void *base, long stride_elems, int D, size_t esz)
 size_t attention_simt_part_floats(int B, int N, int H, int HKV, int D);
 cudaError_t launch_attention_simt(const Attn &a, int dtype, cudaStream_t s);
 
+// bf16 on the tensor cores, one item per (query tile pair, head): prompts and
+// prompt slices.  Sequences of at most min_rows (query, head of a group) rows
+// are left out.
+bool attention_prompt_supported(const Attn &a, int dtype);
+cudaError_t launch_attention_prompt(const Attn &a, int min_rows, cudaStream_t s);
+// Synchronises s; non-zero when a bounded wait gave up since the last call.
+int attention_timeouts(cudaStream_t s, cudaError_t *e);
+
 }  // namespace gdn

@@ -115,7 +115,18 @@ int gdn_attention_varlen(const void *q, const void *k, const void *v, const int3
     a.max_q = N;
     a.qs = (long)q_stride, a.ks = (long)k_stride, a.vs = (long)v_stride;
     a.scale = scale == 0.f ? 1.f / std::sqrt((float)D) : scale;
-    return launched(launch_attention_simt(a, dtype, static_cast<cudaStream_t>(stream)), "attention kernel launch");
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return launched(attention_prompt_supported(a, dtype) ? launch_attention_prompt(a, 0, st)
+                                                         : launch_attention_simt(a, dtype, st),
+                    "attention kernel launch");
+}
+
+int gdn_attention_status(void *stream) {
+    set_error(GDN_OK, "%s", "");
+    cudaError_t e;
+    const int late = attention_timeouts(static_cast<cudaStream_t>(stream), &e);
+    if (e != cudaSuccess) return launched(e, "attention status");
+    return late ? set_error(GDN_ERR_TIMEOUT, "a wait inside an attention kernel gave up") : GDN_OK;
 }
 
 size_t gdn_attention_paged_workspace_bytes(int B, int N, int H, int HKV, int D, int max_q) {
@@ -158,7 +169,10 @@ int gdn_attention_paged(const void *q, const void *k_cache, const void *v_cache,
     a.scale = scale == 0.f ? 1.f / std::sqrt((float)D) : scale;
     a.part = static_cast<float *>(workspace);
     a.part_floats = attention_simt_part_floats(B, N, H, HKV, D);
-    return launched(launch_attention_simt(a, dtype, static_cast<cudaStream_t>(stream)), "paged attention kernel launch");
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool prompt = (long)a.max_q * (H / HKV) > 64 && attention_prompt_supported(a, dtype);
+    return launched(prompt ? launch_attention_prompt(a, 0, st) : launch_attention_simt(a, dtype, st),
+                    "paged attention kernel launch");
 }
 
 }  // extern "C"
