@@ -1,0 +1,523 @@
+// attention_split.cu - attention of few new tokens over long paged histories
+// (decode steps, drafted tokens): bf16, at most 64 (token, head of a group) rows
+// to a sequence and key-value head.
+//
+// Every key and value is read once for all rows that share it, and each takes
+// only 4 operations a row and channel: bound by HBM at 4 D bytes a key and
+// key-value head.  So the work is cut by bytes, not by rows: the 64-key tiles of
+// all (sequence, key-value head) pairs form one list, and every CTA takes an
+// equal run of it.  A run may begin and end inside a pair; such a CTA leaves the
+// running maximum m, the sum l and an unscaled output of its part, and a second
+// kernel joins the parts of a pair: with M = max m_i, o = sum o_i 2^(m_i - M) /
+// sum l_i 2^(m_i - M).  Which parts exist follows from the lengths alone, so the
+// result does not depend on timing.
+//
+// Key and value rows stream through a ring of tiles filled by 16-byte cp.async
+// copies, a warp copying 16 keys (their slots are looked up once, by lane).  The
+// products are 16-row mma.sync: with rows this few they are far from binding,
+// and registers hold scores, probabilities and output without the staging that
+// larger tiles need.  With up to 16 rows the four warps share out the keys of a
+// tile, with 32 they form two pairs, with 64 each has its own 16 rows; warps that
+// share rows join at the end of a part through shared memory.
+#include <cmath>
+
+#include "attention.cuh"
+#include "sm100.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kKeys = 64, kThreads = 128;
+constexpr int kMaxCtas = 2 * 160;
+
+struct SplitParams {
+    Attn a;
+    int G;
+    float c;      // |scale| log2(e)
+    int negate;   // scale < 0
+    int2 *spans;  // [B * HKV]: first and last CTA of a pair
+    float *part;  // [2 * CTAs][ROWS * (2 + DP)]
+};
+
+template <int DP, int MT>
+struct Split {
+    static constexpr int ROWS = 16 * MT;       // padded rows of a pair
+    static constexpr int WK = 4 / MT;          // warps that share the keys of a tile
+    static constexpr int KW = kKeys / WK;      // keys of a warp in a tile
+    static constexpr int STAGES = DP > 128 ? 2 : 3;
+    static constexpr int HALF = kKeys * DP * 2;  // bytes of a K (or V) tile
+    // Q rows (bf16) and, at the end of a part, the joined output (fp32, WK > 1)
+    static constexpr int Q_BYTES = ROWS * DP * 2;
+    static constexpr int SUM_BYTES = WK > 1 ? ROWS * DP * 4 : 0;
+    static constexpr bool QREG = DP <= 128;    // Q fragments stay in registers
+    static constexpr int SCRATCH = QREG ? (Q_BYTES > SUM_BYTES ? Q_BYTES : SUM_BYTES) : Q_BYTES + SUM_BYTES;
+    static constexpr int SMEM = STAGES * 2 * HALF + SCRATCH;
+    static constexpr int PART = ROWS * (2 + DP);  // floats of a part: m, l, o
+};
+
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 16 bytes to shared memory, or zeros
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool read) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Byte offset of 16-byte chunk c of row r: chunks of 8 neighbouring rows fall into different banks.
+template <int DP>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+    return (uint32_t)(r * DP * 2 + ((c ^ (r & 7)) << 4));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Key tiles of one key-value head of sequence b; 0: not ours.
+__device__ __forceinline__ int pair_tiles(const SplitParams &p, int rows, int b, int &start, int &len, int &kv) {
+    if (b >= p.a.B || !attn_seq(p.a, b, start, len, kv) || len == 0 || (long)len * p.G > rows) return 0;
+    return kv > 0 ? (kv + kKeys - 1) / kKeys : 1;  // (no keys: one tile that gives zeros)
+}
+
+// A place in the list of tiles.
+struct Cursor {
+    int b, h, tile, tiles, start, len, kv;
+};
+
+template <int DP, int MT>
+__global__ void __launch_bounds__(kThreads) attn_split_kernel(const SplitParams p) {
+    using C = Split<DP, MT>;
+    constexpr int CH = DP / 8, WK = C::WK, KW = C::KW, STAGES = C::STAGES;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ long long s_scan[4];
+    __shared__ long long s_first;
+    __shared__ int s_seq, s_bad;
+    __shared__ float s_ml[4][2][16];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, t4 = lane & 3;
+    const int mt = warp / WK, wk = warp % WK;  // this warp's rows and keys
+    const uint32_t ring = sm100::smem_u32(smem), s_q = ring + STAGES * 2 * C::HALF;
+    float *s_sum = reinterpret_cast<float *>(smem + STAGES * 2 * C::HALF + (C::QREG ? 0 : C::Q_BYTES));
+    const int D = p.a.D, G = p.G, HKV = p.a.HKV;
+    pdl_wait_primary();
+    pdl_launch_dependents();
+
+    // ---- this CTA's run of tiles [u0, u1): threads own neighbouring sequences
+    const int per = (p.a.B + kThreads - 1) / kThreads;
+    long long mine = 0;
+    int start, len, kv;
+    for (int i = 0; i < per; ++i) mine += pair_tiles(p, C::ROWS, tid * per + i, start, len, kv);
+    long long sum = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += x;
+    }
+    if (lane == 31) s_scan[warp] = sum;
+    if (tid == 0) s_seq = -1, s_bad = 0;
+    __syncthreads();
+    long long all = 0;
+    for (int w = 0; w < 4; ++w) {
+        if (w < warp) sum += s_scan[w];
+        all += s_scan[w];
+    }
+    // every CTA that takes part has at least one tile
+    const long long U = all * HKV, ctas = U < gridDim.x ? U : gridDim.x, cta = blockIdx.x;
+    if (cta >= ctas) return;
+    const long long u0 = cta * U / ctas, u1 = (cta + 1) * U / ctas;
+    {
+        long long at = (sum - mine) * HKV;
+        if (u0 >= at && u0 < sum * HKV)
+            for (int i = 0; i < per; ++i) {
+                const long long n = (long long)pair_tiles(p, C::ROWS, tid * per + i, start, len, kv) * HKV;
+                if (u0 < at + n) {
+                    s_seq = tid * per + i, s_first = at;
+                    break;
+                }
+                at += n;
+            }
+    }
+    __syncthreads();
+    Cursor cur;
+    cur.b = s_seq;
+    cur.tiles = pair_tiles(p, C::ROWS, cur.b, cur.start, cur.len, cur.kv);
+    cur.h = (int)((u0 - s_first) / cur.tiles);
+    cur.tile = (int)((u0 - s_first) % cur.tiles);
+    auto advance = [&](Cursor &x) {
+        if (++x.tile < x.tiles) return;
+        x.tile = 0;
+        if (++x.h < HKV) return;
+        x.h = 0;
+        do x.tiles = pair_tiles(p, C::ROWS, ++x.b, x.start, x.len, x.kv);
+        while (x.tiles == 0 && x.b < p.a.B);
+    };
+
+    // ---- copies: warp w brings keys 16 w .. 16 w + 15 of a tile
+    const __nv_bfloat16 *kc = static_cast<const __nv_bfloat16 *>(p.a.k), *vc = static_cast<const __nv_bfloat16 *>(p.a.v);
+    auto fetch = [&](const Cursor &x, int stage) {
+        const int key = x.tile * kKeys + warp * 16 + (lane & 15);
+        long row = -1;
+        if (key < x.kv) row = attn_key_row(p.a, x.b, x.start, key, p.a.ks);
+        const uint32_t kd = ring + stage * 2 * C::HALF, vd = kd + C::HALF;
+        constexpr int RPI = 32 / CH > 0 ? 32 / CH : 1;  // rows a warp copies at a time
+#pragma unroll
+        for (int i = 0; i < 16 / RPI; ++i) {
+            const int r = i * RPI + (CH < 32 ? lane / CH : 0), c = lane % CH;
+            const long at = __shfl_sync(0xffffffffu, row, r);
+            const bool read = at >= 0 && c * 8 < D;
+            const long e = read ? at + (long)x.h * D + c * 8 : 0;
+            copy16(kd + chunk_at<DP>(warp * 16 + r, c), kc + e, read);
+            copy16(vd + chunk_at<DP>(warp * 16 + r, c), vc + e, read);
+        }
+    };
+
+    Cursor ahead = cur;
+    long long u_ahead = u0;
+    for (int i = 0; i < STAGES - 1; ++i) {
+        if (u_ahead < u1) {
+            fetch(ahead, i);
+            ++u_ahead;
+            if (u_ahead < u1) advance(ahead);
+        }
+        copy_commit();
+    }
+
+    uint32_t qf[C::QREG ? DP / 16 : 1][4];
+    float o[DP / 8][4], m[2], l[2];
+    int stage = 0;
+    bool fresh = true;   // the next tile begins a part
+    int first_tile = 0;  // of this part
+    for (long long u = u0; u < u1; ++u) {
+        const int n = cur.len, rows = n * G, shift = cur.kv - n;
+        if (fresh) {
+            fresh = false;
+            first_tile = cur.tile;
+            __syncthreads();  // the last part's use of the scratch is over
+            for (int i = tid; i < C::ROWS * CH; i += kThreads) {
+                const int r = i / CH, c = i % CH;
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (r < rows && c * 8 < D) {
+                    x = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.a.q) +
+                                                              (long)(cur.start + r / G) * p.a.qs + (long)(cur.h * G + r % G) * D + c * 8));
+                    if (p.negate) x.x ^= 0x80008000u, x.y ^= 0x80008000u, x.z ^= 0x80008000u, x.w ^= 0x80008000u;
+                }
+                *reinterpret_cast<uint4 *>(smem + STAGES * 2 * C::HALF + chunk_at<DP>(r, c)) = x;
+            }
+            if (tid == 0) s_bad = 0;
+            __syncthreads();
+            if constexpr (C::QREG)
+#pragma unroll
+                for (int ks = 0; ks < DP / 16; ++ks)
+                    ldmatrix4(s_q + chunk_at<DP>(mt * 16 + (lane & 15), ks * 2 + (lane >> 4)), qf[ks]);
+            m[0] = m[1] = -INFINITY, l[0] = l[1] = 0.f;
+#pragma unroll
+            for (int i = 0; i < DP / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        }
+        copy_wait<STAGES - 2>();
+        __syncthreads();  // the tile is here, and the slot that is filled next is free
+        {
+            const int next = stage == 0 ? STAGES - 1 : stage - 1;
+            if (u_ahead < u1) {
+                fetch(ahead, next);
+                ++u_ahead;
+                if (u_ahead < u1) advance(ahead);
+            }
+            copy_commit();
+        }
+        const uint32_t kd = ring + stage * 2 * C::HALF, vd = kd + C::HALF;
+        const int j0 = cur.tile * kKeys;
+        const bool edge = j0 + kKeys > shift + 1;  // some row does not see the whole tile
+        if (edge && n > 1) {
+            // values that some row must not see: non-finite ones become 0 and join their rows at the end
+            const int r0 = max(0, shift + 1 - j0), r1 = min(kKeys, cur.kv - j0);
+            for (int i = tid; i < max(0, r1 - r0) * CH; i += kThreads) {
+                uint32_t *w = reinterpret_cast<uint32_t *>(smem + stage * 2 * C::HALF + C::HALF + chunk_at<DP>(r0 + i / CH, i % CH));
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    const uint32_t x = w[z];
+                    const bool lo = (x & 0x7f80u) == 0x7f80u, hi = (x & 0x7f800000u) == 0x7f800000u;
+                    if (lo | hi) w[z] = x & (lo ? 0xffff0000u : 0xffffffffu) & (hi ? 0x0000ffffu : 0xffffffffu), s_bad = 1;
+                }
+            }
+            __syncthreads();
+        }
+        // ---- scores of 16 rows and KW keys
+        float s[KW / 8][4];
+#pragma unroll
+        for (int i = 0; i < KW / 8; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < DP / 16; ++ks) {
+            uint32_t qa[4];
+            if constexpr (C::QREG) {
+#pragma unroll
+                for (int z = 0; z < 4; ++z) qa[z] = qf[ks][z];
+            } else {
+                ldmatrix4(s_q + chunk_at<DP>(mt * 16 + (lane & 15), ks * 2 + (lane >> 4)), qa);
+            }
+#pragma unroll
+            for (int i = 0; i < KW / 16; ++i) {
+                uint32_t kb[4];
+                ldmatrix4(kd + chunk_at<DP>(wk * KW + i * 16 + (lane >> 4) * 8 + (lane & 7), ks * 2 + ((lane >> 3) & 1)), kb);
+                mma16816(s[2 * i], qa, kb[0], kb[1]);
+                mma16816(s[2 * i + 1], qa, kb[2], kb[3]);
+            }
+        }
+        // ---- running softmax of rows g and g + 8
+        float mx[2] = {m[0], m[1]};
+        const int rr = mt * 16 + g;
+        const int seen[2] = {shift + rr / G + 1 - j0, shift + (rr + 8) / G + 1 - j0};
+#pragma unroll
+        for (int i = 0; i < KW / 8; ++i)
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                if (edge && wk * KW + i * 8 + t4 * 2 + (z & 1) >= seen[z >> 1]) s[i][z] = -INFINITY;
+                mx[z >> 1] = fmaxf(mx[z >> 1], s[i][z]);
+            }
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            mx[z] = fmaxf(mx[z], __shfl_xor_sync(0xffffffffu, mx[z], 1));
+            mx[z] = fmaxf(mx[z], __shfl_xor_sync(0xffffffffu, mx[z], 2));
+        }
+        if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
+            // (a row that has seen nothing keeps l = o = 0 under any factor but NaN)
+            const float f0 = m[0] == -INFINITY ? 1.f : exp2_fast((m[0] - mx[0]) * p.c);
+            const float f1 = m[1] == -INFINITY ? 1.f : exp2_fast((m[1] - mx[1]) * p.c);
+            l[0] *= f0, l[1] *= f1;
+#pragma unroll
+            for (int i = 0; i < DP / 8; ++i) o[i][0] *= f0, o[i][1] *= f0, o[i][2] *= f1, o[i][3] *= f1;
+            m[0] = mx[0], m[1] = mx[1];
+        }
+        const float b0 = m[0] == -INFINITY ? 0.f : -m[0] * p.c, b1 = m[1] == -INFINITY ? 0.f : -m[1] * p.c;
+#pragma unroll
+        for (int i = 0; i < KW / 8; ++i) {
+            s[i][0] = exp2_fast(fmaf(s[i][0], p.c, b0)), s[i][1] = exp2_fast(fmaf(s[i][1], p.c, b0));
+            s[i][2] = exp2_fast(fmaf(s[i][2], p.c, b1)), s[i][3] = exp2_fast(fmaf(s[i][3], p.c, b1));
+            l[0] += s[i][0] + s[i][1];
+            l[1] += s[i][2] + s[i][3];
+        }
+        // ---- o += P V
+#pragma unroll
+        for (int i = 0; i < KW / 16; ++i) {
+            const uint32_t pa[4] = {pack_bf16(s[2 * i][0], s[2 * i][1]), pack_bf16(s[2 * i][2], s[2 * i][3]),
+                                    pack_bf16(s[2 * i + 1][0], s[2 * i + 1][1]), pack_bf16(s[2 * i + 1][2], s[2 * i + 1][3])};
+#pragma unroll
+            for (int c = 0; c < CH; c += 2) {
+                uint32_t vb[4];
+                ldmatrix4_trans(vd + chunk_at<DP>(wk * KW + i * 16 + (lane & 15), c + (lane >> 4)), vb);
+                mma16816(o[c], pa, vb[0], vb[1]);
+                mma16816(o[c + 1], pa, vb[2], vb[3]);
+            }
+        }
+        stage = stage == STAGES - 1 ? 0 : stage + 1;
+
+        const bool last = cur.tile + 1 == cur.tiles;
+        if (last || u + 1 == u1) {
+            // ---- the part ends: join the warps that share rows, then write the pair or the part
+            fresh = true;
+            const bool whole = last && first_tile == 0;
+            if (last && tid == 0) {
+                const long long pair = u - cur.tile;  // the pair's first tile
+                p.spans[cur.b * HKV + cur.h] = make_int2((int)(((pair + 1) * ctas - 1) / U), (int)cta);
+            }
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                l[z] += __shfl_xor_sync(0xffffffffu, l[z], 1);
+                l[z] += __shfl_xor_sync(0xffffffffu, l[z], 2);
+            }
+            if (WK > 1) {
+                if (t4 == 0) {
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) s_ml[warp][0][g + 8 * z] = m[z], s_ml[warp][1][g + 8 * z] = l[z];
+                }
+                __syncthreads();
+                float f[2];
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    float M = -INFINITY, L = 0.f;
+#pragma unroll
+                    for (int w = 0; w < WK; ++w) M = fmaxf(M, s_ml[mt * WK + w][0][g + 8 * z]);
+#pragma unroll
+                    for (int w = 0; w < WK; ++w) {
+                        const float mw = s_ml[mt * WK + w][0][g + 8 * z], lw = s_ml[mt * WK + w][1][g + 8 * z];
+                        L += mw == -INFINITY ? lw : lw * exp2_fast((mw - M) * p.c);
+                    }
+                    f[z] = m[z] == -INFINITY ? 1.f : exp2_fast((m[z] - M) * p.c);
+                    m[z] = M, l[z] = L;
+                }
+#pragma unroll
+                for (int w = 0; w < WK; ++w) {
+                    if (wk == w) {
+#pragma unroll
+                        for (int i = 0; i < DP / 8; ++i)
+#pragma unroll
+                            for (int z = 0; z < 2; ++z) {
+                                float2 *at = reinterpret_cast<float2 *>(s_sum + (mt * 16 + g + 8 * z) * DP + i * 8 + t4 * 2);
+                                float2 x = make_float2(o[i][2 * z] * f[z], o[i][2 * z + 1] * f[z]);
+                                if (w > 0) x.x += at->x, x.y += at->y;
+                                if (w == WK - 1) o[i][2 * z] = x.x, o[i][2 * z + 1] = x.y;
+                                else *at = x;
+                            }
+                    }
+                    if (w < WK - 1) __syncthreads();
+                }
+            }
+            if (wk == WK - 1) {  // this warp holds the joined rows mt 16 + g, + 8
+                const bool bad = s_bad != 0;
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    const int r = mt * 16 + g + 8 * z;
+                    if (r >= rows) continue;
+                    if (bad) {
+                        const int end = min(cur.kv, shift + r / G + 1);
+                        for (int j = max(first_tile * kKeys, shift + 1); j < min(end, j0 + kKeys); ++j) {
+                            const long at = attn_key_row(p.a, cur.b, cur.start, j, p.a.vs);
+                            if (at < 0) continue;
+#pragma unroll
+                            for (int i = 0; i < DP / 8; ++i)
+#pragma unroll
+                                for (int y = 0; y < 2; ++y) {
+                                    const int d = i * 8 + t4 * 2 + y;
+                                    const float v = d < D ? __bfloat162float(vc[at + (long)cur.h * D + d]) : 0.f;
+                                    if (!isfinite(v)) o[i][2 * z + y] += v;
+                                }
+                        }
+                    }
+                    if (whole) {
+                        const float inv = l[z] > 0.f ? 1.f / l[z] : (l[z] == 0.f ? 0.f : l[z]);  // (NaN stays)
+                        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) +
+                                             ((size_t)(cur.start + r / G) * p.a.H + cur.h * G + r % G) * D;
+#pragma unroll
+                        for (int i = 0; i < DP / 8; ++i)
+                            if (i * 8 < D)
+                                *reinterpret_cast<uint32_t *>(out + i * 8 + t4 * 2) =
+                                    pack_bf16(o[i][2 * z] * inv, o[i][2 * z + 1] * inv);
+                    } else {
+                        // a part that begins its pair is the CTA's last, any other its first
+                        float *part = p.part + (2 * cta + (first_tile == 0)) * C::PART;
+                        if (t4 == 0) part[r] = m[z], part[C::ROWS + r] = l[z];
+                        part += 2 * C::ROWS + r * DP;
+#pragma unroll
+                        for (int i = 0; i < DP / 8; ++i)
+                            *reinterpret_cast<float2 *>(part + i * 8 + t4 * 2) = make_float2(o[i][2 * z], o[i][2 * z + 1]);
+                    }
+                }
+            }
+        }
+        advance(cur);
+    }
+}
+
+// Joins the parts of each pair that several CTAs shared: a block to a (pair, row).
+template <int DP, int MT>
+__global__ void __launch_bounds__(128) attn_split_join_kernel(const SplitParams p) {
+    using C = Split<DP, MT>;
+    const int b = blockIdx.x / p.a.HKV, h = blockIdx.x % p.a.HKV, r = blockIdx.y;
+    pdl_wait_primary();
+    int start, len, kv;
+    if (pair_tiles(p, C::ROWS, b, start, len, kv) == 0 || r >= len * p.G) return;
+    const int2 span = p.spans[blockIdx.x];
+    if (span.x == span.y) return;
+    auto part = [&](int c) { return p.part + (2L * c + (c == span.x)) * C::PART; };
+    float M = -INFINITY, L = 0.f;
+    for (int c = span.x; c <= span.y; ++c) M = fmaxf(M, part(c)[r]);
+    float o[(DP + 127) / 128] = {};
+    for (int c = span.x; c <= span.y; ++c) {
+        const float *x = part(c);
+        const float mc = x[r], f = mc == -INFINITY ? 1.f : exp2_fast((mc - M) * p.c);
+        L += x[C::ROWS + r] * f;
+#pragma unroll
+        for (int i = 0; i < (DP + 127) / 128; ++i)
+            if (i * 128 + threadIdx.x < DP) {
+                const float v = x[2 * C::ROWS + r * DP + i * 128 + threadIdx.x];
+                o[i] += f > 0.f ? v * f : 0.f;  // (a part that counts for nothing may hold inf)
+            }
+    }
+    const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) +
+                         ((size_t)(start + r / p.G) * p.a.H + h * p.G + r % p.G) * p.a.D;
+#pragma unroll
+    for (int i = 0; i < (DP + 127) / 128; ++i) {
+        const int d = i * 128 + threadIdx.x;
+        if (d < p.a.D) out[d] = __float2bfloat16_rn(L != 0.f ? o[i] * inv : 0.f);
+    }
+}
+
+size_t span_bytes(int B, int HKV) { return ((size_t)B * HKV * 8 + 255) & ~size_t(255); }
+
+template <int DP, int MT>
+cudaError_t launch(const Attn &a, void *ws, cudaStream_t s) {
+    using C = Split<DP, MT>;
+    static std::atomic<uint64_t> attr_set{0};
+    cudaError_t e = once_per_device(attr_set, [] {
+        return cudaFuncSetAttribute(attn_split_kernel<DP, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    });
+    if (e != cudaSuccess) return e;
+    SplitParams p{};
+    p.a = a;
+    p.G = a.H / a.HKV;
+    p.c = std::fmax(std::fabs(a.scale) * kLog2e, 1e-30f);
+    p.negate = a.scale < 0.f;
+    p.spans = static_cast<int2 *>(ws);
+    p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + span_bytes(a.B, a.HKV));
+    int dev = 0, sms = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const long slots = (long)sms * (DP > 128 ? 1 : 2);
+    const long most = (long)a.B * a.HKV * (((long)a.max_pages * a.page_size + kKeys - 1) / kKeys);
+    long grid = slots < kMaxCtas ? slots : kMaxCtas;
+    if (most < grid) grid = most;
+    if ((long)a.B * a.HKV > INT32_MAX) return cudaErrorInvalidConfiguration;
+    e = launch_kernel(attn_split_kernel<DP, MT>, dim3((unsigned)grid), dim3(kThreads), C::SMEM, s, false, p);
+    note_launch();
+    if (e != cudaSuccess) return e;
+    const long rows = (long)a.max_q * p.G < C::ROWS ? (long)a.max_q * p.G : C::ROWS;
+    e = launch_kernel(attn_split_join_kernel<DP, MT>, dim3((unsigned)(a.B * a.HKV), (unsigned)rows), dim3(128), 0, s,
+                      true, p);
+    note_launch();
+    return e;
+}
+
+template <int DP>
+cudaError_t launch_rows(const Attn &a, void *ws, cudaStream_t s) {
+    const long rows = (long)a.max_q * (a.H / a.HKV);
+    if (rows <= 16) return launch<DP, 1>(a, ws, s);
+    if (rows <= 32) return launch<DP, 2>(a, ws, s);
+    return launch<DP, 4>(a, ws, s);
+}
+
+}  // namespace
+
+bool attention_split_supported(const Attn &a, int dtype) {
+    return dtype == GDN_BF16 && a.block_table != nullptr && a.H / a.HKV <= kSplitRows && rows_aligned(a.q, a.qs, a.D, 2) &&
+           rows_aligned(a.k, a.ks, a.D, 2) && rows_aligned(a.v, a.vs, a.D, 2) && ((uintptr_t)a.out & 15) == 0;
+}
+
+size_t attention_split_workspace(int B, int H, int HKV, int D, int max_q) {
+    const long rows = (long)max_q * (H / HKV);
+    const int R = rows <= 16 ? 16 : rows <= 32 ? 32 : 64, dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
+    return span_bytes(B, HKV) + 2 * (size_t)kMaxCtas * R * (2 + dp) * 4;
+}
+
+cudaError_t launch_attention_split(const Attn &a, void *ws, cudaStream_t s) {
+    if (a.D <= 64) return launch_rows<64>(a, ws, s);
+    if (a.D <= 128) return launch_rows<128>(a, ws, s);
+    return launch_rows<256>(a, ws, s);
+}
+
+}  // namespace gdn

@@ -57,6 +57,13 @@ inline bool rows_aligned(const void *base, long stride_elems, int D, size_t esz)
 size_t attention_simt_part_floats(int B, int N, int H, int HKV, int D);
 cudaError_t launch_attention_simt(const Attn &a, int dtype, cudaStream_t s);
 
+// bf16, few rows over long paged histories: sequences of at most kSplitRows
+// (query, head of a group) rows, the others are left out.
+constexpr int kSplitRows = 64;
+bool attention_split_supported(const Attn &a, int dtype);
+size_t attention_split_workspace(int B, int H, int HKV, int D, int max_q);
+cudaError_t launch_attention_split(const Attn &a, void *ws, cudaStream_t s);
+
 // bf16 on the tensor cores, one item per (query tile pair, head): prompts and
 // prompt slices.  Sequences of at most min_rows (query, head of a group) rows
 // are left out.

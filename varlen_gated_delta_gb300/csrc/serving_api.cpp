@@ -23,6 +23,7 @@ int check_dtype(int dtype, const char *what) {
 
 int check_geometry(int N, int H, int HKV, int D, const char *what) {
     if (N < 0) return set_error(GDN_ERR_SHAPE, "%s: N=%d is negative", what, N);
+    if (N > INT_MAX - 1024) return set_error(GDN_ERR_OVERFLOW, "%s: N=%d is out of range", what, N);
     if (H < 1 || HKV < 1 || D < 1)
         return set_error(GDN_ERR_SHAPE, "%s: head geometry must be positive (H=%d HKV=%d D=%d)", what, H, HKV, D);
     if (D > 256) return set_error(GDN_ERR_SHAPE, "%s: head width D=%d exceeds 256", what, D);
@@ -131,7 +132,9 @@ int gdn_attention_status(void *stream) {
 
 size_t gdn_attention_paged_workspace_bytes(int B, int N, int H, int HKV, int D, int max_q) {
     if (B < 1 || max_q < 0 || check_geometry(N, H, HKV, D, "attention")) return 0;
-    return round256(attention_simt_part_floats(B, N, H, HKV, D) * 4) + 256;
+    const size_t simt = attention_simt_part_floats(B, N, H, HKV, D) * 4;
+    const size_t split = attention_split_workspace(B, H, HKV, D, max_q);
+    return round256(simt > split ? simt : split);
 }
 
 int gdn_attention_paged(const void *q, const void *k_cache, const void *v_cache,
@@ -147,7 +150,8 @@ int gdn_attention_paged(const void *q, const void *k_cache, const void *v_cache,
     if (page_size < 1 || max_pages < 1 || num_pages < 1 || max_q < 0)
         return set_error(GDN_ERR_SHAPE, "paged attention: page_size=%d, max_pages=%d, num_pages=%d must be positive, max_q=%d not negative",
                          page_size, max_pages, num_pages, max_q);
-    if ((long)page_size * num_pages > INT_MAX || (long)page_size * max_pages > INT_MAX)
+    // (room for a tile of keys past the end)
+    if ((long)page_size * num_pages > INT_MAX - 1024 || (long)page_size * max_pages > INT_MAX - 1024)
         return set_error(GDN_ERR_OVERFLOW, "paged attention: page_size * num_pages and page_size * max_pages must fit int32");
     if ((rc = check_stride(q_stride, (int64_t)H * D, N, "q_stride"))) return rc;
     if (!std::isfinite(scale)) return set_error(GDN_ERR_SHAPE, "paged attention: scale must be finite");
@@ -170,9 +174,16 @@ int gdn_attention_paged(const void *q, const void *k_cache, const void *v_cache,
     a.part = static_cast<float *>(workspace);
     a.part_floats = attention_simt_part_floats(B, N, H, HKV, D);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const bool prompt = (long)a.max_q * (H / HKV) > 64 && attention_prompt_supported(a, dtype);
-    return launched(prompt ? launch_attention_prompt(a, 0, st) : launch_attention_simt(a, dtype, st),
-                    "paged attention kernel launch");
+    // Sequences of few rows run split over their keys, longer ones as prompt slices; a call
+    // that may hold both launches both, and each kernel takes its own.
+    const bool some_long = (long)a.max_q * (H / HKV) > kSplitRows;
+    const bool split = attention_split_supported(a, dtype);
+    if (some_long ? !attention_prompt_supported(a, dtype) : !split)
+        return launched(launch_attention_simt(a, dtype, st), "paged attention kernel launch");
+    if (split) rc = launched(launch_attention_split(a, workspace, st), "split attention kernel launch");
+    if (!rc && some_long)
+        rc = launched(launch_attention_prompt(a, split ? kSplitRows : 0, st), "prompt attention kernel launch");
+    return rc;
 }
 
 }  // extern "C"
