@@ -15,6 +15,7 @@ fused layer ``gdn_layer_varlen``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -169,6 +170,14 @@ def _ptr(t, name, dtype=None, shape=None, device=None):
 
 def _stream(device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
+
+
+def _raw_stream(device) -> int:
+    """_stream without building a torch.cuda.Stream object, where torch offers that."""
+    return _current_raw_stream(device.index) if _current_raw_stream else _stream(device)
+
+
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _host_offsets(offsets_host):
@@ -647,8 +656,36 @@ def gdn_segment_plan(offsets, H: int, V: int, sm_count: int) -> list:
 
 # ------------------------------------------------------------------ softmax-attention layers
 
+# These calls run in decode loops, where the host's time counts: a tensor that is as it
+# should be passes one combined test, any other gets its message from the full checks.
+
+def _on_gpu(device, name):
+    if device.type != "cuda":
+        raise GdnError(6, f"{name} must be a CUDA tensor")
+    return device
+
+
+def _at(t, name, dtype, shape, device):
+    """_ptr for a tensor that must be there."""
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape
+            and t.get_device() == device.index and t.is_contiguous()):
+        return t.data_ptr()
+    return _ptr(t, name, dtype, shape, device)
+
+
+def _out(t, name, dtype, shape, device):
+    """An output and its pointer: the caller's tensor, or a new one."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        return t, t.data_ptr()
+    return t, _at(t, name, dtype, shape, device)
+
+
 def _rows(t, name, dtype, shape, device):
     """Pointer and token stride of a tensor of rows: contiguous but for the token stride."""
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape
+            and t.get_device() == device.index and t.is_contiguous()):
+        return t.data_ptr(), t.stride(0)
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda or t.device != device:
@@ -681,19 +718,19 @@ def gdn_page_plan(new_lens, cached_lens, block_table, free_pages, *, page_size, 
     cursor_out [1], status [1]), all int32; when status[0] != 0 nothing was handed out."""
     lib = load_library()
     B, max_pages = block_table.shape
-    dev, i32 = block_table.device, torch.int32
-    new = lambda t, n: torch.empty((n,), dtype=i32, device=dev) if t is None else t
-    offsets, kv_lens, cursor_out = new(offsets, B + 1), new(kv_lens, B), new(cursor_out, 1)
-    positions, slots, status = new(positions, N), new(slots, N), new(status, 1)
-    args = [_ptr(new_lens, "new_lens", i32, (B,), dev), _ptr(cached_lens, "cached_lens", i32, (B,), dev),
-            _ptr(block_table, "block_table", i32, (B, max_pages), dev),
-            _ptr(free_pages, "free_pages", i32, (free_pages.numel(),), dev),
-            _ptr(cursor, "cursor", i32, (1,), dev), _ptr(offsets, "offsets", i32, (B + 1,), dev),
-            _ptr(kv_lens, "kv_lens", i32, (B,), dev), _ptr(positions, "positions", i32, (N,), dev),
-            _ptr(slots, "slots", i32, (N,), dev), _ptr(cursor_out, "cursor_out", i32, (1,), dev),
-            _ptr(status, "status", i32, (1,), dev)]
-    _check(lib.gdn_page_plan(*args, B, N, int(page_size), max_pages, free_pages.numel(),
-                             _stream(dev)))
+    dev, i32 = _on_gpu(block_table.device, "block_table"), torch.int32
+    n_free = free_pages.numel()
+    offsets, op = _out(offsets, "offsets", i32, (B + 1,), dev)
+    kv_lens, kp = _out(kv_lens, "kv_lens", i32, (B,), dev)
+    positions, pp = _out(positions, "positions", i32, (N,), dev)
+    slots, sp = _out(slots, "slots", i32, (N,), dev)
+    cursor_out, cp = _out(cursor_out, "cursor_out", i32, (1,), dev)
+    status, tp = _out(status, "status", i32, (1,), dev)
+    _check(lib.gdn_page_plan(
+        _at(new_lens, "new_lens", i32, (B,), dev), _at(cached_lens, "cached_lens", i32, (B,), dev),
+        _at(block_table, "block_table", i32, (B, max_pages), dev),
+        _at(free_pages, "free_pages", i32, (n_free,), dev), _at(cursor, "cursor", i32, (1,), dev),
+        op, kp, pp, sp, cp, tp, B, N, int(page_size), max_pages, n_free, _raw_stream(dev)))
     return offsets, kv_lens, positions, slots, cursor_out, status
 
 
@@ -708,11 +745,12 @@ def gdn_qk_norm_rope(qkv, cos_sin=None, positions=None, *, H, HKV, D, q_weight=N
     is only written when a tensor ``k`` is given.  Returns (q [N,H,D], k [N,HKV,D] or None)."""
     lib = load_library()
     N = qkv.shape[0]
-    T, dev, f32, i32 = qkv.dtype, qkv.device, torch.float32, torch.int32
+    T, dev, f32, i32 = qkv.dtype, _on_gpu(qkv.device, "qkv"), torch.float32, torch.int32
     base, stride = _rows(qkv, "qkv", T, (N, (H + 2 * HKV) * D), dev)
-    q = torch.empty((N, H, D), dtype=T, device=dev) if q is None else q
-    if k is None and slots is None:
-        k = torch.empty((N, HKV, D), dtype=T, device=dev)
+    q, qp = _out(q, "q", T, (N, H, D), dev)
+    kp = None
+    if k is not None or slots is None:
+        k, kp = _out(k, "k", T, (N, HKV, D), dev)
     max_pos, R = (0, 0) if cos_sin is None else cos_sin.shape
     num_slots = 0
     kc = vc = None
@@ -721,13 +759,14 @@ def gdn_qk_norm_rope(qkv, cos_sin=None, positions=None, *, H, HKV, D, q_weight=N
             raise GdnError(1, "slots need k_cache and v_cache")
         cshape = (*k_cache.shape[:2], HKV, D)
         num_slots = cshape[0] * cshape[1]
-        kc, vc = _ptr(k_cache, "k_cache", T, cshape, dev), _ptr(v_cache, "v_cache", T, cshape, dev)
+        kc, vc = _at(k_cache, "k_cache", T, cshape, dev), _at(v_cache, "v_cache", T, cshape, dev)
     _check(lib.gdn_qk_norm_rope(
-        base, stride, _ptr(q_weight, "q_weight", f32, (D,), dev), _ptr(k_weight, "k_weight", f32, (D,), dev),
-        float(eps), _ptr(cos_sin, "cos_sin", f32, (max_pos, R), dev),
-        _ptr(positions, "positions", i32, (N,), dev), max_pos, _ptr(slots, "slots", i32, (N,), dev),
-        _ptr(q, "q", T, (N, H, D), dev), _ptr(k, "k", T, (N, HKV, D), dev), kc, vc, num_slots, N, H,
-        HKV, D, R, int(style), _dtype_code(qkv), _stream(dev)))
+        base, stride, None if q_weight is None else _at(q_weight, "q_weight", f32, (D,), dev),
+        None if k_weight is None else _at(k_weight, "k_weight", f32, (D,), dev), float(eps),
+        None if R == 0 else _at(cos_sin, "cos_sin", f32, (max_pos, R), dev),
+        None if positions is None else _at(positions, "positions", i32, (N,), dev), max_pos,
+        None if slots is None else _at(slots, "slots", i32, (N,), dev),
+        qp, kp, kc, vc, num_slots, N, H, HKV, D, R, int(style), _dtype_code(qkv), _raw_stream(dev)))
     return q, k
 
 
@@ -739,14 +778,14 @@ def gdn_attention_varlen(q, k, v, offsets, *, scale=0.0, out=None):
     lib = load_library()
     N, H, D = q.shape
     HKV = k.shape[1]
-    T, dev = q.dtype, q.device
+    T, dev = q.dtype, _on_gpu(q.device, "q")
     B = offsets.numel() - 1
-    out = torch.empty((N, H, D), dtype=T, device=dev) if out is None else out
+    out, op = _out(out, "out", T, (N, H, D), dev)
     (qp, qs), (kp, ks), (vp, vs) = (_rows(q, "q", T, (N, H, D), dev), _rows(k, "k", T, (N, HKV, D), dev),
                                     _rows(v, "v", T, (N, HKV, D), dev))
-    _check(lib.gdn_attention_varlen(qp, kp, vp, _ptr(offsets, "offsets", torch.int32, (B + 1,), dev),
-                                    _ptr(out, "out", T, (N, H, D), dev), B, N, H, HKV, D, qs, ks, vs,
-                                    float(scale), _dtype_code(q), _stream(dev)))
+    _check(lib.gdn_attention_varlen(qp, kp, vp, _at(offsets, "offsets", torch.int32, (B + 1,), dev),
+                                    op, B, N, H, HKV, D, qs, ks, vs,
+                                    float(scale), _dtype_code(q), _raw_stream(dev)))
     return out
 
 
@@ -754,10 +793,12 @@ def gdn_attention_status(device=None) -> None:
     """Synchronise the current stream; raise GdnError (GDN_ERR_TIMEOUT) when a wait inside an
     attention kernel gave up since the last query."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
-    _check(load_library().gdn_attention_status(_stream(dev)))
+    _check(load_library().gdn_attention_status(_raw_stream(dev)))
 
 
+@functools.lru_cache(maxsize=256)
 def gdn_attention_paged_workspace_bytes(B, N, H, HKV, D, max_q) -> int:
+    """Workspace bytes of gdn_attention_paged for these sizes."""
     return int(load_library().gdn_attention_paged_workspace_bytes(B, N, H, HKV, D, max_q))
 
 
@@ -774,17 +815,17 @@ def gdn_attention_paged(q, k_cache, v_cache, block_table, kv_lens, offsets, *, m
     N, H, D = q.shape
     pages, page_size, HKV, _ = k_cache.shape
     B, max_pages = block_table.shape
-    T, dev, i32 = q.dtype, q.device, torch.int32
-    out = torch.empty((N, H, D), dtype=T, device=dev) if out is None else out
+    T, dev, i32 = q.dtype, _on_gpu(q.device, "q"), torch.int32
+    out, op = _out(out, "out", T, (N, H, D), dev)
     qp, qs = _rows(q, "q", T, (N, H, D), dev)
     if workspace is None:
         need = gdn_attention_paged_workspace_bytes(B, N, H, HKV, D, int(max_q))
         workspace = torch.empty((max(need, 256),), dtype=torch.uint8, device=dev)
     cshape = (pages, page_size, HKV, D)
     _check(lib.gdn_attention_paged(
-        qp, _ptr(k_cache, "k_cache", T, cshape, dev), _ptr(v_cache, "v_cache", T, cshape, dev),
-        _ptr(block_table, "block_table", i32, (B, max_pages), dev), _ptr(kv_lens, "kv_lens", i32, (B,), dev),
-        _ptr(offsets, "offsets", i32, (B + 1,), dev), _ptr(out, "out", T, (N, H, D), dev), B, N, H, HKV, D,
+        qp, _at(k_cache, "k_cache", T, cshape, dev), _at(v_cache, "v_cache", T, cshape, dev),
+        _at(block_table, "block_table", i32, (B, max_pages), dev), _at(kv_lens, "kv_lens", i32, (B,), dev),
+        _at(offsets, "offsets", i32, (B + 1,), dev), op, B, N, H, HKV, D,
         page_size, max_pages, pages, int(max_q), qs, float(scale), _dtype_code(q),
-        _ptr(workspace, "workspace", torch.uint8, None, dev), workspace.numel(), _stream(dev)))
+        _ptr(workspace, "workspace", torch.uint8, None, dev), workspace.numel(), _raw_stream(dev)))
     return out
