@@ -9,12 +9,12 @@
 //
 // A CTA holds a pair of query tiles (one for D > 128) and every key tile it
 // loads serves both.  Warp roles: one softmax warpgroup per query tile (a thread
-// owns a row, so row maxima and sums need no exchange), one TMA warp, one MMA
-// warp, two warps that mend V tiles.  S and O live in tensor memory; P replaces
-// S in place as bf16 (A operand of the second product, read from tensor
-// memory).  The MMA warp alternates the tiles, so one tile's softmax runs under
-// the other's products; with a single query tile S is double buffered instead
-// and the products of the next key tile run under the softmax.
+// owns a row, so row maxima and sums need no exchange), one MMA warp per query
+// tile, one TMA warp, one warp that mends V tiles.  S and O live in tensor memory;
+// P replaces S in place as bf16 (A operand of the second product, read from
+// tensor memory).  One tile's softmax runs under the other's products; with a
+// single query tile S is double buffered instead and the scores of the next key
+// tile run under the softmax.
 //
 // O is rescaled only when the row maximum has grown by more than 2^8 since the
 // last time: P then stays below 2^8, with the same relative precision, and
@@ -22,9 +22,9 @@
 //
 // V rows that some query of the tile must not see (later tokens, other
 // sequences, stale cache slots) meet P = 0, and 0 * inf would be NaN: in the few
-// key tiles that have masked scores, warps 2 and 3 of the last warpgroup replace
-// non-finite V values by 0 before the product, and, if there were any, the
-// epilogue adds them to the rows that do see them.
+// key tiles that have masked scores, a warp replaces non-finite V values by 0
+// before the product, and, if there were any, the epilogue adds them to the rows
+// that do see them.
 //
 // Persistent CTAs, one per SM, take (query tile pair, head) items in a fixed
 // interleaved order, longest first by the tile's place in its sequence; heads
@@ -46,6 +46,12 @@ constexpr float kLazy = 8.f;    // growth of the row maximum (log2) that O waits
 // Set when a bounded wait of an attention kernel has given up.
 __device__ int g_attention_timeout;
 
+// Registers a thread of this warpgroup gives up (Dec) or takes (Inc) from here on.
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
 template <int DP>
 struct Cfg {
     static constexpr int NQ = DP > 128 ? 1 : 2;    // query tiles of a CTA
@@ -55,6 +61,10 @@ struct Cfg {
     static constexpr int QBYTES = 128 * DP * 2, SLOT = BN * DP * 2;
     static constexpr int SLOTS = 4;
     static constexpr int THREADS = NQ * 128 + 128;
+    // registers a thread at launch and after the split: a softmax thread holds a row of scores
+    static constexpr int REGS = 65536 / THREADS / 8 * 8 > 255 ? 248 : 65536 / THREADS / 8 * 8;
+    static constexpr int REGS_IO = 80, REGS_SOFTMAX = NQ == 2 ? 208 : REGS;
+    static_assert(NQ * REGS_SOFTMAX + REGS_IO <= (NQ + 1) * REGS, "more registers than the CTA was launched with");
     // tensor memory: two score buffers, then O of each query tile
     static constexpr int COL_O = 2 * BN;
 };
@@ -112,6 +122,13 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// True in one lane of the converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
 }
 
 // One item: TM queries from row0 on of one head of sequence b.
@@ -202,14 +219,16 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(s_abort + 1);
     int *suffix = s_abort + 4;  // [bins + 1]
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    constexpr int kTmaWarp = NQ * 4, kMmaWarp = NQ * 4 + 1;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (the same in every lane, as the compiler sees it)
+    // the last warpgroup: loads, products of each query tile, V values
+    constexpr int kTmaWarp = NQ * 4, kMmaWarp = NQ * 4 + 1, kFixWarp = NQ * 4 + 3;
 
     if (tid == 0) {
         for (int i = 0; i < SLOTS; ++i) {
             mbar_init(full + i, 1);
-            mbar_init(empty + i, i & 1 ? 3 : 1);  // V (odd) slots: the products and both mending warps
-            mbar_init(v_fixed + i, 64);
+            mbar_init(empty + i, NQ + (i & 1));  // every product warp and, for V (odd slots), the mending warp
+            mbar_init(v_fixed + i, 32);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full + i, 1), mbar_init(q_empty + i, 1);
@@ -256,183 +275,154 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
     Item it;
     it.n[1] = 0;
 
-    if (warp == kTmaWarp) {
-        // ---------------------------------------------------------------- loads
-        uint32_t slot = 0, phase = 0, q_phase = 0;
-        const int boxes = BN / p.box_rows;  // boxes of a 64-channel block of a key tile
-        auto next_slot = [&]() {
-            if (++slot == SLOTS) slot = 0, phase ^= 1;
-        };
-        for (long idx = blockIdx.x; get_item<DP>(p, suffix, idx, it); idx += step) {
-#pragma unroll
-            for (int t = 0; t < NQ; ++t) {
-                if (it.n[t] == 0) continue;
-                if (!wait_or_abort(q_empty + t, ((q_phase >> t) & 1) ^ 1, abort)) goto done;
-                q_phase ^= 1u << t;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(q_full + t, C::QBYTES);
-                    for (int c = 0; c < NB; ++c)
-                        tma_load_3d(sq + t * C::QBYTES + c * 128 * 128, &qmap, q_full + t, c * 64, it.h,
-                                    it.start + it.row0 + t * 128);
-                }
-            }
-            for (int j = 0; j < it.tiles; ++j) {
-                // the row of this lane's box (packed keys: one box, at its token)
-                int row = it.start + j * BN;
-                if (p.a.block_table != nullptr && lane < boxes) {
-                    const int key = j * BN + lane * p.box_rows;
-                    const int page = key < it.kv ? __ldg(p.a.block_table + (size_t)it.b * p.a.max_pages + key / p.a.page_size) : -1;
-                    // outside the cache: past its end, where the load gives zeros
-                    row = page < 0 || page >= p.a.num_pages ? p.a.num_pages * p.a.page_size
-                                                            : page * p.a.page_size + key % p.a.page_size;
-                }
-                for (int kv = 0; kv < 2; ++kv) {
-                    if (!wait_or_abort(empty + slot, phase ^ 1, abort)) goto done;
-                    if (lane == 0) mbar_arrive_expect_tx(full + slot, C::SLOT);
-                    __syncwarp();
-                    if (lane < boxes) {
-                        unsigned char *dst = ring + slot * C::SLOT + lane * p.box_rows * 128;
-                        for (int c = 0; c < NB; ++c)
-                            tma_load_3d(dst + c * BN * 128, kv ? &vmap : &kmap, full + slot, c * 64, it.h / p.G, row);
-                    }
-                    next_slot();
-                }
-            }
-        }
-    } else if (warp == kMmaWarp) {
-        // ---------------------------------------------------------------- products
-        const uint32_t id_s = idesc_bf16(128, BN, false, false) | (p.negate ? 1u << 13 : 0u);
-        const uint32_t id_o = idesc_bf16(128, DP, false, true);
-        const uint32_t q_addr = smem_u32(sq), r_addr = smem_u32(ring);
-        uint32_t q_phase = 0, p_phase = 0, fix_phase = 0;  // one bit a barrier
-        uint32_t seq = 0;  // loads before this item: K_j is load seq + 2 j, V_j the one after it
+    if (warp >= kTmaWarp) {
+        if constexpr (NQ == 2) regs_dec<C::REGS_IO>();
         auto slot_of = [&](uint32_t s) { return s % SLOTS; };
         auto phase_of = [&](uint32_t s) { return (s / SLOTS) & 1; };
-        for (long idx = blockIdx.x; get_item<DP>(p, suffix, idx, it); idx += step) {
-            // S[buf] = Q[t] K_j^T
-            auto scores = [&](int t, int buf, int j) {
-                if (lane == 0) {
-                    const uint32_t kb = r_addr + slot_of(seq + 2 * j) * C::SLOT, qb = q_addr + t * C::QBYTES;
-#pragma unroll
-                    for (int ks = 0; ks < DP / 16; ++ks)
-                        mma_bf16(tmem + buf * BN, sdesc_sw128(qb + (ks >> 2) * 128 * 128 + (ks & 3) * 32, 16, 1024),
-                                 sdesc_sw128(kb + (ks >> 2) * BN * 128 + (ks & 3) * 32, 16, 1024), id_s, ks > 0);
-                    mma_commit(s_full + buf);
-                }
-                __syncwarp();
-            };
-            auto wait_slot = [&](uint32_t s) {
-                const bool ok = wait_or_abort(full + slot_of(s), phase_of(s), abort);
-                tc_fence_after();
-                return ok;
-            };
-            auto free_slot = [&](uint32_t s) {
-                if (lane == 0) mma_commit(empty + slot_of(s));
-                __syncwarp();
-            };
-            auto free_q = [&](int t) {
-                if (lane == 0) mma_commit(q_empty + t);
-                __syncwarp();
-            };
-            // O[t] (+)= P[buf] V_j
-            auto values = [&](int t, int buf, int j) {
-                if (!wait_or_abort(p_full + buf, (p_phase >> buf) & 1, abort)) return false;
-                p_phase ^= 1u << buf;
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t vb = r_addr + slot_of(seq + 2 * j + 1) * C::SLOT;
-#pragma unroll
-                    for (int ks = 0; ks < BN / 16; ++ks)
-                        mma_bf16_ts(tmem + C::COL_O + t * DP, tmem + buf * BN + ks * 8,
-                                    sdesc_sw128(vb + ks * 2048, BN * 128, 1024), id_o, j > 0 || ks > 0);
-                    mma_commit(o_done + t);
-                }
-                __syncwarp();
-                return true;
-            };
-            if (it.tiles > 0) {
-                if (!wait_slot(seq)) goto done;
+        uint32_t seq = 0;  // loads before this item: K_j is load seq + 2 j, V_j the one after it
+        if (warp == kTmaWarp) {
+            // ------------------------------------------------------------ loads
+            uint32_t q_phase = 0;
+            const int boxes = BN / p.box_rows;  // boxes of a 64-channel block of a key tile
+            for (long idx = blockIdx.x; get_item<DP>(p, suffix, idx, it); idx += step, seq += 2 * it.tiles) {
 #pragma unroll
                 for (int t = 0; t < NQ; ++t) {
                     if (it.n[t] == 0) continue;
-                    if (!wait_or_abort(q_full + t, (q_phase >> t) & 1, abort)) goto done;
+                    if (!wait_or_abort(q_empty + t, ((q_phase >> t) & 1) ^ 1, abort)) goto done;
                     q_phase ^= 1u << t;
-                    tc_fence_after();
-                    scores(t, t, 0);
-                    if (it.n[t] == 1) free_q(t);
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(q_full + t, C::QBYTES);
+                        for (int c = 0; c < NB; ++c)
+                            tma_load_3d(sq + t * C::QBYTES + c * 128 * 128, &qmap, q_full + t, c * 64, it.h,
+                                        it.start + it.row0 + t * 128);
+                    }
                 }
-                free_slot(seq);
-            }
-            for (int j = 0; j < it.tiles; ++j) {
-                const bool more = j + 1 < it.tiles;
-                if (NQ == 1 && more) {  // the next scores run under this tile's softmax
-                    if (!wait_slot(seq + 2 * (j + 1))) goto done;
-                    scores(0, (j + 1) & 1, j + 1);
-                    if (j + 2 == it.n[0]) free_q(0);
-                    free_slot(seq + 2 * (j + 1));
-                }
-                if (!wait_slot(seq + 2 * j + 1)) goto done;
-                if (j >= it.fix) {
-                    const uint32_t v = slot_of(seq + 2 * j + 1);
-                    if (!wait_or_abort(v_fixed + v, (fix_phase >> v) & 1, abort)) goto done;
-                    fix_phase ^= 1u << v;
-                    tc_fence_after();
-                }
-                if (NQ == 1) {
-                    if (!values(0, j & 1, j)) goto done;
-                } else {
-                    bool have_k = false;
+                for (int j = 0; j < it.tiles; ++j) {
+                    // the row of this lane's box (packed keys: one box, at its token)
+                    int row = it.start + j * BN;
+                    if (p.a.block_table != nullptr && lane < boxes) {
+                        const int key = j * BN + lane * p.box_rows;
+                        const int page =
+                            key < it.kv ? __ldg(p.a.block_table + (size_t)it.b * p.a.max_pages + key / p.a.page_size) : -1;
+                        // outside the cache: past its end, where the load gives zeros
+                        row = page < 0 || page >= p.a.num_pages ? p.a.num_pages * p.a.page_size
+                                                                : page * p.a.page_size + key % p.a.page_size;
+                    }
 #pragma unroll
-                    for (int t = 0; t < NQ; ++t) {
-                        if (j >= it.n[t]) continue;
-                        if (!values(t, t, j)) goto done;
-                        if (j + 1 < it.n[t]) {
-                            if (!have_k && !wait_slot(seq + 2 * (j + 1))) goto done;
-                            have_k = true;
-                            scores(t, t, j + 1);
-                            if (j + 2 == it.n[t]) free_q(t);
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const uint32_t s = seq + 2 * j + kv, slot = slot_of(s);
+                        if (!wait_or_abort(empty + slot, phase_of(s) ^ 1, abort)) goto done;
+                        if (lane == 0) mbar_arrive_expect_tx(full + slot, C::SLOT);
+                        __syncwarp();
+                        if (lane < boxes) {
+                            unsigned char *dst = ring + slot * C::SLOT + lane * p.box_rows * 128;
+                            for (int c = 0; c < NB; ++c)
+                                tma_load_3d(dst + c * BN * 128, kv ? &vmap : &kmap, full + slot, c * 64, it.h / p.G, row);
                         }
                     }
-                    if (more) free_slot(seq + 2 * (j + 1));
                 }
-                free_slot(seq + 2 * j + 1);
             }
-            seq += 2 * it.tiles;
-        }
-    } else if (warp > kMmaWarp) {
-        // ---------------------------------------------------------------- non-finite V values
-        uint32_t seq = 0, n_item = 0;
-        const int ft = (warp - kMmaWarp - 1) * 32 + lane;
-        for (long idx = blockIdx.x; get_item<DP>(p, suffix, idx, it); idx += step, ++n_item) {
-            for (int j = 0; j < it.tiles; ++j) {
-                // every V tile is waited for, so that no phase of its barrier goes by unseen
-                const uint32_t s = seq + 2 * j + 1;
-                if (!wait_or_abort(full + s % SLOTS, (s / SLOTS) & 1, abort)) goto done;
-                if (lane == 0) mbar_arrive(empty + s % SLOTS);
-                if (j < it.fix) continue;
-                uint4 *tile = reinterpret_cast<uint4 *>(ring + (s % SLOTS) * C::SLOT);
-                bool bad = false;
-#pragma unroll 4
-                for (int i = ft; i < C::SLOT / 16; i += 64) {
-                    uint4 x = tile[i];
-                    uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                    bool hit = false;
+        } else if (warp < kMmaWarp + NQ) {
+            // ------------------------------------------------------------ products of query tile t
+            const int t = warp - kMmaWarp;
+            const uint32_t id_s = idesc_bf16(128, BN, false, false) | (p.negate ? 1u << 13 : 0u);
+            const uint32_t id_o = idesc_bf16(128, DP, false, true);
+            const uint64_t qd0 = sdesc_sw128(smem_u32(sq) + t * C::QBYTES, 16, 1024);
+            const uint32_t r_addr = smem_u32(ring), o_tmem = tmem + C::COL_O + t * DP;
+            uint32_t q_phase = 0, p_phase = 0, fix_phase = 0;  // one bit a barrier
+            for (long idx = blockIdx.x; get_item<DP>(p, suffix, idx, it); idx += step, seq += 2 * it.tiles) {
+                const int n = NQ == 2 && t ? it.n[1] : it.n[0];
+                auto wait_slot = [&](uint32_t s) { return wait_or_abort(full + slot_of(s), phase_of(s), abort); };
+                // S[buf] = Q[t] K_j^T, and the slot is free after it
+                auto scores = [&](int j) {
+                    const int buf = NQ == 2 ? t : j & 1;
+                    const uint32_t slot = slot_of(seq + 2 * j);
+                    if (!wait_slot(seq + 2 * j)) return false;
+                    tc_fence_after();
+                    uint64_t kd = sdesc_sw128(r_addr + slot * C::SLOT, 16, 1024), qd = qd0;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        const bool lo = (w[z] & 0x7f80u) == 0x7f80u, hi = (w[z] & 0x7f800000u) == 0x7f800000u;
-                        hit |= lo | hi;
-                        w[z] &= (lo ? 0xffff0000u : 0xffffffffu) & (hi ? 0x0000ffffu : 0xffffffffu);
+                        for (int ks = 0; ks < DP / 16; ++ks)
+                            mma_bf16(tmem + buf * BN, qd + (((ks >> 2) * 128 * 128 + (ks & 3) * 32) >> 4),
+                                     kd + (((ks >> 2) * BN * 128 + (ks & 3) * 32) >> 4), id_s, ks > 0);
+                        mma_commit(s_full + buf);
+                        mma_commit(empty + slot);
+                        if (j + 1 == n) mma_commit(q_empty + t);
                     }
-                    if (hit) tile[i] = make_uint4(w[0], w[1], w[2], w[3]);
-                    bad |= hit;
+                    __syncwarp();
+                    return true;
+                };
+                if (n > 0) {
+                    if (!wait_or_abort(q_full + t, q_phase, abort)) goto done;
+                    q_phase ^= 1;
+                    if (!scores(0)) goto done;
                 }
-                if (bad) s_bad[n_item & 3] = (int)n_item + 1;
-                fence_async_smem();
-                mbar_arrive(v_fixed + s % SLOTS);
+                for (int j = 0; j < it.tiles; ++j) {
+                    const uint32_t v = slot_of(seq + 2 * j + 1);
+                    if (j >= n) {  // only the other query tile sees these keys: let the slots go by
+                        if (!wait_slot(seq + 2 * j)) goto done;
+                        if (elect_one()) mbar_arrive(empty + slot_of(seq + 2 * j));
+                        __syncwarp();
+                    } else if (NQ == 1 && j + 1 < n) {
+                        if (!scores(j + 1)) goto done;  // the next scores run under this tile's softmax
+                    }
+                    if (!wait_slot(seq + 2 * j + 1)) goto done;
+                    if (j >= it.fix) {
+                        if (!wait_or_abort(v_fixed + v, (fix_phase >> v) & 1, abort)) goto done;
+                        fix_phase ^= 1u << v;
+                    }
+                    if (j >= n) {
+                        if (elect_one()) mbar_arrive(empty + v);
+                        __syncwarp();
+                        continue;
+                    }
+                    // O[t] (+)= P[buf] V_j
+                    const int buf = NQ == 2 ? t : j & 1;
+                    if (!wait_or_abort(p_full + buf, (p_phase >> buf) & 1, abort)) goto done;
+                    p_phase ^= 1u << buf;
+                    tc_fence_after();
+                    uint64_t vd = sdesc_sw128(r_addr + v * C::SLOT, BN * 128, 1024);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int ks = 0; ks < BN / 16; ++ks)
+                            mma_bf16_ts(o_tmem, tmem + buf * BN + ks * 8, vd + ((ks * 2048) >> 4), id_o, j > 0 || ks > 0);
+                        mma_commit(o_done + t);
+                        mma_commit(empty + v);
+                    }
+                    __syncwarp();
+                    if (NQ == 2 && j + 1 < n && !scores(j + 1)) goto done;
+                }
             }
-            seq += 2 * it.tiles;
+        } else if (warp == kFixWarp) {
+            // ------------------------------------------------------------ non-finite V values
+            uint32_t n_item = 0;
+            for (long idx = blockIdx.x; get_item<DP>(p, suffix, idx, it); idx += step, seq += 2 * it.tiles, ++n_item) {
+                for (int j = 0; j < it.tiles; ++j) {
+                    // every V tile is waited for, so that no phase of its barrier goes by unseen
+                    const uint32_t s = seq + 2 * j + 1, slot = slot_of(s);
+                    if (!wait_or_abort(full + slot, phase_of(s), abort)) goto done;
+                    if (lane == 0) mbar_arrive(empty + slot);
+                    if (j < it.fix) continue;
+                    uint4 *tile = reinterpret_cast<uint4 *>(ring + slot * C::SLOT);
+                    bool bad = false;
+#pragma unroll 8
+                    for (int i = lane; i < C::SLOT / 16; i += 32) {
+                        const uint4 x = tile[i];
+                        // an exponent of all ones carries into its value's top bit
+                        auto hit = [](uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
+                        if ((hit(x.x) | hit(x.y) | hit(x.z) | hit(x.w)) == 0) continue;
+                        auto mend = [&](uint32_t w) { return w & ~((hit(w) >> 15) * 0xffffu); };
+                        tile[i] = make_uint4(mend(x.x), mend(x.y), mend(x.z), mend(x.w));
+                        bad = true;
+                    }
+                    if (bad) s_bad[n_item & 3] = (int)n_item + 1;
+                    fence_async_smem();
+                    mbar_arrive(v_fixed + slot);
+                }
+            }
         }
     } else {
+        if constexpr (NQ == 2) regs_inc<C::REGS_SOFTMAX>();
         // ---------------------------------------------------------------- softmax of query tile t
         const int t = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
