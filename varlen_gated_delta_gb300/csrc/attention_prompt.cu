@@ -213,8 +213,8 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
     unsigned char *sq = smem, *ring = smem + NQ * C::QBYTES;
     uint64_t *bars = reinterpret_cast<uint64_t *>(ring + SLOTS * C::SLOT);
     uint64_t *full = bars, *empty = full + SLOTS, *q_full = empty + SLOTS, *q_empty = q_full + 2,
-             *s_full = q_empty + 2, *p_full = s_full + 2, *o_done = p_full + 2, *v_fixed = o_done + 2;
-    int *s_bad = reinterpret_cast<int *>(v_fixed + SLOTS);  // item that had non-finite masked V values
+             *s_full = q_empty + 2, *p_full = s_full + 2, *o_done = p_full + 2, *v_fixed = o_done + 2, *turn = v_fixed + SLOTS;
+    int *s_bad = reinterpret_cast<int *>(turn + 2);  // item that had non-finite masked V values
     int *s_abort = s_bad + 4;
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(s_abort + 1);
     int *suffix = s_abort + 4;  // [bins + 1]
@@ -233,6 +233,7 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full + i, 1), mbar_init(q_empty + i, 1);
             mbar_init(s_full + i, 1), mbar_init(p_full + i, 128), mbar_init(o_done + i, 1);
+            mbar_init(turn + i, 128);
         }
         fence_mbar_init();
         for (int i = 0; i < 4; ++i) s_bad[i] = 0;
@@ -427,16 +428,27 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
         const int t = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t o_col = lanes + C::COL_O + t * DP;
-        uint32_t s_phase = 0, o_count = 0, n_item = 0;
+        uint32_t s_phase = 0, o_count = 0, n_item = 0, turn_phase = 0;
+        if (NQ == 2 && t == 1) mbar_arrive(turn + 0);  // query tile 0 goes first
         for (long idx = blockIdx.x; get_item<DP>(p, suffix, idx, it); idx += step, ++n_item) {
             const int shift = it.kv - it.len, r = it.row0 + t * 128 + row;
             const int n = NQ == 2 && t ? it.n[1] : it.n[0];
             const int least = shift + it.row0 + t * 128 + 1;  // keys that the tile's first row sees
             float m = -INFINITY, l = 0.f;
-            for (int j = 0; j < n; ++j) {
+            for (int j = 0; j < it.tiles; ++j) {
+                if (j >= n) {  // only the other query tile sees these keys
+                    if (!wait_or_abort(turn + t, turn_phase, abort)) goto done;
+                    turn_phase ^= 1;
+                    mbar_arrive(turn + 1 - t);
+                    continue;
+                }
                 const int buf = NQ == 2 ? t : j & 1;
                 if (!wait_or_abort(s_full + buf, (s_phase >> buf) & 1, abort)) goto done;
                 s_phase ^= 1u << buf;
+                if (NQ == 2) {
+                    if (!wait_or_abort(turn + t, turn_phase, abort)) goto done;
+                    turn_phase ^= 1;
+                }
                 tc_fence_after();
                 const uint32_t s_col = lanes + buf * BN;
                 uint32_t x[BN / 32][32];
@@ -494,6 +506,7 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                     }
                     tmem_st32(s_col + c * 32, pk);
                 }
+                if (NQ == 2) mbar_arrive(turn + 1 - t);
                 l += sum.x + sum.y;
                 tmem_wait_st();
                 tc_fence_before();
