@@ -40,7 +40,7 @@ namespace {
 using namespace sm100;
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
-constexpr int kMaxBins = 4096;  // bins of the longest-first order
+constexpr int kMaxBins = 2048;  // bins of the longest-first order
 constexpr float kLazy = 8.f;    // growth of the row maximum (log2) that O waits for
 
 // Set when a bounded wait of an attention kernel has given up.
@@ -60,10 +60,11 @@ struct Cfg {
     static constexpr int NB = DP / 64;             // 64-channel blocks (128 swizzled bytes a row)
     static constexpr int QBYTES = 128 * DP * 2, SLOT = BN * DP * 2;
     static constexpr int SLOTS = 4;
+    static constexpr int STAGING = NQ * 4 * 2048;  // 32 rows of 32 outputs for each softmax warp
     static constexpr int THREADS = NQ * 128 + 128;
     // registers a thread at launch and after the split: a softmax thread holds a row of scores
     static constexpr int REGS = 65536 / THREADS / 8 * 8 > 255 ? 248 : 65536 / THREADS / 8 * 8;
-    static constexpr int REGS_IO = 80, REGS_SOFTMAX = NQ == 2 ? 208 : REGS;
+    static constexpr int REGS_IO = 96, REGS_SOFTMAX = NQ == 2 ? 200 : REGS;
     static_assert(NQ * REGS_SOFTMAX + REGS_IO <= (NQ + 1) * REGS, "more registers than the CTA was launched with");
     // tensor memory: two score buffers, then O of each query tile
     static constexpr int COL_O = 2 * BN;
@@ -210,11 +211,13 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    unsigned char *sq = smem, *ring = smem + NQ * C::QBYTES;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(ring + SLOTS * C::SLOT);
+    unsigned char *sq = smem, *ring = smem + NQ * C::QBYTES, *staging = ring + SLOTS * C::SLOT;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(staging + C::STAGING);
     uint64_t *full = bars, *empty = full + SLOTS, *q_full = empty + SLOTS, *q_empty = q_full + 2,
-             *s_full = q_empty + 2, *p_full = s_full + 2, *o_done = p_full + 2, *v_fixed = o_done + 2, *turn = v_fixed + SLOTS;
-    int *s_bad = reinterpret_cast<int *>(turn + 2);  // item that had non-finite masked V values
+             *s_full = q_empty + 2, *p_full = s_full + 2, *o_done = p_full + 2, *v_fixed = o_done + 2, *turn = v_fixed + SLOTS,
+             *p_half = turn + 2, *item_full = p_half + 2, *item_empty = item_full + 4;
+    Item *s_item = reinterpret_cast<Item *>(item_empty + 4);
+    int *s_bad = reinterpret_cast<int *>(s_item + 4);  // item that had non-finite masked V values
     int *s_abort = s_bad + 4;
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(s_abort + 1);
     int *suffix = s_abort + 4;  // [bins + 1]
@@ -233,8 +236,9 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full + i, 1), mbar_init(q_empty + i, 1);
             mbar_init(s_full + i, 1), mbar_init(p_full + i, 128), mbar_init(o_done + i, 1);
-            mbar_init(turn + i, 128);
+            mbar_init(turn + i, 128), mbar_init(p_half + i, 128);
         }
+        for (int i = 0; i < 4; ++i) mbar_init(item_full + i, 1), mbar_init(item_empty + i, NQ * 5 + 1);
         fence_mbar_init();
         for (int i = 0; i < 4; ++i) s_bad[i] = 0;
         *s_abort = 0;
@@ -275,6 +279,17 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
     const long step = gridDim.x;
     Item it;
     it.n[1] = 0;
+    // Items come from the load warp through a ring of four; false past the last one.
+    uint32_t n_item = 0;
+    auto next_item = [&]() {
+        const uint32_t k = n_item & 3;
+        if (!wait_or_abort(item_full + k, (n_item >> 2) & 1, abort)) return false;
+        it = s_item[k];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(item_empty + k);
+        ++n_item;
+        return it.b >= 0;
+    };
 
     if (warp >= kTmaWarp) {
         if constexpr (NQ == 2) regs_dec<C::REGS_IO>();
@@ -285,7 +300,14 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
             // ------------------------------------------------------------ loads
             uint32_t q_phase = 0;
             const int boxes = BN / p.box_rows;  // boxes of a 64-channel block of a key tile
-            for (long idx = blockIdx.x; get_item<DP>(p, suffix, idx, it); idx += step, seq += 2 * it.tiles) {
+            for (long idx = blockIdx.x;; idx += step, seq += 2 * it.tiles, ++n_item) {
+                if (!get_item<DP>(p, suffix, idx, it)) it.b = -1;
+                if (!wait_or_abort(item_empty + (n_item & 3), ((n_item >> 2) & 1) ^ 1, abort)) goto done;
+                if (lane == 0) {
+                    s_item[n_item & 3] = it;
+                    mbar_arrive(item_full + (n_item & 3));
+                }
+                if (it.b < 0) break;
 #pragma unroll
                 for (int t = 0; t < NQ; ++t) {
                     if (it.n[t] == 0) continue;
@@ -331,15 +353,13 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
             const uint64_t qd0 = sdesc_sw128(smem_u32(sq) + t * C::QBYTES, 16, 1024);
             const uint32_t r_addr = smem_u32(ring), o_tmem = tmem + C::COL_O + t * DP;
             uint32_t q_phase = 0, p_phase = 0, fix_phase = 0;  // one bit a barrier
-            for (long idx = blockIdx.x; get_item<DP>(p, suffix, idx, it); idx += step, seq += 2 * it.tiles) {
+            for (; next_item(); seq += 2 * it.tiles) {
                 const int n = NQ == 2 && t ? it.n[1] : it.n[0];
                 auto wait_slot = [&](uint32_t s) { return wait_or_abort(full + slot_of(s), phase_of(s), abort); };
                 // S[buf] = Q[t] K_j^T, and the slot is free after it
                 auto scores = [&](int j) {
                     const int buf = NQ == 2 ? t : j & 1;
                     const uint32_t slot = slot_of(seq + 2 * j);
-                    if (!wait_slot(seq + 2 * j)) return false;
-                    tc_fence_after();
                     uint64_t kd = sdesc_sw128(r_addr + slot * C::SLOT, 16, 1024), qd = qd0;
                     if (elect_one()) {
 #pragma unroll
@@ -351,12 +371,12 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                         if (j + 1 == n) mma_commit(q_empty + t);
                     }
                     __syncwarp();
-                    return true;
                 };
                 if (n > 0) {
-                    if (!wait_or_abort(q_full + t, q_phase, abort)) goto done;
+                    if (!wait_or_abort(q_full + t, q_phase, abort) || !wait_slot(seq)) goto done;
                     q_phase ^= 1;
-                    if (!scores(0)) goto done;
+                    tc_fence_after();
+                    scores(0);
                 }
                 for (int j = 0; j < it.tiles; ++j) {
                     const uint32_t v = slot_of(seq + 2 * j + 1);
@@ -364,9 +384,11 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                         if (!wait_slot(seq + 2 * j)) goto done;
                         if (elect_one()) mbar_arrive(empty + slot_of(seq + 2 * j));
                         __syncwarp();
-                    } else if (NQ == 1 && j + 1 < n) {
-                        if (!scores(j + 1)) goto done;  // the next scores run under this tile's softmax
+                    } else if (j + 1 < n) {
+                        if (!wait_slot(seq + 2 * j + 2)) goto done;
+                        if (NQ == 1) tc_fence_after(), scores(j + 1);  // they run under this tile's softmax
                     }
+                    // (all that the products wait for but P comes before P)
                     if (!wait_slot(seq + 2 * j + 1)) goto done;
                     if (j >= it.fix) {
                         if (!wait_or_abort(v_fixed + v, (fix_phase >> v) & 1, abort)) goto done;
@@ -379,25 +401,33 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                     }
                     // O[t] (+)= P[buf] V_j
                     const int buf = NQ == 2 ? t : j & 1;
+                    uint64_t vd = sdesc_sw128(r_addr + v * C::SLOT, BN * 128, 1024);
+                    if (NQ == 2) {  // the first half of P is used while the second is computed
+                        if (!wait_or_abort(p_half + buf, (p_phase >> buf) & 1, abort)) goto done;
+                        tc_fence_after();
+                        if (elect_one())
+#pragma unroll
+                            for (int ks = 0; ks < BN / 32; ++ks)
+                                mma_bf16_ts(o_tmem, tmem + buf * BN + ks * 8, vd + ((ks * 2048) >> 4), id_o, j > 0 || ks > 0);
+                        __syncwarp();
+                    }
                     if (!wait_or_abort(p_full + buf, (p_phase >> buf) & 1, abort)) goto done;
                     p_phase ^= 1u << buf;
                     tc_fence_after();
-                    uint64_t vd = sdesc_sw128(r_addr + v * C::SLOT, BN * 128, 1024);
                     if (elect_one()) {
 #pragma unroll
-                        for (int ks = 0; ks < BN / 16; ++ks)
+                        for (int ks = NQ == 2 ? BN / 32 : 0; ks < BN / 16; ++ks)
                             mma_bf16_ts(o_tmem, tmem + buf * BN + ks * 8, vd + ((ks * 2048) >> 4), id_o, j > 0 || ks > 0);
                         mma_commit(o_done + t);
                         mma_commit(empty + v);
                     }
                     __syncwarp();
-                    if (NQ == 2 && j + 1 < n && !scores(j + 1)) goto done;
+                    if (NQ == 2 && j + 1 < n) scores(j + 1);
                 }
             }
         } else if (warp == kFixWarp) {
             // ------------------------------------------------------------ non-finite V values
-            uint32_t n_item = 0;
-            for (long idx = blockIdx.x; get_item<DP>(p, suffix, idx, it); idx += step, seq += 2 * it.tiles, ++n_item) {
+            for (; next_item(); seq += 2 * it.tiles) {
                 for (int j = 0; j < it.tiles; ++j) {
                     // every V tile is waited for, so that no phase of its barrier goes by unseen
                     const uint32_t s = seq + 2 * j + 1, slot = slot_of(s);
@@ -416,7 +446,7 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                         tile[i] = make_uint4(mend(x.x), mend(x.y), mend(x.z), mend(x.w));
                         bad = true;
                     }
-                    if (bad) s_bad[n_item & 3] = (int)n_item + 1;
+                    if (bad) s_bad[n_item & 3] = (int)n_item;
                     fence_async_smem();
                     mbar_arrive(v_fixed + slot);
                 }
@@ -428,9 +458,9 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
         const int t = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t o_col = lanes + C::COL_O + t * DP;
-        uint32_t s_phase = 0, o_count = 0, n_item = 0, turn_phase = 0;
+        uint32_t s_phase = 0, o_count = 0, turn_phase = 0;
         if (NQ == 2 && t == 1) mbar_arrive(turn + 0);  // query tile 0 goes first
-        for (long idx = blockIdx.x; get_item<DP>(p, suffix, idx, it); idx += step, ++n_item) {
+        while (next_item()) {
             const int shift = it.kv - it.len, r = it.row0 + t * 128 + row;
             const int n = NQ == 2 && t ? it.n[1] : it.n[0];
             const int least = shift + it.row0 + t * 128 + 1;  // keys that the tile's first row sees
@@ -505,6 +535,11 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                         pk[i] = *reinterpret_cast<const uint32_t *>(&h);
                     }
                     tmem_st32(s_col + c * 32, pk);
+                    if (NQ == 2 && c == 0) {
+                        tmem_wait_st();
+                        tc_fence_before();
+                        mbar_arrive(p_half + buf);
+                    }
                 }
                 if (NQ == 2) mbar_arrive(turn + 1 - t);
                 l += sum.x + sum.y;
@@ -522,10 +557,11 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                 tc_fence_after();
             }
             const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (NaN stays)
-            const bool bad = n > 0 && s_bad[n_item & 3] == (int)n_item + 1;
+            const bool bad = n > 0 && s_bad[n_item & 3] == (int)n_item;
             const int seen = min(it.kv, shift + r + 1);
-            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) +
-                                 ((size_t)(it.start + r) * p.a.H + it.h) * p.a.D;
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) +  // of the warp's first row
+                                 ((size_t)(it.start + r - lane) * p.a.H + it.h) * p.a.D;
+            uint4 *stage = reinterpret_cast<uint4 *>(staging) + warp * 128;
 #pragma unroll 1
             for (int c = 0; c < DP; c += 32) {
                 __syncwarp();
@@ -552,15 +588,23 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                                 if (!isfinite(y)) f[i] += y;
                             }
                     }
-                if (r < it.len)
+                // through shared memory, so that a store covers runs of 64 bytes of 8 rows
+                __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8)
-                        if (c + i < p.a.D) {
-                            Vec16<__nv_bfloat16> w;
+                for (int i = 0; i < 4; ++i) {
+                    Vec16<__nv_bfloat16> w;
 #pragma unroll
-                            for (int z = 0; z < 8; ++z) w.v[z] = __float2bfloat16_rn(f[i + z]);
-                            *reinterpret_cast<uint4 *>(out + c + i) = w.u;
-                        }
+                    for (int z = 0; z < 8; ++z) w.v[z] = __float2bfloat16_rn(f[i * 8 + z]);
+                    stage[lane * 4 + (i ^ ((lane >> 1) & 3))] = w.u;
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int sr = i * 8 + (lane >> 2), sc = lane & 3;
+                    const uint4 w = stage[sr * 4 + (sc ^ ((sr >> 1) & 3))];
+                    if (r - lane + sr < it.len && c + sc * 8 < p.a.D)
+                        *reinterpret_cast<uint4 *>(out + (long)sr * p.a.H * p.a.D + c + sc * 8) = w;
+                }
             }
             tc_fence_before();  // the next item's products follow this tile's next arrival
         }
@@ -627,7 +671,7 @@ cudaError_t launch(const Attn &a, int min_rows, cudaStream_t s) {
         !encode_rows(&vm, a.v, kv_rows, a.HKV, a.D, a.vs, p.box_rows))
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> attr_set{0};
-    constexpr size_t kFixed = (size_t)C::NQ * C::QBYTES + C::SLOTS * C::SLOT + 256 + 1024;
+    constexpr size_t kFixed = (size_t)C::NQ * C::QBYTES + C::SLOTS * C::SLOT + C::STAGING + 512 + 1024;
     cudaError_t e = once_per_device(attr_set, [] {
         return cudaFuncSetAttribute(attn_prompt_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)(kFixed + (kMaxBins + 1) * 4));
