@@ -40,7 +40,7 @@ namespace {
 using namespace sm100;
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
-constexpr int kMaxBins = 2048;  // bins of the longest-first order
+constexpr int kMaxBins = 4096;  // bins of the longest-first order
 constexpr float kLazy = 8.f;    // growth of the row maximum (log2) that O waits for
 
 // Set when a bounded wait of an attention kernel has given up.
@@ -60,7 +60,6 @@ struct Cfg {
     static constexpr int NB = DP / 64;             // 64-channel blocks (128 swizzled bytes a row)
     static constexpr int QBYTES = 128 * DP * 2, SLOT = BN * DP * 2;
     static constexpr int SLOTS = 4;
-    static constexpr int STAGING = NQ * 4 * 2048;  // 32 rows of 32 outputs for each softmax warp
     static constexpr int THREADS = NQ * 128 + 128;
     // registers a thread at launch and after the split: a softmax thread holds a row of scores
     static constexpr int REGS = 65536 / THREADS / 8 * 8 > 255 ? 248 : 65536 / THREADS / 8 * 8;
@@ -78,6 +77,7 @@ struct PromptParams {
     int min_rows;   // sequences with at most this many (query, head of a group) rows are not ours
     float c;        // |scale| log2(e)
     int negate;     // scale < 0
+    int out32;      // output rows lie on 32-byte boundaries
 };
 
 // Warp-wide mbarrier wait that gives up, for the whole warp, after kWaitLimitNs
@@ -125,6 +125,19 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         : "memory");
 }
 
+// Orders every use of loaded registers after the wait before it, for the compiler.
+__device__ __forceinline__ void landed(uint32_t (&r)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+        asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                     "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+// 32 bytes, to a 32-byte boundary.
+__device__ __forceinline__ void store32(void *dst, const uint32_t *w) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
 // True in one lane of the converged warp.
 __device__ __forceinline__ bool elect_one() {
     uint32_t one;
@@ -211,8 +224,8 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    unsigned char *sq = smem, *ring = smem + NQ * C::QBYTES, *staging = ring + SLOTS * C::SLOT;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(staging + C::STAGING);
+    unsigned char *sq = smem, *ring = smem + NQ * C::QBYTES;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(ring + SLOTS * C::SLOT);
     uint64_t *full = bars, *empty = full + SLOTS, *q_full = empty + SLOTS, *q_empty = q_full + 2,
              *s_full = q_empty + 2, *p_full = s_full + 2, *o_done = p_full + 2, *v_fixed = o_done + 2, *turn = v_fixed + SLOTS,
              *p_half = turn + 2, *item_full = p_half + 2, *item_empty = item_full + 4;
@@ -418,7 +431,7 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
 #pragma unroll
                         for (int ks = NQ == 2 ? BN / 32 : 0; ks < BN / 16; ++ks)
                             mma_bf16_ts(o_tmem, tmem + buf * BN + ks * 8, vd + ((ks * 2048) >> 4), id_o, j > 0 || ks > 0);
-                        mma_commit(o_done + t);
+                        mma_commit(o_done + buf);
                         mma_commit(empty + v);
                     }
                     __syncwarp();
@@ -458,7 +471,8 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
         const int t = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t o_col = lanes + C::COL_O + t * DP;
-        uint32_t s_phase = 0, o_count = 0, turn_phase = 0;
+        uint32_t s_phase = 0, turn_phase = 0;
+        uint32_t o_phase = 0;  // a bit for each score buffer: products with its P so far, mod 2
         if (NQ == 2 && t == 1) mbar_arrive(turn + 0);  // query tile 0 goes first
         while (next_item()) {
             const int shift = it.kv - it.len, r = it.row0 + t * 128 + row;
@@ -485,6 +499,8 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < BN / 32; ++c) tmem_ld32(s_col + c * 32, x[c]);
                 tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < BN / 32; ++c) landed(x[c]);
                 if ((j + 1) * BN > least) {  // some row does not see all of these keys
                     const int seen = shift + r + 1 - j * BN;
 #pragma unroll
@@ -506,13 +522,15 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                     const float f = move ? exp2_fast((m - top) * p.c) : 1.f;
                     if (move) m = top, l *= f;
                     // (j > 0 here: a first tile sets m itself)
-                    if (!wait_or_abort(o_done + t, (o_count - 1) & 1, abort)) goto done;
+                    const int prev = NQ == 2 ? t : buf ^ 1;
+                    if (!wait_or_abort(o_done + prev, ((o_phase >> prev) & 1) ^ 1, abort)) goto done;
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < DP; c += 32) {
                         uint32_t o[32];
                         tmem_ld32(o_col + c, o);
                         tmem_wait_ld();
+                        landed(o);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
                         tmem_st32(o_col + c, o);
@@ -546,22 +564,18 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(p_full + buf);
-                ++o_count;
+                o_phase ^= 1u << buf;
             }
             // ---- out = O / l
-            // (the scores of the last key tile were committed after the products before the last
-            // one but, with a single query tile, not after that one: wait for both in turn)
             if (n > 0) {
-                if (NQ == 1 && n > 1 && !wait_or_abort(o_done + t, o_count & 1, abort)) goto done;
-                if (!wait_or_abort(o_done + t, (o_count - 1) & 1, abort)) goto done;
+                const int prev = NQ == 2 ? t : (n - 1) & 1;
+                if (!wait_or_abort(o_done + prev, ((o_phase >> prev) & 1) ^ 1, abort)) goto done;
                 tc_fence_after();
             }
             const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (NaN stays)
             const bool bad = n > 0 && s_bad[n_item & 3] == (int)n_item;
             const int seen = min(it.kv, shift + r + 1);
-            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) +  // of the warp's first row
-                                 ((size_t)(it.start + r - lane) * p.a.H + it.h) * p.a.D;
-            uint4 *stage = reinterpret_cast<uint4 *>(staging) + warp * 128;
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) + ((size_t)(it.start + r) * p.a.H + it.h) * p.a.D;
 #pragma unroll 1
             for (int c = 0; c < DP; c += 32) {
                 __syncwarp();
@@ -569,14 +583,16 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                 if (n > 0) {
                     tmem_ld32(o_col + c, o);
                     tmem_wait_ld();
+                    landed(o);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = 0u;
                 }
+                if (r >= it.len) continue;
                 float f[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) f[i] = l != 0.f ? __uint_as_float(o[i]) * inv : 0.f;
-                if (bad && r < it.len)
+                if (bad)
                     for (int j = it.fix * BN; j < seen; ++j) {
                         const long at = attn_key_row(p.a, it.b, it.start, j, p.a.vs);
                         if (at < 0) continue;
@@ -588,24 +604,23 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                                 if (!isfinite(y)) f[i] += y;
                             }
                     }
-                // through shared memory, so that a store covers runs of 64 bytes of 8 rows
-                __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    Vec16<__nv_bfloat16> w;
+                for (int i = 0; i < 32; i += 16) {
+                    uint32_t w[8];
 #pragma unroll
-                    for (int z = 0; z < 8; ++z) w.v[z] = __float2bfloat16_rn(f[i * 8 + z]);
-                    stage[lane * 4 + (i ^ ((lane >> 1) & 3))] = w.u;
-                }
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int sr = i * 8 + (lane >> 2), sc = lane & 3;
-                    const uint4 w = stage[sr * 4 + (sc ^ ((sr >> 1) & 3))];
-                    if (r - lane + sr < it.len && c + sc * 8 < p.a.D)
-                        *reinterpret_cast<uint4 *>(out + (long)sr * p.a.H * p.a.D + c + sc * 8) = w;
+                    for (int z = 0; z < 8; ++z) {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(f[i + 2 * z], f[i + 2 * z + 1]);
+                        w[z] = *reinterpret_cast<const uint32_t *>(&h);
+                    }
+                    if (p.out32) {
+                        if (c + i < p.a.D) store32(out + c + i, w);
+                    } else {
+                        if (c + i < p.a.D) *reinterpret_cast<uint4 *>(out + c + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                        if (c + i + 8 < p.a.D) *reinterpret_cast<uint4 *>(out + c + i + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                    }
                 }
             }
+            __syncwarp();
             tc_fence_before();  // the next item's products follow this tile's next arrival
         }
     }
@@ -658,6 +673,7 @@ cudaError_t launch(const Attn &a, int min_rows, cudaStream_t s) {
     p.min_rows = min_rows;
     p.c = std::fmax(std::fabs(a.scale) * kLog2e, 1e-30f);
     p.negate = a.scale < 0.f;
+    p.out32 = ((uintptr_t)a.out & 31) == 0 && a.D % 16 == 0;
     const bool paged = a.block_table != nullptr;
     p.box_rows = C::BN;
     if (paged) while (a.page_size % p.box_rows != 0) p.box_rows /= 2;
@@ -671,7 +687,7 @@ cudaError_t launch(const Attn &a, int min_rows, cudaStream_t s) {
         !encode_rows(&vm, a.v, kv_rows, a.HKV, a.D, a.vs, p.box_rows))
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> attr_set{0};
-    constexpr size_t kFixed = (size_t)C::NQ * C::QBYTES + C::SLOTS * C::SLOT + C::STAGING + 512 + 1024;
+    constexpr size_t kFixed = (size_t)C::NQ * C::QBYTES + C::SLOTS * C::SLOT + 512 + 1024;
     cudaError_t e = once_per_device(attr_set, [] {
         return cudaFuncSetAttribute(attn_prompt_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)(kFixed + (kMaxBins + 1) * 4));
