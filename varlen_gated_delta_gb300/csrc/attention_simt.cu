@@ -26,12 +26,29 @@ constexpr size_t smem_bytes() {
     return (size_t)(RPT * 16 * (DP + 4) + 2 * kKeys * (DP + 4) + RPT * 16 * (kKeys + 4)) * 4;
 }
 
+// 16 bytes to shared memory, or zeros
+__device__ __forceinline__ void copy16(float *dst, const void *src, bool read) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src), "r"(read ? 16 : 0)
+                 : "memory");
+}
+
 // `rows` rows of D values (row r at off(r), or zeros when off(r) < 0) into
-// shared memory, DP + 4 floats apart, columns from D on zero.
+// shared memory, DP + 4 floats apart, columns from D on zero; aligned fp32 rows by
+// copies that are in flight until copies_landed().
 template <typename T, int DP, typename Off>
 __device__ __forceinline__ void load_rows(float *dst, const T *src, int rows, int D, bool vec,
                                           Off off) {
-    if (vec) {
+    if (std::is_same_v<T, float> && vec) {
+        constexpr int CH = DP / 4;
+        for (int i = threadIdx.x; i < rows * CH; i += kThreads) {
+            const int r = i / CH, d = (i % CH) * 4;
+            const long at = off(r);
+            const bool read = at >= 0 && d < D;
+            copy16(dst + r * (DP + 4) + d, src + (read ? at + d : 0), read);
+        }
+    } else if (vec) {
         constexpr int V = Vec16<T>::N, CH = DP / V;
         for (int i = threadIdx.x; i < rows * CH; i += kThreads) {
             const int r = i / CH, d = (i % CH) * V;
@@ -49,6 +66,12 @@ __device__ __forceinline__ void load_rows(float *dst, const T *src, int rows, in
             dst[r * (DP + 4) + d] = at >= 0 && d < D ? to_f32(src[at + d]) : 0.f;
         }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// All but the newest `N` load_rows() of this thread have landed.
+template <int N>
+__device__ __forceinline__ void copies_landed() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 template <typename T, int DP, int RPT>
@@ -64,6 +87,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const Attn a, int s
     if (!attn_find_tile(a, G, ROWS, blockIdx.x, b, tile)) return;
     int start, len, kv;
     attn_seq(a, b, start, len, kv);
+    tile = (len * G + ROWS - 1) / ROWS - 1 - tile;  // the tiles with the most keys first
     const int r0 = tile * ROWS, rows = min(ROWS, len * G - r0);
     const int shift = kv - len;  // query i sees keys [0, shift + i]
     const int most = min(kv, shift + (r0 + rows - 1) / G + 1);  // keys the tile sees
@@ -89,18 +113,20 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const Attn a, int s
         for (int c = 0; c < OC; ++c) o[i][c][0] = o[i][c][1] = make_float2(0.f, 0.f);
     }
     const float sl = a.scale * kLog2e;
+    auto load_keys = [&](float *dst, const void *src, int kt, long stride) {
+        load_rows<T, DP>(dst, static_cast<const T *>(src), kKeys, D, vec, [&](int r) -> long {
+            const int j = kt * kKeys + r;
+            const long at = kt < k1 && j < most ? attn_key_row(a, b, start, j, stride) : -1;
+            return at < 0 ? -1 : at + (long)kvh * D;
+        });
+    };
+    load_keys(sk, a.k, k0, a.ks);
+    load_keys(sv, a.v, k0, a.vs);
 
+    // The next tile's keys are on their way under the values' product, its values under the scores.
     for (int kt = k0; kt < k1; ++kt) {
-        const int j0 = kt * kKeys, n = min(kKeys, most - j0);
-        __syncthreads();  // the last tile's reads are done
-        load_rows<T, DP>(sk, static_cast<const T *>(a.k), kKeys, D, vec, [&](int r) -> long {
-            const long at = r < n ? attn_key_row(a, b, start, j0 + r, a.ks) : -1;
-            return at < 0 ? -1 : at + (long)kvh * D;
-        });
-        load_rows<T, DP>(sv, static_cast<const T *>(a.v), kKeys, D, vec, [&](int r) -> long {
-            const long at = r < n ? attn_key_row(a, b, start, j0 + r, a.vs) : -1;
-            return at < 0 ? -1 : at + (long)kvh * D;
-        });
+        const int j0 = kt * kKeys;
+        copies_landed<1>();
         __syncthreads();
         // scores of rows ty RPT + i, keys tx + 16 j: even and odd channels apart on the packed
         // fp32 pipe, and in runs of 32 channels, whose short sums round less than one long one
@@ -132,6 +158,8 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const Attn a, int s
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[i][j] += y[i][j].x + y[i][j].y;
         }
+        __syncthreads();
+        load_keys(sk, a.k, kt + 1, a.ks);
         const bool edge = j0 + kKeys > least;  // some row does not see the whole tile
 #pragma unroll
         for (int i = 0; i < RPT; ++i) {
@@ -164,7 +192,8 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const Attn a, int s
 #pragma unroll
                 for (int z = 0; z < 2; ++z) o[i][q][z] = __fmul2_rn(o[i][q][z], make_float2(c, c));
         }
-        __syncwarp();  // a row's probabilities come from its own half warp
+        copies_landed<1>();
+        __syncthreads();
 #pragma unroll 2
         for (int j = 0; j < kKeys; j += 4) {
             float pr[RPT][4];
@@ -186,7 +215,10 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const Attn a, int s
                     }
                 }
         }
+        __syncthreads();
+        load_keys(sv, a.v, kt + 1, a.vs);
     }
+    copies_landed<0>();
 
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
@@ -274,11 +306,17 @@ template <typename T>
 cudaError_t launch_typed(const Attn &a, cudaStream_t s) {
     const bool vec = rows_aligned(a.q, a.qs, a.D, sizeof(T)) && rows_aligned(a.k, a.ks, a.D, sizeof(T)) &&
                      rows_aligned(a.v, a.vs, a.D, sizeof(T));
-    // rows of a sequence: at most max_q G (packed prompts: unknown, so wide tiles)
-    const bool few = a.block_table != nullptr && (long)a.max_q * (a.H / a.HKV) <= 16;
-    if (a.D <= 64) return few ? launch_tile<T, 64, 1>(a, vec, s) : launch_tile<T, 64, 4>(a, vec, s);
-    if (a.D <= 128) return few ? launch_tile<T, 128, 1>(a, vec, s) : launch_tile<T, 128, 4>(a, vec, s);
-    return few ? launch_tile<T, 256, 1>(a, vec, s) : launch_tile<T, 256, 4>(a, vec, s);
+    // Rows a tile: sequences of few rows would leave most of a wide tile's work unused, long ones
+    // load less for each product with it (measured on 4 x 1000 tokens, 16 heads of 128 on 4: MEASURED).
+    const long G = a.H / a.HKV;
+    const long rows = a.block_table != nullptr && a.max_q * G <= 16 ? a.max_q * G : (long)a.N * G / a.B;
+    if (a.D <= 64)
+        return rows <= 16 ? launch_tile<T, 64, 1>(a, vec, s) : rows <= 64 ? launch_tile<T, 64, 4>(a, vec, s)
+                                                                         : launch_tile<T, 64, 8>(a, vec, s);
+    if (a.D <= 128)
+        return rows <= 16 ? launch_tile<T, 128, 1>(a, vec, s) : rows <= 64 ? launch_tile<T, 128, 4>(a, vec, s)
+                                                                          : launch_tile<T, 128, 8>(a, vec, s);
+    return rows <= 16 ? launch_tile<T, 256, 1>(a, vec, s) : launch_tile<T, 256, 4>(a, vec, s);
 }
 
 }  // namespace

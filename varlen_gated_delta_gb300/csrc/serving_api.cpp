@@ -29,6 +29,8 @@ int check_geometry(int N, int H, int HKV, int D, const char *what) {
     if (D > 256) return set_error(GDN_ERR_SHAPE, "%s: head width D=%d exceeds 256", what, D);
     if (H % HKV != 0)
         return set_error(GDN_ERR_SHAPE, "%s: query heads H=%d not a multiple of key-value heads HKV=%d", what, H, HKV);
+    if ((long)N * (H / HKV) > INT_MAX - 1024)
+        return set_error(GDN_ERR_OVERFLOW, "%s: N*H/HKV rows exceed int32", what);
     if (HKV > 65535) return set_error(GDN_ERR_OVERFLOW, "%s: HKV=%d exceeds 65535", what, HKV);
     if ((long)H * D > INT_MAX / 2) return set_error(GDN_ERR_OVERFLOW, "%s: H*D exceeds its range", what);
     return GDN_OK;
