@@ -56,7 +56,6 @@ template <int DP>
 struct Cfg {
     static constexpr int NQ = DP > 128 ? 1 : 2;    // query tiles of a CTA
     static constexpr int BN = DP > 128 ? 64 : 128; // keys of a tile
-    static constexpr int TM = NQ * 128;            // queries of an item
     static constexpr int NB = DP / 64;             // 64-channel blocks (128 swizzled bytes a row)
     static constexpr int QBYTES = 128 * DP * 2, SLOT = BN * DP * 2;
     static constexpr int SLOTS = 4;
@@ -72,6 +71,8 @@ struct Cfg {
 struct PromptParams {
     Attn a;
     int G;
+    int tm;         // queries of an item along its sequence
+    int pair;       // its two query tiles are two heads of a group (else 256 queries of one head)
     int box_rows;   // key rows of a TMA box
     int bins, bin_shift;
     int min_rows;   // sequences with at most this many (query, head of a group) rows are not ours
@@ -145,7 +146,7 @@ __device__ __forceinline__ bool elect_one() {
     return one != 0;
 }
 
-// One item: TM queries from row0 on of one head of sequence b.
+// One item: tm queries of sequence b from row0 on, of head h (and h + 1 with pair).
 struct Item {
     int b, h, start, len, kv, row0;
     int n[2];     // key tiles of each query tile (0: no rows, or none that sees a key)
@@ -157,7 +158,7 @@ template <int DP>
 __device__ __forceinline__ int seq_tiles(const PromptParams &p, int b) {
     int start, len, kv;
     if (!attn_seq(p.a, b, start, len, kv) || (long)len * p.G <= p.min_rows) return 0;
-    return (len + Cfg<DP>::TM - 1) / Cfg<DP>::TM;
+    return (len + p.tm - 1) / p.tm;
 }
 
 // Tiles of a sequence of n tiles that fall into bin.
@@ -170,10 +171,10 @@ template <int DP>
 __device__ __forceinline__ bool get_item(const PromptParams &p, const int *suffix, long idx, Item &it) {
     using C = Cfg<DP>;
     const int lane = threadIdx.x & 31;
-    const long total = (long)suffix[0] * p.a.H;
-    if (idx >= total) return false;
-    int rank = (int)(idx / p.a.H);
-    it.h = (int)(idx % p.a.H);
+    const int heads = p.pair ? p.a.H >> 1 : p.a.H;
+    if (idx >= (long)suffix[0] * heads) return false;
+    int rank = (int)(idx / heads);
+    it.h = (int)(idx % heads) << p.pair;
     int lo = 0, hi = p.bins - 1;  // the bin with suffix[bin + 1] <= rank < suffix[bin]
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -199,12 +200,12 @@ __device__ __forceinline__ bool get_item(const PromptParams &p, const int *suffi
         it.b = b0 + at;
         const int level = (lo << p.bin_shift) + mine - 1 - (rank - before);
         attn_seq(p.a, it.b, it.start, it.len, it.kv);
-        it.row0 = level * C::TM;
+        it.row0 = level * p.tm;
         it.tiles = 0;
         const int shift = it.kv - it.len;
 #pragma unroll
         for (int t = 0; t < C::NQ; ++t) {
-            const int r = it.row0 + t * 128, rows = min(128, it.len - r);
+            const int r = it.row0 + (p.pair ? 0 : t * 128), rows = min(128, it.len - r);
             const int most = rows > 0 ? min(it.kv, shift + r + rows) : 0;
             it.n[t] = most > 0 ? (most + C::BN - 1) / C::BN : 0;
             it.tiles = max(it.tiles, it.n[t]);
@@ -329,8 +330,8 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                     if (lane == 0) {
                         mbar_arrive_expect_tx(q_full + t, C::QBYTES);
                         for (int c = 0; c < NB; ++c)
-                            tma_load_3d(sq + t * C::QBYTES + c * 128 * 128, &qmap, q_full + t, c * 64, it.h,
-                                        it.start + it.row0 + t * 128);
+                            tma_load_3d(sq + t * C::QBYTES + c * 128 * 128, &qmap, q_full + t, c * 64,
+                                        it.h + (p.pair ? t : 0), it.start + it.row0 + (p.pair ? 0 : t * 128));
                     }
                 }
                 for (int j = 0; j < it.tiles; ++j) {
@@ -475,9 +476,9 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
         uint32_t o_phase = 0;  // a bit for each score buffer: products with its P so far, mod 2
         if (NQ == 2 && t == 1) mbar_arrive(turn + 0);  // query tile 0 goes first
         while (next_item()) {
-            const int shift = it.kv - it.len, r = it.row0 + t * 128 + row;
+            const int shift = it.kv - it.len, first = it.row0 + (p.pair ? 0 : t * 128), r = first + row;
             const int n = NQ == 2 && t ? it.n[1] : it.n[0];
-            const int least = shift + it.row0 + t * 128 + 1;  // keys that the tile's first row sees
+            const int least = shift + first + 1;  // keys that the tile's first row sees
             float m = -INFINITY, l = 0.f;
             for (int j = 0; j < it.tiles; ++j) {
                 if (j >= n) {  // only the other query tile sees these keys
@@ -575,7 +576,7 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
             const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (NaN stays)
             const bool bad = n > 0 && s_bad[n_item & 3] == (int)n_item;
             const int seen = min(it.kv, shift + r + 1);
-            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) + ((size_t)(it.start + r) * p.a.H + it.h) * p.a.D;
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) + ((size_t)(it.start + r) * p.a.H + it.h + (p.pair ? t : 0)) * p.a.D;
 #pragma unroll 1
             for (int c = 0; c < DP; c += 32) {
                 __syncwarp();
@@ -677,7 +678,11 @@ cudaError_t launch(const Attn &a, int min_rows, cudaStream_t s) {
     const bool paged = a.block_table != nullptr;
     p.box_rows = C::BN;
     if (paged) while (a.page_size % p.box_rows != 0) p.box_rows /= 2;
-    const long levels = ((long)a.max_q + C::TM - 1) / C::TM;
+    // Two heads of a group see the same keys to the same extent, and an item of 128 queries leaves
+    // less of a short sequence unused than one of 256.
+    p.pair = C::NQ == 2 && p.G % 2 == 0;
+    p.tm = p.pair ? 128 : C::NQ * 128;
+    const long levels = ((long)a.max_q + p.tm - 1) / p.tm;
     while (((levels + (1L << p.bin_shift) - 1) >> p.bin_shift) > kMaxBins) ++p.bin_shift;
     p.bins = (int)((levels + (1L << p.bin_shift) - 1) >> p.bin_shift);
     const long kv_rows = paged ? (long)a.num_pages * a.page_size : a.N;
@@ -696,7 +701,7 @@ cudaError_t launch(const Attn &a, int min_rows, cudaStream_t s) {
     int dev = 0, sms = 0;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const long items = ((long)a.N / C::TM + a.B) * a.H;
+    const long items = ((long)a.N / p.tm + a.B) * (a.H >> p.pair);
     const long grid = items < sms ? items : sms;
     e = launch_kernel(attn_prompt_kernel<DP>, dim3((unsigned)grid), dim3(C::THREADS), kFixed + (p.bins + 1) * 4, s,
                       false, qm, km, vm, p);
