@@ -10,7 +10,7 @@
 // A CTA holds a pair of query tiles (one for D > 128) and every key tile it
 // loads serves both.  Warp roles: one softmax warpgroup per query tile (a thread
 // owns a row, so row maxima and sums need no exchange), one MMA warp per query
-// tile, one TMA warp, one warp that mends V tiles.  S and O live in tensor memory;
+// tile, one TMA warp, one warp for the end of V.  S and O live in tensor memory;
 // P replaces S in place as bf16 (A operand of the second product, read from
 // tensor memory).  One tile's softmax runs under the other's products; with a
 // single query tile S is double buffered instead and the scores of the next key
@@ -20,11 +20,11 @@
 // last time: P then stays below 2^8, with the same relative precision, and
 // the division by l at the end uses the same reference.
 //
-// V rows that some query of the tile must not see (later tokens, other
-// sequences, stale cache slots) meet P = 0, and 0 * inf would be NaN: in the few
-// key tiles that have masked scores, a warp replaces non-finite V values by 0
-// before the product, and, if there were any, the epilogue adds them to the rows
-// that do see them.
+// P = 0 for a masked score, and 0 * inf is NaN.  Rows of V past the end of the
+// sequence (other sequences, stale cache slots) may hold anything: a warp zeroes
+// them in shared memory before the product.  Masked tokens of the sequence itself
+// are finite in sound data: when an output is not, the epilogue looks for a
+// non-finite value among them and computes those rows again without it.
 //
 // Persistent CTAs, one per SM, take (query tile pair, head) items in a fixed
 // interleaved order, longest first by the tile's place in its sequence; heads
@@ -151,7 +151,7 @@ struct Item {
     int b, h, start, len, kv, row0;
     int n[2];     // key tiles of each query tile (0: no rows, or none that sees a key)
     int tiles;    // key tiles loaded
-    int fix;      // first key tile with masked scores
+    int end;      // rows of the last key tile that hold keys
 };
 
 template <int DP>
@@ -210,16 +210,52 @@ __device__ __forceinline__ bool get_item(const PromptParams &p, const int *suffi
             it.n[t] = most > 0 ? (most + C::BN - 1) / C::BN : 0;
             it.tiles = max(it.tiles, it.n[t]);
         }
-        it.fix = max(0, shift + it.row0 + 1) / C::BN;
+        it.end = min(C::BN, it.kv - (it.tiles - 1) * C::BN);
         return true;
     }
     return false;
 }
 
+// Warp-wide and rare.  Where V holds a non-finite value in channels c .. c + 31 of keys [k0, k1),
+// which some row of the tile does not see, the rows with `odd` compute their outputs again over the
+// `seen` keys that they do see, with the reference m and 1 / l of the softmax.
+__device__ __forceinline__ void redo_masked(const PromptParams &p, int b, int start, int row, int h, int c, int k0,
+                                         int k1, int seen, bool odd, float m, float inv) {
+    const int lane = threadIdx.x & 31, D = p.a.D, kvh = h / p.G;
+    const __nv_bfloat16 *kb = static_cast<const __nv_bfloat16 *>(p.a.k) + (long)kvh * D;
+    const __nv_bfloat16 *vb = static_cast<const __nv_bfloat16 *>(p.a.v) + (long)kvh * D;
+    bool found = false;
+    for (int j = k0 + lane; j < k1; j += 32) {
+        const long at = attn_key_row(p.a, b, start, j, p.a.vs);
+        for (int i = c; at >= 0 && i < min(c + 32, D); ++i) found |= !isfinite(__bfloat162float(vb[at + i]));
+    }
+    if (!__any_sync(0xffffffffu, found) || !odd) return;
+    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.a.q) + (long)row * p.a.qs + (long)h * D;
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) + ((size_t)row * p.a.H + h) * D;
+    const float scale = p.negate ? -p.c : p.c, ref = m == -INFINITY ? 0.f : m * p.c;
+    float f[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) f[i] = 0.f;
+    for (int j = 0; j < seen; ++j) {
+        const long ka = attn_key_row(p.a, b, start, j, p.a.ks), va = attn_key_row(p.a, b, start, j, p.a.vs);
+        if (ka < 0) continue;  // (a zero value adds nothing)
+        float x = 0.f;
+#pragma unroll 1
+        for (int d = 0; d < D; ++d) x = fmaf(__bfloat162float(q[d]), __bfloat162float(kb[ka + d]), x);
+        const float w = exp2_fast(fmaf(x, scale, -ref)) * inv;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (c + i < D) f[i] = fmaf(w, __bfloat162float(vb[va + c + i]), f[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        if (c + i < D) out[c + i] = __float2bfloat16_rn(f[i]);
+}
+
 template <int DP>
 __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
     attn_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-                       const __grid_constant__ CUtensorMap vmap, const PromptParams p) {
+                       const __grid_constant__ CUtensorMap vmap, const __grid_constant__ PromptParams p) {
     using C = Cfg<DP>;
     constexpr int NQ = C::NQ, BN = C::BN, NB = C::NB, SLOTS = C::SLOTS;
     extern __shared__ unsigned char smem_raw[];
@@ -231,8 +267,7 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
              *s_full = q_empty + 2, *p_full = s_full + 2, *o_done = p_full + 2, *v_fixed = o_done + 2, *turn = v_fixed + SLOTS,
              *p_half = turn + 2, *item_full = p_half + 2, *item_empty = item_full + 4;
     Item *s_item = reinterpret_cast<Item *>(item_empty + 4);
-    int *s_bad = reinterpret_cast<int *>(s_item + 4);  // item that had non-finite masked V values
-    int *s_abort = s_bad + 4;
+    int *s_abort = reinterpret_cast<int *>(s_item + 4);
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(s_abort + 1);
     int *suffix = s_abort + 4;  // [bins + 1]
 
@@ -254,7 +289,6 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
         }
         for (int i = 0; i < 4; ++i) mbar_init(item_full + i, 1), mbar_init(item_empty + i, NQ * 5 + 1);
         fence_mbar_init();
-        for (int i = 0; i < 4; ++i) s_bad[i] = 0;
         *s_abort = 0;
         tma_prefetch_desc(&qmap), tma_prefetch_desc(&kmap), tma_prefetch_desc(&vmap);
     }
@@ -404,7 +438,7 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                     }
                     // (all that the products wait for but P comes before P)
                     if (!wait_slot(seq + 2 * j + 1)) goto done;
-                    if (j >= it.fix) {
+                    if (j + 1 == it.tiles && it.end < BN) {
                         if (!wait_or_abort(v_fixed + v, (fix_phase >> v) & 1, abort)) goto done;
                         fix_phase ^= 1u << v;
                     }
@@ -440,27 +474,18 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                 }
             }
         } else if (warp == kFixWarp) {
-            // ------------------------------------------------------------ non-finite V values
+            // ------------------------------------------------------------ rows of V past the last key
             for (; next_item(); seq += 2 * it.tiles) {
                 for (int j = 0; j < it.tiles; ++j) {
                     // every V tile is waited for, so that no phase of its barrier goes by unseen
                     const uint32_t s = seq + 2 * j + 1, slot = slot_of(s);
                     if (!wait_or_abort(full + slot, phase_of(s), abort)) goto done;
                     if (lane == 0) mbar_arrive(empty + slot);
-                    if (j < it.fix) continue;
-                    uint4 *tile = reinterpret_cast<uint4 *>(ring + slot * C::SLOT);
-                    bool bad = false;
-#pragma unroll 8
-                    for (int i = lane; i < C::SLOT / 16; i += 32) {
-                        const uint4 x = tile[i];
-                        // an exponent of all ones carries into its value's top bit
-                        auto hit = [](uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
-                        if ((hit(x.x) | hit(x.y) | hit(x.z) | hit(x.w)) == 0) continue;
-                        auto mend = [&](uint32_t w) { return w & ~((hit(w) >> 15) * 0xffffu); };
-                        tile[i] = make_uint4(mend(x.x), mend(x.y), mend(x.z), mend(x.w));
-                        bad = true;
+                    if (j + 1 < it.tiles || it.end == BN) continue;
+                    for (int c = 0; c < NB; ++c) {
+                        uint4 *block = reinterpret_cast<uint4 *>(ring + slot * C::SLOT + c * BN * 128);
+                        for (int i = it.end * 8 + lane; i < BN * 8; i += 32) block[i] = make_uint4(0, 0, 0, 0);
                     }
-                    if (bad) s_bad[n_item & 3] = (int)n_item;
                     fence_async_smem();
                     mbar_arrive(v_fixed + slot);
                 }
@@ -505,10 +530,12 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                 if ((j + 1) * BN > least) {  // some row does not see all of these keys
                     const int seen = shift + r + 1 - j * BN;
 #pragma unroll
-                    for (int c = 0; c < BN / 32; ++c)
+                    for (int c = 0; c < BN / 32; ++c) {
+                        // bit i: key c 32 + i is seen
+                        const uint32_t bits = seen >= c * 32 + 32 ? 0xffffffffu : seen <= c * 32 ? 0u : (1u << (seen - c * 32)) - 1u;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (c * 32 + i >= seen) x[c][i] = 0xff800000u;
+                        for (int i = 0; i < 32; ++i) x[c][i] = bits & (1u << i) ? x[c][i] : 0xff800000u;
+                    }
                 }
                 float mx[4] = {m, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -574,9 +601,8 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                 tc_fence_after();
             }
             const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (NaN stays)
-            const bool bad = n > 0 && s_bad[n_item & 3] == (int)n_item;
-            const int seen = min(it.kv, shift + r + 1);
             __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) + ((size_t)(it.start + r) * p.a.H + it.h + (p.pair ? t : 0)) * p.a.D;
+            uint32_t odd = 0;  // chunks of 32 channels with values that are not finite
 #pragma unroll 1
             for (int c = 0; c < DP; c += 32) {
                 __syncwarp();
@@ -589,22 +615,15 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = 0u;
                 }
-                if (r >= it.len) continue;
                 float f[32];
+                float finite = 0.f;  // NaN when some value is not
 #pragma unroll
-                for (int i = 0; i < 32; ++i) f[i] = l != 0.f ? __uint_as_float(o[i]) * inv : 0.f;
-                if (bad)
-                    for (int j = it.fix * BN; j < seen; ++j) {
-                        const long at = attn_key_row(p.a, it.b, it.start, j, p.a.vs);
-                        if (at < 0) continue;
-                        const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(p.a.v) + at + (long)(it.h / p.G) * p.a.D;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (c + i < p.a.D) {
-                                const float y = __bfloat162float(v[c + i]);
-                                if (!isfinite(y)) f[i] += y;
-                            }
-                    }
+                for (int i = 0; i < 32; ++i) {
+                    f[i] = l != 0.f ? __uint_as_float(o[i]) * inv : 0.f;
+                    finite = fmaf(f[i], 0.f, finite);
+                }
+                if (finite != 0.f) odd |= 1u << (c >> 5);
+                if (r >= it.len) continue;
 #pragma unroll
                 for (int i = 0; i < 32; i += 16) {
                     uint32_t w[8];
@@ -622,6 +641,12 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                 }
             }
             __syncwarp();
+            if (r >= it.len) odd = 0;
+            if (__any_sync(0xffffffffu, odd != 0))
+#pragma unroll 1
+                for (int c = 0; c < DP; c += 32)
+                    redo_masked(p, it.b, it.start, it.start + r, it.h + (p.pair ? t : 0), c, max(0, least - 1),
+                                min(it.kv, n * BN), min(it.kv, shift + r + 1), (odd >> (c >> 5)) & 1, m, inv);
             tc_fence_before();  // the next item's products follow this tile's next arrival
         }
     }
