@@ -729,7 +729,7 @@ cudaError_t launch(const Attn &a, int min_rows, cudaStream_t s) {
     const long items = ((long)a.N / p.tm + a.B) * (a.H >> p.pair);
     const long grid = items < sms ? items : sms;
     e = launch_kernel(attn_prompt_kernel<DP>, dim3((unsigned)grid), dim3(C::THREADS), kFixed + (p.bins + 1) * 4, s,
-                      false, qm, km, vm, p);
+                      true, qm, km, vm, p);
     note_launch();
     return e;
 }

@@ -27,7 +27,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kKeys = 64, kThreads = 128;
+constexpr int kKeys = 64;
 constexpr int kMaxCtas = 2 * 160;
 
 struct SplitParams {
@@ -42,16 +42,18 @@ struct SplitParams {
 template <int DP, int MT>
 struct Split {
     static constexpr int ROWS = 16 * MT;       // padded rows of a pair
-    static constexpr int WK = 4 / MT;          // warps that share the keys of a tile
+    // Wide heads leave one CTA to an SM: with rows for it, eight warps instead of four hide each
+    // other's latency (16 x 5 drafts over 4096 keys, 16 heads of 256 on 2: 65 -> 62 us).
+    static constexpr int WARPS = DP > 128 && MT > 1 ? 8 : 4, THREADS = WARPS * 32;
+    static constexpr int WK = WARPS / MT;      // warps that share the keys of a tile
+    static constexpr int COPY = kKeys / WARPS; // keys that a warp copies of a tile
     static constexpr int KW = kKeys / WK;      // keys of a warp in a tile
-    static constexpr int STAGES = DP > 128 ? 2 : 3;
+    static constexpr int STAGES = 3;
     static constexpr int HALF = kKeys * DP * 2;  // bytes of a K (or V) tile
-    // Q rows (bf16) and, at the end of a part, the joined output (fp32, WK > 1)
+    // Q rows (bf16); at the end of a part, half of the channels of the joined output (fp32)
     static constexpr int Q_BYTES = ROWS * DP * 2;
-    static constexpr int SUM_BYTES = WK > 1 ? ROWS * DP * 4 : 0;
-    static constexpr bool QREG = DP <= 128;    // Q fragments stay in registers
-    static constexpr int SCRATCH = QREG ? (Q_BYTES > SUM_BYTES ? Q_BYTES : SUM_BYTES) : Q_BYTES + SUM_BYTES;
-    static constexpr int SMEM = STAGES * 2 * HALF + SCRATCH;
+    static constexpr bool QREG = DP <= 128;      // Q fragments stay in registers
+    static constexpr int SMEM = STAGES * 2 * HALF + Q_BYTES;
     static constexpr int PART = ROWS * (2 + DP);  // floats of a part: m, l, o
 };
 
@@ -101,28 +103,32 @@ struct Cursor {
 };
 
 template <int DP, int MT>
-__global__ void __launch_bounds__(kThreads) attn_split_kernel(const SplitParams p) {
+__global__ void __launch_bounds__(Split<DP, MT>::THREADS) attn_split_kernel(const SplitParams p) {
     using C = Split<DP, MT>;
-    constexpr int CH = DP / 8, WK = C::WK, KW = C::KW, STAGES = C::STAGES;
+    constexpr int CH = DP / 8, WK = C::WK, KW = C::KW, STAGES = C::STAGES, kThreads = C::THREADS;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ long long s_scan[4];
+    __shared__ long long s_scan[C::WARPS];
     __shared__ long long s_first;
-    __shared__ int s_seq, s_bad;
-    __shared__ float s_ml[4][2][16];
+    __shared__ Cursor s_cur;
+    __shared__ int s_bad;
+    __shared__ float s_ml[C::WARPS][2][16];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t4 = lane & 3;
     const int mt = warp / WK, wk = warp % WK;  // this warp's rows and keys
     const uint32_t ring = sm100::smem_u32(smem), s_q = ring + STAGES * 2 * C::HALF;
-    float *s_sum = reinterpret_cast<float *>(smem + STAGES * 2 * C::HALF + (C::QREG ? 0 : C::Q_BYTES));
+    float *s_sum = reinterpret_cast<float *>(smem + STAGES * 2 * C::HALF);  // [ROWS][DP / 2]
     const int D = p.a.D, G = p.G, HKV = p.a.HKV;
     pdl_wait_primary();
-    pdl_launch_dependents();
+    pdl_launch_dependents();  // (the joining blocks wait for this grid's end)
 
     // ---- this CTA's run of tiles [u0, u1): threads own neighbouring sequences
     const int per = (p.a.B + kThreads - 1) / kThreads;
     long long mine = 0;
-    int start, len, kv;
-    for (int i = 0; i < per; ++i) mine += pair_tiles(p, C::ROWS, tid * per + i, start, len, kv);
+    Cursor own;  // (with one sequence a thread, all that is read of it)
+    for (int i = 0; i < per; ++i) {
+        own.b = tid * per + i;
+        mine += own.tiles = pair_tiles(p, C::ROWS, own.b, own.start, own.len, own.kv);
+    }
     long long sum = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -130,10 +136,10 @@ __global__ void __launch_bounds__(kThreads) attn_split_kernel(const SplitParams 
         if (lane >= d) sum += x;
     }
     if (lane == 31) s_scan[warp] = sum;
-    if (tid == 0) s_seq = -1, s_bad = 0;
+    if (tid == 0) s_bad = 0;
     __syncthreads();
     long long all = 0;
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < C::WARPS; ++w) {
         if (w < warp) sum += s_scan[w];
         all += s_scan[w];
     }
@@ -145,18 +151,20 @@ __global__ void __launch_bounds__(kThreads) attn_split_kernel(const SplitParams 
         long long at = (sum - mine) * HKV;
         if (u0 >= at && u0 < sum * HKV)
             for (int i = 0; i < per; ++i) {
-                const long long n = (long long)pair_tiles(p, C::ROWS, tid * per + i, start, len, kv) * HKV;
+                if (per > 1) {
+                    own.b = tid * per + i;
+                    own.tiles = pair_tiles(p, C::ROWS, own.b, own.start, own.len, own.kv);
+                }
+                const long long n = (long long)own.tiles * HKV;
                 if (u0 < at + n) {
-                    s_seq = tid * per + i, s_first = at;
+                    s_cur = own, s_first = at;
                     break;
                 }
                 at += n;
             }
     }
     __syncthreads();
-    Cursor cur;
-    cur.b = s_seq;
-    cur.tiles = pair_tiles(p, C::ROWS, cur.b, cur.start, cur.len, cur.kv);
+    Cursor cur = s_cur;
     cur.h = (int)((u0 - s_first) / cur.tiles);
     cur.tile = (int)((u0 - s_first) % cur.tiles);
     auto advance = [&](Cursor &x) {
@@ -168,22 +176,22 @@ __global__ void __launch_bounds__(kThreads) attn_split_kernel(const SplitParams 
         while (x.tiles == 0 && x.b < p.a.B);
     };
 
-    // ---- copies: warp w brings keys 16 w .. 16 w + 15 of a tile
+    // ---- copies: warp w brings keys COPY w .. COPY (w + 1) - 1 of a tile
     const __nv_bfloat16 *kc = static_cast<const __nv_bfloat16 *>(p.a.k), *vc = static_cast<const __nv_bfloat16 *>(p.a.v);
     auto fetch = [&](const Cursor &x, int stage) {
-        const int key = x.tile * kKeys + warp * 16 + (lane & 15);
+        const int key = x.tile * kKeys + warp * C::COPY + (lane & (C::COPY - 1));
         long row = -1;
         if (key < x.kv) row = attn_key_row(p.a, x.b, x.start, key, p.a.ks);
         const uint32_t kd = ring + stage * 2 * C::HALF, vd = kd + C::HALF;
         constexpr int RPI = 32 / CH > 0 ? 32 / CH : 1;  // rows a warp copies at a time
 #pragma unroll
-        for (int i = 0; i < 16 / RPI; ++i) {
+        for (int i = 0; i < C::COPY / RPI; ++i) {
             const int r = i * RPI + (CH < 32 ? lane / CH : 0), c = lane % CH;
             const long at = __shfl_sync(0xffffffffu, row, r);
             const bool read = at >= 0 && c * 8 < D;
             const long e = read ? at + (long)x.h * D + c * 8 : 0;
-            copy16(kd + chunk_at<DP>(warp * 16 + r, c), kc + e, read);
-            copy16(vd + chunk_at<DP>(warp * 16 + r, c), vc + e, read);
+            copy16(kd + chunk_at<DP>(warp * C::COPY + r, c), kc + e, read);
+            copy16(vd + chunk_at<DP>(warp * C::COPY + r, c), vc + e, read);
         }
     };
 
@@ -361,20 +369,24 @@ __global__ void __launch_bounds__(kThreads) attn_split_kernel(const SplitParams 
                     m[z] = M, l[z] = L;
                 }
 #pragma unroll
-                for (int w = 0; w < WK; ++w) {
-                    if (wk == w) {
+                for (int half = 0; half < 2; ++half) {
 #pragma unroll
-                        for (int i = 0; i < DP / 8; ++i)
+                    for (int w = 0; w < WK; ++w) {
+                        if (wk == w) {
 #pragma unroll
-                            for (int z = 0; z < 2; ++z) {
-                                float2 *at = reinterpret_cast<float2 *>(s_sum + (mt * 16 + g + 8 * z) * DP + i * 8 + t4 * 2);
-                                float2 x = make_float2(o[i][2 * z] * f[z], o[i][2 * z + 1] * f[z]);
-                                if (w > 0) x.x += at->x, x.y += at->y;
-                                if (w == WK - 1) o[i][2 * z] = x.x, o[i][2 * z + 1] = x.y;
-                                else *at = x;
-                            }
+                            for (int i = 0; i < DP / 16; ++i)
+#pragma unroll
+                                for (int z = 0; z < 2; ++z) {
+                                    float(&v)[4] = o[half * (DP / 16) + i];
+                                    float2 *at = reinterpret_cast<float2 *>(s_sum + (mt * 16 + g + 8 * z) * (DP / 2) + i * 8 + t4 * 2);
+                                    float2 x = make_float2(v[2 * z] * f[z], v[2 * z + 1] * f[z]);
+                                    if (w > 0) x.x += at->x, x.y += at->y;
+                                    if (w == WK - 1) v[2 * z] = x.x, v[2 * z + 1] = x.y;
+                                    else *at = x;
+                                }
+                        }
+                        __syncthreads();
                     }
-                    if (w < WK - 1) __syncthreads();
                 }
             }
             if (wk == WK - 1) {  // this warp holds the joined rows mt 16 + g, + 8
@@ -430,9 +442,8 @@ __global__ void __launch_bounds__(128) attn_split_join_kernel(const SplitParams 
     const int b = blockIdx.x / p.a.HKV, h = blockIdx.x % p.a.HKV, r = blockIdx.y;
     pdl_wait_primary();
     int start, len, kv;
-    if (pair_tiles(p, C::ROWS, b, start, len, kv) == 0 || r >= len * p.G) return;
-    const int2 span = p.spans[blockIdx.x];
-    if (span.x == span.y) return;
+    const int2 span = p.spans[blockIdx.x];  // (written for the pairs of valid sequences only)
+    if (pair_tiles(p, C::ROWS, b, start, len, kv) == 0 || r >= len * p.G || span.x == span.y) return;
     auto part = [&](int c) { return p.part + (2L * c + (c == span.x)) * C::PART; };
     float M = -INFINITY, L = 0.f;
     for (int c = span.x; c <= span.y; ++c) M = fmaxf(M, part(c)[r]);
@@ -483,7 +494,7 @@ cudaError_t launch(const Attn &a, void *ws, cudaStream_t s) {
     long grid = slots < kMaxCtas ? slots : kMaxCtas;
     if (most < grid) grid = most;
     if ((long)a.B * a.HKV > INT32_MAX) return cudaErrorInvalidConfiguration;
-    e = launch_kernel(attn_split_kernel<DP, MT>, dim3((unsigned)grid), dim3(kThreads), C::SMEM, s, false, p);
+    e = launch_kernel(attn_split_kernel<DP, MT>, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, s, true, p);
     note_launch();
     if (e != cudaSuccess) return e;
     const long rows = (long)a.max_q * p.G < C::ROWS ? (long)a.max_q * p.G : C::ROWS;

@@ -123,27 +123,45 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const PagePlan p) {
         const int b = find(s_page, p.B, i), old = (s_cached[b] + ps - 1) / ps;
         p.block_table[(size_t)b * p.max_pages + old + i - s_page[b]] = __ldg(p.free_pages + cursor + i);
     }
-    for (int t = t0; t < p.N; t += step) {
-        int pos = 0, slot = -1;
-        if (t < total) {
-            const int b = find(s_ofs, p.B, t);
+    // With many tokens a thread takes four neighbouring ones: one search, and mostly one page.
+    const int run = p.N > 4 * kThreads ? 4 : 1;
+    for (long t4 = (long)run * t0; t4 < p.N; t4 += (long)run * step) {
+        int pos[4], slot[4], b = t4 < total ? find(s_ofs, p.B, (int)t4) : 0, page = -1;
+        long long base = -1;  // the first slot of `page`
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = (int)t4 + i;
+            pos[i] = 0, slot[i] = -1;
+            if (i >= run || t >= total) continue;
+            while (t >= s_ofs[b + 1]) ++b, page = -1;
             const int c = s_cached[b], old = (c + ps - 1) / ps;
-            pos = c + t - s_ofs[b];
-            const int page = pos / ps;
-            // a page of before this step, or the one that the loop above hands out
-            const long long id = page < old ? p.block_table[(size_t)b * p.max_pages + page]
-                                            : __ldg(p.free_pages + cursor + s_page[b] + page - old);
-            const long long at = id * ps + pos % ps;
-            slot = id < 0 || at > INT32_MAX ? -1 : (int)at;
+            pos[i] = c + t - s_ofs[b];
+            if (pos[i] / ps != page) {
+                page = pos[i] / ps;
+                // a page of before this step, or the one that the loop above hands out
+                base = page < old ? p.block_table[(size_t)b * p.max_pages + page]
+                                  : __ldg(p.free_pages + cursor + s_page[b] + page - old);
+                base *= ps;
+            }
+            const long long at = base + pos[i] - (long long)page * ps;
+            slot[i] = base < 0 || at > INT32_MAX ? -1 : (int)at;
         }
-        p.positions[t] = pos;
-        p.slots[t] = slot;
+        if (p.wide && run == 4 && t4 + 4 <= p.N) {
+            *reinterpret_cast<int4 *>(p.positions + t4) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+            *reinterpret_cast<int4 *>(p.slots + t4) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < run && t4 + i < p.N) p.positions[t4 + i] = pos[i], p.slots[t4 + i] = slot[i];
+        }
     }
 }
 
 }  // namespace
 
-cudaError_t launch_page_plan(const PagePlan &p, cudaStream_t s) {
+cudaError_t launch_page_plan(const PagePlan &plan, cudaStream_t s) {
+    PagePlan p = plan;
+    p.wide = (((uintptr_t)p.positions | (uintptr_t)p.slots) & 15) == 0;
     static std::atomic<uint64_t> attr_set{0};
     const size_t smem = 3 * ((size_t)p.B + 1) * 4;
     cudaError_t e = once_per_device(attr_set, [] {

@@ -7,11 +7,13 @@
 //
 // Vector kernel: a head takes D / VEC neighbouring lanes of 16 bytes each, so a
 // warp holds one or several heads; it stays with one token and walks its heads.
-// A lane's channels are then the same in every step: its weights, cosines and
-// sines are loaded once and stay in registers, and the rows stream through
-// with UNROLL loads in flight.  The partner of a channel in the half style sits
-// in the lane R / 2 channels away, at a fixed xor distance when R is a power of
-// two.  All arithmetic is fp32 with one rounding at the store.
+// A lane's channels are then the same in every step, and with rs = 1 / sqrt(mean
+// + eps) an output is rs (x A + x' B) with A = w cos and B = +- w' sin, x' and w'
+// the partner channel's: A and B are computed once and stay in registers.  In the
+// half style x' sits in the lane R / 2 channels away, at a fixed xor distance when
+// R is a power of two, and comes over in the packed type.  The rows stream
+// through with UNROLL loads in flight.  All arithmetic is fp32 with one rounding at
+// the store.
 #include "common.cuh"
 #include "serving.h"
 
@@ -20,95 +22,116 @@ namespace {
 
 constexpr int kThreads = 128;
 
-// One lane's channels d0 .. d0 + VEC of a head (LPH lanes to a head).
-template <typename T, int LPH, int UNROLL>
-__global__ void __launch_bounds__(kThreads) norm_rope_vec_kernel(const NormRope p, int splits) {
+// N (a multiple of 2) floats from an address on a boundary of min(N, 4) of them.
+template <int N>
+__device__ __forceinline__ void load_floats(const float *src, float *dst) {
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const float4 v = __ldg(reinterpret_cast<const float4 *>(src + i));
+            dst[i] = v.x, dst[i + 1] = v.y, dst[i + 2] = v.z, dst[i + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const float2 v = __ldg(reinterpret_cast<const float2 *>(src + i));
+            dst[i] = v.x, dst[i + 1] = v.y;
+        }
+    }
+}
+
+// The factors A and B of a lane's VEC channels from d0 on, for weight w (NULL: 1).
+template <int VEC, bool HALVES>
+__device__ __forceinline__ void factors(const float *w, const float *row, int d0, int R, float (&a)[VEC], float (&b)[VEC]) {
+    const int half = R >> 1, e0 = d0 < half ? d0 + half : d0 - half;  // (halves: the partner channels)
+    float other[VEC], c[VEC], sn[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) a[i] = other[i] = 1.f, b[i] = 0.f;
+    if (w != nullptr) load_floats<VEC>(w + d0, a);
+    if (d0 >= R) return;  // (R is a multiple of VEC)
+    if constexpr (HALVES) {
+        const int j0 = min(d0, e0);
+        if (w != nullptr) load_floats<VEC>(w + e0, other);
+        load_floats<VEC>(row + j0, c), load_floats<VEC>(row + half + j0, sn);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) b[i] = (d0 < half ? -sn[i] : sn[i]) * other[i], a[i] *= c[i];
+    } else {
+        load_floats<VEC / 2>(row + d0 / 2, c), load_floats<VEC / 2>(row + half + d0 / 2, sn);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) b[i] = (i & 1 ? sn[i / 2] : -sn[i / 2]) * a[i ^ 1];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) a[i] *= c[i / 2];
+    }
+}
+
+// LPH lanes to a head, a lane's channels from (lane % LPH) VEC on.
+template <typename T, int LPH, bool HALVES, int UNROLL>
+__global__ void __launch_bounds__(kThreads, 8) norm_rope_vec_kernel(const NormRope p, int splits) {
     constexpr int VEC = Vec16<T>::N, HPW = 32 / LPH, D = LPH * VEC;
     const int lane = threadIdx.x & 31;
     const long wid = (long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     const int t = (int)(wid / splits), part = (int)(wid % splits);
     if (t >= p.N) return;
-    const int d0 = (lane % LPH) * VEC, R = p.R, half = R >> 1;
-    const bool halves = p.style == GDN_ROPE_HALF;
+    const int d0 = (lane % LPH) * VEC, R = p.R;
     pdl_wait_primary();
-
-    float cs[VEC], sn[VEC];  // the rotation y = x cs + partner sn (sn holds the sign)
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) cs[i] = 1.f, sn[i] = 0.f;
-    if (R > 0) {
-        const int pos = __ldg(p.positions + t);
-        if (pos < 0 || pos >= p.max_pos) return;
-        const float *row = p.cos_sin + (size_t)pos * R;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const int d = d0 + i;
-            if (d >= R) continue;
-            const int j = halves ? (d < half ? d : d - half) : d >> 1;
-            const bool first = halves ? d < half : (d & 1) == 0;
-            cs[i] = __ldg(row + j);
-            sn[i] = first ? -__ldg(row + half + j) : __ldg(row + half + j);
-        }
-    }
+    const int pos = R > 0 ? __ldg(p.positions + t) : 0;
+    if (R > 0 && (pos < 0 || pos >= p.max_pos)) return;
+    const float *row = p.cos_sin + (size_t)pos * R;
     const int slot = p.slots ? __ldg(p.slots + t) : -1;
     const bool cached = slot >= 0 && slot < p.num_slots;
-    const T *x = static_cast<const T *>(p.qkv) + (size_t)t * p.row_stride;
-    T *q = static_cast<T *>(p.q) + (size_t)t * p.H * D;
-    T *k = p.k ? static_cast<T *>(p.k) + (size_t)t * p.HKV * D : nullptr;
-    T *kc = cached ? static_cast<T *>(p.k_cache) + (size_t)slot * p.HKV * D : nullptr;
-    T *vc = cached ? static_cast<T *>(p.v_cache) + (size_t)slot * p.HKV * D : nullptr;
-    // the warps of a token share its heads: groups of HPW heads, splits apart
-    const int heads = p.H + p.HKV + (cached ? p.HKV : 0);
-    const int lane_head = lane / LPH;
+    const T *x = static_cast<const T *>(p.qkv) + (size_t)t * p.row_stride + d0;
+    const bool turned = d0 < R;
+    const int apart = HALVES ? (R >> 1) / VEC : 0;
 
-    for (int g0 = part * HPW; g0 < heads; g0 += splits * HPW * UNROLL) {
-        Vec16<T> in[UNROLL];
+    // heads [first, last) of the row, this warp's share, through put(head - first, raw, result)
+    float a[VEC], b[VEC];
+    auto walk = [&](int first, int last, bool norm, auto put) {
+        for (int g0 = first + part * HPW + lane / LPH; g0 - lane / LPH < last; g0 += splits * HPW * UNROLL) {
+            Vec16<T> in[UNROLL];
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-            const int h = g0 + u * splits * HPW + lane_head;
-            if (h < heads) in[u].u = __ldcs(reinterpret_cast<const uint4 *>(x + (size_t)h * D + d0));
-            else in[u].u = make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-            const int h = g0 + u * splits * HPW + lane_head;
-            const bool is_q = h < p.H, is_k = !is_q && h < p.H + p.HKV;
-            const float *w = is_q ? p.qw : p.kw;
-            float f[VEC], ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) f[i] = to_f32(in[u].v[i]), ss += f[i] * f[i];
-            ss = group_sum<LPH>(ss);  // (all lanes take part, whatever their head is)
-            if (w != nullptr) {
-                const float r = rsqrtf(ss * (1.f / D) + p.eps);
-#pragma unroll
-                for (int i = 0; i < VEC; i += 4) {
-                    const float4 ww = __ldg(reinterpret_cast<const float4 *>(w + d0 + i));
-                    f[i] *= r * ww.x, f[i + 1] *= r * ww.y, f[i + 2] *= r * ww.z, f[i + 3] *= r * ww.w;
-                }
+            for (int u = 0; u < UNROLL; ++u) {
+                const int h = g0 + u * splits * HPW;
+                if (h < last) in[u].u = __ldcs(reinterpret_cast<const uint4 *>(x + (size_t)h * D));
+                else in[u].u = make_uint4(0, 0, 0, 0);
             }
-            Vec16<T> o;
-            if (halves) {
-                const int apart = half / VEC;  // lanes (0: no rotation)
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) {
+                const int h = g0 + u * splits * HPW;
+                float f[VEC], ss = 0.f;
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) f[i] = to_f32(in[u].v[i]), ss += f[i] * f[i];
+                ss = group_sum<LPH>(ss);  // (all lanes take part, whatever their head is)
+                const float r = norm ? rsqrtf(ss * (1.f / D) + p.eps) : 1.f;
+                Vec16<T> other = in[u], o;
+                if (HALVES) {
+                    other.u.x = __shfl_xor_sync(0xffffffffu, in[u].u.x, apart);
+                    other.u.y = __shfl_xor_sync(0xffffffffu, in[u].u.y, apart);
+                    other.u.z = __shfl_xor_sync(0xffffffffu, in[u].u.z, apart);
+                    other.u.w = __shfl_xor_sync(0xffffffffu, in[u].u.w, apart);
+                }
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
-                    const float other = __shfl_xor_sync(0xffffffffu, f[i], apart);
-                    o.v[i] = from_f32<T>(d0 < R ? f[i] * cs[i] + other * sn[i] : f[i]);
+                    float y = f[i] * a[i];
+                    if (turned) y = fmaf(to_f32(other.v[HALVES ? i : i ^ 1]), b[i], y);
+                    o.v[i] = from_f32<T>(y * r);
                 }
-            } else {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i)
-                    o.v[i] = from_f32<T>(d0 + i < R ? f[i] * cs[i] + f[i ^ 1] * sn[i] : f[i]);
-            }
-            if (is_q) {
-                *reinterpret_cast<uint4 *>(q + (size_t)h * D + d0) = o.u;
-            } else if (is_k) {
-                const size_t at = (size_t)(h - p.H) * D + d0;
-                if (k) *reinterpret_cast<uint4 *>(k + at) = o.u;
-                if (kc) *reinterpret_cast<uint4 *>(kc + at) = o.u;
-            } else if (h < heads) {
-                *reinterpret_cast<uint4 *>(vc + (size_t)(h - p.H - p.HKV) * D + d0) = in[u].u;
+                if (h < last) put(h - first, in[u].u, o.u);
             }
         }
-    }
+    };
+    auto at = [&](void *base, size_t token, int heads, int h) {
+        return reinterpret_cast<uint4 *>(static_cast<T *>(base) + (token * heads + h) * D + d0);
+    };
+    factors<VEC, HALVES>(p.qw, row, d0, R, a, b);
+    walk(0, p.H, p.qw != nullptr, [&](int h, uint4, uint4 y) { *at(p.q, t, p.H, h) = y; });
+    factors<VEC, HALVES>(p.kw, row, d0, R, a, b);
+    walk(p.H, p.H + p.HKV, p.kw != nullptr, [&](int h, uint4, uint4 y) {
+        if (p.k) *at(p.k, t, p.HKV, h) = y;
+        if (cached) *at(p.k_cache, slot, p.HKV, h) = y;
+    });
+    if (cached)
+        for (int h = part * HPW + lane / LPH; h < p.HKV; h += splits * HPW)
+            *at(p.v_cache, slot, p.HKV, h) = __ldcs(reinterpret_cast<const uint4 *>(x + (size_t)(p.H + p.HKV + h) * D));
 }
 
 // Any width and alignment: one warp per (token, head), channels 32 lanes apart.
@@ -166,15 +189,18 @@ __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(const NormRope 
 
 template <typename T, int LPH>
 cudaError_t launch_vec(const NormRope &p, cudaStream_t s) {
-    constexpr int kUnroll = 4, kGroup = 32 / LPH * kUnroll;
+    // (16 channels a lane in flight: with 32, the registers of bf16 rows cost more warps than they bring)
+    constexpr int kUnroll = 16 / Vec16<T>::N, kGroup = 32 / LPH * kUnroll;
     // one warp a token when tokens abound; for few, its heads go over more warps
     const int heads = p.H + 2 * p.HKV;
     int splits = 1;
     while (splits * kGroup < heads && (long)p.N * splits < 4 * 152 * 8) splits *= 2;
     const long warps = (long)p.N * splits, ctas = (warps + kThreads / 32 - 1) / (kThreads / 32);
     if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
-    const cudaError_t e = launch_kernel(norm_rope_vec_kernel<T, LPH, kUnroll>, dim3((unsigned)ctas),
-                                        dim3(kThreads), 0, s, false, p, splits);
+    const cudaError_t e =
+        p.style == GDN_ROPE_HALF
+            ? launch_kernel(norm_rope_vec_kernel<T, LPH, true, kUnroll>, dim3((unsigned)ctas), dim3(kThreads), 0, s, true, p, splits)
+            : launch_kernel(norm_rope_vec_kernel<T, LPH, false, kUnroll>, dim3((unsigned)ctas), dim3(kThreads), 0, s, true, p, splits);
     note_launch();
     return e;
 }
@@ -186,10 +212,10 @@ cudaError_t launch_typed(const NormRope &p, cudaStream_t s) {
     const int lph = p.D / VEC, half_lanes = p.R / 2 / VEC;
     const bool aligned = p.D % VEC == 0 && rows_aligned(p.qkv, p.row_stride, p.D, sizeof(T)) &&
                          at16(p.q) && at16(p.k) && at16(p.k_cache) && at16(p.v_cache) &&
-                         at16(p.qw) && at16(p.kw);
-    // the half style reaches a partner lane by xor: R a power of two of whole lanes
-    const bool reach = p.style == GDN_ROPE_PAIRS || p.R == 0 ||
-                       (p.R % (2 * VEC) == 0 && (half_lanes & (half_lanes - 1)) == 0);
+                         at16(p.qw) && at16(p.kw) && at16(p.cos_sin);
+    // whole lanes turn or do not; the half style reaches a partner lane by xor: R / 2 a power of two of them
+    const bool reach = p.style == GDN_ROPE_PAIRS ? p.R % 8 == 0
+                                                 : p.R % (2 * VEC) == 0 && (half_lanes & (half_lanes - 1)) == 0;
     if (aligned && reach) {
         if (lph == 8) return launch_vec<T, 8>(p, s);
         if (lph == 16) return launch_vec<T, 16>(p, s);
@@ -198,7 +224,7 @@ cudaError_t launch_typed(const NormRope &p, cudaStream_t s) {
     const long warps = (long)p.N * (p.H + 2 * p.HKV), ctas = (warps + kThreads / 32 - 1) / (kThreads / 32);
     if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
     const cudaError_t e = launch_kernel(norm_rope_any_kernel<T>, dim3((unsigned)ctas), dim3(kThreads), 0,
-                                        s, false, p);
+                                        s, true, p);
     note_launch();
     return e;
 }

@@ -15,6 +15,7 @@ struct PagePlan {
     const int32_t *free_pages, *cursor;
     int32_t *offsets, *kv_lens, *positions, *slots, *cursor_out, *status;
     int B, N, page_size, max_pages, n_free;
+    int wide;  // positions and slots lie on 16-byte boundaries (set by the launcher)
 };
 cudaError_t launch_page_plan(const PagePlan &p, cudaStream_t s);
 

@@ -66,7 +66,7 @@ int gdn_page_plan(const int32_t *new_lens, const int32_t *cached_lens, int32_t *
         !kv_lens || (N > 0 && (!positions || !slots)) || !cursor_out || !status)
         return set_error(GDN_ERR_NULL, "page plan: a required pointer is NULL");
     const PagePlan p{new_lens, cached_lens, block_table, free_pages, cursor, offsets, kv_lens, positions, slots,
-                     cursor_out, status, B, N, page_size, max_pages, n_free};
+                     cursor_out, status, B, N, page_size, max_pages, n_free, 0};
     return launched(launch_page_plan(p, static_cast<cudaStream_t>(stream)), "page plan kernel launch");
 }
 
