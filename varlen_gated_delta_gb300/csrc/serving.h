@@ -54,9 +54,9 @@ inline bool rows_aligned(const void *base, long stride_elems, int D, size_t esz)
            (size_t)D * esz % 16 == 0;
 }
 
-// Any type, head width and alignment, on the fp32 pipe.
-size_t attention_simt_part_floats(int B, int N, int H, int HKV, int D);
-cudaError_t launch_attention_simt(const Attn &a, int dtype, cudaStream_t s);
+// Any type, head width and alignment, with fp32 accuracy.
+size_t attention_f32_part_floats(int N, int H, int D);
+cudaError_t launch_attention_f32(const Attn &a, int dtype, cudaStream_t s);
 
 // bf16, few rows over long paged histories: sequences of at most kSplitRows
 // (query, head of a group) rows, the others are left out.

@@ -120,7 +120,7 @@ int gdn_attention_varlen(const void *q, const void *k, const void *v, const int3
     a.scale = scale == 0.f ? 1.f / std::sqrt((float)D) : scale;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     return launched(attention_prompt_supported(a, dtype) ? launch_attention_prompt(a, 0, st)
-                                                         : launch_attention_simt(a, dtype, st),
+                                                         : launch_attention_f32(a, dtype, st),
                     "attention kernel launch");
 }
 
@@ -134,9 +134,9 @@ int gdn_attention_status(void *stream) {
 
 size_t gdn_attention_paged_workspace_bytes(int B, int N, int H, int HKV, int D, int max_q) {
     if (B < 1 || max_q < 0 || check_geometry(N, H, HKV, D, "attention")) return 0;
-    const size_t simt = attention_simt_part_floats(B, N, H, HKV, D) * 4;
+    const size_t wide = attention_f32_part_floats(N, H, D) * 4;
     const size_t split = attention_split_workspace(B, H, HKV, D, max_q);
-    return round256(simt > split ? simt : split);
+    return round256(wide > split ? wide : split);
 }
 
 int gdn_attention_paged(const void *q, const void *k_cache, const void *v_cache,
@@ -174,14 +174,14 @@ int gdn_attention_paged(const void *q, const void *k_cache, const void *v_cache,
     a.qs = (long)q_stride, a.ks = a.vs = (long)HKV * D;
     a.scale = scale == 0.f ? 1.f / std::sqrt((float)D) : scale;
     a.part = static_cast<float *>(workspace);
-    a.part_floats = attention_simt_part_floats(B, N, H, HKV, D);
+    a.part_floats = attention_f32_part_floats(N, H, D);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     // Sequences of few rows run split over their keys, longer ones as prompt slices; a call
     // that may hold both launches both, and each kernel takes its own.
     const bool some_long = (long)a.max_q * (H / HKV) > kSplitRows;
     const bool split = attention_split_supported(a, dtype);
     if (some_long ? !attention_prompt_supported(a, dtype) : !split)
-        return launched(launch_attention_simt(a, dtype, st), "paged attention kernel launch");
+        return launched(launch_attention_f32(a, dtype, st), "paged attention kernel launch");
     if (split) rc = launched(launch_attention_split(a, workspace, st), "split attention kernel launch");
     if (!rc && some_long)
         rc = launched(launch_attention_prompt(a, split ? kSplitRows : 0, st), "prompt attention kernel launch");
