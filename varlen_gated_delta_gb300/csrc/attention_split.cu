@@ -269,21 +269,25 @@ __global__ void __launch_bounds__(Split<DP, MT>::THREADS) attn_split_kernel(cons
         float s[KW / 8][4];
 #pragma unroll
         for (int i = 0; i < KW / 8; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+        // (fragments are loaded one step ahead of the products that use them, here and below)
+        uint32_t qa[2][4], kb[2][KW / 16][4];
+        auto load_qk = [&](int ks) {
+            if constexpr (!C::QREG)
+                ldmatrix4(s_q + chunk_at<DP>(mt * 16 + (lane & 15), ks * 2 + (lane >> 4)), qa[ks & 1]);
+#pragma unroll
+            for (int i = 0; i < KW / 16; ++i)
+                ldmatrix4(kd + chunk_at<DP>(wk * KW + i * 16 + (lane >> 4) * 8 + (lane & 7), ks * 2 + ((lane >> 3) & 1)),
+                          kb[ks & 1][i]);
+        };
+        load_qk(0);
 #pragma unroll
         for (int ks = 0; ks < DP / 16; ++ks) {
-            uint32_t qa[4];
-            if constexpr (C::QREG) {
-#pragma unroll
-                for (int z = 0; z < 4; ++z) qa[z] = qf[ks][z];
-            } else {
-                ldmatrix4(s_q + chunk_at<DP>(mt * 16 + (lane & 15), ks * 2 + (lane >> 4)), qa);
-            }
+            if (ks + 1 < DP / 16) load_qk(ks + 1);
 #pragma unroll
             for (int i = 0; i < KW / 16; ++i) {
-                uint32_t kb[4];
-                ldmatrix4(kd + chunk_at<DP>(wk * KW + i * 16 + (lane >> 4) * 8 + (lane & 7), ks * 2 + ((lane >> 3) & 1)), kb);
-                mma16816(s[2 * i], qa, kb[0], kb[1]);
-                mma16816(s[2 * i + 1], qa, kb[2], kb[3]);
+                const uint32_t(&q)[4] = C::QREG ? qf[C::QREG ? ks : 0] : qa[ks & 1];
+                mma16816(s[2 * i], q, kb[ks & 1][i][0], kb[ks & 1][i][1]);
+                mma16816(s[2 * i + 1], q, kb[ks & 1][i][2], kb[ks & 1][i][3]);
             }
         }
         // ---- running softmax of rows g and g + 8
@@ -319,17 +323,26 @@ __global__ void __launch_bounds__(Split<DP, MT>::THREADS) attn_split_kernel(cons
             l[0] += s[i][0] + s[i][1];
             l[1] += s[i][2] + s[i][3];
         }
-        // ---- o += P V
+        // ---- o += P V: a step is 16 keys and four blocks of eight channels
+        constexpr int STEPS = KW / 16 * (CH / 4);
+        uint32_t vb[2][2][4];
+        auto load_v = [&](int step) {
+            const int i = step / (CH / 4), c = step % (CH / 4) * 4;
 #pragma unroll
-        for (int i = 0; i < KW / 16; ++i) {
+            for (int y = 0; y < 2; ++y)
+                ldmatrix4_trans(vd + chunk_at<DP>(wk * KW + i * 16 + (lane & 15), c + 2 * y + (lane >> 4)), vb[step & 1][y]);
+        };
+        load_v(0);
+#pragma unroll
+        for (int step = 0; step < STEPS; ++step) {
+            const int i = step / (CH / 4), c = step % (CH / 4) * 4;
+            if (step + 1 < STEPS) load_v(step + 1);
             const uint32_t pa[4] = {pack_bf16(s[2 * i][0], s[2 * i][1]), pack_bf16(s[2 * i][2], s[2 * i][3]),
                                     pack_bf16(s[2 * i + 1][0], s[2 * i + 1][1]), pack_bf16(s[2 * i + 1][2], s[2 * i + 1][3])};
 #pragma unroll
-            for (int c = 0; c < CH; c += 2) {
-                uint32_t vb[4];
-                ldmatrix4_trans(vd + chunk_at<DP>(wk * KW + i * 16 + (lane & 15), c + (lane >> 4)), vb);
-                mma16816(o[c], pa, vb[0], vb[1]);
-                mma16816(o[c + 1], pa, vb[2], vb[3]);
+            for (int y = 0; y < 2; ++y) {
+                mma16816(o[c + 2 * y], pa, vb[step & 1][y][0], vb[step & 1][y][1]);
+                mma16816(o[c + 2 * y + 1], pa, vb[step & 1][y][2], vb[step & 1][y][3]);
             }
         }
         stage = stage == STAGES - 1 ? 0 : stage + 1;
@@ -445,27 +458,37 @@ __global__ void __launch_bounds__(128) attn_split_join_kernel(const SplitParams 
     const int2 span = p.spans[blockIdx.x];  // (written for the pairs of valid sequences only)
     if (pair_tiles(p, C::ROWS, b, start, len, kv) == 0 || r >= len * p.G || span.x == span.y) return;
     auto part = [&](int c) { return p.part + (2L * c + (c == span.x)) * C::PART; };
+    // every part's weight first (a history over many CTAs has many parts), then the weighted sum
+    __shared__ float s_w[kMaxCtas], s_red[2][4];
+    const int tid = threadIdx.x, n = span.y - span.x + 1;
     float M = -INFINITY, L = 0.f;
-    for (int c = span.x; c <= span.y; ++c) M = fmaxf(M, part(c)[r]);
-    float o[(DP + 127) / 128] = {};
-    for (int c = span.x; c <= span.y; ++c) {
-        const float *x = part(c);
-        const float mc = x[r], f = mc == -INFINITY ? 1.f : exp2_fast((mc - M) * p.c);
-        L += x[C::ROWS + r] * f;
+    for (int i = tid; i < n; i += 128) M = fmaxf(M, part(span.x + i)[r]);
 #pragma unroll
-        for (int i = 0; i < (DP + 127) / 128; ++i)
-            if (i * 128 + threadIdx.x < DP) {
-                const float v = x[2 * C::ROWS + r * DP + i * 128 + threadIdx.x];
-                o[i] += f > 0.f ? v * f : 0.f;  // (a part that counts for nothing may hold inf)
-            }
+    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    if ((tid & 31) == 0) s_red[0][tid >> 5] = M;
+    __syncthreads();
+    M = fmaxf(fmaxf(s_red[0][0], s_red[0][1]), fmaxf(s_red[0][2], s_red[0][3]));
+    for (int i = tid; i < n; i += 128) {
+        const float *x = part(span.x + i);
+        const float mc = x[r], f = mc == -INFINITY ? 1.f : exp2_fast((mc - M) * p.c);
+        s_w[i] = f;
+        L += x[C::ROWS + r] * f;
     }
-    const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+    L = group_sum<32>(L);
+    if ((tid & 31) == 0) s_red[1][tid >> 5] = L;
+    __syncthreads();
+    L = s_red[1][0] + s_red[1][1] + s_red[1][2] + s_red[1][3];
+    const float inv = L > 0.f ? 1.f / L : L;  // (0 gives 0, NaN stays)
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) +
                          ((size_t)(start + r / p.G) * p.a.H + h * p.G + r % p.G) * p.a.D;
-#pragma unroll
-    for (int i = 0; i < (DP + 127) / 128; ++i) {
-        const int d = i * 128 + threadIdx.x;
-        if (d < p.a.D) out[d] = __float2bfloat16_rn(L != 0.f ? o[i] * inv : 0.f);
+    for (int d = tid; d < p.a.D; d += 128) {
+        float o = 0.f;
+#pragma unroll 8
+        for (int i = 0; i < n; ++i) {
+            const float f = s_w[i], v = part(span.x + i)[2 * C::ROWS + r * DP + d];
+            o += f > 0.f ? v * f : 0.f;  // (a part that counts for nothing may hold inf)
+        }
+        out[d] = __float2bfloat16_rn(L != 0.f ? o * inv : 0.f);
     }
 }
 
