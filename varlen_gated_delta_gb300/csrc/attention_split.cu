@@ -28,7 +28,7 @@ namespace gdn {
 namespace {
 
 constexpr int kKeys = 64;
-constexpr int kMaxCtas = 2 * 160;
+constexpr int kMaxCtas = 3 * 160;
 
 struct SplitParams {
     Attn a;
@@ -53,7 +53,11 @@ struct Split {
     // Q rows (bf16); at the end of a part, half of the channels of the joined output (fp32)
     static constexpr int Q_BYTES = ROWS * DP * 2;
     static constexpr bool QREG = DP <= 128;      // Q fragments stay in registers
-    static constexpr int SMEM = STAGES * 2 * HALF + Q_BYTES;
+    // With one row group Q comes with its part's first tile, in the same stage, so that a part
+    // begins without a load of its own to wait for (64 x U[1, 8192] keys, 32 heads of 128 on 8: 166 -> 160 us).
+    static constexpr bool QSTAGE = QREG && MT == 1;
+    static constexpr int SMEM = STAGES * 2 * HALF + (QSTAGE ? 1 + STAGES : 1) * Q_BYTES;
+    static constexpr int PER_SM = DP > 128 ? 1 : DP > 64 ? 2 : 3;  // CTAs that fit
     static constexpr int PART = ROWS * (2 + DP);  // floats of a part: m, l, o
 };
 
@@ -110,7 +114,7 @@ __global__ void __launch_bounds__(Split<DP, MT>::THREADS) attn_split_kernel(cons
     __shared__ long long s_scan[C::WARPS];
     __shared__ long long s_first;
     __shared__ Cursor s_cur;
-    __shared__ int s_bad;
+    __shared__ int s_bad[3];  // of this part, the last and the next
     __shared__ float s_ml[C::WARPS][2][16];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t4 = lane & 3;
@@ -136,7 +140,7 @@ __global__ void __launch_bounds__(Split<DP, MT>::THREADS) attn_split_kernel(cons
         if (lane >= d) sum += x;
     }
     if (lane == 31) s_scan[warp] = sum;
-    if (tid == 0) s_bad = 0;
+    if (tid < 3) s_bad[tid] = 0;
     __syncthreads();
     long long all = 0;
     for (int w = 0; w < C::WARPS; ++w) {
@@ -178,7 +182,16 @@ __global__ void __launch_bounds__(Split<DP, MT>::THREADS) attn_split_kernel(cons
 
     // ---- copies: warp w brings keys COPY w .. COPY (w + 1) - 1 of a tile
     const __nv_bfloat16 *kc = static_cast<const __nv_bfloat16 *>(p.a.k), *vc = static_cast<const __nv_bfloat16 *>(p.a.v);
-    auto fetch = [&](const Cursor &x, int stage) {
+    auto load_q = [&](const Cursor &x, uint32_t dst) {  // asynchronous; without the sign of a negative scale
+        for (int i = tid; i < C::ROWS * CH; i += kThreads) {
+            const int r = i / CH, c = i % CH;
+            const bool read = r < x.len * G && c * 8 < D;
+            const long e = read ? (long)(x.start + r / G) * p.a.qs + (long)(x.h * G + r % G) * D + c * 8 : 0;
+            copy16(dst + chunk_at<DP>(r, c), static_cast<const __nv_bfloat16 *>(p.a.q) + e, read);
+        }
+    };
+    auto fetch = [&](const Cursor &x, int stage, bool first) {
+        if (C::QSTAGE && (first || x.tile == 0)) load_q(x, s_q + (1 + stage) * C::Q_BYTES);
         const int key = x.tile * kKeys + warp * C::COPY + (lane & (C::COPY - 1));
         long row = -1;
         if (key < x.kv) row = attn_key_row(p.a, x.b, x.start, key, p.a.ks);
@@ -199,7 +212,7 @@ __global__ void __launch_bounds__(Split<DP, MT>::THREADS) attn_split_kernel(cons
     long long u_ahead = u0;
     for (int i = 0; i < STAGES - 1; ++i) {
         if (u_ahead < u1) {
-            fetch(ahead, i);
+            fetch(ahead, i, i == 0);
             ++u_ahead;
             if (u_ahead < u1) advance(ahead);
         }
@@ -211,38 +224,49 @@ __global__ void __launch_bounds__(Split<DP, MT>::THREADS) attn_split_kernel(cons
     int stage = 0;
     bool fresh = true;   // the next tile begins a part
     int first_tile = 0;  // of this part
+    int bad_at = 0;      // its place in s_bad
     for (long long u = u0; u < u1; ++u) {
         const int n = cur.len, rows = n * G, shift = cur.kv - n;
-        if (fresh) {
+        const bool begins = fresh;
+        if (begins) {
             fresh = false;
             first_tile = cur.tile;
-            __syncthreads();  // the last part's use of the scratch is over
-            for (int i = tid; i < C::ROWS * CH; i += kThreads) {
-                const int r = i / CH, c = i % CH;
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (r < rows && c * 8 < D) {
-                    x = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.a.q) +
-                                                              (long)(cur.start + r / G) * p.a.qs + (long)(cur.h * G + r % G) * D + c * 8));
-                    if (p.negate) x.x ^= 0x80008000u, x.y ^= 0x80008000u, x.z ^= 0x80008000u, x.w ^= 0x80008000u;
+            if constexpr (!C::QSTAGE) {
+                __syncthreads();  // the last part's use of this place is over
+                for (int i = tid; i < C::ROWS * CH; i += kThreads) {
+                    const int r = i / CH, c = i % CH;
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (r < rows && c * 8 < D) {
+                        x = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.a.q) +
+                                                                  (long)(cur.start + r / G) * p.a.qs + (long)(cur.h * G + r % G) * D + c * 8));
+                        if (p.negate) x.x ^= 0x80008000u, x.y ^= 0x80008000u, x.z ^= 0x80008000u, x.w ^= 0x80008000u;
+                    }
+                    *reinterpret_cast<uint4 *>(smem + STAGES * 2 * C::HALF + chunk_at<DP>(r, c)) = x;
                 }
-                *reinterpret_cast<uint4 *>(smem + STAGES * 2 * C::HALF + chunk_at<DP>(r, c)) = x;
+                __syncthreads();
             }
-            if (tid == 0) s_bad = 0;
-            __syncthreads();
-            if constexpr (C::QREG)
-#pragma unroll
-                for (int ks = 0; ks < DP / 16; ++ks)
-                    ldmatrix4(s_q + chunk_at<DP>(mt * 16 + (lane & 15), ks * 2 + (lane >> 4)), qf[ks]);
+            bad_at = bad_at == 2 ? 0 : bad_at + 1;
+            if (tid == 0) s_bad[bad_at == 2 ? 0 : bad_at + 1] = 0;  // (two parts ago: read by all)
             m[0] = m[1] = -INFINITY, l[0] = l[1] = 0.f;
 #pragma unroll
             for (int i = 0; i < DP / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
         }
         copy_wait<STAGES - 2>();
         __syncthreads();  // the tile is here, and the slot that is filled next is free
+        if (C::QREG && begins) {
+            const uint32_t q = s_q + (C::QSTAGE ? (1 + stage) * C::Q_BYTES : 0);
+#pragma unroll
+            for (int ks = 0; ks < (C::QREG ? DP / 16 : 0); ++ks) {
+                ldmatrix4(q + chunk_at<DP>(mt * 16 + (lane & 15), ks * 2 + (lane >> 4)), qf[ks]);
+                if (C::QSTAGE && p.negate)
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) qf[ks][z] ^= 0x80008000u;
+            }
+        }
         {
             const int next = stage == 0 ? STAGES - 1 : stage - 1;
             if (u_ahead < u1) {
-                fetch(ahead, next);
+                fetch(ahead, next, false);
                 ++u_ahead;
                 if (u_ahead < u1) advance(ahead);
             }
@@ -260,7 +284,7 @@ __global__ void __launch_bounds__(Split<DP, MT>::THREADS) attn_split_kernel(cons
                 for (int z = 0; z < 4; ++z) {
                     const uint32_t x = w[z];
                     const bool lo = (x & 0x7f80u) == 0x7f80u, hi = (x & 0x7f800000u) == 0x7f800000u;
-                    if (lo | hi) w[z] = x & (lo ? 0xffff0000u : 0xffffffffu) & (hi ? 0x0000ffffu : 0xffffffffu), s_bad = 1;
+                    if (lo | hi) w[z] = x & (lo ? 0xffff0000u : 0xffffffffu) & (hi ? 0x0000ffffu : 0xffffffffu), s_bad[bad_at] = 1;
                 }
             }
             __syncthreads();
@@ -403,7 +427,7 @@ __global__ void __launch_bounds__(Split<DP, MT>::THREADS) attn_split_kernel(cons
                 }
             }
             if (wk == WK - 1) {  // this warp holds the joined rows mt 16 + g, + 8
-                const bool bad = s_bad != 0;
+                const bool bad = s_bad[bad_at] != 0;
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
                     const int r = mt * 16 + g + 8 * z;
@@ -512,7 +536,7 @@ cudaError_t launch(const Attn &a, void *ws, cudaStream_t s) {
     int dev = 0, sms = 0;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const long slots = (long)sms * (DP > 128 ? 1 : 2);
+    const long slots = (long)sms * C::PER_SM;
     const long most = (long)a.B * a.HKV * (((long)a.max_pages * a.page_size + kKeys - 1) / kKeys);
     long grid = slots < kMaxCtas ? slots : kMaxCtas;
     if (most < grid) grid = most;
