@@ -26,9 +26,10 @@
 // are finite in sound data: when an output is not, the epilogue looks for a
 // non-finite value among them and computes those rows again without it.
 //
-// Persistent CTAs, one per SM, take (query tile pair, head) items in a fixed
-// interleaved order, longest first by the tile's place in its sequence; heads
-// are innermost, so that the heads of a group read the same keys out of L2.
+// Persistent CTAs, one per SM, take (query tile pair, head) items round by round
+// in a fixed order, longest first by the tile's place in its sequence and to and
+// fro over the CTAs; heads are innermost, so that the heads of a group read the
+// same keys out of L2.
 #include <cmath>
 
 #include "attention.cuh"
@@ -328,7 +329,6 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
     volatile int *abort = s_abort;
-    const long step = gridDim.x;
     Item it;
     it.n[1] = 0;
     // Items come from the load warp through a ring of four; false past the last one.
@@ -352,7 +352,10 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
             // ------------------------------------------------------------ loads
             uint32_t q_phase = 0;
             const int boxes = BN / p.box_rows;  // boxes of a 64-channel block of a key tile
-            for (long idx = blockIdx.x;; idx += step, seq += 2 * it.tiles, ++n_item) {
+            // Every other round of items goes the other way round: the CTA that took the longest item
+            // of one takes the shortest of the next.
+            for (long first = 0;; first += gridDim.x, seq += 2 * it.tiles, ++n_item) {
+                const long idx = first + (n_item & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
                 if (!get_item<DP>(p, suffix, idx, it)) it.b = -1;
                 if (!wait_or_abort(item_empty + (n_item & 3), ((n_item >> 2) & 1) ^ 1, abort)) goto done;
                 if (lane == 0) {
