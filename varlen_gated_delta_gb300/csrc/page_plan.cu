@@ -10,7 +10,8 @@
 // cluster: every CTA computes both prefix sums for itself in shared memory (B
 // is small), and the CTAs share the tokens and pages.  The cluster barrier
 // between the last read and the first write is what lets cursor_out and
-// kv_lens be the inputs' own buffers.
+// kv_lens be the inputs' own buffers.  One CTA for small steps (64 requests of one
+// token: 4.6 us), eight for others (131072 tokens of 32 requests: 12.3 us).
 #include <cooperative_groups.h>
 
 #include "common.cuh"
