@@ -261,6 +261,28 @@ def test_paged_long_history_few_sequences(dt, D):
 
 
 @pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("H,HKV,D", [(8, 2, 128), (3, 1, 64), (4, 4, 64), (4, 1, 256), (2, 2, 96)])
+@pytest.mark.parametrize("news,history", [([130], [3000]), ([70, 3, 200], [2900, 2500, 0]), ([65, 129], [127, 4000])])
+def test_paged_slices_over_long_histories(dt, H, HKV, D, news, history):
+    """Few items over many key tiles, which are then split; beside them sequences that see few keys or one tile."""
+    run_paged(news, [n + h for n, h in zip(news, history)], H, HKV, D, 64, dt, seed=D + sum(news))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_paged_split_slices_with_non_finite_values_and_rows_that_see_nothing(D):
+    news, kvs = [100, 90], [2500, 20]
+    q, kc, vc, table = make_paged(news, kvs, 4, 2, D, 16, BF16, max_pages=200)
+    where = lambda b, t: (int(table[b, t // 16]), t % 16)
+    vc[where(0, 2460)][0, 4] = float("nan")           # the 60th of the new tokens
+    vc[where(0, 2499)][1, 5] = float("inf")
+    kc[where(0, 2480)][1, 0] = float("nan")
+    out = torch.full(q.shape, SENTINEL, device=DEV, dtype=BF16)
+    gdn.gdn_attention_paged(q, kc, vc, i32(table), i32(kvs), i32([0, 100, 190]), max_q=100, out=out)
+    check_paged(out, q, kc, vc, table, news, kvs, BF16)
+    assert bool(torch.isfinite(out[:60]).all()) and not out[100:170].any()
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
 @pytest.mark.parametrize("news", [[1, 1, 1, 1], [3, 8, 2, 1], [70, 3, 300, 1]])
 def test_paged_rows_that_see_nothing_give_zero(dt, news):
     """Histories of no tokens, or of fewer than the new ones."""
@@ -340,7 +362,8 @@ def test_paged_cache_elements_past_32_bits(n):
     check_paged(out, q, kc, vc, table, [n], [kv], dt)
 
 
-@pytest.mark.parametrize("dt,D,n", [(F32, 128, 1), (BF16, 128, 1), (BF16, 64, 5), (BF16, 256, 1), (BF16, 128, 200)])
+@pytest.mark.parametrize("dt,D,n", [(F32, 128, 1), (BF16, 128, 1), (BF16, 64, 5), (BF16, 256, 1), (BF16, 128, 200),
+                                    (BF16, 256, 70)])
 def test_paged_is_repeatable(dt, D, n):
     q, kc, vc, table = make_paged([n] * 3, [700 + n, 30 + n, 2000 + n], 8, 2, D, 16, dt)
     call = lambda: gdn.gdn_attention_paged(q, kc, vc, i32(table), i32([700 + n, 30 + n, 2000 + n]),

@@ -36,6 +36,17 @@ __device__ __forceinline__ long attn_key_row(const Attn &a, int b, int start, in
     return ((long)page * a.page_size + j % a.page_size) * stride;
 }
 
+// Where split `i` of `splits` of a (token, head) row leaves its part: an unscaled output o, and ml =
+// {maximum in base 2, sum}.
+struct Part {
+    float *o, *ml;
+    __device__ __forceinline__ Part(const Attn &a, int splits, size_t row, int i) {
+        const size_t at = row * splits + i;
+        o = a.part + at * a.D;
+        ml = a.part + (size_t)a.N * a.H * splits * a.D + at * 2;
+    }
+};
+
 // Warp-wide: the idx-th tile of `rows` rows over all sequences, whose row
 // counts are len * per_token; false past the last one.  Malformed sequences
 // have no tiles.

@@ -340,20 +340,21 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const Attn a, int sp
                 for (int y = 0; y < 2; ++y)
                     if (i * 8 + 2 * t4 + y < D) out[i * 8 + 2 * t4 + y] = from_f32<T>(l[z] != 0.f ? o[i][2 * z + y] * inv : 0.f);
         } else {
-            float *part = a.part + (row * splits + blockIdx.z) * (D + 2);
-            if (t4 == 0) part[0] = m[z], part[1] = l[z];
+            const Part part(a, splits, row, blockIdx.z);
+            if (t4 == 0) part.ml[0] = m[z], part.ml[1] = l[z];
 #pragma unroll
             for (int i = 0; i < DP / 8; ++i)
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
-                    if (i * 8 + 2 * t4 + y < D) part[2 + i * 8 + 2 * t4 + y] = o[i][2 * z + y];
+                    if (i * 8 + 2 * t4 + y < D) part.o[i * 8 + 2 * t4 + y] = o[i][2 * z + y];
         }
     }
 }
 
-// Joins the splits of each row: one warp a (token, head).
+// Joins the splits of each row: one warp a (token, head).  Sequences of at most min_rows (query, head
+// of a group) rows have none.
 template <typename T>
-__global__ void __launch_bounds__(128) attn_f32_join_kernel(const Attn a, int splits) {
+__global__ void __launch_bounds__(128) attn_join_kernel(const Attn a, int splits, int min_rows) {
     const int lane = threadIdx.x & 31, D = a.D;
     const long row = (long)blockIdx.x * 4 + (threadIdx.x >> 5);
     pdl_wait_primary();
@@ -362,21 +363,25 @@ __global__ void __launch_bounds__(128) attn_f32_join_kernel(const Attn a, int sp
     if (t >= total || total > a.N) return;
     int start, len, kv;
     const int b = seq_of_token(a.offsets, a.B, t);
-    if (!attn_seq(a, b, start, len, kv) || t < start || t >= start + len) return;
-    const float *part = a.part + row * splits * (D + 2);
+    if (!attn_seq(a, b, start, len, kv) || t < start || t >= start + len || (long)len * (a.H / a.HKV) <= min_rows) return;
+    const Part first(a, splits, row, 0);
     float m = -INFINITY, l = 0.f;
-    for (int s = 0; s < splits; ++s) m = fmaxf(m, part[s * (D + 2)]);
+    for (int s = lane; s < splits; s += 32) m = fmaxf(m, first.ml[2 * s]);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     const float ref = m == -INFINITY ? 0.f : m;
-    for (int s = 0; s < splits; ++s) l += part[s * (D + 2) + 1] * exp2_fast(part[s * (D + 2)] - ref);
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    for (int s = lane; s < splits; s += 32) l += first.ml[2 * s + 1] * exp2_fast(first.ml[2 * s] - ref);
+    l = group_sum<32>(l);
+    const float inv = l > 0.f ? 1.f / l : l;  // (0 gives 0, NaN stays)
     T *out = static_cast<T *>(a.out) + row * D;
     for (int d = lane; d < D; d += 32) {
         float o = 0.f;
+#pragma unroll 8
         for (int s = 0; s < splits; ++s) {
-            const float c = exp2_fast(part[s * (D + 2)] - ref);
-            o += c > 0.f ? part[s * (D + 2) + 2 + d] * c : 0.f;
+            const float c = exp2_fast(first.ml[2 * s] - ref), v = first.o[(size_t)s * D + d];
+            o += c > 0.f ? v * c : 0.f;  // (a split that counts for nothing may hold inf)
         }
-        out[d] = from_f32<T>(o * inv);
+        out[d] = from_f32<T>(l != 0.f ? o * inv : 0.f);
     }
 }
 
@@ -402,10 +407,7 @@ cudaError_t launch_tile(const Attn &a, bool vec, cudaStream_t s) {
                       a, splits, vec);
     note_launch();
     if (e != cudaSuccess || splits == 1) return e;
-    const long ctas = ((long)a.N * a.H + 3) / 4;
-    e = launch_kernel(attn_f32_join_kernel<T>, dim3((unsigned)ctas), dim3(128), 0, s, true, a, splits);
-    note_launch();
-    return e;
+    return launch_attention_join(a, splits, 0, std::is_same_v<T, float> ? GDN_F32 : GDN_BF16, s);
 }
 
 template <typename T>
@@ -431,6 +433,16 @@ size_t attention_f32_part_floats(int N, int H, int D) {
     // Splits are chosen while tiles * HKV * splits < 4 * 152 tiles of at most 128 rows; doubled once more.
     const size_t rows = (size_t)N * H, most = rows * kMaxSplits, cap = 2 * 4 * 152 * 128;
     return (most < cap ? most : cap) * (D + 2);
+}
+
+cudaError_t launch_attention_join(const Attn &a, int splits, int min_rows, int dtype, cudaStream_t s) {
+    const dim3 ctas((unsigned)(((long)a.N * a.H + 3) / 4));
+    const cudaError_t e =
+        dtype == GDN_BF16
+            ? launch_kernel(attn_join_kernel<__nv_bfloat16>, ctas, dim3(128), 0, s, true, a, splits, min_rows)
+            : launch_kernel(attn_join_kernel<float>, ctas, dim3(128), 0, s, true, a, splits, min_rows);
+    note_launch();
+    return e;
 }
 
 cudaError_t launch_attention_f32(const Attn &a, int dtype, cudaStream_t s) {

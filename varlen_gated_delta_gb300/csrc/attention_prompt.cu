@@ -26,6 +26,9 @@
 // are finite in sound data: when an output is not, the epilogue looks for a
 // non-finite value among them and computes those rows again without it.
 //
+// A slice of a prompt over a long history has few items: its key tiles are then
+// split, and each split leaves m, l and an unscaled o for a second kernel.
+//
 // Persistent CTAs, one per SM, take (query tile pair, head) items round by round
 // in a fixed order, longest first by the tile's place in its sequence and to and
 // fro over the CTAs; heads are innermost, so that the heads of a group read the
@@ -91,6 +94,7 @@ struct PromptParams {
     float c;        // |scale| log2(e)
     int negate;     // scale < 0
     int out32;      // output rows lie on 32-byte boundaries
+    int splits;     // of the key tiles of an item; more than one: parts for a second kernel
 };
 
 // Warp-wide mbarrier wait that gives up, for the whole warp, after kWaitLimitNs
@@ -158,9 +162,11 @@ __device__ __forceinline__ bool elect_one() {
     return one != 0;
 }
 
-// One item: tm queries of sequence b from row0 on, of head h (and h + 1 with pair).
+// One item: tm queries of sequence b from row0 on, of head h (and h + 1 with pair), over its key
+// tiles from lo on.
 struct Item {
     int b, h, start, len, kv, row0;
+    int split, lo;
     int n[2];     // key tiles of each query tile (0: no rows, or none that sees a key)
     int tiles;    // key tiles loaded
     int end;      // rows of the last key tile that hold keys
@@ -184,6 +190,8 @@ __device__ __forceinline__ bool get_item(const PromptParams &p, const int *suffi
     using C = Cfg<DP>;
     const int lane = threadIdx.x & 31;
     const int heads = p.pair ? p.a.H >> 1 : p.a.H;
+    it.split = (int)(idx % p.splits);
+    idx /= p.splits;
     if (idx >= (long)suffix[0] * heads) return false;
     int rank = (int)(idx / heads);
     it.h = (int)(idx % heads) << p.pair;
@@ -223,6 +231,15 @@ __device__ __forceinline__ bool get_item(const PromptParams &p, const int *suffi
             it.tiles = max(it.tiles, it.n[t]);
         }
         it.end = min(C::BN, it.kv - (it.tiles - 1) * C::BN);
+        it.lo = 0;
+        if (p.splits > 1) {  // this split's key tiles
+            const int per = (it.tiles + p.splits - 1) / p.splits, all = it.tiles;
+            it.lo = min(it.split * per, all);
+            it.tiles = min(all, it.lo + per) - it.lo;
+            if (it.lo + it.tiles < all) it.end = C::BN;
+#pragma unroll
+            for (int t = 0; t < C::NQ; ++t) it.n[t] = max(0, min(it.n[t] - it.lo, it.tiles));
+        }
         return true;
     }
     return false;
@@ -230,9 +247,10 @@ __device__ __forceinline__ bool get_item(const PromptParams &p, const int *suffi
 
 // Warp-wide and rare.  Where V holds a non-finite value in channels c .. c + 31 of keys [k0, k1),
 // which some row of the tile does not see, the rows with `odd` compute their outputs again over the
-// `seen` keys that they do see, with the reference m and 1 / l of the softmax.
+// keys [lo, seen) before k1 that they do see, with the reference m and 1 / l of the softmax (a part:
+// with 1, into part).
 __device__ __forceinline__ void redo_masked(const PromptParams &p, int b, int start, int row, int h, int c, int k0,
-                                         int k1, int seen, bool odd, float m, float inv) {
+                                            int k1, int lo, int seen, bool odd, float m, float inv, float *part) {
     const int lane = threadIdx.x & 31, D = p.a.D, kvh = h / p.G;
     const __nv_bfloat16 *kb = static_cast<const __nv_bfloat16 *>(p.a.k) + (long)kvh * D;
     const __nv_bfloat16 *vb = static_cast<const __nv_bfloat16 *>(p.a.v) + (long)kvh * D;
@@ -248,7 +266,7 @@ __device__ __forceinline__ void redo_masked(const PromptParams &p, int b, int st
     float f[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) f[i] = 0.f;
-    for (int j = 0; j < seen; ++j) {
+    for (int j = lo; j < min(seen, k1); ++j) {
         const long ka = attn_key_row(p.a, b, start, j, p.a.ks), va = attn_key_row(p.a, b, start, j, p.a.vs);
         if (ka < 0) continue;  // (a zero value adds nothing)
         float x = 0.f;
@@ -261,7 +279,10 @@ __device__ __forceinline__ void redo_masked(const PromptParams &p, int b, int st
     }
 #pragma unroll
     for (int i = 0; i < 32; ++i)
-        if (c + i < D) out[c + i] = __float2bfloat16_rn(f[i]);
+        if (c + i < D) {
+            if (part) part[c + i] = f[i];
+            else out[c + i] = __float2bfloat16_rn(f[i]);
+        }
 }
 
 template <int DP>
@@ -384,9 +405,9 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                 }
                 for (int j = 0; j < it.tiles; ++j) {
                     // the row of this lane's box (packed keys: one box, at its token)
-                    int row = it.start + j * BN;
+                    int row = it.start + (it.lo + j) * BN;
                     if (p.a.block_table != nullptr && lane < boxes) {
-                        const int key = j * BN + lane * p.box_rows;
+                        const int key = (it.lo + j) * BN + lane * p.box_rows;
                         const int page =
                             key < it.kv ? __ldg(p.a.block_table + (size_t)it.b * p.a.max_pages + key / p.a.page_size) : -1;
                         // outside the cache: past its end, where the load gives zeros
@@ -541,8 +562,8 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                 tmem_wait_ld();
 #pragma unroll
                 for (int c = 0; c < BN / 32; ++c) landed(x[c]);
-                if ((j + 1) * BN > least) {  // some row does not see all of these keys
-                    const int seen = shift + r + 1 - j * BN;
+                if ((it.lo + j + 1) * BN > least) {  // some row does not see all of these keys
+                    const int seen = shift + r + 1 - (it.lo + j) * BN;
 #pragma unroll
                     for (int c = 0; c < BN / 32; ++c) {
                         // bit i: key c 32 + i is seen
@@ -615,8 +636,13 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                 if (!wait_or_abort(o_done + prev, ((o_phase >> prev) & 1) ^ 1, abort)) goto done;
                 tc_fence_after();
             }
-            const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (NaN stays)
-            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) + ((size_t)(it.start + r) * p.a.H + it.h + (p.pair ? t : 0)) * p.a.D;
+            const bool whole = p.splits == 1;
+            const float inv = !whole ? 1.f : l > 0.f ? 1.f / l : l;  // (0 gives 0, NaN stays)
+            const int head = it.h + (p.pair ? t : 0);
+            const size_t out_row = (size_t)(it.start + r) * p.a.H + head;
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) + out_row * p.a.D;
+            const Part part(p.a, p.splits, out_row, it.split);
+            if (!whole && r < it.len) part.ml[0] = m * p.c, part.ml[1] = l;
             uint32_t odd = 0;  // chunks of 32 channels with values that are not finite
             constexpr int OC = DP < 128 ? DP / 32 : 4;  // chunks loaded at a time
 #pragma unroll 1
@@ -650,7 +676,11 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                     }
                     if (finite[0].x + finite[0].y + finite[1].x + finite[1].y != 0.f) odd |= 1u << (c >> 5);
                     if (r >= it.len) continue;
-                    if (p.out32) {
+                    if (!whole) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8)
+                            if (c + i < p.a.D) store32(part.o + c + i, &o[k][i]);
+                    } else if (p.out32) {
                         if (c < p.a.D) store32(out + c, w);
                         if (c + 16 < p.a.D) store32(out + c + 16, w + 8);
                     } else {
@@ -666,15 +696,19 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
             if (__any_sync(0xffffffffu, odd != 0))
 #pragma unroll 1
                 for (int c = 0; c < DP; c += 32)
-                    redo_masked(p, it.b, it.start, it.start + r, it.h + (p.pair ? t : 0), c, max(0, least - 1),
-                                min(it.kv, n * BN), min(it.kv, shift + r + 1), (odd >> (c >> 5)) & 1, m, inv);
+                    redo_masked(p, it.b, it.start, it.start + r, head, c, max(it.lo * BN, least - 1),
+                                min(it.kv, (it.lo + n) * BN), it.lo * BN, min(it.kv, shift + r + 1),
+                                (odd >> (c >> 5)) & 1, m, inv, whole ? nullptr : part.o);
             tc_fence_before();  // the next item's products follow this tile's next arrival
         }
     }
 done:
     __syncwarp();
     if (warp == kTmaWarp && *abort)  // copies in flight land before the CTA's memory goes
-        for (int i = 0; i < SLOTS; ++i) mbar_wait(full + i, 0, 1000000), mbar_wait(full + i, 1, 1000000);
+        for (int i = 0; i < SLOTS; ++i) {
+            mbar_wait(full + i, 0, 1000000), mbar_wait(full + i, 1, 1000000);
+            if (i < NQ) mbar_wait(q_full + i, 0, 1000000), mbar_wait(q_full + i, 1, 1000000);
+        }
     tc_fence_before();
     __syncthreads();
     if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
@@ -712,7 +746,7 @@ bool encode_rows(CUtensorMap *map, const void *base, long rows, int heads, int D
 }
 
 template <int DP>
-cudaError_t launch(const Attn &a, int min_rows, cudaStream_t s) {
+cudaError_t launch(const Attn &a, int min_rows, int splits, cudaStream_t s) {
     using C = Cfg<DP>;
     PromptParams p{};
     p.a = a;
@@ -747,15 +781,35 @@ cudaError_t launch(const Attn &a, int min_rows, cudaStream_t s) {
     int dev = 0, sms = 0;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const long items = ((long)a.N / p.tm + a.B) * (a.H >> p.pair);
+    // at least four key tiles to a split
+    const long key_tiles = paged ? ((long)a.max_pages * a.page_size + C::BN - 1) / C::BN : 1;
+    p.splits = 1;
+    while (p.splits * 2 <= splits && p.splits * 8 <= key_tiles) p.splits *= 2;
+    const long items = ((long)a.N / p.tm + a.B) * (a.H >> p.pair) * p.splits;
     const long grid = items < sms ? items : sms;
     e = launch_kernel(attn_prompt_kernel<DP>, dim3((unsigned)grid), dim3(C::THREADS), kFixed + (p.bins + 1) * 4, s,
                       true, qm, km, vm, p);
     note_launch();
-    return e;
+    if (e != cudaSuccess || p.splits == 1) return e;
+    return launch_attention_join(a, p.splits, min_rows, GDN_BF16, s);
+}
+
+// Splits of the key tiles when items are few: one request's slice of a prompt over a long history
+// would keep a handful of CTAs busy (64 tokens on 32768, 32 heads of 128 on 8: 390 us, split 80).
+int prompt_splits(int B, int N, int H, int HKV, int D) {
+    const bool pair = D <= 128 && H / HKV % 2 == 0;
+    const long tm = D > 128 || pair ? 128 : 256, items = ((long)N / tm + B) * (H >> pair);
+    int splits = 1;
+    while (splits < 32 && items * splits * 2 <= 2 * 152) splits *= 2;
+    return splits;
 }
 
 }  // namespace
+
+size_t attention_prompt_part_floats(int B, int N, int H, int HKV, int D) {
+    const int splits = prompt_splits(B, N, H, HKV, D);
+    return splits == 1 ? 0 : (size_t)N * H * splits * (D + 2);
+}
 
 int attention_timeouts(cudaStream_t s, cudaError_t *e) {
     int seen = 0;
@@ -775,9 +829,10 @@ bool attention_prompt_supported(const Attn &a, int dtype) {
 }
 
 cudaError_t launch_attention_prompt(const Attn &a, int min_rows, cudaStream_t s) {
-    if (a.D <= 64) return launch<64>(a, min_rows, s);
-    if (a.D <= 128) return launch<128>(a, min_rows, s);
-    return launch<256>(a, min_rows, s);
+    const int splits = a.part == nullptr ? 1 : prompt_splits(a.B, a.N, a.H, a.HKV, a.D);
+    if (a.D <= 64) return launch<64>(a, min_rows, splits, s);
+    if (a.D <= 128) return launch<128>(a, min_rows, splits, s);
+    return launch<256>(a, min_rows, splits, s);
 }
 
 }  // namespace gdn

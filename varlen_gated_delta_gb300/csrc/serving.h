@@ -44,7 +44,7 @@ struct Attn {
     int page_size, max_pages, num_pages, max_q;
     long qs, ks, vs;  // token strides in elements (paged: HKV * D for k and v)
     float scale;
-    float *part;  // partial results of key splits (paged only)
+    float *part;  // parts of key splits (paged only): [N][H][splits][D], then [N][H][splits][2]
     size_t part_floats;
 };
 
@@ -58,6 +58,10 @@ inline bool rows_aligned(const void *base, long stride_elems, int D, size_t esz)
 size_t attention_f32_part_floats(int N, int H, int D);
 cudaError_t launch_attention_f32(const Attn &a, int dtype, cudaStream_t s);
 
+// The output of rows whose keys were split into parts (Attn::part, see attention.cuh) of sequences
+// with more than min_rows (query, head of a group) rows.
+cudaError_t launch_attention_join(const Attn &a, int splits, int min_rows, int dtype, cudaStream_t s);
+
 // bf16, few rows over long paged histories: sequences of at most kSplitRows
 // (query, head of a group) rows, the others are left out.
 constexpr int kSplitRows = 64;
@@ -69,6 +73,7 @@ cudaError_t launch_attention_split(const Attn &a, void *ws, cudaStream_t s);
 // prompt slices.  Sequences of at most min_rows (query, head of a group) rows
 // are left out.
 bool attention_prompt_supported(const Attn &a, int dtype);
+size_t attention_prompt_part_floats(int B, int N, int H, int HKV, int D);
 cudaError_t launch_attention_prompt(const Attn &a, int min_rows, cudaStream_t s);
 // Synchronises s; non-zero when a bounded wait gave up since the last call.
 int attention_timeouts(cudaStream_t s, cudaError_t *e);
