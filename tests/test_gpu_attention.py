@@ -268,6 +268,14 @@ def test_paged_slices_over_long_histories(dt, H, HKV, D, news, history):
     run_paged(news, [n + h for n, h in zip(news, history)], H, HKV, D, 64, dt, seed=D + sum(news))
 
 
+@pytest.mark.parametrize("H,HKV,D,news,history", [
+    (8, 1, 128, [20, 9, 33], [0, 700, 63]), (16, 2, 256, [30, 12], [1500, 5]), (128, 1, 64, [2, 1, 3], [40, 0, 900]),
+    (32, 1, 64, [5, 0, 3], [77, 10, 2000]), (4, 1, 96, [100, 17], [0, 333]), (4, 2, 128, [127, 33], [130, 1])])
+def test_paged_short_slices_with_shared_heads(H, HKV, D, news, history):
+    """Fewer tokens than a query tile has rows: the tile holds the heads of a group side by side."""
+    run_paged(news, [n + h for n, h in zip(news, history)], H, HKV, D, 16, BF16, seed=H + D, max_pages=130)
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_paged_split_slices_with_non_finite_values_and_rows_that_see_nothing(D):
     news, kvs = [100, 90], [2500, 20]

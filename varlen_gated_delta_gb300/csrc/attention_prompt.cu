@@ -1,7 +1,7 @@
 // attention_prompt.cu - causal softmax attention of prompts and prompt slices on
 // the tcgen05 tensor cores (bf16).
 //
-// For a tile of 128 queries of one head, over tiles of BN keys:
+// For a tile of 128 queries, (token, head) pairs that share a key-value head, over tiles of BN keys:
 //   S = Q K^T,  m' = max(m, rowmax S),  P = 2^(c (S - m')),  l' = l 2^(c (m - m')) + rowsum P,
 //   O' = O 2^(c (m - m')) + P V,   c = scale log2(e),   out = O / l.
 // 4 D operations for each visible (query, key): bound by the tensor cores, with
@@ -86,8 +86,12 @@ struct Cfg {
 struct PromptParams {
     Attn a;
     int G;
-    int tm;         // queries of an item along its sequence
-    int pair;       // its two query tiles are two heads of a group (else 256 queries of one head)
+    int tm;         // tokens of an item
+    // What the two query tiles of an item hold, 128 rows each (one tile for D > 128):
+    //   packed > 0: 2^packed heads of a group for each token, the second tile the next tokens;
+    //   pair: 128 tokens of one head and of the next; neither: 256 tokens of one head.
+    int packed, pair;
+    int heads;      // items side by side
     int box_rows;   // key rows of a TMA box
     int bins, bin_shift;
     int min_rows;   // sequences with at most this many (query, head of a group) rows are not ours
@@ -162,8 +166,8 @@ __device__ __forceinline__ bool elect_one() {
     return one != 0;
 }
 
-// One item: tm queries of sequence b from row0 on, of head h (and h + 1 with pair), over its key
-// tiles from lo on.
+// One item: tm tokens of sequence b from row0 on, of head h (with packing: of the heads of a group
+// from h on), over its key tiles from lo on.
 struct Item {
     int b, h, start, len, kv, row0;
     int split, lo;
@@ -189,12 +193,11 @@ template <int DP>
 __device__ __forceinline__ bool get_item(const PromptParams &p, const int *suffix, long idx, Item &it) {
     using C = Cfg<DP>;
     const int lane = threadIdx.x & 31;
-    const int heads = p.pair ? p.a.H >> 1 : p.a.H;
     it.split = (int)(idx % p.splits);
     idx /= p.splits;
-    if (idx >= (long)suffix[0] * heads) return false;
-    int rank = (int)(idx / heads);
-    it.h = (int)(idx % heads) << p.pair;
+    if (idx >= (long)suffix[0] * p.heads) return false;
+    int rank = (int)(idx / p.heads);
+    it.h = (int)(idx % p.heads) << (p.packed + p.pair);
     int lo = 0, hi = p.bins - 1;  // the bin with suffix[bin + 1] <= rank < suffix[bin]
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -225,7 +228,7 @@ __device__ __forceinline__ bool get_item(const PromptParams &p, const int *suffi
         const int shift = it.kv - it.len;
 #pragma unroll
         for (int t = 0; t < C::NQ; ++t) {
-            const int r = it.row0 + (p.pair ? 0 : t * 128), rows = min(128, it.len - r);
+            const int r = it.row0 + (p.pair ? 0 : t * (128 >> p.packed)), rows = min(128 >> p.packed, it.len - r);
             const int most = rows > 0 ? min(it.kv, shift + r + rows) : 0;
             it.n[t] = most > 0 ? (most + C::BN - 1) / C::BN : 0;
             it.tiles = max(it.tiles, it.n[t]);
@@ -400,7 +403,8 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                         mbar_arrive_expect_tx(q_full + t, C::QBYTES);
                         for (int c = 0; c < NB; ++c)
                             tma_load_3d(sq + t * C::QBYTES + c * 128 * 128, &qmap, q_full + t, c * 64,
-                                        it.h + (p.pair ? t : 0), it.start + it.row0 + (p.pair ? 0 : t * 128));
+                                        it.h + (p.pair ? t : 0),
+                                        it.start + it.row0 + (p.pair ? 0 : t * (128 >> p.packed)));
                     }
                 }
                 for (int j = 0; j < it.tiles; ++j) {
@@ -536,7 +540,8 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
         uint32_t o_phase = 0;  // a bit for each score buffer: products with its P so far, mod 2
         if (NQ == 2 && t == 1) mbar_arrive(turn + 0);  // query tile 0 goes first
         while (next_item()) {
-            const int shift = it.kv - it.len, first = it.row0 + (p.pair ? 0 : t * 128), r = first + row;
+            const int shift = it.kv - it.len, first = it.row0 + (p.pair ? 0 : t * (128 >> p.packed)),
+                      r = first + (row >> p.packed);
             const int n = NQ == 2 && t ? it.n[1] : it.n[0];
             const int least = shift + first + 1;  // keys that the tile's first row sees
             float m = -INFINITY, l = 0.f;
@@ -638,7 +643,7 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
             }
             const bool whole = p.splits == 1;
             const float inv = !whole ? 1.f : l > 0.f ? 1.f / l : l;  // (0 gives 0, NaN stays)
-            const int head = it.h + (p.pair ? t : 0);
+            const int head = it.h + (p.pair ? t : row & ((1 << p.packed) - 1));
             const size_t out_row = (size_t)(it.start + r) * p.a.H + head;
             __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) + out_row * p.a.D;
             const Part part(p.a, p.splits, out_row, it.split);
@@ -733,17 +738,32 @@ EncodeTiledFn encode_fn() {
 }
 
 // [rows][heads][D] bf16 with `stride` elements a row, read in boxes of 64 channels
-// of one head and box_rows rows; channels past D and rows past the end read as 0.
-bool encode_rows(CUtensorMap *map, const void *base, long rows, int heads, int D, long stride, int box_rows) {
+// of box_heads heads and box_rows rows; channels past D and rows past the end read as 0.
+bool encode_rows(CUtensorMap *map, const void *base, long rows, int heads, int D, long stride, int box_heads,
+                 int box_rows) {
     const EncodeTiledFn enc = encode_fn();
     if (enc == nullptr) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
     const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
-    const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows}, es[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows}, es[3] = {1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+// log2 of the heads of a group that a query tile holds for each token: all of them, when they are a
+// power of two and no sequence has the 128 tokens that would fill a tile with one head (slices of
+// 64 tokens on 32768, 32 heads of 128 on 8: 81 us with one head a tile, 55 packed; long prompts are 4%
+// slower packed, 8 x 4096 tokens: 719 and 749 us).
+int packed_heads(int G, int max_q) {
+    int n = 0;
+    while (n < 7 && (G >> n) > 1) ++n;
+    return G == 1 << n && max_q < 128 ? n : 0;
+}
+// Without that, two heads of a group are the two query tiles: they see the same keys to the same
+// extent, and an item of 128 tokens leaves less of a short sequence unused than one of 256 (64 x 100
+// tokens, 32 heads of 128 on 8: 70 us with 256 tokens, 53 with pairs).
+bool paired_heads(int G, int D, int packed) { return packed == 0 && D <= 128 && G % 2 == 0; }
 
 template <int DP>
 cudaError_t launch(const Attn &a, int min_rows, int splits, cudaStream_t s) {
@@ -758,18 +778,18 @@ cudaError_t launch(const Attn &a, int min_rows, int splits, cudaStream_t s) {
     const bool paged = a.block_table != nullptr;
     p.box_rows = C::BN;
     if (paged) while (a.page_size % p.box_rows != 0) p.box_rows /= 2;
-    // Two heads of a group see the same keys to the same extent, and an item of 128 queries leaves
-    // less of a short sequence unused than one of 256.
-    p.pair = C::NQ == 2 && p.G % 2 == 0;
-    p.tm = p.pair ? 128 : C::NQ * 128;
+    p.packed = packed_heads(p.G, a.max_q);
+    p.pair = paired_heads(p.G, a.D, p.packed);
+    p.tm = p.pair ? 128 : C::NQ * 128 >> p.packed;
+    p.heads = a.H >> (p.packed + p.pair);
     const long levels = ((long)a.max_q + p.tm - 1) / p.tm;
     while (((levels + (1L << p.bin_shift) - 1) >> p.bin_shift) > kMaxBins) ++p.bin_shift;
     p.bins = (int)((levels + (1L << p.bin_shift) - 1) >> p.bin_shift);
     const long kv_rows = paged ? (long)a.num_pages * a.page_size : a.N;
     CUtensorMap qm, km, vm;
-    if (!encode_rows(&qm, a.q, a.N, a.H, a.D, a.qs, 128) ||
-        !encode_rows(&km, a.k, kv_rows, a.HKV, a.D, a.ks, p.box_rows) ||
-        !encode_rows(&vm, a.v, kv_rows, a.HKV, a.D, a.vs, p.box_rows))
+    if (!encode_rows(&qm, a.q, a.N, a.H, a.D, a.qs, 1 << p.packed, 128 >> p.packed) ||
+        !encode_rows(&km, a.k, kv_rows, a.HKV, a.D, a.ks, 1, p.box_rows) ||
+        !encode_rows(&vm, a.v, kv_rows, a.HKV, a.D, a.vs, 1, p.box_rows))
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> attr_set{0};
     constexpr size_t kFixed = (size_t)C::NQ * C::QBYTES + C::SLOTS * C::SLOT + 512 + 1024;
@@ -785,7 +805,7 @@ cudaError_t launch(const Attn &a, int min_rows, int splits, cudaStream_t s) {
     const long key_tiles = paged ? ((long)a.max_pages * a.page_size + C::BN - 1) / C::BN : 1;
     p.splits = 1;
     while (p.splits * 2 <= splits && p.splits * 8 <= key_tiles) p.splits *= 2;
-    const long items = ((long)a.N / p.tm + a.B) * (a.H >> p.pair) * p.splits;
+    const long items = ((long)a.N / p.tm + a.B) * p.heads * p.splits;
     const long grid = items < sms ? items : sms;
     e = launch_kernel(attn_prompt_kernel<DP>, dim3((unsigned)grid), dim3(C::THREADS), kFixed + (p.bins + 1) * 4, s,
                       true, qm, km, vm, p);
@@ -796,9 +816,9 @@ cudaError_t launch(const Attn &a, int min_rows, int splits, cudaStream_t s) {
 
 // Splits of the key tiles when items are few: one request's slice of a prompt over a long history
 // would keep a handful of CTAs busy (64 tokens on 32768, 32 heads of 128 on 8: 390 us, split 80).
-int prompt_splits(int B, int N, int H, int HKV, int D) {
-    const bool pair = D <= 128 && H / HKV % 2 == 0;
-    const long tm = D > 128 || pair ? 128 : 256, items = ((long)N / tm + B) * (H >> pair);
+int prompt_splits(int B, int N, int H, int HKV, int D, int max_q) {
+    const int packed = packed_heads(H / HKV, max_q), pair = paired_heads(H / HKV, D, packed);
+    const long tm = pair ? 128 : (D > 128 ? 128 : 256) >> packed, items = ((long)N / tm + B) * (H >> (packed + pair));
     int splits = 1;
     while (splits < 32 && items * splits * 2 <= 2 * 152) splits *= 2;
     return splits;
@@ -806,8 +826,8 @@ int prompt_splits(int B, int N, int H, int HKV, int D) {
 
 }  // namespace
 
-size_t attention_prompt_part_floats(int B, int N, int H, int HKV, int D) {
-    const int splits = prompt_splits(B, N, H, HKV, D);
+size_t attention_prompt_part_floats(int B, int N, int H, int HKV, int D, int max_q) {
+    const int splits = prompt_splits(B, N, H, HKV, D, max_q);
     return splits == 1 ? 0 : (size_t)N * H * splits * (D + 2);
 }
 
@@ -829,7 +849,7 @@ bool attention_prompt_supported(const Attn &a, int dtype) {
 }
 
 cudaError_t launch_attention_prompt(const Attn &a, int min_rows, cudaStream_t s) {
-    const int splits = a.part == nullptr ? 1 : prompt_splits(a.B, a.N, a.H, a.HKV, a.D);
+    const int splits = a.part == nullptr ? 1 : prompt_splits(a.B, a.N, a.H, a.HKV, a.D, a.max_q);
     if (a.D <= 64) return launch<64>(a, min_rows, splits, s);
     if (a.D <= 128) return launch<128>(a, min_rows, splits, s);
     return launch<256>(a, min_rows, splits, s);

@@ -73,7 +73,7 @@ cudaError_t launch_attention_split(const Attn &a, void *ws, cudaStream_t s);
 // prompt slices.  Sequences of at most min_rows (query, head of a group) rows
 // are left out.
 bool attention_prompt_supported(const Attn &a, int dtype);
-size_t attention_prompt_part_floats(int B, int N, int H, int HKV, int D);
+size_t attention_prompt_part_floats(int B, int N, int H, int HKV, int D, int max_q);
 cudaError_t launch_attention_prompt(const Attn &a, int min_rows, cudaStream_t s);
 // Synchronises s; non-zero when a bounded wait gave up since the last call.
 int attention_timeouts(cudaStream_t s, cudaError_t *e);

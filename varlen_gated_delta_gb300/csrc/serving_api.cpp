@@ -136,7 +136,7 @@ size_t gdn_attention_paged_workspace_bytes(int B, int N, int H, int HKV, int D, 
     if (B < 1 || max_q < 0 || check_geometry(N, H, HKV, D, "attention")) return 0;
     const size_t wide = attention_f32_part_floats(N, H, D) * 4;
     const size_t split = attention_split_workspace(B, H, HKV, D, max_q);
-    const size_t prompt = (long)max_q * (H / HKV) > kSplitRows ? attention_prompt_part_floats(B, N, H, HKV, D) * 4 : 0;
+    const size_t prompt = (long)max_q * (H / HKV) > kSplitRows ? attention_prompt_part_floats(B, N, H, HKV, D, max_q < N ? max_q : N) * 4 : 0;
     const size_t most = wide > split ? wide : split;
     return round256(most > prompt ? most : prompt);
 }
