@@ -583,7 +583,7 @@ typedef enum gdn_rope_style {
  * Per head x: y = x w / sqrt(mean(x^2) + eps) (y = x without a weight), then
  * the first R channels are rotated in pairs (a, b) -> (a c - b s, b c + a s).
  * Computed in fp32 and rounded once to T.  A token whose position is outside
- * [0, max_pos) is skipped.  Tokens with the same slot leave one of their rows.
+ * [0, max_pos) is skipped.  No two tokens may have the same slot in range.
  * Requires R even, 0 <= R <= D.
  */
 GDN_API int gdn_qk_norm_rope(const void *qkv, int64_t row_stride, const float *q_weight,

@@ -202,12 +202,12 @@ def make_paged(news, kvs, H, HKV, D, ps, dt, seed=0, garbage=float("nan"), max_p
     return q, kc, vc, table
 
 
-def check_paged(out, q, kc, vc, table, news, kvs, dt, what=""):
+def check_paged(out, q, kc, vc, table, news, kvs, dt, what="", scale=None):
     at = 0
     for b, (n, kv) in enumerate(zip(news, kvs)):
         if n:
             k, v = ref.cached_rows(kc, table[b], kv), ref.cached_rows(vc, table[b], kv)
-            want, mag = ref.attention(q[at:at + n], k, v)
+            want, mag = ref.attention(q[at:at + n], k, v, scale)
             check(out[at:at + n], want, mag, dt, f"{what} sequence {b}: {n} of {kv}")
         at += n
 
@@ -343,6 +343,23 @@ def test_paged_non_finite_values_reach_only_the_queries_that_see_them(dt, D):
         gdn.gdn_attention_paged(q, kc, vc, i32(table), i32(kvs), i32([0, news[0], sum(news)]), max_q=max(news), out=out)
         check_paged(out, q, kc, vc, table, news, kvs, dt)
         assert bool(torch.isfinite(out[:news[0] - 3]).all()) and bool(torch.isfinite(out[news[0]:-1]).all())
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("scale", [-0.2, 0.03])
+@pytest.mark.parametrize("news", [[1, 1], [5, 2], [80, 3]])
+def test_paged_scale_and_strided_queries(dt, D, scale, news):
+    kvs = [n + h for n, h in zip(news, (130, 70))]
+    q, kc, vc, table = make_paged(news, kvs, 8, 2, D, 16, dt)
+    wide = torch.zeros(q.shape[0], 8 * D + 64, device=DEV, dtype=dt)
+    wide[:, 64:] = q.view(q.shape[0], -1)
+    view = wide[:, 64:].view(q.shape[0], 8, D) if q.shape[0] == 1 else \
+        torch.as_strided(wide, q.shape, (8 * D + 64, D, 1), 64)
+    out = gdn.gdn_attention_paged(view, kc, vc, i32(table), i32(kvs), i32([0, news[0], sum(news)]), max_q=max(news),
+                                  scale=scale)
+    check_paged(out, q, kc, vc, table, news, kvs, dt, scale=scale)
+    gdn.gdn_attention_status()
 
 
 def test_paged_padded_step():
