@@ -5,7 +5,8 @@ function has the C call's name and only marshals arguments: it checks device,
 dtype, shape and contiguity of torch tensors, passes their data pointers and
 the current CUDA stream, and raises :class:`GdnError` on a non-zero status.
 All arithmetic runs in the library's CUDA kernels; there is no CPU fallback.
-If the library is missing, every call raises.
+If the library is missing, every call raises.  The calls that serve
+softmax-attention layers are marshalled by a compiled module (binding/marshal.cpp).
 
 Operations follow paged_ssm.rs (onnxruntime-ep-mlx 0.31.1): the
 VarlenCausalConvWithState operator (``gdn_conv1d_varlen``) and the
@@ -15,7 +16,6 @@ fused layer ``gdn_layer_varlen``.
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 import os
 
@@ -170,14 +170,6 @@ def _ptr(t, name, dtype=None, shape=None, device=None):
 
 def _stream(device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
-
-
-def _raw_stream(device) -> int:
-    """_stream without building a torch.cuda.Stream object, where torch offers that."""
-    return _current_raw_stream(device.index) if _current_raw_stream else _stream(device)
-
-
-_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _host_offsets(offsets_host):
@@ -656,53 +648,30 @@ def gdn_segment_plan(offsets, H: int, V: int, sm_count: int) -> list:
 
 # ------------------------------------------------------------------ softmax-attention layers
 
-# These calls run in decode loops, where the host's time counts: a tensor that is as it
-# should be passes one combined test, any other gets its message from the full checks.
+# These calls run in decode loops, where the host's time counts: binding/marshal.cpp checks
+# and marshals their arguments.
 
-def _on_gpu(device, name):
-    if device.type != "cuda":
-        raise GdnError(6, f"{name} must be a CUDA tensor")
-    return device
+_marshal_module = None
 
 
-def _at(t, name, dtype, shape, device):
-    """_ptr for a tensor that must be there."""
-    if (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape
-            and t.get_device() == device.index and t.is_contiguous()):
-        return t.data_ptr()
-    return _ptr(t, name, dtype, shape, device)
+def _marshal():
+    """The compiled part of the binding; raise if it was not built for this torch."""
+    global _marshal_module
+    if _marshal_module is None:
+        import importlib.util
 
-
-def _out(t, name, dtype, shape, device):
-    """An output and its pointer: the caller's tensor, or a new one."""
-    if t is None:
-        t = torch.empty(shape, dtype=dtype, device=device)
-        return t, t.data_ptr()
-    return t, _at(t, name, dtype, shape, device)
-
-
-def _rows(t, name, dtype, shape, device):
-    """Pointer and token stride of a tensor of rows: contiguous but for the token stride."""
-    if (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape
-            and t.get_device() == device.index and t.is_contiguous()):
-        return t.data_ptr(), t.stride(0)
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda or t.device != device:
-        raise GdnError(6, f"{name} is on {t.device}, expected {device}")
-    if t.dtype != dtype:
-        raise GdnError(2, f"{name} has dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise GdnError(2, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    width = 1
-    for n, stride in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
-        if n != 1 and stride != width:
-            raise GdnError(2, f"{name} must be contiguous within a token")
-        width *= n
-    stride = t.stride(0) if shape[0] > 1 else width
-    if stride < width:
-        raise GdnError(2, f"{name} has token stride {stride}, below its row width {width}")
-    return (t.data_ptr() if t.numel() > 0 else None), stride
+        from .build import marshal_path
+        load_library()
+        path = marshal_path()
+        if not os.path.exists(path):
+            raise GdnError(6, f"{path} is missing: build it with "
+                              "`python -m varlen_gated_delta_gb300.build`")
+        spec = importlib.util.spec_from_file_location("_marshal", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.init(GdnError)
+        _marshal_module = module
+    return _marshal_module
 
 
 def gdn_page_plan(new_lens, cached_lens, block_table, free_pages, *, page_size, N, cursor,
@@ -716,22 +685,9 @@ def gdn_page_plan(new_lens, cached_lens, block_table, free_pages, *, page_size, 
     new token are -1).  ``kv_lens`` may be ``cached_lens`` and ``cursor_out`` may be
     ``cursor``.  Returns (offsets [B+1], kv_lens [B], positions [N], slots [N],
     cursor_out [1], status [1]), all int32; when status[0] != 0 nothing was handed out."""
-    lib = load_library()
-    B, max_pages = block_table.shape
-    dev, i32 = _on_gpu(block_table.device, "block_table"), torch.int32
-    n_free = free_pages.numel()
-    offsets, op = _out(offsets, "offsets", i32, (B + 1,), dev)
-    kv_lens, kp = _out(kv_lens, "kv_lens", i32, (B,), dev)
-    positions, pp = _out(positions, "positions", i32, (N,), dev)
-    slots, sp = _out(slots, "slots", i32, (N,), dev)
-    cursor_out, cp = _out(cursor_out, "cursor_out", i32, (1,), dev)
-    status, tp = _out(status, "status", i32, (1,), dev)
-    _check(lib.gdn_page_plan(
-        _at(new_lens, "new_lens", i32, (B,), dev), _at(cached_lens, "cached_lens", i32, (B,), dev),
-        _at(block_table, "block_table", i32, (B, max_pages), dev),
-        _at(free_pages, "free_pages", i32, (n_free,), dev), _at(cursor, "cursor", i32, (1,), dev),
-        op, kp, pp, sp, cp, tp, B, N, int(page_size), max_pages, n_free, _raw_stream(dev)))
-    return offsets, kv_lens, positions, slots, cursor_out, status
+    return (_marshal_module or _marshal()).page_plan(
+        new_lens, cached_lens, block_table, free_pages, page_size, N, cursor, offsets, kv_lens, positions,
+        slots, cursor_out, status)
 
 
 def gdn_qk_norm_rope(qkv, cos_sin=None, positions=None, *, H, HKV, D, q_weight=None, k_weight=None,
@@ -743,31 +699,8 @@ def gdn_qk_norm_rope(qkv, cos_sin=None, positions=None, *, H, HKV, D, q_weight=N
     cosines then R/2 sines per position (None: no rotation).  With ``slots`` [N] the k and
     v rows go to ``k_cache`` / ``v_cache`` [num_pages, page_size, HKV, D], and a packed k
     is only written when a tensor ``k`` is given.  Returns (q [N,H,D], k [N,HKV,D] or None)."""
-    lib = load_library()
-    N = qkv.shape[0]
-    T, dev, f32, i32 = qkv.dtype, _on_gpu(qkv.device, "qkv"), torch.float32, torch.int32
-    base, stride = _rows(qkv, "qkv", T, (N, (H + 2 * HKV) * D), dev)
-    q, qp = _out(q, "q", T, (N, H, D), dev)
-    kp = None
-    if k is not None or slots is None:
-        k, kp = _out(k, "k", T, (N, HKV, D), dev)
-    max_pos, R = (0, 0) if cos_sin is None else cos_sin.shape
-    num_slots = 0
-    kc = vc = None
-    if slots is not None:
-        if k_cache is None or v_cache is None:
-            raise GdnError(1, "slots need k_cache and v_cache")
-        cshape = (*k_cache.shape[:2], HKV, D)
-        num_slots = cshape[0] * cshape[1]
-        kc, vc = _at(k_cache, "k_cache", T, cshape, dev), _at(v_cache, "v_cache", T, cshape, dev)
-    _check(lib.gdn_qk_norm_rope(
-        base, stride, None if q_weight is None else _at(q_weight, "q_weight", f32, (D,), dev),
-        None if k_weight is None else _at(k_weight, "k_weight", f32, (D,), dev), float(eps),
-        None if R == 0 else _at(cos_sin, "cos_sin", f32, (max_pos, R), dev),
-        None if positions is None else _at(positions, "positions", i32, (N,), dev), max_pos,
-        None if slots is None else _at(slots, "slots", i32, (N,), dev),
-        qp, kp, kc, vc, num_slots, N, H, HKV, D, R, int(style), _dtype_code(qkv), _raw_stream(dev)))
-    return q, k
+    return (_marshal_module or _marshal()).qk_norm_rope(
+        qkv, cos_sin, positions, H, HKV, D, q_weight, k_weight, eps, style, q, k, slots, k_cache, v_cache)
 
 
 def gdn_attention_varlen(q, k, v, offsets, *, scale=0.0, out=None):
@@ -775,28 +708,16 @@ def gdn_attention_varlen(q, k, v, offsets, *, scale=0.0, out=None):
 
     q [N, H, D], k and v [N, HKV, D] (any token stride), offsets [B+1] int32.
     Returns out [N, H, D]; rows from offsets[B] on are not written."""
-    lib = load_library()
-    N, H, D = q.shape
-    HKV = k.shape[1]
-    T, dev = q.dtype, _on_gpu(q.device, "q")
-    B = offsets.numel() - 1
-    out, op = _out(out, "out", T, (N, H, D), dev)
-    (qp, qs), (kp, ks), (vp, vs) = (_rows(q, "q", T, (N, H, D), dev), _rows(k, "k", T, (N, HKV, D), dev),
-                                    _rows(v, "v", T, (N, HKV, D), dev))
-    _check(lib.gdn_attention_varlen(qp, kp, vp, _at(offsets, "offsets", torch.int32, (B + 1,), dev),
-                                    op, B, N, H, HKV, D, qs, ks, vs,
-                                    float(scale), _dtype_code(q), _raw_stream(dev)))
-    return out
+    return (_marshal_module or _marshal()).attention_varlen(q, k, v, offsets, scale, out)
 
 
 def gdn_attention_status(device=None) -> None:
     """Synchronise the current stream; raise GdnError (GDN_ERR_TIMEOUT) when a wait inside an
     attention kernel gave up since the last query."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
-    _check(load_library().gdn_attention_status(_raw_stream(dev)))
+    _check(load_library().gdn_attention_status(_stream(dev)))
 
 
-@functools.lru_cache(maxsize=256)
 def gdn_attention_paged_workspace_bytes(B, N, H, HKV, D, max_q) -> int:
     """Workspace bytes of gdn_attention_paged for these sizes."""
     return int(load_library().gdn_attention_paged_workspace_bytes(B, N, H, HKV, D, max_q))
@@ -811,21 +732,5 @@ def gdn_attention_paged(q, k_cache, v_cache, block_table, kv_lens, offsets, *, m
     with n rows sees its keys [0, kv_len - n + i].  ``max_q`` bounds n (1 for decode).
     ``workspace`` is an optional uint8 tensor of gdn_attention_paged_workspace_bytes
     bytes.  Returns out [N, H, D]; rows from offsets[B] on are not written."""
-    lib = load_library()
-    N, H, D = q.shape
-    pages, page_size, HKV, _ = k_cache.shape
-    B, max_pages = block_table.shape
-    T, dev, i32 = q.dtype, _on_gpu(q.device, "q"), torch.int32
-    out, op = _out(out, "out", T, (N, H, D), dev)
-    qp, qs = _rows(q, "q", T, (N, H, D), dev)
-    if workspace is None:
-        need = gdn_attention_paged_workspace_bytes(B, N, H, HKV, D, int(max_q))
-        workspace = torch.empty((max(need, 256),), dtype=torch.uint8, device=dev)
-    cshape = (pages, page_size, HKV, D)
-    _check(lib.gdn_attention_paged(
-        qp, _at(k_cache, "k_cache", T, cshape, dev), _at(v_cache, "v_cache", T, cshape, dev),
-        _at(block_table, "block_table", i32, (B, max_pages), dev), _at(kv_lens, "kv_lens", i32, (B,), dev),
-        _at(offsets, "offsets", i32, (B + 1,), dev), op, B, N, H, HKV, D,
-        page_size, max_pages, pages, int(max_q), qs, float(scale), _dtype_code(q),
-        _ptr(workspace, "workspace", torch.uint8, None, dev), workspace.numel(), _raw_stream(dev)))
-    return out
+    return (_marshal_module or _marshal()).attention_paged(
+        q, k_cache, v_cache, block_table, kv_lens, offsets, max_q, scale, out, workspace)

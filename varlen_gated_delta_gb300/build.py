@@ -4,6 +4,8 @@ Every translation unit under csrc/ is compiled by nvcc in parallel with
 ``-gencode arch=compute_103a,code=sm_103a`` and linked into
 ``varlen_gated_delta_gb300/libgdn.so`` (static CUDA runtime; the driver API
 is reached through the runtime's entry-point query, so no -lcuda).
+binding/marshal.cpp, the compiled part of the Python binding, becomes an
+extension module beside it that is named for the torch it was built against.
 """
 from __future__ import annotations
 
@@ -17,6 +19,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libgdn.so")
+MARSHAL_SRC = os.path.join(PKG, "binding", "marshal.cpp")
 BUILD_DIR = os.path.join(PKG, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -62,9 +65,45 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def marshal_path() -> str:
+    """The extension module of the running torch and Python."""
+    import torch
+    tag = "".join(c if c.isalnum() else "_" for c in torch.__version__)
+    return os.path.join(PKG, f"_marshal_{sys.implementation.cache_tag}_{tag}.so")
+
+
+def _build_marshal(force: bool) -> None:
+    out = marshal_path()
+    deps = [MARSHAL_SRC, os.path.join(ROOT, "include", "gdn.h")]
+    if not force and os.path.exists(out) and all(os.path.getmtime(d) <= os.path.getmtime(out) for d in deps):
+        return
+    import sysconfig
+
+    import torch
+    top = os.path.dirname(torch.__file__)
+    lib, inc = os.path.join(top, "lib"), os.path.join(top, "include")
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    tmp = out + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *(f"-I{d}" for d in (os.path.join(ROOT, "include"), inc, os.path.join(inc, "torch", "csrc", "api", "include"),
+                                sysconfig.get_paths()["include"], os.path.join(cuda, "include"))),
+           MARSHAL_SRC, "-o", tmp, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+           "-L", PKG, "-lgdn", f"-Wl,-rpath,{lib}", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {MARSHAL_SRC}:\n{r.stderr}")
+    os.replace(tmp, out)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _stale():
-        return LIB
+    if force or _stale():
+        _build_lib(verbose)
+    _build_marshal(force)
+    return LIB
+
+
+def _build_lib(verbose: bool) -> None:
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = sources()
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
@@ -75,7 +114,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":
