@@ -89,6 +89,20 @@ def test_lengths_and_cursor_carried_in_place_over_steps():
         new = i32([1] * B)
 
 
+@pytest.mark.parametrize("over", ["cached", "new", "cursor", "none"])
+def test_outputs_over_inputs_in_a_large_step(over):
+    # many CTAs, every one of which reads the lengths and the cursor
+    rs = np.random.RandomState(5)
+    c = _case(rs.randint(0, 700, 200), rs.randint(0, 300, 200), 16, pad=9)
+    new, cached, cursor, table = i32(c["new"]), i32(c["cached"]), i32([c["cursor"]]), i32(c["table"])
+    out = {"cached": dict(kv_lens=cached), "new": dict(kv_lens=new), "cursor": dict(cursor_out=cursor), "none": {}}[over]
+    got = gdn.gdn_page_plan(new, cached, table, i32(c["free"]), page_size=16, N=c["N"], cursor=cursor, **out)
+    offsets, kv, positions, slots, at, status = [x.tolist() for x in got]
+    want = ref.page_plan(c["new"], c["cached"], c["table"].tolist(), c["free"], 16, c["cursor"], c["N"])
+    assert status == [0]
+    assert (offsets, kv, positions, slots, table.tolist(), at[0]) == want
+
+
 @pytest.mark.parametrize("what,status", [("negative", 2), ("negative cached", 2), ("cursor", 2), ("N", 4),
                                          ("free", 9), ("table", 9), ("overflow", 9)])
 def test_a_step_that_cannot_be_planned_changes_nothing(what, status):

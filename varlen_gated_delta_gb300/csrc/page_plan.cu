@@ -8,11 +8,11 @@
 // new page.  There is next to nothing to read or write: the call is bound by
 // its launch and by the latency of the scan.  One launch: every CTA computes both
 // prefix sums for itself in shared memory (B is small), and the CTAs share the
-// tokens and pages.  With the lengths or the cursor carried in place an output is
-// an input's own buffer; then the CTAs form one thread-block cluster, whose barrier
-// between the last read and the first write keeps them apart.  One CTA for small
-// steps (64 requests of one token: 4.6 us); 131072 tokens of 32 requests: 12.8 us
-// carried in place, 6.1 us otherwise.
+// tokens and pages.  Where an output lies over an input (the lengths or the cursor
+// carried in place), the CTAs form one thread-block cluster, whose barrier between
+// the last read and the first write keeps them apart.  One CTA for small steps (64
+// requests of one token: 4.6 us); 131072 tokens of 32 requests: 11.8 us carried in
+// place, 6.2 us otherwise.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -173,7 +173,15 @@ cudaError_t launch_page_plan(const PagePlan &plan, cudaStream_t s) {
                                     3 * (kPagePlanMaxB + 1) * 4);
     });
     if (e != cudaSuccess) return e;
-    const bool in_place = p.cursor_out == p.cursor || p.kv_lens == p.cached_lens;
+    // Does an output lie over an input that every CTA reads?
+    const auto over = [](const int *out, long n, const int *in, long m) {
+        return (uintptr_t)out < (uintptr_t)(in + m) && (uintptr_t)in < (uintptr_t)(out + n);
+    };
+    const auto over_input = [&](const int *out, long n) {
+        return over(out, n, p.new_lens, p.B) || over(out, n, p.cached_lens, p.B) || over(out, n, p.cursor, 1);
+    };
+    const bool in_place = over_input(p.offsets, p.B + 1L) || over_input(p.kv_lens, p.B) || over_input(p.positions, p.N) ||
+                          over_input(p.slots, p.N) || over_input(p.cursor_out, 1) || over_input(p.status, 1);
     const long work = (long)p.N + p.B;
     const int ctas = work <= 2 * kThreads ? 1 : in_place ? 8 : (int)std::min(64L, (work + 4 * kThreads - 1) / (4 * kThreads));
     cudaLaunchConfig_t cfg = {};
