@@ -26,9 +26,10 @@ namespace {
 
 PyObject *g_error = nullptr;  // GdnError, set by init()
 
-// Up to so many new tokens the six outputs of a plan share one allocation: six of them take longer
-// than the rest of the call (64 requests: 9.7 us with six, 6.4 with one).
-constexpr int kSharedN = 16384;
+// Up to so many new tokens (8 MB) the six outputs of a plan share one allocation, which any one of them
+// keeps alive: six allocations take longer than the rest of the call (64 requests: 9.7 us with six, 6.4
+// with one; with 131072 new tokens a call among others 13.1 and 8.6).
+constexpr int kSharedN = 1 << 20;
 
 // A refusal with a gdn_status.
 struct Refusal {
