@@ -13,8 +13,9 @@
 // + (hi lo' + lo hi'), which leaves out another 2^-22 |a b|.  The large and
 // the small terms of a score have accumulators of their own, and the output of
 // a key tile is summed apart and then added in fp32, so that few additions
-// round inside the tensor cores.  Bound by the rate of these products (mma.sync in
-// tf32, three for each one wanted): 465 us, 35 TFLOP/s, for 4 x 1000 tokens, 16
+// round inside the tensor cores.  Bound by these products (mma.sync in tf32, three for
+// each one wanted) and their latency: the tensor pipe is 50% active, and the two warps
+// of a scheduler mostly wait for it or for a product's result.  465 us, 35 TFLOP/s, for 4 x 1000 tokens, 16
 // heads of 128 on 4, where multiply-adds on the fp32 pipe in the same tiles took
 // 558 us, and 301 against 445 us for 2 histories of up to 101321 tokens.
 //

@@ -23,8 +23,11 @@
 // 16 requests of 16384 tokens, 32 heads of 128 on 8, one token each: 161 us, 6.7
 // TB/s, the measured copy's rate.  Short steps are bound by the launches and the
 // dependent loads before the first tile (one request of 64 tokens: 7.5 us), and
-// the most rows of wide heads by the mma.sync rate (16 x 5 drafts over 4096 keys, 16
-// heads of 256 on 2, 40 rows in 64: 63 us, 2.1 TB/s).
+// the most rows of wide heads by latency: their registers leave eight warps to an SM,
+// which wait for fragments, products and copies in turn (16 x 5 drafts over 4096 keys,
+// 16 heads of 256 on 2, 40 rows in 64: 62 us, 2.2 TB/s, tensor pipe 29% active).  Leaving
+// out the row group without rows, sharing twelve units of three groups evenly among
+// the schedulers, and looking key slots up a tile ahead gave 62, 65 and 64 us.
 #include <cmath>
 
 #include "attention.cuh"
