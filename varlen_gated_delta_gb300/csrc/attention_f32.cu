@@ -360,11 +360,19 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const Attn a, int splits
     const long row = (long)blockIdx.x * 4 + (threadIdx.x >> 5);
     pdl_wait_primary();
     if (row >= (long)a.N * a.H) return;
-    const int t = (int)(row / a.H), total = __ldg(a.offsets + a.B);
-    if (t >= total || total > a.N) return;
+    // The row's sequence.  Each sequence is judged by itself, as where the parts were left: past a malformed
+    // one the offsets may go down, and the binary search then misses sound ones.
+    const int t = (int)(row / a.H);
     int start, len, kv;
-    const int b = seq_of_token(a.offsets, a.B, t);
-    if (!attn_seq(a, b, start, len, kv) || t < start || t >= start + len || (long)len * (a.H / a.HKV) <= min_rows) return;
+    auto holds = [&](int b) { return attn_seq(a, b, start, len, kv) && t >= start && t < start + len; };
+    if (!holds(seq_of_token(a.offsets, a.B, t))) {
+        int b0 = 0;
+        unsigned found = 0;
+        for (; found == 0 && b0 < a.B; b0 += 32) found = __ballot_sync(0xffffffffu, b0 + lane < a.B && holds(b0 + lane));
+        if (found == 0) return;
+        holds(b0 - 32 + __ffs(found) - 1);
+    }
+    if ((long)len * (a.H / a.HKV) <= min_rows) return;
     const Part first(a, splits, row, 0);
     float m = -INFINITY, l = 0.f;
     for (int s = lane; s < splits; s += 32) m = fmaxf(m, first.ml[2 * s]);
