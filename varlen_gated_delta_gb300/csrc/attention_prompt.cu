@@ -24,7 +24,11 @@
 // sequence (other sequences, stale cache slots) may hold anything: a warp zeroes
 // them in shared memory before the product.  Masked tokens of the sequence itself
 // are finite in sound data: when an output is not, the epilogue looks for a
-// non-finite value among them and computes those rows again without it.
+// non-finite value among them, and where there is one the CTA takes its items a
+// second time.  In that pass the warp also clears such values of the diagonal
+// tiles, and the epilogue adds them to the rows that do see them.  Sound data pays
+// nothing for it; with one NaN near the end 8 x 4096 tokens, 32 heads of 128 on 8,
+// take 1954 us instead of 735, 65536 tokens, 16 heads of 256 on 2, 60.4 ms instead of 29.6.
 //
 // A slice of a prompt over a long history has few items: its key tiles are then
 // split, and each split leaves m, l and an unscaled o for a second kernel.
@@ -166,6 +170,9 @@ __device__ __forceinline__ bool elect_one() {
     return one != 0;
 }
 
+// Where a CTA is: its items, the same again for the sake of non-finite values, or past them.
+enum Pass { kFirst, kMending, kOver };
+
 // One item: tm tokens of sequence b from row0 on, of head h (with packing: of the heads of a group
 // from h on), over its key tiles from lo on.
 struct Item {
@@ -174,6 +181,7 @@ struct Item {
     int n[2];     // key tiles of each query tile (0: no rows, or none that sees a key)
     int tiles;    // key tiles loaded
     int end;      // rows of the last key tile that hold keys
+    int mend;     // non-finite values of V are cleared from this key on (that the first row does not see)
 };
 
 template <int DP>
@@ -248,44 +256,58 @@ __device__ __forceinline__ bool get_item(const PromptParams &p, const int *suffi
     return false;
 }
 
-// Warp-wide and rare.  Where V holds a non-finite value in channels c .. c + 31 of keys [k0, k1),
-// which some row of the tile does not see, the rows with `odd` compute their outputs again over the
-// keys [lo, seen) before k1 that they do see, with the reference m and 1 / l of the softmax (a part:
-// with 1, into part).
-__device__ __forceinline__ void redo_masked(const PromptParams &p, int b, int start, int row, int h, int c, int k0,
-                                            int k1, int lo, int seen, bool odd, float m, float inv, float *part) {
-    const int lane = threadIdx.x & 31, D = p.a.D, kvh = h / p.G;
-    const __nv_bfloat16 *kb = static_cast<const __nv_bfloat16 *>(p.a.k) + (long)kvh * D;
-    const __nv_bfloat16 *vb = static_cast<const __nv_bfloat16 *>(p.a.v) + (long)kvh * D;
-    bool found = false;
-    for (int j = k0 + lane; j < k1; j += 32) {
-        const long at = attn_key_row(p.a, b, start, j, p.a.vs);
-        for (int i = c; at >= 0 && i < min(c + 32, D); ++i) found |= !isfinite(__bfloat162float(vb[at + i]));
-    }
-    if (!__any_sync(0xffffffffu, found) || !odd) return;
-    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.a.q) + (long)row * p.a.qs + (long)h * D;
-    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) + ((size_t)row * p.a.H + h) * D;
-    const float scale = p.negate ? -p.c : p.c, ref = m == -INFINITY ? 0.f : m * p.c;
+// Bits 0 and 1: the low and the high bf16 of x are not finite.
+__device__ __forceinline__ uint32_t non_finite2(uint32_t x) {
+    return ((x & 0x7f80u) == 0x7f80u ? 1u : 0u) | ((x & 0x7f800000u) == 0x7f800000u ? 2u : 0u);
+}
+
+// Warp-wide: whether V holds a non-finite value in channels c .. c + 31 of keys [k0, k1).  With `add`,
+// each lane's row takes those of the keys before `seen` into its output (a part: into part).
+__device__ __forceinline__ bool masked_non_finite(const PromptParams &p, int b, int start, int kvh, int c, int k0, int k1,
+                                                  bool add, int seen, __nv_bfloat16 *out, float *part) {
+    const int lane = threadIdx.x & 31, D = p.a.D;
+    const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(p.a.v) + (long)kvh * D + c;
+    const int words = min(32, D - c) / 8;  // of 16 bytes; none past the last channel
     float f[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) f[i] = 0.f;
-    for (int j = lo; j < min(seen, k1); ++j) {
-        const long ka = attn_key_row(p.a, b, start, j, p.a.ks), va = attn_key_row(p.a, b, start, j, p.a.vs);
-        if (ka < 0) continue;  // (a zero value adds nothing)
-        float x = 0.f;
-#pragma unroll 1
-        for (int d = 0; d < D; ++d) x = fmaf(__bfloat162float(q[d]), __bfloat162float(kb[ka + d]), x);
-        const float w = exp2_fast(fmaf(x, scale, -ref)) * inv;
+    bool found = false;
+    for (int j0 = k0; j0 < k1; j0 += 32) {
+        const long at = j0 + lane < k1 ? attn_key_row(p.a, b, start, j0 + lane, p.a.vs) : -1;
+        uint32_t odd = 0;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (c + i < D) f[i] = fmaf(w, __bfloat162float(vb[va + c + i]), f[i]);
+        for (int i = 0; i < 4; ++i)
+            if (at >= 0 && i < words) {
+                const uint4 x = __ldg(reinterpret_cast<const uint4 *>(v + at + i * 8));
+                odd |= non_finite2(x.x) | non_finite2(x.y) | non_finite2(x.z) | non_finite2(x.w);
+            }
+        unsigned keys = __ballot_sync(0xffffffffu, odd != 0);
+        found |= keys != 0;
+        for (; add && keys != 0; keys &= keys - 1) {
+            const int k = __ffs(keys) - 1;
+            const long row = __shfl_sync(0xffffffffu, at, k);
+            if (j0 + k >= seen) continue;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < words) {
+                    const uint4 x = __ldg(reinterpret_cast<const uint4 *>(v + row + i * 8));
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        const uint32_t which = non_finite2(w[z]);
+                        f[i * 8 + 2 * z] += which & 1u ? __uint_as_float(w[z] << 16) : 0.f;
+                        f[i * 8 + 2 * z + 1] += which & 2u ? __uint_as_float(w[z] & 0xffff0000u) : 0.f;
+                    }
+                }
+        }
     }
 #pragma unroll
     for (int i = 0; i < 32; ++i)
-        if (c + i < D) {
-            if (part) part[c + i] = f[i];
-            else out[c + i] = __float2bfloat16_rn(f[i]);
+        if (f[i] != 0.f) {  // (NaN too)
+            if (part) part[c + i] += f[i];
+            else out[c + i] = __float2bfloat16_rn(__bfloat162float(out[c + i]) + f[i]);
         }
+    return found;
 }
 
 template <int DP>
@@ -305,6 +327,7 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
     Item *s_item = reinterpret_cast<Item *>(item_empty + 4);
     int *s_abort = reinterpret_cast<int *>(s_item + 4);
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(s_abort + 1);
+    volatile int *s_again = s_abort + 2, *s_pass = s_abort + 3;
     int *suffix = s_abort + 4;  // [bins + 1]
 
     const int tid = threadIdx.x, lane = tid & 31;
@@ -325,7 +348,7 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
         }
         for (int i = 0; i < 4; ++i) mbar_init(item_full + i, 1), mbar_init(item_empty + i, NQ * 5 + 1);
         fence_mbar_init();
-        *s_abort = 0;
+        *s_abort = 0, *s_again = 0, *s_pass = kFirst;
         tma_prefetch_desc(&qmap), tma_prefetch_desc(&kmap), tma_prefetch_desc(&vmap);
     }
     if (warp == kMmaWarp) {
@@ -362,16 +385,29 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
     volatile int *abort = s_abort;
     Item it;
     it.n[1] = 0;
+    // V tiles that the warp at the end of V changes in shared memory before they are used.
+    auto mended = [&](int j) { return (j + 1 == it.tiles && it.end < BN) || (it.lo + j + 1) * BN > it.mend; };
+    // The end of a pass of every warp, also of one that has given up: whether a second pass follows.
+    auto again = [&]() {
+        __syncwarp();
+        asm volatile("barrier.sync 1, %0;" ::"n"(C::THREADS) : "memory");
+        if (tid == 0) *s_pass = *s_pass == kFirst && *s_again && !*abort ? kMending : kOver;
+        asm volatile("barrier.sync 1, %0;" ::"n"(C::THREADS) : "memory");
+        return *s_pass == kMending;
+    };
     // Items come from the load warp through a ring of four; false past the last one.
     uint32_t n_item = 0;
     auto next_item = [&]() {
-        const uint32_t k = n_item & 3;
-        if (!wait_or_abort(item_full + k, (n_item >> 2) & 1, abort)) return false;
-        it = s_item[k];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(item_empty + k);
-        ++n_item;
-        return it.b >= 0;
+        while (true) {
+            const uint32_t k = n_item & 3;
+            if (!wait_or_abort(item_full + k, (n_item >> 2) & 1, abort)) return false;
+            it = s_item[k];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(item_empty + k);
+            ++n_item;
+            if (it.b >= 0) return true;
+            if (!again()) return false;
+        }
     };
 
     if (warp >= kTmaWarp) {
@@ -384,16 +420,23 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
             uint32_t q_phase = 0;
             const int boxes = BN / p.box_rows;  // boxes of a 64-channel block of a key tile
             // Every other round of items goes the other way round: the CTA that took the longest item
-            // of one takes the shortest of the next.
-            for (long first = 0;; first += gridDim.x, seq += 2 * it.tiles, ++n_item) {
-                const long idx = first + (n_item & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            // of one takes the shortest of the next.  (A second pass gives it the items of the first.)
+            bool back = false, mending = false;
+            for (long first = 0;;) {
+                const long idx = first + (back ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
                 if (!get_item<DP>(p, suffix, idx, it)) it.b = -1;
+                it.mend = mending ? it.kv - it.len + it.row0 + 1 : INT32_MAX;
                 if (!wait_or_abort(item_empty + (n_item & 3), ((n_item >> 2) & 1) ^ 1, abort)) goto done;
                 if (lane == 0) {
                     s_item[n_item & 3] = it;
                     mbar_arrive(item_full + (n_item & 3));
                 }
-                if (it.b < 0) break;
+                ++n_item;
+                if (it.b < 0) {
+                    if (!again()) break;
+                    first = 0, back = false, mending = true;
+                    continue;
+                }
 #pragma unroll
                 for (int t = 0; t < NQ; ++t) {
                     if (it.n[t] == 0) continue;
@@ -431,6 +474,7 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                         }
                     }
                 }
+                first += gridDim.x, back = !back, seq += 2 * it.tiles;
             }
         } else if (warp < kMmaWarp + NQ) {
             // ------------------------------------------------------------ products of query tile t
@@ -477,7 +521,7 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                     }
                     // (all that the products wait for but P comes before P)
                     if (!wait_slot(seq + 2 * j + 1)) goto done;
-                    if (j + 1 == it.tiles && it.end < BN) {
+                    if (mended(j)) {
                         if (!wait_or_abort(v_fixed + v, (fix_phase >> v) & 1, abort)) goto done;
                         fix_phase ^= 1u << v;
                     }
@@ -513,22 +557,35 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                 }
             }
         } else if (warp == kFixWarp) {
-            // ------------------------------------------------------------ rows of V past the last key
+            // ------------------------------------------------------------ rows of V past the last key, and in
+            // a second pass its non-finite values
             for (; next_item(); seq += 2 * it.tiles) {
                 for (int j = 0; j < it.tiles; ++j) {
                     // every V tile is waited for, so that no phase of its barrier goes by unseen
                     const uint32_t s = seq + 2 * j + 1, slot = slot_of(s);
                     if (!wait_or_abort(full + slot, phase_of(s), abort)) goto done;
                     if (lane == 0) mbar_arrive(empty + slot);
-                    if (j + 1 < it.tiles || it.end == BN) continue;
+                    if (!mended(j)) continue;
+                    const int end = j + 1 == it.tiles ? it.end : BN;
                     for (int c = 0; c < NB; ++c) {
                         uint4 *block = reinterpret_cast<uint4 *>(ring + slot * C::SLOT + c * BN * 128);
-                        for (int i = it.end * 8 + lane; i < BN * 8; i += 32) block[i] = make_uint4(0, 0, 0, 0);
+                        if (it.mend < INT32_MAX)
+                            for (int i = max(0, it.mend - (it.lo + j) * BN) * 8 + lane; i < end * 8; i += 32) {
+                                uint32_t *w = reinterpret_cast<uint32_t *>(block + i);
+#pragma unroll
+                                for (int z = 0; z < 4; ++z) {
+                                    const uint32_t x = w[z], which = non_finite2(x);
+                                    if (which) w[z] = x & (which & 1u ? 0xffff0000u : 0xffffffffu) & (which & 2u ? 0x0000ffffu : 0xffffffffu);
+                                }
+                            }
+                        for (int i = end * 8 + lane; i < BN * 8; i += 32) block[i] = make_uint4(0, 0, 0, 0);
                     }
                     fence_async_smem();
                     mbar_arrive(v_fixed + slot);
                 }
             }
+        } else {
+            while (again()) {}  // (one query tile: a warp without a role)
         }
     } else {
         if constexpr (NQ == 2) regs_inc<C::REGS_SOFTMAX>();
@@ -698,16 +755,23 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
             }
             __syncwarp();
             if (r >= it.len) odd = 0;
-            if (__any_sync(0xffffffffu, odd != 0))
+            // (a second pass: all keys that the V tiles were mended from)
+            const bool mending = *s_pass == kMending;
+            const int k0 = max(it.lo * BN, mending ? shift + it.row0 + 1 : least), k1 = min(it.kv, (it.lo + n) * BN);
+            if (k0 < k1 && (mending || __any_sync(0xffffffffu, odd != 0))) {
+                bool found = false;
 #pragma unroll 1
-                for (int c = 0; c < DP; c += 32)
-                    redo_masked(p, it.b, it.start, it.start + r, head, c, max(it.lo * BN, least - 1),
-                                min(it.kv, (it.lo + n) * BN), it.lo * BN, min(it.kv, shift + r + 1),
-                                (odd >> (c >> 5)) & 1, m, inv, whole ? nullptr : part.o);
+                for (int c = 0; c < p.a.D; c += 32)
+                    if (mending || __any_sync(0xffffffffu, (odd >> (c >> 5)) & 1))
+                        found |= masked_non_finite(p, it.b, it.start, it.h / p.G, c, k0, k1, mending,
+                                                   r < it.len ? min(it.kv, shift + r + 1) : 0, out, whole ? nullptr : part.o);
+                if (!mending && found && lane == 0) *s_again = 1;
+            }
             tc_fence_before();  // the next item's products follow this tile's next arrival
         }
     }
 done:
+    if (*s_pass != kOver) again();  // (gave up: the others wait for this warp at the end of the pass)
     __syncwarp();
     if (warp == kTmaWarp && *abort)  // copies in flight land before the CTA's memory goes
         for (int i = 0; i < SLOTS; ++i) {
