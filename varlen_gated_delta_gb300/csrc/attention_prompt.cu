@@ -26,9 +26,9 @@
 // are finite in sound data: when an output is not, the epilogue looks for a
 // non-finite value among them, and where there is one the CTA takes its items a
 // second time.  In that pass the warp also clears such values of the diagonal
-// tiles, and the epilogue adds them to the rows that do see them.  Sound data pays
-// nothing for it; with one NaN near the end 8 x 4096 tokens, 32 heads of 128 on 8,
-// take 1954 us instead of 735, 65536 tokens, 16 heads of 256 on 2, 60.4 ms instead of 29.6.
+// tiles, and the epilogue adds them to the rows that do see them.  8 x 4096 tokens, 32
+// heads of 128 on 8, take 1918 us instead of 709 with one NaN near the end; 65536 tokens,
+// 16 heads of 256 on 2, 60.6 ms instead of 29.8.
 //
 // A slice of a prompt over a long history has few items: its key tiles are then
 // split, and each split leaves m, l and an unscaled o for a second kernel.
@@ -170,8 +170,7 @@ __device__ __forceinline__ bool elect_one() {
     return one != 0;
 }
 
-// Where a CTA is: its items, the same again for the sake of non-finite values, or past them.
-enum Pass { kFirst, kMending, kOver };
+constexpr int kMend = 1 << 16;  // marks the items of a second pass
 
 // One item: tm tokens of sequence b from row0 on, of head h (with packing: of the heads of a group
 // from h on), over its key tiles from lo on.
@@ -180,8 +179,14 @@ struct Item {
     int split, lo;
     int n[2];     // key tiles of each query tile (0: no rows, or none that sees a key)
     int tiles;    // key tiles loaded
-    int end;      // rows of the last key tile that hold keys
-    int mend;     // non-finite values of V are cleared from this key on (that the first row does not see)
+    int end;      // rows of the last key tile that hold keys; a second pass adds kMend
+    // Keys from here on are hidden from the item's first row.
+    __device__ __forceinline__ int masked() const { return kv - len + row0 + 1; }
+    // Whether V tile j has rows to change before they are used: past the last key, and in a second pass
+    // those that are hidden from some row.
+    __device__ __forceinline__ bool changes_v(int j, int BN) const {
+        return (j + 1 == tiles && (end & (kMend - 1)) < BN) || (end >= kMend && (lo + j + 1) * BN > masked());
+    }
 };
 
 template <int DP>
@@ -261,6 +266,18 @@ __device__ __forceinline__ uint32_t non_finite2(uint32_t x) {
     return ((x & 0x7f80u) == 0x7f80u ? 1u : 0u) | ((x & 0x7f800000u) == 0x7f800000u ? 2u : 0u);
 }
 
+// Warp-wide: non-finite values of the rows from `from` on of a V tile in shared memory become 0.
+template <int DP>
+__device__ __noinline__ void clear_non_finite(unsigned char *tile, int from) {
+    for (int c = 0; c < Cfg<DP>::NB; ++c) {
+        uint32_t *block = reinterpret_cast<uint32_t *>(tile + c * Cfg<DP>::BN * 128);
+        for (int i = from * 32 + (threadIdx.x & 31); i < Cfg<DP>::BN * 32; i += 32) {
+            const uint32_t x = block[i], which = non_finite2(x);
+            if (which) block[i] = x & (which & 1u ? 0xffff0000u : 0xffffffffu) & (which & 2u ? 0x0000ffffu : 0xffffffffu);
+        }
+    }
+}
+
 // Warp-wide: whether V holds a non-finite value in channels c .. c + 31 of keys [k0, k1).  With `add`,
 // each lane's row takes those of the keys before `seen` into its output (a part: into part).
 __device__ __forceinline__ bool masked_non_finite(const PromptParams &p, int b, int start, int kvh, int c, int k0, int k1,
@@ -327,7 +344,7 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
     Item *s_item = reinterpret_cast<Item *>(item_empty + 4);
     int *s_abort = reinterpret_cast<int *>(s_item + 4);
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(s_abort + 1);
-    volatile int *s_again = s_abort + 2, *s_pass = s_abort + 3;
+    volatile int *s_again = s_abort + 2;
     int *suffix = s_abort + 4;  // [bins + 1]
 
     const int tid = threadIdx.x, lane = tid & 31;
@@ -348,7 +365,7 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
         }
         for (int i = 0; i < 4; ++i) mbar_init(item_full + i, 1), mbar_init(item_empty + i, NQ * 5 + 1);
         fence_mbar_init();
-        *s_abort = 0, *s_again = 0, *s_pass = kFirst;
+        *s_abort = 0, *s_again = 0;
         tma_prefetch_desc(&qmap), tma_prefetch_desc(&kmap), tma_prefetch_desc(&vmap);
     }
     if (warp == kMmaWarp) {
@@ -385,29 +402,16 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
     volatile int *abort = s_abort;
     Item it;
     it.n[1] = 0;
-    // V tiles that the warp at the end of V changes in shared memory before they are used.
-    auto mended = [&](int j) { return (j + 1 == it.tiles && it.end < BN) || (it.lo + j + 1) * BN > it.mend; };
-    // The end of a pass of every warp, also of one that has given up: whether a second pass follows.
-    auto again = [&]() {
-        __syncwarp();
-        asm volatile("barrier.sync 1, %0;" ::"n"(C::THREADS) : "memory");
-        if (tid == 0) *s_pass = *s_pass == kFirst && *s_again && !*abort ? kMending : kOver;
-        asm volatile("barrier.sync 1, %0;" ::"n"(C::THREADS) : "memory");
-        return *s_pass == kMending;
-    };
     // Items come from the load warp through a ring of four; false past the last one.
     uint32_t n_item = 0;
     auto next_item = [&]() {
-        while (true) {
-            const uint32_t k = n_item & 3;
-            if (!wait_or_abort(item_full + k, (n_item >> 2) & 1, abort)) return false;
-            it = s_item[k];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(item_empty + k);
-            ++n_item;
-            if (it.b >= 0) return true;
-            if (!again()) return false;
-        }
+        const uint32_t k = n_item & 3;
+        if (!wait_or_abort(item_full + k, (n_item >> 2) & 1, abort)) return false;
+        it = s_item[k];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(item_empty + k);
+        ++n_item;
+        return it.b >= 0;
     };
 
     if (warp >= kTmaWarp) {
@@ -420,23 +424,35 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
             uint32_t q_phase = 0;
             const int boxes = BN / p.box_rows;  // boxes of a 64-channel block of a key tile
             // Every other round of items goes the other way round: the CTA that took the longest item
-            // of one takes the shortest of the next.  (A second pass gives it the items of the first.)
+            // of one takes the shortest of the next.
+            long first = 0;
             bool back = false, mending = false;
-            for (long first = 0;;) {
-                const long idx = first + (back ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-                if (!get_item<DP>(p, suffix, idx, it)) it.b = -1;
-                it.mend = mending ? it.kv - it.len + it.row0 + 1 : INT32_MAX;
-                if (!wait_or_abort(item_empty + (n_item & 3), ((n_item >> 2) & 1) ^ 1, abort)) goto done;
+            auto send = [&]() {
+                if (!wait_or_abort(item_empty + (n_item & 3), ((n_item >> 2) & 1) ^ 1, abort)) return false;
                 if (lane == 0) {
                     s_item[n_item & 3] = it;
                     mbar_arrive(item_full + (n_item & 3));
                 }
                 ++n_item;
-                if (it.b < 0) {
-                    if (!again()) break;
-                    first = 0, back = false, mending = true;
-                    continue;
+                return true;
+            };
+            while (true) {
+                if (!get_item<DP>(p, suffix, first + (back ? gridDim.x - 1 - blockIdx.x : blockIdx.x), it)) {
+                    // An item of nothing: when it has been taken, the items before it are at their end.  If one of
+                    // them found cause, all are sent again.
+                    it = Item{};
+                    it.end = BN;
+                    const uint32_t k = n_item & 3, phase = (n_item >> 2) & 1;
+                    if (!mending && (!send() || !wait_or_abort(item_empty + k, phase, abort))) goto done;
+                    if (!mending && *s_again) {
+                        first = 0, back = false, mending = true;
+                        continue;
+                    }
+                    it.b = -1;
                 }
+                if (mending) it.end += kMend;
+                if (!send()) goto done;
+                if (it.b < 0) break;
 #pragma unroll
                 for (int t = 0; t < NQ; ++t) {
                     if (it.n[t] == 0) continue;
@@ -521,7 +537,7 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                     }
                     // (all that the products wait for but P comes before P)
                     if (!wait_slot(seq + 2 * j + 1)) goto done;
-                    if (mended(j)) {
+                    if (it.changes_v(j, BN)) {
                         if (!wait_or_abort(v_fixed + v, (fix_phase >> v) & 1, abort)) goto done;
                         fix_phase ^= 1u << v;
                     }
@@ -565,27 +581,20 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                     const uint32_t s = seq + 2 * j + 1, slot = slot_of(s);
                     if (!wait_or_abort(full + slot, phase_of(s), abort)) goto done;
                     if (lane == 0) mbar_arrive(empty + slot);
-                    if (!mended(j)) continue;
-                    const int end = j + 1 == it.tiles ? it.end : BN;
-                    for (int c = 0; c < NB; ++c) {
-                        uint4 *block = reinterpret_cast<uint4 *>(ring + slot * C::SLOT + c * BN * 128);
-                        if (it.mend < INT32_MAX)
-                            for (int i = max(0, it.mend - (it.lo + j) * BN) * 8 + lane; i < end * 8; i += 32) {
-                                uint32_t *w = reinterpret_cast<uint32_t *>(block + i);
-#pragma unroll
-                                for (int z = 0; z < 4; ++z) {
-                                    const uint32_t x = w[z], which = non_finite2(x);
-                                    if (which) w[z] = x & (which & 1u ? 0xffff0000u : 0xffffffffu) & (which & 2u ? 0x0000ffffu : 0xffffffffu);
-                                }
-                            }
-                        for (int i = end * 8 + lane; i < BN * 8; i += 32) block[i] = make_uint4(0, 0, 0, 0);
+                    if (!it.changes_v(j, BN)) continue;
+                    unsigned char *tile = ring + slot * C::SLOT;
+                    if (it.end >= kMend) clear_non_finite<DP>(tile, max(0, it.masked() - (it.lo + j) * BN));
+                    if (j + 1 == it.tiles) {
+                        const int end = it.end % kMend;
+                        for (int c = 0; c < NB; ++c) {
+                            uint4 *block = reinterpret_cast<uint4 *>(tile + c * BN * 128);
+                            for (int i = end * 8 + lane; i < BN * 8; i += 32) block[i] = make_uint4(0, 0, 0, 0);
+                        }
                     }
                     fence_async_smem();
                     mbar_arrive(v_fixed + slot);
                 }
             }
-        } else {
-            while (again()) {}  // (one query tile: a warp without a role)
         }
     } else {
         if constexpr (NQ == 2) regs_inc<C::REGS_SOFTMAX>();
@@ -756,8 +765,8 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
             __syncwarp();
             if (r >= it.len) odd = 0;
             // (a second pass: all keys that the V tiles were mended from)
-            const bool mending = *s_pass == kMending;
-            const int k0 = max(it.lo * BN, mending ? shift + it.row0 + 1 : least), k1 = min(it.kv, (it.lo + n) * BN);
+            const bool mending = it.end >= kMend;
+            const int k0 = max(it.lo * BN, mending ? it.masked() : least), k1 = min(it.kv, (it.lo + n) * BN);
             if (k0 < k1 && (mending || __any_sync(0xffffffffu, odd != 0))) {
                 bool found = false;
 #pragma unroll 1
@@ -765,13 +774,15 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                     if (mending || __any_sync(0xffffffffu, (odd >> (c >> 5)) & 1))
                         found |= masked_non_finite(p, it.b, it.start, it.h / p.G, c, k0, k1, mending,
                                                    r < it.len ? min(it.kv, shift + r + 1) : 0, out, whole ? nullptr : part.o);
-                if (!mending && found && lane == 0) *s_again = 1;
+                if (!mending && found && lane == 0) {
+                    *s_again = 1;
+                    __threadfence_block();
+                }
             }
             tc_fence_before();  // the next item's products follow this tile's next arrival
         }
     }
 done:
-    if (*s_pass != kOver) again();  // (gave up: the others wait for this warp at the end of the pass)
     __syncwarp();
     if (warp == kTmaWarp && *abort)  // copies in flight land before the CTA's memory goes
         for (int i = 0; i < SLOTS; ++i) {
