@@ -13,9 +13,12 @@
 // + (hi lo' + lo hi'), which leaves out another 2^-22 |a b|.  The large and
 // the small terms of a score have accumulators of their own, and the output of
 // a key tile is summed apart and then added in fp32, so that few additions
-// round inside the tensor cores.  Bound by these products (mma.sync in tf32, three for
+// round inside the tensor cores.  Infinities, and what rounds up to one, have no such
+// split: scores that come out NaN are taken again as plain sums, and a tile whose output
+// is not finite goes by a second time, without the non-finite values, which then join the
+// rows that see them.  Bound by these products (mma.sync in tf32, three for
 // each one wanted) and their latency: the tensor pipe is 50% active, and the two warps
-// of a scheduler mostly wait for it or for a product's result.  465 us, 35 TFLOP/s, for 4 x 1000 tokens, 16
+// of a scheduler mostly wait for it or for a product's result.  471 us, 35 TFLOP/s, for 4 x 1000 tokens, 16
 // heads of 128 on 4, where multiply-adds on the fp32 pipe in the same tiles took
 // 558 us, and 301 against 445 us for 2 histories of up to 101321 tokens.
 //
@@ -147,134 +150,149 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const Attn a, int sp
     };
     constexpr std::integral_constant<int, LD> kLd{};
     constexpr std::integral_constant<int, LDV> kLdv{};
-    load_keys(kLd, sk, a.k, k0, a.ks);
-    load_keys(kLdv, sv, a.v, k0, a.vs);
 
-    float o[DP / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < DP / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    float o[DP / 8][4], m[2], l[2];
     int seen[2];  // keys that rows g and g + 8 see
 #pragma unroll
     for (int z = 0; z < 2; ++z) seen[z] = min(kv, shift + (r0 + mt * 16 + g + 8 * z) / G + 1);
     const float c = a.scale * kLog2e;
 
-    // The next tile's keys are on their way under the values' product, its values under the scores.
-    for (int kt = k0; kt < k1; ++kt) {
-        const int j0 = kt * kKeys;
-        copies_landed<1>();
-        __syncthreads();
-        const bool edge = j0 + kKeys > least;  // some row does not see the whole tile
-        // ---- scores of 16 rows and KW keys
-        float s[KW / 8][4], small[KW / 8][4];
+    // The keys' way past the rows.  Where it leaves an output that is not finite it is taken again, and then
+    // looks at all values: the non-finite ones become 0, the others are halved, so that none rounds up to inf.
+    auto pass = [&](auto looks) {
+        constexpr bool careful = decltype(looks)::value;
+        load_keys(kLd, sk, a.k, k0, a.ks);
+        load_keys(kLdv, sv, a.v, k0, a.vs);
+        m[0] = m[1] = -INFINITY, l[0] = l[1] = 0.f;
 #pragma unroll
-        for (int n = 0; n < KW / 8; ++n)
+        for (int i = 0; i < DP / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        // The next tile's keys are on their way under the values' product, its values under the scores.
+        for (int kt = k0; kt < k1; ++kt) {
+            const int j0 = kt * kKeys;
+            copies_landed<1>();
+            __syncthreads();
+            const bool edge = j0 + kKeys > least;  // some row does not see the whole tile
+            // ---- scores of 16 rows and KW keys
+            float s[KW / 8][4], small[KW / 8][4];
 #pragma unroll
-            for (int z = 0; z < 4; ++z) s[n][z] = small[n][z] = 0.f;
+            for (int n = 0; n < KW / 8; ++n)
+#pragma unroll
+                for (int z = 0; z < 4; ++z) s[n][z] = small[n][z] = 0.f;
 #pragma unroll 2
-        for (int ks = 0; ks < DP; ks += 8) {
-            const float2 q0 = *reinterpret_cast<const float2 *>(sq + (mt * 16 + g) * LD + ks + 2 * t4);
-            const float2 q1 = *reinterpret_cast<const float2 *>(sq + (mt * 16 + g + 8) * LD + ks + 2 * t4);
-            uint32_t qh[4], ql[4];
-            split(q0.x, qh[0], ql[0]), split(q1.x, qh[1], ql[1]);
-            split(q0.y, qh[2], ql[2]), split(q1.y, qh[3], ql[3]);
+            for (int ks = 0; ks < DP; ks += 8) {
+                const float2 q0 = *reinterpret_cast<const float2 *>(sq + (mt * 16 + g) * LD + ks + 2 * t4);
+                const float2 q1 = *reinterpret_cast<const float2 *>(sq + (mt * 16 + g + 8) * LD + ks + 2 * t4);
+                uint32_t qh[4], ql[4];
+                split(q0.x, qh[0], ql[0]), split(q1.x, qh[1], ql[1]);
+                split(q0.y, qh[2], ql[2]), split(q1.y, qh[3], ql[3]);
 #pragma unroll
-            for (int n = 0; n < KW / 8; ++n) {
-                const float2 kk = *reinterpret_cast<const float2 *>(sk + (wk * KW + n * 8 + g) * LD + ks + 2 * t4);
-                uint32_t h0, l0, h1, l1;
-                split(kk.x, h0, l0), split(kk.y, h1, l1);
-                mma1688(small[n], ql, h0, h1);
-                mma1688(small[n], qh, l0, l1);
-                mma1688(s[n], qh, h0, h1);
+                for (int n = 0; n < KW / 8; ++n) {
+                    const float2 kk = *reinterpret_cast<const float2 *>(sk + (wk * KW + n * 8 + g) * LD + ks + 2 * t4);
+                    uint32_t h0, l0, h1, l1;
+                    split(kk.x, h0, l0), split(kk.y, h1, l1);
+                    mma1688(small[n], ql, h0, h1);
+                    mma1688(small[n], qh, l0, l1);
+                    mma1688(s[n], qh, h0, h1);
+                }
             }
-        }
-        bool odd = false;
+            bool odd = false;
 #pragma unroll
-        for (int n = 0; n < KW / 8; ++n)
+            for (int n = 0; n < KW / 8; ++n)
 #pragma unroll
-            for (int z = 0; z < 4; ++z) s[n][z] += small[n][z], odd |= s[n][z] != s[n][z];
-        if (__any_sync(0xffffffffu, odd)) {
-            // inf has no split: take the scores of this warp as plain sums
+                for (int z = 0; z < 4; ++z) s[n][z] += small[n][z], odd |= s[n][z] != s[n][z];
+            if (__any_sync(0xffffffffu, odd)) {
+                // inf has no split: take the scores of this warp as plain sums
+#pragma unroll
+                for (int n = 0; n < KW / 8; ++n)
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        const float *qr = sq + (mt * 16 + g + 8 * (z >> 1)) * LD, *kr = sk + (wk * KW + n * 8 + 2 * t4 + (z & 1)) * LD;
+                        float x = 0.f;
+#pragma unroll 1
+                        for (int d = 0; d < D; ++d) x = fmaf(qr[d], kr[d], x);
+                        s[n][z] = x;
+                    }
+            }
+            __syncthreads();
+            load_keys(kLd, sk, a.k, kt + 1, a.ks);
+            // ---- running softmax of rows g and g + 8
+            float mx[2] = {m[0], m[1]};
 #pragma unroll
             for (int n = 0; n < KW / 8; ++n)
 #pragma unroll
                 for (int z = 0; z < 4; ++z) {
-                    const float *qr = sq + (mt * 16 + g + 8 * (z >> 1)) * LD, *kr = sk + (wk * KW + n * 8 + 2 * t4 + (z & 1)) * LD;
-                    float x = 0.f;
-#pragma unroll 1
-                    for (int d = 0; d < D; ++d) x = fmaf(qr[d], kr[d], x);
-                    s[n][z] = x;
+                    s[n][z] *= c;
+                    if (edge && j0 + wk * KW + n * 8 + 2 * t4 + (z & 1) >= seen[z >> 1]) s[n][z] = -INFINITY;
+                    mx[z >> 1] = fmaxf(mx[z >> 1], s[n][z]);
                 }
-        }
-        __syncthreads();
-        load_keys(kLd, sk, a.k, kt + 1, a.ks);
-        // ---- running softmax of rows g and g + 8
-        float mx[2] = {m[0], m[1]};
+            float ref[2];
 #pragma unroll
-        for (int n = 0; n < KW / 8; ++n)
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {
-                s[n][z] *= c;
-                if (edge && j0 + wk * KW + n * 8 + 2 * t4 + (z & 1) >= seen[z >> 1]) s[n][z] = -INFINITY;
-                mx[z >> 1] = fmaxf(mx[z >> 1], s[n][z]);
+            for (int z = 0; z < 2; ++z) {
+                mx[z] = fmaxf(mx[z], __shfl_xor_sync(0xffffffffu, mx[z], 1));
+                mx[z] = fmaxf(mx[z], __shfl_xor_sync(0xffffffffu, mx[z], 2));
+                ref[z] = mx[z] == -INFINITY ? 0.f : mx[z];  // (a row that has seen nothing yet)
             }
-        float ref[2];
+            if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
+                const float f0 = exp2_fast(m[0] - ref[0]), f1 = exp2_fast(m[1] - ref[1]);
+                l[0] *= f0, l[1] *= f1;
 #pragma unroll
-        for (int z = 0; z < 2; ++z) {
-            mx[z] = fmaxf(mx[z], __shfl_xor_sync(0xffffffffu, mx[z], 1));
-            mx[z] = fmaxf(mx[z], __shfl_xor_sync(0xffffffffu, mx[z], 2));
-            ref[z] = mx[z] == -INFINITY ? 0.f : mx[z];  // (a row that has seen nothing yet)
-        }
-        if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
-            const float f0 = exp2_fast(m[0] - ref[0]), f1 = exp2_fast(m[1] - ref[1]);
-            l[0] *= f0, l[1] *= f1;
+                for (int i = 0; i < DP / 8; ++i) o[i][0] *= f0, o[i][1] *= f0, o[i][2] *= f1, o[i][3] *= f1;
+                m[0] = mx[0], m[1] = mx[1];
+            }
+            // probabilities as operand fragments: k index t is key 2 t, t + 4 is key 2 t + 1
+            uint32_t ph[KW / 8][4], pl[KW / 8][4];
 #pragma unroll
-            for (int i = 0; i < DP / 8; ++i) o[i][0] *= f0, o[i][1] *= f0, o[i][2] *= f1, o[i][3] *= f1;
-            m[0] = mx[0], m[1] = mx[1];
-        }
-        // probabilities as operand fragments: k index t is key 2 t, t + 4 is key 2 t + 1
-        uint32_t ph[KW / 8][4], pl[KW / 8][4];
+            for (int n = 0; n < KW / 8; ++n) {
+                float e[4];
 #pragma unroll
-        for (int n = 0; n < KW / 8; ++n) {
-            float e[4];
+                for (int z = 0; z < 4; ++z) e[z] = exp2_fast(s[n][z] - ref[z >> 1]), l[z >> 1] += e[z];
+                split(e[0], ph[n][0], pl[n][0]), split(e[2], ph[n][1], pl[n][1]);
+                split(e[1], ph[n][2], pl[n][2]), split(e[3], ph[n][3], pl[n][3]);
+            }
+            copies_landed<1>();
+            __syncthreads();
+            if (edge || careful) {
+                // values that some row must not see: non-finite ones become 0 and join their rows at the end
+                for (int i = threadIdx.x; i < kKeys * DP; i += kThreads) {
+                    float &v = sv[(i / DP) * LDV + i % DP];
+                    if (!isfinite(v)) v = 0.f, s_bad = 1;
+                    else if (careful) v *= 0.5f;
+                }
+                __syncthreads();
+            }
+            // ---- o += P V, two blocks of eight channels at a time
 #pragma unroll
-            for (int z = 0; z < 4; ++z) e[z] = exp2_fast(s[n][z] - ref[z >> 1]), l[z >> 1] += e[z];
-            split(e[0], ph[n][0], pl[n][0]), split(e[2], ph[n][1], pl[n][1]);
-            split(e[1], ph[n][2], pl[n][2]), split(e[3], ph[n][3], pl[n][3]);
-        }
-        copies_landed<1>();
-        __syncthreads();
-        if (edge) {
-            // values that some row must not see: non-finite ones become 0 and join their rows at the end
-            for (int i = threadIdx.x; i < kKeys * DP; i += kThreads) {
-                float &v = sv[(i / DP) * LDV + i % DP];
-                if (!isfinite(v)) v = 0.f, s_bad = 1;
+            for (int i = 0; i < DP / 8; i += 2) {
+                float big[2][4] = {}, rest[2][4] = {};
+#pragma unroll
+                for (int n = 0; n < KW / 8; ++n)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const float *v = sv + (wk * KW + n * 8 + 2 * t4) * LDV + (i + y) * 8 + g;
+                        uint32_t h0, l0, h1, l1;
+                        split(v[0], h0, l0), split(v[LDV], h1, l1);
+                        mma1688(rest[y], pl[n], h0, h1);
+                        mma1688(rest[y], ph[n], l0, l1);
+                        mma1688(big[y], ph[n], h0, h1);
+                    }
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) o[i + y][z] += big[y][z] + rest[y][z];
             }
             __syncthreads();
+            load_keys(kLdv, sv, a.v, kt + 1, a.vs);
         }
-        // ---- o += P V, two blocks of eight channels at a time
+        copies_landed<0>();
+    };
+    pass(std::false_type{});
+    float finite = 0.f;  // NaN when an output is not
 #pragma unroll
-        for (int i = 0; i < DP / 8; i += 2) {
-            float big[2][4] = {}, rest[2][4] = {};
+    for (int i = 0; i < DP / 8; ++i)
 #pragma unroll
-            for (int n = 0; n < KW / 8; ++n)
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const float *v = sv + (wk * KW + n * 8 + 2 * t4) * LDV + (i + y) * 8 + g;
-                    uint32_t h0, l0, h1, l1;
-                    split(v[0], h0, l0), split(v[LDV], h1, l1);
-                    mma1688(rest[y], pl[n], h0, h1);
-                    mma1688(rest[y], ph[n], l0, l1);
-                    mma1688(big[y], ph[n], h0, h1);
-                }
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-#pragma unroll
-                for (int z = 0; z < 4; ++z) o[i + y][z] += big[y][z] + rest[y][z];
-        }
-        __syncthreads();
-        load_keys(kLdv, sv, a.v, kt + 1, a.vs);
-    }
-    copies_landed<0>();
+        for (int z = 0; z < 4; ++z) finite = fmaf(o[i][z], 0.f, finite);
+    const bool careful = __syncthreads_or(finite != 0.f);
+    if (careful) pass(std::true_type{});
 #pragma unroll
     for (int z = 0; z < 2; ++z) {
         l[z] += __shfl_xor_sync(0xffffffffu, l[z], 1);
@@ -312,13 +330,39 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const Attn a, int sp
                     }
             __syncthreads();
         }
+        if (wk != WK - 1 && !careful) return;
+    }
+    if (careful) {
+        // the values that were taken out, to the rows that see them
+        for (int kt = k0; kt < k1; ++kt) {
+            __syncthreads();
+            load_keys(kLdv, sv, a.v, kt, a.vs);
+            copies_landed<0>();
+            __syncthreads();
+            bool odd = false;
+            for (int i = threadIdx.x; i < kKeys * DP; i += kThreads) odd |= !isfinite(sv[(i / DP) * LDV + i % DP]);
+            if (!__syncthreads_or(odd)) continue;
+#pragma unroll 1
+            for (int j = 0; j < kKeys; ++j)
+#pragma unroll
+                for (int z = 0; z < 2; ++z)
+                    if (kt * kKeys + j < seen[z])
+#pragma unroll
+                        for (int i = 0; i < DP / 8; ++i)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const float v = sv[j * LDV + i * 8 + 2 * t4 + y];
+                                if (!isfinite(v)) o[i][2 * z + y] += v;
+                            }
+        }
         if (wk != WK - 1) return;
     }
+    const float unit = careful ? 2.f : 1.f;  // of o
 #pragma unroll
     for (int z = 0; z < 2; ++z) {
         const int r = mt * 16 + g + 8 * z;
         if (r >= rows) continue;
-        if (s_bad)
+        if (s_bad && !careful)
             for (int j = max(0, min(least, k1 * kKeys) / kKeys) * kKeys; j < min(seen[z], k1 * kKeys); ++j) {
                 const long at = j >= k0 * kKeys ? attn_key_row(a, b, start, j, a.vs) : -1;
                 if (at < 0) continue;
@@ -339,7 +383,7 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const Attn a, int sp
             for (int i = 0; i < DP / 8; ++i)
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
-                    if (i * 8 + 2 * t4 + y < D) out[i * 8 + 2 * t4 + y] = from_f32<T>(l[z] != 0.f ? o[i][2 * z + y] * inv : 0.f);
+                    if (i * 8 + 2 * t4 + y < D) out[i * 8 + 2 * t4 + y] = from_f32<T>(l[z] != 0.f ? o[i][2 * z + y] * inv * unit : 0.f);
         } else {
             const Part part(a, splits, row, blockIdx.z);
             if (t4 == 0) part.ml[0] = m[z], part.ml[1] = l[z];
@@ -347,7 +391,7 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const Attn a, int sp
             for (int i = 0; i < DP / 8; ++i)
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
-                    if (i * 8 + 2 * t4 + y < D) part.o[i * 8 + 2 * t4 + y] = o[i][2 * z + y];
+                    if (i * 8 + 2 * t4 + y < D) part.o[i * 8 + 2 * t4 + y] = o[i][2 * z + y] * unit;
         }
     }
 }
