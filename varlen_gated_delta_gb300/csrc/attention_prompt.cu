@@ -340,8 +340,8 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(ring + SLOTS * C::SLOT);
     uint64_t *full = bars, *empty = full + SLOTS, *q_full = empty + SLOTS, *q_empty = q_full + 2,
              *s_full = q_empty + 2, *p_full = s_full + 2, *o_done = p_full + 2, *v_fixed = o_done + 2, *turn = v_fixed + SLOTS,
-             *p_half = turn + 2, *item_full = p_half + 2, *item_empty = item_full + 4;
-    Item *s_item = reinterpret_cast<Item *>(item_empty + 4);
+             *p_half = turn + 2, *item_full = p_half + 2, *item_empty = item_full + 4, *drained = item_empty + 4;
+    Item *s_item = reinterpret_cast<Item *>(drained + 2);
     int *s_abort = reinterpret_cast<int *>(s_item + 4);
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(s_abort + 1);
     volatile int *s_again = s_abort + 2;
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full + i, 1), mbar_init(q_empty + i, 1);
             mbar_init(s_full + i, 1), mbar_init(p_full + i, 128), mbar_init(o_done + i, 1);
-            mbar_init(turn + i, 128), mbar_init(p_half + i, 128);
+            mbar_init(turn + i, 128), mbar_init(p_half + i, 128), mbar_init(drained + i, 1);
         }
         for (int i = 0; i < 4; ++i) mbar_init(item_full + i, 1), mbar_init(item_empty + i, NQ * 5 + 1);
         fence_mbar_init();
@@ -784,13 +784,21 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
     }
 done:
     __syncwarp();
-    if (warp == kTmaWarp && *abort)  // copies in flight land before the CTA's memory goes
-        for (int i = 0; i < SLOTS; ++i) {
-            mbar_wait(full + i, 0, 1000000), mbar_wait(full + i, 1, 1000000);
-            if (i < NQ) mbar_wait(q_full + i, 0, 1000000), mbar_wait(q_full + i, 1, 1000000);
-        }
     tc_fence_before();
     __syncthreads();
+    if (*abort) {  // copies and products in flight end before the CTA's memory goes
+        if (warp == kTmaWarp)
+            for (int i = 0; i < SLOTS; ++i) {
+                mbar_wait(full + i, 0, 1000000), mbar_wait(full + i, 1, 1000000);
+                if (i < NQ) mbar_wait(q_full + i, 0, 1000000), mbar_wait(q_full + i, 1, 1000000);
+            }
+        if (warp >= kMmaWarp && warp < kMmaWarp + NQ) {
+            if (elect_one()) mma_commit(drained + (warp - kMmaWarp));
+            __syncwarp();
+            mbar_wait(drained + (warp - kMmaWarp), 0, 10000000);
+        }
+        __syncthreads();
+    }
     if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
