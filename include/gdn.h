@@ -638,10 +638,18 @@ GDN_API int gdn_attention_paged(const void *q, const void *k_cache, const void *
 
 /*
  * Synchronises `stream` and returns GDN_ERR_TIMEOUT when a bounded device-side
- * wait of an attention call has given up on the current device since the last
- * query (the outputs of that call are then incomplete), else GDN_OK.
+ * wait of an attention call has given up on the current device, on any stream,
+ * since the last query on this stream (the outputs of that call are then
+ * incomplete), else GDN_OK.  A stream's first query covers all that came before.
  */
 GDN_API int gdn_attention_status(void *stream);
+
+/*
+ * gdn_selftest_attention_timeout - the wait of the attention kernels on a
+ * barrier that nothing completes: it gives up after limit_us (1 .. 1000000)
+ * microseconds, which gdn_attention_status then reports.
+ */
+GDN_API int gdn_selftest_attention_timeout(int limit_us, void *stream);
 
 /* Workspace bytes of gdn_attention_paged (0 on bad input). */
 GDN_API size_t gdn_attention_paged_workspace_bytes(int B, int N, int H, int HKV, int D,

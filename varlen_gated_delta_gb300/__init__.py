@@ -36,8 +36,7 @@ __all__ = [
     "gdn_selftest_wait_timeout", "gdn_dense_workspace_bytes", "gdn_workspace_bytes_ex",
     "gdn_dense_workspace_bytes_ex", "gdn_page_plan", "gdn_qk_norm_rope", "gdn_attention_varlen",
     "gdn_attention_paged", "gdn_attention_paged_workspace_bytes", "gdn_attention_status",
-    "GDN_ROPE_HALF",
-    "GDN_ROPE_PAIRS",
+    "gdn_selftest_attention_timeout", "GDN_ROPE_HALF", "GDN_ROPE_PAIRS",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -125,6 +124,8 @@ def load_library():
     lib.gdn_attention_paged.argtypes = [vp] * 7 + [i] * 9 + [i64, f, i, vp, sz, vp]
     lib.gdn_attention_status.argtypes = [vp]
     lib.gdn_attention_status.restype = i
+    lib.gdn_selftest_attention_timeout.argtypes = [i, vp]
+    lib.gdn_selftest_attention_timeout.restype = i
     lib.gdn_attention_paged_workspace_bytes.argtypes = [i] * 6
     lib.gdn_attention_paged_workspace_bytes.restype = sz
     for name in ("gdn_conv1d_varlen", "gdn_prepare", "gdn_delta_varlen", "gdn_layer_varlen",
@@ -713,9 +714,15 @@ def gdn_attention_varlen(q, k, v, offsets, *, scale=0.0, out=None):
 
 def gdn_attention_status(device=None) -> None:
     """Synchronise the current stream; raise GdnError (GDN_ERR_TIMEOUT) when a wait inside an
-    attention kernel gave up since the last query."""
+    attention kernel gave up, on any stream of the device, since the last query on this one."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
     _check(load_library().gdn_attention_status(_stream(dev)))
+
+
+def gdn_selftest_attention_timeout(limit_us: int = 1000) -> None:
+    """Launch, on the current stream, a wait of the attention kernels that gives up after
+    ``limit_us``; gdn_attention_status then reports it."""
+    _check(load_library().gdn_selftest_attention_timeout(limit_us, _stream(torch.device("cuda", torch.cuda.current_device()))))
 
 
 def gdn_attention_paged_workspace_bytes(B, N, H, HKV, D, max_q) -> int:

@@ -45,6 +45,10 @@
 // warpgroups, whose work a score is the same for half the products.  32 x U[1, 512],
 // 32 heads on 8: 54 us, bound by the chain of one or two key tiles an item.
 #include <cmath>
+#include <exception>
+#include <map>
+#include <mutex>
+#include <utility>
 
 #include "attention.cuh"
 #include "sm100.cuh"
@@ -58,8 +62,9 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr int kMaxBins = 4096;  // bins of the longest-first order
 constexpr float kLazy = 8.f;    // growth of the row maximum (log2) that O waits for
 
-// Set when a bounded wait of an attention kernel has given up.
-__device__ int g_attention_timeout;
+// Bounded waits of attention kernels that have given up.  It only grows, so that no query takes a report
+// from another.
+__device__ unsigned g_attention_timeouts;
 
 // Registers a thread of this warpgroup gives up (Dec) or takes (Inc) from here on.
 template <int N>
@@ -105,9 +110,9 @@ struct PromptParams {
     int splits;     // of the key tiles of an item; more than one: parts for a second kernel
 };
 
-// Warp-wide mbarrier wait that gives up, for the whole warp, after kWaitLimitNs
-// or when another role has.
-__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile int *abort) {
+// Warp-wide mbarrier wait that gives up, for the whole warp, after limit_ns or when another role has.
+__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                              uint64_t limit_ns = kWaitLimitNs) {
     const uint32_t addr = smem_u32(bar);
     bool ok = mbar_try_wait(addr, parity);
     if (!ok) {
@@ -117,9 +122,9 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, vo
 #pragma unroll 1
             for (int i = 0; i < 32 && !ok; ++i) ok = mbar_try_wait(addr, parity);
             if (!ok && *abort) stop = true;
-            if (!ok && !stop && global_timer_ns() - t0 > kWaitLimitNs) {
+            if (!ok && !stop && global_timer_ns() - t0 > limit_ns) {
                 *abort = 1;
-                atomicExch(&g_attention_timeout, 1);
+                atomicAdd(&g_attention_timeouts, 1u);
                 stop = true;
             }
         }
@@ -802,6 +807,19 @@ done:
     if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
+// A wait that nothing ends: how the way out of one is tested.
+__global__ void wait_probe_kernel(uint64_t limit_ns) {
+    __shared__ __align__(8) uint64_t bar;
+    __shared__ int s_abort;
+    if (threadIdx.x == 0) {
+        mbar_init(&bar, 1);
+        fence_mbar_init();
+        s_abort = 0;
+    }
+    __syncwarp();
+    wait_or_abort(&bar, 0, &s_abort, limit_ns);
+}
+
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -915,14 +933,31 @@ size_t attention_prompt_part_floats(int B, int N, int H, int HKV, int D, int max
 }
 
 int attention_timeouts(cudaStream_t s, cudaError_t *e) {
-    int seen = 0;
-    const int none = 0;
-    *e = cudaMemcpyFromSymbolAsync(&seen, g_attention_timeout, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+    // What the last query on each stream has seen.
+    static std::mutex lock;
+    static std::map<std::pair<int, cudaStream_t>, unsigned> last;
+    unsigned now = 0;
+    int dev = 0;
+    if ((*e = cudaGetDevice(&dev)) != cudaSuccess) return 0;
+    *e = cudaMemcpyFromSymbolAsync(&now, g_attention_timeouts, sizeof(now), 0, cudaMemcpyDeviceToHost, s);
     if (*e == cudaSuccess) *e = cudaStreamSynchronize(s);
-    if (*e == cudaSuccess && seen)
-        *e = cudaMemcpyToSymbolAsync(g_attention_timeout, &none, sizeof(int), 0, cudaMemcpyHostToDevice, s);
-    if (*e == cudaSuccess && seen) *e = cudaStreamSynchronize(s);
-    return seen;
+    if (*e != cudaSuccess) return 0;
+    try {
+        const std::lock_guard<std::mutex> hold(lock);
+        unsigned &was = last[{dev, s}];
+        const bool late = was != now;
+        was = now;
+        return late;
+    } catch (const std::exception &) {  // (no memory: the next query tells)
+        *e = cudaErrorMemoryAllocation;
+        return 0;
+    }
+}
+
+cudaError_t launch_attention_wait_probe(int limit_us, cudaStream_t s) {
+    const cudaError_t e = launch_kernel(wait_probe_kernel, dim3(1), dim3(32), 0, s, false, (uint64_t)limit_us * 1000u);
+    note_launch();
+    return e;
 }
 
 bool attention_prompt_supported(const Attn &a, int dtype) {

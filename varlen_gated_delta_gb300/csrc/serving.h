@@ -75,7 +75,9 @@ cudaError_t launch_attention_split(const Attn &a, void *ws, cudaStream_t s);
 bool attention_prompt_supported(const Attn &a, int dtype);
 size_t attention_prompt_part_floats(int B, int N, int H, int HKV, int D, int max_q);
 cudaError_t launch_attention_prompt(const Attn &a, int min_rows, cudaStream_t s);
-// Synchronises s; non-zero when a bounded wait gave up since the last call.
+// Synchronises s; non-zero when a bounded wait gave up since the last call for this stream.
 int attention_timeouts(cudaStream_t s, cudaError_t *e);
+// A kernel whose only wait gives up.
+cudaError_t launch_attention_wait_probe(int limit_us, cudaStream_t s);
 
 }  // namespace gdn

@@ -132,6 +132,13 @@ int gdn_attention_status(void *stream) {
     return late ? set_error(GDN_ERR_TIMEOUT, "a wait inside an attention kernel gave up") : GDN_OK;
 }
 
+int gdn_selftest_attention_timeout(int limit_us, void *stream) {
+    set_error(GDN_OK, "%s", "");
+    if (limit_us < 1 || limit_us > 1000000)
+        return set_error(GDN_ERR_SHAPE, "limit_us=%d outside [1, 1000000]", limit_us);
+    return launched(launch_attention_wait_probe(limit_us, static_cast<cudaStream_t>(stream)), "self-test launch");
+}
+
 size_t gdn_attention_paged_workspace_bytes(int B, int N, int H, int HKV, int D, int max_q) {
     if (B < 1 || max_q < 0 || check_geometry(N, H, HKV, D, "attention")) return 0;
     const size_t wide = attention_f32_part_floats(N, H, D) * 4;
