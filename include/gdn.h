@@ -646,8 +646,10 @@ GDN_API int gdn_attention_status(void *stream);
 
 /*
  * gdn_selftest_attention_timeout - the wait of the attention kernels on a
- * barrier that nothing completes: it gives up after limit_us (1 .. 1000000)
- * microseconds, which gdn_attention_status then reports.
+ * barrier that nothing completes: it gives up after about limit_us (1 ..
+ * 1000000) microseconds, which gdn_attention_status then reports.  (The waits
+ * count their tries, of up to 3.8 us each, so that time in which the GPU belongs
+ * to another process does not count.)
  */
 GDN_API int gdn_selftest_attention_timeout(int limit_us, void *stream);
 

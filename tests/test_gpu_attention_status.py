@@ -44,6 +44,18 @@ def test_no_query_takes_a_report_from_another_stream():
     assert not timed_out()
 
 
+@pytest.mark.parametrize("limit_us", [5000, 100000])
+def test_a_wait_lasts_about_as_long_as_its_tries(limit_us):
+    """A wait counts its tries, not the clock.  A try takes up to 3.8 us and is taken for 4."""
+    gdn.gdn_selftest_attention_timeout(10)
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    a.record()
+    gdn.gdn_selftest_attention_timeout(limit_us)
+    b.record()
+    assert timed_out()
+    assert 0.25 * limit_us <= a.elapsed_time(b) * 1e3 <= 2 * limit_us + 50000
+
+
 @pytest.mark.parametrize("limit", [0, -1, 1000001])
 def test_refusals(limit):
     with pytest.raises(gdn.GdnError) as e:

@@ -721,7 +721,7 @@ def gdn_attention_status(device=None) -> None:
 
 def gdn_selftest_attention_timeout(limit_us: int = 1000) -> None:
     """Launch, on the current stream, a wait of the attention kernels that gives up after
-    ``limit_us``; gdn_attention_status then reports it."""
+    about ``limit_us``; gdn_attention_status then reports it."""
     _check(load_library().gdn_selftest_attention_timeout(limit_us, _stream(torch.device("cuda", torch.cuda.current_device()))))
 
 

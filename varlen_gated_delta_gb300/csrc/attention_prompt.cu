@@ -58,7 +58,9 @@ namespace {
 
 using namespace sm100;
 
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
+// A try suspends the warp for up to 3.8 us: some 2 s of the kernel's own time, however long the GPU
+// belongs to others meanwhile.
+constexpr int kWaitTries = 1 << 19;
 constexpr int kMaxBins = 4096;  // bins of the longest-first order
 constexpr float kLazy = 8.f;    // growth of the row maximum (log2) that O waits for
 
@@ -110,25 +112,16 @@ struct PromptParams {
     int splits;     // of the key tiles of an item; more than one: parts for a second kernel
 };
 
-// Warp-wide mbarrier wait that gives up, for the whole warp, after limit_ns or when another role has.
-__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile int *abort,
-                                              uint64_t limit_ns = kWaitLimitNs) {
+// Warp-wide mbarrier wait that gives up, for the whole warp, after so many tries or when another role has.
+__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile int *abort, int tries = kWaitTries) {
     const uint32_t addr = smem_u32(bar);
-    bool ok = mbar_try_wait(addr, parity);
-    if (!ok) {
-        const uint64_t t0 = global_timer_ns();
-        bool stop = false;
-        while (!ok && !stop) {
+    bool ok;
 #pragma unroll 1
-            for (int i = 0; i < 32 && !ok; ++i) ok = mbar_try_wait(addr, parity);
-            if (!ok && *abort) stop = true;
-            if (!ok && !stop && global_timer_ns() - t0 > limit_ns) {
-                *abort = 1;
-                atomicAdd(&g_attention_timeouts, 1u);
-                stop = true;
-            }
+    while (!(ok = mbar_try_wait(addr, parity)) && !*abort)
+        if (--tries < 0) {
+            *abort = 1;
+            atomicAdd(&g_attention_timeouts, 1u);
         }
-    }
     return __all_sync(0xffffffffu, ok);
 }
 
@@ -808,7 +801,7 @@ done:
 }
 
 // A wait that nothing ends: how the way out of one is tested.
-__global__ void wait_probe_kernel(uint64_t limit_ns) {
+__global__ void wait_probe_kernel(int tries) {
     __shared__ __align__(8) uint64_t bar;
     __shared__ int s_abort;
     if (threadIdx.x == 0) {
@@ -817,7 +810,7 @@ __global__ void wait_probe_kernel(uint64_t limit_ns) {
         s_abort = 0;
     }
     __syncwarp();
-    wait_or_abort(&bar, 0, &s_abort, limit_ns);
+    wait_or_abort(&bar, 0, &s_abort, tries);
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
@@ -954,8 +947,8 @@ int attention_timeouts(cudaStream_t s, cudaError_t *e) {
     }
 }
 
-cudaError_t launch_attention_wait_probe(int limit_us, cudaStream_t s) {
-    const cudaError_t e = launch_kernel(wait_probe_kernel, dim3(1), dim3(32), 0, s, false, (uint64_t)limit_us * 1000u);
+cudaError_t launch_attention_wait_probe(int tries, cudaStream_t s) {
+    const cudaError_t e = launch_kernel(wait_probe_kernel, dim3(1), dim3(32), 0, s, false, tries);
     note_launch();
     return e;
 }

@@ -78,6 +78,6 @@ cudaError_t launch_attention_prompt(const Attn &a, int min_rows, cudaStream_t s)
 // Synchronises s; non-zero when a bounded wait gave up since the last call for this stream.
 int attention_timeouts(cudaStream_t s, cudaError_t *e);
 // A kernel whose only wait gives up.
-cudaError_t launch_attention_wait_probe(int limit_us, cudaStream_t s);
+cudaError_t launch_attention_wait_probe(int tries, cudaStream_t s);
 
 }  // namespace gdn
