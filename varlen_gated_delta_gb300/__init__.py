@@ -713,10 +713,11 @@ def gdn_attention_varlen(q, k, v, offsets, *, scale=0.0, out=None):
 
 
 def gdn_attention_status(device=None) -> None:
-    """Synchronise the current stream; raise GdnError (GDN_ERR_TIMEOUT) when a wait inside an
+    """Synchronise the current stream of ``device`` (the current device); raise GdnError (GDN_ERR_TIMEOUT) when a wait inside an
     attention kernel gave up, on any stream of the device, since the last query on this one."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
-    _check(load_library().gdn_attention_status(_stream(dev)))
+    with torch.cuda.device(dev):
+        _check(load_library().gdn_attention_status(_stream(dev)))
 
 
 def gdn_selftest_attention_timeout(limit_us: int = 1000) -> None:
