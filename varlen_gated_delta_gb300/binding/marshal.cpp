@@ -31,6 +31,22 @@ PyObject *g_error = nullptr;  // GdnError, set by init()
 // with one; with 131072 new tokens a call among others 13.1 and 8.6).
 constexpr int kSharedN = 1 << 20;
 
+// Lets other Python threads run while it lives: allocations and launches may wait for the device, and what the
+// device waits for (a host function in a stream) may need the interpreter.
+class Unlocked {
+    PyThreadState *state_ = PyEval_SaveThread();
+
+public:
+    Unlocked() = default;
+    Unlocked(const Unlocked &) = delete;
+    ~Unlocked() { PyEval_RestoreThread(state_); }
+};
+
+at::Tensor allocate(at::IntArrayRef shape, at::ScalarType type, c10::Device dev) {
+    const Unlocked others;
+    return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+}
+
 // A refusal with a gdn_status.
 struct Refusal {
     int status;
@@ -116,7 +132,7 @@ struct Out {
     void *ptr = nullptr;
     Out(PyObject *o, const char *name, at::ScalarType type, at::IntArrayRef shape, c10::Device dev) {
         if (o == Py_None) {
-            at::Tensor t = at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+            at::Tensor t = allocate(shape, type, dev);
             ptr = t.data_ptr();
             object = THPVariable_Wrap(std::move(t));
             if (!object) throw Raised{};
@@ -174,7 +190,14 @@ int activation(at::ScalarType t) {
 
 void *stream(c10::Device dev) { return c10::cuda::getCurrentCUDAStream(dev.index()).stream(); }
 
-void done(int status) {
+// The call, whose refusal becomes an exception.
+template <typename F>
+void launch(F call) {
+    int status;
+    {
+        const Unlocked others;
+        status = call();
+    }
     if (status != GDN_OK) throw Refusal{status, gdn_last_error()};
 }
 
@@ -232,16 +255,17 @@ PyObject *page_plan(PyObject *, PyObject *const *a, Py_ssize_t n) {
         int32_t *bt = (int32_t *)at(a[2], "block_table", i32, {B, M}, dev);
         const int32_t *fp = (int32_t *)at(a[3], "free_pages", i32, {F}, dev), *cu = (int32_t *)at(a[6], "cursor", i32, {1}, dev);
         auto call = [&](Out &offsets, Out &kv, Out &pos, Out &slots, Out &cout, Out &status) {
-            done(gdn_page_plan(nl, cl, bt, fp, cu, (int32_t *)offsets.ptr, (int32_t *)kv.ptr, (int32_t *)pos.ptr,
-                               (int32_t *)slots.ptr, (int32_t *)cout.ptr, (int32_t *)status.ptr, B, N, ps, M, F, stream(dev)));
+            launch([&] {
+                return gdn_page_plan(nl, cl, bt, fp, cu, (int32_t *)offsets.ptr, (int32_t *)kv.ptr, (int32_t *)pos.ptr,
+                                     (int32_t *)slots.ptr, (int32_t *)cout.ptr, (int32_t *)status.ptr, B, N, ps, M, F, stream(dev));
+            });
             return tuple({&offsets, &kv, &pos, &slots, &cout, &status});
         };
         bool fresh = N <= kSharedN;
         for (int i = 7; i < 13; ++i) fresh = fresh && a[i] == Py_None;
         if (fresh) {
             const at::AutoDispatchBelowADInplaceOrView plain;  // (nothing here is differentiated)
-            const at::Tensor all = at::empty({2 * ((int64_t)N + 3) + 2 * ((int64_t)B + 4) + 8},
-                                             at::TensorOptions().dtype(i32).device(dev));
+            const at::Tensor all = allocate({2 * ((int64_t)N + 3) + 2 * ((int64_t)B + 4) + 8}, i32, dev);
             int64_t from = 0;
             Out offsets(all, B + 1, from), kv(all, B, from), pos(all, N, from), slots(all, N, from), cout(all, 1, from),
                 status(all, 1, from);
@@ -289,9 +313,11 @@ PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const bool packed = a[11] != Py_None || !cached;
         std::optional<Out> k;
         if (packed) k.emplace(a[11], "k", T, at::IntArrayRef({N, HKV, D}), dev);
-        done(gdn_qk_norm_rope(base, stride, (const float *)qw, (const float *)kw, eps, (const float *)table, (const int32_t *)pos,
-                              max_pos, (const int32_t *)slots, q.ptr, k ? k->ptr : nullptr, kc, vc, num_slots, N, H, HKV, D, R, style, dtype,
-                              stream(dev)));
+        launch([&] {
+            return gdn_qk_norm_rope(base, stride, (const float *)qw, (const float *)kw, eps, (const float *)table,
+                                    (const int32_t *)pos, max_pos, (const int32_t *)slots, q.ptr, k ? k->ptr : nullptr, kc, vc,
+                                    num_slots, N, H, HKV, D, R, style, dtype, stream(dev));
+        });
         return tuple({&q, k ? &*k : nullptr});
     });
 }
@@ -313,7 +339,10 @@ PyObject *attention_varlen(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const float scale = real(a[4]);
         const c10::cuda::CUDAGuard guard(dev);
         Out out(a[5], "out", T, {N, H, D}, dev);
-        done(gdn_attention_varlen(qp, kp, vp, (const int32_t *)offsets, out.ptr, B, N, H, HKV, D, qs, ks, vs, scale, dtype, stream(dev)));
+        launch([&] {
+            return gdn_attention_varlen(qp, kp, vp, (const int32_t *)offsets, out.ptr, B, N, H, HKV, D, qs, ks, vs, scale, dtype,
+                                        stream(dev));
+        });
         return out.give();
     });
 }
@@ -339,14 +368,16 @@ PyObject *attention_paged(PyObject *, PyObject *const *a, Py_ssize_t n) {
         at::Tensor ws;
         if (a[9] == Py_None) {
             const size_t need = gdn_attention_paged_workspace_bytes(B, N, H, HKV, D, max_q);
-            ws = at::empty({(int64_t)(need > 256 ? need : 256)}, at::TensorOptions().dtype(at::kByte).device(dev));
+            ws = allocate({(int64_t)(need > 256 ? need : 256)}, at::kByte, dev);
         } else {
             ws = tensor(a[9], "workspace");
             check(ws, "workspace", at::kByte, ws.sizes(), dev);
             if (!ws.is_contiguous()) throw Refusal{GDN_ERR_SHAPE, "workspace must be contiguous"};
         }
-        done(gdn_attention_paged(qp, kc, vc, bt, kv, of, out.ptr, B, N, H, HKV, D, ps, M, pages, max_q, qs, scale, dtype, ws.data_ptr(),
-                                 (size_t)ws.numel(), stream(dev)));
+        launch([&] {
+            return gdn_attention_paged(qp, kc, vc, bt, kv, of, out.ptr, B, N, H, HKV, D, ps, M, pages, max_q, qs, scale, dtype,
+                                       ws.data_ptr(), (size_t)ws.numel(), stream(dev));
+        });
         return out.give();
     });
 }
