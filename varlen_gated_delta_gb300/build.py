@@ -14,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
@@ -77,6 +78,8 @@ def _build_marshal(force: bool) -> None:
     deps = [MARSHAL_SRC, os.path.join(ROOT, "include", "gdn.h")]
     if not force and os.path.exists(out) and all(os.path.getmtime(d) <= os.path.getmtime(out) for d in deps):
         return
+    if os.path.exists(out):
+        os.remove(out)  # (of another source or library: rather none)
     import sysconfig
 
     import torch
@@ -97,9 +100,15 @@ def _build_marshal(force: bool) -> None:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    """Build what is out of date; returns the library's path.  Where the compiled part of the binding
+    cannot be built (it needs g++ and the headers of Python and torch), the library still is: a
+    warning tells why, and only the calls that go through that part raise."""
     if force or _stale():
         _build_lib(verbose)
-    _build_marshal(force)
+    try:
+        _build_marshal(force)
+    except (RuntimeError, OSError, ImportError) as e:
+        warnings.warn(f"the attention-layer calls have no binding: {e}", RuntimeWarning, stacklevel=2)
     return LIB
 
 
