@@ -44,6 +44,7 @@
 // U[1, 4096] tokens, 16 heads of 64: 202 us, 742 TFLOP/s, bound by the softmax
 // warpgroups, whose work a score is the same for half the products.  32 x U[1, 512],
 // 32 heads on 8: 54 us, bound by the chain of one or two key tiles an item.
+#include <algorithm>
 #include <cmath>
 #include <exception>
 #include <map>
@@ -910,9 +911,12 @@ cudaError_t launch(const Attn &a, int min_rows, int splits, cudaStream_t s) {
 
 // Splits of the key tiles when items are few: one request's slice of a prompt over a long history
 // would keep a handful of CTAs busy (64 tokens on 32768, 32 heads of 128 on 8: 390 us, split 80).
-int prompt_splits(int B, int N, int H, int HKV, int D, int max_q) {
-    const int packed = packed_heads(H / HKV, max_q), pair = paired_heads(H / HKV, D, packed);
-    const long tm = pair ? 128 : (D > 128 ? 128 : 256) >> packed, items = ((long)N / tm + B) * (H >> (packed + pair));
+// Sequences of at most min_rows (query, head of a group) rows have no items, and N tokens hold only so
+// many longer ones.
+int prompt_splits(int B, int N, int H, int HKV, int D, int max_q, int min_rows) {
+    const int G = H / HKV, packed = packed_heads(G, max_q), pair = paired_heads(G, D, packed);
+    const long seqs = std::min<long>(B, N / (min_rows / G + 1));
+    const long tm = pair ? 128 : (D > 128 ? 128 : 256) >> packed, items = ((long)N / tm + seqs) * (H >> (packed + pair));
     int splits = 1;
     while (splits < 32 && items * splits * 2 <= 2 * 152) splits *= 2;
     return splits;
@@ -921,7 +925,7 @@ int prompt_splits(int B, int N, int H, int HKV, int D, int max_q) {
 }  // namespace
 
 size_t attention_prompt_part_floats(int B, int N, int H, int HKV, int D, int max_q) {
-    const int splits = prompt_splits(B, N, H, HKV, D, max_q);
+    const int splits = prompt_splits(B, N, H, HKV, D, max_q, kSplitRows);  // (fewer without that kernel)
     return splits == 1 ? 0 : (size_t)N * H * splits * (D + 2);
 }
 
@@ -960,7 +964,7 @@ bool attention_prompt_supported(const Attn &a, int dtype) {
 }
 
 cudaError_t launch_attention_prompt(const Attn &a, int min_rows, cudaStream_t s) {
-    const int splits = a.part == nullptr ? 1 : prompt_splits(a.B, a.N, a.H, a.HKV, a.D, a.max_q);
+    const int splits = a.part == nullptr ? 1 : prompt_splits(a.B, a.N, a.H, a.HKV, a.D, a.max_q, min_rows);
     if (a.D <= 64) return launch<64>(a, min_rows, splits, s);
     if (a.D <= 128) return launch<128>(a, min_rows, splits, s);
     return launch<256>(a, min_rows, splits, s);
