@@ -685,7 +685,9 @@ def gdn_page_plan(new_lens, cached_lens, block_table, free_pages, *, page_size, 
     in place.  ``N`` is the capacity of ``positions`` and ``slots`` (slots past the last
     new token are -1).  ``kv_lens`` may be ``cached_lens`` and ``cursor_out`` may be
     ``cursor``.  Returns (offsets [B+1], kv_lens [B], positions [N], slots [N],
-    cursor_out [1], status [1]), all int32; when status[0] != 0 nothing was handed out."""
+    cursor_out [1], status [1]), all int32; when status[0] != 0 nothing was handed out.
+    Where all six are new (and N <= 2^20), they share one allocation, which any one of them
+    keeps alive: pass a tensor of your own for one that outlives the step."""
     return (_marshal_module or _marshal()).page_plan(
         new_lens, cached_lens, block_table, free_pages, page_size, N, cursor, offsets, kv_lens, positions,
         slots, cursor_out, status)

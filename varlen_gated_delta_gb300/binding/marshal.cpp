@@ -4,8 +4,8 @@
 // binding it only checks device, type, shape and strides of torch tensors,
 // allocates outputs that were not given, and passes pointers and the current
 // stream to libgdn.so.  On the GB300's host a gdn_page_plan call takes 6.4 us this
-// way (20.5 through ctypes), gdn_qk_norm_rope 4.8 (16), gdn_attention_paged 7.3
-// (22), gdn_attention_varlen 4.1 (17).
+// way (20.5 through ctypes), gdn_qk_norm_rope 4.1 (16), gdn_attention_paged 7.1
+// (22), gdn_attention_varlen 4.3 (17).
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -28,7 +28,7 @@ PyObject *g_error = nullptr;  // GdnError, set by init()
 
 // Up to so many new tokens (8 MB) the six outputs of a plan share one allocation, which any one of them
 // keeps alive: six allocations take longer than the rest of the call (64 requests: 9.7 us with six, 6.4
-// with one; with 131072 new tokens a call among others 13.1 and 8.6).
+// with one; with 107781 new tokens a call among others 13.1 and 8.8).
 constexpr int kSharedN = 1 << 20;
 
 // Lets other Python threads run while it lives: allocations and launches may wait for the device, and what the

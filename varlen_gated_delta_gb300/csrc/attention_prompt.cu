@@ -27,8 +27,8 @@
 // non-finite value among them, and where there is one the CTA takes its items a
 // second time.  In that pass the warp also clears such values of the diagonal
 // tiles, and the epilogue adds them to the rows that do see them.  8 x 4096 tokens, 32
-// heads of 128 on 8, take 1918 us instead of 709 with one NaN near the end; 65536 tokens,
-// 16 heads of 256 on 2, 60.6 ms instead of 29.8.
+// heads of 128 on 8, take 1910 us instead of 719 with one NaN near the end; 65536 tokens,
+// 16 heads of 256 on 2, 61.0 ms instead of 30.1.
 //
 // A slice of a prompt over a long history has few items: its key tiles are then
 // split, and each split leaves m, l and an unscaled o for a second kernel.
@@ -38,12 +38,14 @@
 // fro over the CTAs; heads are innermost, so that the heads of a group read the
 // same keys out of L2.
 //
-// 8 x 4096 tokens, 32 heads of 128 on 8: 720 us, 1527 TFLOP/s of causal work, 0.78
-// of the measured bf16 rate (the tensor pipe is active 0.69 of the cycles; what is
-// left is the softmax between the products and each item's start and end).  16 x
-// U[1, 4096] tokens, 16 heads of 64: 202 us, 742 TFLOP/s, bound by the softmax
-// warpgroups, whose work a score is the same for half the products.  32 x U[1, 512],
-// 32 heads on 8: 54 us, bound by the chain of one or two key tiles an item.
+// 8 x 4096 tokens, 32 heads of 128 on 8: 806 us a call under sustained load, 1365 TFLOP/s
+// of causal work, 0.70 of the measured bf16 burst rate and 0.78 of the sustained one (720
+// us in a burst; the tensor pipe is active 0.69 of the cycles; what is left is the softmax
+// between the products and each item's start and end).  16 x U[1, 4096] tokens, 16 heads
+// of 64: 199 us, 754 TFLOP/s, bound by the softmax warpgroups, whose work a score is the
+// same for half the products; no pipe of theirs is full (special functions 35%, issue
+// slots 44%), they wait for tensor memory and for each other.  32 x U[1, 512], 32 heads on
+// 8: 54 us, bound by the chain of one or two key tiles an item.
 #include <algorithm>
 #include <cmath>
 #include <exception>

@@ -11,8 +11,8 @@
 // tokens and pages.  Where an output lies over an input (the lengths or the cursor
 // carried in place), the CTAs form one thread-block cluster, whose barrier between
 // the last read and the first write keeps them apart.  One CTA for small steps (64
-// requests of one token: 4.6 us); 131072 tokens of 32 requests: 11.8 us carried in
-// place, 6.2 us otherwise.
+// requests of one token: 4.6 us); 107781 tokens of 32 requests: 11.8 us carried in
+// place, 6.6 us otherwise.
 #include <cooperative_groups.h>
 
 #include <algorithm>
