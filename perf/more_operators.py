@@ -411,7 +411,7 @@ def _plain_fork(s):
     src = table[i, last]
     table[i, last] = dst
     copies = torch.full((B, 2), -1, dtype=torch.int32, device="cuda")
-    copies[i] = torch.stack([src, dst], 1)
+    copies[:i.numel()] = torch.stack([src, dst], 1)
     _move(s["caches"], src.long(), dst.long())
     return dict(table=table, kv_lens=kv, copies=copies, cursor=start + i.numel(), status=torch.zeros_like(start), free=free,
                 caches=s["caches"])
@@ -576,8 +576,8 @@ def _exact_fork(s):
     at -= len(back)
     free[at:at + len(back)] = back
     copies = np.full((len(parents), 2), -1)
-    for i in copied:
-        copies[i] = new[i][-1], free[at]
+    for j, i in enumerate(copied):
+        copies[j] = new[i][-1], free[at]
         new[i][-1] = free[at]
         at += 1
     table = np.full(old.shape, -1)
