@@ -657,6 +657,181 @@ GDN_API int gdn_selftest_attention_timeout(int limit_us, void *stream);
 GDN_API size_t gdn_attention_paged_workspace_bytes(int B, int N, int H, int HKV, int D,
                                                    int max_q);
 
+/*
+ * 4-bit caches
+ * ------------
+ * A paged cache may hold keys and values in 4 bits, with the pages, slots and
+ * block tables of the other calls.  16 neighbouring channels of a head share a
+ * scale s (8 bits, e4m3); each value is u c, with u = s ts, ts the scale of its
+ * key-value head (k_scale, v_scale [HKV] f32, positive; NULL: 1) and c one of
+ * 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives (codes 0..7, 8..15; e2m1).
+ * k_cache and v_cache are [num_pages, HKV, page_size * D * 9/16] bytes, 16-byte
+ * aligned: for each page and head first the codes of its tokens,
+ * [page_size, D/2], the even channel in the low half of a byte, then the
+ * scales, [page_size, D/16].  A scale byte of 0x7f counts as 480 and 0xff too,
+ * so no byte is a NaN.  D is a multiple of 16 up to 256, page_size a multiple
+ * of 16 (GDN_ERR_UNSUPPORTED otherwise).
+ */
+
+/*
+ * gdn_kv4_write - keys and values of N tokens into the slots of a 4-bit cache.
+ *   k, v         N rows of HKV heads of D T, k_stride and v_stride elements
+ *                apart (>= HKV D; so both may be columns of a projection)
+ *   slots        [N] int32; a slot outside [0, num_pages * page_size) writes
+ *                nothing to the cache.  No two tokens have the same slot.
+ *   k_out, v_out [N, HKV, D] T, or both NULL: the values held, u c
+ * Per group x: s = e4m3(min(448, max |x| / (6 ts))), u = s ts, c the nearest
+ * code of x (1 / u), halfway to the even one, at most 6; each operation rounded
+ * to fp32 (s and c to nearest even).  s = 0 holds zeros.  Infinite values
+ * become 6 u.  NaN does not count in max |x| and becomes 6 u.
+ */
+GDN_API int gdn_kv4_write(const void *k, const void *v, int64_t k_stride, int64_t v_stride,
+                          const int32_t *slots, const float *k_scale, const float *v_scale,
+                          void *k_cache, void *v_cache, void *k_out, void *v_out, int N, int HKV,
+                          int D, int page_size, int num_pages, int dtype, void *stream);
+
+/*
+ * gdn_attention_paged_kv4 - gdn_attention_paged over a 4-bit cache; the same
+ * rows, masks, offsets, max_q and workspace rules.  out is 16-byte aligned.
+ * The cache's values are used as they are (exact in the products); fp32
+ * queries and probabilities as sums of two fp16 values, bf16 queries exactly,
+ * their probabilities rounded to 11 bits; scores, sums and outputs in fp32.
+ */
+GDN_API int gdn_attention_paged_kv4(const void *q, const void *k_cache, const void *v_cache,
+                                    const float *k_scale, const float *v_scale,
+                                    const int32_t *block_table, const int32_t *kv_lens,
+                                    const int32_t *offsets, void *out, int B, int N, int H, int HKV,
+                                    int D, int page_size, int max_pages, int num_pages, int max_q,
+                                    int64_t q_stride, float scale, int dtype, void *workspace,
+                                    size_t ws_bytes, void *stream);
+
+/* Workspace bytes of gdn_attention_paged_kv4 (0 on bad input). */
+GDN_API size_t gdn_attention_paged_kv4_workspace_bytes(int B, int N, int H, int HKV, int D,
+                                                       int max_q);
+
+/*
+ * Beams
+ * -----
+ * G groups (requests) of K beams; beam k of group g is row g K + k of the
+ * logits, the states and the block table.  A step of a search: gdn_beam_select
+ * picks the continuations, gdn_state_reorder takes the recurrent and conv states
+ * along, gdn_page_fork the block tables, and gdn_page_copy copies the pages that
+ * two beams would both write.
+ */
+
+/*
+ * gdn_beam_select - of each group's K V continuations the n with the largest
+ *   scores[g, k] + x[g K + k, t] - log sum_t' exp x[g K + k, t'],
+ * descending, ties to the lowest k V + t.
+ *   logits       G K rows of V values T, row_stride elements apart (>= V)
+ *   scores       [G, K] f32: log probabilities so far
+ *   finished     [G, K] bytes or NULL: a beam whose flag is not 0 has one
+ *                continuation, end_token, with its score unchanged; its logits
+ *                are not read
+ *   keep_rows    0, or 1 with n == K: instead of descending, a beam's best
+ *                continuation takes the beam's own place, the others take the
+ *                places that are left in order (so that gdn_state_reorder and
+ *                gdn_page_fork move least)
+ *   tokens       [G, n] int32
+ *   parents      [G, n] int32: the row g K + k that each one continues
+ *   scores_out   [G, n] f32; may equal scores when n == K
+ *   finished_out [G, n] bytes or NULL: 1 where the beam was finished or the
+ *                token is end_token; may equal finished when n == K
+ *   workspace    device, 256-byte aligned, gdn_beam_select_workspace_bytes()
+ *                bytes, not shared with a concurrently running call
+ * Scores are compared in 64 bits; the sum of a row is of fp32 terms.  NaN
+ * logits and scores count as -inf.  A row whose largest logit is infinite has
+ * -inf throughout.  Continuations at -inf come last, the lowest k V + t first.
+ * Requires K <= 128, n <= 128, n <= K V; end_token in [0, V) when flags are
+ * given or asked for.
+ */
+GDN_API int gdn_beam_select(const void *logits, int64_t row_stride, const float *scores,
+                            const uint8_t *finished, int end_token, int keep_rows, int32_t *tokens,
+                            int32_t *parents, float *scores_out, uint8_t *finished_out, int G, int K,
+                            int V, int n, int dtype, void *workspace, size_t ws_bytes, void *stream);
+GDN_API size_t gdn_beam_select_workspace_bytes(int G, int K, int V, int n);
+
+/*
+ * gdn_state_reorder - row i of each state <- its row parents[i], in place.
+ *   states     `count` device pointers (a host array), each to B rows
+ *   row_bytes  their rows' bytes (a host array)
+ *   parents    [B] int32 on the device; a row whose parent lies outside [0, B)
+ *              keeps its content
+ * Requires count <= 64 and B <= 4096; the states do not overlap.
+ */
+GDN_API int gdn_state_reorder(void *const *states, const int64_t *row_bytes, int count,
+                              const int32_t *parents, int B, void *stream);
+
+/*
+ * gdn_page_fork - block tables that follow the chosen beams: row i of the new
+ * table continues row parents[i] of the old one.  Pages are shared between
+ * rows that have them in common; but a last page that is not full stays with its
+ * first child alone, and every other child gets a page of its own for it, to
+ * be filled by gdn_page_copy.  Pages of no new row go back to the free list.
+ * So full pages may have many owners and are not written again, a page that is
+ * not full has one, and gdn_page_plan goes on from there.
+ *   parents      [B_out] int32; a negative parent gives an empty row (so a
+ *                request is freed by giving its row no child)
+ *   kv_lens      [B] int32: tokens of the old rows
+ *   block_table  [B, max_pages] int32: all rows that hold pages of the pool
+ *   free_pages   [n_free] int32, cursor [1] int32, as in gdn_page_plan: pages
+ *                that go back are put before the cursor, in ascending order;
+ *                then the new ones are taken from there on
+ *   table_out    [B_out, max_pages] int32; may equal block_table (B_out == B);
+ *                -1 past a row's pages
+ *   kv_lens_out  [B_out] int32; may equal kv_lens (B_out == B)
+ *   copies       [B_out, 2] int32: (from, to) pages of gdn_page_copy, -1 past
+ *                the last pair
+ *   cursor_out   [1] int32; may equal cursor
+ *   status       [1] int32: GDN_OK, GDN_ERR_SHAPE (a length, parent, cursor or
+ *                page out of range, or more pages go back than were handed
+ *                out) or GDN_ERR_CAPACITY (free pages are too few)
+ *   workspace    device, 256-byte aligned, gdn_page_fork_workspace_bytes()
+ * When status is not GDN_OK nothing is given back or taken: the cursor keeps its
+ * value, copies are -1, and table_out and kv_lens_out are unchanged where they are
+ * the inputs, else -1 and 0.  Requires B, B_out <= 8192, 1 <= page_size <=
+ * 65536.
+ */
+GDN_API int gdn_page_fork(const int32_t *parents, const int32_t *kv_lens,
+                          const int32_t *block_table, int32_t *free_pages, const int32_t *cursor,
+                          int32_t *table_out, int32_t *kv_lens_out, int32_t *copies,
+                          int32_t *cursor_out, int32_t *status, int B, int B_out, int page_size,
+                          int max_pages, int num_pages, int n_free, void *workspace, size_t ws_bytes,
+                          void *stream);
+GDN_API size_t gdn_page_fork_workspace_bytes(int B, int max_pages, int num_pages);
+
+/*
+ * gdn_page_compact - moves the live pages of a pool to its front.  With L pages
+ * in the rows of the block table (all rows that hold pages of the pool), those
+ * with numbers from L on move, in ascending order, into the gaps before L, in
+ * ascending order.
+ *   table_out   [B, max_pages] int32; may equal block_table; -1 past a row's pages
+ *   copies      [num_pages / 2, 2] int32: pairs of gdn_page_copy, -1 past the last
+ *   free_pages  [num_pages] int32: 0, 1, 2, ...
+ *   cursor_out  [1] int32: L
+ *   status      [1] int32: GDN_OK, or GDN_ERR_SHAPE (a length or page out of
+ *               range: copies are -1, free_pages and cursor_out are not written,
+ *               table_out is unchanged where it is the input, else -1)
+ *   workspace   device, 256-byte aligned, gdn_page_compact_workspace_bytes()
+ */
+GDN_API int gdn_page_compact(const int32_t *kv_lens, const int32_t *block_table, int32_t *table_out,
+                             int32_t *copies, int32_t *free_pages, int32_t *cursor_out,
+                             int32_t *status, int B, int page_size, int max_pages, int num_pages,
+                             void *workspace, size_t ws_bytes, void *stream);
+GDN_API size_t gdn_page_compact_workspace_bytes(int num_pages);
+
+/*
+ * gdn_page_copy - copies whole pages within each of several caches.
+ *   caches      `count` device pointers (a host array), [num_pages] pages each
+ *   page_bytes  bytes of a page of each (a host array)
+ *   copies      [n, 2] int32 on the device: (from, to); pairs outside the pool
+ *               (-1) are skipped.  No page is written that another pair reads or
+ *               writes.
+ * Requires count <= 128, page_bytes <= 2^32.
+ */
+GDN_API int gdn_page_copy(void *const *caches, const int64_t *page_bytes, int count,
+                          const int32_t *copies, int n, int num_pages, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -37,6 +37,9 @@ __all__ = [
     "gdn_dense_workspace_bytes_ex", "gdn_page_plan", "gdn_qk_norm_rope", "gdn_attention_varlen",
     "gdn_attention_paged", "gdn_attention_paged_workspace_bytes", "gdn_attention_status",
     "gdn_selftest_attention_timeout", "GDN_ROPE_HALF", "GDN_ROPE_PAIRS",
+    "gdn_kv4_write", "gdn_attention_paged_kv4", "gdn_attention_paged_kv4_workspace_bytes", "gdn_beam_select",
+    "gdn_beam_select_workspace_bytes", "gdn_state_reorder", "gdn_page_fork", "gdn_page_fork_workspace_bytes",
+    "gdn_page_compact", "gdn_page_compact_workspace_bytes", "gdn_page_copy", "kv4_page_bytes",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -128,11 +131,23 @@ def load_library():
     lib.gdn_selftest_attention_timeout.restype = i
     lib.gdn_attention_paged_workspace_bytes.argtypes = [i] * 6
     lib.gdn_attention_paged_workspace_bytes.restype = sz
+    lib.gdn_kv4_write.argtypes = [vp, vp, i64, i64] + [vp] * 7 + [i] * 6 + [vp]
+    lib.gdn_attention_paged_kv4.argtypes = [vp] * 9 + [i] * 9 + [i64, f, i, vp, sz, vp]
+    lib.gdn_beam_select.argtypes = [vp, i64, vp, vp, i, i] + [vp] * 4 + [i] * 5 + [vp, sz, vp]
+    lib.gdn_state_reorder.argtypes = [vp, vp, i, vp, i, vp]
+    lib.gdn_page_fork.argtypes = [vp] * 10 + [i] * 6 + [vp, sz, vp]
+    lib.gdn_page_compact.argtypes = [vp] * 7 + [i] * 4 + [vp, sz, vp]
+    lib.gdn_page_copy.argtypes = [vp, vp, i, vp, i, i, vp]
+    for name, many in (("gdn_attention_paged_kv4", 6), ("gdn_beam_select", 4), ("gdn_page_fork", 3), ("gdn_page_compact", 1)):
+        query = getattr(lib, name + "_workspace_bytes")
+        query.argtypes, query.restype = [i] * many, sz
     for name in ("gdn_conv1d_varlen", "gdn_prepare", "gdn_delta_varlen", "gdn_layer_varlen",
                  "gdn_workspace_status", "gdn_set_chunk_min_len", "gdn_conv1d_varlen_capture",
                  "gdn_delta_varlen_capture", "gdn_layer_varlen_capture", "gdn_prepare_ex",
                  "gdn_delta_varlen_ex", "gdn_layer_varlen_ex", "gdn_gated_delta_dense",
-                 "gdn_page_plan", "gdn_qk_norm_rope", "gdn_attention_varlen", "gdn_attention_paged"):
+                 "gdn_page_plan", "gdn_qk_norm_rope", "gdn_attention_varlen", "gdn_attention_paged",
+                 "gdn_kv4_write", "gdn_attention_paged_kv4", "gdn_beam_select", "gdn_state_reorder",
+                 "gdn_page_fork", "gdn_page_compact", "gdn_page_copy"):
         getattr(lib, name).restype = i
     _lib = lib
     return lib
@@ -744,3 +759,112 @@ def gdn_attention_paged(q, k_cache, v_cache, block_table, kv_lens, offsets, *, m
     bytes.  Returns out [N, H, D]; rows from offsets[B] on are not written."""
     return (_marshal_module or _marshal()).attention_paged(
         q, k_cache, v_cache, block_table, kv_lens, offsets, max_q, scale, out, workspace)
+
+
+# ------------------------------------------------------------------ 4-bit caches
+
+def kv4_page_bytes(page_size: int, D: int) -> int:
+    """Bytes of a page and head of a 4-bit cache: uint8 tensors [num_pages, HKV, kv4_page_bytes(page_size, D)]."""
+    return page_size * D * 9 // 16
+
+
+def gdn_kv4_write(k, v, slots, k_cache, v_cache, *, k_scale=None, v_scale=None, values=False,
+                  k_out=None, v_out=None):
+    """Keys and values [N, HKV, D] (any token stride) into the ``slots`` [N] int32 of a 4-bit cache.
+
+    ``k_cache``, ``v_cache`` [num_pages, HKV, kv4_page_bytes(page_size, D)] uint8; D and the
+    page size are multiples of 16.  16 channels share an 8-bit scale on top of ``k_scale`` /
+    ``v_scale`` [HKV] f32 (None: 1).  A slot outside the cache writes nothing.  With ``values``
+    (or tensors k_out, v_out) returns what the cache now stands for, (k, v) [N, HKV, D], else
+    (None, None)."""
+    return (_marshal_module or _marshal()).kv4_write(k, v, slots, k_cache, v_cache, k_scale, v_scale, values,
+                                                     k_out, v_out)
+
+
+def gdn_attention_paged_kv4_workspace_bytes(B, N, H, HKV, D, max_q) -> int:
+    """Workspace bytes of gdn_attention_paged_kv4 for these sizes."""
+    return int(load_library().gdn_attention_paged_kv4_workspace_bytes(B, N, H, HKV, D, max_q))
+
+
+def gdn_attention_paged_kv4(q, k_cache, v_cache, block_table, kv_lens, offsets, *, max_q, k_scale=None,
+                            v_scale=None, scale=0.0, out=None, workspace=None):
+    """gdn_attention_paged over a 4-bit cache (see gdn_kv4_write); the same rows and masks.
+
+    ``workspace`` is an optional uint8 tensor of gdn_attention_paged_kv4_workspace_bytes bytes.
+    Returns out [N, H, D]; rows from offsets[B] on are not written."""
+    return (_marshal_module or _marshal()).attention_paged_kv4(
+        q, k_cache, v_cache, block_table, kv_lens, offsets, max_q, k_scale, v_scale, scale, out, workspace)
+
+
+# ------------------------------------------------------------------ beams
+
+def gdn_beam_select_workspace_bytes(G, K, V, n) -> int:
+    """Workspace bytes of gdn_beam_select for these sizes."""
+    return int(load_library().gdn_beam_select_workspace_bytes(G, K, V, n))
+
+
+def gdn_beam_select(logits, scores, *, n=None, finished=None, end_token=-1, keep_rows=False, tokens=None,
+                    parents=None, scores_out=None, finished_out=None, workspace=None):
+    """The ``n`` (default: K) best continuations of each group of K beams.
+
+    ``logits`` [G * K, V] (any row stride), ``scores`` [G, K] f32 log probabilities so far.
+    A beam whose ``finished`` [G, K] flag (bool or uint8) is set goes on as it is, with
+    ``end_token``.  Ordered by score, ties to the lowest beam and token; with ``keep_rows``
+    (n == K) a beam's best continuation takes the beam's own place instead, the others take
+    the places that are left.  ``scores_out`` may be ``scores`` and ``finished_out``
+    ``finished``.  Returns (tokens, parents, scores, finished) [G, n]; parents are rows
+    g * K + k; finished is None unless flags were given or asked for."""
+    return (_marshal_module or _marshal()).beam_select(logits, scores, n, finished, end_token, keep_rows, tokens,
+                                                       parents, scores_out, finished_out, workspace)
+
+
+def gdn_state_reorder(states, parents) -> None:
+    """Row i of each of ``states`` (contiguous tensors of B rows, any types) <- its row ``parents[i]``, in place.
+
+    A row whose parent [B] int32 lies outside [0, B) keeps its content.  Up to 64 tensors
+    and 4096 rows in one launch."""
+    (_marshal_module or _marshal()).state_reorder(states, parents)
+
+
+def gdn_page_fork_workspace_bytes(B, max_pages, num_pages) -> int:
+    """Workspace bytes of gdn_page_fork for these sizes."""
+    return int(load_library().gdn_page_fork_workspace_bytes(B, max_pages, num_pages))
+
+
+def gdn_page_fork(parents, kv_lens, block_table, free_pages, *, page_size, num_pages, cursor, table_out=None,
+                  kv_lens_out=None, copies=None, cursor_out=None, status=None, workspace=None):
+    """Block tables that follow the chosen beams: new row i continues old row ``parents[i]``.
+
+    Full pages are shared; a last page that is not full stays with its first child, the others
+    get pages of their own for it (pass ``copies`` to gdn_page_copy).  A negative parent gives
+    an empty row.  Pages of no new row go back before ``cursor`` in ``free_pages`` (in place).
+    ``table_out`` may be ``block_table``, ``kv_lens_out`` ``kv_lens`` and ``cursor_out``
+    ``cursor``.  Returns (table, kv_lens, copies [B_out, 2], cursor, status); when
+    status[0] != 0 nothing was given back or taken."""
+    return (_marshal_module or _marshal()).page_fork(
+        parents, kv_lens, block_table, free_pages, page_size, num_pages, cursor, table_out, kv_lens_out, copies,
+        cursor_out, status, workspace)
+
+
+def gdn_page_compact_workspace_bytes(num_pages) -> int:
+    """Workspace bytes of gdn_page_compact for a pool of this size."""
+    return int(load_library().gdn_page_compact_workspace_bytes(num_pages))
+
+
+def gdn_page_compact(kv_lens, block_table, *, page_size, num_pages, table_out=None, copies=None, free_pages=None,
+                     cursor_out=None, status=None, workspace=None):
+    """Moves the live pages of a pool, those of the rows of ``block_table``, to its front.
+
+    ``table_out`` may be ``block_table``.  Returns (table, copies [num_pages // 2, 2] for
+    gdn_page_copy, free_pages [num_pages], cursor, status); when status[0] != 0 free_pages
+    and cursor were not written."""
+    return (_marshal_module or _marshal()).page_compact(kv_lens, block_table, page_size, num_pages, table_out, copies,
+                                                        free_pages, cursor_out, status, workspace)
+
+
+def gdn_page_copy(caches, copies) -> None:
+    """Copies pages within each of ``caches`` (contiguous tensors [num_pages, ...], any types), in place.
+
+    ``copies`` [n, 2] int32 holds (from, to); pairs outside the pool (-1) are skipped.  Up to
+    128 caches in one launch."""
+    (_marshal_module or _marshal()).page_copy(caches, copies)

@@ -19,6 +19,7 @@
 #include <exception>
 #include <optional>
 #include <string>
+#include <vector>
 
 #include "gdn.h"
 
@@ -382,6 +383,240 @@ PyObject *attention_paged(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// The heads, pages and tokens to a page of a 4-bit cache [num_pages, HKV, page_size * D * 9/16] bytes.
+struct Kv4Cache {
+    int pages, HKV, page_size;
+    void *k, *v;
+    const float *k_scale, *v_scale;
+    Kv4Cache(PyObject *kc, PyObject *vc, PyObject *ks, PyObject *vs, int D, c10::Device dev) {
+        const at::Tensor &c = tensor_of(kc, "k_cache", 3);
+        pages = extent(c.size(0), "num_pages"), HKV = extent(c.size(1), "HKV");
+        if (D < 16 || D % 16 != 0 || D > 256)
+            throw Refusal{GDN_ERR_UNSUPPORTED, "head width D=" + std::to_string(D) + " is not a multiple of 16 up to 256"};
+        const int64_t token = D / 16 * 9, bytes = c.size(2);
+        if (bytes < 1 || bytes % token != 0)
+            throw Refusal{GDN_ERR_SHAPE, "k_cache has " + std::to_string(bytes) + " bytes a page and head, not a multiple of " +
+                                             std::to_string(token) + " (D * 9/16)"};
+        page_size = extent(bytes / token, "page_size");
+        k = at(kc, "k_cache", at::kByte, {pages, HKV, bytes}, dev), v = at(vc, "v_cache", at::kByte, {pages, HKV, bytes}, dev);
+        k_scale = (const float *)at(ks, "k_scale", at::kFloat, {HKV}, dev, true);
+        v_scale = (const float *)at(vs, "v_scale", at::kFloat, {HKV}, dev, true);
+    }
+};
+
+// A workspace that was given, or a new one of `need` bytes.
+at::Tensor workspace(PyObject *o, size_t need, c10::Device dev) {
+    if (o == Py_None) return allocate({(int64_t)(need > 256 ? need : 256)}, at::kByte, dev);
+    const at::Tensor &ws = tensor(o, "workspace");
+    check(ws, "workspace", at::kByte, ws.sizes(), dev);
+    if (!ws.is_contiguous()) throw Refusal{GDN_ERR_SHAPE, "workspace must be contiguous"};
+    return ws;
+}
+
+// Bytes or truth values: pointer of a contiguous tensor of either type.
+void *flags_at(PyObject *o, const char *name, at::IntArrayRef shape, c10::Device dev) {
+    const bool truth = THPVariable_Check(o) && THPVariable_Unpack(o).scalar_type() == at::kBool;
+    return at(o, name, truth ? at::kBool : at::kByte, shape, dev);
+}
+
+// Device pointers of a sequence of contiguous CUDA tensors on one device, whose first dimension is `rows` (-1: that of the
+// first tensor), and the bytes of a row of each.
+struct Tensors {
+    std::vector<void *> ptr;
+    std::vector<int64_t> row_bytes;
+    std::optional<c10::Device> dev;
+    int64_t rows = -1;
+    Tensors(PyObject *o, const char *name) {
+        PyObject *seq = PySequence_Fast(o, "a sequence of tensors is expected");
+        if (!seq) throw Raised{};
+        try {
+            for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(seq); ++i) {
+                const std::string at = std::string(name) + "[" + std::to_string(i) + "]";
+                const at::Tensor &t = tensor(PySequence_Fast_GET_ITEM(seq, i), at.c_str());
+                if (!dev) dev = cuda_device(t, at.c_str());
+                if (t.device() != *dev) throw Refusal{GDN_ERR_CUDA, at + " is on " + t.device().str() + ", expected " + dev->str()};
+                if (t.dim() < 1) throw Refusal{GDN_ERR_SHAPE, at + " has no dimensions"};
+                if (rows < 0) rows = t.size(0);
+                if (t.size(0) != rows)
+                    throw Refusal{GDN_ERR_SHAPE, at + " has " + std::to_string(t.size(0)) + " rows, expected " + std::to_string(rows)};
+                if (!t.is_contiguous()) throw Refusal{GDN_ERR_SHAPE, at + " must be contiguous"};
+                ptr.push_back(t.data_ptr());
+                row_bytes.push_back(rows > 0 ? (int64_t)t.nbytes() / rows : 0);
+            }
+        } catch (...) {
+            Py_DECREF(seq);
+            throw;
+        }
+        Py_DECREF(seq);
+    }
+};
+
+// (k, v, slots, k_cache, v_cache, k_scale, v_scale, values, k_out, v_out)
+PyObject *kv4_write(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 10, [&] {
+        const at::Tensor &k = tensor_of(a[0], "k", 3), &v = tensor_of(a[1], "v", 3);
+        const c10::Device dev = cuda_device(k, "k");
+        const at::ScalarType T = k.scalar_type();
+        const int N = extent(k.size(0), "N"), HKV = extent(k.size(1), "HKV"), D = extent(k.size(2), "D");
+        int64_t ks, vs;
+        const void *kp = rows(k, "k", T, {N, HKV, D}, dev, ks), *vp = rows(v, "v", T, {N, HKV, D}, dev, vs);
+        const int dtype = activation(T);
+        const Kv4Cache c(a[3], a[4], a[5], a[6], D, dev);
+        if (c.HKV != HKV)
+            throw Refusal{GDN_ERR_SHAPE, "k_cache has " + std::to_string(c.HKV) + " heads, expected " + std::to_string(HKV)};
+        const int32_t *slots = (int32_t *)at(a[2], "slots", at::kInt, {N}, dev);
+        const int wanted = PyObject_IsTrue(a[7]);
+        if (wanted < 0) throw Raised{};
+        const c10::cuda::CUDAGuard guard(dev);
+        std::optional<Out> ko, vo;
+        if (wanted || a[8] != Py_None || a[9] != Py_None)
+            ko.emplace(a[8], "k_out", T, at::IntArrayRef({N, HKV, D}), dev), vo.emplace(a[9], "v_out", T, at::IntArrayRef({N, HKV, D}), dev);
+        launch([&] {
+            return gdn_kv4_write(kp, vp, ks, vs, slots, c.k_scale, c.v_scale, c.k, c.v, ko ? ko->ptr : nullptr, vo ? vo->ptr : nullptr, N,
+                                 HKV, D, c.page_size, c.pages, dtype, stream(dev));
+        });
+        return tuple({ko ? &*ko : nullptr, vo ? &*vo : nullptr});
+    });
+}
+
+// (q, k_cache, v_cache, block_table, kv_lens, offsets, max_q, k_scale, v_scale, scale, out, workspace)
+PyObject *attention_paged_kv4(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 12, [&] {
+        const at::Tensor &q = tensor_of(a[0], "q", 3), &table = tensor_of(a[3], "block_table", 2);
+        const c10::Device dev = cuda_device(q, "q");
+        const at::ScalarType T = q.scalar_type();
+        const int N = extent(q.size(0), "N"), H = extent(q.size(1), "H"), D = extent(q.size(2), "D");
+        const int B = extent(table.size(0), "B"), M = extent(table.size(1), "max_pages"), max_q = whole(a[6], "max_q");
+        int64_t qs;
+        const void *qp = rows(q, "q", T, {N, H, D}, dev, qs);
+        const int dtype = activation(T);
+        const Kv4Cache c(a[1], a[2], a[7], a[8], D, dev);
+        const float scale = real(a[9]);
+        const int32_t *bt = (int32_t *)at(a[3], "block_table", at::kInt, {B, M}, dev), *kv = (int32_t *)at(a[4], "kv_lens", at::kInt, {B}, dev),
+                      *of = (int32_t *)at(a[5], "offsets", at::kInt, {B + 1}, dev);
+        const c10::cuda::CUDAGuard guard(dev);
+        Out out(a[10], "out", T, {N, H, D}, dev);
+        const at::Tensor ws = workspace(a[11], gdn_attention_paged_kv4_workspace_bytes(B, N, H, c.HKV, D, max_q), dev);
+        launch([&] {
+            return gdn_attention_paged_kv4(qp, c.k, c.v, c.k_scale, c.v_scale, bt, kv, of, out.ptr, B, N, H, c.HKV, D, c.page_size, M,
+                                           c.pages, max_q, qs, scale, dtype, ws.data_ptr(), (size_t)ws.numel(), stream(dev));
+        });
+        return out.give();
+    });
+}
+
+// (logits, scores, n, finished, end_token, keep_rows, tokens, parents, scores_out, finished_out, workspace)
+PyObject *beam_select(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 11, [&] {
+        const at::Tensor &x = tensor_of(a[0], "logits", 2), &scores = tensor_of(a[1], "scores", 2);
+        const c10::Device dev = cuda_device(x, "logits");
+        const at::ScalarType T = x.scalar_type();
+        const int G = extent(scores.size(0), "G"), K = extent(scores.size(1), "K"), V = extent(x.size(1), "V");
+        const int many = a[2] == Py_None ? K : whole(a[2], "n"), end = whole(a[4], "end_token"), keep = PyObject_IsTrue(a[5]);
+        if (keep < 0) throw Raised{};
+        if (G < 1 || K < 1 || V < 1 || many < 1) throw Refusal{GDN_ERR_SHAPE, "groups, beams, vocabulary and n must be positive"};
+        int64_t stride;
+        const void *xp = rows(x, "logits", T, {(int64_t)G * K, V}, dev, stride);
+        const int dtype = activation(T);
+        const float *sp = (const float *)at(a[1], "scores", at::kFloat, {G, K}, dev);
+        const uint8_t *done = a[3] == Py_None ? nullptr : (const uint8_t *)flags_at(a[3], "finished", {G, K}, dev);
+        const c10::cuda::CUDAGuard guard(dev);
+        Out tokens(a[6], "tokens", at::kInt, {G, many}, dev), parents(a[7], "parents", at::kInt, {G, many}, dev),
+            so(a[8], "scores_out", at::kFloat, {G, many}, dev);
+        std::optional<Out> fo;
+        if (a[9] != Py_None) {
+            const bool truth = THPVariable_Check(a[9]) && THPVariable_Unpack(a[9]).scalar_type() == at::kBool;
+            fo.emplace(a[9], "finished_out", truth ? at::kBool : at::kByte, at::IntArrayRef({G, many}), dev);
+        } else if (done) {
+            fo.emplace(a[9], "finished_out", THPVariable_Unpack(a[3]).scalar_type(), at::IntArrayRef({G, many}), dev);
+        }
+        const at::Tensor ws = workspace(a[10], gdn_beam_select_workspace_bytes(G, K, V, many), dev);
+        launch([&] {
+            return gdn_beam_select(xp, stride, sp, done, end, keep, (int32_t *)tokens.ptr, (int32_t *)parents.ptr, (float *)so.ptr,
+                                   fo ? (uint8_t *)fo->ptr : nullptr, G, K, V, many, dtype, ws.data_ptr(), (size_t)ws.numel(), stream(dev));
+        });
+        return tuple({&tokens, &parents, &so, fo ? &*fo : nullptr});
+    });
+}
+
+PyObject *none() {
+    Py_INCREF(Py_None);
+    return Py_None;
+}
+
+// (states, parents)
+PyObject *state_reorder(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 2, [&] {
+        const Tensors t(a[0], "states");
+        if (t.ptr.empty()) return none();
+        const int B = extent(t.rows, "B"), count = extent((int64_t)t.ptr.size(), "states");
+        const int32_t *parents = (int32_t *)at(a[1], "parents", at::kInt, {B}, *t.dev);
+        const c10::cuda::CUDAGuard guard(*t.dev);
+        launch([&] { return gdn_state_reorder(t.ptr.data(), t.row_bytes.data(), count, parents, B, stream(*t.dev)); });
+        return none();
+    });
+}
+
+// (parents, kv_lens, block_table, free_pages, page_size, num_pages, cursor, table_out, kv_lens_out, copies, cursor_out, status,
+//  workspace)
+PyObject *page_fork(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 13, [&] {
+        const at::Tensor &parents = tensor_of(a[0], "parents", 1), &table = tensor_of(a[2], "block_table", 2), &free = tensor(a[3], "free_pages");
+        const c10::Device dev = cuda_device(table, "block_table");
+        const int B = extent(table.size(0), "B"), M = extent(table.size(1), "max_pages"), R = extent(parents.size(0), "B_out"),
+                  F = extent(free.numel(), "n_free"), ps = whole(a[4], "page_size"), pages = whole(a[5], "num_pages");
+        const auto i32 = at::kInt;
+        const int32_t *pp = (int32_t *)at(a[0], "parents", i32, {R}, dev), *kv = (int32_t *)at(a[1], "kv_lens", i32, {B}, dev),
+                      *bt = (int32_t *)at(a[2], "block_table", i32, {B, M}, dev), *cu = (int32_t *)at(a[6], "cursor", i32, {1}, dev);
+        int32_t *fp = (int32_t *)at(a[3], "free_pages", i32, {F}, dev);
+        const c10::cuda::CUDAGuard guard(dev);
+        Out to(a[7], "table_out", i32, {R, M}, dev), ko(a[8], "kv_lens_out", i32, {R}, dev), copies(a[9], "copies", i32, {R, 2}, dev),
+            co(a[10], "cursor_out", i32, {1}, dev), status(a[11], "status", i32, {1}, dev);
+        const at::Tensor ws = workspace(a[12], gdn_page_fork_workspace_bytes(B, M, pages), dev);
+        launch([&] {
+            return gdn_page_fork(pp, kv, bt, fp, cu, (int32_t *)to.ptr, (int32_t *)ko.ptr, (int32_t *)copies.ptr, (int32_t *)co.ptr,
+                                 (int32_t *)status.ptr, B, R, ps, M, pages, F, ws.data_ptr(), (size_t)ws.numel(), stream(dev));
+        });
+        return tuple({&to, &ko, &copies, &co, &status});
+    });
+}
+
+// (kv_lens, block_table, page_size, num_pages, table_out, copies, free_pages, cursor_out, status, workspace)
+PyObject *page_compact(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 10, [&] {
+        const at::Tensor &table = tensor_of(a[1], "block_table", 2);
+        const c10::Device dev = cuda_device(table, "block_table");
+        const int B = extent(table.size(0), "B"), M = extent(table.size(1), "max_pages"), ps = whole(a[2], "page_size"),
+                  pages = whole(a[3], "num_pages");
+        if (pages < 1) throw Refusal{GDN_ERR_SHAPE, "num_pages must be positive"};
+        const auto i32 = at::kInt;
+        const int32_t *kv = (int32_t *)at(a[0], "kv_lens", i32, {B}, dev), *bt = (int32_t *)at(a[1], "block_table", i32, {B, M}, dev);
+        const c10::cuda::CUDAGuard guard(dev);
+        Out to(a[4], "table_out", i32, {B, M}, dev), copies(a[5], "copies", i32, {pages / 2, 2}, dev), free(a[6], "free_pages", i32, {pages}, dev),
+            co(a[7], "cursor_out", i32, {1}, dev), status(a[8], "status", i32, {1}, dev);
+        const at::Tensor ws = workspace(a[9], gdn_page_compact_workspace_bytes(pages), dev);
+        launch([&] {
+            return gdn_page_compact(kv, bt, (int32_t *)to.ptr, (int32_t *)copies.ptr, (int32_t *)free.ptr, (int32_t *)co.ptr,
+                                    (int32_t *)status.ptr, B, ps, M, pages, ws.data_ptr(), (size_t)ws.numel(), stream(dev));
+        });
+        return tuple({&to, &copies, &free, &co, &status});
+    });
+}
+
+// (caches, copies)
+PyObject *page_copy(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 2, [&] {
+        const Tensors t(a[0], "caches");
+        if (t.ptr.empty()) return none();
+        const at::Tensor &copies = tensor_of(a[1], "copies", 2);
+        const int pairs = extent(copies.size(0), "copies"), pages = extent(t.rows, "num_pages"), count = extent((int64_t)t.ptr.size(), "caches");
+        const int32_t *cp = (int32_t *)at(a[1], "copies", at::kInt, {pairs, 2}, *t.dev);
+        const c10::cuda::CUDAGuard guard(*t.dev);
+        launch([&] { return gdn_page_copy(t.ptr.data(), t.row_bytes.data(), count, cp, pairs, pages, stream(*t.dev)); });
+        return none();
+    });
+}
+
 // (GdnError)
 PyObject *init(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded(n, 1, [&] {
@@ -399,6 +634,13 @@ PyMethodDef g_methods[] = {{"init", CALL(init)},
                            {"qk_norm_rope", CALL(qk_norm_rope)},
                            {"attention_varlen", CALL(attention_varlen)},
                            {"attention_paged", CALL(attention_paged)},
+                           {"kv4_write", CALL(kv4_write)},
+                           {"attention_paged_kv4", CALL(attention_paged_kv4)},
+                           {"beam_select", CALL(beam_select)},
+                           {"state_reorder", CALL(state_reorder)},
+                           {"page_fork", CALL(page_fork)},
+                           {"page_compact", CALL(page_compact)},
+                           {"page_copy", CALL(page_copy)},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, g_methods};
 

@@ -1,0 +1,550 @@
+// attention_kv4.cu - gdn_attention_paged_kv4: attention of new tokens over a paged cache of 4-bit values (kv4.cuh).
+//
+// As gdn_attention_paged, with k_j = ks u_j c_j and v_j likewise; the heads' own scales ks and vs go into the softmax's
+// factor and the output, so that what is multiplied, s c, is exact in fp16.  Queries are brought to the same type: each row by
+// a power of two that puts its largest value into [1, 2), which the row's softmax factor takes back.  That keeps a bf16 query
+// exact (down to 2^-24 of the row's largest value); an fp32 query is the sum of two fp16 values.  Probabilities
+// are taken 2^14 times as large, so that fp16 holds them to 11 bits down to 2^-28 of the row's largest; with
+// fp32 activations they too are sums of two.
+//
+// Keys are read once for the rows that share them, 9/16 bytes a channel of k and v: a tile's codes and scales
+// stream through a ring filled by 16-byte cp.async copies, are turned into fp16 tiles in shared memory, and
+// multiplied by 16-row mma.sync, a warp to 16 of 64 rows.  Work is cut by key tiles: the tiles of all (sequence, row block,
+// key-value head) triples form one list, of which every CTA takes an equal run; a CTA whose run begins or ends inside a triple
+// leaves m, l and an unscaled o for a second kernel that joins the parts.
+#include <algorithm>
+#include <cmath>
+
+#include "attention.cuh"
+#include "kv4.cuh"
+#include "sm100.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kMaxCtas = 4 * 160;
+constexpr float kShift = 14.f;  // log2 of the probabilities' factor
+
+struct Kv4Params {
+    Attn a;
+    const float *ks, *vs;  // of each key-value head, or NULL
+    int G;
+    float c;       // |scale| log2(e)
+    float sign;    // of scale
+    int blocks;    // row blocks of the longest sequence
+    int2 *spans;   // [B][blocks][HKV]: first and last CTA of a triple
+    float *part;   // [2 * CTAs][ROWS * (3 + DP)]
+};
+
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 16 bytes to shared memory, or zeros
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool read) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+// What fp16 leaves of two values.
+__device__ __forceinline__ uint32_t rest_f16(float lo, float hi, uint32_t kept) {
+    const float2 f = f16x2_to_f32(kept);
+    return pack_f16(lo - f.x, hi - f.y);
+}
+template <typename T>
+__device__ __forceinline__ void store2(T *at, float x, float y);
+template <>
+__device__ __forceinline__ void store2(float *at, float x, float y) { *reinterpret_cast<float2 *>(at) = make_float2(x, y); }
+template <>
+__device__ __forceinline__ void store2(__nv_bfloat16 *at, float x, float y) {
+    *reinterpret_cast<__nv_bfloat162 *>(at) = __floats2bfloat162_rn(x, y);
+}
+// The power of two that brings a row's largest magnitude into [1, 2), and its inverse (for rows below 2^-63, nothing
+// but zeros among them, 2^63, so that the inverse stays far from zero).
+__device__ __forceinline__ float row_power(float amax, float &inverse) {
+    const int e = max(64, min((int)(__float_as_uint(amax) >> 23 & 255u), 253));  // (biased)
+    inverse = __uint_as_float((uint32_t)e << 23);
+    return __uint_as_float((uint32_t)(254 - e) << 23);
+}
+
+// Byte offset of 16-byte chunk c of row r: chunks of 8 neighbouring rows fall into different banks.
+template <int DP>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+    return (uint32_t)(r * DP * 2 + ((c ^ (r & 7)) << 4));
+}
+
+// ---------------------------------------------------------------- the list of tiles
+
+// The key tiles of one row block (ROWS rows) of sequence b, whose rows number len * G.
+__device__ __forceinline__ int block_tiles(const Kv4Params &p, int rows, int keys, int block, int len, int kv) {
+    const long last = min((long)(block + 1) * rows, (long)len * p.G) - 1;
+    const int seen = min(kv, kv - len + (int)(last / p.G) + 1);
+    return seen > 0 ? (seen + keys - 1) / keys : 1;  // (no keys: one tile that gives zeros)
+}
+// Row blocks of sequence b; 0: not ours.
+__device__ __forceinline__ int seq_blocks(const Kv4Params &p, int rows, int b, int &start, int &len, int &kv) {
+    if (b >= p.a.B || !attn_seq(p.a, b, start, len, kv) || len == 0) return 0;
+    return (int)(((long)len * p.G + rows - 1) / rows);
+}
+__device__ __forceinline__ long seq_tiles(const Kv4Params &p, int rows, int keys, int b) {
+    int start, len, kv;
+    const int n = seq_blocks(p, rows, b, start, len, kv);
+    long all = 0;
+    for (int i = 0; i < n; ++i) all += block_tiles(p, rows, keys, i, len, kv);
+    return all * p.a.HKV;
+}
+
+struct Cursor {
+    int b, block, h, tile, tiles, blocks, start, len, kv;
+};
+__device__ __forceinline__ void advance(const Kv4Params &p, int rows, int keys, Cursor &x) {
+    if (++x.tile < x.tiles) return;
+    x.tile = 0;
+    if (++x.h < p.a.HKV) return;
+    x.h = 0;
+    if (++x.block == x.blocks) {
+        x.block = 0;
+        do x.blocks = seq_blocks(p, rows, ++x.b, x.start, x.len, x.kv);
+        while (x.blocks == 0 && x.b < p.a.B);
+        if (x.blocks == 0) return;
+    }
+    x.tiles = block_tiles(p, rows, keys, x.block, x.len, x.kv);
+}
+
+// Block-wide: this CTA's run [u0, u1) of the U tiles and its first place; false when it has none.
+template <int THREADS>
+__device__ __forceinline__ bool find_run(const Kv4Params &p, int rows, int keys, long long &u0, long long &u1, long long &U,
+                                         long long &ctas, Cursor &cur) {
+    __shared__ long long s_scan[THREADS / 32], s_at;
+    __shared__ int s_b;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (p.a.B + THREADS - 1) / THREADS;  // threads own neighbouring sequences
+    long long mine = 0;
+    for (int i = 0; i < per; ++i) mine += seq_tiles(p, rows, keys, tid * per + i);
+    long long sum = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += x;
+    }
+    if (lane == 31) s_scan[warp] = sum;
+    __syncthreads();
+    U = 0;
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) sum += s_scan[w];
+        U += s_scan[w];
+    }
+    ctas = U < gridDim.x ? U : gridDim.x;  // every CTA that takes part has at least one tile
+    const long long cta = blockIdx.x;
+    if (cta >= ctas) return false;
+    u0 = cta * U / ctas, u1 = (cta + 1) * U / ctas;
+    long long at = sum - mine;
+    if (u0 >= at && u0 < sum)
+        for (int i = 0; i < per; ++i) {
+            const long long n = per > 1 ? seq_tiles(p, rows, keys, tid * per + i) : mine;
+            if (u0 < at + n) {
+                s_at = at, s_b = tid * per + i;
+                break;
+            }
+            at += n;
+        }
+    __syncthreads();
+    cur.b = s_b;
+    cur.blocks = seq_blocks(p, rows, cur.b, cur.start, cur.len, cur.kv);
+    long long left = u0 - s_at;
+    for (cur.block = 0;; ++cur.block) {
+        cur.tiles = block_tiles(p, rows, keys, cur.block, cur.len, cur.kv);
+        if (left < (long long)cur.tiles * p.a.HKV) break;
+        left -= (long long)cur.tiles * p.a.HKV;
+    }
+    cur.h = (int)(left / cur.tiles);
+    cur.tile = (int)(left % cur.tiles);
+    return true;
+}
+
+__device__ __forceinline__ long span_of(const Kv4Params &p, const Cursor &x) {
+    return ((long)x.b * p.blocks + x.block) * p.a.HKV + x.h;
+}
+__device__ __forceinline__ float head_scale(const float *s, int h) { return s ? __ldg(s + h) : 1.f; }
+
+// Block of 16 tokens of a cache: its page's (key-value head) block, or NULL.
+__device__ __forceinline__ const uint8_t *token_block(const Kv4Params &p, const void *cache, int b, int h, int key) {
+    const int page = __ldg(p.a.block_table + (size_t)b * p.a.max_pages + key / p.a.page_size);
+    if (page < 0 || page >= p.a.num_pages) return nullptr;
+    return static_cast<const uint8_t *>(cache) + ((long)page * p.a.HKV + h) * ((long)p.a.page_size * (p.a.D / 16) * 9);
+}
+
+// ---------------------------------------------------------------- rows by the block of 64
+
+template <int DP, typename T>
+struct Wide {
+    static constexpr int KEYS = 64, ROWS = 64, THREADS = 128, STAGES = 3;
+    static constexpr int Q = sizeof(T) == 4 ? 2 : 1;            // fp16 values to a query's
+    static constexpr int RAW = KEYS * DP / 16 * 9;              // bytes of a tile of K (or V): codes, then scales
+    static constexpr int TILE = KEYS * DP * 2;                  // the same in fp16
+    static constexpr int QBYTES = ROWS * DP * 2;
+    static constexpr int SMEM = STAGES * 2 * RAW + 2 * TILE + Q * QBYTES;
+    static constexpr int PART = ROWS * (3 + DP);  // floats of a part: m, l, the rows' factors, o
+};
+
+template <int DP, typename T>
+__global__ void __launch_bounds__(128) kv4_wide_kernel(const Kv4Params p) {
+    using C = Wide<DP, T>;
+    constexpr int KEYS = C::KEYS, STAGES = C::STAGES;
+    constexpr bool F32 = sizeof(T) == 4;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ float s_c[C::ROWS];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+    const uint32_t raw = sm100::smem_u32(smem), s_k = raw + STAGES * 2 * C::RAW, s_v = s_k + C::TILE, s_q = s_v + C::TILE;
+    unsigned char *tiles = smem + STAGES * 2 * C::RAW, *q_rows = tiles + 2 * C::TILE;
+    const int D = p.a.D, G = p.G, GR = D / 16;
+    pdl_wait_primary();
+    pdl_launch_dependents();  // (the joining blocks wait for this grid's end)
+    long long u0, u1, U, ctas;
+    Cursor cur;
+    if (!find_run<C::THREADS>(p, C::ROWS, KEYS, u0, u1, U, ctas, cur)) return;
+    const long long cta = blockIdx.x;
+    if (D < DP)  // channels past the last: zeros, for good
+        for (int i = tid; i < 2 * KEYS * (DP / 8); i += C::THREADS)
+            *reinterpret_cast<uint4 *>(tiles + (i / (KEYS * (DP / 8))) * C::TILE + chunk_at<DP>(i / (DP / 8) % KEYS, i % (DP / 8))) =
+                make_uint4(0, 0, 0, 0);
+
+    auto fetch = [&](const Cursor &x, int stage) {
+        const uint32_t dst = raw + stage * 2 * C::RAW;
+        const int codes = 8 * GR, per = 9 * GR;  // 16-byte chunks of 16 tokens
+#pragma unroll 1
+        for (int i = tid; i < KEYS / 16 * per; i += C::THREADS) {
+            const int block = i / per, c = i % per, key = x.tile * KEYS + block * 16;
+            const uint8_t *kb = nullptr, *vb = nullptr;
+            if (key < x.kv) kb = token_block(p, p.a.k, x.b, x.h, key), vb = token_block(p, p.a.v, x.b, x.h, key);
+            const int at = key % p.a.page_size;
+            const long from = c < codes ? (long)at * GR * 8 + c * 16 : (long)p.a.page_size * GR * 8 + at * GR + (c - codes) * 16;
+            const uint32_t to = c < codes ? block * codes * 16 + c * 16 : KEYS * GR * 8 + block * GR * 16 + (c - codes) * 16;
+            copy16(dst + to, kb ? kb + from : p.a.k, kb != nullptr);
+            copy16(dst + C::RAW + to, vb ? vb + from : p.a.v, vb != nullptr);
+        }
+    };
+    Cursor ahead = cur;
+    long long u_ahead = u0;
+    for (int i = 0; i < STAGES - 1; ++i) {
+        if (u_ahead < u1) {
+            fetch(ahead, i);
+            if (++u_ahead < u1) advance(p, C::ROWS, KEYS, ahead);
+        }
+        copy_commit();
+    }
+
+    float o[DP / 8][4], m[2], l[2], cr[2];
+    int stage = 0, first_tile = 0;
+    bool fresh = true;  // the next tile begins a part
+    for (long long u = u0; u < u1; ++u) {
+        const int n = cur.len, row0 = cur.block * C::ROWS, rows = min(C::ROWS, n * G - row0), shift = cur.kv - n;
+        if (fresh) {
+            fresh = false;
+            first_tile = cur.tile;
+            // this warp's 16 rows of Q
+            const float c = fmaxf(p.c * head_scale(p.ks, cur.h), 1e-18f);
+            __syncwarp();
+            for (int r = warp * 16; r < warp * 16 + 16; ++r) {
+                const bool real = r < rows;
+                const T *src = static_cast<const T *>(p.a.q) +
+                               (real ? (long)(cur.start + (row0 + r) / G) * p.a.qs + (long)(cur.h * G + (row0 + r) % G) * D : 0);
+                float x[DP / 32], amax = 0.f;
+#pragma unroll
+                for (int i = 0; i < DP / 32; ++i) {
+                    const int d = lane + 32 * i;
+                    x[i] = real && d < D ? to_f32(src[d]) : 0.f;
+                    amax = fmaxf(amax, fabsf(x[i]));
+                }
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+                float back;
+                const float power = row_power(amax, back) * p.sign;
+#pragma unroll
+                for (int i = 0; i < DP / 32; ++i) {
+                    const int d = lane + 32 * i;
+                    const uint32_t at = chunk_at<DP>(r, d / 8) + (d % 8) * 2;
+                    const __half hi = __float2half_rn(x[i] * power);
+                    *reinterpret_cast<__half *>(q_rows + at) = hi;
+                    if constexpr (F32)
+                        *reinterpret_cast<__half *>(q_rows + C::QBYTES + at) = __float2half_rn(x[i] * power - __half2float(hi));
+                }
+                if (lane == 0) s_c[r] = c * back;
+            }
+            __syncwarp();
+            cr[0] = s_c[warp * 16 + g], cr[1] = s_c[warp * 16 + g + 8];
+            m[0] = m[1] = -INFINITY, l[0] = l[1] = 0.f;
+#pragma unroll
+            for (int i = 0; i < DP / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        }
+        copy_wait<STAGES - 2>();
+        __syncthreads();  // the tile is here, and the last one's products are done
+        {
+            if (u_ahead < u1) {
+                fetch(ahead, stage == 0 ? STAGES - 1 : stage - 1);
+                if (++u_ahead < u1) advance(p, C::ROWS, KEYS, ahead);
+            }
+            copy_commit();
+        }
+        // ---- codes to fp16, 16 channels at a time
+        const unsigned char *from = smem + stage * 2 * C::RAW;
+#pragma unroll 2
+        for (int i = tid; i < 2 * KEYS * GR; i += C::THREADS) {
+            const int which = i >= KEYS * GR, k = i - which * KEYS * GR, key = k / GR, grp = k % GR;
+            const unsigned char *src = from + which * C::RAW;
+            const uint2 w = *reinterpret_cast<const uint2 *>(src + k * 8);
+            const uint32_t b = src[KEYS * GR * 8 + k], s = kv4_scales(b | b << 8);
+            uint32_t d[2][4];
+            kv4_codes(w.x, d[0]), kv4_codes(w.y, d[1]);
+            unsigned char *to = tiles + which * C::TILE;
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+                *reinterpret_cast<uint4 *>(to + chunk_at<DP>(key, grp * 2 + half)) =
+                    make_uint4(mul_f16x2(d[half][0], s), mul_f16x2(d[half][1], s), mul_f16x2(d[half][2], s), mul_f16x2(d[half][3], s));
+        }
+        __syncthreads();
+        // ---- scores of 16 rows
+        const int j0 = cur.tile * KEYS;
+        float s[KEYS / 8][4];
+#pragma unroll
+        for (int i = 0; i < KEYS / 8; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < DP / 16; ++ks) {
+            uint32_t q[C::Q][4], k[4];
+#pragma unroll
+            for (int z = 0; z < C::Q; ++z)
+                ldmatrix4(s_q + z * C::QBYTES + chunk_at<DP>(warp * 16 + (lane & 15), ks * 2 + (lane >> 4)), q[z]);
+#pragma unroll
+            for (int i = 0; i < KEYS / 16; ++i) {
+                ldmatrix4(s_k + chunk_at<DP>(i * 16 + (lane >> 4) * 8 + (lane & 7), ks * 2 + ((lane >> 3) & 1)), k);
+#pragma unroll
+                for (int z = 0; z < C::Q; ++z) {
+                    mma16816(s[2 * i], q[z], k[0], k[1]);
+                    mma16816(s[2 * i + 1], q[z], k[2], k[3]);
+                }
+            }
+        }
+        // ---- running softmax of rows g and g + 8
+        float mx[2] = {m[0], m[1]};
+        const int rr = row0 + warp * 16 + g;
+        const int seen[2] = {shift + rr / G + 1 - j0, shift + (rr + 8) / G + 1 - j0};
+        const bool edge = j0 + KEYS > shift + row0 / G + 1;  // some row does not see the whole tile
+        // (rows past the last hold zeros and see no more keys than there are)
+        const int end = cur.kv - j0;
+#pragma unroll
+        for (int i = 0; i < KEYS / 8; ++i)
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                if (edge && i * 8 + t4 * 2 + (z & 1) >= min(seen[z >> 1], end)) s[i][z] = -INFINITY;
+                mx[z >> 1] = fmaxf(mx[z >> 1], s[i][z]);
+            }
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            mx[z] = fmaxf(mx[z], __shfl_xor_sync(0xffffffffu, mx[z], 1));
+            mx[z] = fmaxf(mx[z], __shfl_xor_sync(0xffffffffu, mx[z], 2));
+            if (mx[z] > m[z]) {
+                // (a row that has seen nothing keeps l = o = 0 under any factor but NaN)
+                const float f = m[z] == -INFINITY ? 1.f : exp2_fast((m[z] - mx[z]) * cr[z]);
+                l[z] *= f;
+#pragma unroll
+                for (int i = 0; i < DP / 8; ++i) o[i][2 * z] *= f, o[i][2 * z + 1] *= f;
+                m[z] = mx[z];
+            }
+        }
+        const float base[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+#pragma unroll
+        for (int i = 0; i < KEYS / 8; ++i)
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                s[i][z] = exp2_fast(fmaf(s[i][z] - base[z >> 1], cr[z >> 1], kShift));
+                l[z >> 1] += s[i][z];
+            }
+        // ---- o += P V
+#pragma unroll
+        for (int i = 0; i < KEYS / 16; ++i) {
+            uint32_t pa[C::Q][4];
+            pa[0][0] = pack_f16(s[2 * i][0], s[2 * i][1]), pa[0][1] = pack_f16(s[2 * i][2], s[2 * i][3]);
+            pa[0][2] = pack_f16(s[2 * i + 1][0], s[2 * i + 1][1]), pa[0][3] = pack_f16(s[2 * i + 1][2], s[2 * i + 1][3]);
+            if constexpr (F32) {
+                pa[1][0] = rest_f16(s[2 * i][0], s[2 * i][1], pa[0][0]), pa[1][1] = rest_f16(s[2 * i][2], s[2 * i][3], pa[0][1]);
+                pa[1][2] = rest_f16(s[2 * i + 1][0], s[2 * i + 1][1], pa[0][2]);
+                pa[1][3] = rest_f16(s[2 * i + 1][2], s[2 * i + 1][3], pa[0][3]);
+            }
+#pragma unroll
+            for (int c = 0; c < DP / 16; ++c) {
+                uint32_t v[4];
+                ldmatrix4_trans(s_v + chunk_at<DP>(i * 16 + (lane & 15), 2 * c + (lane >> 4)), v);
+#pragma unroll
+                for (int z = 0; z < C::Q; ++z) {
+                    mma16816(o[2 * c], pa[z], v[0], v[1]);
+                    mma16816(o[2 * c + 1], pa[z], v[2], v[3]);
+                }
+            }
+        }
+        stage = stage == STAGES - 1 ? 0 : stage + 1;
+
+        const bool last = cur.tile + 1 == cur.tiles;
+        if (last || u + 1 == u1) {
+            // ---- the part ends
+            fresh = true;
+            const bool whole = last && first_tile == 0;
+            if (last && tid == 0) {
+                const long long first = u - cur.tile;  // the triple's first tile
+                p.spans[span_of(p, cur)] = make_int2((int)(((first + 1) * ctas - 1) / U), (int)cta);
+            }
+            const float vs = head_scale(p.vs, cur.h);
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                l[z] += __shfl_xor_sync(0xffffffffu, l[z], 1);
+                l[z] += __shfl_xor_sync(0xffffffffu, l[z], 2);
+                const int r = warp * 16 + g + 8 * z;
+                if (r >= rows) continue;
+                if (whole) {
+                    const float inv = l[z] > 0.f ? vs / l[z] : l[z];  // (0 gives 0, NaN stays)
+                    T *out = static_cast<T *>(p.a.out) + ((size_t)(cur.start + (row0 + r) / G) * p.a.H + cur.h * G + (row0 + r) % G) * D;
+#pragma unroll
+                    for (int i = 0; i < DP / 8; ++i)
+                        if (i * 8 < D) store2(out + i * 8 + t4 * 2, o[i][2 * z] * inv, o[i][2 * z + 1] * inv);
+                } else {
+                    // a part that begins its triple is the CTA's last, any other its first
+                    float *part = p.part + (2 * cta + (first_tile == 0)) * C::PART;
+                    if (t4 == 0) part[r] = m[z], part[C::ROWS + r] = l[z], part[2 * C::ROWS + r] = cr[z];
+                    part += 3 * C::ROWS + r * DP;
+#pragma unroll
+                    for (int i = 0; i < DP / 8; ++i)
+                        *reinterpret_cast<float2 *>(part + i * 8 + t4 * 2) = make_float2(o[i][2 * z], o[i][2 * z + 1]);
+                }
+            }
+        }
+        advance(p, C::ROWS, KEYS, cur);
+    }
+}
+
+// ---------------------------------------------------------------- parts
+
+// Joins the parts of each triple that several CTAs shared: a block to a (triple, row), its warps to every fourth part.
+template <int DP, typename T>
+__global__ void __launch_bounds__(128) kv4_join_kernel(const Kv4Params p, int rows, int keys) {
+    constexpr int E = DP / 32;  // channels of a lane
+    __shared__ float s_m[4], s_l[4], s_o[4][DP];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.y;
+    const int h = blockIdx.x % p.a.HKV, block = blockIdx.x / p.a.HKV % p.blocks, b = blockIdx.x / p.a.HKV / p.blocks;
+    pdl_wait_primary();
+    int start, len, kv;
+    if (block >= seq_blocks(p, rows, b, start, len, kv)) return;
+    const long row = (long)block * rows + r;
+    if (row >= (long)len * p.G) return;
+    const int2 span = p.spans[blockIdx.x];
+    if (span.x == span.y) return;
+    const int PART = rows * (3 + DP);
+    auto part = [&](int c) { return p.part + (2L * c + (c == span.x)) * PART; };
+    float M = -INFINITY;
+    for (int c = span.x + tid; c <= span.y; c += 128) M = fmaxf(M, part(c)[r]);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    if (lane == 0) s_m[warp] = M;
+    __syncthreads();
+    M = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+    float L = 0.f, o[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) o[i] = 0.f;
+#pragma unroll 4
+    for (int c = span.x + warp; c <= span.y; c += 4) {
+        const float *x = part(c);
+        const float mc = x[r], f = mc == -INFINITY ? 0.f : exp2_fast((mc - M) * x[2 * rows + r]);
+        L += f * x[rows + r];
+        x += 3 * rows + r * DP + lane * E;
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+            const float2 y = *reinterpret_cast<const float2 *>(x + i);
+            o[i] += f * y.x, o[i + 1] += f * y.y;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) s_o[warp][lane * E + i] = o[i];
+    if (lane == 0) s_l[warp] = L;
+    __syncthreads();
+    L = s_l[0] + s_l[1] + s_l[2] + s_l[3];
+    const float inv = L > 0.f ? head_scale(p.vs, h) / L : L;  // (0 gives 0, NaN stays)
+    T *out = static_cast<T *>(p.a.out) + ((size_t)(start + row / p.G) * p.a.H + h * p.G + row % p.G) * p.a.D;
+    for (int d = tid; d < p.a.D; d += 128) out[d] = from_f32<T>((s_o[0][d] + s_o[1][d] + s_o[2][d] + s_o[3][d]) * inv);
+}
+
+// ---------------------------------------------------------------- host
+
+int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+size_t span_bytes(int B, int HKV, long blocks) { return ((size_t)B * blocks * HKV * 8 + 255) & ~size_t(255); }
+long row_blocks(int H, int HKV, int max_q, int rows) { return ((long)max_q * (H / HKV) + rows - 1) / rows; }
+
+template <int DP, typename T>
+cudaError_t launch_wide(Kv4Params p, void *ws, cudaStream_t s) {
+    using C = Wide<DP, T>;
+    static std::atomic<uint64_t> attr_set{0};
+    cudaError_t e = once_per_device(attr_set, [] {
+        return cudaFuncSetAttribute(kv4_wide_kernel<DP, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    });
+    if (e != cudaSuccess) return e;
+    p.blocks = (int)row_blocks(p.a.H, p.a.HKV, p.a.max_q, C::ROWS);
+    p.spans = static_cast<int2 *>(ws);
+    p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + span_bytes(p.a.B, p.a.HKV, p.blocks));
+    int dev = 0, sms = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const long triples = (long)p.a.B * p.blocks * p.a.HKV;
+    if (triples > INT32_MAX) return cudaErrorInvalidConfiguration;
+    const long most = triples * (((long)p.a.max_pages * p.a.page_size + C::KEYS - 1) / C::KEYS);
+    const long per_sm = std::max(1, 220 * 1024 / (C::SMEM + 1024));
+    const long grid = std::min(std::min(per_sm * sms, (long)kMaxCtas), most);
+    e = launch_kernel(kv4_wide_kernel<DP, T>, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, s, true, p);
+    note_launch();
+    if (e != cudaSuccess) return e;
+    const long rows = std::min((long)p.a.max_q * p.G, (long)C::ROWS);
+    e = launch_kernel(kv4_join_kernel<DP, T>, dim3((unsigned)triples, (unsigned)rows), dim3(128), 0, s, true, p, C::ROWS, C::KEYS);
+    note_launch();
+    return e;
+}
+
+template <typename T>
+cudaError_t launch(const Kv4Params &p, void *ws, cudaStream_t s) {
+    switch (padded(p.a.D)) {
+    case 64: return launch_wide<64, T>(p, ws, s);
+    case 128: return launch_wide<128, T>(p, ws, s);
+    default: return launch_wide<256, T>(p, ws, s);
+    }
+}
+
+}  // namespace
+
+size_t attention_kv4_workspace(int B, int N, int H, int HKV, int D, int max_q) {
+    return span_bytes(B, HKV, row_blocks(H, HKV, max_q, 64)) + 2 * (size_t)kMaxCtas * 64 * (3 + padded(D)) * 4;
+}
+
+cudaError_t launch_attention_kv4(const Attn &a, const float *k_scale, const float *v_scale, int dtype, void *ws, cudaStream_t s) {
+    Kv4Params p{};
+    p.a = a;
+    p.ks = k_scale, p.vs = v_scale;
+    p.G = a.H / a.HKV;
+    p.c = std::fabs(a.scale) * kLog2e;
+    p.sign = a.scale < 0.f ? -1.f : 1.f;
+    return dtype == GDN_BF16 ? launch<__nv_bfloat16>(p, ws, s) : launch<float>(p, ws, s);
+}
+
+}  // namespace gdn

@@ -1,0 +1,414 @@
+// page_fork.cu - gdn_page_fork, gdn_page_compact and gdn_page_copy: block tables follow the chosen beams, live
+// pages move to the front of the pool, and the pages' contents are copied.
+//
+// Who owns a page is read off the block table itself: a page is live while a row holds it among its first
+// ceil(len / page_size) entries.  So both plans are marks on the pool's pages (one byte each, plain
+// stores of the same value), prefix sums over the marks and over the rows, and independent rewriting of the entries:
+// a few hundred kilobytes at most, bound by the launch and by the latency of some dependent steps.  One launch
+// each: a thread-block cluster, whose barrier parts the steps (one CTA for small pools).  Order comes from
+// page numbers and row numbers alone, so results do not depend on timing.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "serving.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kCluster = 8;
+
+// Exclusive sum over the block; returns the block's total in `all`.
+__device__ __forceinline__ int block_scan(int x, int &all, int *s_sum) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, x0 = x;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+    }
+    __syncthreads();  // an earlier scan's sums have been read
+    if (lane == 31) s_sum[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int w = s_sum[lane];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, w, d);
+            if (lane >= d) w += y;
+        }
+        s_sum[lane] = w;
+    }
+    __syncthreads();
+    all = s_sum[31];
+    return x - x0 + (warp ? s_sum[warp - 1] : 0);
+}
+
+// The part of n things that thread `i` of `of` takes: [lo, hi), in whole multiples of 16.
+__device__ __forceinline__ void share(long n, long i, long of, long &lo, long &hi) {
+    const long per = (((n + of - 1) / of) + 15) / 16 * 16;
+    lo = min(n, i * per), hi = min(n, lo + per);
+}
+
+struct ForkSpace {  // in the workspace; every part on a 16-byte boundary
+    int *total;     // [kCluster] a CTA's sum
+    int *error;     // [kCluster]
+    int *old;       // [B][max_pages] the table before the call
+    uint8_t *was, *is;  // [num_pages] live before and after
+};
+
+__global__ void __launch_bounds__(kThreads) page_fork_kernel(const PageFork p, ForkSpace w) {
+    extern __shared__ int s_fork[];
+    int *s_len = s_fork, *s_first = s_len + p.B, *s_rank = s_first + p.B;  // [B], [B], [B_out + 1]
+    __shared__ int s_sum[32], s_bad;
+    const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+    const int tid = threadIdx.x, rank = blockIdx.x, ranks = gridDim.x, ps = p.page_size, M = p.max_pages;
+    const long t0 = (long)rank * kThreads + tid, step = (long)ranks * kThreads;
+    pdl_wait_primary();
+
+    // ---- clear the marks; copy the table, which may be written in place; look for what is wrong
+    for (long i = t0 * 16; i < p.num_pages; i += step * 16)  // (the marks' rooms are multiples of 16)
+        *reinterpret_cast<uint4 *>(w.was + i) = *reinterpret_cast<uint4 *>(w.is + i) = make_uint4(0, 0, 0, 0);
+    if (tid == 0) s_bad = 0;
+    __syncthreads();
+    const int cursor = __ldg(p.cursor);
+    bool bad = cursor < 0;
+    for (int b = tid; b < p.B; b += kThreads) {
+        const int len = p.kv_lens[b];
+        const bool fits = len >= 0 && len <= (long)M * ps;
+        bad |= !fits;
+        s_len[b] = fits ? len : 0;
+        s_first[b] = p.B_out;
+    }
+    __syncthreads();
+    for (int i = tid; i < p.B_out; i += kThreads) {
+        const int parent = __ldg(p.parents + i);
+        bad |= parent >= p.B;
+        if (parent >= 0 && parent < p.B) atomicMin(s_first + parent, i);
+    }
+    for (long e = t0; e < (long)p.B * M; e += step) {
+        const int b = (int)(e / M), j = (int)(e % M);
+        if (j >= (s_len[b] + ps - 1) / ps) continue;
+        const int page = p.block_table[e];
+        bad |= page < 0 || page >= p.num_pages;
+        w.old[e] = page;
+    }
+    if (bad) s_bad = 1;
+    __syncthreads();
+    if (tid == 0) w.error[rank] = s_bad;
+
+    // ---- rows that need a page of their own for their last, partly filled one: all children but the first
+    const auto copies_last = [&](int i) {
+        const int parent = __ldg(p.parents + i);
+        return parent >= 0 && parent < p.B && s_len[parent] % ps != 0 && s_first[parent] != i;
+    };
+    int copies = 0, mine = 0;
+    {
+        const int per = (p.B_out + kThreads - 1) / kThreads, i0 = min(p.B_out, tid * per), i1 = min(p.B_out, i0 + per);
+        for (int i = i0; i < i1; ++i) mine += copies_last(i);
+        int at = block_scan(mine, copies, s_sum);
+        for (int i = i0; i < i1; ++i) {
+            s_rank[i] = at;
+            at += copies_last(i);
+        }
+    }
+    cluster.sync();
+    bad = false;
+    for (int r = 0; r < ranks; ++r) bad |= __ldcg(w.error + r) != 0;
+
+    // ---- marks
+    if (!bad) {
+        for (long e = t0; e < (long)p.B * M; e += step) {
+            const int b = (int)(e / M), j = (int)(e % M);
+            if (j < (s_len[b] + ps - 1) / ps) w.was[__ldcg(w.old + e)] = 1;
+        }
+        for (long e = t0; e < (long)p.B_out * M; e += step) {
+            const int i = (int)(e / M), j = (int)(e % M), parent = __ldg(p.parents + i);
+            if (parent >= 0 && j < (s_len[parent] + ps - 1) / ps - copies_last(i)) w.is[__ldcg(w.old + (long)parent * M + j)] = 1;
+        }
+    }
+    cluster.sync();
+
+    // ---- pages that go back to the list, in their order
+    long lo, hi;
+    share(p.num_pages, t0, step, lo, hi);
+    int back = 0, all = 0;
+    for (long i = lo; i < hi; i += 16) {
+        const uint4 a = __ldcg(reinterpret_cast<const uint4 *>(w.was + i)), b = __ldcg(reinterpret_cast<const uint4 *>(w.is + i));
+        back += __popc(a.x & ~b.x) + __popc(a.y & ~b.y) + __popc(a.z & ~b.z) + __popc(a.w & ~b.w);
+    }
+    int at = block_scan(back, all, s_sum);
+    if (tid == 0) w.total[rank] = all;
+    cluster.sync();
+    int freed = 0;
+    for (int r = 0; r < ranks; ++r) {
+        const int x = __ldcg(w.total + r);
+        if (r < rank) at += x;
+        freed += x;
+    }
+    const long start = (long)cursor - freed;  // the list's place of the first page that goes back
+    const int status = bad || start < 0 ? GDN_ERR_SHAPE : start + copies > p.n_free ? GDN_ERR_CAPACITY : GDN_OK;
+    const bool ok = status == GDN_OK;
+    if (ok && back > 0)
+        for (long i = lo; i < hi; ++i)
+            if (__ldcg(w.was + i) && !__ldcg(w.is + i)) p.free_pages[start + at++] = (int)i;
+    cluster.sync();
+
+    // ---- the new rows
+    const bool same_table = p.table_out == p.block_table, same_lens = p.kv_lens_out == p.kv_lens;
+    if (ok || !same_table)
+        for (long e = t0; e < (long)p.B_out * M; e += step) {
+            const int i = (int)(e / M), j = (int)(e % M), parent = __ldg(p.parents + i);
+            const int n = !ok || parent < 0 ? 0 : (s_len[parent] + ps - 1) / ps;
+            int page = -1;
+            if (j < n) page = j == n - 1 && copies_last(i) ? __ldcg(p.free_pages + start + s_rank[i]) : __ldcg(w.old + (long)parent * M + j);
+            p.table_out[e] = page;
+        }
+    for (long i = t0; i < p.B_out; i += step) {
+        const int parent = __ldg(p.parents + i);
+        if (ok || !same_lens) p.kv_lens_out[i] = ok && parent >= 0 ? s_len[parent] : 0;
+        if (ok && copies_last((int)i))
+            reinterpret_cast<int2 *>(p.copies)[s_rank[i]] =
+                make_int2(__ldcg(w.old + (long)parent * M + s_len[parent] / ps), __ldcg(p.free_pages + start + s_rank[i]));
+    }
+    for (long i = (ok ? copies : 0) + t0; i < p.B_out; i += step) reinterpret_cast<int2 *>(p.copies)[i] = make_int2(-1, -1);
+    if (t0 == 0) {
+        *p.cursor_out = ok ? (int)(start + copies) : cursor;
+        *p.status = status;
+    }
+}
+
+struct CompactSpace {
+    int *total, *error, *below;  // [kCluster], [kCluster], [1]: live pages among the first `live`
+    uint8_t *is;                 // [num_pages]
+    int *list;                   // [num_pages] holes from the front, pages that fill them from the back
+    int *to;                     // [num_pages] where such a page goes
+};
+
+__global__ void __launch_bounds__(kThreads) page_compact_kernel(const PageCompact p, CompactSpace w) {
+    __shared__ int s_sum[32], s_bad;
+    const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+    const int tid = threadIdx.x, rank = blockIdx.x, ranks = gridDim.x, ps = p.page_size, M = p.max_pages;
+    const long t0 = (long)rank * kThreads + tid, step = (long)ranks * kThreads;
+    pdl_wait_primary();
+    for (long i = t0 * 16; i < p.num_pages; i += step * 16) *reinterpret_cast<uint4 *>(w.is + i) = make_uint4(0, 0, 0, 0);
+    if (tid == 0) s_bad = 0;
+    __syncthreads();
+    bool bad = false;
+    const auto used = [&](int b) {
+        const int len = __ldg(p.kv_lens + b);
+        return len < 0 || len > (long)M * ps ? -1 : (len + ps - 1) / ps;
+    };
+    for (long e = t0; e < (long)p.B * M; e += step) {
+        const int n = used((int)(e / M));
+        if (n < 0) bad = true;
+        if ((int)(e % M) < n) {
+            const int page = p.block_table[e];
+            bad |= page < 0 || page >= p.num_pages;
+        }
+    }
+    if (bad) s_bad = 1;
+    __syncthreads();
+    if (tid == 0) w.error[rank] = s_bad;
+    cluster.sync();
+    bad = false;
+    for (int r = 0; r < ranks; ++r) bad |= __ldcg(w.error + r) != 0;
+    if (!bad)
+        for (long e = t0; e < (long)p.B * M; e += step)
+            if ((int)(e % M) < used((int)(e / M))) w.is[p.block_table[e]] = 1;
+    cluster.sync();
+
+    long lo, hi;
+    share(p.num_pages, t0, step, lo, hi);
+    int mine = 0, all = 0;
+    for (long i = lo; i < hi; i += 16) {
+        const uint4 a = __ldcg(reinterpret_cast<const uint4 *>(w.is + i));
+        mine += __popc(a.x) + __popc(a.y) + __popc(a.z) + __popc(a.w);
+    }
+    int before = block_scan(mine, all, s_sum);  // live pages before lo
+    if (tid == 0) w.total[rank] = all;
+    cluster.sync();
+    int live = 0;
+    for (int r = 0; r < ranks; ++r) {
+        const int x = __ldcg(w.total + r);
+        if (r < rank) before += x;
+        live += x;
+    }
+    // holes among the first `live` pages by their rank from the front, the live ones behind them by their rank
+    // among all live ones from the back: with H holes, H <= num_pages - live, and those fill the last `live` places at
+    // most, so the two lists do not meet
+    if (!bad)
+        for (long i = lo; i < hi; ++i) {
+            const bool is = __ldcg(w.is + i) != 0;
+            if (i == live) *w.below = before;
+            if (i < live && !is) w.list[i - before] = (int)i;
+            if (i >= live && is) w.list[p.num_pages - 1 - before] = (int)i;
+            before += is;
+        }
+    cluster.sync();
+    const int below = bad ? 0 : live < p.num_pages ? __ldcg(w.below) : live, moved = bad ? 0 : live - below;
+    for (long i = t0; i < p.num_pages / 2; i += step) {
+        int2 pair = make_int2(-1, -1);
+        if (i < moved) {
+            pair = make_int2(__ldcg(w.list + p.num_pages - 1 - below - i), __ldcg(w.list + i));
+            w.to[pair.x] = pair.y;
+        }
+        reinterpret_cast<int2 *>(p.copies)[i] = pair;
+    }
+    cluster.sync();
+    const bool same = p.table_out == p.block_table;
+    if (!bad || !same)
+        for (long e = t0; e < (long)p.B * M; e += step) {
+            int page = -1;
+            if (!bad && (int)(e % M) < used((int)(e / M))) {
+                page = p.block_table[e];
+                if (page >= live) page = __ldcg(w.to + page);
+            }
+            p.table_out[e] = page;
+        }
+    if (!bad)
+        for (long i = t0; i < p.num_pages; i += step) p.free_pages[i] = (int)i;
+    if (t0 == 0) {
+        if (!bad) *p.cursor_out = live;
+        *p.status = bad ? GDN_ERR_SHAPE : GDN_OK;
+    }
+}
+
+constexpr int kCopyThreads = 256, kCopyBytes = kCopyThreads * 16 * 4;  // of a CTA's turn
+
+struct CopyParams {
+    PageCopy c;
+    int first[kPageMaxCaches + 1];  // first piece of each cache's page
+    int vec[kPageMaxCaches];
+};
+
+template <typename T>
+__device__ __forceinline__ void copy_piece(unsigned char *dst, const unsigned char *src, long bytes) {
+    constexpr int N = 4;
+    const long n = bytes / (long)sizeof(T);
+    for (long i0 = threadIdx.x; i0 < n; i0 += N * kCopyThreads) {
+        T x[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (i0 + k * kCopyThreads < n) x[k] = reinterpret_cast<const T *>(src)[i0 + k * kCopyThreads];
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (i0 + k * kCopyThreads < n) reinterpret_cast<T *>(dst)[i0 + k * kCopyThreads] = x[k];
+    }
+}
+
+// CTAs take (pair, piece) items in turn.  Lists may be mostly empty: the threads of a CTA look at the pairs of its next 256
+// items at once, and only those with something to copy are gone through.
+__global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const __grid_constant__ CopyParams p) {
+    __shared__ unsigned s_have[kCopyThreads / 32];
+    const int pieces = p.first[p.c.count], tid = threadIdx.x;
+    const long items = (long)p.c.n * pieces;
+    pdl_wait_primary();
+    const auto pair_of = [&](long item) { return __ldg(reinterpret_cast<const int2 *>(p.c.copies) + item / pieces); };
+    for (long first = blockIdx.x; first < items; first += (long)gridDim.x * kCopyThreads) {
+        const long mine = first + (long)tid * gridDim.x;
+        bool have = false;
+        if (mine < items) {
+            const int2 pair = pair_of(mine);
+            have = pair.x >= 0 && pair.x < p.c.num_pages && pair.y >= 0 && pair.y < p.c.num_pages && pair.x != pair.y;
+        }
+        const unsigned bits = __ballot_sync(0xffffffffu, have);
+        __syncthreads();  // the last items' words have been read
+        if ((tid & 31) == 0) s_have[tid >> 5] = bits;
+        __syncthreads();
+        for (int w = 0; w < kCopyThreads / 32; ++w)
+            for (unsigned left = s_have[w]; left != 0; left &= left - 1) {
+                const long item = first + (long)(w * 32 + __ffs(left) - 1) * gridDim.x;
+                const int2 pair = pair_of(item);
+                const int piece = (int)(item % pieces);
+                int t = 0;
+                while (piece >= p.first[t + 1]) ++t;
+                const long page = p.c.page_bytes[t], from = (long)(piece - p.first[t]) * kCopyBytes;
+                const long bytes = min((long)kCopyBytes, page - from);
+                unsigned char *base = static_cast<unsigned char *>(p.c.caches[t]) + from;
+                unsigned char *dst = base + pair.y * page;
+                const unsigned char *src = base + pair.x * page;
+                switch (p.vec[t]) {
+                case 16: copy_piece<uint4>(dst, src, bytes); break;
+                case 4: copy_piece<uint32_t>(dst, src, bytes); break;
+                default: copy_piece<uint8_t>(dst, src, bytes);
+                }
+            }
+    }
+}
+
+size_t round16(size_t x) { return (x + 15) & ~size_t(15); }
+
+template <typename K, typename P, typename W>
+cudaError_t launch_plan(K kernel, size_t smem, long work, const P &p, const W &w, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    const int ctas = work <= 2 * kThreads ? 1 : kCluster;
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p, w);
+    note_launch();
+    return e;
+}
+
+}  // namespace
+
+size_t page_fork_workspace(int B, int max_pages, int num_pages) {
+    return 64 + round16((size_t)B * max_pages * 4) + 2 * round16(num_pages);
+}
+
+cudaError_t launch_page_fork(const PageFork &p, void *ws, cudaStream_t s) {
+    ForkSpace w;
+    char *at = static_cast<char *>(ws);
+    w.total = reinterpret_cast<int *>(at), w.error = w.total + kCluster;
+    w.old = reinterpret_cast<int *>(at += 64);
+    w.was = reinterpret_cast<uint8_t *>(at += round16((size_t)p.B * p.max_pages * 4));
+    w.is = reinterpret_cast<uint8_t *>(at + round16(p.num_pages));
+    static std::atomic<uint64_t> attr_set{0};
+    const cudaError_t e = once_per_device(attr_set, [] {
+        return cudaFuncSetAttribute(page_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (3 * kPagePlanMaxB + 1) * 4);
+    });
+    if (e != cudaSuccess) return e;
+    const long work = std::max(std::max((long)p.B, (long)p.B_out) * p.max_pages, p.num_pages / 4L);
+    return launch_plan(page_fork_kernel, (2 * (size_t)p.B + p.B_out + 1) * 4, work, p, w, s);
+}
+
+size_t page_compact_workspace(int num_pages) { return 128 + round16(num_pages) + 8 * (size_t)num_pages; }
+
+cudaError_t launch_page_compact(const PageCompact &p, void *ws, cudaStream_t s) {
+    CompactSpace w;
+    char *at = static_cast<char *>(ws);
+    w.total = reinterpret_cast<int *>(at), w.error = w.total + kCluster, w.below = w.error + kCluster;
+    w.is = reinterpret_cast<uint8_t *>(at += 128);
+    w.list = reinterpret_cast<int *>(at += round16(p.num_pages));
+    w.to = w.list + p.num_pages;
+    return launch_plan(page_compact_kernel, 0, std::max((long)p.B * p.max_pages, p.num_pages / 4L), p, w, s);
+}
+
+cudaError_t launch_page_copy(const PageCopy &c, cudaStream_t s) {
+    CopyParams p{};
+    p.c = c;
+    for (int t = 0; t < c.count; ++t) {
+        p.first[t + 1] = p.first[t] + (int)((c.page_bytes[t] + kCopyBytes - 1) / kCopyBytes);
+        const uintptr_t at = (uintptr_t)c.caches[t] | (uintptr_t)c.page_bytes[t];
+        p.vec[t] = at % 16 == 0 ? 16 : at % 4 == 0 ? 4 : 1;
+    }
+    int dev = 0, sms = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const long grid = std::min((long)c.n * p.first[c.count], 8L * sms);
+    if (grid == 0) return cudaSuccess;
+    const cudaError_t e = launch_kernel(page_copy_kernel, dim3((unsigned)grid), dim3(kCopyThreads), 0, s, true, p);
+    note_launch();
+    return e;
+}
+
+}  // namespace gdn

@@ -1,6 +1,7 @@
 // serving.h - host-side interface of the kernels that serve softmax-attention
-// layers (page_plan.cu, qk_norm_rope.cu, attention_*.cu), called by
-// serving_api.cpp.  Not installed; the public ABI is include/gdn.h.
+// layers and beams (page_plan.cu, page_fork.cu, qk_norm_rope.cu, kv4_write.cu,
+// attention_*.cu, beam_select.cu, state_reorder.cu), called by serving_api.cpp
+// and beam_api.cpp.  Not installed; the public ABI is include/gdn.h.
 #pragma once
 
 #include "internal.h"
@@ -79,5 +80,76 @@ cudaError_t launch_attention_prompt(const Attn &a, int min_rows, cudaStream_t s)
 int attention_timeouts(cudaStream_t s, cudaError_t *e);
 // A kernel whose only wait gives up.
 cudaError_t launch_attention_wait_probe(int tries, cudaStream_t s);
+
+// ---------------------------------------------------------------- 4-bit cache (kv4.cuh)
+
+struct Kv4Write {
+    const void *k, *v;
+    long k_stride, v_stride;  // elements
+    const int32_t *slots;
+    const float *k_scale, *v_scale;
+    void *k_cache, *v_cache, *k_out, *v_out;
+    int N, HKV, D, page_size, num_pages;
+};
+cudaError_t launch_kv4_write(const Kv4Write &p, int dtype, cudaStream_t s);
+
+// Any rows; a.k and a.v are the 4-bit caches.
+size_t attention_kv4_workspace(int B, int N, int H, int HKV, int D, int max_q);
+cudaError_t launch_attention_kv4(const Attn &a, const float *k_scale, const float *v_scale, int dtype, void *ws,
+                                 cudaStream_t s);
+
+// ---------------------------------------------------------------- beams
+
+constexpr int kBeamMaxK = 128, kBeamMaxN = 128;  // beams of a group, selected of a group
+struct BeamSelect {
+    const void *logits;
+    long stride;  // elements
+    const float *scores;
+    const uint8_t *finished;
+    int end_token, keep_rows;
+    int32_t *tokens, *parents;
+    float *scores_out;
+    uint8_t *finished_out;
+    int G, K, V, n;
+};
+size_t beam_select_workspace(int G, int K, int V, int n);
+bool beam_select_fits(int G, int K, int V, int n);  // in the kernels' integers
+cudaError_t launch_beam_select(const BeamSelect &p, int dtype, void *ws, cudaStream_t s);
+
+constexpr int kStateMaxTensors = 64, kStateMaxRows = 4096;  // kernel parameters; 24 bytes a row in shared memory
+struct StateReorder {
+    void *states[kStateMaxTensors];
+    long row_bytes[kStateMaxTensors];
+    int count, B;
+    const int32_t *parents;
+};
+cudaError_t launch_state_reorder(const StateReorder &r, cudaStream_t s);
+
+struct PageFork {
+    const int32_t *parents, *kv_lens, *block_table;
+    int32_t *free_pages;
+    const int32_t *cursor;
+    int32_t *table_out, *kv_lens_out, *copies, *cursor_out, *status;
+    int B, B_out, page_size, max_pages, num_pages, n_free;
+};
+size_t page_fork_workspace(int B, int max_pages, int num_pages);
+cudaError_t launch_page_fork(const PageFork &p, void *ws, cudaStream_t s);
+
+struct PageCompact {
+    const int32_t *kv_lens, *block_table;
+    int32_t *table_out, *copies, *free_pages, *cursor_out, *status;
+    int B, page_size, max_pages, num_pages;
+};
+size_t page_compact_workspace(int num_pages);
+cudaError_t launch_page_compact(const PageCompact &p, void *ws, cudaStream_t s);
+
+constexpr int kPageMaxCaches = 128;
+struct PageCopy {
+    void *caches[kPageMaxCaches];
+    long page_bytes[kPageMaxCaches];
+    int count, n, num_pages;
+    const int32_t *copies;
+};
+cudaError_t launch_page_copy(const PageCopy &c, cudaStream_t s);
 
 }  // namespace gdn
