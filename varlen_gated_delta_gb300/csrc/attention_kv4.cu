@@ -32,6 +32,7 @@ struct Kv4Params {
     float c;       // |scale| log2(e)
     float sign;    // of scale
     int blocks;    // row blocks of the longest sequence
+    int min_rows, max_rows;  // sequences of more than min_rows and at most max_rows rows are ours
     int2 *spans;   // [B][blocks][HKV]: first and last CTA of a triple
     float *part;   // [2 * CTAs][ROWS * (3 + DP)]
 };
@@ -101,7 +102,8 @@ __device__ __forceinline__ int block_tiles(const Kv4Params &p, int rows, int key
 }
 // Row blocks of sequence b; 0: not ours.
 __device__ __forceinline__ int seq_blocks(const Kv4Params &p, int rows, int b, int &start, int &len, int &kv) {
-    if (b >= p.a.B || !attn_seq(p.a, b, start, len, kv) || len == 0) return 0;
+    if (b >= p.a.B || !attn_seq(p.a, b, start, len, kv)) return 0;
+    if ((long)len * p.G <= p.min_rows || (long)len * p.G > p.max_rows) return 0;
     return (int)(((long)len * p.G + rows - 1) / rows);
 }
 __device__ __forceinline__ long seq_tiles(const Kv4Params &p, int rows, int keys, int b) {
@@ -438,6 +440,384 @@ __global__ void __launch_bounds__(128) kv4_wide_kernel(const Kv4Params p) {
     }
 }
 
+// ---------------------------------------------------------------- up to 16 rows
+
+// Rows are the columns of the products, keys and channels their rows: S^T = K Q^T and O^T = V^T P^T with 16 keys or 16
+// channels to a tile, so that a cached value is converted into the registers of one product and no row
+// of it is wasted on the few queries (8 to a column tile, NT of those).  Both contractions run over things that
+// may be permuted: thread t of a quad takes the neighbouring channels [t DP/4, (t+1) DP/4) of its keys, group g of the warp the
+// channels [g DP/8, (g+1) DP/8) of V, so that codes come from shared memory in wide loads; two keys' codes are
+// interleaved by halves of bytes before they are converted, which pairs them as the second product needs.
+//
+// Every warp streams its own 32 of a tile's 128 keys through a ring of its own and waits for no other
+// warp before the end of a part.
+template <int DP, int NT, typename T>
+struct Narrow {
+    static constexpr int WARP_KEYS = 32, KEYS = 4 * WARP_KEYS, ROWS = 8 * NT, THREADS = 128, STAGES = 3;
+    static constexpr int Q = sizeof(T) == 4 ? 2 : 1;         // fp16 values to a query's
+    static constexpr int RAW = WARP_KEYS * DP / 16 * 9;      // bytes of a warp's tile of K (or V): codes, then scales
+    static constexpr int SMEM = 4 * STAGES * 2 * RAW + 64;   // (loads of channels past D may pass the end)
+    static constexpr int PART = ROWS * (3 + DP);
+    static constexpr int PER_SM = DP > 128 || NT * Q > 2 ? 2 : NT * Q > 1 ? 3 : 4;
+    static_assert(2 * RAW >= 8 * DP * 4, "a column tile's output fits a stage");
+};
+
+// The key of a block of 16 that is row m < 8 of the products' tiles (row m + 8: this one + 8).
+__device__ __forceinline__ int key_of_row(int m) { return m & 1 ? 4 + ((m >> 1) ^ 1) : m >> 1; }
+
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+// N words from shared memory that begin on a boundary of at least 8 bytes (WIDE: of their size).
+template <int N, bool WIDE>
+__device__ __forceinline__ void load_words(const unsigned char *at, uint32_t (&w)[N]) {
+    if constexpr (N == 1) {
+        w[0] = *reinterpret_cast<const uint32_t *>(at);
+    } else if constexpr (N == 2 || !WIDE) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const uint2 x = *reinterpret_cast<const uint2 *>(at + i * 4);
+            w[i] = x.x, w[i + 1] = x.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(at + i * 4);
+            w[i] = x.x, w[i + 1] = x.y, w[i + 2] = x.z, w[i + 3] = x.w;
+        }
+    }
+}
+// N bytes, in one load if their place allows (WIDE).
+template <int N, bool WIDE>
+__device__ __forceinline__ uint32_t load_bytes(const unsigned char *at) {
+    if constexpr (N == 1) return *at;
+    else if constexpr (WIDE && N == 2) return *reinterpret_cast<const uint16_t *>(at);
+    else if constexpr (WIDE) return *reinterpret_cast<const uint32_t *>(at);
+    else {
+        uint32_t x = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) x |= (uint32_t)at[i] << (8 * i);
+        return x;
+    }
+}
+
+template <int DP, int NT, typename T, bool FULL>
+__global__ void __launch_bounds__(128, Narrow<DP, NT, T>::PER_SM) kv4_narrow_kernel(const Kv4Params p) {
+    using C = Narrow<DP, NT, T>;
+    constexpr int KEYS = C::KEYS, STAGES = C::STAGES, QN = C::Q, RAW = C::RAW;
+    constexpr int KW = DP / 32, VW = DP / 64;  // words of a thread: of a key's channels, of a key's values
+    constexpr int VS = DP > 128 ? 2 : 1;       // scales of a key's values
+    constexpr int MT = DP / 16;                // tiles of channels, and steps of 16 channels
+    constexpr bool F32 = sizeof(T) == 4;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ float s_m[4][C::ROWS], s_l[4][C::ROWS];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+    unsigned char *ring = smem + warp * STAGES * 2 * RAW;
+    const uint32_t ring_at = sm100::smem_u32(ring);
+    const int D = FULL ? DP : p.a.D, GR = D / 16, G = p.G;
+    pdl_wait_primary();
+    pdl_launch_dependents();  // (the joining blocks wait for this grid's end)
+    long long u0, u1, U, ctas;
+    Cursor cur;
+    if (!find_run<C::THREADS>(p, C::ROWS, KEYS, u0, u1, U, ctas, cur)) return;
+    const long long cta = blockIdx.x;
+
+    // The blocks of 16 keys of this warp's part of a tile: pages looked up a tile ahead.
+    const long page_bytes = (long)p.a.page_size * GR * 9;
+    auto look_up = [&](const Cursor &x, int (&page)[2]) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int key = x.tile * KEYS + warp * C::WARP_KEYS + i * 16;
+            page[i] = key < x.kv ? __ldg(p.a.block_table + (size_t)x.b * p.a.max_pages + key / p.a.page_size) : -1;
+        }
+    };
+    auto fetch = [&](const Cursor &x, const int (&page)[2], int stage) {
+        const uint32_t dst = ring_at + stage * 2 * RAW;
+        const unsigned char *kc = static_cast<const unsigned char *>(p.a.k), *vc = static_cast<const unsigned char *>(p.a.v);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const bool read = page[i] >= 0 && page[i] < p.a.num_pages;
+            const int at = (x.tile * KEYS + warp * C::WARP_KEYS + i * 16) % p.a.page_size;
+            const long block = read ? ((long)page[i] * p.a.HKV + x.h) * page_bytes : 0;
+            const long codes = block + (read ? (long)at * GR * 8 : 0), scales = block + (read ? ((long)p.a.page_size * 8 + at) * GR : 0);
+#pragma unroll
+            for (int c = lane; c < GR * 8; c += 32) {
+                copy16(dst + (i * GR * 8 + c) * 16, kc + codes + (read ? c * 16 : 0), read);
+                copy16(dst + RAW + (i * GR * 8 + c) * 16, vc + codes + (read ? c * 16 : 0), read);
+            }
+            // lanes 0 to 15 bring K's scales, the others V's
+            const int c = lane & 15;
+            if (c < GR)
+                copy16(dst + (lane < 16 ? 0 : RAW) + (GR * 16 + i * GR + c) * 16, (lane < 16 ? kc : vc) + scales + (read ? c * 16 : 0), read);
+        }
+    };
+
+    Cursor ahead = cur;
+    long long u_ahead = u0;
+    int page[2] = {-1, -1};
+    look_up(ahead, page);
+    auto fetch_next = [&](int stage) {
+        if (u_ahead < u1) {
+            fetch(ahead, page, stage);
+            if (++u_ahead < u1) {
+                advance(p, C::ROWS, KEYS, ahead);
+                look_up(ahead, page);
+            }
+        }
+        copy_commit();
+    };
+#pragma unroll 1
+    for (int i = 0; i < STAGES - 1; ++i) fetch_next(i);
+
+    uint32_t q[QN][NT][MT][2];
+    float o[NT][MT][4], m[NT][2], l[NT][2], cr[NT][2];
+    int stage = 0, first_tile = 0;
+    bool fresh = true;  // the next tile begins a part
+#pragma unroll 1
+    for (long long u = u0; u < u1; ++u) {
+        const int n = cur.len, rows = n * G, shift = cur.kv - n;
+        if (fresh) {
+            fresh = false;
+            first_tile = cur.tile;
+            const float c = fmaxf(p.c * head_scale(p.ks, cur.h), 1e-18f);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int r = nt * 8 + g;
+                const T *src = static_cast<const T *>(p.a.q);
+                if (r < rows) src += (long)(cur.start + r / G) * p.a.qs + (long)(cur.h * G + r % G) * D;
+                float x[DP / 4], amax = 0.f;
+#pragma unroll
+                for (int i = 0; i < DP / 4; ++i) {
+                    const int d = t4 * (DP / 4) + i;
+                    x[i] = r < rows && (FULL || d < D) ? to_f32(src[d]) : 0.f;
+                    amax = fmaxf(amax, fabsf(x[i]));
+                }
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                float back;
+                const float power = row_power(amax, back) * p.sign;
+#pragma unroll
+                for (int i = 0; i < DP / 4; i += 2) {
+                    const float a = x[i] * power, b = x[i + 1] * power;
+                    const uint32_t hi = pack_f16(a, b);
+                    q[0][nt][i / 4][i / 2 % 2] = hi;
+                    if constexpr (F32) q[1][nt][i / 4][i / 2 % 2] = rest_f16(a, b, hi);
+                }
+                // this thread's columns are rows 2 t4 and 2 t4 + 1
+                cr[nt][0] = c * __shfl_sync(0xffffffffu, back, t4 * 8), cr[nt][1] = c * __shfl_sync(0xffffffffu, back, t4 * 8 + 4);
+                m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+                for (int i = 0; i < MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+            }
+        }
+        copy_wait<STAGES - 2>();
+        __syncwarp();  // the warp's keys are here, and it is done with the slot that is filled next
+        fetch_next(stage == 0 ? STAGES - 1 : stage - 1);
+
+        const int j0 = cur.tile * KEYS + warp * C::WARP_KEYS;
+        const unsigned char *kt = ring + stage * 2 * RAW, *vt = kt + RAW;
+        if (j0 < cur.kv) {
+            // ---- scores of 32 keys
+            float s[NT][2][4];
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) s[nt][kb][0] = s[nt][kb][1] = s[nt][kb][2] = s[nt][kb][3] = 0.f;
+                uint32_t w[2][KW], sc[2][DP / 64];
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int key = kb * 16 + y * 8 + key_of_row(g);
+                    load_words<KW, FULL>(kt + key * (D / 2) + t4 * (DP / 8), w[y]);
+                    const uint32_t b = load_bytes<DP / 64, FULL>(kt + C::WARP_KEYS * (D / 2) + key * GR + t4 * (DP / 64));
+#pragma unroll
+                    for (int i = 0; i < DP / 64; i += 2) {
+                        const uint32_t two = kv4_scales(i ? b >> 16 : b);
+                        sc[y][i] = __byte_perm(two, 0, 0x1010);
+                        if (i + 1 < DP / 64) sc[y][i + 1] = __byte_perm(two, 0, 0x3232);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < KW; ++i) {  // eight channels, two steps
+                    uint32_t lo[4], hi[4];
+                    kv4_codes(w[0][i], lo), kv4_codes(w[1][i], hi);
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const uint32_t a[4] = {mul_f16x2(lo[2 * y], sc[0][i / 2]), mul_f16x2(hi[2 * y], sc[1][i / 2]),
+                                               mul_f16x2(lo[2 * y + 1], sc[0][i / 2]), mul_f16x2(hi[2 * y + 1], sc[1][i / 2])};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int z = 0; z < QN; ++z) mma16816(s[nt][kb], a, q[z][nt][2 * i + y][0], q[z][nt][2 * i + y][1]);
+                    }
+                }
+            }
+            // ---- running softmax: this thread's rows 2 t4 and 2 t4 + 1, its keys of key_of_row(g)
+            const bool edge = j0 + C::WARP_KEYS > shift + 1;  // some row does not see all of these
+            uint32_t pt[QN][NT][2][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                if (edge)
+#pragma unroll
+                    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            const int key = j0 + kb * 16 + (z >> 1) * 8 + key_of_row(g), r = nt * 8 + t4 * 2 + (z & 1);
+                            if (key >= min(cur.kv, shift + r / G + 1)) s[nt][kb][z] = -INFINITY;
+                        }
+                float f[2], base[2];
+                bool moved = false;
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    float mx = fmaxf(fmaxf(s[nt][0][y], s[nt][0][y + 2]), fmaxf(s[nt][1][y], s[nt][1][y + 2]));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                    mx = fmaxf(fmaxf(mx, m[nt][y]), __shfl_xor_sync(0xffffffffu, mx, 16));
+                    // (a row that has seen nothing keeps l = o = 0 under any factor but NaN)
+                    f[y] = m[nt][y] == -INFINITY ? 1.f : exp2_fast((m[nt][y] - mx) * cr[nt][y]);
+                    moved |= mx > m[nt][y];
+                    m[nt][y] = mx;
+                    base[y] = mx == -INFINITY ? 0.f : mx;
+                }
+                if (__any_sync(0xffffffffu, moved)) {
+                    l[nt][0] *= f[0], l[nt][1] *= f[1];
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) o[nt][i][0] *= f[0], o[nt][i][1] *= f[1], o[nt][i][2] *= f[0], o[nt][i][3] *= f[1];
+                }
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        s[nt][kb][z] = exp2_fast(fmaf(s[nt][kb][z] - base[z & 1], cr[nt][z & 1], kShift));
+                        l[nt][z & 1] += s[nt][kb][z];
+                    }
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const float a = s[nt][kb][2 * y], b = s[nt][kb][2 * y + 1];
+                        const uint32_t hi = pack_f16(a, b);
+                        pt[0][nt][kb][y] = transposed(hi);
+                        if constexpr (F32) pt[1][nt][kb][y] = transposed(rest_f16(a, b, hi));
+                    }
+                }
+            }
+            // ---- O^T += V^T P^T
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                uint32_t w[4][VW], sc[2][VS];
+                const unsigned char *vs = vt + C::WARP_KEYS * (D / 2);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    uint32_t b[2];
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        const int key = kb * 16 + y * 8 + (z ? 4 + (t4 ^ 1) : t4);  // rows 2 t4 and 2 t4 + 1
+                        load_words<VW, FULL>(vt + key * (D / 2) + g * (DP / 16), w[2 * y + z]);
+                        b[z] = load_bytes<VS, FULL>(vs + key * GR + g * (DP / 8) / 16);
+                    }
+                    sc[y][0] = kv4_scales(__byte_perm(b[0], b[1], 0x0040));
+                    if constexpr (DP > 128) sc[y][1] = kv4_scales(__byte_perm(b[0], b[1], 0x0051));
+                }
+#pragma unroll
+                for (int i = 0; i < VW; ++i) {
+                    uint32_t even[2][4], odd[2][4];  // of two neighbouring keys, the channels of a word
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const uint32_t a = w[2 * y][i], b = w[2 * y + 1][i];
+                        kv4_codes((a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u), even[y]);
+                        kv4_codes(((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u), odd[y]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t s0 = sc[0][i / 2], s1 = sc[1][i / 2];
+                        const uint32_t a[4] = {mul_f16x2(even[0][j], s0), mul_f16x2(odd[0][j], s0), mul_f16x2(even[1][j], s1),
+                                               mul_f16x2(odd[1][j], s1)};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int z = 0; z < QN; ++z) mma16816(o[nt][4 * i + j], a, pt[z][nt][kb][0], pt[z][nt][kb][1]);
+                    }
+                }
+            }
+        }
+
+        const bool last = cur.tile + 1 == cur.tiles;
+        if (last || u + 1 == u1) {
+            // ---- the part ends: the warps' outputs meet in their stages, which are free now
+            fresh = true;
+            const bool whole = last && first_tile == 0;
+            if (last && tid == 0) {
+                const long long first = u - cur.tile;  // the triple's first tile
+                p.spans[span_of(p, cur)] = make_int2((int)(((first + 1) * ctas - 1) / U), (int)cta);
+            }
+            const float vs = head_scale(p.vs, cur.h);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) l[nt][y] += __shfl_xor_sync(0xffffffffu, l[nt][y], d);
+                    if (g == 0) s_m[warp][nt * 8 + t4 * 2 + y] = m[nt][y], s_l[warp][nt * 8 + t4 * 2 + y] = l[nt][y];
+                }
+            __syncthreads();
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float f[2];
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int r = nt * 8 + t4 * 2 + y;
+                    const float M = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
+                    float L = 0.f;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) L += s_m[w][r] == -INFINITY ? s_l[w][r] : s_l[w][r] * exp2_fast((s_m[w][r] - M) * cr[nt][y]);
+                    f[y] = m[nt][y] == -INFINITY ? 1.f : exp2_fast((m[nt][y] - M) * cr[nt][y]);
+                    m[nt][y] = M, l[nt][y] = L;
+                }
+                float *mine = reinterpret_cast<float *>(ring + stage * 2 * RAW);  // [8][DP]
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                        *reinterpret_cast<float2 *>(mine + (t4 * 2 + y) * DP + g * (DP / 8) + 2 * i) =
+                            make_float2(o[nt][i][y] * f[y], o[nt][i][y + 2] * f[y]);
+                __syncthreads();
+                // a warp to two rows
+                const float *all = reinterpret_cast<const float *>(smem + stage * 2 * RAW);
+                constexpr int NEXT = STAGES * 2 * RAW / 4;
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int row = warp * 2 + y, r = nt * 8 + row;
+                    if (r >= rows) continue;
+                    float M, L, c;  // from a thread that has this row's column
+                    {
+                        const int from = warp;  // (t4 of column 2 warp + y)
+                        M = __shfl_sync(0xffffffffu, m[nt][y], from), L = __shfl_sync(0xffffffffu, l[nt][y], from);
+                        c = __shfl_sync(0xffffffffu, cr[nt][y], from);
+                    }
+                    const float inv = L > 0.f ? vs / L : L;  // (0 gives 0, NaN stays)
+                    float *part = p.part + (2 * cta + (first_tile == 0)) * C::PART;
+                    T *out = static_cast<T *>(p.a.out) + ((size_t)(cur.start + r / G) * p.a.H + cur.h * G + r % G) * D;
+                    if (!whole && lane == 0) part[r] = M, part[C::ROWS + r] = L, part[2 * C::ROWS + r] = c;
+#pragma unroll
+                    for (int d = lane * 2; d < DP; d += 64) {
+                        float2 x = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const float2 v = *reinterpret_cast<const float2 *>(all + w * NEXT + row * DP + d);
+                            x.x += v.x, x.y += v.y;
+                        }
+                        if (!whole) *reinterpret_cast<float2 *>(part + 3 * C::ROWS + r * DP + d) = x;
+                        else if (FULL || d < D) store2(out + d, x.x * inv, x.y * inv);
+                    }
+                }
+                __syncthreads();  // read, before the next column tile's or the copies to come
+            }
+        }
+        stage = stage == STAGES - 1 ? 0 : stage + 1;
+        advance(p, C::ROWS, KEYS, cur);
+    }
+}
+
 // ---------------------------------------------------------------- parts
 
 // Joins the parts of each triple that several CTAs shared: a block to a (triple, row), its warps to every fourth part.
@@ -494,15 +874,13 @@ int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 size_t span_bytes(int B, int HKV, long blocks) { return ((size_t)B * blocks * HKV * 8 + 255) & ~size_t(255); }
 long row_blocks(int H, int HKV, int max_q, int rows) { return ((long)max_q * (H / HKV) + rows - 1) / rows; }
 
-template <int DP, typename T>
-cudaError_t launch_wide(Kv4Params p, void *ws, cudaStream_t s) {
-    using C = Wide<DP, T>;
-    static std::atomic<uint64_t> attr_set{0};
-    cudaError_t e = once_per_device(attr_set, [] {
-        return cudaFuncSetAttribute(kv4_wide_kernel<DP, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    });
-    if (e != cudaSuccess) return e;
+constexpr int kNarrowRows = 16;
+
+// A kernel over the sequences of its rows (C: its sizes), then the join of what several CTAs shared.
+template <int DP, typename T, typename C>
+cudaError_t launch_kernels(void (*kernel)(Kv4Params), int per_sm, Kv4Params p, void *ws, cudaStream_t s) {
     p.blocks = (int)row_blocks(p.a.H, p.a.HKV, p.a.max_q, C::ROWS);
+    if (C::ROWS <= kNarrowRows) p.blocks = 1;
     p.spans = static_cast<int2 *>(ws);
     p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + span_bytes(p.a.B, p.a.HKV, p.blocks));
     int dev = 0, sms = 0;
@@ -511,9 +889,8 @@ cudaError_t launch_wide(Kv4Params p, void *ws, cudaStream_t s) {
     const long triples = (long)p.a.B * p.blocks * p.a.HKV;
     if (triples > INT32_MAX) return cudaErrorInvalidConfiguration;
     const long most = triples * (((long)p.a.max_pages * p.a.page_size + C::KEYS - 1) / C::KEYS);
-    const long per_sm = std::max(1, 220 * 1024 / (C::SMEM + 1024));
-    const long grid = std::min(std::min(per_sm * sms, (long)kMaxCtas), most);
-    e = launch_kernel(kv4_wide_kernel<DP, T>, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, s, true, p);
+    const long grid = std::min(std::min((long)per_sm * sms, (long)kMaxCtas), most);
+    cudaError_t e = launch_kernel(kernel, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, s, true, p);
     note_launch();
     if (e != cudaSuccess) return e;
     const long rows = std::min((long)p.a.max_q * p.G, (long)C::ROWS);
@@ -522,12 +899,53 @@ cudaError_t launch_wide(Kv4Params p, void *ws, cudaStream_t s) {
     return e;
 }
 
+template <int DP, typename T>
+cudaError_t launch_wide(Kv4Params p, int min_rows, void *ws, cudaStream_t s) {
+    using C = Wide<DP, T>;
+    static std::atomic<uint64_t> attr_set{0};
+    const cudaError_t e = once_per_device(attr_set, [] {
+        return cudaFuncSetAttribute(kv4_wide_kernel<DP, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    });
+    if (e != cudaSuccess) return e;
+    p.min_rows = min_rows, p.max_rows = INT32_MAX;
+    return launch_kernels<DP, T, C>(kv4_wide_kernel<DP, T>, std::max(1, 220 * 1024 / (C::SMEM + 1024)), p, ws, s);
+}
+
+template <int DP, int NT, typename T, bool FULL>
+cudaError_t launch_narrow(Kv4Params p, void *ws, cudaStream_t s) {
+    using C = Narrow<DP, NT, T>;
+    static std::atomic<uint64_t> attr_set{0};
+    const cudaError_t e = once_per_device(attr_set, [] {
+        return cudaFuncSetAttribute(kv4_narrow_kernel<DP, NT, T, FULL>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    });
+    if (e != cudaSuccess) return e;
+    p.min_rows = 0, p.max_rows = kNarrowRows < C::ROWS ? kNarrowRows : C::ROWS;
+    return launch_kernels<DP, T, C>(kv4_narrow_kernel<DP, NT, T, FULL>, C::PER_SM, p, ws, s);
+}
+
+template <int DP, typename T>
+cudaError_t launch_rows(const Kv4Params &p, void *ws, cudaStream_t s) {
+    const long rows = (long)p.a.max_q * p.G;
+    const bool full = p.a.D == DP;
+    int narrow = 0;  // sequences of up to so many rows are done
+    cudaError_t e = cudaSuccess;
+    if (rows <= 8 || (rows > kNarrowRows && p.G <= 8)) {
+        narrow = 8;
+        e = full ? launch_narrow<DP, 1, T, true>(p, ws, s) : launch_narrow<DP, 1, T, false>(p, ws, s);
+    } else if (p.G <= 16) {
+        narrow = 16;
+        e = full ? launch_narrow<DP, 2, T, true>(p, ws, s) : launch_narrow<DP, 2, T, false>(p, ws, s);
+    }
+    if (e != cudaSuccess || rows <= narrow) return e;
+    return launch_wide<DP, T>(p, narrow, ws, s);
+}
+
 template <typename T>
 cudaError_t launch(const Kv4Params &p, void *ws, cudaStream_t s) {
     switch (padded(p.a.D)) {
-    case 64: return launch_wide<64, T>(p, ws, s);
-    case 128: return launch_wide<128, T>(p, ws, s);
-    default: return launch_wide<256, T>(p, ws, s);
+    case 64: return launch_rows<64, T>(p, ws, s);
+    case 128: return launch_rows<128, T>(p, ws, s);
+    default: return launch_rows<256, T>(p, ws, s);
     }
 }
 
