@@ -32,6 +32,7 @@ struct Kv4Params {
     float c;       // |scale| log2(e)
     float sign;    // of scale
     int blocks;    // row blocks of the longest sequence
+    int page_shift;  // log2 of page_size, or -1
     int min_rows, max_rows;  // sequences of more than min_rows and at most max_rows rows are ours
     int2 *spans;   // [B][blocks][HKV]: first and last CTA of a triple
     float *part;   // [2 * CTAs][ROWS * (3 + DP)]
@@ -449,16 +450,17 @@ __global__ void __launch_bounds__(128) kv4_wide_kernel(const Kv4Params p) {
 // channels [g DP/8, (g+1) DP/8) of V, so that codes come from shared memory in wide loads; two keys' codes are
 // interleaved by halves of bytes before they are converted, which pairs them as the second product needs.
 //
-// Every warp streams its own 32 of a tile's 128 keys through a ring of its own and waits for no other
+// Every warp streams its own quarter of a tile's keys through two stages of its own and waits for no other
 // warp before the end of a part.
 template <int DP, int NT, typename T>
 struct Narrow {
-    static constexpr int WARP_KEYS = 32, KEYS = 4 * WARP_KEYS, ROWS = 8 * NT, THREADS = 128, STAGES = 3;
+    static constexpr int WARP_KEYS = DP > 128 ? 32 : 64, KEYS = 4 * WARP_KEYS, ROWS = 8 * NT, THREADS = 128, STAGES = 2;
+    static constexpr int KB = WARP_KEYS / 16;                // blocks of 16 keys
     static constexpr int Q = sizeof(T) == 4 ? 2 : 1;         // fp16 values to a query's
     static constexpr int RAW = WARP_KEYS * DP / 16 * 9;      // bytes of a warp's tile of K (or V): codes, then scales
     static constexpr int SMEM = 4 * STAGES * 2 * RAW + 64;   // (loads of channels past D may pass the end)
     static constexpr int PART = ROWS * (3 + DP);
-    static constexpr int PER_SM = DP > 128 || NT * Q > 2 ? 2 : NT * Q > 1 ? 3 : 4;
+    static constexpr int PER_SM = DP > 128 || NT * Q > 1 ? 2 : DP > 64 ? 3 : 4;
     static_assert(2 * RAW >= 8 * DP * 4, "a column tile's output fits a stage");
 };
 
@@ -525,58 +527,69 @@ __global__ void __launch_bounds__(128, Narrow<DP, NT, T>::PER_SM) kv4_narrow_ker
     const long long cta = blockIdx.x;
 
     // The blocks of 16 keys of this warp's part of a tile: pages looked up a tile ahead.
-    const long page_bytes = (long)p.a.page_size * GR * 9;
-    auto look_up = [&](const Cursor &x, int (&page)[2]) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int key = x.tile * KEYS + warp * C::WARP_KEYS + i * 16;
-            page[i] = key < x.kv ? __ldg(p.a.block_table + (size_t)x.b * p.a.max_pages + key / p.a.page_size) : -1;
-        }
+    const int ps = p.a.page_size;
+    const long page_bytes = (long)ps * GR * 9;
+    const unsigned char *kc = static_cast<const unsigned char *>(p.a.k), *vc = static_cast<const unsigned char *>(p.a.v);
+    auto split = [&](int key, int &index, int &at) {
+        if (p.page_shift >= 0) index = key >> p.page_shift, at = key & (ps - 1);
+        else index = key / ps, at = key - index * ps;
     };
-    auto fetch = [&](const Cursor &x, const int (&page)[2], int stage) {
-        const uint32_t dst = ring_at + stage * 2 * RAW;
-        const unsigned char *kc = static_cast<const unsigned char *>(p.a.k), *vc = static_cast<const unsigned char *>(p.a.v);
+    // (pages of several blocks of 16 keys are looked up by lane: lane i holds that of block i)
+    auto look_up = [&](const Cursor &x) {
+        const int key = x.tile * KEYS + warp * C::WARP_KEYS + (lane & (C::KB - 1)) * 16;
+        int index, at;
+        split(key, index, at);
+        return key < x.kv ? __ldg(p.a.block_table + (size_t)x.b * p.a.max_pages + index) : -1;
+    };
+    auto fetch = [&](const Cursor &x, int pages, int stage) {
+        const uint32_t dst = ring_at + stage * 2 * RAW + lane * 16;
+        const long between = vc - kc;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const bool read = page[i] >= 0 && page[i] < p.a.num_pages;
-            const int at = (x.tile * KEYS + warp * C::WARP_KEYS + i * 16) % p.a.page_size;
-            const long block = read ? ((long)page[i] * p.a.HKV + x.h) * page_bytes : 0;
-            const long codes = block + (read ? (long)at * GR * 8 : 0), scales = block + (read ? ((long)p.a.page_size * 8 + at) * GR : 0);
+        for (int i = 0; i < C::KB; ++i) {
+            const int page = __shfl_sync(0xffffffffu, pages, i);
+            const bool read = page >= 0 && page < p.a.num_pages;
+            int index, at;
+            split(x.tile * KEYS + warp * C::WARP_KEYS + i * 16, index, at);
+            // (nothing is read without a page; the addresses then lie in the cache's first block)
+            const unsigned char *block = kc;
+            if (read) block += ((long)page * p.a.HKV + x.h) * page_bytes;
+            else at = 0;
+            const unsigned char *codes = block + (at * GR * 8 + lane * 16);
 #pragma unroll
-            for (int c = lane; c < GR * 8; c += 32) {
-                copy16(dst + (i * GR * 8 + c) * 16, kc + codes + (read ? c * 16 : 0), read);
-                copy16(dst + RAW + (i * GR * 8 + c) * 16, vc + codes + (read ? c * 16 : 0), read);
-            }
+            for (int c = 0; c < (FULL ? DP / 2 : 128); c += 32)
+                if (FULL || c + lane < GR * 8) {
+                    copy16(dst + (i * GR * 8 + c) * 16, codes + c * 16, read);
+                    copy16(dst + RAW + (i * GR * 8 + c) * 16, codes + between + c * 16, read);
+                }
             // lanes 0 to 15 bring K's scales, the others V's
-            const int c = lane & 15;
-            if (c < GR)
-                copy16(dst + (lane < 16 ? 0 : RAW) + (GR * 16 + i * GR + c) * 16, (lane < 16 ? kc : vc) + scales + (read ? c * 16 : 0), read);
+            if ((lane & 15) < GR)
+                copy16(dst + (lane < 16 ? 0 : RAW - 256) + (C::KB * GR * 8 + i * GR) * 16,
+                       block + (lane < 16 ? 0 : between) + ((ps * 8 + at) * GR + (lane & 15) * 16), read);
         }
     };
 
     Cursor ahead = cur;
-    long long u_ahead = u0;
-    int page[2] = {-1, -1};
-    look_up(ahead, page);
+    int n_ahead = (int)min(u1 - u0, (long long)INT32_MAX), n_left = n_ahead;  // tiles to fetch, tiles to go
+    int pages = look_up(ahead);
     auto fetch_next = [&](int stage) {
-        if (u_ahead < u1) {
-            fetch(ahead, page, stage);
-            if (++u_ahead < u1) {
+        if (n_ahead > 0) {
+            fetch(ahead, pages, stage);
+            if (--n_ahead > 0) {
                 advance(p, C::ROWS, KEYS, ahead);
-                look_up(ahead, page);
+                pages = look_up(ahead);
             }
         }
         copy_commit();
     };
 #pragma unroll 1
-    for (int i = 0; i < STAGES - 1; ++i) fetch_next(i);
+    for (int i = 0; i < STAGES; ++i) fetch_next(i);
 
     uint32_t q[QN][NT][MT][2];
     float o[NT][MT][4], m[NT][2], l[NT][2], cr[NT][2];
     int stage = 0, first_tile = 0;
     bool fresh = true;  // the next tile begins a part
 #pragma unroll 1
-    for (long long u = u0; u < u1; ++u) {
+    for (; n_left > 0; --n_left) {
         const int n = cur.len, rows = n * G, shift = cur.kv - n;
         if (fresh) {
             fresh = false;
@@ -612,17 +625,16 @@ __global__ void __launch_bounds__(128, Narrow<DP, NT, T>::PER_SM) kv4_narrow_ker
                 for (int i = 0; i < MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
             }
         }
-        copy_wait<STAGES - 2>();
-        __syncwarp();  // the warp's keys are here, and it is done with the slot that is filled next
-        fetch_next(stage == 0 ? STAGES - 1 : stage - 1);
+        copy_wait<STAGES - 1>();
+        __syncwarp();  // the warp's keys are here
 
         const int j0 = cur.tile * KEYS + warp * C::WARP_KEYS;
         const unsigned char *kt = ring + stage * 2 * RAW, *vt = kt + RAW;
         if (j0 < cur.kv) {
-            // ---- scores of 32 keys
-            float s[NT][2][4];
+            // ---- scores
+            float s[NT][C::KB][4];
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
+            for (int kb = 0; kb < C::KB; ++kb) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) s[nt][kb][0] = s[nt][kb][1] = s[nt][kb][2] = s[nt][kb][3] = 0.f;
                 uint32_t w[2][KW], sc[2][DP / 64];
@@ -655,12 +667,12 @@ __global__ void __launch_bounds__(128, Narrow<DP, NT, T>::PER_SM) kv4_narrow_ker
             }
             // ---- running softmax: this thread's rows 2 t4 and 2 t4 + 1, its keys of key_of_row(g)
             const bool edge = j0 + C::WARP_KEYS > shift + 1;  // some row does not see all of these
-            uint32_t pt[QN][NT][2][2];
+            uint32_t pt[QN][NT][C::KB][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 if (edge)
 #pragma unroll
-                    for (int kb = 0; kb < 2; ++kb)
+                    for (int kb = 0; kb < C::KB; ++kb)
 #pragma unroll
                         for (int z = 0; z < 4; ++z) {
                             const int key = j0 + kb * 16 + (z >> 1) * 8 + key_of_row(g), r = nt * 8 + t4 * 2 + (z & 1);
@@ -670,7 +682,9 @@ __global__ void __launch_bounds__(128, Narrow<DP, NT, T>::PER_SM) kv4_narrow_ker
                 bool moved = false;
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    float mx = fmaxf(fmaxf(s[nt][0][y], s[nt][0][y + 2]), fmaxf(s[nt][1][y], s[nt][1][y + 2]));
+                    float mx = fmaxf(s[nt][0][y], s[nt][0][y + 2]);
+#pragma unroll
+                    for (int kb = 1; kb < C::KB; ++kb) mx = fmaxf(mx, fmaxf(s[nt][kb][y], s[nt][kb][y + 2]));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                     mx = fmaxf(fmaxf(mx, m[nt][y]), __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -686,7 +700,7 @@ __global__ void __launch_bounds__(128, Narrow<DP, NT, T>::PER_SM) kv4_narrow_ker
                     for (int i = 0; i < MT; ++i) o[nt][i][0] *= f[0], o[nt][i][1] *= f[1], o[nt][i][2] *= f[0], o[nt][i][3] *= f[1];
                 }
 #pragma unroll
-                for (int kb = 0; kb < 2; ++kb) {
+                for (int kb = 0; kb < C::KB; ++kb) {
 #pragma unroll
                     for (int z = 0; z < 4; ++z) {
                         s[nt][kb][z] = exp2_fast(fmaf(s[nt][kb][z] - base[z & 1], cr[nt][z & 1], kShift));
@@ -703,7 +717,7 @@ __global__ void __launch_bounds__(128, Narrow<DP, NT, T>::PER_SM) kv4_narrow_ker
             }
             // ---- O^T += V^T P^T
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
+            for (int kb = 0; kb < C::KB; ++kb) {
                 uint32_t w[4][VW], sc[2][VS];
                 const unsigned char *vs = vt + C::WARP_KEYS * (D / 2);
 #pragma unroll
@@ -742,12 +756,12 @@ __global__ void __launch_bounds__(128, Narrow<DP, NT, T>::PER_SM) kv4_narrow_ker
         }
 
         const bool last = cur.tile + 1 == cur.tiles;
-        if (last || u + 1 == u1) {
+        if (last || n_left == 1) {
             // ---- the part ends: the warps' outputs meet in their stages, which are free now
             fresh = true;
             const bool whole = last && first_tile == 0;
             if (last && tid == 0) {
-                const long long first = u - cur.tile;  // the triple's first tile
+                const long long first = u1 - n_left - cur.tile;  // the triple's first tile
                 p.spans[span_of(p, cur)] = make_int2((int)(((first + 1) * ctas - 1) / U), (int)cta);
             }
             const float vs = head_scale(p.vs, cur.h);
@@ -813,59 +827,92 @@ __global__ void __launch_bounds__(128, Narrow<DP, NT, T>::PER_SM) kv4_narrow_ker
                 __syncthreads();  // read, before the next column tile's or the copies to come
             }
         }
-        stage = stage == STAGES - 1 ? 0 : stage + 1;
+        __syncwarp();  // the warp is done with this stage
+        fetch_next(stage);
+        stage ^= 1;
         advance(p, C::ROWS, KEYS, cur);
     }
 }
 
 // ---------------------------------------------------------------- parts
 
-// Joins the parts of each triple that several CTAs shared: a block to a (triple, row), its warps to every fourth part.
-template <int DP, typename T>
-__global__ void __launch_bounds__(128) kv4_join_kernel(const Kv4Params p, int rows, int keys) {
-    constexpr int E = DP / 32;  // channels of a lane
-    __shared__ float s_m[4], s_l[4], s_o[4][DP];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.y;
+// Joins the parts of each triple that several CTAs shared: a block to a (triple, row), or to several of a triple's rows.  A
+// warp goes by every kJoinWarps-th part with a running maximum of its own, so that nothing but the span is waited for
+// before the parts are loaded.
+template <int DP, typename T, int kJoinWarps>
+__global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const Kv4Params p, int rows) {
+    constexpr int E = DP / 32, N = 4;  // channels of a lane, parts loaded at a time
+    __shared__ float s_m[kJoinWarps], s_l[kJoinWarps], s_o[kJoinWarps][DP];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int h = blockIdx.x % p.a.HKV, block = blockIdx.x / p.a.HKV % p.blocks, b = blockIdx.x / p.a.HKV / p.blocks;
     pdl_wait_primary();
     int start, len, kv;
     if (block >= seq_blocks(p, rows, b, start, len, kv)) return;
-    const long row = (long)block * rows + r;
-    if (row >= (long)len * p.G) return;
     const int2 span = p.spans[blockIdx.x];
     if (span.x == span.y) return;
     const int PART = rows * (3 + DP);
     auto part = [&](int c) { return p.part + (2L * c + (c == span.x)) * PART; };
-    float M = -INFINITY;
-    for (int c = span.x + tid; c <= span.y; c += 128) M = fmaxf(M, part(c)[r]);
+    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+        const long row = (long)block * rows + r;
+        if (row >= (long)len * p.G) return;
+        const float c_row = part(span.x)[2 * rows + r];
+        float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-    if (lane == 0) s_m[warp] = M;
-    __syncthreads();
-    M = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-    float L = 0.f, o[E];
+        for (int i = 0; i < E; ++i) o[i] = 0.f;
+        for (int c0 = span.x + warp; c0 <= span.y; c0 += N * kJoinWarps) {
+            float pm[N], pl[N];
+            float2 po[N][E / 2];
 #pragma unroll
-    for (int i = 0; i < E; ++i) o[i] = 0.f;
-#pragma unroll 4
-    for (int c = span.x + warp; c <= span.y; c += 4) {
-        const float *x = part(c);
-        const float mc = x[r], f = mc == -INFINITY ? 0.f : exp2_fast((mc - M) * x[2 * rows + r]);
-        L += f * x[rows + r];
-        x += 3 * rows + r * DP + lane * E;
+            for (int k = 0; k < N; ++k) {
+                const bool real = c0 + k * kJoinWarps <= span.y;
+                const float *x = part(real ? c0 + k * kJoinWarps : c0);
+                pm[k] = real ? x[r] : -INFINITY, pl[k] = x[rows + r];
+                x += 3 * rows + r * DP + lane * E;
 #pragma unroll
-        for (int i = 0; i < E; i += 2) {
-            const float2 y = *reinterpret_cast<const float2 *>(x + i);
-            o[i] += f * y.x, o[i + 1] += f * y.y;
+                for (int i = 0; i < E / 2; ++i) po[k][i] = reinterpret_cast<const float2 *>(x)[i];
+            }
+            float M = m;
+#pragma unroll
+            for (int k = 0; k < N; ++k) M = fmaxf(M, pm[k]);
+            const float f = m == -INFINITY ? 0.f : exp2_fast((m - M) * c_row);
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < E; ++i) o[i] *= f;
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                // (a part that saw no key has l = o = 0; NaN, of a row whose query is not finite, has m = -inf too)
+                const bool real = c0 + k * kJoinWarps <= span.y;
+                const float w = pm[k] == -INFINITY ? (real && pl[k] != 0.f ? 1.f : 0.f) : exp2_fast((pm[k] - M) * c_row);
+                l = fmaf(w, pl[k], l);
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i)
+                    o[2 * i] = fmaf(w, po[k][i].x, o[2 * i]), o[2 * i + 1] = fmaf(w, po[k][i].y, o[2 * i + 1]);
+            }
+            m = M;
         }
-    }
+        if (lane == 0) s_m[warp] = m;
+        __syncthreads();
+        float M = s_m[0];
 #pragma unroll
-    for (int i = 0; i < E; ++i) s_o[warp][lane * E + i] = o[i];
-    if (lane == 0) s_l[warp] = L;
-    __syncthreads();
-    L = s_l[0] + s_l[1] + s_l[2] + s_l[3];
-    const float inv = L > 0.f ? head_scale(p.vs, h) / L : L;  // (0 gives 0, NaN stays)
-    T *out = static_cast<T *>(p.a.out) + ((size_t)(start + row / p.G) * p.a.H + h * p.G + row % p.G) * p.a.D;
-    for (int d = tid; d < p.a.D; d += 128) out[d] = from_f32<T>((s_o[0][d] + s_o[1][d] + s_o[2][d] + s_o[3][d]) * inv);
+        for (int w = 1; w < kJoinWarps; ++w) M = fmaxf(M, s_m[w]);
+        const float f = m == -INFINITY ? (l != 0.f ? 1.f : 0.f) : exp2_fast((m - M) * c_row);
+#pragma unroll
+        for (int i = 0; i < E; ++i) s_o[warp][lane * E + i] = o[i] * f;
+        if (lane == 0) s_l[warp] = l * f;
+        __syncthreads();
+        float L = 0.f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) L += s_l[w];
+        const float inv = L > 0.f ? head_scale(p.vs, h) / L : L;  // (0 gives 0, NaN stays)
+        T *out = static_cast<T *>(p.a.out) + ((size_t)(start + row / p.G) * p.a.H + h * p.G + row % p.G) * p.a.D;
+        for (int d = tid; d < p.a.D; d += kJoinWarps * 32) {
+            float x = 0.f;
+#pragma unroll
+            for (int w = 0; w < kJoinWarps; ++w) x += s_o[w][d];
+            out[d] = from_f32<T>(x * inv);
+        }
+        __syncthreads();  // the sums have been read
+    }
 }
 
 // ---------------------------------------------------------------- host
@@ -893,8 +940,12 @@ cudaError_t launch_kernels(void (*kernel)(Kv4Params), int per_sm, Kv4Params p, v
     cudaError_t e = launch_kernel(kernel, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, s, true, p);
     note_launch();
     if (e != cudaSuccess) return e;
+    // Few triples have many parts each, many have few: then fewer warps, and with many blocks several rows to each (most
+    // of them have nothing to join, and leaving takes its time too).
     const long rows = std::min((long)p.a.max_q * p.G, (long)C::ROWS);
-    e = launch_kernel(kv4_join_kernel<DP, T>, dim3((unsigned)triples, (unsigned)rows), dim3(128), 0, s, true, p, C::ROWS, C::KEYS);
+    const dim3 blocks((unsigned)triples, (unsigned)std::min(rows, std::max(1L, 4096 / triples)));
+    e = triples * 2 <= sms ? launch_kernel(kv4_join_kernel<DP, T, 8>, blocks, dim3(256), 0, s, true, p, C::ROWS)
+                           : launch_kernel(kv4_join_kernel<DP, T, 4>, blocks, dim3(128), 0, s, true, p, C::ROWS);
     note_launch();
     return e;
 }
@@ -962,6 +1013,9 @@ cudaError_t launch_attention_kv4(const Attn &a, const float *k_scale, const floa
     p.G = a.H / a.HKV;
     p.c = std::fabs(a.scale) * kLog2e;
     p.sign = a.scale < 0.f ? -1.f : 1.f;
+    p.page_shift = -1;
+    for (int i = 0; i < 31; ++i)
+        if (a.page_size == 1 << i) p.page_shift = i;
     return dtype == GDN_BF16 ? launch<__nv_bfloat16>(p, ws, s) : launch<float>(p, ws, s);
 }
 

@@ -5,8 +5,8 @@
 // launches.
 //
 // The first cuts every row into pieces, one CTA each, held in registers: the piece's maximum m and sum of
-// exp(x - m), and its n largest logits.  For these, the CTA's threads form at least n groups whose maxima are at
-// hand: at least n values reach the least of them, and few more do (8 groups: some 22 of 8192 values), so
+// exp(x - m), and its n largest logits.  For these, the CTA's threads form groups whose maxima are at hand: at
+// least n values reach the n-th largest of them, and few more do (n = 8 of 32 groups: some 9 of 8192 values), so
 // those go into a list and are ranked by counting.  A list that overflows (many equal logits) is left for n
 // rounds of the CTA-wide largest value below the last one.
 //
@@ -24,6 +24,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kList = 1024;  // candidates that are ranked by counting
+constexpr int kNear = 4096;  // candidates of a group whose totals are kept in shared memory
 
 struct Pieces {  // in the workspace
     float *m;    // [rows][pieces]: maximum
@@ -35,9 +36,15 @@ struct Pieces {  // in the workspace
 // A value in the order of its bits as an unsigned number, and the position behind it: of equal values the
 // lowest position is the largest key.
 __device__ __forceinline__ unsigned long long key_of(float x, int at) {
-    const uint32_t b = __float_as_uint(x);
+    const uint32_t b = __float_as_uint(x + 0.f);  // (no negative zeros)
     return (unsigned long long)(b & 0x80000000u ? ~b : b | 0x80000000u) << 32 | (0xffffffffu - (uint32_t)at);
 }
+// The same for 64 bits, and back.  Keys are compared as whole numbers: the 64-bit pipe takes two lanes a clock.
+__device__ __forceinline__ unsigned long long key_of(double x) {
+    const unsigned long long b = __double_as_longlong(x + 0.0);
+    return b >> 63 ? ~b : b | 1ull << 63;
+}
+__device__ __forceinline__ double of_key(unsigned long long k) { return __longlong_as_double(k >> 63 ? k & ~(1ull << 63) : ~k); }
 
 template <typename T>
 __device__ __forceinline__ T warp_max(T x) {
@@ -49,39 +56,59 @@ __device__ __forceinline__ T warp_max(T x) {
     return x;
 }
 
-// The least of the maxima of `groups` (8, 32, 128 or 256) equal sets of neighbouring threads.
-template <typename T>
-__device__ __forceinline__ T least_of_maxima(T x, int groups, T *s_warp, T most) {
-    const int width = kThreads / groups;
+// A sum held in two values: x + y = hi + lo exactly, added to lo.
+__device__ __forceinline__ void add_two(float &hi, float &lo, float y, float y_lo) {
+    const float s = __fadd_rn(hi, y), back = __fsub_rn(s, hi);
+    lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(s, back)), __fsub_rn(y, back)) + y_lo;
+    hi = s;
+}
+__device__ __forceinline__ void warp_sum_two(float &hi, float &lo) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
-        const T y = __shfl_xor_sync(0xffffffffu, x, d);
-        if (d < width && y > x) x = y;
+        const float y = __shfl_xor_sync(0xffffffffu, hi, d), y_lo = __shfl_xor_sync(0xffffffffu, lo, d);
+        add_two(hi, lo, y, y_lo);
     }
-    // (the least over the warp's groups)
-    T least = x;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        const T y = __shfl_xor_sync(0xffffffffu, least, d);
-        if (y < least) least = y;
-    }
-    if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = least;
-    __syncthreads();
-    least = most;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) least = s_warp[w] < least ? s_warp[w] : least;
-    return least;
 }
 
-__device__ __forceinline__ int groups_for(int n) { return n <= 8 ? 8 : n <= 32 ? 32 : n <= 128 ? 128 : 256; }
+// The n-th largest (any of them, if there are fewer) of the maxima of `groups` (32 or 256) equal sets of neighbouring
+// threads.  Calls have a barrier between them.
+__device__ __forceinline__ float nth_maximum(float x, int n, int groups, float *s_all, float *s_warp) {
+    const int tid = threadIdx.x;
+    if (groups == 32) {
+#pragma unroll
+        for (int d = 4; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+        if (tid % 8 == 0) s_all[tid / 8] = x;
+        __syncthreads();
+        x = s_all[tid & 31];
+    } else {
+        s_all[tid] = x;
+        __syncthreads();
+    }
+    int larger = 0;
+#pragma unroll 8
+    for (int i = 0; i < groups; i += 4) {
+        const float4 y = *reinterpret_cast<const float4 *>(s_all + i);
+        larger += (y.x > x) + (y.y > x) + (y.z > x) + (y.w > x);
+    }
+    x = larger < n ? x : INFINITY;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) x = fminf(x, __shfl_xor_sync(0xffffffffu, x, d));
+    if (groups == 32) return x;
+    if ((tid & 31) == 0) s_warp[tid >> 5] = x;
+    __syncthreads();
+    x = s_warp[0];
+#pragma unroll
+    for (int w = 1; w < kThreads / 32; ++w) x = fminf(x, s_warp[w]);
+    return x;
+}
 
 template <typename T, int ELEMS>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
     beam_pieces_kernel(const T *__restrict__ logits, long stride, const uint8_t *__restrict__ finished, Pieces out, int V,
                        int n, int pieces) {
     constexpr int VEC = 16 / sizeof(T), VECS = ELEMS / VEC;
-    __shared__ float s_warp[kThreads / 32], s_least[kThreads / 32];
-    __shared__ double s_sum[kThreads / 32];
+    __shared__ float s_warp[kThreads / 32], s_sum[2][kThreads / 32];
+    __shared__ __align__(16) float s_all[kThreads];
     __shared__ unsigned long long s_list[kList], s_top[kThreads / 32];
     __shared__ int s_n;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -95,30 +122,27 @@ __global__ void __launch_bounds__(kThreads)
     const int skew = (int)(((uintptr_t)x / sizeof(T)) % VEC);
     const long first = (long)piece * (ELEMS * kThreads) - skew;
 
-    float v[ELEMS];
+    Vec16<T> w[VECS];
+    const auto value = [&](int i) { return fmaxf(to_f32(w[i / VEC].v[i % VEC]), -INFINITY); };  // (NaN is no candidate)
+    const auto token = [&](int i) { return (int)(first + (long)(i / VEC * kThreads + tid) * VEC + i % VEC); };
     if (tid == 0) s_n = 0;
 #pragma unroll
     for (int j = 0; j < VECS; ++j) {
         const long at = first + (long)(j * kThreads + tid) * VEC;
         if (at >= 0 && at + VEC <= V) {
-            Vec16<T> w;
-            w.u = __ldg(reinterpret_cast<const uint4 *>(x + at));
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) v[j * VEC + i] = to_f32(w.v[i]);
+            w[j].u = __ldg(reinterpret_cast<const uint4 *>(x + at));
         } else {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) v[j * VEC + i] = at + i >= 0 && at + i < V ? to_f32(x[at + i]) : -INFINITY;
+            for (int i = 0; i < VEC; ++i) w[j].v[i] = at + i >= 0 && at + i < V ? x[at + i] : from_f32<T>(-INFINITY);
         }
     }
     float mine = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < ELEMS; ++i) {
-        v[i] = v[i] != v[i] ? -INFINITY : v[i] + 0.f;  // (NaN is no candidate; no negative zeros)
-        mine = fmaxf(mine, v[i]);
-    }
+    for (int i = 0; i < ELEMS; ++i) mine = fmaxf(mine, value(i));
     const float wm = warp_max(mine);
     if (lane == 0) s_warp[warp] = wm;
-    const float least = least_of_maxima(mine, groups_for(n), s_least, INFINITY);  // (a barrier)
+    // (a barrier)
+    const float least = nth_maximum(mine, n, n <= 32 ? 32 : kThreads, s_all, s_sum[0]);
     float m = s_warp[0];
 #pragma unroll
     for (int w = 1; w < kThreads / 32; ++w) m = fmaxf(m, s_warp[w]);
@@ -127,25 +151,29 @@ __global__ void __launch_bounds__(kThreads)
     const float base = m == -INFINITY ? 0.f : m;
     float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < ELEMS; ++i) {
-        part[i & 3] += __expf(v[i] - base);
-        if (v[i] >= least && v[i] != -INFINITY) {
+    for (int i = 0; i < ELEMS; ++i) part[i & 3] += __expf(value(i) - base);
+    // Few threads have such values: the warp reads those of one of them at a time again (registers would have to be indexed).
+    const auto read = [&](long at) { return at >= 0 && at < V ? fmaxf(to_f32(x[at]), -INFINITY) : -INFINITY; };
+    for (unsigned left = __ballot_sync(0xffffffffu, mine >= least && mine != -INFINITY); left != 0; left &= left - 1) {
+        const long at = first + (long)(lane / VEC * kThreads + warp * 32 + __ffs(left) - 1) * VEC + lane % VEC;
+        const float v = lane < ELEMS ? read(at) : -INFINITY;
+        if (v >= least && v != -INFINITY) {
             const int k = atomicAdd(&s_n, 1);
-            const int at = (int)(first + (long)(i / VEC * kThreads + tid) * VEC + i % VEC);
-            if (k < kList) s_list[k] = key_of(v[i], at);
+            if (k < kList) s_list[k] = key_of(v, (int)at);
         }
     }
-    double sum = ((double)part[0] + part[1]) + ((double)part[2] + part[3]);
+    float sum = part[0], lo = 0.f;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if (lane == 0) s_sum[warp] = sum;
+    for (int i = 1; i < 4; ++i) add_two(sum, lo, part[i], 0.f);
+    warp_sum_two(sum, lo);
+    __syncthreads();  // (their room has been used above)
+    if (lane == 0) s_sum[0][warp] = sum, s_sum[1][warp] = lo;
     __syncthreads();
     const long o = row * pieces + piece;
     if (tid == 0) {
-        sum = 0;
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) sum += s_sum[w];
-        out.m[o] = m, out.sum[o] = (float)sum;
+        for (int w = 1; w < kThreads / 32; ++w) add_two(sum, lo, s_sum[0][w], s_sum[1][w]);
+        out.m[o] = m, out.sum[o] = sum + lo;
     }
     auto put = [&](int rank, unsigned long long key) {
         const uint32_t b = (uint32_t)(key >> 32);
@@ -164,10 +192,11 @@ __global__ void __launch_bounds__(kThreads)
         unsigned long long last = ~0ull;
         for (found = 0; found < n; ++found) {
             unsigned long long best = 0;
-#pragma unroll
+#pragma unroll 4
             for (int i = 0; i < ELEMS; ++i) {
-                const unsigned long long key = key_of(v[i], (int)(first + (long)(i / VEC * kThreads + tid) * VEC + i % VEC));
-                if (v[i] != -INFINITY && key < last && key > best) best = key;
+                const float v = read(token(i));
+                const unsigned long long key = key_of(v, token(i));
+                if (v != -INFINITY && key < last && key > best) best = key;
             }
             best = warp_max(best);
             if (lane == 0) s_top[warp] = best;
@@ -183,21 +212,23 @@ __global__ void __launch_bounds__(kThreads)
     for (int i = min(found, n) + tid; i < n; i += kThreads) out.x[o * n + i] = -INFINITY, out.token[o * n + i] = -1;
 }
 
-struct Beam {
-    double total;
-    int at;  // k V + t
+struct Pick {
+    unsigned long long total;  // key_of
+    int at;                    // k V + t
 };
-__device__ __forceinline__ bool before(double a, int ia, double b, int ib) { return a > b || (a == b && ia < ib); }
+__device__ __forceinline__ bool before(unsigned long long a, int ia, unsigned long long b, int ib) {
+    return a > b || (a == b && ia < ib);
+}
 
 __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamSelect p, Pieces in, int pieces) {
-    __shared__ double s_lse[kBeamMaxK], s_least[kThreads / 32];
-    __shared__ float s_score[kBeamMaxK];
+    __shared__ double s_lse[kBeamMaxK];
+    __shared__ __align__(16) float s_all[kThreads];
+    __shared__ float s_least[kThreads / 32], s_score[kBeamMaxK], s_m[kBeamMaxK], s_sum[kBeamMaxK], s_lse32[kBeamMaxK];
     __shared__ uint8_t s_done[kBeamMaxK];
-    __shared__ double s_total[kList];
-    __shared__ int s_at[kList];
-    __shared__ Beam s_pick[kBeamMaxN];
-    __shared__ int s_place[kBeamMaxN];
-    __shared__ Beam s_top[kThreads / 32];
+    __shared__ unsigned long long s_total[kList];
+    __shared__ int s_at[kList], s_place[kBeamMaxN], s_rest[kBeamMaxN];
+    __shared__ Pick s_pick[kBeamMaxN], s_top[kThreads / 32];
+    __shared__ float s_near[kNear];
     __shared__ int s_n;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = blockIdx.x, K = p.K, n = p.n;
     // scores and flags may be written over below, by this CTA alone
@@ -210,129 +241,146 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamSelect p,
     }
     __syncthreads();
     for (int k = warp; k < K; k += kThreads / 32) {
-        double lse = -INFINITY;
+        float m = -INFINITY, sum = 0.f, lo = 0.f;
         if (!s_done[k]) {
             const long o = ((long)g * K + k) * pieces;
-            float m = -INFINITY;
             for (int i = lane; i < pieces; i += 32) m = fmaxf(m, __ldcg(in.m + o + i));
             m = warp_max(m);
-            double sum = 0;
             for (int i = lane; i < pieces; i += 32) {
                 const float mi = __ldcg(in.m + o + i);
-                if (mi != -INFINITY) sum += (double)__ldcg(in.sum + o + i) * exp((double)mi - (double)m);
+                if (mi != -INFINITY) add_two(sum, lo, __ldcg(in.sum + o + i) * expf(mi - m), 0.f);
             }
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            lse = m == -INFINITY ? -INFINITY : (double)m + log(sum);
+            warp_sum_two(sum, lo);
         }
-        if (lane == 0) s_lse[k] = lse;
+        if (lane == 0) s_m[k] = m, s_sum[k] = sum + lo;
+    }
+    __syncthreads();
+    for (int k = tid; k < K; k += kThreads) {
+        const double lse = s_m[k] == -INFINITY ? -INFINITY : (double)s_m[k] + log((double)s_sum[k]);
+        s_lse[k] = lse, s_lse32[k] = (float)lse;
     }
     __syncthreads();
 
-    // Candidate c of the group: its total (NaN: none) and place.
+    // Candidate c of the group: beam and logit; -inf: none.  (A beam at its end goes on as it is, once.)
     const int per_beam = pieces * n, all = K * per_beam;
-    auto candidate = [&](int c, double &total, int &at) {
-        const int k = c / per_beam, i = c % per_beam;
-        if (s_done[k]) {  // it goes on as it is, once
-            total = i == 0 && s_score[k] != -INFINITY ? (double)s_score[k] : NAN;
-            at = k * p.V + p.end_token;
-            return;
-        }
-        const long o = ((long)g * K + k) * per_beam + i;
-        const float x = __ldcg(in.x + o);
-        total = (double)s_score[k] + ((double)x - s_lse[k]);
-        at = k * p.V + __ldcg(in.token + o);
-        if (x == -INFINITY || !(total > -INFINITY)) total = NAN;
+    auto logit = [&](int c, int k) {
+        if (s_done[k]) return c - k * per_beam == 0 ? 0.f : -INFINITY;
+        return __ldcg(in.x + (long)g * all + c);
     };
-    double mine = -INFINITY;
+    // Its total in 32 bits, near enough to leave most of them out.
+    auto about = [&](float x, int k) { return s_done[k] ? s_score[k] + x : s_score[k] + (x - s_lse32[k]); };
+    auto total = [&](int c, int k, float x) {
+        return key_of(s_done[k] ? (double)s_score[k] : (double)s_score[k] + ((double)x - s_lse[k]));
+    };
+    auto place = [&](int c, int k) { return k * p.V + (s_done[k] ? p.end_token : __ldcg(in.token + (long)g * all + c)); };
+    float mine = -INFINITY, size = 0.f;
+#pragma unroll 4
     for (int c = tid; c < all; c += kThreads) {
-        double t;
-        int at;
-        candidate(c, t, at);
-        if (t > mine) mine = t;
+        const int k = c / per_beam;
+        const float x = logit(c, k), t = about(x, k);
+        const bool some = x != -INFINITY && t > -INFINITY;
+        if (c < kNear) s_near[c] = some ? t : -INFINITY;
+        if (some) mine = fmaxf(mine, t), size = fmaxf(size, fabsf(x) + (s_done[k] ? 0.f : fabsf(s_lse32[k])) + fabsf(s_score[k]));
     }
-    const double least = least_of_maxima(mine, groups_for(n), s_least, (double)INFINITY);
+    // The row's term and two sums are rounded, each to 2^-24 of these sizes: 2^-21 is more than two totals can be off.
+    // (Infinite scores leave everything in.)
+    size = warp_max(size);
+    if (lane == 0) s_m[warp] = size;  // (K <= 128 >= 8 places; the maxima have been used)
+    const float reach = nth_maximum(mine, n, kThreads, s_all, s_least);  // (barriers)
+    size = s_m[0];
+#pragma unroll
+    for (int w = 1; w < kThreads / 32; ++w) size = fmaxf(size, s_m[w]);
+    const float least = size < 1e30f ? reach - size * 0x1p-21f : -INFINITY;
     for (int c = tid; c < all; c += kThreads) {
-        double t;
-        int at;
-        candidate(c, t, at);
-        if (t >= least) {
+        if (c < kNear && !(s_near[c] >= least && s_near[c] > -INFINITY)) continue;
+        const int k = c / per_beam;
+        const float x = logit(c, k), t = about(x, k);
+        if (x != -INFINITY && t >= least && t > -INFINITY) {
             const int i = atomicAdd(&s_n, 1);
-            if (i < kList) s_total[i] = t, s_at[i] = at;
+            if (i < kList) s_total[i] = total(c, k, x), s_at[i] = place(c, k);
         }
     }
     __syncthreads();
     int found = s_n;
     if (found <= kList) {
         for (int i = tid; i < found; i += kThreads) {
-            const double t = s_total[i];
+            const unsigned long long t = s_total[i];
             const int at = s_at[i];
             int rank = 0;
             for (int j = 0; j < found && rank < n; ++j) rank += before(s_total[j], s_at[j], t, at);
-            if (rank < n) s_pick[rank] = Beam{t, at};
+            if (rank < n) s_pick[rank] = Pick{t, at};
         }
     } else {
-        double lt = INFINITY;
+        unsigned long long lt = ~0ull;
         int la = -1;
         for (found = 0; found < n; ++found) {
-            double bt = -INFINITY;
+            unsigned long long bt = 0;
             int ba = INT_MAX;
             for (int c = tid; c < all; c += kThreads) {
-                double t;
-                int at;
-                candidate(c, t, at);
-                if (t == t && before(lt, la, t, at) && before(t, at, bt, ba)) bt = t, ba = at;
+                const int k = c / per_beam;
+                const float x = logit(c, k);
+                if (x == -INFINITY || !(about(x, k) > -INFINITY)) continue;
+                const unsigned long long t = total(c, k, x);
+                const int at = place(c, k);
+                if (before(lt, la, t, at) && before(t, at, bt, ba)) bt = t, ba = at;
             }
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) {
-                const double t = __shfl_xor_sync(0xffffffffu, bt, d);
+                const unsigned long long t = __shfl_xor_sync(0xffffffffu, bt, d);
                 const int at = __shfl_xor_sync(0xffffffffu, ba, d);
                 if (before(t, at, bt, ba)) bt = t, ba = at;
             }
-            if (lane == 0) s_top[warp] = Beam{bt, ba};
+            if (lane == 0) s_top[warp] = Pick{bt, ba};
             __syncthreads();
 #pragma unroll
             for (int w = 0; w < kThreads / 32; ++w)
                 if (before(s_top[w].total, s_top[w].at, bt, ba)) bt = s_top[w].total, ba = s_top[w].at;
             __syncthreads();
             if (ba == INT_MAX) break;
-            if (tid == 0) s_pick[found] = Beam{bt, ba};
+            if (tid == 0) s_pick[found] = Pick{bt, ba};
             lt = bt, la = ba;
         }
     }
     found = min(found, n);
     __syncthreads();
-    if (tid == 0) {
+    if (tid == 0 && found < n) {
         // too few: the lowest places of those that are left, all of them at -inf
         for (int at = 0; found < n; ++at) {
             bool have = false;
             for (int i = 0; i < found; ++i) have |= s_pick[i].at == at;
-            if (!have) s_pick[found++] = Beam{-INFINITY, at};
-        }
-        for (int i = 0; i < n; ++i) s_place[i] = i;
-        if (p.keep_rows) {  // a beam's best child takes its row, the others take the rows that are left in order
-            for (int i = 0; i < n; ++i) s_place[i] = -1;
-            for (int i = 0; i < n; ++i) {
-                const int k = s_pick[i].at / p.V;
-                if (s_place[k] < 0) s_place[k] = i, s_at[i] = 1;
-                else s_at[i] = 0;
-            }
-            int row = 0;
-            for (int i = 0; i < n; ++i)
-                if (!s_at[i]) {
-                    while (s_place[row] >= 0) ++row;
-                    s_place[row] = i;
-                }
+            if (!have) s_pick[found++] = Pick{key_of(-(double)INFINITY), at};
         }
     }
     __syncthreads();
+    // With keep_rows a beam's best child takes its row; the others, in order, the rows that are left.
+    if (p.keep_rows) {
+        for (int i = tid; i < n; i += kThreads) s_rest[i] = -1;
+        __syncthreads();
+        for (int i = tid; i < n; i += kThreads) {
+            const int k = s_pick[i].at / p.V;
+            bool best = true;
+            for (int j = 0; j < i; ++j) best &= s_pick[j].at / p.V != k;
+            s_at[i] = best ? k : -1;
+            if (best) s_rest[k] = i;
+        }
+        __syncthreads();
+        for (int i = tid; i < n; i += kThreads) {
+            if (s_rest[i] >= 0) s_place[i] = s_rest[i];
+            if (s_at[i] >= 0) continue;
+            int others = 0, row = -1;  // the others before this one, and the row that many are left before
+            for (int j = 0; j < i; ++j) others += s_at[j] < 0;
+            while (others >= 0) others -= s_rest[++row] < 0;
+            s_place[row] = i;
+        }
+        __syncthreads();
+    }
     for (int i = tid; i < n; i += kThreads) {
-        const Beam b = s_pick[s_place[i]];
+        const Pick b = s_pick[p.keep_rows ? s_place[i] : i];
         const int k = b.at / p.V, token = b.at % p.V;
         const long o = (long)g * n + i;
         p.tokens[o] = token;
         p.parents[o] = g * K + k;
-        p.scores_out[o] = (float)b.total;
+        p.scores_out[o] = (float)of_key(b.total);
         if (p.finished_out != nullptr) p.finished_out[o] = s_done[k] || token == p.end_token;
     }
 }
