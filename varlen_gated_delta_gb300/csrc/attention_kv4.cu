@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(128) kv4_wide_kernel(const Kv4Params p) {
     }
 }
 
-// ---------------------------------------------------------------- up to 16 rows
+// ---------------------------------------------------------------- rows by the block of 8 or 16
 
 // Rows are the columns of the products, keys and channels their rows: S^T = K Q^T and O^T = V^T P^T with 16 keys or 16
 // channels to a tile, so that a cached value is converted into the registers of one product and no row
@@ -458,7 +458,9 @@ struct Narrow {
     static constexpr int KB = WARP_KEYS / 16;                // blocks of 16 keys
     static constexpr int Q = sizeof(T) == 4 ? 2 : 1;         // fp16 values to a query's
     static constexpr int RAW = WARP_KEYS * DP / 16 * 9;      // bytes of a warp's tile of K (or V): codes, then scales
-    static constexpr int SMEM = 4 * STAGES * 2 * RAW + 64;   // (loads of channels past D may pass the end)
+    static constexpr bool QREG = Q * NT * DP <= 256;         // queries stay in registers, else in shared memory
+    static constexpr int QBYTES = QREG ? 0 : Q * ROWS * DP * 2;
+    static constexpr int SMEM = 4 * STAGES * 2 * RAW + 64 + QBYTES;  // (loads of channels past D may pass the end)
     static constexpr int PART = ROWS * (3 + DP);
     static constexpr int PER_SM = DP > 128 || NT * Q > 1 ? 2 : DP > 64 ? 3 : 4;
     static_assert(2 * RAW >= 8 * DP * 4, "a column tile's output fits a stage");
@@ -514,7 +516,7 @@ __global__ void __launch_bounds__(128, Narrow<DP, NT, T>::PER_SM) kv4_narrow_ker
     constexpr int MT = DP / 16;                // tiles of channels, and steps of 16 channels
     constexpr bool F32 = sizeof(T) == 4;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ float s_m[4][C::ROWS], s_l[4][C::ROWS];
+    __shared__ float s_m[4][C::ROWS], s_l[4][C::ROWS], s_back[C::ROWS];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     unsigned char *ring = smem + warp * STAGES * 2 * RAW;
     const uint32_t ring_at = sm100::smem_u32(ring);
@@ -536,7 +538,7 @@ __global__ void __launch_bounds__(128, Narrow<DP, NT, T>::PER_SM) kv4_narrow_ker
     };
     // (pages of several blocks of 16 keys are looked up by lane: lane i holds that of block i)
     auto look_up = [&](const Cursor &x) {
-        const int key = x.tile * KEYS + warp * C::WARP_KEYS + (lane & (C::KB - 1)) * 16;
+        const int key = x.tile * KEYS + warp * C::WARP_KEYS + min(lane, C::KB - 1) * 16;
         int index, at;
         split(key, index, at);
         return key < x.kv ? __ldg(p.a.block_table + (size_t)x.b * p.a.max_pages + index) : -1;
@@ -584,22 +586,23 @@ __global__ void __launch_bounds__(128, Narrow<DP, NT, T>::PER_SM) kv4_narrow_ker
 #pragma unroll 1
     for (int i = 0; i < STAGES; ++i) fetch_next(i);
 
-    uint32_t q[QN][NT][MT][2];
+    // Queries as the second operand of the products: of step `ks`, two words of each lane.
+    uint32_t q[C::QREG ? QN : 1][NT][C::QREG ? MT : 1][2];
+    uint2 *s_q = reinterpret_cast<uint2 *>(smem + 4 * STAGES * 2 * RAW + 64);  // [QN][NT][MT][32]
     float o[NT][MT][4], m[NT][2], l[NT][2], cr[NT][2];
     int stage = 0, first_tile = 0;
     bool fresh = true;  // the next tile begins a part
 #pragma unroll 1
     for (; n_left > 0; --n_left) {
-        const int n = cur.len, rows = n * G, shift = cur.kv - n;
+        const int n = cur.len, row0 = cur.block * C::ROWS, rows = min(C::ROWS, n * G - row0), shift = cur.kv - n;
         if (fresh) {
             fresh = false;
             first_tile = cur.tile;
             const float c = fmaxf(p.c * head_scale(p.ks, cur.h), 1e-18f);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+            const auto load_rows = [&](int nt, auto put) {  // rows nt 8 + g, DP / 4 channels of each a thread
                 const int r = nt * 8 + g;
                 const T *src = static_cast<const T *>(p.a.q);
-                if (r < rows) src += (long)(cur.start + r / G) * p.a.qs + (long)(cur.h * G + r % G) * D;
+                if (r < rows) src += (long)(cur.start + (row0 + r) / G) * p.a.qs + (long)(cur.h * G + (row0 + r) % G) * D;
                 float x[DP / 4], amax = 0.f;
 #pragma unroll
                 for (int i = 0; i < DP / 4; ++i) {
@@ -612,14 +615,32 @@ __global__ void __launch_bounds__(128, Narrow<DP, NT, T>::PER_SM) kv4_narrow_ker
                 float back;
                 const float power = row_power(amax, back) * p.sign;
 #pragma unroll
-                for (int i = 0; i < DP / 4; i += 2) {
-                    const float a = x[i] * power, b = x[i + 1] * power;
-                    const uint32_t hi = pack_f16(a, b);
-                    q[0][nt][i / 4][i / 2 % 2] = hi;
-                    if constexpr (F32) q[1][nt][i / 4][i / 2 % 2] = rest_f16(a, b, hi);
+                for (int i = 0; i < DP / 4; i += 4) {
+                    const float y[4] = {x[i] * power, x[i + 1] * power, x[i + 2] * power, x[i + 3] * power};
+                    const uint32_t hi[2] = {pack_f16(y[0], y[1]), pack_f16(y[2], y[3])};
+                    put(0, i / 4, hi[0], hi[1]);
+                    if constexpr (F32) put(1, i / 4, rest_f16(y[0], y[1], hi[0]), rest_f16(y[2], y[3], hi[1]));
                 }
-                // this thread's columns are rows 2 t4 and 2 t4 + 1
-                cr[nt][0] = c * __shfl_sync(0xffffffffu, back, t4 * 8), cr[nt][1] = c * __shfl_sync(0xffffffffu, back, t4 * 8 + 4);
+                return back;
+            };
+            if constexpr (C::QREG) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float back = load_rows(nt, [&](int z, int ks, uint32_t a, uint32_t b) { q[z][nt][ks][0] = a, q[z][nt][ks][1] = b; });
+                    // this thread's columns are rows 2 t4 and 2 t4 + 1
+                    cr[nt][0] = c * __shfl_sync(0xffffffffu, back, t4 * 8), cr[nt][1] = c * __shfl_sync(0xffffffffu, back, t4 * 8 + 4);
+                }
+            } else {
+                if (warp < NT) {
+                    const float back = load_rows(warp, [&](int z, int ks, uint32_t a, uint32_t b) { s_q[((z * NT + warp) * MT + ks) * 32 + lane] = make_uint2(a, b); });
+                    if (t4 == 0) s_back[warp * 8 + g] = back;
+                }
+                __syncthreads();
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) cr[nt][0] = c * s_back[nt * 8 + t4 * 2], cr[nt][1] = c * s_back[nt * 8 + t4 * 2 + 1];
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
                 m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
                 for (int i = 0; i < MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
@@ -661,12 +682,19 @@ __global__ void __launch_bounds__(128, Narrow<DP, NT, T>::PER_SM) kv4_narrow_ker
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int z = 0; z < QN; ++z) mma16816(s[nt][kb], a, q[z][nt][2 * i + y][0], q[z][nt][2 * i + y][1]);
+                            for (int z = 0; z < QN; ++z) {
+                                if constexpr (C::QREG) {
+                                    mma16816(s[nt][kb], a, q[z][nt][2 * i + y][0], q[z][nt][2 * i + y][1]);
+                                } else {
+                                    const uint2 b = s_q[((z * NT + nt) * MT + 2 * i + y) * 32 + lane];
+                                    mma16816(s[nt][kb], a, b.x, b.y);
+                                }
+                            }
                     }
                 }
             }
             // ---- running softmax: this thread's rows 2 t4 and 2 t4 + 1, its keys of key_of_row(g)
-            const bool edge = j0 + C::WARP_KEYS > shift + 1;  // some row does not see all of these
+            const bool edge = j0 + C::WARP_KEYS > shift + row0 / G + 1;  // some row does not see all of these
             uint32_t pt[QN][NT][C::KB][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -675,7 +703,7 @@ __global__ void __launch_bounds__(128, Narrow<DP, NT, T>::PER_SM) kv4_narrow_ker
                     for (int kb = 0; kb < C::KB; ++kb)
 #pragma unroll
                         for (int z = 0; z < 4; ++z) {
-                            const int key = j0 + kb * 16 + (z >> 1) * 8 + key_of_row(g), r = nt * 8 + t4 * 2 + (z & 1);
+                            const int key = j0 + kb * 16 + (z >> 1) * 8 + key_of_row(g), r = row0 + nt * 8 + t4 * 2 + (z & 1);
                             if (key >= min(cur.kv, shift + r / G + 1)) s[nt][kb][z] = -INFINITY;
                         }
                 float f[2], base[2];
@@ -810,7 +838,7 @@ __global__ void __launch_bounds__(128, Narrow<DP, NT, T>::PER_SM) kv4_narrow_ker
                     }
                     const float inv = L > 0.f ? vs / L : L;  // (0 gives 0, NaN stays)
                     float *part = p.part + (2 * cta + (first_tile == 0)) * C::PART;
-                    T *out = static_cast<T *>(p.a.out) + ((size_t)(cur.start + r / G) * p.a.H + cur.h * G + r % G) * D;
+                    T *out = static_cast<T *>(p.a.out) + ((size_t)(cur.start + (row0 + r) / G) * p.a.H + cur.h * G + (row0 + r) % G) * D;
                     if (!whole && lane == 0) part[r] = M, part[C::ROWS + r] = L, part[2 * C::ROWS + r] = c;
 #pragma unroll
                     for (int d = lane * 2; d < DP; d += 64) {
@@ -829,7 +857,7 @@ __global__ void __launch_bounds__(128, Narrow<DP, NT, T>::PER_SM) kv4_narrow_ker
         }
         __syncwarp();  // the warp is done with this stage
         fetch_next(stage);
-        stage ^= 1;
+        stage = stage == STAGES - 1 ? 0 : stage + 1;
         advance(p, C::ROWS, KEYS, cur);
     }
 }
@@ -918,16 +946,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const Kv4Para
 // ---------------------------------------------------------------- host
 
 int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+// (the most that any of the kernels asks for: blocks of 8 rows)
 size_t span_bytes(int B, int HKV, long blocks) { return ((size_t)B * blocks * HKV * 8 + 255) & ~size_t(255); }
 long row_blocks(int H, int HKV, int max_q, int rows) { return ((long)max_q * (H / HKV) + rows - 1) / rows; }
 
-constexpr int kNarrowRows = 16;
+// Sequences of up to so many rows run in blocks of 8 or 16, which convert the cache anew: still less than tiles of 64 rows
+// in shared memory take.
+constexpr int kNarrowRows = 64;
 
 // A kernel over the sequences of its rows (C: its sizes), then the join of what several CTAs shared.
 template <int DP, typename T, typename C>
 cudaError_t launch_kernels(void (*kernel)(Kv4Params), int per_sm, Kv4Params p, void *ws, cudaStream_t s) {
-    p.blocks = (int)row_blocks(p.a.H, p.a.HKV, p.a.max_q, C::ROWS);
-    if (C::ROWS <= kNarrowRows) p.blocks = 1;
+    p.blocks = (int)((std::min((long)p.a.max_q * p.G, (long)p.max_rows) + C::ROWS - 1) / C::ROWS);
     p.spans = static_cast<int2 *>(ws);
     p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + span_bytes(p.a.B, p.a.HKV, p.blocks));
     int dev = 0, sms = 0;
@@ -970,7 +1000,7 @@ cudaError_t launch_narrow(Kv4Params p, void *ws, cudaStream_t s) {
         return cudaFuncSetAttribute(kv4_narrow_kernel<DP, NT, T, FULL>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     });
     if (e != cudaSuccess) return e;
-    p.min_rows = 0, p.max_rows = kNarrowRows < C::ROWS ? kNarrowRows : C::ROWS;
+    p.min_rows = 0, p.max_rows = kNarrowRows;
     return launch_kernels<DP, T, C>(kv4_narrow_kernel<DP, NT, T, FULL>, C::PER_SM, p, ws, s);
 }
 
@@ -978,17 +1008,19 @@ template <int DP, typename T>
 cudaError_t launch_rows(const Kv4Params &p, void *ws, cudaStream_t s) {
     const long rows = (long)p.a.max_q * p.G;
     const bool full = p.a.D == DP;
-    int narrow = 0;  // sequences of up to so many rows are done
     cudaError_t e = cudaSuccess;
-    if (rows <= 8 || (rows > kNarrowRows && p.G <= 8)) {
-        narrow = 8;
-        e = full ? launch_narrow<DP, 1, T, true>(p, ws, s) : launch_narrow<DP, 1, T, false>(p, ws, s);
-    } else if (p.G <= 16) {
-        narrow = 16;
-        e = full ? launch_narrow<DP, 2, T, true>(p, ws, s) : launch_narrow<DP, 2, T, false>(p, ws, s);
+    if (p.G <= kNarrowRows) {
+        // (a batch of single tokens beside longer slices: blocks of 8 if those hold them; wide fp32 heads: 16 rows would not
+        // fit the registers)
+        const bool one = rows <= 8 || (rows > kNarrowRows && p.G <= 8) || (DP > 128 && sizeof(T) == 4);
+        if (one) {
+            e = full ? launch_narrow<DP, 1, T, true>(p, ws, s) : launch_narrow<DP, 1, T, false>(p, ws, s);
+        } else if constexpr (DP <= 128 || sizeof(T) == 2) {
+            e = full ? launch_narrow<DP, 2, T, true>(p, ws, s) : launch_narrow<DP, 2, T, false>(p, ws, s);
+        }
     }
-    if (e != cudaSuccess || rows <= narrow) return e;
-    return launch_wide<DP, T>(p, narrow, ws, s);
+    if (e != cudaSuccess || rows <= kNarrowRows) return e;
+    return launch_wide<DP, T>(p, kNarrowRows, ws, s);
 }
 
 template <typename T>
@@ -1003,7 +1035,7 @@ cudaError_t launch(const Kv4Params &p, void *ws, cudaStream_t s) {
 }  // namespace
 
 size_t attention_kv4_workspace(int B, int N, int H, int HKV, int D, int max_q) {
-    return span_bytes(B, HKV, row_blocks(H, HKV, max_q, 64)) + 2 * (size_t)kMaxCtas * 64 * (3 + padded(D)) * 4;
+    return span_bytes(B, HKV, std::max(row_blocks(H, HKV, max_q, 64), row_blocks(H, HKV, std::min(max_q, kNarrowRows), 8))) + 2 * (size_t)kMaxCtas * 64 * (3 + padded(D)) * 4;
 }
 
 cudaError_t launch_attention_kv4(const Attn &a, const float *k_scale, const float *v_scale, int dtype, void *ws, cudaStream_t s) {
