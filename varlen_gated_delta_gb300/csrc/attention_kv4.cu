@@ -79,14 +79,6 @@ template <>
 __device__ __forceinline__ void store2(__nv_bfloat16 *at, float x, float y) {
     *reinterpret_cast<__nv_bfloat162 *>(at) = __floats2bfloat162_rn(x, y);
 }
-// The power of two that brings a row's largest magnitude into [1, 2), and its inverse (for rows below 2^-63, nothing
-// but zeros among them, 2^63, so that the inverse stays far from zero).
-__device__ __forceinline__ float row_power(float amax, float &inverse) {
-    const int e = max(64, min((int)(__float_as_uint(amax) >> 23 & 255u), 253));  // (biased)
-    inverse = __uint_as_float((uint32_t)e << 23);
-    return __uint_as_float((uint32_t)(254 - e) << 23);
-}
-
 // Byte offset of 16-byte chunk c of row r: chunks of 8 neighbouring rows fall into different banks.
 template <int DP>
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
@@ -280,7 +272,7 @@ __global__ void __launch_bounds__(128) kv4_wide_kernel(const Kv4Params p) {
 #pragma unroll
                 for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
                 float back;
-                const float power = row_power(amax, back) * p.sign;
+                const float power = kv4_row_power(amax, back) * p.sign;
 #pragma unroll
                 for (int i = 0; i < DP / 32; ++i) {
                     const int d = lane + 32 * i;
@@ -613,7 +605,7 @@ __global__ void __launch_bounds__(128, Narrow<DP, NT, T>::PER_SM) kv4_narrow_ker
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
                 float back;
-                const float power = row_power(amax, back) * p.sign;
+                const float power = kv4_row_power(amax, back) * p.sign;
 #pragma unroll
                 for (int i = 0; i < DP / 4; i += 4) {
                     const float y[4] = {x[i] * power, x[i + 1] * power, x[i + 2] * power, x[i + 3] * power};
@@ -952,7 +944,7 @@ long row_blocks(int H, int HKV, int max_q, int rows) { return ((long)max_q * (H 
 
 // Sequences of up to so many rows run in blocks of 8 or 16, which convert the cache anew: still less than tiles of 64 rows
 // in shared memory take.
-constexpr int kNarrowRows = 64;
+constexpr int kNarrowRows = kSplitRows;
 
 // A kernel over the sequences of its rows (C: its sizes), then the join of what several CTAs shared.
 template <int DP, typename T, typename C>
@@ -1020,7 +1012,13 @@ cudaError_t launch_rows(const Kv4Params &p, void *ws, cudaStream_t s) {
         }
     }
     if (e != cudaSuccess || rows <= kNarrowRows) return e;
-    return launch_wide<DP, T>(p, kNarrowRows, ws, s);
+    if constexpr (sizeof(T) == 4) {
+        return launch_wide<DP, T>(p, kNarrowRows, ws, s);
+    } else {
+        Attn a = p.a;
+        a.part = static_cast<float *>(ws);
+        return launch_attention_prompt_kv4(a, p.ks, p.vs, kNarrowRows, s);
+    }
 }
 
 template <typename T>
@@ -1035,7 +1033,10 @@ cudaError_t launch(const Kv4Params &p, void *ws, cudaStream_t s) {
 }  // namespace
 
 size_t attention_kv4_workspace(int B, int N, int H, int HKV, int D, int max_q) {
-    return span_bytes(B, HKV, std::max(row_blocks(H, HKV, max_q, 64), row_blocks(H, HKV, std::min(max_q, kNarrowRows), 8))) + 2 * (size_t)kMaxCtas * 64 * (3 + padded(D)) * 4;
+    const long blocks = std::max(row_blocks(H, HKV, max_q, 64), row_blocks(H, HKV, std::min(max_q, kNarrowRows), 8));
+    const size_t parts = span_bytes(B, HKV, blocks) + 2 * (size_t)kMaxCtas * 64 * (3 + padded(D)) * 4;
+    const bool slices = (long)max_q * (H / HKV) > kNarrowRows;
+    return std::max(parts, slices ? attention_prompt_part_floats(B, N, H, HKV, D, max_q) * 4 : 0);
 }
 
 cudaError_t launch_attention_kv4(const Attn &a, const float *k_scale, const float *v_scale, int dtype, void *ws, cudaStream_t s) {

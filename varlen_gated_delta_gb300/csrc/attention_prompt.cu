@@ -54,6 +54,7 @@
 #include <utility>
 
 #include "attention.cuh"
+#include "kv4.cuh"
 #include "sm100.cuh"
 
 namespace gdn {
@@ -66,6 +67,7 @@ using namespace sm100;
 constexpr int kWaitTries = 1 << 19;
 constexpr int kMaxBins = 4096;  // bins of the longest-first order
 constexpr float kLazy = 8.f;    // growth of the row maximum (log2) that O waits for
+constexpr float kKv4Shift = 7.f;  // log2 of the factor of fp16 probabilities: 2^(kLazy + 7) still fits
 
 // Bounded waits of attention kernels that have given up.  It only grows, so that no query takes a report
 // from another.
@@ -77,7 +79,9 @@ __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.a
 template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 
-template <int DP>
+// KV4: the cache holds 4-bit values (kv4.cuh).  A warpgroup more turns them, and the queries, into fp16 tiles; the load warp
+// then only hands out items.
+template <int DP, bool KV4 = false>
 struct Cfg {
     static constexpr int NQ = DP > 128 ? 1 : 2;    // query tiles of a CTA
     static constexpr int BN = DP > 128 ? 64 : 128; // keys of a tile
@@ -88,11 +92,16 @@ struct Cfg {
     // leave it more to do than the products (16 x 2048 tokens, 16 heads of 64: 200 -> 195 us; 8 x 4096,
     // 32 heads of 128: 729 -> 733).
     static constexpr bool EARLY = DP == 64;
-    static constexpr int THREADS = NQ * 128 + 128;
+    static constexpr int IO = KV4 ? 2 : 1;           // warpgroups beside the softmax ones
+    static constexpr int THREADS = (NQ + IO) * 128;
     // registers a thread at launch and after the split: a softmax thread holds a row of scores
     static constexpr int REGS = 65536 / THREADS / 8 * 8 > 255 ? 248 : 65536 / THREADS / 8 * 8;
-    static constexpr int REGS_IO = 96, REGS_SOFTMAX = NQ == 2 ? 200 : REGS;
-    static_assert(NQ * REGS_SOFTMAX + REGS_IO <= (NQ + 1) * REGS, "more registers than the CTA was launched with");
+    static constexpr bool SPLIT_REGS = NQ == 2 || KV4;
+    static constexpr int REGS_IO = !KV4 ? 96 : NQ == 2 ? 64 : 128;
+    static constexpr int REGS_SOFTMAX = !SPLIT_REGS ? REGS : !KV4 ? 200 : NQ == 2 ? 192 : 248;
+    static_assert(NQ * REGS_SOFTMAX + IO * REGS_IO <= (NQ + IO) * REGS, "more registers than the CTA was launched with");
+    // KV4: softmax factors of the rows of four items, and the barriers that tell of them
+    static constexpr int FACTORS = KV4 ? 4 * 2 * 128 * 4 + 4 * 8 : 0;
     // tensor memory: two score buffers, then O of each query tile
     static constexpr int COL_O = 2 * BN;
 };
@@ -113,6 +122,8 @@ struct PromptParams {
     int negate;     // scale < 0
     int out32;      // output rows lie on 32-byte boundaries
     int splits;     // of the key tiles of an item; more than one: parts for a second kernel
+    const float *ks, *vs;  // KV4: scales of the key-value heads, or NULL
+    int q_wide;            // KV4: query rows lie on 16-byte boundaries
 };
 
 // Warp-wide mbarrier wait that gives up, for the whole warp, after so many tries or when another role has.
@@ -328,17 +339,106 @@ __device__ __forceinline__ bool masked_non_finite(const PromptParams &p, int b, 
     return found;
 }
 
+// ---------------------------------------------------------------- the converting warpgroup (KV4)
+
+// Rows of a query tile to fp16, each by the power of two that puts its largest value into [1, 2) (and the sign of the scale);
+// the softmax factor of each row takes that back.  tid: of the warpgroup.
 template <int DP>
-__global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
+__device__ __forceinline__ void convert_queries(const PromptParams &p, const Item &it, int t, unsigned char *tile, float *factors, int tid) {
+    constexpr int LANES = DP / 8, STEP = 128 / LANES, BATCH = 4;  // lanes to a row, rows at a time, loads in flight
+    const int c = tid % LANES;
+    const float factor = fmaxf(p.c * (p.ks ? __ldg(p.ks + it.h / p.G) : 1.f), 1e-18f);
+#pragma unroll 1
+    for (int r0 = tid / LANES; r0 < 128; r0 += STEP * BATCH) {
+        Vec16<__nv_bfloat16> x[BATCH];
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            const int row = r0 + k * STEP;
+            const int token = it.row0 + (p.pair ? 0 : t * (128 >> p.packed)) + (row >> p.packed);
+            const int head = it.h + (p.pair ? t : row & ((1 << p.packed) - 1));
+            x[k].u = make_uint4(0, 0, 0, 0);
+            if (token < it.len && c * 8 < p.a.D) {
+                const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.a.q) + (long)(it.start + token) * p.a.qs + (long)head * p.a.D + c * 8;
+                if (p.q_wide) x[k].u = __ldg(reinterpret_cast<const uint4 *>(src));
+                else
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[k].v[i] = src[i];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            const int row = r0 + k * STEP;
+            float amax = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(to_f32(x[k].v[i])));
+#pragma unroll
+            for (int d = LANES / 2; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+            float back;
+            const float power = kv4_row_power(amax, back) * (p.negate ? -1.f : 1.f);
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __half2 h = __floats2half2_rn(to_f32(x[k].v[2 * i]) * power, to_f32(x[k].v[2 * i + 1]) * power);
+                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+            *reinterpret_cast<uint4 *>(tile + (c >> 3) * 128 * 128 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (c == 0) factors[row] = factor * back;
+        }
+    }
+}
+
+// Codes and scales of a tile of keys (or values), some groups of 16 channels to each thread, on their way in registers.
+template <int DP>
+struct RawTile {
+    static constexpr int BN = Cfg<DP, true>::BN, GROUPS = DP / 16, N = BN * GROUPS / 128;
+    uint2 codes[N];
+    uint32_t scale[N];
+    __device__ __forceinline__ void load(const PromptParams &p, const Item &it, int j, bool values, int tid) {
+        const int grp = tid % GROUPS, GR = p.a.D / 16, ps = p.a.page_size;
+        const uint8_t *cache = static_cast<const uint8_t *>(values ? p.a.v : p.a.k);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int key = (it.lo + j) * BN + tid / GROUPS + i * (128 / GROUPS);
+            codes[i] = make_uint2(0, 0), scale[i] = 0;
+            if (key >= it.kv || grp >= GR) continue;
+            const int index = key / ps, at = key - index * ps;
+            const int page = __ldg(p.a.block_table + (size_t)it.b * p.a.max_pages + index);
+            if (page < 0 || page >= p.a.num_pages) continue;  // (reads as zeros)
+            const uint8_t *block = cache + ((long)page * p.a.HKV + it.h / p.G) * ((long)ps * GR * 9);
+            codes[i] = __ldg(reinterpret_cast<const uint2 *>(block + ((long)at * GR + grp) * 8));
+            scale[i] = __ldg(block + (long)ps * GR * 8 + at * GR + grp);
+        }
+    }
+    __device__ __forceinline__ void store(unsigned char *slot, int tid) const {
+        const int grp = tid % GROUPS;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int key = tid / GROUPS + i * (128 / GROUPS);
+            const uint32_t s = kv4_scales(scale[i] | scale[i] << 8);
+            unsigned char *row = slot + (grp >> 2) * BN * 128 + key * 128;
+            uint32_t d[2][4];
+            kv4_codes(codes[i].x, d[0]), kv4_codes(codes[i].y, d[1]);
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+                *reinterpret_cast<uint4 *>(row + ((((grp & 3) * 2 + half) ^ (key & 7)) << 4)) =
+                    make_uint4(mul_f16x2(d[half][0], s), mul_f16x2(d[half][1], s), mul_f16x2(d[half][2], s), mul_f16x2(d[half][3], s));
+        }
+    }
+};
+
+template <int DP, bool KV4>
+__global__ void __launch_bounds__(Cfg<DP, KV4>::THREADS, 1)
     attn_prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap, const __grid_constant__ PromptParams p) {
-    using C = Cfg<DP>;
+    using C = Cfg<DP, KV4>;
     constexpr int NQ = C::NQ, BN = C::BN, NB = C::NB, SLOTS = C::SLOTS;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     unsigned char *sq = smem, *ring = smem + NQ * C::QBYTES;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(ring + SLOTS * C::SLOT);
+    float *factors = reinterpret_cast<float *>(ring + SLOTS * C::SLOT);  // KV4: [4 items][2 query tiles][128 rows]
+    uint64_t *f_full = reinterpret_cast<uint64_t *>(factors + 4 * 2 * 128);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(ring + SLOTS * C::SLOT + C::FACTORS);
     uint64_t *full = bars, *empty = full + SLOTS, *q_full = empty + SLOTS, *q_empty = q_full + 2,
              *s_full = q_empty + 2, *p_full = s_full + 2, *o_done = p_full + 2, *v_fixed = o_done + 2, *turn = v_fixed + SLOTS,
              *p_half = turn + 2, *item_full = p_half + 2, *item_empty = item_full + 4, *drained = item_empty + 4;
@@ -355,19 +455,21 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
 
     if (tid == 0) {
         for (int i = 0; i < SLOTS; ++i) {
-            mbar_init(full + i, 1);
-            mbar_init(empty + i, NQ + (i & 1));  // every product warp and, for V (odd slots), the mending warp
+            mbar_init(full + i, KV4 ? 128 : 1);
+            // every product warp and, for V (odd slots), the mending warp
+            mbar_init(empty + i, KV4 ? NQ : NQ + (i & 1));
             mbar_init(v_fixed + i, 32);
+            if (KV4) mbar_init(f_full + i, 128);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(q_full + i, 1), mbar_init(q_empty + i, 1);
+            mbar_init(q_full + i, KV4 ? 128 : 1), mbar_init(q_empty + i, 1);
             mbar_init(s_full + i, 1), mbar_init(p_full + i, 128), mbar_init(o_done + i, 1);
             mbar_init(turn + i, 128), mbar_init(p_half + i, 128), mbar_init(drained + i, 1);
         }
-        for (int i = 0; i < 4; ++i) mbar_init(item_full + i, 1), mbar_init(item_empty + i, NQ * 5 + 1);
+        for (int i = 0; i < 4; ++i) mbar_init(item_full + i, 1), mbar_init(item_empty + i, NQ * 5 + (KV4 ? 4 : 1));
         fence_mbar_init();
         *s_abort = 0, *s_again = 0;
-        tma_prefetch_desc(&qmap), tma_prefetch_desc(&kmap), tma_prefetch_desc(&vmap);
+        if (!KV4) tma_prefetch_desc(&qmap), tma_prefetch_desc(&kmap), tma_prefetch_desc(&vmap);
     }
     if (warp == kMmaWarp) {
         tmem_alloc(s_tmem, 512);
@@ -416,11 +518,42 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
     };
 
     if (warp >= kTmaWarp) {
-        if constexpr (NQ == 2) regs_dec<C::REGS_IO>();
+        if constexpr (C::SPLIT_REGS) regs_dec<C::REGS_IO>();
         auto slot_of = [&](uint32_t s) { return s % SLOTS; };
         auto phase_of = [&](uint32_t s) { return (s / SLOTS) & 1; };
         uint32_t seq = 0;  // loads before this item: K_j is load seq + 2 j, V_j the one after it
-        if (warp == kTmaWarp) {
+        if (KV4 && warp >= kTmaWarp + 4) {
+            // ------------------------------------------------------------ queries, keys and values to fp16
+            if constexpr (KV4) {
+                const int ctid = tid - (kTmaWarp + 4) * 32;
+                uint32_t q_phase = 0;
+                while (next_item()) {
+                    RawTile<DP> raw;  // (the first keys come while the queries are converted)
+                    if (it.tiles > 0) raw.load(p, it, 0, false, ctid);
+                    const uint32_t k = (n_item - 1) & 3;
+#pragma unroll 1
+                    for (int t = 0; t < NQ; ++t) {
+                        if ((t ? it.n[1] : it.n[0]) == 0) continue;
+                        if (!wait_or_abort(q_empty + t, ((q_phase >> t) & 1) ^ 1, abort)) goto done;
+                        q_phase ^= 1u << t;
+                        convert_queries<DP>(p, it, t, sq + t * C::QBYTES, factors + (k * 2 + t) * 128, ctid);
+                        fence_async_smem();
+                        mbar_arrive(q_full + t);
+                    }
+                    mbar_arrive(f_full + k);
+#pragma unroll 1
+                    for (int i = 0; i < 2 * it.tiles; ++i) {
+                        const uint32_t slot = slot_of(seq + i);
+                        if (!wait_or_abort(empty + slot, phase_of(seq + i) ^ 1, abort)) goto done;
+                        raw.store(ring + slot * C::SLOT, ctid);
+                        fence_async_smem();
+                        mbar_arrive(full + slot);
+                        if (i + 1 < 2 * it.tiles) raw.load(p, it, (i + 1) >> 1, (i + 1) & 1, ctid);
+                    }
+                    seq += 2 * it.tiles;
+                }
+            }
+        } else if (warp == kTmaWarp) {
             // ------------------------------------------------------------ loads
             uint32_t q_phase = 0;
             const int boxes = BN / p.box_rows;  // boxes of a 64-channel block of a key tile
@@ -438,7 +571,15 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                 return true;
             };
             while (true) {
-                if (!get_item<DP>(p, suffix, first + (back ? gridDim.x - 1 - blockIdx.x : blockIdx.x), it)) {
+                const bool more = get_item<DP>(p, suffix, first + (back ? gridDim.x - 1 - blockIdx.x : blockIdx.x), it);
+                if (KV4) {
+                    if (!more) it.b = -1;
+                    if (!send()) goto done;
+                    if (!more) break;
+                    first += gridDim.x, back = !back;
+                    continue;
+                }
+                if (!more) {
                     // An item of nothing: when it has been taken, the items before it are at their end.  If one of
                     // them found cause, all are sent again.
                     it = Item{};
@@ -496,8 +637,9 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
         } else if (warp < kMmaWarp + NQ) {
             // ------------------------------------------------------------ products of query tile t
             const int t = warp - kMmaWarp;
-            const uint32_t id_s = idesc_bf16(128, BN, false, false) | (p.negate ? 1u << 13 : 0u);
-            const uint32_t id_o = idesc_bf16(128, DP, false, true);
+            constexpr uint32_t kTypes = KV4 ? 1u << 7 | 1u << 10 : 0u;  // (without these bits: fp16)
+            const uint32_t id_s = (idesc_bf16(128, BN, false, false) & ~kTypes) | (!KV4 && p.negate ? 1u << 13 : 0u);
+            const uint32_t id_o = idesc_bf16(128, DP, false, true) & ~kTypes;
             const uint64_t qd0 = sdesc_sw128(smem_u32(sq) + t * C::QBYTES, 16, 1024);
             const uint32_t r_addr = smem_u32(ring), o_tmem = tmem + C::COL_O + t * DP;
             uint32_t q_phase = 0, p_phase = 0, fix_phase = 0;  // one bit a barrier
@@ -538,7 +680,7 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                     }
                     // (all that the products wait for but P comes before P)
                     if (!wait_slot(seq + 2 * j + 1)) goto done;
-                    if (it.changes_v(j, BN)) {
+                    if (!KV4 && it.changes_v(j, BN)) {
                         if (!wait_or_abort(v_fixed + v, (fix_phase >> v) & 1, abort)) goto done;
                         fix_phase ^= 1u << v;
                     }
@@ -573,7 +715,7 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                     if (NQ == 2 && j + 1 < n) scores(j + 1);
                 }
             }
-        } else if (warp == kFixWarp) {
+        } else if (!KV4 && warp == kFixWarp) {
             // ------------------------------------------------------------ rows of V past the last key, and in
             // a second pass its non-finite values
             for (; next_item(); seq += 2 * it.tiles) {
@@ -598,7 +740,7 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
             }
         }
     } else {
-        if constexpr (NQ == 2) regs_inc<C::REGS_SOFTMAX>();
+        if constexpr (C::SPLIT_REGS) regs_inc<C::REGS_SOFTMAX>();
         // ---------------------------------------------------------------- softmax of query tile t
         const int t = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -612,6 +754,12 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
             const int n = NQ == 2 && t ? it.n[1] : it.n[0];
             const int least = shift + first + 1;  // keys that the tile's first row sees
             float m = -INFINITY, l = 0.f;
+            float pc = p.c;
+            if constexpr (KV4) {
+                const uint32_t k = (n_item - 1) & 3;
+                if (!wait_or_abort(f_full + k, ((n_item - 1) >> 2) & 1, abort)) goto done;
+                pc = n > 0 ? factors[(k * 2 + t) * 128 + row] : 1.f;
+            }
             for (int j = 0; j < it.tiles; ++j) {
                 if (j >= n) {  // only the other query tile sees these keys
                     if (!wait_or_abort(turn + t, turn_phase, abort)) goto done;
@@ -652,9 +800,9 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 if (m == -INFINITY) m = top;  // nothing summed yet
                 // rescale O when the reference of some row of the warp has to move
-                const bool move = (top - m) * p.c > kLazy;
+                const bool move = (top - m) * pc > kLazy;
                 if (__any_sync(0xffffffffu, move)) {
-                    const float f = move ? exp2_fast((m - top) * p.c) : 1.f;
+                    const float f = move ? exp2_fast((m - top) * pc) : 1.f;
                     if (move) m = top, l *= f;
                     // (j > 0 here: a first tile sets m itself)
                     const int prev = NQ == 2 ? t : buf ^ 1;
@@ -672,7 +820,7 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                     }
                     tmem_wait_st();
                 }
-                const float mc = m == -INFINITY ? 0.f : -m * p.c;
+                const float mc = (m == -INFINITY ? 0.f : -m * pc) + (KV4 ? kKv4Shift : 0.f);
                 float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int c = 0; c < BN / 64; ++c) {
@@ -681,11 +829,16 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                     for (int i = 0; i < 32; ++i) {
                         const float2 s2 = make_float2(__uint_as_float(x[2 * c + (i >> 4)][(2 * i) & 31]),
                                                       __uint_as_float(x[2 * c + (i >> 4)][(2 * i + 1) & 31]));
-                        float2 e = __ffma2_rn(s2, make_float2(p.c, p.c), make_float2(mc, mc));
+                        float2 e = __ffma2_rn(s2, make_float2(pc, pc), make_float2(mc, mc));
                         e.x = exp2_fast(e.x), e.y = exp2_fast(e.y);
                         sum = __fadd2_rn(sum, e);
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(e.x, e.y);
-                        pk[i] = *reinterpret_cast<const uint32_t *>(&h);
+                        if constexpr (KV4) {
+                            const __half2 h = __floats2half2_rn(e.x, e.y);
+                            pk[i] = *reinterpret_cast<const uint32_t *>(&h);
+                        } else {
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(e.x, e.y);
+                            pk[i] = *reinterpret_cast<const uint32_t *>(&h);
+                        }
                     }
                     tmem_st32(s_col + c * 32, pk);
                     if (NQ == 2 && c == 0) {
@@ -709,12 +862,13 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                 tc_fence_after();
             }
             const bool whole = p.splits == 1;
-            const float inv = !whole ? 1.f : l > 0.f ? 1.f / l : l;  // (0 gives 0, NaN stays)
+            const float vs = KV4 && p.vs ? __ldg(p.vs + it.h / p.G) : 1.f;
+            const float inv = !whole ? vs : l > 0.f ? vs / l : l;  // (0 gives 0, NaN stays)
             const int head = it.h + (p.pair ? t : row & ((1 << p.packed) - 1));
             const size_t out_row = (size_t)(it.start + r) * p.a.H + head;
             __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) + out_row * p.a.D;
             const Part part(p.a, p.splits, out_row, it.split);
-            if (!whole && r < it.len) part.ml[0] = m * p.c, part.ml[1] = l;
+            if (!whole && r < it.len) part.ml[0] = m * pc, part.ml[1] = l;
             uint32_t odd = 0;  // chunks of 32 channels with values that are not finite
             constexpr int OC = DP < 128 ? DP / 32 : 4;  // chunks loaded at a time
 #pragma unroll 1
@@ -749,6 +903,9 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
                     if (finite[0].x + finite[0].y + finite[1].x + finite[1].y != 0.f) odd |= 1u << (c >> 5);
                     if (r >= it.len) continue;
                     if (!whole) {
+                        if constexpr (KV4)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[k][i] = __float_as_uint(__uint_as_float(o[k][i]) * inv);
 #pragma unroll
                         for (int i = 0; i < 32; i += 8)
                             if (c + i < p.a.D) store32(part.o + c + i, &o[k][i]);
@@ -768,7 +925,7 @@ __global__ void __launch_bounds__(Cfg<DP>::THREADS, 1)
             // (a second pass: all keys that the V tiles were mended from)
             const bool mending = it.end >= kMend;
             const int k0 = max(it.lo * BN, mending ? it.masked() : least), k1 = min(it.kv, (it.lo + n) * BN);
-            if (k0 < k1 && (mending || __any_sync(0xffffffffu, odd != 0))) {
+            if (!KV4 && k0 < k1 && (mending || __any_sync(0xffffffffu, odd != 0))) {
                 bool found = false;
 #pragma unroll 1
                 for (int c = 0; c < p.a.D; c += 32)
@@ -788,7 +945,7 @@ done:
     tc_fence_before();
     __syncthreads();
     if (*abort) {  // copies and products in flight end before the CTA's memory goes
-        if (warp == kTmaWarp)
+        if (!KV4 && warp == kTmaWarp)
             for (int i = 0; i < SLOTS; ++i) {
                 mbar_wait(full + i, 0, 1000000), mbar_wait(full + i, 1, 1000000);
                 if (i < NQ) mbar_wait(q_full + i, 0, 1000000), mbar_wait(q_full + i, 1, 1000000);
@@ -862,11 +1019,13 @@ int packed_heads(int G, int max_q) {
 // tokens, 32 heads of 128 on 8: 70 us with 256 tokens, 53 with pairs).
 bool paired_heads(int G, int D, int packed) { return packed == 0 && D <= 128 && G % 2 == 0; }
 
-template <int DP>
-cudaError_t launch(const Attn &a, int min_rows, int splits, cudaStream_t s) {
-    using C = Cfg<DP>;
+template <int DP, bool KV4>
+cudaError_t launch(const Attn &a, int min_rows, int splits, cudaStream_t s, const float *ks = nullptr, const float *vs = nullptr) {
+    using C = Cfg<DP, KV4>;
     PromptParams p{};
     p.a = a;
+    p.ks = ks, p.vs = vs;
+    p.q_wide = rows_aligned(a.q, a.qs, a.D, 2);
     p.G = a.H / a.HKV;
     p.min_rows = min_rows;
     p.c = std::fmax(std::fabs(a.scale) * kLog2e, 1e-30f);
@@ -883,15 +1042,15 @@ cudaError_t launch(const Attn &a, int min_rows, int splits, cudaStream_t s) {
     while (((levels + (1L << p.bin_shift) - 1) >> p.bin_shift) > kMaxBins) ++p.bin_shift;
     p.bins = (int)((levels + (1L << p.bin_shift) - 1) >> p.bin_shift);
     const long kv_rows = paged ? (long)a.num_pages * a.page_size : a.N;
-    CUtensorMap qm, km, vm;
-    if (!encode_rows(&qm, a.q, a.N, a.H, a.D, a.qs, 1 << p.packed, 128 >> p.packed) ||
-        !encode_rows(&km, a.k, kv_rows, a.HKV, a.D, a.ks, 1, p.box_rows) ||
-        !encode_rows(&vm, a.v, kv_rows, a.HKV, a.D, a.vs, 1, p.box_rows))
+    CUtensorMap qm{}, km{}, vm{};
+    if (!KV4 && (!encode_rows(&qm, a.q, a.N, a.H, a.D, a.qs, 1 << p.packed, 128 >> p.packed) ||
+                 !encode_rows(&km, a.k, kv_rows, a.HKV, a.D, a.ks, 1, p.box_rows) ||
+                 !encode_rows(&vm, a.v, kv_rows, a.HKV, a.D, a.vs, 1, p.box_rows)))
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> attr_set{0};
-    constexpr size_t kFixed = (size_t)C::NQ * C::QBYTES + C::SLOTS * C::SLOT + 512 + 1024;
+    constexpr size_t kFixed = (size_t)C::NQ * C::QBYTES + C::SLOTS * C::SLOT + C::FACTORS + 512 + 1024;
     cudaError_t e = once_per_device(attr_set, [] {
-        return cudaFuncSetAttribute(attn_prompt_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(attn_prompt_kernel<DP, KV4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)(kFixed + (kMaxBins + 1) * 4));
     });
     if (e != cudaSuccess) return e;
@@ -904,7 +1063,7 @@ cudaError_t launch(const Attn &a, int min_rows, int splits, cudaStream_t s) {
     while (p.splits * 2 <= splits && p.splits * 8 <= key_tiles) p.splits *= 2;
     const long items = ((long)a.N / p.tm + a.B) * p.heads * p.splits;
     const long grid = items < sms ? items : sms;
-    e = launch_kernel(attn_prompt_kernel<DP>, dim3((unsigned)grid), dim3(C::THREADS), kFixed + (p.bins + 1) * 4, s,
+    e = launch_kernel(attn_prompt_kernel<DP, KV4>, dim3((unsigned)grid), dim3(C::THREADS), kFixed + (p.bins + 1) * 4, s,
                       true, qm, km, vm, p);
     note_launch();
     if (e != cudaSuccess || p.splits == 1) return e;
@@ -967,9 +1126,16 @@ bool attention_prompt_supported(const Attn &a, int dtype) {
 
 cudaError_t launch_attention_prompt(const Attn &a, int min_rows, cudaStream_t s) {
     const int splits = a.part == nullptr ? 1 : prompt_splits(a.B, a.N, a.H, a.HKV, a.D, a.max_q, min_rows);
-    if (a.D <= 64) return launch<64>(a, min_rows, splits, s);
-    if (a.D <= 128) return launch<128>(a, min_rows, splits, s);
-    return launch<256>(a, min_rows, splits, s);
+    if (a.D <= 64) return launch<64, false>(a, min_rows, splits, s);
+    if (a.D <= 128) return launch<128, false>(a, min_rows, splits, s);
+    return launch<256, false>(a, min_rows, splits, s);
+}
+
+cudaError_t launch_attention_prompt_kv4(const Attn &a, const float *ks, const float *vs, int min_rows, cudaStream_t s) {
+    const int splits = prompt_splits(a.B, a.N, a.H, a.HKV, a.D, a.max_q, min_rows);
+    if (a.D <= 64) return launch<64, true>(a, min_rows, splits, s, ks, vs);
+    if (a.D <= 128) return launch<128, true>(a, min_rows, splits, s, ks, vs);
+    return launch<256, true>(a, min_rows, splits, s, ks, vs);
 }
 
 }  // namespace gdn

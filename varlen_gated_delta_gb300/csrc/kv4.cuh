@@ -58,4 +58,12 @@ __device__ __forceinline__ uint32_t kv4_encode(const float (&t)[8]) {
     return r;
 }
 
+// The power of two that brings a row's largest magnitude into [1, 2), and its inverse (for rows below 2^-63, nothing
+// but zeros among them, 2^63, so that the inverse stays far from zero).
+__device__ __forceinline__ float kv4_row_power(float amax, float &inverse) {
+    const int e = max(64, min((int)(__float_as_uint(amax) >> 23 & 255u), 253));  // (biased)
+    inverse = __uint_as_float((uint32_t)e << 23);
+    return __uint_as_float((uint32_t)(254 - e) << 23);
+}
+
 }  // namespace gdn

@@ -93,6 +93,9 @@ struct Kv4Write {
 };
 cudaError_t launch_kv4_write(const Kv4Write &p, int dtype, cudaStream_t s);
 
+// bf16 sequences of more than min_rows rows over a 4-bit cache.
+cudaError_t launch_attention_prompt_kv4(const Attn &a, const float *ks, const float *vs, int min_rows, cudaStream_t s);
+
 // Any rows; a.k and a.v are the 4-bit caches.
 size_t attention_kv4_workspace(int B, int N, int H, int HKV, int D, int max_q);
 cudaError_t launch_attention_kv4(const Attn &a, const float *k_scale, const float *v_scale, int dtype, void *ws,
