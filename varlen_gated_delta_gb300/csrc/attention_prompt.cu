@@ -65,7 +65,7 @@ using namespace sm100;
 // A try suspends the warp for up to 3.8 us: some 2 s of the kernel's own time, however long the GPU
 // belongs to others meanwhile.
 constexpr int kWaitTries = 1 << 19;
-constexpr int kMaxBins = 4096;  // bins of the longest-first order
+constexpr int kMaxBins = 4096;  // bins of the longest-first order (half for KV4, whose shared memory is full)
 constexpr float kLazy = 8.f;    // growth of the row maximum (log2) that O waits for
 constexpr float kKv4Shift = 7.f;  // log2 of the factor of fp16 probabilities: 2^(kLazy + 7) still fits
 
@@ -79,8 +79,8 @@ __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.a
 template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 
-// KV4: the cache holds 4-bit values (kv4.cuh).  A warpgroup more turns them, and the queries, into fp16 tiles; the load warp
-// then only hands out items.
+// KV4: the cache holds 4-bit values (kv4.cuh).  The load warp copies codes and scales to a ring of their own, and a warpgroup
+// more turns them, and the queries, into fp16 tiles.
 template <int DP, bool KV4 = false>
 struct Cfg {
     static constexpr int NQ = DP > 128 ? 1 : 2;    // query tiles of a CTA
@@ -97,11 +97,14 @@ struct Cfg {
     // registers a thread at launch and after the split: a softmax thread holds a row of scores
     static constexpr int REGS = 65536 / THREADS / 8 * 8 > 255 ? 248 : 65536 / THREADS / 8 * 8;
     static constexpr bool SPLIT_REGS = NQ == 2 || KV4;
-    static constexpr int REGS_IO = !KV4 ? 96 : NQ == 2 ? 64 : 128;
-    static constexpr int REGS_SOFTMAX = !SPLIT_REGS ? REGS : !KV4 ? 200 : NQ == 2 ? 192 : 248;
+    static constexpr int REGS_IO = !KV4 ? 96 : NQ == 2 ? 72 : 128;
+    static constexpr int REGS_SOFTMAX = !SPLIT_REGS ? REGS : !KV4 ? 200 : NQ == 2 ? 184 : 248;
     static_assert(NQ * REGS_SOFTMAX + IO * REGS_IO <= (NQ + IO) * REGS, "more registers than the CTA was launched with");
-    // KV4: softmax factors of the rows of four items, and the barriers that tell of them
-    static constexpr int FACTORS = KV4 ? 4 * 2 * 128 * 4 + 4 * 8 : 0;
+    // KV4: codes and scales of a tile of keys (or values), and how many of those there are; softmax factors of the rows
+    // of four items; the barriers of both, and which tokens of a raw tile are there
+    static constexpr int RAW = BN * DP / 16 * 9, RAWS = 2;
+    static constexpr int EXTRA = KV4 ? RAWS * RAW + 4 * 2 * 128 * 4 + 4 * 8 + RAWS * (2 * 8 + 8) : 0;
+    static constexpr int MAX_BINS = KV4 ? kMaxBins / 2 : kMaxBins;
     // tensor memory: two score buffers, then O of each query tile
     static constexpr int COL_O = 2 * BN;
 };
@@ -387,44 +390,31 @@ __device__ __forceinline__ void convert_queries(const PromptParams &p, const Ite
     }
 }
 
-// Codes and scales of a tile of keys (or values), some groups of 16 channels to each thread, on their way in registers.
+// A raw tile of keys (or values) to fp16, 16 channels at a time.  Bit i of `there`: tokens 16 i .. 16 i + 15 were copied; the
+// others (past the last key, or of a page outside the cache) read as zeros.
 template <int DP>
-struct RawTile {
-    static constexpr int BN = Cfg<DP, true>::BN, GROUPS = DP / 16, N = BN * GROUPS / 128;
-    uint2 codes[N];
-    uint32_t scale[N];
-    __device__ __forceinline__ void load(const PromptParams &p, const Item &it, int j, bool values, int tid) {
-        const int grp = tid % GROUPS, GR = p.a.D / 16, ps = p.a.page_size;
-        const uint8_t *cache = static_cast<const uint8_t *>(values ? p.a.v : p.a.k);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int key = (it.lo + j) * BN + tid / GROUPS + i * (128 / GROUPS);
-            codes[i] = make_uint2(0, 0), scale[i] = 0;
-            if (key >= it.kv || grp >= GR) continue;
-            const int index = key / ps, at = key - index * ps;
-            const int page = __ldg(p.a.block_table + (size_t)it.b * p.a.max_pages + index);
-            if (page < 0 || page >= p.a.num_pages) continue;  // (reads as zeros)
-            const uint8_t *block = cache + ((long)page * p.a.HKV + it.h / p.G) * ((long)ps * GR * 9);
-            codes[i] = __ldg(reinterpret_cast<const uint2 *>(block + ((long)at * GR + grp) * 8));
-            scale[i] = __ldg(block + (long)ps * GR * 8 + at * GR + grp);
+__device__ __forceinline__ void convert_tile(int D, const unsigned char *raw, uint32_t there, unsigned char *slot, int tid) {
+    constexpr int BN = Cfg<DP, true>::BN, GROUPS = DP / 16;
+    const int grp = tid % GROUPS, GR = D / 16;
+#pragma unroll 4
+    for (int i = 0; i < BN * GROUPS / 128; ++i) {
+        const int key = tid / GROUPS + i * (128 / GROUPS);
+        uint2 codes = make_uint2(0, 0);
+        uint32_t s = 0;
+        if ((there >> (key >> 4) & 1) && grp < GR) {
+            codes = *reinterpret_cast<const uint2 *>(raw + (key * GR + grp) * 8);
+            s = raw[BN * GR * 8 + key * GR + grp];
         }
-    }
-    __device__ __forceinline__ void store(unsigned char *slot, int tid) const {
-        const int grp = tid % GROUPS;
+        s = kv4_scales(s | s << 8);
+        unsigned char *row = slot + (grp >> 2) * BN * 128 + key * 128;
+        uint32_t d[2][4];
+        kv4_codes(codes.x, d[0]), kv4_codes(codes.y, d[1]);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int key = tid / GROUPS + i * (128 / GROUPS);
-            const uint32_t s = kv4_scales(scale[i] | scale[i] << 8);
-            unsigned char *row = slot + (grp >> 2) * BN * 128 + key * 128;
-            uint32_t d[2][4];
-            kv4_codes(codes[i].x, d[0]), kv4_codes(codes[i].y, d[1]);
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-                *reinterpret_cast<uint4 *>(row + ((((grp & 3) * 2 + half) ^ (key & 7)) << 4)) =
-                    make_uint4(mul_f16x2(d[half][0], s), mul_f16x2(d[half][1], s), mul_f16x2(d[half][2], s), mul_f16x2(d[half][3], s));
-        }
+        for (int half = 0; half < 2; ++half)
+            *reinterpret_cast<uint4 *>(row + ((((grp & 3) * 2 + half) ^ (key & 7)) << 4)) =
+                make_uint4(mul_f16x2(d[half][0], s), mul_f16x2(d[half][1], s), mul_f16x2(d[half][2], s), mul_f16x2(d[half][3], s));
     }
-};
+}
 
 template <int DP, bool KV4>
 __global__ void __launch_bounds__(Cfg<DP, KV4>::THREADS, 1)
@@ -436,9 +426,11 @@ __global__ void __launch_bounds__(Cfg<DP, KV4>::THREADS, 1)
     unsigned char *smem = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     unsigned char *sq = smem, *ring = smem + NQ * C::QBYTES;
-    float *factors = reinterpret_cast<float *>(ring + SLOTS * C::SLOT);  // KV4: [4 items][2 query tiles][128 rows]
-    uint64_t *f_full = reinterpret_cast<uint64_t *>(factors + 4 * 2 * 128);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(ring + SLOTS * C::SLOT + C::FACTORS);
+    unsigned char *raws = ring + SLOTS * C::SLOT;  // (this and the next three: KV4)
+    float *factors = reinterpret_cast<float *>(raws + C::RAWS * C::RAW);  // [4 items][2 query tiles][128 rows]
+    uint64_t *f_full = reinterpret_cast<uint64_t *>(factors + 4 * 2 * 128), *raw_full = f_full + 4, *raw_empty = raw_full + C::RAWS;
+    volatile uint32_t *s_there = reinterpret_cast<uint32_t *>(raw_empty + C::RAWS);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(ring + SLOTS * C::SLOT + C::EXTRA);
     uint64_t *full = bars, *empty = full + SLOTS, *q_full = empty + SLOTS, *q_empty = q_full + 2,
              *s_full = q_empty + 2, *p_full = s_full + 2, *o_done = p_full + 2, *v_fixed = o_done + 2, *turn = v_fixed + SLOTS,
              *p_half = turn + 2, *item_full = p_half + 2, *item_empty = item_full + 4, *drained = item_empty + 4;
@@ -460,6 +452,7 @@ __global__ void __launch_bounds__(Cfg<DP, KV4>::THREADS, 1)
             mbar_init(empty + i, KV4 ? NQ : NQ + (i & 1));
             mbar_init(v_fixed + i, 32);
             if (KV4) mbar_init(f_full + i, 128);
+            if (KV4 && i < C::RAWS) mbar_init(raw_full + i, 1), mbar_init(raw_empty + i, 4);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full + i, KV4 ? 128 : 1), mbar_init(q_empty + i, 1);
@@ -528,8 +521,6 @@ __global__ void __launch_bounds__(Cfg<DP, KV4>::THREADS, 1)
                 const int ctid = tid - (kTmaWarp + 4) * 32;
                 uint32_t q_phase = 0;
                 while (next_item()) {
-                    RawTile<DP> raw;  // (the first keys come while the queries are converted)
-                    if (it.tiles > 0) raw.load(p, it, 0, false, ctid);
                     const uint32_t k = (n_item - 1) & 3;
 #pragma unroll 1
                     for (int t = 0; t < NQ; ++t) {
@@ -542,15 +533,17 @@ __global__ void __launch_bounds__(Cfg<DP, KV4>::THREADS, 1)
                     }
                     mbar_arrive(f_full + k);
 #pragma unroll 1
-                    for (int i = 0; i < 2 * it.tiles; ++i) {
-                        const uint32_t slot = slot_of(seq + i);
-                        if (!wait_or_abort(empty + slot, phase_of(seq + i) ^ 1, abort)) goto done;
-                        raw.store(ring + slot * C::SLOT, ctid);
+                    for (int i = 0; i < 2 * it.tiles; ++i, ++seq) {
+                        const uint32_t slot = slot_of(seq), r = seq % C::RAWS;
+                        if (!wait_or_abort(raw_full + r, (seq / C::RAWS) & 1, abort) ||
+                            !wait_or_abort(empty + slot, phase_of(seq) ^ 1, abort))
+                            goto done;
+                        convert_tile<DP>(p.a.D, raws + r * C::RAW, s_there[r], ring + slot * C::SLOT, ctid);
                         fence_async_smem();
                         mbar_arrive(full + slot);
-                        if (i + 1 < 2 * it.tiles) raw.load(p, it, (i + 1) >> 1, (i + 1) & 1, ctid);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(raw_empty + r);
                     }
-                    seq += 2 * it.tiles;
                 }
             }
         } else if (warp == kTmaWarp) {
@@ -576,6 +569,33 @@ __global__ void __launch_bounds__(Cfg<DP, KV4>::THREADS, 1)
                     if (!more) it.b = -1;
                     if (!send()) goto done;
                     if (!more) break;
+                    // pieces of box_rows tokens, that many to a tile; even lanes copy codes, odd ones scales
+                    const int piece = lane >> 1, GR = p.a.D / 16, ps = p.a.page_size, kvh = it.h / p.G;
+#pragma unroll 1
+                    for (int j = 0; j < it.tiles; ++j) {
+                        const int key = (it.lo + j) * BN + piece * p.box_rows, index = key / ps, at = key - index * ps;
+                        int page = -1;
+                        if (piece < boxes && key < it.kv) page = __ldg(p.a.block_table + (size_t)it.b * p.a.max_pages + index);
+                        const bool read = page >= 0 && page < p.a.num_pages;
+                        const uint32_t pieces = __ballot_sync(0xffffffffu, read && !(lane & 1));
+                        uint32_t there = 0;  // blocks of 16 tokens of this piece, then of all
+                        if (read) there = ((1u << (p.box_rows >> 4)) - 1u) << (piece * (p.box_rows >> 4));
+                        there = __reduce_or_sync(0xffffffffu, there);
+                        const long block = read ? ((long)page * p.a.HKV + kvh) * ((long)ps * GR * 9) : 0;
+                        const long from = block + (lane & 1 ? ((long)ps * 8 + at) * GR : (long)at * GR * 8);
+                        const uint32_t bytes = p.box_rows * GR * (lane & 1 ? 1 : 8), to = (lane & 1 ? BN * GR * 8 : 0) + piece * bytes;
+#pragma unroll 1
+                        for (int kv = 0; kv < 2; ++kv, ++seq) {
+                            const uint32_t r = seq % C::RAWS;
+                            if (!wait_or_abort(raw_empty + r, ((seq / C::RAWS) & 1) ^ 1, abort)) goto done;
+                            if (lane == 0) {
+                                s_there[r] = there;
+                                mbar_arrive_expect_tx(raw_full + r, __popc(pieces) * p.box_rows * GR * 9);
+                            }
+                            __syncwarp();
+                            if (read) bulk_load(raws + r * C::RAW + to, static_cast<const unsigned char *>(kv ? p.a.v : p.a.k) + from, bytes, raw_full + r);
+                        }
+                    }
                     first += gridDim.x, back = !back;
                     continue;
                 }
@@ -945,6 +965,8 @@ done:
     tc_fence_before();
     __syncthreads();
     if (*abort) {  // copies and products in flight end before the CTA's memory goes
+        if (KV4 && warp == kTmaWarp)
+            for (int i = 0; i < C::RAWS; ++i) mbar_wait(raw_full + i, 0, 1000000), mbar_wait(raw_full + i, 1, 1000000);
         if (!KV4 && warp == kTmaWarp)
             for (int i = 0; i < SLOTS; ++i) {
                 mbar_wait(full + i, 0, 1000000), mbar_wait(full + i, 1, 1000000);
@@ -1039,7 +1061,7 @@ cudaError_t launch(const Attn &a, int min_rows, int splits, cudaStream_t s, cons
     p.tm = p.pair ? 128 : C::NQ * 128 >> p.packed;
     p.heads = a.H >> (p.packed + p.pair);
     const long levels = ((long)a.max_q + p.tm - 1) / p.tm;
-    while (((levels + (1L << p.bin_shift) - 1) >> p.bin_shift) > kMaxBins) ++p.bin_shift;
+    while (((levels + (1L << p.bin_shift) - 1) >> p.bin_shift) > C::MAX_BINS) ++p.bin_shift;
     p.bins = (int)((levels + (1L << p.bin_shift) - 1) >> p.bin_shift);
     const long kv_rows = paged ? (long)a.num_pages * a.page_size : a.N;
     CUtensorMap qm{}, km{}, vm{};
@@ -1048,10 +1070,10 @@ cudaError_t launch(const Attn &a, int min_rows, int splits, cudaStream_t s, cons
                  !encode_rows(&vm, a.v, kv_rows, a.HKV, a.D, a.vs, 1, p.box_rows)))
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> attr_set{0};
-    constexpr size_t kFixed = (size_t)C::NQ * C::QBYTES + C::SLOTS * C::SLOT + C::FACTORS + 512 + 1024;
+    constexpr size_t kFixed = (size_t)C::NQ * C::QBYTES + C::SLOTS * C::SLOT + C::EXTRA + 512 + 1024;
     cudaError_t e = once_per_device(attr_set, [] {
         return cudaFuncSetAttribute(attn_prompt_kernel<DP, KV4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)(kFixed + (kMaxBins + 1) * 4));
+                                    (int)(kFixed + (C::MAX_BINS + 1) * 4));
     });
     if (e != cudaSuccess) return e;
     int dev = 0, sms = 0;
