@@ -67,6 +67,14 @@ def test_masked_logits_and_beams(V):
     scores = torch.tensor([[0.0, -1.0, -inf, -0.5], [-1.0, -inf, float("nan"), -2.0]], device="cuda")
     for n in (4, 6):
         _check(logits, scores, n, gdn.gdn_beam_select(logits, scores, n=n))
+    # masks of the type's lowest value, a whole row of them among others, and logits of any size
+    for dtype in (F32, BF16):
+        low = torch.finfo(dtype).min
+        big = torch.randn(8, V, generator=gen, device="cuda").to(dtype)
+        big[0], big[1, 4:], big[2, ::2], big[3] = low, low, low, big[3] * 1e6
+        big[4], big[5, 7], big[6] = big[4] * 1e30, -low, big[6] + 3e4
+        zero = torch.zeros(2, 4, device="cuda")
+        _check(big, zero, 4, gdn.gdn_beam_select(big, zero))
     # the first step of a search: one live beam
     scores = torch.tensor([[0.0, -inf, -inf, -inf]], device="cuda")
     _check(logits[1:5], scores, 4, gdn.gdn_beam_select(logits[1:5], scores))

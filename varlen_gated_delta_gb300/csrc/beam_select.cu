@@ -24,7 +24,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kList = 1024;  // candidates that are ranked by counting
-constexpr int kNear = 4096;  // candidates of a group whose totals are kept in shared memory
+constexpr int kNear = 3072;  // candidates of a group that are kept in shared memory
 
 struct Pieces {  // in the workspace
     float *m;    // [rows][pieces]: maximum
@@ -71,34 +71,33 @@ __device__ __forceinline__ void warp_sum_two(float &hi, float &lo) {
 }
 
 // The n-th largest (any of them, if there are fewer) of the maxima of `groups` (32 or 256) equal sets of neighbouring
-// threads.  Calls have a barrier between them.
-__device__ __forceinline__ float nth_maximum(float x, int n, int groups, float *s_all, float *s_warp) {
+// threads.
+__device__ __forceinline__ float nth_maximum(float x, int n, int groups, float *s_all, float *s_nth) {
     const int tid = threadIdx.x;
-    if (groups == 32) {
+    if (groups == 32) {  // (one warp ranks them)
 #pragma unroll
         for (int d = 4; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
         if (tid % 8 == 0) s_all[tid / 8] = x;
-        __syncthreads();
-        x = s_all[tid & 31];
     } else {
         s_all[tid] = x;
-        __syncthreads();
     }
-    int larger = 0;
-#pragma unroll 8
-    for (int i = 0; i < groups; i += 4) {
-        const float4 y = *reinterpret_cast<const float4 *>(s_all + i);
-        larger += (y.x > x) + (y.y > x) + (y.z > x) + (y.w > x);
-    }
-    x = larger < n ? x : INFINITY;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) x = fminf(x, __shfl_xor_sync(0xffffffffu, x, d));
-    if (groups == 32) return x;
-    if ((tid & 31) == 0) s_warp[tid >> 5] = x;
     __syncthreads();
-    x = s_warp[0];
+    if (tid < groups) {
+        x = s_all[tid];
+        int larger = 0;
+#pragma unroll 8
+        for (int i = 0; i < groups; i += 4) {
+            const float4 y = *reinterpret_cast<const float4 *>(s_all + i);
+            larger += (y.x > x) + (y.y > x) + (y.z > x) + (y.w > x);
+        }
+        x = larger < n ? x : INFINITY;
 #pragma unroll
-    for (int w = 1; w < kThreads / 32; ++w) x = fminf(x, s_warp[w]);
+        for (int d = 16; d > 0; d >>= 1) x = fminf(x, __shfl_xor_sync(0xffffffffu, x, d));
+        if ((tid & 31) == 0) s_nth[tid >> 5] = x;
+    }
+    __syncthreads();
+    x = s_nth[0];
+    for (int w = 1; w < groups / 32; ++w) x = fminf(x, s_nth[w]);
     return x;
 }
 
@@ -110,6 +109,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
     __shared__ float s_warp[kThreads / 32], s_sum[2][kThreads / 32];
     __shared__ __align__(16) float s_all[kThreads];
     __shared__ unsigned long long s_list[kList], s_top[kThreads / 32];
+    __shared__ float s_nth[kThreads / 32];
     __shared__ int s_n;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long row = blockIdx.x / pieces;
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
     const long first = (long)piece * (ELEMS * kThreads) - skew;
 
     Vec16<T> w[VECS];
-    const auto value = [&](int i) { return fmaxf(to_f32(w[i / VEC].v[i % VEC]), -INFINITY); };  // (NaN is no candidate)
+    const auto value = [&](int i) { return to_f32(w[i / VEC].v[i % VEC]); };
     const auto token = [&](int i) { return (int)(first + (long)(i / VEC * kThreads + tid) * VEC + i % VEC); };
     if (tid == 0) s_n = 0;
 #pragma unroll
@@ -136,22 +136,53 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
             for (int i = 0; i < VEC; ++i) w[j].v[i] = at + i >= 0 && at + i < V ? x[at + i] : from_f32<T>(-INFINITY);
         }
     }
+    // (NaN is passed over: it is no candidate)
     float mine = -INFINITY;
+    if constexpr (sizeof(T) == 2) {
+        __nv_bfloat162 top = __float2bfloat162_rn(-INFINITY);
 #pragma unroll
-    for (int i = 0; i < ELEMS; ++i) mine = fmaxf(mine, value(i));
+        for (int j = 0; j < VECS; ++j)
+#pragma unroll
+            for (int i = 0; i < VEC / 2; ++i) top = __hmax2(top, reinterpret_cast<const __nv_bfloat162 *>(w + j)[i]);
+        mine = fmaxf(__low2float(top), __high2float(top));
+    } else {
+#pragma unroll
+        for (int i = 0; i < ELEMS; ++i) mine = fmaxf(mine, value(i));
+    }
     const float wm = warp_max(mine);
     if (lane == 0) s_warp[warp] = wm;
-    // (a barrier)
-    const float least = nth_maximum(mine, n, n <= 32 ? 32 : kThreads, s_all, s_sum[0]);
+    // (barriers)
+    const float least = nth_maximum(mine, n, n <= 32 ? 32 : kThreads, s_all, s_nth);
     float m = s_warp[0];
 #pragma unroll
     for (int w = 1; w < kThreads / 32; ++w) m = fmaxf(m, s_warp[w]);
 
-    // ---- sum, and the list of what reaches `least`
-    const float base = m == -INFINITY ? 0.f : m;
-    float part[4] = {0.f, 0.f, 0.f, 0.f};
+    // ---- sum of exp(x - m) = 2^(x L - m L), L = log2(e): a product and a sum in one rounding, and the rounding of m L, which
+    // all terms share, is taken back at the end (2^-t = 1 - t ln 2 + ..., t < 2^-10).  Large m, or a NaN: x - m first.
+    constexpr float kL = 1.4426950408889634f;
+    const float base = m == -INFINITY ? 0.f : m, mL = __fmul_rn(base, kL);
+    const auto sum_of = [&](auto term) {
+        float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-    for (int i = 0; i < ELEMS; ++i) part[i & 3] += __expf(value(i) - base);
+        for (int i = 0; i < ELEMS; i += 2) {
+            float2 e = term(make_float2(value(i), value(i + 1)));
+            asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+            asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+            part[i / 2 & 1] = __fadd2_rn(part[i / 2 & 1], e);
+        }
+        const float2 both = __fadd2_rn(part[0], part[1]);
+        return both.x + both.y;
+    };
+    float sum = sum_of([&](float2 x) { return __ffma2_rn(x, make_float2(kL, kL), make_float2(-mL, -mL)); }), lo = 0.f;
+    const float t = 0.69314718f * __fmaf_rn(base, kL, -mL);
+    sum *= 1.f + t * (0.5f * t - 1.f);
+    if (sum != sum || fabsf(base) > 8192.f)
+        sum = sum_of([&](float2 x) {
+            return make_float2((fmaxf(x.x, -INFINITY) - base) * kL, (fmaxf(x.y, -INFINITY) - base) * kL);
+        });
+    warp_sum_two(sum, lo);
+
+    // ---- the list of what reaches `least`
     // Few threads have such values: the warp reads those of one of them at a time again (registers would have to be indexed).
     const auto read = [&](long at) { return at >= 0 && at < V ? fmaxf(to_f32(x[at]), -INFINITY) : -INFINITY; };
     for (unsigned left = __ballot_sync(0xffffffffu, mine >= least && mine != -INFINITY); left != 0; left &= left - 1) {
@@ -162,11 +193,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
             if (k < kList) s_list[k] = key_of(v, (int)at);
         }
     }
-    float sum = part[0], lo = 0.f;
-#pragma unroll
-    for (int i = 1; i < 4; ++i) add_two(sum, lo, part[i], 0.f);
-    warp_sum_two(sum, lo);
-    __syncthreads();  // (their room has been used above)
     if (lane == 0) s_sum[0][warp] = sum, s_sum[1][warp] = lo;
     __syncthreads();
     const long o = row * pieces + piece;
@@ -228,59 +254,66 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamSelect p,
     __shared__ unsigned long long s_total[kList];
     __shared__ int s_at[kList], s_place[kBeamMaxN], s_rest[kBeamMaxN];
     __shared__ Pick s_pick[kBeamMaxN], s_top[kThreads / 32];
-    __shared__ float s_near[kNear];
+    __shared__ float s_x[kNear];
+    __shared__ int s_token[kNear];
     __shared__ int s_n;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = blockIdx.x, K = p.K, n = p.n;
-    // scores and flags may be written over below, by this CTA alone
+    const int per_beam = pieces * n, all = K * per_beam;
     pdl_wait_primary();
+    // All that is read comes at once: the candidates (as many as there is room for), scores and flags (which may be written
+    // over below, by this CTA alone), and the pieces' sums.
+#pragma unroll 4
+    for (int c = tid; c < min(all, kNear); c += kThreads) {
+        s_x[c] = __ldcg(in.x + (long)g * all + c);
+        s_token[c] = __ldcg(in.token + (long)g * all + c);
+    }
     if (tid == 0) s_n = 0;
     for (int k = tid; k < K; k += kThreads) {
         const float s = p.scores[(long)g * K + k];
         s_score[k] = s != s ? -INFINITY : s;
         s_done[k] = p.finished != nullptr && p.finished[(long)g * K + k] != 0;
     }
-    __syncthreads();
-    for (int k = warp; k < K; k += kThreads / 32) {
+    for (int k = warp; k < K; k += kThreads / 32) {  // (of a beam at its end: of no meaning)
+        const long o = ((long)g * K + k) * pieces;
         float m = -INFINITY, sum = 0.f, lo = 0.f;
-        if (!s_done[k]) {
-            const long o = ((long)g * K + k) * pieces;
-            for (int i = lane; i < pieces; i += 32) m = fmaxf(m, __ldcg(in.m + o + i));
-            m = warp_max(m);
-            for (int i = lane; i < pieces; i += 32) {
-                const float mi = __ldcg(in.m + o + i);
-                if (mi != -INFINITY) add_two(sum, lo, __ldcg(in.sum + o + i) * expf(mi - m), 0.f);
+        for (int i0 = 0; i0 < pieces; i0 += 32) {
+            const int i = i0 + lane;
+            const float mi = i < pieces ? __ldcg(in.m + o + i) : -INFINITY, si = i < pieces ? __ldcg(in.sum + o + i) : 0.f;
+            const float top = fmaxf(m, warp_max(mi));
+            if (top > m && m != -INFINITY) {
+                const float f = expf(m - top);
+                sum *= f, lo *= f;
             }
-            warp_sum_two(sum, lo);
+            m = top;
+            if (mi != -INFINITY) add_two(sum, lo, si * expf(mi - m), 0.f);
         }
+        warp_sum_two(sum, lo);
         if (lane == 0) s_m[k] = m, s_sum[k] = sum + lo;
     }
     __syncthreads();
     for (int k = tid; k < K; k += kThreads) {
-        const double lse = s_m[k] == -INFINITY ? -INFINITY : (double)s_m[k] + log((double)s_sum[k]);
+        const double lse = s_done[k] || s_m[k] == -INFINITY ? -INFINITY : (double)s_m[k] + log((double)s_sum[k]);
         s_lse[k] = lse, s_lse32[k] = (float)lse;
     }
     __syncthreads();
 
     // Candidate c of the group: beam and logit; -inf: none.  (A beam at its end goes on as it is, once.)
-    const int per_beam = pieces * n, all = K * per_beam;
     auto logit = [&](int c, int k) {
         if (s_done[k]) return c - k * per_beam == 0 ? 0.f : -INFINITY;
-        return __ldcg(in.x + (long)g * all + c);
+        return c < kNear ? s_x[c] : __ldcg(in.x + (long)g * all + c);
     };
     // Its total in 32 bits, near enough to leave most of them out.
     auto about = [&](float x, int k) { return s_done[k] ? s_score[k] + x : s_score[k] + (x - s_lse32[k]); };
     auto total = [&](int c, int k, float x) {
         return key_of(s_done[k] ? (double)s_score[k] : (double)s_score[k] + ((double)x - s_lse[k]));
     };
-    auto place = [&](int c, int k) { return k * p.V + (s_done[k] ? p.end_token : __ldcg(in.token + (long)g * all + c)); };
+    auto place = [&](int c, int k) { return k * p.V + (s_done[k] ? p.end_token : c < kNear ? s_token[c] : __ldcg(in.token + (long)g * all + c)); };
     float mine = -INFINITY, size = 0.f;
-#pragma unroll 4
     for (int c = tid; c < all; c += kThreads) {
         const int k = c / per_beam;
         const float x = logit(c, k), t = about(x, k);
-        const bool some = x != -INFINITY && t > -INFINITY;
-        if (c < kNear) s_near[c] = some ? t : -INFINITY;
-        if (some) mine = fmaxf(mine, t), size = fmaxf(size, fabsf(x) + (s_done[k] ? 0.f : fabsf(s_lse32[k])) + fabsf(s_score[k]));
+        if (x != -INFINITY && t > -INFINITY)
+            mine = fmaxf(mine, t), size = fmaxf(size, fabsf(x) + (s_done[k] ? 0.f : fabsf(s_lse32[k])) + fabsf(s_score[k]));
     }
     // The row's term and two sums are rounded, each to 2^-24 of these sizes: 2^-21 is more than two totals can be off.
     // (Infinite scores leave everything in.)
@@ -292,7 +325,6 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamSelect p,
     for (int w = 1; w < kThreads / 32; ++w) size = fmaxf(size, s_m[w]);
     const float least = size < 1e30f ? reach - size * 0x1p-21f : -INFINITY;
     for (int c = tid; c < all; c += kThreads) {
-        if (c < kNear && !(s_near[c] >= least && s_near[c] > -INFINITY)) continue;
         const int k = c / per_beam;
         const float x = logit(c, k), t = about(x, k);
         if (x != -INFINITY && t >= least && t > -INFINITY) {

@@ -54,24 +54,42 @@ __device__ __forceinline__ void share(long n, long i, long of, long &lo, long &h
 struct ForkSpace {  // in the workspace; every part on a 16-byte boundary
     int *total;     // [kCluster] a CTA's sum
     int *error;     // [kCluster]
-    int *old;       // [B][max_pages] the table before the call
+    int *old;       // [B][max_pages] a table that is written in place, before the call
     uint8_t *was, *is;  // [num_pages] live before and after
 };
 
+// f(row, column) for the first width(row) of `columns` columns of each row, shared out among the grid's warps: a warp takes 128
+// entries of a row at a time.
+template <typename W, typename F>
+__device__ __forceinline__ void for_entries(int rows, int columns, W width, F f) {
+    const int lane = threadIdx.x & 31, warp = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), warps = gridDim.x * (kThreads / 32);
+    const int parts = (columns + 127) / 128;
+    for (long item = warp; item < (long)rows * parts; item += warps) {
+        const int row = (int)(item / parts), first = (int)(item % parts) * 128 + lane, n = width(row);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (first + 32 * k < n) f(row, first + 32 * k);
+    }
+}
+
 __global__ void __launch_bounds__(kThreads) page_fork_kernel(const PageFork p, ForkSpace w) {
     extern __shared__ int s_fork[];
-    int *s_len = s_fork, *s_first = s_len + p.B, *s_rank = s_first + p.B;  // [B], [B], [B_out + 1]
+    // [B]: tokens of an old row, its first child; [B_out]: parent of a new row, and its place among the rows that need a page
+    // of their own for their last, partly filled one (all children but the first), or -1
+    int *s_len = s_fork, *s_first = s_len + p.B, *s_parent = s_first + p.B, *s_rank = s_parent + p.B_out;
     __shared__ int s_sum[32], s_bad;
     const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
     const int tid = threadIdx.x, rank = blockIdx.x, ranks = gridDim.x, ps = p.page_size, M = p.max_pages;
     const long t0 = (long)rank * kThreads + tid, step = (long)ranks * kThreads;
+    const bool same_table = p.table_out == p.block_table, same_lens = p.kv_lens_out == p.kv_lens;
+    const auto pages = [&](int b) { return (s_len[b] + ps - 1) / ps; };
+    const auto child_pages = [&](int i) { return s_parent[i] < 0 ? 0 : pages(s_parent[i]); };
     pdl_wait_primary();
 
-    // ---- clear the marks; copy the table, which may be written in place; look for what is wrong
+    // ---- clear the marks; copy a table that is written in place; look for what is wrong
     for (long i = t0 * 16; i < p.num_pages; i += step * 16)  // (the marks' rooms are multiples of 16)
         *reinterpret_cast<uint4 *>(w.was + i) = *reinterpret_cast<uint4 *>(w.is + i) = make_uint4(0, 0, 0, 0);
     if (tid == 0) s_bad = 0;
-    __syncthreads();
     const int cursor = __ldg(p.cursor);
     bool bad = cursor < 0;
     for (int b = tid; b < p.B; b += kThreads) {
@@ -81,52 +99,44 @@ __global__ void __launch_bounds__(kThreads) page_fork_kernel(const PageFork p, F
         s_len[b] = fits ? len : 0;
         s_first[b] = p.B_out;
     }
-    __syncthreads();
     for (int i = tid; i < p.B_out; i += kThreads) {
         const int parent = __ldg(p.parents + i);
         bad |= parent >= p.B;
-        if (parent >= 0 && parent < p.B) atomicMin(s_first + parent, i);
+        s_parent[i] = parent < p.B ? parent : -1;
     }
-    for (long e = t0; e < (long)p.B * M; e += step) {
-        const int b = (int)(e / M), j = (int)(e % M);
-        if (j >= (s_len[b] + ps - 1) / ps) continue;
-        const int page = p.block_table[e];
+    __syncthreads();
+    for (int i = tid; i < p.B_out; i += kThreads)
+        if (s_parent[i] >= 0) atomicMin(s_first + s_parent[i], i);
+    for_entries(p.B, M, pages, [&](int b, int j) {
+        const int page = p.block_table[(long)b * M + j];
         bad |= page < 0 || page >= p.num_pages;
-        w.old[e] = page;
-    }
+        if (same_table) w.old[(long)b * M + j] = page;
+    });
     if (bad) s_bad = 1;
     __syncthreads();
     if (tid == 0) w.error[rank] = s_bad;
-
-    // ---- rows that need a page of their own for their last, partly filled one: all children but the first
-    const auto copies_last = [&](int i) {
-        const int parent = __ldg(p.parents + i);
-        return parent >= 0 && parent < p.B && s_len[parent] % ps != 0 && s_first[parent] != i;
-    };
     int copies = 0, mine = 0;
     {
         const int per = (p.B_out + kThreads - 1) / kThreads, i0 = min(p.B_out, tid * per), i1 = min(p.B_out, i0 + per);
-        for (int i = i0; i < i1; ++i) mine += copies_last(i);
-        int at = block_scan(mine, copies, s_sum);
         for (int i = i0; i < i1; ++i) {
-            s_rank[i] = at;
-            at += copies_last(i);
+            const int parent = s_parent[i];
+            const bool own = parent >= 0 && s_len[parent] % ps != 0 && s_first[parent] != i;
+            s_rank[i] = own ? mine++ : -1;
         }
+        const int at = block_scan(mine, copies, s_sum);
+        for (int i = i0; i < i1; ++i)
+            if (s_rank[i] >= 0) s_rank[i] += at;
     }
     cluster.sync();
     bad = false;
     for (int r = 0; r < ranks; ++r) bad |= __ldcg(w.error + r) != 0;
+    const int *old = same_table ? w.old : p.block_table;
 
     // ---- marks
     if (!bad) {
-        for (long e = t0; e < (long)p.B * M; e += step) {
-            const int b = (int)(e / M), j = (int)(e % M);
-            if (j < (s_len[b] + ps - 1) / ps) w.was[__ldcg(w.old + e)] = 1;
-        }
-        for (long e = t0; e < (long)p.B_out * M; e += step) {
-            const int i = (int)(e / M), j = (int)(e % M), parent = __ldg(p.parents + i);
-            if (parent >= 0 && j < (s_len[parent] + ps - 1) / ps - copies_last(i)) w.is[__ldcg(w.old + (long)parent * M + j)] = 1;
-        }
+        for_entries(p.B, M, pages, [&](int b, int j) { w.was[__ldcg(old + (long)b * M + j)] = 1; });
+        for_entries(p.B_out, M, [&](int i) { return child_pages(i) - (s_rank[i] >= 0); },
+                    [&](int i, int j) { w.is[__ldcg(old + (long)s_parent[i] * M + j)] = 1; });
     }
     cluster.sync();
 
@@ -156,21 +166,19 @@ __global__ void __launch_bounds__(kThreads) page_fork_kernel(const PageFork p, F
     cluster.sync();
 
     // ---- the new rows
-    const bool same_table = p.table_out == p.block_table, same_lens = p.kv_lens_out == p.kv_lens;
     if (ok || !same_table)
-        for (long e = t0; e < (long)p.B_out * M; e += step) {
-            const int i = (int)(e / M), j = (int)(e % M), parent = __ldg(p.parents + i);
-            const int n = !ok || parent < 0 ? 0 : (s_len[parent] + ps - 1) / ps;
+        for_entries(p.B_out, M, [&](int) { return M; }, [&](int i, int j) {
+            const int n = ok ? child_pages(i) : 0;
             int page = -1;
-            if (j < n) page = j == n - 1 && copies_last(i) ? __ldcg(p.free_pages + start + s_rank[i]) : __ldcg(w.old + (long)parent * M + j);
-            p.table_out[e] = page;
-        }
+            if (j < n) page = j == n - 1 && s_rank[i] >= 0 ? __ldcg(p.free_pages + start + s_rank[i]) : __ldcg(old + (long)s_parent[i] * M + j);
+            p.table_out[(long)i * M + j] = page;
+        });
     for (long i = t0; i < p.B_out; i += step) {
-        const int parent = __ldg(p.parents + i);
+        const int parent = s_parent[i];
         if (ok || !same_lens) p.kv_lens_out[i] = ok && parent >= 0 ? s_len[parent] : 0;
-        if (ok && copies_last((int)i))
+        if (ok && s_rank[i] >= 0)
             reinterpret_cast<int2 *>(p.copies)[s_rank[i]] =
-                make_int2(__ldcg(w.old + (long)parent * M + s_len[parent] / ps), __ldcg(p.free_pages + start + s_rank[i]));
+                make_int2(__ldcg(old + (long)parent * M + s_len[parent] / ps), __ldcg(p.free_pages + start + s_rank[i]));
     }
     for (long i = (ok ? copies : 0) + t0; i < p.B_out; i += step) reinterpret_cast<int2 *>(p.copies)[i] = make_int2(-1, -1);
     if (t0 == 0) {
@@ -200,23 +208,21 @@ __global__ void __launch_bounds__(kThreads) page_compact_kernel(const PageCompac
         const int len = __ldg(p.kv_lens + b);
         return len < 0 || len > (long)M * ps ? -1 : (len + ps - 1) / ps;
     };
-    for (long e = t0; e < (long)p.B * M; e += step) {
-        const int n = used((int)(e / M));
-        if (n < 0) bad = true;
-        if ((int)(e % M) < n) {
-            const int page = p.block_table[e];
-            bad |= page < 0 || page >= p.num_pages;
-        }
-    }
+    for_entries(p.B, M, [&](int b) {
+        const int n = used(b);
+        bad |= n < 0;
+        return n;
+    }, [&](int b, int j) {
+        const int page = p.block_table[(long)b * M + j];
+        bad |= page < 0 || page >= p.num_pages;
+    });
     if (bad) s_bad = 1;
     __syncthreads();
     if (tid == 0) w.error[rank] = s_bad;
     cluster.sync();
     bad = false;
     for (int r = 0; r < ranks; ++r) bad |= __ldcg(w.error + r) != 0;
-    if (!bad)
-        for (long e = t0; e < (long)p.B * M; e += step)
-            if ((int)(e % M) < used((int)(e / M))) w.is[p.block_table[e]] = 1;
+    if (!bad) for_entries(p.B, M, used, [&](int b, int j) { w.is[p.block_table[(long)b * M + j]] = 1; });
     cluster.sync();
 
     long lo, hi;
@@ -259,14 +265,14 @@ __global__ void __launch_bounds__(kThreads) page_compact_kernel(const PageCompac
     cluster.sync();
     const bool same = p.table_out == p.block_table;
     if (!bad || !same)
-        for (long e = t0; e < (long)p.B * M; e += step) {
+        for_entries(p.B, M, [&](int) { return M; }, [&](int b, int j) {
             int page = -1;
-            if (!bad && (int)(e % M) < used((int)(e / M))) {
-                page = p.block_table[e];
+            if (!bad && j < used(b)) {
+                page = p.block_table[(long)b * M + j];
                 if (page >= live) page = __ldcg(w.to + page);
             }
-            p.table_out[e] = page;
-        }
+            p.table_out[(long)b * M + j] = page;
+        });
     if (!bad)
         for (long i = t0; i < p.num_pages; i += step) p.free_pages[i] = (int)i;
     if (t0 == 0) {
@@ -374,11 +380,11 @@ cudaError_t launch_page_fork(const PageFork &p, void *ws, cudaStream_t s) {
     w.is = reinterpret_cast<uint8_t *>(at + round16(p.num_pages));
     static std::atomic<uint64_t> attr_set{0};
     const cudaError_t e = once_per_device(attr_set, [] {
-        return cudaFuncSetAttribute(page_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (3 * kPagePlanMaxB + 1) * 4);
+        return cudaFuncSetAttribute(page_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kPagePlanMaxB * 4);
     });
     if (e != cudaSuccess) return e;
     const long work = std::max(std::max((long)p.B, (long)p.B_out) * p.max_pages, p.num_pages / 4L);
-    return launch_plan(page_fork_kernel, (2 * (size_t)p.B + p.B_out + 1) * 4, work, p, w, s);
+    return launch_plan(page_fork_kernel, 2 * ((size_t)p.B + p.B_out) * 4, work, p, w, s);
 }
 
 size_t page_compact_workspace(int num_pages) { return 128 + round16(num_pages) + 8 * (size_t)num_pages; }
