@@ -54,7 +54,7 @@ int check_kv4(int N, int HKV, int D, int page_size, int num_pages, const char *w
         return set_error(GDN_ERR_SHAPE, "%s: page_size=%d and num_pages=%d must be positive", what, page_size, num_pages);
     if (page_size % 16 != 0)
         return set_error(GDN_ERR_UNSUPPORTED, "%s: page_size=%d is not a multiple of 16", what, page_size);
-    if (N > INT_MAX - 1024 || HKV > 65535 || (long)page_size * num_pages > INT_MAX - 1024 ||
+    if (N > INT_MAX - 1024 || HKV > 32767 || (long)page_size * num_pages > INT_MAX - 1024 ||
         (long)N * HKV > (1L << 40) / (D * 2))
         return set_error(GDN_ERR_OVERFLOW, "%s: N, HKV or page_size * num_pages out of range", what);
     return GDN_OK;
@@ -102,12 +102,12 @@ int gdn_kv4_write(const void *k, const void *v, int64_t k_stride, int64_t v_stri
     if ((((uintptr_t)k_cache | (uintptr_t)v_cache | (uintptr_t)k_out | (uintptr_t)v_out) & 15) != 0)
         return set_error(GDN_ERR_UNSUPPORTED, "kv4 write: caches and outputs must be 16-byte aligned");
     const Kv4Write p{k, v, (long)k_stride, (long)v_stride, slots, k_scale, v_scale, k_cache, v_cache, k_out, v_out, N, HKV, D,
-                     page_size, num_pages};
+                     page_size, num_pages, 0, 0};
     return launched(launch_kv4_write(p, dtype, static_cast<cudaStream_t>(stream)), "kv4 write kernel launch");
 }
 
 size_t gdn_attention_paged_kv4_workspace_bytes(int B, int N, int H, int HKV, int D, int max_q) {
-    if (B < 1 || N < 0 || max_q < 0 || H < 1 || HKV < 1 || H % HKV != 0 || D < 1 || D > 256 || D % 16 != 0 || HKV > 65535) return 0;
+    if (B < 1 || N < 0 || max_q < 0 || H < 1 || HKV < 1 || H % HKV != 0 || D < 1 || D > 256 || D % 16 != 0 || HKV > 32767) return 0;
     return round256(attention_kv4_workspace(B, N, H, HKV, D, max_q < N ? max_q : N));
 }
 

@@ -5,8 +5,8 @@
 // written as rows of T too.
 //
 // Bound by HBM: each value read once (2 or 4 bytes), 9/16 byte written, and T again for the values.  A thread takes
-// one group: 16 values are two or four 16-byte loads, its codes one 8-byte store.  Four neighbouring tokens of a head
-// come before the next head, so that a warp's stores cover whole sectors where slots follow one another.
+// one group: 16 values are two or four 16-byte loads, its codes one 8-byte store.  A CTA takes neighbouring tokens of one
+// head, so that its stores cover whole sectors where slots follow one another.
 #include "kv4.cuh"
 #include "serving.h"
 
@@ -14,21 +14,15 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTokens = 4;
 
 template <typename T, bool WIDE>
 __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const Kv4Write p) {
     constexpr int VEC = 16 / sizeof(T);
-    const int groups = p.D / 16, per = groups * kTokens;
+    const int groups = p.D / 16, tid = threadIdx.x;
     pdl_wait_primary();
-    const long i = (long)blockIdx.x * kThreads + threadIdx.x;
-    const int in = (int)(i % per);  // (token, group) of four tokens of a head
-    long rest = i / per;
-    const int kv = (int)(rest % 2);
-    rest /= 2;
-    const int h = (int)(rest % p.HKV), g = in % groups;
-    const long token = rest / p.HKV * kTokens + in / groups;
-    if (token >= p.N) return;
+    const int in = tid / groups, g = tid - in * groups, kv = blockIdx.y & 1, h = blockIdx.y >> 1;
+    const long token = (long)blockIdx.x * p.tokens + in;
+    if (in >= p.tokens || token >= p.N) return;
     const int slot = __ldg(p.slots + token);
     const bool held = slot >= 0 && slot < (long)p.num_pages * p.page_size;
     T *out = static_cast<T *>(kv ? p.v_out : p.k_out);
@@ -64,7 +58,7 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const Kv4Write p) {
         code[half] = kv4_encode(t);
     }
     if (held) {
-        const int page = slot / p.page_size, at = slot % p.page_size;
+        const int page = p.page_shift >= 0 ? slot >> p.page_shift : slot / p.page_size, at = slot - page * p.page_size;
         uint8_t *block = static_cast<uint8_t *>(kv ? p.v_cache : p.k_cache) +
                          ((long)page * p.HKV + h) * ((long)p.page_size * groups * 9);
         *reinterpret_cast<uint2 *>(block + ((long)at * groups + g) * 8) = make_uint2(code[0], code[1]);
@@ -93,11 +87,15 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const Kv4Write p) {
 
 template <typename T>
 cudaError_t launch(const Kv4Write &p, cudaStream_t s) {
+    Kv4Write w = p;
+    w.tokens = kThreads / (p.D / 16);
+    w.page_shift = -1;
+    for (int i = 0; i < 31; ++i)
+        if (p.page_size == 1 << i) w.page_shift = i;
     const bool wide = rows_aligned(p.k, p.k_stride, p.D, sizeof(T)) && rows_aligned(p.v, p.v_stride, p.D, sizeof(T));
-    const long all = ((long)p.N + kTokens - 1) / kTokens * kTokens * 2 * p.HKV * (p.D / 16);
-    const dim3 grid((unsigned)((all + kThreads - 1) / kThreads));
-    const cudaError_t e = wide ? launch_kernel(kv4_write_kernel<T, true>, grid, dim3(kThreads), 0, s, true, p)
-                               : launch_kernel(kv4_write_kernel<T, false>, grid, dim3(kThreads), 0, s, true, p);
+    const dim3 grid((unsigned)((p.N + w.tokens - 1) / w.tokens), (unsigned)(2 * p.HKV));
+    const cudaError_t e = wide ? launch_kernel(kv4_write_kernel<T, true>, grid, dim3(kThreads), 0, s, true, w)
+                               : launch_kernel(kv4_write_kernel<T, false>, grid, dim3(kThreads), 0, s, true, w);
     note_launch();
     return e;
 }

@@ -51,6 +51,26 @@ __device__ __forceinline__ void share(long n, long i, long of, long &lo, long &h
     lo = min(n, i * per), hi = min(n, lo + per);
 }
 
+// f(i) for the pages of [lo, hi) (lo a multiple of 16) whose mark in `a` is set and whose mark in `b`, if given, is not;
+// neither(i) for the others.
+template <typename F, typename G>
+__device__ __forceinline__ void for_marks(const uint8_t *a, const uint8_t *b, long lo, long hi, F f, G neither) {
+    for (long i = lo; i < hi; i += 16) {
+        const uint4 x = __ldcg(reinterpret_cast<const uint4 *>(a + i));
+        uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        if (b != nullptr) {
+            const uint4 y = __ldcg(reinterpret_cast<const uint4 *>(b + i));
+            w[0] &= ~y.x, w[1] &= ~y.y, w[2] &= ~y.z, w[3] &= ~y.w;
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            if (i + k >= hi) break;
+            if (w[k / 4] >> (k % 4 * 8) & 1) f(i + k);
+            else neither(i + k);
+        }
+    }
+}
+
 struct ForkSpace {  // in the workspace; every part on a 16-byte boundary
     int *total;     // [kCluster] a CTA's sum
     int *error;     // [kCluster]
@@ -160,9 +180,7 @@ __global__ void __launch_bounds__(kThreads) page_fork_kernel(const PageFork p, F
     const long start = (long)cursor - freed;  // the list's place of the first page that goes back
     const int status = bad || start < 0 ? GDN_ERR_SHAPE : start + copies > p.n_free ? GDN_ERR_CAPACITY : GDN_OK;
     const bool ok = status == GDN_OK;
-    if (ok && back > 0)
-        for (long i = lo; i < hi; ++i)
-            if (__ldcg(w.was + i) && !__ldcg(w.is + i)) p.free_pages[start + at++] = (int)i;
+    if (ok && back > 0) for_marks(w.was, w.is, lo, hi, [&](long i) { p.free_pages[start + at++] = (int)i; }, [](long) {});
     cluster.sync();
 
     // ---- the new rows
@@ -244,14 +262,19 @@ __global__ void __launch_bounds__(kThreads) page_compact_kernel(const PageCompac
     // holes among the first `live` pages by their rank from the front, the live ones behind them by their rank
     // among all live ones from the back: with H holes, H <= num_pages - live, and those fill the last `live` places at
     // most, so the two lists do not meet
-    if (!bad)
-        for (long i = lo; i < hi; ++i) {
-            const bool is = __ldcg(w.is + i) != 0;
-            if (i == live) *w.below = before;
-            if (i < live && !is) w.list[i - before] = (int)i;
-            if (i >= live && is) w.list[p.num_pages - 1 - before] = (int)i;
-            before += is;
+    if (!bad) {
+        if (lo <= live && live < hi) {  // (this thread meets the page numbered `live`)
+            int n = before;
+            for_marks(w.is, nullptr, lo, live, [&](long) { ++n; }, [](long) {});
+            *w.below = n;
         }
+        for_marks(w.is, nullptr, lo, hi, [&](long i) {
+            if (i >= live) w.list[p.num_pages - 1 - before] = (int)i;
+            ++before;
+        }, [&](long i) {
+            if (i < live) w.list[i - before] = (int)i;
+        });
+    }
     cluster.sync();
     const int below = bad ? 0 : live < p.num_pages ? __ldcg(w.below) : live, moved = bad ? 0 : live - below;
     for (long i = t0; i < p.num_pages / 2; i += step) {

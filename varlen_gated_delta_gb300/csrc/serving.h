@@ -90,6 +90,7 @@ struct Kv4Write {
     const float *k_scale, *v_scale;
     void *k_cache, *v_cache, *k_out, *v_out;
     int N, HKV, D, page_size, num_pages;
+    int tokens, page_shift;  // of a CTA; log2 of page_size or -1 (set by the launcher)
 };
 cudaError_t launch_kv4_write(const Kv4Write &p, int dtype, cudaStream_t s);
 
