@@ -6,13 +6,14 @@
 //
 // The first cuts every row into pieces, one CTA each, held in registers: the piece's maximum m and sum of
 // exp(x - m), and its n largest logits.  For these, the CTA's threads form groups whose maxima are at hand: at
-// least n values reach the n-th largest of them, and few more do (n = 8 of 32 groups: some 9 of 8192 values), so
+// least n values reach the n-th largest of them, and few more do (n = 8 of 32 groups: some 9 of 16384 values), so
 // those go into a list and are ranked by counting.  A list that overflows (many equal logits) is left for n
 // rounds of the CTA-wide largest value below the last one.
 //
 // The second, a CTA to a group of beams, joins the pieces' sums, and takes the n best of their candidates the
 // same way.  Totals and their comparison are in 64 bits: only the error of the row's sum (fp32 terms) is left
 // in the order of beams.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 
@@ -102,7 +103,7 @@ __device__ __forceinline__ float nth_maximum(float x, int n, int groups, float *
 }
 
 template <typename T, int ELEMS>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
+__global__ void __launch_bounds__(kThreads, ELEMS <= 8 ? 6 : 4)
     beam_pieces_kernel(const T *__restrict__ logits, long stride, const uint8_t *__restrict__ finished, Pieces out, int V,
                        int n, int pieces) {
     constexpr int VEC = 16 / sizeof(T), VECS = ELEMS / VEC;
@@ -186,11 +187,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
     // Few threads have such values: the warp reads those of one of them at a time again (registers would have to be indexed).
     const auto read = [&](long at) { return at >= 0 && at < V ? fmaxf(to_f32(x[at]), -INFINITY) : -INFINITY; };
     for (unsigned left = __ballot_sync(0xffffffffu, mine >= least && mine != -INFINITY); left != 0; left &= left - 1) {
-        const long at = first + (long)(lane / VEC * kThreads + warp * 32 + __ffs(left) - 1) * VEC + lane % VEC;
-        const float v = lane < ELEMS ? read(at) : -INFINITY;
-        if (v >= least && v != -INFINITY) {
-            const int k = atomicAdd(&s_n, 1);
-            if (k < kList) s_list[k] = key_of(v, (int)at);
+#pragma unroll
+        for (int e = lane; e < ELEMS; e += 32) {
+            const long at = first + (long)(e / VEC * kThreads + warp * 32 + __ffs(left) - 1) * VEC + e % VEC;
+            const float v = read(at);
+            if (v >= least && v != -INFINITY) {
+                const int k = atomicAdd(&s_n, 1);
+                if (k < kList) s_list[k] = key_of(v, (int)at);
+            }
         }
     }
     if (lane == 0) s_sum[0][warp] = sum, s_sum[1][warp] = lo;
@@ -417,14 +421,16 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamSelect p,
     }
 }
 
-// A piece of 8 values a thread while that leaves SMs without a CTA, 32 otherwise.
+// 128 bytes to a thread, or 8 values while that leaves SMs without work.
 int piece_size(int rows, int V, int dtype) {
-    return (long)rows * ((V + 8191) / 8192) < 4 * 152 ? 2048 : 8192;
+    const int most = dtype == GDN_BF16 ? 16384 : 8192;
+    return (long)rows * ((V + (long)most - 1) / most) < 4 * 152 ? 2048 : most;
 }
 int piece_count(int rows, int V, int dtype) {
     const int size = piece_size(rows, V, dtype);
     return (int)(((long)V + 7 + size - 1) / size);  // (up to 7 values of the first vector lie before the row)
 }
+int most_pieces(int rows, int V) { return std::max(piece_count(rows, V, GDN_BF16), piece_count(rows, V, GDN_F32)); }
 
 template <typename T, int ELEMS>
 cudaError_t launch_pieces(const BeamSelect &p, const Pieces &w, int pieces, cudaStream_t s) {
@@ -438,13 +444,12 @@ cudaError_t launch_pieces(const BeamSelect &p, const Pieces &w, int pieces, cuda
 }  // namespace
 
 size_t beam_select_workspace(int G, int K, int V, int n) {
-    // (of the two piece sizes the one that asks for more)
-    const size_t rows = (size_t)G * K, pieces = (size_t)piece_count(G * K, V, 0);
+    const size_t rows = (size_t)G * K, pieces = (size_t)most_pieces(G * K, V);
     return rows * pieces * (8 + 8 * (size_t)n);
 }
 
 bool beam_select_fits(int G, int K, int V, int n) {
-    return (long)G * K * piece_count(G * K, V, 0) <= INT_MAX && (long)K * piece_count(G * K, V, 0) * n <= INT_MAX;
+    return (long)G * K * most_pieces(G * K, V) <= INT_MAX && (long)K * most_pieces(G * K, V) * n <= INT_MAX;
 }
 
 cudaError_t launch_beam_select(const BeamSelect &p, int dtype, void *ws, cudaStream_t s) {
@@ -456,7 +461,7 @@ cudaError_t launch_beam_select(const BeamSelect &p, int dtype, void *ws, cudaStr
     const bool small = piece_size(rows, p.V, dtype) == 2048;
     cudaError_t e;
     if (dtype == GDN_BF16)
-        e = small ? launch_pieces<__nv_bfloat16, 8>(p, w, pieces, s) : launch_pieces<__nv_bfloat16, 32>(p, w, pieces, s);
+        e = small ? launch_pieces<__nv_bfloat16, 8>(p, w, pieces, s) : launch_pieces<__nv_bfloat16, 64>(p, w, pieces, s);
     else
         e = small ? launch_pieces<float, 8>(p, w, pieces, s) : launch_pieces<float, 32>(p, w, pieces, s);
     if (e != cudaSuccess) return e;

@@ -12,6 +12,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "copy.cuh"
 #include "serving.h"
 
 namespace gdn {
@@ -312,21 +313,6 @@ struct CopyParams {
     int vec[kPageMaxCaches];
 };
 
-template <typename T>
-__device__ __forceinline__ void copy_piece(unsigned char *dst, const unsigned char *src, long bytes) {
-    constexpr int N = 4;
-    const long n = bytes / (long)sizeof(T);
-    for (long i0 = threadIdx.x; i0 < n; i0 += N * kCopyThreads) {
-        T x[N];
-#pragma unroll
-        for (int k = 0; k < N; ++k)
-            if (i0 + k * kCopyThreads < n) x[k] = reinterpret_cast<const T *>(src)[i0 + k * kCopyThreads];
-#pragma unroll
-        for (int k = 0; k < N; ++k)
-            if (i0 + k * kCopyThreads < n) reinterpret_cast<T *>(dst)[i0 + k * kCopyThreads] = x[k];
-    }
-}
-
 // CTAs take (pair, piece) items in turn.  Lists may be mostly empty: the threads of a CTA look at the pairs of its next 256
 // items at once, and only those with something to copy are gone through.
 __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const __grid_constant__ CopyParams p) {
@@ -358,11 +344,7 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const __grid_co
                 unsigned char *base = static_cast<unsigned char *>(p.c.caches[t]) + from;
                 unsigned char *dst = base + pair.y * page;
                 const unsigned char *src = base + pair.x * page;
-                switch (p.vec[t]) {
-                case 16: copy_piece<uint4>(dst, src, bytes); break;
-                case 4: copy_piece<uint32_t>(dst, src, bytes); break;
-                default: copy_piece<uint8_t>(dst, src, bytes);
-                }
+                copy_bytes<kCopyThreads, 4>(dst, src, bytes, p.vec[t]);
             }
     }
 }
@@ -427,8 +409,7 @@ cudaError_t launch_page_copy(const PageCopy &c, cudaStream_t s) {
     p.c = c;
     for (int t = 0; t < c.count; ++t) {
         p.first[t + 1] = p.first[t] + (int)((c.page_bytes[t] + kCopyBytes - 1) / kCopyBytes);
-        const uintptr_t at = (uintptr_t)c.caches[t] | (uintptr_t)c.page_bytes[t];
-        p.vec[t] = at % 16 == 0 ? 16 : at % 4 == 0 ? 4 : 1;
+        p.vec[t] = copy_width((uintptr_t)c.caches[t], (uintptr_t)c.page_bytes[t]);
     }
     int dev = 0, sms = 0;
     cudaGetDevice(&dev);

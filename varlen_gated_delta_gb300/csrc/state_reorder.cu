@@ -2,14 +2,17 @@
 // row i <- row parents[i], in place, for several state tensors in one launch.
 //
 // Nothing is computed: bound by HBM at one read of every row that is a parent of another
-// and one write of every row that changes.  In place, a row may be read by one and written by
-// another: so a CTA owns a strip of columns of all rows, brings the strips of all changed rows'
-// parents into shared memory, and writes them after a barrier; strips of different CTAs do not touch.
-// The strip is as wide as shared memory allows for B rows, which keeps the accesses long (256
-// rows: 256 bytes).  Rows that keep their place are neither read nor written.
+// and one write of every row that changes.  Rows that keep their place are neither read nor written.
+//
+// A row that takes the content of one that keeps its place, and that nobody else takes anything from, is
+// copied in long pieces (so all of them, when gdn_beam_select keeps rows).  Among the others a row may be
+// read by one and written by another: for these a CTA owns a strip of columns of all rows, brings the
+// strips of all their parents into shared memory, and writes them after a barrier; strips of different
+// CTAs do not touch.  The strip is as wide as shared memory allows for B rows (256 rows: 256 bytes).
 #include <algorithm>
 
 #include "common.cuh"
+#include "copy.cuh"
 #include "serving.h"
 
 namespace gdn {
@@ -18,8 +21,11 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kStrip = 64 * 1024;  // bytes of all strips of a CTA: three CTAs to an SM
 
+constexpr int kPiece = kThreads * 16 * 8;  // bytes of a row that a CTA copies at a time
+
 struct ReorderParams {
     StateReorder r;
+    long first_piece[kStateMaxTensors + 1];  // first piece of each tensor's rows
     long first[kStateMaxTensors + 1];  // first strip of each tensor
     int strip;                         // bytes, a multiple of 16
     int vec[kStateMaxTensors];         // bytes of an access: 16, 8, 4, 2 or 1
@@ -51,17 +57,55 @@ __device__ __forceinline__ void move_strip(unsigned char *base, long row_bytes, 
 
 __global__ void __launch_bounds__(kThreads) state_reorder_kernel(const __grid_constant__ ReorderParams p) {
     extern __shared__ __align__(16) unsigned char s_data[];
-    __shared__ int s_n;
-    int2 *s_move = reinterpret_cast<int2 *>(s_data + (size_t)p.r.B * p.strip);  // (parent, row)
+    // (parent, row) of the rows that change: the simple ones from the back, the others from the front; which rows are read
+    // by others and which change, a byte to each
+    __shared__ int2 s_count[kThreads / 32];
+    int2 *s_move = reinterpret_cast<int2 *>(s_data + (size_t)p.r.B * p.strip);
+    uint8_t *s_read = reinterpret_cast<uint8_t *>(s_move + p.r.B), *s_changes = s_read + p.r.B;
+    const int B = p.r.B;
     pdl_wait_primary();
-    if (threadIdx.x == 0) s_n = 0;
+    for (int i = threadIdx.x; i < B; i += kThreads) s_read[i] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < p.r.B; i += kThreads) {
+    const auto parent = [&](int i) {
         const int from = __ldg(p.r.parents + i);
-        if (from != i && from >= 0 && from < p.r.B) s_move[atomicAdd(&s_n, 1)] = make_int2(from, i);
+        return from >= 0 && from < B ? from : i;
+    };
+    for (int i = threadIdx.x; i < B; i += kThreads) {
+        const int from = parent(i);
+        s_changes[i] = from != i;
+        if (from != i) s_read[from] = 1;
     }
     __syncthreads();
-    const int moved = s_n;
+    // (in the order of rows: all CTAs have to agree on who copies which)
+    int moved = 0, simple = 0;
+    for (int i0 = 0; i0 < B; i0 += kThreads) {
+        const int i = i0 + threadIdx.x, from = i < B ? parent(i) : i;
+        const bool is_simple = from != i && !s_changes[from] && !s_read[i], other = from != i && !is_simple;
+        const unsigned a = __ballot_sync(0xffffffffu, is_simple), b = __ballot_sync(0xffffffffu, other);
+        const unsigned before = (1u << (threadIdx.x & 31)) - 1;
+        if ((threadIdx.x & 31) == 0) s_count[threadIdx.x >> 5] = make_int2(__popc(a), __popc(b));
+        __syncthreads();
+        int at_simple = simple + __popc(a & before), at_other = moved + __popc(b & before);
+        for (int w = 0; w < kThreads / 32; ++w) {
+            const int2 c = s_count[w];
+            if (w < threadIdx.x >> 5) at_simple += c.x, at_other += c.y;
+            simple += c.x, moved += c.y;
+        }
+        if (is_simple) s_move[B - 1 - at_simple] = make_int2(from, i);
+        if (other) s_move[at_other] = make_int2(from, i);
+        __syncthreads();
+    }
+    // (the rows of a piece follow one another, so that children of one parent find it in L2)
+    if (simple > 0)
+        for (long item = blockIdx.x; item < p.first_piece[p.r.count] * simple; item += gridDim.x) {
+            const long piece = item / simple;
+            const int2 move = s_move[B - 1 - (int)(item - piece * simple)];
+            int t = 0;
+            while (piece >= p.first_piece[t + 1]) ++t;
+            const long row = p.r.row_bytes[t], from = (piece - p.first_piece[t]) * kPiece, bytes = min((long)kPiece, row - from);
+            unsigned char *base = static_cast<unsigned char *>(p.r.states[t]) + from;
+            copy_bytes<kThreads, 8>(base + move.y * row, base + move.x * row, bytes, p.vec[t]);
+        }
     if (moved == 0) return;
     for (long strip = blockIdx.x; strip < p.first[p.r.count]; strip += gridDim.x) {
         int t = 0;
@@ -86,24 +130,23 @@ cudaError_t launch_state_reorder(const StateReorder &r, cudaStream_t s) {
     ReorderParams p{};
     p.r = r;
     p.strip = std::max(16, std::min(4096, kStrip / r.B / 16 * 16));
-    p.first[0] = 0;
     for (int t = 0; t < r.count; ++t) {
+        p.first_piece[t + 1] = p.first_piece[t] + (r.row_bytes[t] + kPiece - 1) / kPiece;
         p.first[t + 1] = p.first[t] + (r.row_bytes[t] + p.strip - 1) / p.strip;
-        const uintptr_t at = (uintptr_t)r.states[t] | (uintptr_t)r.row_bytes[t];
-        p.vec[t] = at % 16 == 0 ? 16 : at % 8 == 0 ? 8 : at % 4 == 0 ? 4 : at % 2 == 0 ? 2 : 1;
+        p.vec[t] = copy_width((uintptr_t)r.states[t], (uintptr_t)r.row_bytes[t]);
     }
     if (p.first[r.count] == 0) return cudaSuccess;
-    const size_t smem = (size_t)r.B * (p.strip + sizeof(int2));
+    const size_t smem = (size_t)r.B * (p.strip + sizeof(int2) + 2);
     static std::atomic<uint64_t> attr_set{0};
     cudaError_t e = once_per_device(attr_set, [] {
         return cudaFuncSetAttribute(state_reorder_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    std::max(kStrip + kStateMaxRows * 8, kStateMaxRows * 24));
+                                    std::max(kStrip + kStateMaxRows * 10, kStateMaxRows * 26));
     });
     if (e != cudaSuccess) return e;
     int dev = 0, sms = 0;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const long grid = std::min(p.first[r.count], 3L * sms);
+    const long grid = std::min(std::max(p.first[r.count], p.first_piece[r.count] * r.B), 3L * sms);
     e = launch_kernel(state_reorder_kernel, dim3((unsigned)grid), dim3(kThreads), smem, s, true, p);
     note_launch();
     return e;
