@@ -33,6 +33,7 @@ struct Kv4Params {
     float sign;    // of scale
     int blocks;    // row blocks of the longest sequence
     int page_shift;  // log2 of page_size, or -1
+    int q_wide;      // query rows lie on 16-byte boundaries
     int min_rows, max_rows;  // sequences of more than min_rows and at most max_rows rows are ours
     int2 *spans;   // [B][blocks][HKV]: first and last CTA of a triple
     float *part;   // [2 * CTAs][ROWS * (3 + DP)]
@@ -596,12 +597,26 @@ __global__ void __launch_bounds__(128, Narrow<DP, NT, T>::PER_SM) kv4_narrow_ker
                 const T *src = static_cast<const T *>(p.a.q);
                 if (r < rows) src += (long)(cur.start + (row0 + r) / G) * p.a.qs + (long)(cur.h * G + (row0 + r) % G) * D;
                 float x[DP / 4], amax = 0.f;
+                if (p.q_wide) {  // (D is a multiple of 16: no 16 bytes lie across its end)
+                    constexpr int VEC = 16 / sizeof(T);
 #pragma unroll
-                for (int i = 0; i < DP / 4; ++i) {
-                    const int d = t4 * (DP / 4) + i;
-                    x[i] = r < rows && (FULL || d < D) ? to_f32(src[d]) : 0.f;
-                    amax = fmaxf(amax, fabsf(x[i]));
+                    for (int i = 0; i < DP / 4; i += VEC) {
+                        const int d = t4 * (DP / 4) + i;
+                        Vec16<T> w;
+                        w.u = make_uint4(0, 0, 0, 0);
+                        if (r < rows && (FULL || d < D)) w.u = __ldg(reinterpret_cast<const uint4 *>(src + d));
+#pragma unroll
+                        for (int k = 0; k < VEC; ++k) x[i + k] = to_f32(w.v[k]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < DP / 4; ++i) {
+                        const int d = t4 * (DP / 4) + i;
+                        x[i] = r < rows && (FULL || d < D) ? to_f32(src[d]) : 0.f;
+                    }
                 }
+#pragma unroll
+                for (int i = 0; i < DP / 4; ++i) amax = fmaxf(amax, fabsf(x[i]));
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
                 float back;
@@ -1046,6 +1061,7 @@ cudaError_t launch_attention_kv4(const Attn &a, const float *k_scale, const floa
     p.G = a.H / a.HKV;
     p.c = std::fabs(a.scale) * kLog2e;
     p.sign = a.scale < 0.f ? -1.f : 1.f;
+    p.q_wide = rows_aligned(a.q, a.qs, a.D, dtype == GDN_BF16 ? 2 : 4);
     p.page_shift = -1;
     for (int i = 0; i < 31; ++i)
         if (a.page_size == 1 << i) p.page_shift = i;
