@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kCluster = 8;
+static_assert(kThreads == 32 * 32, "the scan's last step is one warp's");
 
 // Exclusive sum over the block; returns the block's total in `all`.
 __device__ __forceinline__ int block_scan(int x, int &all, int *s_sum) {
