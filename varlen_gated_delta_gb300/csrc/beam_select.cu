@@ -72,8 +72,8 @@ __device__ __forceinline__ void warp_sum_two(float &hi, float &lo) {
 }
 
 // The n-th largest (any of them, if there are fewer) of the maxima of `groups` (32 or 256) equal sets of neighbouring
-// threads.
-__device__ __forceinline__ float nth_maximum(float x, int n, int groups, float *s_all, float *s_nth) {
+// threads, and the largest.
+__device__ __forceinline__ float nth_maximum(float x, int n, int groups, float *s_all, float2 *s_nth, float &top) {
     const int tid = threadIdx.x;
     if (groups == 32) {  // (one warp ranks them)
 #pragma unroll
@@ -91,15 +91,19 @@ __device__ __forceinline__ float nth_maximum(float x, int n, int groups, float *
             const float4 y = *reinterpret_cast<const float4 *>(s_all + i);
             larger += (y.x > x) + (y.y > x) + (y.z > x) + (y.w > x);
         }
-        x = larger < n ? x : INFINITY;
+        float nth = larger < n ? x : INFINITY;
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) x = fminf(x, __shfl_xor_sync(0xffffffffu, x, d));
-        if ((tid & 31) == 0) s_nth[tid >> 5] = x;
+        for (int d = 16; d > 0; d >>= 1) {
+            nth = fminf(nth, __shfl_xor_sync(0xffffffffu, nth, d));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+        }
+        if ((tid & 31) == 0) s_nth[tid >> 5] = make_float2(nth, x);
     }
     __syncthreads();
-    x = s_nth[0];
-    for (int w = 1; w < groups / 32; ++w) x = fminf(x, s_nth[w]);
-    return x;
+    float2 y = s_nth[0];
+    for (int w = 1; w < groups / 32; ++w) y.x = fminf(y.x, s_nth[w].x), y.y = fmaxf(y.y, s_nth[w].y);
+    top = y.y;
+    return y.x;
 }
 
 template <typename T, int ELEMS>
@@ -107,10 +111,9 @@ __global__ void __launch_bounds__(kThreads, ELEMS <= 8 ? 6 : 4)
     beam_pieces_kernel(const T *__restrict__ logits, long stride, const uint8_t *__restrict__ finished, Pieces out, int V,
                        int n, int pieces) {
     constexpr int VEC = 16 / sizeof(T), VECS = ELEMS / VEC;
-    __shared__ float s_warp[kThreads / 32], s_sum[2][kThreads / 32];
     __shared__ __align__(16) float s_all[kThreads];
     __shared__ unsigned long long s_list[kList], s_top[kThreads / 32];
-    __shared__ float s_nth[kThreads / 32];
+    __shared__ float2 s_nth[kThreads / 32];
     __shared__ int s_n;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long row = blockIdx.x / pieces;
@@ -121,16 +124,16 @@ __global__ void __launch_bounds__(kThreads, ELEMS <= 8 ? 6 : 4)
     const T *x = logits + row * stride;
     // Vectors lie on 16-byte boundaries: the first may begin before the row.
     const int skew = (int)(((uintptr_t)x / sizeof(T)) % VEC);
-    const long first = (long)piece * (ELEMS * kThreads) - skew;
+    const int first = piece * (ELEMS * kThreads) - skew;  // (places up to a piece past V: see beam_select_fits)
 
     Vec16<T> w[VECS];
     const auto value = [&](int i) { return to_f32(w[i / VEC].v[i % VEC]); };
-    const auto token = [&](int i) { return (int)(first + (long)(i / VEC * kThreads + tid) * VEC + i % VEC); };
+    const auto token = [&](int i) { return first + (i / VEC * kThreads + tid) * VEC + i % VEC; };
     if (tid == 0) s_n = 0;
 #pragma unroll
     for (int j = 0; j < VECS; ++j) {
-        const long at = first + (long)(j * kThreads + tid) * VEC;
-        if (at >= 0 && at + VEC <= V) {
+        const int at = first + (j * kThreads + tid) * VEC;
+        if (at >= 0 && at <= V - VEC) {
             w[j].u = __ldg(reinterpret_cast<const uint4 *>(x + at));
         } else {
 #pragma unroll
@@ -150,13 +153,8 @@ __global__ void __launch_bounds__(kThreads, ELEMS <= 8 ? 6 : 4)
 #pragma unroll
         for (int i = 0; i < ELEMS; ++i) mine = fmaxf(mine, value(i));
     }
-    const float wm = warp_max(mine);
-    if (lane == 0) s_warp[warp] = wm;
-    // (barriers)
-    const float least = nth_maximum(mine, n, n <= 32 ? 32 : kThreads, s_all, s_nth);
-    float m = s_warp[0];
-#pragma unroll
-    for (int w = 1; w < kThreads / 32; ++w) m = fmaxf(m, s_warp[w]);
+    float m;  // (barriers)
+    const float least = nth_maximum(mine, n, n <= 32 ? 32 : kThreads, s_all, s_nth, m);
 
     // ---- sum of exp(x - m) = 2^(x L - m L), L = log2(e): a product and a sum in one rounding, and the rounding of m L, which
     // all terms share, is taken back at the end (2^-t = 1 - t ln 2 + ..., t < 2^-10).  Large m, or a NaN: x - m first.
@@ -174,36 +172,38 @@ __global__ void __launch_bounds__(kThreads, ELEMS <= 8 ? 6 : 4)
         const float2 both = __fadd2_rn(part[0], part[1]);
         return both.x + both.y;
     };
-    float sum = sum_of([&](float2 x) { return __ffma2_rn(x, make_float2(kL, kL), make_float2(-mL, -mL)); }), lo = 0.f;
+    float sum = sum_of([&](float2 x) { return __ffma2_rn(x, make_float2(kL, kL), make_float2(-mL, -mL)); });
     const float t = 0.69314718f * __fmaf_rn(base, kL, -mL);
     sum *= 1.f + t * (0.5f * t - 1.f);
     if (sum != sum || fabsf(base) > 8192.f)
         sum = sum_of([&](float2 x) {
             return make_float2((fmaxf(x.x, -INFINITY) - base) * kL, (fmaxf(x.y, -INFINITY) - base) * kL);
         });
-    warp_sum_two(sum, lo);
+    s_all[tid] = sum;  // (the maxima have been read)
 
     // ---- the list of what reaches `least`
     // Few threads have such values: the warp reads those of one of them at a time again (registers would have to be indexed).
-    const auto read = [&](long at) { return at >= 0 && at < V ? fmaxf(to_f32(x[at]), -INFINITY) : -INFINITY; };
+    const auto read = [&](int at) { return at >= 0 && at < V ? fmaxf(to_f32(x[at]), -INFINITY) : -INFINITY; };
     for (unsigned left = __ballot_sync(0xffffffffu, mine >= least && mine != -INFINITY); left != 0; left &= left - 1) {
 #pragma unroll
         for (int e = lane; e < ELEMS; e += 32) {
-            const long at = first + (long)(e / VEC * kThreads + warp * 32 + __ffs(left) - 1) * VEC + e % VEC;
+            const int at = first + (e / VEC * kThreads + warp * 32 + __ffs(left) - 1) * VEC + e % VEC;
             const float v = read(at);
             if (v >= least && v != -INFINITY) {
                 const int k = atomicAdd(&s_n, 1);
-                if (k < kList) s_list[k] = key_of(v, (int)at);
+                if (k < kList) s_list[k] = key_of(v, at);
             }
         }
     }
-    if (lane == 0) s_sum[0][warp] = sum, s_sum[1][warp] = lo;
     __syncthreads();
     const long o = row * pieces + piece;
-    if (tid == 0) {
+    if (warp == kThreads / 32 - 1) {  // (the first warp ranks the list)
+        float lo = 0.f;
+        sum = s_all[lane];
 #pragma unroll
-        for (int w = 1; w < kThreads / 32; ++w) add_two(sum, lo, s_sum[0][w], s_sum[1][w]);
-        out.m[o] = m, out.sum[o] = sum + lo;
+        for (int w = 1; w < kThreads / 32; ++w) add_two(sum, lo, s_all[w * 32 + lane], 0.f);
+        warp_sum_two(sum, lo);
+        if (lane == 0) out.m[o] = m, out.sum[o] = sum + lo;
     }
     auto put = [&](int rank, unsigned long long key) {
         const uint32_t b = (uint32_t)(key >> 32);
@@ -253,7 +253,8 @@ __device__ __forceinline__ bool before(unsigned long long a, int ia, unsigned lo
 __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamSelect p, Pieces in, int pieces) {
     __shared__ double s_lse[kBeamMaxK];
     __shared__ __align__(16) float s_all[kThreads];
-    __shared__ float s_least[kThreads / 32], s_score[kBeamMaxK], s_m[kBeamMaxK], s_sum[kBeamMaxK], s_lse32[kBeamMaxK];
+    __shared__ float2 s_least[kThreads / 32];
+    __shared__ float s_score[kBeamMaxK], s_m[kBeamMaxK], s_sum[kBeamMaxK], s_lse32[kBeamMaxK];
     __shared__ uint8_t s_done[kBeamMaxK];
     __shared__ unsigned long long s_total[kList];
     __shared__ int s_at[kList], s_place[kBeamMaxN], s_rest[kBeamMaxN];
@@ -323,7 +324,8 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamSelect p,
     // (Infinite scores leave everything in.)
     size = warp_max(size);
     if (lane == 0) s_m[warp] = size;  // (K <= 128 >= 8 places; the maxima have been used)
-    const float reach = nth_maximum(mine, n, kThreads, s_all, s_least);  // (barriers)
+    float best;  // (barriers)
+    const float reach = nth_maximum(mine, n, kThreads, s_all, s_least, best);
     size = s_m[0];
 #pragma unroll
     for (int w = 1; w < kThreads / 32; ++w) size = fmaxf(size, s_m[w]);
@@ -449,7 +451,7 @@ size_t beam_select_workspace(int G, int K, int V, int n) {
 }
 
 bool beam_select_fits(int G, int K, int V, int n) {
-    return (long)G * K * most_pieces(G * K, V) <= INT_MAX && (long)K * most_pieces(G * K, V) * n <= INT_MAX;
+    return (long)G * K * most_pieces(G * K, V) <= INT_MAX && V <= INT_MAX - 4 * 16384 && (long)K * most_pieces(G * K, V) * n <= INT_MAX;
 }
 
 cudaError_t launch_beam_select(const BeamSelect &p, int dtype, void *ws, cudaStream_t s) {
