@@ -85,6 +85,31 @@ def test_masked_logits_and_beams(V):
         _check(logits, scores, 4, gdn.gdn_beam_select(logits, scores, finished=done, end_token=7, keep_rows=keep), done, 7, keep)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows", [4, 160])
+def test_long_rows_of_every_kind(rows, dtype):
+    """Rows that a CTA goes through in several pieces: rising, falling, equal, masked at the front, largest at the end."""
+    V, K = 150001, 4
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    x = torch.randn(rows, V, generator=gen, device="cuda")
+    ramp = torch.arange(V, device="cuda") / 1000
+    x[0], x[1], x[2, :] = ramp, ramp.flip(0), 2.0
+    x[3, :100000] = -float("inf")
+    x[3, 100003:] = -float("inf")
+    if rows > 4:
+        x[4, -3:] += 60                                   # the reference moves in the last piece
+        x[5, 20000:] += 30
+        x[6, ::2] = -float("inf")
+        x[7, 140000] = float("nan")
+        x[8] = torch.where(ramp > 100, 3.0, -float("inf"))
+        x[9, 70000:] = 0.0
+        x[10, 16384 * 3 - 2:16384 * 3 + 2] = 9.0          # equal ones across a border
+    x = x.to(dtype)
+    scores = -torch.rand(rows // K, K, generator=gen, device="cuda")
+    for n in (4, 40, 128):
+        _check(x, scores, n, gdn.gdn_beam_select(x, scores, n=n))
+
+
 def test_rows_of_any_stride_and_outputs_in_place():
     gen = torch.Generator(device="cuda").manual_seed(5)
     wide = torch.randn(12, 5003, generator=gen, device="cuda").to(BF16)

@@ -4,13 +4,14 @@
 // and of a group's K V totals the n largest, ties to the lowest k V + t.  The logits are read once, in two
 // launches.
 //
-// The first cuts every row into pieces, one CTA each, held in registers: the piece's maximum m and sum of
-// exp(x - m), and its n largest logits.  For these, the CTA's threads form groups whose maxima are at hand: at
-// least n values reach the n-th largest of them, and few more do (n = 8 of 32 groups: some 9 of 16384 values), so
-// those go into a list and are ranked by counting.  A list that overflows (many equal logits) is left for n
-// rounds of the CTA-wide largest value below the last one.
+// The first gives a CTA a span of a row, which it goes through in pieces that fit its registers, with a reference m, the
+// sum of exp(x - m), and the n largest logits so far.  In a first piece (with at least n values above -inf, else in the next too) the threads form groups whose maxima are at hand: at
+// least n values reach the n-th largest of them, and few more do (n = 8 of 32 groups: some 9 of 16384 values).  Later
+// pieces have few values above the n-th largest so far.  Those go into a list and are ranked by counting, together with
+// the ones before.  A list that overflows (equal or rising logits) is left for n rounds of the CTA-wide largest value
+// below the last one.
 //
-// The second, a CTA to a group of beams, joins the pieces' sums, and takes the n best of their candidates the
+// The second, a CTA to a group of beams, joins the spans' sums, and takes the n best of their candidates the
 // same way.  Totals and their comparison are in 64 bits: only the error of the row's sum (fp32 terms) is left
 // in the order of beams.
 #include <algorithm>
@@ -25,13 +26,14 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kList = 1024;  // candidates that are ranked by counting
+constexpr int kSpanTarget = 8 * 152;  // spans to go for
 constexpr int kNear = 3072;  // candidates of a group that are kept in shared memory
 
-struct Pieces {  // in the workspace
-    float *m;    // [rows][pieces]: maximum
-    float *sum;  // [rows][pieces]: sum of exp(x - m), 0 for a piece of nothing but -inf
-    float *x;    // [rows][pieces][n]: the largest logits, descending; -inf past the last
-    int *token;  // [rows][pieces][n]
+struct Spans {   // in the workspace
+    float *m;    // [rows][spans]: what the sum is relative to, within 16 of the maximum; -inf: nothing but -inf
+    float *sum;  // [rows][spans]: sum of exp(x - m)
+    float *x;    // [rows][spans][n]: the largest logits, descending; -inf past the last
+    int *token;  // [rows][spans][n]
 };
 
 // A value in the order of its bits as an unsigned number, and the position behind it: of equal values the
@@ -106,140 +108,192 @@ __device__ __forceinline__ float nth_maximum(float x, int n, int groups, float *
     return y.x;
 }
 
+__device__ __forceinline__ float of_key(uint32_t high) {
+    return __uint_as_float(high & 0x80000000u ? high & 0x7fffffffu : ~high);
+}
+
 template <typename T, int ELEMS>
 __global__ void __launch_bounds__(kThreads, ELEMS <= 8 ? 6 : 4)
-    beam_pieces_kernel(const T *__restrict__ logits, long stride, const uint8_t *__restrict__ finished, Pieces out, int V,
-                       int n, int pieces) {
+    beam_spans_kernel(const T *__restrict__ logits, long stride, const uint8_t *__restrict__ finished, Spans out, int V,
+                      int n, int spans, int pieces) {
     constexpr int VEC = 16 / sizeof(T), VECS = ELEMS / VEC;
+    using Key = unsigned long long;
     __shared__ __align__(16) float s_all[kThreads];
-    __shared__ unsigned long long s_list[kList], s_top[kThreads / 32];
+    __shared__ Key s_list[kList], s_top[kThreads / 32], s_best[2][kBeamMaxN];
     __shared__ float2 s_nth[kThreads / 32];
-    __shared__ int s_n;
+    __shared__ int s_n[3];  // of a piece; cleared a piece before its turn, when nobody looks at it
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const long row = blockIdx.x / pieces;
-    const int piece = blockIdx.x % pieces;
+    const long row = blockIdx.x / spans;
+    const int span = blockIdx.x % spans;
     pdl_wait_primary();
     pdl_launch_dependents();
     if (finished != nullptr && __ldg(finished + row) != 0) return;  // (nothing of it is looked at)
     const T *x = logits + row * stride;
-    // Vectors lie on 16-byte boundaries: the first may begin before the row.
+    // Vectors lie on 16-byte boundaries: the first may begin before the row.  (Places up to a piece past V fit: beam_select_fits)
     const int skew = (int)(((uintptr_t)x / sizeof(T)) % VEC);
-    const int first = piece * (ELEMS * kThreads) - skew;  // (places up to a piece past V: see beam_select_fits)
+    const int from = span * pieces * (ELEMS * kThreads) - skew;
+    if (tid < 3) s_n[tid] = 0;
 
-    Vec16<T> w[VECS];
-    const auto value = [&](int i) { return to_f32(w[i / VEC].v[i % VEC]); };
-    const auto token = [&](int i) { return first + (i / VEC * kThreads + tid) * VEC + i % VEC; };
-    if (tid == 0) s_n = 0;
+    constexpr float kL = 1.4426950408889634f;
+    float sum = 0.f, sum_lo = 0.f;  // of this thread
+    float base = -INFINITY;         // m
+    float least = -INFINITY;        // the n-th largest so far
+    int have = 0;                   // best ones so far, in s_best[piece & 1]
+#pragma unroll 1
+    for (int piece = 0; piece < pieces; ++piece) {
+        const int first = from + piece * (ELEMS * kThreads);
+        if (first >= V) break;
+        Vec16<T> w[VECS];
+        const auto value = [&](int i) { return to_f32(w[i / VEC].v[i % VEC]); };
+        const auto token = [&](int i) { return first + (i / VEC * kThreads + tid) * VEC + i % VEC; };
+        const auto read = [&](int at) { return at >= 0 && at < V ? fmaxf(to_f32(x[at]), -INFINITY) : -INFINITY; };
 #pragma unroll
-    for (int j = 0; j < VECS; ++j) {
-        const int at = first + (j * kThreads + tid) * VEC;
-        if (at >= 0 && at <= V - VEC) {
-            w[j].u = __ldg(reinterpret_cast<const uint4 *>(x + at));
+        for (int j = 0; j < VECS; ++j) {
+            const int at = first + (j * kThreads + tid) * VEC;
+            if (at >= 0 && at <= V - VEC) {
+                w[j].u = __ldg(reinterpret_cast<const uint4 *>(x + at));
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) w[j].v[i] = at + i >= 0 && at + i < V ? x[at + i] : from_f32<T>(-INFINITY);
+            }
+        }
+        // (NaN is passed over: it is no candidate)
+        float mine = -INFINITY;
+        if constexpr (sizeof(T) == 2) {
+            __nv_bfloat162 top = __float2bfloat162_rn(-INFINITY);
+#pragma unroll
+            for (int j = 0; j < VECS; ++j)
+#pragma unroll
+                for (int i = 0; i < VEC / 2; ++i) top = __hmax2(top, reinterpret_cast<const __nv_bfloat162 *>(w + j)[i]);
+            mine = fmaxf(__low2float(top), __high2float(top));
         } else {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) w[j].v[i] = at + i >= 0 && at + i < V ? x[at + i] : from_f32<T>(-INFINITY);
+            for (int i = 0; i < ELEMS; ++i) mine = fmaxf(mine, value(i));
         }
-    }
-    // (NaN is passed over: it is no candidate)
-    float mine = -INFINITY;
-    if constexpr (sizeof(T) == 2) {
-        __nv_bfloat162 top = __float2bfloat162_rn(-INFINITY);
-#pragma unroll
-        for (int j = 0; j < VECS; ++j)
-#pragma unroll
-            for (int i = 0; i < VEC / 2; ++i) top = __hmax2(top, reinterpret_cast<const __nv_bfloat162 *>(w + j)[i]);
-        mine = fmaxf(__low2float(top), __high2float(top));
-    } else {
-#pragma unroll
-        for (int i = 0; i < ELEMS; ++i) mine = fmaxf(mine, value(i));
-    }
-    float m;  // (barriers)
-    const float least = nth_maximum(mine, n, n <= 32 ? 32 : kThreads, s_all, s_nth, m);
 
-    // ---- sum of exp(x - m) = 2^(x L - m L), L = log2(e): a product and a sum in one rounding, and the rounding of m L, which
-    // all terms share, is taken back at the end (2^-t = 1 - t ln 2 + ..., t < 2^-10).  Large m, or a NaN: x - m first.
-    constexpr float kL = 1.4426950408889634f;
-    const float base = m == -INFINITY ? 0.f : m, mL = __fmul_rn(base, kL);
-    const auto sum_of = [&](auto term) {
-        float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int i = 0; i < ELEMS; i += 2) {
-            float2 e = term(make_float2(value(i), value(i + 1)));
-            asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
-            asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
-            part[i / 2 & 1] = __fadd2_rn(part[i / 2 & 1], e);
+        // ---- the list of what may be among the n largest: values from this piece's n-th largest on (or near it), or above the
+        // n-th largest of earlier pieces, whose places are lower
+        bool some;
+        float reach;
+        if (have < n) {
+            float top;
+            reach = nth_maximum(mine, n, n <= 32 ? 32 : kThreads, s_all, s_nth, top);  // (barriers)
+            some = mine >= reach && mine != -INFINITY;
+        } else {
+            reach = nextafterf(least, INFINITY);
+            some = mine > least;
         }
-        const float2 both = __fadd2_rn(part[0], part[1]);
-        return both.x + both.y;
-    };
-    float sum = sum_of([&](float2 x) { return __ffma2_rn(x, make_float2(kL, kL), make_float2(-mL, -mL)); });
-    const float t = 0.69314718f * __fmaf_rn(base, kL, -mL);
-    sum *= 1.f + t * (0.5f * t - 1.f);
-    if (sum != sum || fabsf(base) > 8192.f)
-        sum = sum_of([&](float2 x) {
-            return make_float2((fmaxf(x.x, -INFINITY) - base) * kL, (fmaxf(x.y, -INFINITY) - base) * kL);
-        });
-    s_all[tid] = sum;  // (the maxima have been read)
-
-    // ---- the list of what reaches `least`
-    // Few threads have such values: the warp reads those of one of them at a time again (registers would have to be indexed).
-    const auto read = [&](int at) { return at >= 0 && at < V ? fmaxf(to_f32(x[at]), -INFINITY) : -INFINITY; };
-    for (unsigned left = __ballot_sync(0xffffffffu, mine >= least && mine != -INFINITY); left != 0; left &= left - 1) {
+        // Few threads have such values: the warp reads those of one of them at a time again (registers would have to be indexed).
+        for (unsigned left = __ballot_sync(0xffffffffu, some); left != 0; left &= left - 1)
 #pragma unroll
-        for (int e = lane; e < ELEMS; e += 32) {
-            const int at = first + (e / VEC * kThreads + warp * 32 + __ffs(left) - 1) * VEC + e % VEC;
-            const float v = read(at);
-            if (v >= least && v != -INFINITY) {
-                const int k = atomicAdd(&s_n, 1);
-                if (k < kList) s_list[k] = key_of(v, at);
+            for (int e = lane; e < ELEMS; e += 32) {
+                const int at = first + (e / VEC * kThreads + warp * 32 + __ffs(left) - 1) * VEC + e % VEC;
+                const float v = read(at);
+                if (v >= reach && v != -INFINITY) {
+                    const int k = atomicAdd(&s_n[piece % 3], 1);
+                    if (k < kList) s_list[k] = key_of(v, at);
+                }
             }
-        }
-    }
-    __syncthreads();
-    const long o = row * pieces + piece;
-    if (warp == kThreads / 32 - 1) {  // (the first warp ranks the list)
-        float lo = 0.f;
-        sum = s_all[lane];
-#pragma unroll
-        for (int w = 1; w < kThreads / 32; ++w) add_two(sum, lo, s_all[w * 32 + lane], 0.f);
-        warp_sum_two(sum, lo);
-        if (lane == 0) out.m[o] = m, out.sum[o] = sum + lo;
-    }
-    auto put = [&](int rank, unsigned long long key) {
-        const uint32_t b = (uint32_t)(key >> 32);
-        out.x[o * n + rank] = __uint_as_float(b & 0x80000000u ? b & 0x7fffffffu : ~b);
-        out.token[o * n + rank] = (int)(0xffffffffu - (uint32_t)key);
-    };
-    int found = s_n;
-    if (found <= kList) {
-        for (int i = tid; i < found; i += kThreads) {
-            const unsigned long long key = s_list[i];
-            int rank = 0;
-            for (int j = 0; j < found && rank < n; ++j) rank += s_list[j] > key;
-            if (rank < n) put(rank, key);
-        }
-    } else {
-        unsigned long long last = ~0ull;
-        for (found = 0; found < n; ++found) {
-            unsigned long long best = 0;
+        const bool any = __syncthreads_or(some);
+        if (tid == 0) s_n[(piece + 2) % 3] = 0;
+        if (any) {
+            const Key *best = s_best[piece & 1];
+            Key *next = s_best[(piece & 1) ^ 1];
+            int found = s_n[piece % 3];
+            if (found <= kList) {
+                for (int i = tid; i < have + found; i += kThreads) {
+                    const Key key = i < have ? best[i] : s_list[i - have];
+                    int rank = 0;
+                    for (int j = 0; j < have; ++j) rank += best[j] > key;
+                    for (int j = 0; j < found && rank < n; ++j) rank += s_list[j] > key;
+                    if (rank < n) next[rank] = key;
+                }
+                have = min(n, have + found);
+            } else {
+                Key last = ~0ull;
+                for (found = 0; found < n; ++found) {
+                    Key top = tid < have && best[tid] < last ? best[tid] : 0;
 #pragma unroll 4
-            for (int i = 0; i < ELEMS; ++i) {
-                const float v = read(token(i));
-                const unsigned long long key = key_of(v, token(i));
-                if (v != -INFINITY && key < last && key > best) best = key;
-            }
-            best = warp_max(best);
-            if (lane == 0) s_top[warp] = best;
-            __syncthreads();
+                    for (int i = 0; i < ELEMS; ++i) {
+                        const float v = read(token(i));
+                        const Key key = key_of(v, token(i));
+                        if (v != -INFINITY && key < last && key > top) top = key;
+                    }
+                    top = warp_max(top);
+                    if (lane == 0) s_top[warp] = top;
+                    __syncthreads();
 #pragma unroll
-            for (int w = 0; w < kThreads / 32; ++w) best = s_top[w] > best ? s_top[w] : best;
+                    for (int w = 0; w < kThreads / 32; ++w) top = s_top[w] > top ? s_top[w] : top;
+                    __syncthreads();
+                    if (top == 0) break;
+                    if (tid == 0) next[found] = top;
+                    last = top;
+                }
+                have = found;
+            }
             __syncthreads();
-            if (best == 0) break;
-            if (tid == 0) put(found, best);
-            last = best;
+            // (have > 0: some value was above -inf)
+            const float top = of_key((uint32_t)(next[0] >> 32));
+            if (have == n) least = of_key((uint32_t)(next[n - 1] >> 32));
+            if (base == -INFINITY) {
+                base = top;
+            } else if (top > base + 16.f) {
+                const float f = exp2f((base - top) * kL);
+                sum *= f, sum_lo *= f, base = top;
+            }
+        } else {  // the best ones stay: in the place where the next piece looks for them
+            if (tid < have) s_best[(piece & 1) ^ 1][tid] = s_best[piece & 1][tid];
+        }
+
+        // ---- sum of exp(x - m) = 2^(x L - m L), L = log2(e): a product and a sum in one rounding, and the rounding of m L, which
+        // all terms share, is taken back at the end (2^-t = 1 - t ln 2 + ..., t < 2^-10).  Large m, or a NaN: x - m first.
+        if (base != -INFINITY) {
+            const float mL = __fmul_rn(base, kL);
+            const auto sum_of = [&](auto term) {
+                float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int i = 0; i < ELEMS; i += 2) {
+                    float2 e = term(make_float2(value(i), value(i + 1)));
+                    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+                    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+                    part[i / 2 & 1] = __fadd2_rn(part[i / 2 & 1], e);
+                }
+                const float2 both = __fadd2_rn(part[0], part[1]);
+                return both.x + both.y;
+            };
+            float more = sum_of([&](float2 x) { return __ffma2_rn(x, make_float2(kL, kL), make_float2(-mL, -mL)); });
+            const float t = 0.69314718f * __fmaf_rn(base, kL, -mL);
+            more *= 1.f + t * (0.5f * t - 1.f);
+            if (more != more || fabsf(base) > 8192.f)
+                more = sum_of([&](float2 x) {
+                    return make_float2((fmaxf(x.x, -INFINITY) - base) * kL, (fmaxf(x.y, -INFINITY) - base) * kL);
+                });
+            add_two(sum, sum_lo, more, 0.f);
+        }
+        if (piece + 1 == pieces || first + ELEMS * kThreads >= V) {  // the span's end
+            warp_sum_two(sum, sum_lo);
+            __syncthreads();
+            if (lane == 0) s_nth[warp] = make_float2(sum, sum_lo);
+            __syncthreads();
+            const long o = row * spans + span;
+            if (tid == 0) {
+#pragma unroll
+                for (int w = 1; w < kThreads / 32; ++w) add_two(sum, sum_lo, s_nth[w].x, s_nth[w].y);
+                out.m[o] = base, out.sum[o] = sum + sum_lo;
+            }
+            const Key *best = s_best[(piece & 1) ^ 1];
+            for (int i = tid; i < n; i += kThreads) {
+                out.x[o * n + i] = i < have ? of_key((uint32_t)(best[i] >> 32)) : -INFINITY;
+                out.token[o * n + i] = i < have ? (int)(0xffffffffu - (uint32_t)best[i]) : -1;
+            }
         }
     }
-    for (int i = min(found, n) + tid; i < n; i += kThreads) out.x[o * n + i] = -INFINITY, out.token[o * n + i] = -1;
+    // (a span that begins past V: rounding up may leave one)
+    if (from >= V) {
+        const long o = row * spans + span;
+        if (tid == 0) out.m[o] = -INFINITY, out.sum[o] = 0.f;
+        for (int i = tid; i < n; i += kThreads) out.x[o * n + i] = -INFINITY, out.token[o * n + i] = -1;
+    }
 }
 
 struct Pick {
@@ -250,7 +304,7 @@ __device__ __forceinline__ bool before(unsigned long long a, int ia, unsigned lo
     return a > b || (a == b && ia < ib);
 }
 
-__global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamSelect p, Pieces in, int pieces) {
+__global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamSelect p, Spans in, int spans) {
     __shared__ double s_lse[kBeamMaxK];
     __shared__ __align__(16) float s_all[kThreads];
     __shared__ float2 s_least[kThreads / 32];
@@ -263,10 +317,10 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamSelect p,
     __shared__ int s_token[kNear];
     __shared__ int s_n;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = blockIdx.x, K = p.K, n = p.n;
-    const int per_beam = pieces * n, all = K * per_beam;
+    const int per_beam = spans * n, all = K * per_beam;
     pdl_wait_primary();
     // All that is read comes at once: the candidates (as many as there is room for), scores and flags (which may be written
-    // over below, by this CTA alone), and the pieces' sums.
+    // over below, by this CTA alone), and the spans' sums.
 #pragma unroll 4
     for (int c = tid; c < min(all, kNear); c += kThreads) {
         s_x[c] = __ldcg(in.x + (long)g * all + c);
@@ -279,11 +333,11 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamSelect p,
         s_done[k] = p.finished != nullptr && p.finished[(long)g * K + k] != 0;
     }
     for (int k = warp; k < K; k += kThreads / 32) {  // (of a beam at its end: of no meaning)
-        const long o = ((long)g * K + k) * pieces;
+        const long o = ((long)g * K + k) * spans;
         float m = -INFINITY, sum = 0.f, lo = 0.f;
-        for (int i0 = 0; i0 < pieces; i0 += 32) {
+        for (int i0 = 0; i0 < spans; i0 += 32) {
             const int i = i0 + lane;
-            const float mi = i < pieces ? __ldcg(in.m + o + i) : -INFINITY, si = i < pieces ? __ldcg(in.sum + o + i) : 0.f;
+            const float mi = i < spans ? __ldcg(in.m + o + i) : -INFINITY, si = i < spans ? __ldcg(in.sum + o + i) : 0.f;
             const float top = fmaxf(m, warp_max(mi));
             if (top > m && m != -INFINITY) {
                 const float f = expf(m - top);
@@ -423,22 +477,29 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamSelect p,
     }
 }
 
-// 128 bytes to a thread, or 8 values while that leaves SMs without work.
-int piece_size(int rows, int V, int dtype) {
-    const int most = dtype == GDN_BF16 ? 16384 : 8192;
-    return (long)rows * ((V + (long)most - 1) / most) < 4 * 152 ? 2048 : most;
+// How rows are cut: pieces of 128 bytes to a thread, several to a span where there are spans enough for all SMs; 8 values to a
+// thread while that leaves SMs without work.
+struct Cut {
+    int elems, spans, pieces;  // of a thread; of a row; of a span
+};
+Cut cut_rows(int rows, int V, int dtype) {
+    const auto pieces = [&](int elems) { return (int)(((long)V + 7 + elems * kThreads - 1) / (elems * kThreads)); };  // (7: the skew)
+    Cut c;
+    c.elems = dtype == GDN_BF16 ? 64 : 32;
+    int all = pieces(c.elems);
+    if ((long)rows * all < 4 * 152) return Cut{8, pieces(8), 1};
+    const int spans = std::max(1, std::min(all, (kSpanTarget + rows - 1) / rows));
+    c.pieces = (all + spans - 1) / spans;
+    c.spans = (all + c.pieces - 1) / c.pieces;
+    return c;
 }
-int piece_count(int rows, int V, int dtype) {
-    const int size = piece_size(rows, V, dtype);
-    return (int)(((long)V + 7 + size - 1) / size);  // (up to 7 values of the first vector lie before the row)
-}
-int most_pieces(int rows, int V) { return std::max(piece_count(rows, V, GDN_BF16), piece_count(rows, V, GDN_F32)); }
+int most_spans(int rows, int V) { return std::max(cut_rows(rows, V, GDN_BF16).spans, cut_rows(rows, V, GDN_F32).spans); }
 
 template <typename T, int ELEMS>
-cudaError_t launch_pieces(const BeamSelect &p, const Pieces &w, int pieces, cudaStream_t s) {
+cudaError_t launch_spans(const BeamSelect &p, const Spans &w, const Cut &c, cudaStream_t s) {
     const cudaError_t e =
-        launch_kernel(beam_pieces_kernel<T, ELEMS>, dim3((unsigned)(p.G * p.K * pieces)), dim3(kThreads), 0, s, true,
-                      static_cast<const T *>(p.logits), p.stride, p.finished, w, p.V, p.n, pieces);
+        launch_kernel(beam_spans_kernel<T, ELEMS>, dim3((unsigned)(p.G * p.K * c.spans)), dim3(kThreads), 0, s, true,
+                      static_cast<const T *>(p.logits), p.stride, p.finished, w, p.V, p.n, c.spans, c.pieces);
     note_launch();
     return e;
 }
@@ -446,28 +507,29 @@ cudaError_t launch_pieces(const BeamSelect &p, const Pieces &w, int pieces, cuda
 }  // namespace
 
 size_t beam_select_workspace(int G, int K, int V, int n) {
-    const size_t rows = (size_t)G * K, pieces = (size_t)most_pieces(G * K, V);
-    return rows * pieces * (8 + 8 * (size_t)n);
+    return (size_t)G * K * most_spans(G * K, V) * (8 + 8 * (size_t)n);
 }
 
 bool beam_select_fits(int G, int K, int V, int n) {
-    return (long)G * K * most_pieces(G * K, V) <= INT_MAX && V <= INT_MAX - 4 * 16384 && (long)K * most_pieces(G * K, V) * n <= INT_MAX;
+    if (V > INT_MAX - 4 * 64 * kThreads) return false;
+    const long spans = most_spans(G * K, V);
+    return (long)G * K * spans <= INT_MAX && K * spans * n <= INT_MAX;
 }
 
 cudaError_t launch_beam_select(const BeamSelect &p, int dtype, void *ws, cudaStream_t s) {
-    const int rows = p.G * p.K, pieces = piece_count(rows, p.V, dtype);
-    const size_t all = (size_t)rows * pieces;
-    Pieces w;
+    const int rows = p.G * p.K;
+    const Cut c = cut_rows(rows, p.V, dtype);
+    const size_t all = (size_t)rows * c.spans;
+    Spans w;
     w.m = static_cast<float *>(ws), w.sum = w.m + all, w.x = w.sum + all;
     w.token = reinterpret_cast<int *>(w.x + all * p.n);
-    const bool small = piece_size(rows, p.V, dtype) == 2048;
     cudaError_t e;
     if (dtype == GDN_BF16)
-        e = small ? launch_pieces<__nv_bfloat16, 8>(p, w, pieces, s) : launch_pieces<__nv_bfloat16, 64>(p, w, pieces, s);
+        e = c.elems == 8 ? launch_spans<__nv_bfloat16, 8>(p, w, c, s) : launch_spans<__nv_bfloat16, 64>(p, w, c, s);
     else
-        e = small ? launch_pieces<float, 8>(p, w, pieces, s) : launch_pieces<float, 32>(p, w, pieces, s);
+        e = c.elems == 8 ? launch_spans<float, 8>(p, w, c, s) : launch_spans<float, 32>(p, w, c, s);
     if (e != cudaSuccess) return e;
-    e = launch_kernel(beam_join_kernel, dim3((unsigned)p.G), dim3(kThreads), 0, s, true, p, w, pieces);
+    e = launch_kernel(beam_join_kernel, dim3((unsigned)p.G), dim3(kThreads), 0, s, true, p, w, c.spans);
     note_launch();
     return e;
 }
