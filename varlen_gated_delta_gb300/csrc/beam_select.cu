@@ -25,7 +25,7 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kList = 1024;  // candidates that are ranked by counting
+constexpr int kList = 512;  // candidates that are ranked by counting
 constexpr int kSpanTarget = 8 * 152;  // spans to go for
 constexpr int kNear = 3072;  // candidates of a group that are kept in shared memory
 
@@ -113,11 +113,12 @@ __device__ __forceinline__ float of_key(uint32_t high) {
 }
 
 template <typename T, int ELEMS>
-__global__ void __launch_bounds__(kThreads, ELEMS <= 8 ? 6 : 4)
+__global__ void __launch_bounds__(kThreads, ELEMS <= 8 ? 6 : 3)
     beam_spans_kernel(const T *__restrict__ logits, long stride, const uint8_t *__restrict__ finished, Spans out, int V,
                       int n, int spans, int pieces) {
     constexpr int VEC = 16 / sizeof(T), VECS = ELEMS / VEC;
     using Key = unsigned long long;
+    extern __shared__ uint4 s_data[];  // [2 stages][VECS][kThreads]: each thread's own vectors of a piece and of the next
     __shared__ __align__(16) float s_all[kThreads];
     __shared__ Key s_list[kList], s_top[kThreads / 32], s_best[2][kBeamMaxN];
     __shared__ float2 s_nth[kThreads / 32];
@@ -139,24 +140,41 @@ __global__ void __launch_bounds__(kThreads, ELEMS <= 8 ? 6 : 4)
     float base = -INFINITY;         // m
     float least = -INFINITY;        // the n-th largest so far
     int have = 0;                   // best ones so far, in s_best[piece & 1]
+    const auto fetch = [&](int piece) {
+        const int first = from + piece * (ELEMS * kThreads);
+        if (piece < pieces && first < V) {
+            uint4 *stage = s_data + (piece & 1) * VECS * kThreads + tid;
+#pragma unroll
+            for (int j = 0; j < VECS; ++j) {
+                const int at = first + (j * kThreads + tid) * VEC;
+                if (at >= 0 && at <= V - VEC) {
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(stage + j * kThreads)),
+                                 "l"(x + at)
+                                 : "memory");
+                } else {
+                    Vec16<T> w;
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) w.v[i] = at + i >= 0 && at + i < V ? x[at + i] : from_f32<T>(-INFINITY);
+                    stage[j * kThreads] = w.u;
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    fetch(0);
 #pragma unroll 1
     for (int piece = 0; piece < pieces; ++piece) {
         const int first = from + piece * (ELEMS * kThreads);
         if (first >= V) break;
+        fetch(piece + 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncwarp();  // (the warp's vectors are here: its lanes read each other's below)
+        const uint4 *stage = s_data + (piece & 1) * VECS * kThreads;
         Vec16<T> w[VECS];
+#pragma unroll
+        for (int j = 0; j < VECS; ++j) w[j].u = stage[j * kThreads + tid];
         const auto value = [&](int i) { return to_f32(w[i / VEC].v[i % VEC]); };
         const auto token = [&](int i) { return first + (i / VEC * kThreads + tid) * VEC + i % VEC; };
-        const auto read = [&](int at) { return at >= 0 && at < V ? fmaxf(to_f32(x[at]), -INFINITY) : -INFINITY; };
-#pragma unroll
-        for (int j = 0; j < VECS; ++j) {
-            const int at = first + (j * kThreads + tid) * VEC;
-            if (at >= 0 && at <= V - VEC) {
-                w[j].u = __ldg(reinterpret_cast<const uint4 *>(x + at));
-            } else {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) w[j].v[i] = at + i >= 0 && at + i < V ? x[at + i] : from_f32<T>(-INFINITY);
-            }
-        }
         // (NaN is passed over: it is no candidate)
         float mine = -INFINITY;
         if constexpr (sizeof(T) == 2) {
@@ -183,12 +201,12 @@ __global__ void __launch_bounds__(kThreads, ELEMS <= 8 ? 6 : 4)
             reach = nextafterf(least, INFINITY);
             some = mine > least;
         }
-        // Few threads have such values: the warp reads those of one of them at a time again (registers would have to be indexed).
+        // Few threads have such values: the warp looks at those of one of them at a time.
         for (unsigned left = __ballot_sync(0xffffffffu, some); left != 0; left &= left - 1)
 #pragma unroll
             for (int e = lane; e < ELEMS; e += 32) {
-                const int at = first + (e / VEC * kThreads + warp * 32 + __ffs(left) - 1) * VEC + e % VEC;
-                const float v = read(at);
+                const int place = e / VEC * kThreads + warp * 32 + __ffs(left) - 1, at = first + place * VEC + e % VEC;
+                const float v = fmaxf(to_f32(reinterpret_cast<const T *>(stage + place)[e % VEC]), -INFINITY);
                 if (v >= reach && v != -INFINITY) {
                     const int k = atomicAdd(&s_n[piece % 3], 1);
                     if (k < kList) s_list[k] = key_of(v, at);
@@ -215,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, ELEMS <= 8 ? 6 : 4)
                     Key top = tid < have && best[tid] < last ? best[tid] : 0;
 #pragma unroll 4
                     for (int i = 0; i < ELEMS; ++i) {
-                        const float v = read(token(i));
+                        const float v = fmaxf(to_f32(reinterpret_cast<const T *>(stage + i / VEC * kThreads + tid)[i % VEC]), -INFINITY);
                         const Key key = key_of(v, token(i));
                         if (v != -INFINITY && key < last && key > top) top = key;
                     }
@@ -497,8 +515,13 @@ int most_spans(int rows, int V) { return std::max(cut_rows(rows, V, GDN_BF16).sp
 
 template <typename T, int ELEMS>
 cudaError_t launch_spans(const BeamSelect &p, const Spans &w, const Cut &c, cudaStream_t s) {
-    const cudaError_t e =
-        launch_kernel(beam_spans_kernel<T, ELEMS>, dim3((unsigned)(p.G * p.K * c.spans)), dim3(kThreads), 0, s, true,
+    constexpr int kBytes = 2 * ELEMS * kThreads * sizeof(T);
+    static std::atomic<uint64_t> attr_set{0};
+    cudaError_t e = once_per_device(attr_set, [] {
+        return cudaFuncSetAttribute(beam_spans_kernel<T, ELEMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    });
+    if (e != cudaSuccess) return e;
+    e = launch_kernel(beam_spans_kernel<T, ELEMS>, dim3((unsigned)(p.G * p.K * c.spans)), dim3(kThreads), kBytes, s, true,
                       static_cast<const T *>(p.logits), p.stride, p.finished, w, p.V, p.n, c.spans, c.pieces);
     note_launch();
     return e;
