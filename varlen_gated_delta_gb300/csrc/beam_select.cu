@@ -222,8 +222,10 @@ __global__ void __launch_bounds__(kThreads, ELEMS <= 8 ? 6 : 3)
                 for (int i = tid; i < have + found; i += kThreads) {
                     const Key key = i < have ? best[i] : s_list[i - have];
                     int rank = 0;
+#pragma unroll 8
                     for (int j = 0; j < have; ++j) rank += best[j] > key;
-                    for (int j = 0; j < found && rank < n; ++j) rank += s_list[j] > key;
+#pragma unroll 8
+                    for (int j = 0; j < found; ++j) rank += s_list[j] > key;
                     if (rank < n) next[rank] = key;
                 }
                 have = min(n, have + found);
@@ -417,7 +419,8 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamSelect p,
             const unsigned long long t = s_total[i];
             const int at = s_at[i];
             int rank = 0;
-            for (int j = 0; j < found && rank < n; ++j) rank += before(s_total[j], s_at[j], t, at);
+#pragma unroll 8
+            for (int j = 0; j < found; ++j) rank += before(s_total[j], s_at[j], t, at);
             if (rank < n) s_pick[rank] = Pick{t, at};
         }
     } else {
