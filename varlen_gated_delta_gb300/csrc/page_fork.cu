@@ -48,16 +48,16 @@ __device__ __forceinline__ int block_scan(int x, int &all, int *s_sum) {
 }
 
 // The part of n things that thread `i` of `of` takes: [lo, hi), in whole multiples of 16.
-__device__ __forceinline__ void share(long n, long i, long of, long &lo, long &hi) {
-    const long per = (((n + of - 1) / of) + 15) / 16 * 16;
-    lo = min(n, i * per), hi = min(n, lo + per);
+__device__ __forceinline__ void share(int n, int i, int of, int &lo, int &hi) {
+    const int per = ((n + of - 1) / of + 15) / 16 * 16;
+    lo = (int)min((long)n, (long)i * per), hi = min(n, lo + per);
 }
 
 // f(i) for the pages of [lo, hi) (lo a multiple of 16) whose mark in `a` is set and whose mark in `b`, if given, is not;
 // neither(i) for the others.
 template <typename F, typename G>
-__device__ __forceinline__ void for_marks(const uint8_t *a, const uint8_t *b, long lo, long hi, F f, G neither) {
-    for (long i = lo; i < hi; i += 16) {
+__device__ __forceinline__ void for_marks(const uint8_t *a, const uint8_t *b, int lo, int hi, F f, G neither) {
+    for (int i = lo; i < hi; i += 16) {
         const uint4 x = __ldcg(reinterpret_cast<const uint4 *>(a + i));
         uint32_t w[4] = {x.x, x.y, x.z, x.w};
         if (b != nullptr) {
@@ -86,8 +86,8 @@ template <typename W, typename F>
 __device__ __forceinline__ void for_entries(int rows, int columns, W width, F f) {
     const int lane = threadIdx.x & 31, warp = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), warps = gridDim.x * (kThreads / 32);
     const int parts = (columns + 127) / 128;
-    for (long item = warp; item < (long)rows * parts; item += warps) {
-        const int row = (int)(item / parts), first = (int)(item % parts) * 128 + lane, n = width(row);
+    for (int item = warp; item < rows * parts; item += warps) {  // (rows * columns fits)
+        const int row = item / parts, first = (item - row * parts) * 128 + lane, n = width(row);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             if (first + 32 * k < n) f(row, first + 32 * k);
@@ -163,10 +163,10 @@ __global__ void __launch_bounds__(kThreads) page_fork_kernel(const PageFork p, F
     cluster.sync();
 
     // ---- pages that go back to the list, in their order
-    long lo, hi;
-    share(p.num_pages, t0, step, lo, hi);
+    int lo, hi;
+    share(p.num_pages, (int)t0, (int)step, lo, hi);
     int back = 0, all = 0;
-    for (long i = lo; i < hi; i += 16) {
+    for (int i = lo; i < hi; i += 16) {
         const uint4 a = __ldcg(reinterpret_cast<const uint4 *>(w.was + i)), b = __ldcg(reinterpret_cast<const uint4 *>(w.is + i));
         back += __popc(a.x & ~b.x) + __popc(a.y & ~b.y) + __popc(a.z & ~b.z) + __popc(a.w & ~b.w);
     }
@@ -182,7 +182,8 @@ __global__ void __launch_bounds__(kThreads) page_fork_kernel(const PageFork p, F
     const long start = (long)cursor - freed;  // the list's place of the first page that goes back
     const int status = bad || start < 0 ? GDN_ERR_SHAPE : start + copies > p.n_free ? GDN_ERR_CAPACITY : GDN_OK;
     const bool ok = status == GDN_OK;
-    if (ok && back > 0) for_marks(w.was, w.is, lo, hi, [&](long i) { p.free_pages[start + at++] = (int)i; }, [](long) {});
+
+    if (ok && back > 0) for_marks(w.was, w.is, lo, hi, [&](int i) { p.free_pages[start + at++] = i; }, [](int) {});
     cluster.sync();
 
     // ---- the new rows
@@ -193,14 +194,14 @@ __global__ void __launch_bounds__(kThreads) page_fork_kernel(const PageFork p, F
             if (j < n) page = j == n - 1 && s_rank[i] >= 0 ? __ldcg(p.free_pages + start + s_rank[i]) : __ldcg(old + (long)s_parent[i] * M + j);
             p.table_out[(long)i * M + j] = page;
         });
-    for (long i = t0; i < p.B_out; i += step) {
+    for (int i = (int)t0; i < p.B_out; i += (int)step) {
         const int parent = s_parent[i];
         if (ok || !same_lens) p.kv_lens_out[i] = ok && parent >= 0 ? s_len[parent] : 0;
         if (ok && s_rank[i] >= 0)
             reinterpret_cast<int2 *>(p.copies)[s_rank[i]] =
                 make_int2(__ldcg(old + (long)parent * M + s_len[parent] / ps), __ldcg(p.free_pages + start + s_rank[i]));
+        if (!ok || i >= copies) reinterpret_cast<int2 *>(p.copies)[i] = make_int2(-1, -1);
     }
-    for (long i = (ok ? copies : 0) + t0; i < p.B_out; i += step) reinterpret_cast<int2 *>(p.copies)[i] = make_int2(-1, -1);
     if (t0 == 0) {
         *p.cursor_out = ok ? (int)(start + copies) : cursor;
         *p.status = status;
@@ -215,6 +216,7 @@ struct CompactSpace {
 };
 
 __global__ void __launch_bounds__(kThreads) page_compact_kernel(const PageCompact p, CompactSpace w) {
+    extern __shared__ int s_used[];  // [B]: pages of a row
     __shared__ int s_sum[32], s_bad;
     const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
     const int tid = threadIdx.x, rank = blockIdx.x, ranks = gridDim.x, ps = p.page_size, M = p.max_pages;
@@ -222,17 +224,16 @@ __global__ void __launch_bounds__(kThreads) page_compact_kernel(const PageCompac
     pdl_wait_primary();
     for (long i = t0 * 16; i < p.num_pages; i += step * 16) *reinterpret_cast<uint4 *>(w.is + i) = make_uint4(0, 0, 0, 0);
     if (tid == 0) s_bad = 0;
-    __syncthreads();
     bool bad = false;
-    const auto used = [&](int b) {
+    for (int b = tid; b < p.B; b += kThreads) {
         const int len = __ldg(p.kv_lens + b);
-        return len < 0 || len > (long)M * ps ? -1 : (len + ps - 1) / ps;
-    };
-    for_entries(p.B, M, [&](int b) {
-        const int n = used(b);
-        bad |= n < 0;
-        return n;
-    }, [&](int b, int j) {
+        const bool fits = len >= 0 && len <= (long)M * ps;
+        bad |= !fits;
+        s_used[b] = fits ? (len + ps - 1) / ps : 0;
+    }
+    __syncthreads();
+    const auto used = [&](int b) { return s_used[b]; };
+    for_entries(p.B, M, used, [&](int b, int j) {
         const int page = p.block_table[(long)b * M + j];
         bad |= page < 0 || page >= p.num_pages;
     });
@@ -245,10 +246,10 @@ __global__ void __launch_bounds__(kThreads) page_compact_kernel(const PageCompac
     if (!bad) for_entries(p.B, M, used, [&](int b, int j) { w.is[p.block_table[(long)b * M + j]] = 1; });
     cluster.sync();
 
-    long lo, hi;
-    share(p.num_pages, t0, step, lo, hi);
+    int lo, hi;
+    share(p.num_pages, (int)t0, (int)step, lo, hi);
     int mine = 0, all = 0;
-    for (long i = lo; i < hi; i += 16) {
+    for (int i = lo; i < hi; i += 16) {
         const uint4 a = __ldcg(reinterpret_cast<const uint4 *>(w.is + i));
         mine += __popc(a.x) + __popc(a.y) + __popc(a.z) + __popc(a.w);
     }
@@ -267,14 +268,14 @@ __global__ void __launch_bounds__(kThreads) page_compact_kernel(const PageCompac
     if (!bad) {
         if (lo <= live && live < hi) {  // (this thread meets the page numbered `live`)
             int n = before;
-            for_marks(w.is, nullptr, lo, live, [&](long) { ++n; }, [](long) {});
+            for_marks(w.is, nullptr, lo, live, [&](int) { ++n; }, [](int) {});
             *w.below = n;
         }
-        for_marks(w.is, nullptr, lo, hi, [&](long i) {
-            if (i >= live) w.list[p.num_pages - 1 - before] = (int)i;
+        for_marks(w.is, nullptr, lo, hi, [&](int i) {
+            if (i >= live) w.list[p.num_pages - 1 - before] = i;
             ++before;
-        }, [&](long i) {
-            if (i < live) w.list[i - before] = (int)i;
+        }, [&](int i) {
+            if (i < live) w.list[i - before] = i;
         });
     }
     cluster.sync();
@@ -402,7 +403,12 @@ cudaError_t launch_page_compact(const PageCompact &p, void *ws, cudaStream_t s) 
     w.is = reinterpret_cast<uint8_t *>(at += 128);
     w.list = reinterpret_cast<int *>(at += round16(p.num_pages));
     w.to = w.list + p.num_pages;
-    return launch_plan(page_compact_kernel, 0, std::max((long)p.B * p.max_pages, p.num_pages / 4L), p, w, s);
+    static std::atomic<uint64_t> attr_set{0};
+    const cudaError_t e = once_per_device(attr_set, [] {
+        return cudaFuncSetAttribute(page_compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPagePlanMaxB * 4);
+    });
+    if (e != cudaSuccess) return e;
+    return launch_plan(page_compact_kernel, (size_t)p.B * 4, std::max((long)p.B * p.max_pages, p.num_pages / 4L), p, w, s);
 }
 
 cudaError_t launch_page_copy(const PageCopy &c, cudaStream_t s) {
