@@ -184,6 +184,15 @@ def test_page_sizes(ps, n):
     _check(p, _run(p))
 
 
+@pytest.mark.parametrize("new", [[1], [0, 1, 3], [1, 1, 1, 70]])
+def test_more_sequences_than_threads(new):
+    rng = torch.Generator().manual_seed(len(new))
+    new = [new[i % len(new)] for i in range(300)]
+    kv = [n + int(k) for n, k in zip(new, torch.randint(0, 150, (300,), generator=rng))]
+    p = _problem(8, new, kv, 4, 2, 64, 16, BF16)
+    _check(p, _run(p))
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("n", [1, 4, 40])
 def test_long_histories_split_over_ctas(n, dtype):
@@ -250,6 +259,36 @@ def test_malformed_sequences_are_left_out(n):
     out.fill_(3.0)
     _run(dict(p, offsets=[0, -1, n, 2 * n]), out=out, max_q=n)
     assert bool((out[n + 1:] != 3).any()) or n == 1
+
+
+@pytest.mark.parametrize("n", [1, 5, 40])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_queries_off_16_byte_boundaries(dtype, n):
+    """Rows that begin at any element take the scalar loads."""
+    p = _problem(9, [n, n], [50, 120], 8, 2, 96, 16, dtype)
+    want = _run(p)
+    for first in (1, 3):
+        room = torch.zeros(2 * n, 8 * 96 + 5, dtype=dtype, device="cuda")
+        view = room[:, first:first + 8 * 96].unflatten(1, (8, 96))
+        view.copy_(p["q"])
+        got = gdn.gdn_attention_paged_kv4(view, p["caches"][0].cuda(), p["caches"][1].cuda(), p["table"].cuda(), _i32(p["kv"]),
+                                          _i32(p["offsets"]), max_q=n)
+        assert torch.equal(got, want)
+
+
+def test_another_stream_and_thread_of_work():
+    """Two calls at once, each on its own stream with a workspace of its own."""
+    p = _problem(10, [1, 30, 4], [900, 700, 65], 8, 2, 128, 64, BF16)
+    want = _run(p)
+    a = [x.cuda() for x in (p["q"], *p["caches"], p["table"])] + [_i32(p["kv"]), _i32(p["offsets"])]
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in range(3)], []
+    for _ in range(4):
+        for s in streams:
+            with torch.cuda.stream(s):
+                outs.append(gdn.gdn_attention_paged_kv4(*a, max_q=30))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
 
 
 def test_strided_queries_and_workspace():

@@ -43,13 +43,12 @@ def _state(rng, B, M, ps, pool):
     return lens, table, free, len(live)
 
 
-@pytest.mark.parametrize("B,R,M,ps,pool", [
-    (1, 1, 1, 1, 1), (4, 4, 5, 16, 40), (3, 8, 4, 3, 30), (64, 64, 20, 64, 900), (256, 100, 33, 16, 5001), (8192, 8192, 2, 16, 20000),
-    (16, 16, 300, 1, 4000)])
-@pytest.mark.parametrize("in_place", [False, True])
+FORKS = [(1, 1, 1, 1, 1), (4, 4, 5, 16, 40), (3, 8, 4, 3, 30), (64, 64, 20, 64, 900), (256, 100, 33, 16, 5001),
+         (8192, 8192, 2, 16, 20000), (16, 16, 300, 1, 4000)]
+
+
+@pytest.mark.parametrize("B,R,M,ps,pool,in_place", [(*f, False) for f in FORKS] + [(*f, True) for f in FORKS if f[0] == f[1]])
 def test_fork(B, R, M, ps, pool, in_place):
-    if in_place and B != R:
-        pytest.skip("rows differ")
     rng = random.Random(B * M + R)
     for kind in ("any", "few", "none", "same"):
         lens, table, free, cursor = _state(rng, B, M, ps, pool)
