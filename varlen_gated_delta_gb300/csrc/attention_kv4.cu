@@ -7,11 +7,21 @@
 // are taken 2^14 times as large, so that fp16 holds them to 11 bits down to 2^-28 of the row's largest; with
 // fp32 activations they too are sums of two.
 //
-// Keys are read once for the rows that share them, 9/16 bytes a channel of k and v: a tile's codes and scales
-// stream through a ring filled by 16-byte cp.async copies, are turned into fp16 tiles in shared memory, and
-// multiplied by 16-row mma.sync, a warp to 16 of 64 rows.  Work is cut by key tiles: the tiles of all (sequence, row block,
-// key-value head) triples form one list, of which every CTA takes an equal run; a CTA whose run begins or ends inside a triple
-// leaves m, l and an unscaled o for a second kernel that joins the parts.
+// Keys are read once for the rows that share them, 9/16 bytes a channel of k and v: bound by HBM for few rows, by the
+// tensor cores for many.  Three kernels, by a sequence's rows (tokens times the heads of a group):
+// - up to 64: blocks of 8 or 16 rows, values converted in the registers that a product reads (below);
+// - more, bf16: the tcgen05 kernel of attention_prompt.cu, with a warpgroup that converts;
+// - more, fp32: tiles of 64 rows by 64 keys, converted to fp16 in shared memory, 16-row mma.sync, products of both parts.
+// The first and the last cut the work by key tiles: the tiles of all (sequence, row block, key-value head) triples form one
+// list, of which every CTA takes an equal run; a CTA whose run begins or ends inside a triple leaves m, l and an
+// unscaled o for a second kernel that joins the parts.  Which parts exist follows from the lengths alone.
+//
+// 64 requests with histories of U[1, 8192] tokens, one token each, 32 heads of 128 on 8: 71 us, 3.8 TB/s.  Longer ones add 55 us
+// for 302 MB (5.5 TB/s, 0.81 of the measured copy), on top of some 15 us for launches, first dependent loads, the first tile
+// and the join (one request: 16384 tokens 17 us, 131072 43, 524288 125).  What bounds the rest is issue and latency: 336
+// instructions a warp for 16 keys of 128 channels, of which 128 convert and interleave, 64 scale and 16 multiply; 12 warps an SM
+// issue 2.1 a clock.  32 and 48 keys a warp at a time with 16 warps an SM gave 45 and 46 us for the request of 131072 tokens,
+// scoring two or four blocks of keys in turn 43 and 44.
 #include <algorithm>
 #include <cmath>
 
@@ -194,7 +204,7 @@ __device__ __forceinline__ const uint8_t *token_block(const Kv4Params &p, const 
     return static_cast<const uint8_t *>(cache) + ((long)page * p.a.HKV + h) * ((long)p.a.page_size * (p.a.D / 16) * 9);
 }
 
-// ---------------------------------------------------------------- rows by the block of 64
+// ---------------------------------------------------------------- rows by the block of 64 (fp32)
 
 template <int DP, typename T>
 struct Wide {
@@ -443,6 +453,8 @@ __global__ void __launch_bounds__(128) kv4_wide_kernel(const Kv4Params p) {
 
 // ---------------------------------------------------------------- rows by the block of 8 or 16
 
+// 16 x 5 drafts over 4096 keys, 16 heads of 256 on 2 (40 rows in three blocks): 38 us, against 80 for a tile of 64 rows.
+//
 // Rows are the columns of the products, keys and channels their rows: S^T = K Q^T and O^T = V^T P^T with 16 keys or 16
 // channels to a tile, so that a cached value is converted into the registers of one product and no row
 // of it is wasted on the few queries (8 to a column tile, NT of those).  Both contractions run over things that

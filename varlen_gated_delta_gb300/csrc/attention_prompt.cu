@@ -46,6 +46,12 @@
 // same for half the products; no pipe of theirs is full (special functions 35%, issue
 // slots 44%), they wait for tensor memory and for each other.  32 x U[1, 512], 32 heads on
 // 8: 54 us, bound by the chain of one or two key tiles an item.
+//
+// Over a 4-bit cache (KV4) the load warp copies codes and scales to a ring of two tiles, and a fourth warpgroup turns them, and
+// the queries, into fp16 tiles where the other instance's loads put bf16 ones.  4 x 512 tokens over 8192, 32 heads of
+// 128 on 8: 286 us, 930 TFLOP/s; 256 items on 152 SMs leave a sixth of the time to the second round.  Loading codes into
+// registers a tile ahead instead took 1393 us (page lookups and divisions in the converting warps); 176, 192 and 200 registers
+// to a softmax thread instead of 184 took 291, 300 and 328.
 #include <algorithm>
 #include <cmath>
 #include <exception>

@@ -14,6 +14,11 @@
 // The second, a CTA to a group of beams, joins the spans' sums, and takes the n best of their candidates the
 // same way.  Totals and their comparison are in 64 bits: only the error of the row's sum (fp32 terms) is left
 // in the order of beams.
+//
+// 64 x 8 beams of 131072 bf16 logits, a tenth of the beams at their end: 45 us, 2.7 TB/s.  Reading is not what bounds it: 20
+// million warp instructions at two a clock (two fifths of them exponentials and the conversions before them), and warps that wait
+// for a piece's ranking.  One launch's pieces without the next one's loads in flight: 55 us; one piece to a CTA: 57.
+// One group of 4 x 32768: 10 us, two launches and chains of dependent steps.
 #include <algorithm>
 #include <climits>
 #include <cmath>

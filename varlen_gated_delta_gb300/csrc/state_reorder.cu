@@ -9,6 +9,9 @@
 // read by one and written by another: for these a CTA owns a strip of columns of all rows, brings the
 // strips of all their parents into shared memory, and writes them after a barrier; strips of different
 // CTAs do not touch.  The strip is as wide as shared memory allows for B rows (256 rows: 256 bytes).
+//
+// 32 x 8 beams, two layers' states (2.1 MB a row and layer), rows kept: 141 us, 6.0 TB/s, 0.88 of the measured copy (strips for
+// all rows: 159); one request's four beams, one layer: 3.4 us.
 #include <algorithm>
 
 #include "common.cuh"
