@@ -32,7 +32,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kList = 512;  // candidates that are ranked by counting
 constexpr int kSpanTarget = 8 * 152;  // spans to go for
-constexpr int kNear = 3072;  // candidates of a group that are kept in shared memory
+constexpr int kNear = 2560;  // candidates of a group that are kept in shared memory
 
 struct Spans {   // in the workspace
     float *m;    // [rows][spans]: what the sum is relative to, within 16 of the maximum; -inf: nothing but -inf
