@@ -184,7 +184,7 @@ def test_page_sizes(ps, n):
     _check(p, _run(p))
 
 
-@pytest.mark.parametrize("new", [[1], [0, 1, 3], [1, 1, 1, 70]])
+@pytest.mark.parametrize("new", [[1], [0, 1, 3], [1, 1, 1, 70], [20, 16, 17]])
 def test_more_sequences_than_threads(new):
     rng = torch.Generator().manual_seed(len(new))
     new = [new[i % len(new)] for i in range(300)]

@@ -9,7 +9,7 @@
 //
 // Keys are read once for the rows that share them, 9/16 bytes a channel of k and v: bound by HBM for few rows, by the
 // tensor cores for many.  Three kernels, by a sequence's rows (tokens times the heads of a group):
-// - up to 64: blocks of 8 or 16 rows, values converted in the registers that a product reads (below);
+// - up to 64 (with many sequences 32): blocks of 8 or 16 rows, values converted in the registers that a product reads (below);
 // - more, bf16: the tcgen05 kernel of attention_prompt.cu, with a warpgroup that converts;
 // - more, fp32: tiles of 64 rows by 64 keys, converted to fp16 in shared memory, 16-row mma.sync, products of both parts.
 // The first and the last cut the work by key tiles: the tiles of all (sequence, row block, key-value head) triples form one
@@ -987,9 +987,15 @@ int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 size_t span_bytes(int B, int HKV, long blocks) { return ((size_t)B * blocks * HKV * 8 + 255) & ~size_t(255); }
 long row_blocks(int H, int HKV, int max_q, int rows) { return ((long)max_q * (H / HKV) + rows - 1) / rows; }
 
-// Sequences of up to so many rows run in blocks of 8 or 16, which convert the cache anew: still less than tiles of 64 rows
-// in shared memory take.
+// Sequences of up to so many rows run in blocks of 8 or 16, which convert the cache anew.  With a pair of (sequence,
+// head) to every half SM the tcgen05 kernel takes three or four blocks' rows at once without splitting keys (64 requests,
+// 16 tokens each over U[1, 4096], 32 heads of 128 on 8: 230 us in four blocks, 156 there; in two blocks 126 and 152);
+// with fewer pairs the blocks' even runs win (8 requests over U[1, 8192]: 57 and 72; 2 over U[1, 65536]: 90 and 93), and for
+// heads of 256 (16 requests of 40 rows: 38 and 53).
 constexpr int kNarrowRows = kSplitRows;
+int narrow_rows(const Attn &a, int dtype) {
+    return dtype == GDN_BF16 && a.D <= 128 && (long)a.B * a.HKV >= 2 * 152 ? kNarrowRows / 2 : kNarrowRows;
+}
 
 // A kernel over the sequences of its rows (C: its sizes), then the join of what several CTAs shared.
 template <int DP, typename T, typename C>
@@ -1037,7 +1043,7 @@ cudaError_t launch_narrow(Kv4Params p, void *ws, cudaStream_t s) {
         return cudaFuncSetAttribute(kv4_narrow_kernel<DP, NT, T, FULL>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     });
     if (e != cudaSuccess) return e;
-    p.min_rows = 0, p.max_rows = kNarrowRows;
+    p.min_rows = 0, p.max_rows = narrow_rows(p.a, sizeof(T) == 2 ? GDN_BF16 : GDN_F32);
     return launch_kernels<DP, T, C>(kv4_narrow_kernel<DP, NT, T, FULL>, C::PER_SM, p, ws, s);
 }
 
@@ -1046,23 +1052,24 @@ cudaError_t launch_rows(const Kv4Params &p, void *ws, cudaStream_t s) {
     const long rows = (long)p.a.max_q * p.G;
     const bool full = p.a.D == DP;
     cudaError_t e = cudaSuccess;
-    if (p.G <= kNarrowRows) {
+    const int most = narrow_rows(p.a, sizeof(T) == 2 ? GDN_BF16 : GDN_F32);
+    if (p.G <= most) {
         // (a batch of single tokens beside longer slices: blocks of 8 if those hold them; wide fp32 heads: 16 rows would not
         // fit the registers)
-        const bool one = rows <= 8 || (rows > kNarrowRows && p.G <= 8) || (DP > 128 && sizeof(T) == 4);
+        const bool one = rows <= 8 || (rows > most && p.G <= 8) || (DP > 128 && sizeof(T) == 4);
         if (one) {
             e = full ? launch_narrow<DP, 1, T, true>(p, ws, s) : launch_narrow<DP, 1, T, false>(p, ws, s);
         } else if constexpr (DP <= 128 || sizeof(T) == 2) {
             e = full ? launch_narrow<DP, 2, T, true>(p, ws, s) : launch_narrow<DP, 2, T, false>(p, ws, s);
         }
     }
-    if (e != cudaSuccess || rows <= kNarrowRows) return e;
+    if (e != cudaSuccess || rows <= most) return e;
     if constexpr (sizeof(T) == 4) {
-        return launch_wide<DP, T>(p, kNarrowRows, ws, s);
+        return launch_wide<DP, T>(p, most, ws, s);
     } else {
         Attn a = p.a;
         a.part = static_cast<float *>(ws);
-        return launch_attention_prompt_kv4(a, p.ks, p.vs, kNarrowRows, s);
+        return launch_attention_prompt_kv4(a, p.ks, p.vs, most, s);
     }
 }
 
@@ -1080,7 +1087,9 @@ cudaError_t launch(const Kv4Params &p, void *ws, cudaStream_t s) {
 size_t attention_kv4_workspace(int B, int N, int H, int HKV, int D, int max_q) {
     const long blocks = std::max(row_blocks(H, HKV, max_q, 64), row_blocks(H, HKV, std::min(max_q, kNarrowRows), 8));
     const size_t parts = span_bytes(B, HKV, blocks) + 2 * (size_t)kMaxCtas * 64 * (3 + padded(D)) * 4;
-    const bool slices = (long)max_q * (H / HKV) > kNarrowRows;
+    Attn a{};
+    a.B = B, a.HKV = HKV, a.D = D;
+    const bool slices = (long)max_q * (H / HKV) > narrow_rows(a, GDN_BF16);
     return std::max(parts, slices ? attention_prompt_part_floats(B, N, H, HKV, D, max_q) * 4 : 0);
 }
 
