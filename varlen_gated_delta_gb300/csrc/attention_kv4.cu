@@ -901,36 +901,39 @@ __global__ void __launch_bounds__(128, Narrow<DP, NT, T>::PER_SM) kv4_narrow_ker
 
 // ---------------------------------------------------------------- parts
 
-// Joins the parts of each triple that several CTAs shared: a block to a (triple, row), or to several of a triple's rows.  A
-// warp goes by every kJoinWarps-th part with a running maximum of its own, so that nothing but the span is waited for
-// before the parts are loaded.
-template <int DP, typename T, int kJoinWarps>
-__global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const Kv4Params p, int rows) {
+// Joins the parts of each triple that several CTAs shared.  With many triples, of few parts each, a warp to a row; with few, of
+// many, eight warps, which go by every eighth part and meet in shared memory.  A running maximum lets the parts be loaded
+// before any other is known.  (What the first kernel did not write is read before its end.)
+template <int DP, typename T, int WARPS>
+__global__ void __launch_bounds__(WARPS == 1 ? 128 : WARPS * 32) kv4_join_kernel(const Kv4Params p, int rows) {
     constexpr int E = DP / 32, N = 4;  // channels of a lane, parts loaded at a time
-    __shared__ float s_m[kJoinWarps], s_l[kJoinWarps], s_o[kJoinWarps][DP];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int AT_ONCE = WARPS == 1 ? 4 : 1;  // rows of a block
+    __shared__ float s_m[WARPS], s_l[WARPS], s_o[WARPS == 1 ? 1 : WARPS][DP];
+    const int tid = threadIdx.x, lane = tid & 31, warp = WARPS == 1 ? 0 : tid >> 5;
     const int h = blockIdx.x % p.a.HKV, block = blockIdx.x / p.a.HKV % p.blocks, b = blockIdx.x / p.a.HKV / p.blocks;
-    pdl_wait_primary();
     int start, len, kv;
     if (block >= seq_blocks(p, rows, b, start, len, kv)) return;
+    const float vs = head_scale(p.vs, h);
+    pdl_wait_primary();
     const int2 span = p.spans[blockIdx.x];
     if (span.x == span.y) return;
     const int PART = rows * (3 + DP);
     auto part = [&](int c) { return p.part + (2L * c + (c == span.x)) * PART; };
-    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    for (int r0 = blockIdx.y * AT_ONCE; r0 < rows; r0 += gridDim.y * AT_ONCE) {
+        const int r = WARPS == 1 ? r0 + (tid >> 5) : r0;
         const long row = (long)block * rows + r;
-        if (row >= (long)len * p.G) return;
+        if (r >= rows || row >= (long)len * p.G) return;
         const float c_row = part(span.x)[2 * rows + r];
         float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
         for (int i = 0; i < E; ++i) o[i] = 0.f;
-        for (int c0 = span.x + warp; c0 <= span.y; c0 += N * kJoinWarps) {
+        for (int c0 = span.x + warp; c0 <= span.y; c0 += N * WARPS) {
             float pm[N], pl[N];
             float2 po[N][E / 2];
 #pragma unroll
             for (int k = 0; k < N; ++k) {
-                const bool real = c0 + k * kJoinWarps <= span.y;
-                const float *x = part(real ? c0 + k * kJoinWarps : c0);
+                const bool real = c0 + k * WARPS <= span.y;
+                const float *x = part(real ? c0 + k * WARPS : c0);
                 pm[k] = real ? x[r] : -INFINITY, pl[k] = x[rows + r];
                 x += 3 * rows + r * DP + lane * E;
 #pragma unroll
@@ -946,7 +949,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const Kv4Para
 #pragma unroll
             for (int k = 0; k < N; ++k) {
                 // (a part that saw no key has l = o = 0; NaN, of a row whose query is not finite, has m = -inf too)
-                const bool real = c0 + k * kJoinWarps <= span.y;
+                const bool real = c0 + k * WARPS <= span.y;
                 const float w = pm[k] == -INFINITY ? (real && pl[k] != 0.f ? 1.f : 0.f) : exp2_fast((pm[k] - M) * c_row);
                 l = fmaf(w, pl[k], l);
 #pragma unroll
@@ -955,28 +958,35 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const Kv4Para
             }
             m = M;
         }
-        if (lane == 0) s_m[warp] = m;
-        __syncthreads();
-        float M = s_m[0];
-#pragma unroll
-        for (int w = 1; w < kJoinWarps; ++w) M = fmaxf(M, s_m[w]);
-        const float f = m == -INFINITY ? (l != 0.f ? 1.f : 0.f) : exp2_fast((m - M) * c_row);
-#pragma unroll
-        for (int i = 0; i < E; ++i) s_o[warp][lane * E + i] = o[i] * f;
-        if (lane == 0) s_l[warp] = l * f;
-        __syncthreads();
-        float L = 0.f;
-#pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) L += s_l[w];
-        const float inv = L > 0.f ? head_scale(p.vs, h) / L : L;  // (0 gives 0, NaN stays)
         T *out = static_cast<T *>(p.a.out) + ((size_t)(start + row / p.G) * p.a.H + h * p.G + row % p.G) * p.a.D;
-        for (int d = tid; d < p.a.D; d += kJoinWarps * 32) {
-            float x = 0.f;
+        if constexpr (WARPS == 1) {
+            const float inv = l > 0.f ? vs / l : l;  // (0 gives 0, NaN stays)
+            if (lane * E < p.a.D)
 #pragma unroll
-            for (int w = 0; w < kJoinWarps; ++w) x += s_o[w][d];
-            out[d] = from_f32<T>(x * inv);
+                for (int i = 0; i < E; i += 2) store2(out + lane * E + i, o[i] * inv, o[i + 1] * inv);
+        } else {
+            if (lane == 0) s_m[warp] = m;
+            __syncthreads();
+            float M = s_m[0];
+#pragma unroll
+            for (int w = 1; w < WARPS; ++w) M = fmaxf(M, s_m[w]);
+            const float f = m == -INFINITY ? (l != 0.f ? 1.f : 0.f) : exp2_fast((m - M) * c_row);
+#pragma unroll
+            for (int i = 0; i < E; ++i) s_o[warp][lane * E + i] = o[i] * f;
+            if (lane == 0) s_l[warp] = l * f;
+            __syncthreads();
+            float L = 0.f;
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) L += s_l[w];
+            const float inv = L > 0.f ? vs / L : L;  // (0 gives 0, NaN stays)
+            for (int d = tid; d < p.a.D; d += WARPS * 32) {
+                float x = 0.f;
+#pragma unroll
+                for (int w = 0; w < WARPS; ++w) x += s_o[w][d];
+                out[d] = from_f32<T>(x * inv);
+            }
+            __syncthreads();  // the sums have been read
         }
-        __syncthreads();  // the sums have been read
     }
 }
 
@@ -1013,12 +1023,12 @@ cudaError_t launch_kernels(void (*kernel)(Kv4Params), int per_sm, Kv4Params p, v
     cudaError_t e = launch_kernel(kernel, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, s, true, p);
     note_launch();
     if (e != cudaSuccess) return e;
-    // Few triples have many parts each, many have few: then fewer warps, and with many blocks several rows to each (most
+    // Few triples have many parts each, many have few: then a warp to a row, and with many blocks several rows to each (most
     // of them have nothing to join, and leaving takes its time too).
-    const long rows = std::min((long)p.a.max_q * p.G, (long)C::ROWS);
-    const dim3 blocks((unsigned)triples, (unsigned)std::min(rows, std::max(1L, 4096 / triples)));
-    e = triples * 2 <= sms ? launch_kernel(kv4_join_kernel<DP, T, 8>, blocks, dim3(256), 0, s, true, p, C::ROWS)
-                           : launch_kernel(kv4_join_kernel<DP, T, 4>, blocks, dim3(128), 0, s, true, p, C::ROWS);
+    const long rows = std::min((long)p.a.max_q * p.G, (long)C::ROWS), few = triples * 2 <= sms;
+    const dim3 blocks((unsigned)triples, (unsigned)std::min(few ? rows : (rows + 3) / 4, std::max(1L, 4096 / triples)));
+    e = few ? launch_kernel(kv4_join_kernel<DP, T, 8>, blocks, dim3(256), 0, s, true, p, C::ROWS)
+            : launch_kernel(kv4_join_kernel<DP, T, 1>, blocks, dim3(128), 0, s, true, p, C::ROWS);
     note_launch();
     return e;
 }
