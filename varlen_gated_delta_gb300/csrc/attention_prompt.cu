@@ -396,31 +396,45 @@ __device__ __forceinline__ void convert_queries(const PromptParams &p, const Ite
     }
 }
 
-// A raw tile of keys (or values) to fp16, 16 channels at a time.  Bit i of `there`: tokens 16 i .. 16 i + 15 were copied; the
-// others (past the last key, or of a page outside the cache) read as zeros.
+// A thread's part of a raw tile of keys (or values), 16 channels at a time.
 template <int DP>
-__device__ __forceinline__ void convert_tile(int D, const unsigned char *raw, uint32_t there, unsigned char *slot, int tid) {
-    constexpr int BN = Cfg<DP, true>::BN, GROUPS = DP / 16;
-    const int grp = tid % GROUPS, GR = D / 16;
-#pragma unroll 4
-    for (int i = 0; i < BN * GROUPS / 128; ++i) {
-        const int key = tid / GROUPS + i * (128 / GROUPS);
-        uint2 codes = make_uint2(0, 0);
-        uint32_t s = 0;
-        if ((there >> (key >> 4) & 1) && grp < GR) {
-            codes = *reinterpret_cast<const uint2 *>(raw + (key * GR + grp) * 8);
-            s = raw[BN * GR * 8 + key * GR + grp];
-        }
-        s = kv4_scales(s | s << 8);
-        unsigned char *row = slot + (grp >> 2) * BN * 128 + key * 128;
-        uint32_t d[2][4];
-        kv4_codes(codes.x, d[0]), kv4_codes(codes.y, d[1]);
+struct RawTile {
+    static constexpr int BN = Cfg<DP, true>::BN, GROUPS = DP / 16, N = BN * GROUPS / 128;
+    uint2 codes[N];
+    uint32_t scale[N];
+    // Bit i of `there`: tokens 16 i .. 16 i + 15 were copied; the others (past the last key, or of a page outside the cache)
+    // read as zeros.
+    __device__ __forceinline__ void load(int D, const unsigned char *raw, uint32_t there, int tid) {
+        const int grp = tid % GROUPS, GR = D / 16;
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
-            *reinterpret_cast<uint4 *>(row + ((((grp & 3) * 2 + half) ^ (key & 7)) << 4)) =
-                make_uint4(mul_f16x2(d[half][0], s), mul_f16x2(d[half][1], s), mul_f16x2(d[half][2], s), mul_f16x2(d[half][3], s));
+        for (int i = 0; i < N; ++i) {
+            const int key = tid / GROUPS + i * (128 / GROUPS);
+            codes[i] = make_uint2(0, 0), scale[i] = 0;
+            if ((there >> (key >> 4) & 1) && grp < GR) {
+                codes[i] = *reinterpret_cast<const uint2 *>(raw + (key * GR + grp) * 8);
+                scale[i] = raw[BN * GR * 8 + key * GR + grp];
+            }
+        }
     }
-}
+    // To fp16.  Groups of the upper 64 channels of 128 begin with their second half: 16 bytes of eight lanes then lie in different
+    // banks.
+    __device__ __forceinline__ void store(unsigned char *slot, int tid) const {
+        const int grp = tid % GROUPS, turn = grp >> 2 & 1;
+        unsigned char *block = slot + (grp >> 2) * BN * 128;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int key = tid / GROUPS + i * (128 / GROUPS);
+            const uint32_t s = kv4_scales(scale[i] | scale[i] << 8);
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                uint32_t d[4];
+                kv4_codes(z == turn ? codes[i].x : codes[i].y, d);
+                *reinterpret_cast<uint4 *>(block + key * 128 + ((((grp & 3) * 2 + (z ^ turn)) ^ (key & 7)) << 4)) =
+                    make_uint4(mul_f16x2(d[0], s), mul_f16x2(d[1], s), mul_f16x2(d[2], s), mul_f16x2(d[3], s));
+            }
+        }
+    }
+};
 
 template <int DP, bool KV4>
 __global__ void __launch_bounds__(Cfg<DP, KV4>::THREADS, 1)
@@ -541,14 +555,15 @@ __global__ void __launch_bounds__(Cfg<DP, KV4>::THREADS, 1)
 #pragma unroll 1
                     for (int i = 0; i < 2 * it.tiles; ++i, ++seq) {
                         const uint32_t slot = slot_of(seq), r = seq % C::RAWS;
-                        if (!wait_or_abort(raw_full + r, (seq / C::RAWS) & 1, abort) ||
-                            !wait_or_abort(empty + slot, phase_of(seq) ^ 1, abort))
-                            goto done;
-                        convert_tile<DP>(p.a.D, raws + r * C::RAW, s_there[r], ring + slot * C::SLOT, ctid);
-                        fence_async_smem();
-                        mbar_arrive(full + slot);
+                        if (!wait_or_abort(raw_full + r, (seq / C::RAWS) & 1, abort)) goto done;
+                        RawTile<DP> raw;
+                        raw.load(p.a.D, raws + r * C::RAW, s_there[r], ctid);
                         __syncwarp();
                         if (lane == 0) mbar_arrive(raw_empty + r);
+                        if (!wait_or_abort(empty + slot, phase_of(seq) ^ 1, abort)) goto done;
+                        raw.store(ring + slot * C::SLOT, ctid);
+                        fence_async_smem();
+                        mbar_arrive(full + slot);
                     }
                 }
             }
