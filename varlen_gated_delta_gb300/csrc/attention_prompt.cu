@@ -405,10 +405,16 @@ struct RawTile {
     // Bit i of `there`: tokens 16 i .. 16 i + 15 were copied; the others (past the last key, or of a page outside the cache)
     // read as zeros.
     __device__ __forceinline__ void load(int D, const unsigned char *raw, uint32_t there, int tid) {
-        const int grp = tid % GROUPS, GR = D / 16;
+        const int grp = tid % GROUPS, GR = D / 16, key0 = tid / GROUPS;
+        if (there == (1u << (BN / 16)) - 1 && GR == GROUPS) {  // (as nearly all are)
+            const unsigned char *at = raw + (key0 * GROUPS + grp) * 8, *s = raw + BN * GROUPS * 8 + key0 * GROUPS + grp;
+#pragma unroll
+            for (int i = 0; i < N; ++i) codes[i] = *reinterpret_cast<const uint2 *>(at + i * 1024), scale[i] = s[i * 128];
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int key = tid / GROUPS + i * (128 / GROUPS);
+            const int key = key0 + i * (128 / GROUPS);
             codes[i] = make_uint2(0, 0), scale[i] = 0;
             if ((there >> (key >> 4) & 1) && grp < GR) {
                 codes[i] = *reinterpret_cast<const uint2 *>(raw + (key * GR + grp) * 8);
@@ -419,17 +425,19 @@ struct RawTile {
     // To fp16.  Groups of the upper 64 channels of 128 begin with their second half: 16 bytes of eight lanes then lie in different
     // banks.
     __device__ __forceinline__ void store(unsigned char *slot, int tid) const {
-        const int grp = tid % GROUPS, turn = grp >> 2 & 1;
-        unsigned char *block = slot + (grp >> 2) * BN * 128;
+        const int grp = tid % GROUPS, turn = grp >> 2 & 1, key0 = tid / GROUPS;
+        unsigned char *row = slot + (grp >> 2) * BN * 128 + key0 * 128;
+        // (rows a multiple of eight apart swizzle alike)
+        static_assert(128 / GROUPS % 8 == 0, "keys of a thread");
+        unsigned char *at[2] = {row + ((((grp & 3) * 2 + turn) ^ (key0 & 7)) << 4), row + ((((grp & 3) * 2 + 1 - turn) ^ (key0 & 7)) << 4)};
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int key = tid / GROUPS + i * (128 / GROUPS);
             const uint32_t s = kv4_scales(scale[i] | scale[i] << 8);
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
                 uint32_t d[4];
                 kv4_codes(z == turn ? codes[i].x : codes[i].y, d);
-                *reinterpret_cast<uint4 *>(block + key * 128 + ((((grp & 3) * 2 + (z ^ turn)) ^ (key & 7)) << 4)) =
+                *reinterpret_cast<uint4 *>(at[z] + i * (128 / GROUPS) * 128) =
                     make_uint4(mul_f16x2(d[0], s), mul_f16x2(d[1], s), mul_f16x2(d[2], s), mul_f16x2(d[3], s));
             }
         }
