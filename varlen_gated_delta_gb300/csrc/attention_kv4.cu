@@ -9,7 +9,7 @@
 //
 // Keys are read once for the rows that share them, 9/16 bytes a channel of k and v: bound by HBM for few rows, by the
 // tensor cores for many.  Three kernels, by a sequence's rows (tokens times the heads of a group):
-// - up to 64 (with many sequences 32): blocks of 8 or 16 rows, values converted in the registers that a product reads (below);
+// - up to 16 to 64 (see narrow_rows): blocks of 8 or 16 rows, values converted in the registers that a product reads (below);
 // - more, bf16: the tcgen05 kernel of attention_prompt.cu, with a warpgroup that converts;
 // - more, fp32: tiles of 64 rows by 64 keys, converted to fp16 in shared memory, 16-row mma.sync, products of both parts.
 // The first and the last cut the work by key tiles: the tiles of all (sequence, row block, key-value head) triples form one
@@ -997,14 +997,17 @@ int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 size_t span_bytes(int B, int HKV, long blocks) { return ((size_t)B * blocks * HKV * 8 + 255) & ~size_t(255); }
 long row_blocks(int H, int HKV, int max_q, int rows) { return ((long)max_q * (H / HKV) + rows - 1) / rows; }
 
-// Sequences of up to so many rows run in blocks of 8 or 16, which convert the cache anew.  With a pair of (sequence,
-// head) to every half SM the tcgen05 kernel takes three or four blocks' rows at once without splitting keys (64 requests,
-// 16 tokens each over U[1, 4096], 32 heads of 128 on 8: 230 us in four blocks, 156 there; in two blocks 126 and 152);
-// with fewer pairs the blocks' even runs win (8 requests over U[1, 8192]: 57 and 72; 2 over U[1, 65536]: 90 and 93), and for
-// heads of 256 (16 requests of 40 rows: 38 and 53).
+// Sequences of up to so many rows run in blocks of 8 or 16, which convert the cache anew; the tcgen05 kernel takes more
+// rows at once, but needs items for its SMs.  With a pair of (sequence, head) to every half SM it has them (64 requests over
+// U[1, 4096], 8 key-value heads: 32 rows of heads of 128 take 120 us in blocks and 118 there, 40 174 and 120; 20 rows of heads of 256
+// 222 and 189).  With fewer pairs the blocks' even runs win up to three blocks (2 requests over U[1, 65536]: 48 rows of
+// heads of 128 71 us and 74, 64 rows 89 and 75; of heads of 64 65 and 62; 8 requests over U[1, 8192]: 42 and 50, 52 and 57,
+// 38 and 48).
 constexpr int kNarrowRows = kSplitRows;
 int narrow_rows(const Attn &a, int dtype) {
-    return dtype == GDN_BF16 && a.D <= 128 && (long)a.B * a.HKV >= 2 * 152 ? kNarrowRows / 2 : kNarrowRows;
+    if (dtype != GDN_BF16) return kNarrowRows;
+    if ((long)a.B * a.HKV >= 2 * 152) return a.D > 128 ? 16 : 32;
+    return a.D > 64 ? 48 : kNarrowRows;
 }
 
 // A kernel over the sequences of its rows (C: its sizes), then the join of what several CTAs shared.
