@@ -101,6 +101,17 @@ def test_fork_takes_and_refuses():
                                           cursor=c), **bad))
 
 
+@pytest.mark.parametrize("cursor", [4, 5, 1 << 30])
+def test_fork_refuses_a_cursor_past_the_list(cursor):
+    # (pages that go back would be put past its end: words behind the list keep their values)
+    room = _i32([5, 6, 4, 77, 77, 77])
+    free = room[:3]
+    to, ko, copies, co, status = gdn.gdn_page_fork(_i32([-1]), _i32([24]), _i32([[5, 6, 0]]), free, page_size=16, num_pages=8,
+                                                   cursor=_i32([cursor]))
+    assert status.item() == 2 and co.item() == cursor and room.tolist() == [5, 6, 4, 77, 77, 77]
+    assert to.tolist() == [[-1, -1, -1]] and ko.tolist() == [0] and copies.tolist() == [[-1, -1]]
+
+
 @pytest.mark.parametrize("B,M,ps,pool", [(1, 1, 1, 1), (1, 2, 16, 2), (4, 5, 16, 40), (64, 20, 64, 900), (300, 33, 16, 7777), (2, 1, 16, 100000),
                                          (9000 - 900, 1, 4, 9000), (16, 2000, 1, 33000)])
 def test_compact(B, M, ps, pool):

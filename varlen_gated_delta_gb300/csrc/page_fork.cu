@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kThreads) page_fork_kernel(const PageFork p, F
         *reinterpret_cast<uint4 *>(w.was + i) = *reinterpret_cast<uint4 *>(w.is + i) = make_uint4(0, 0, 0, 0);
     if (tid == 0) s_bad = 0;
     const int cursor = __ldg(p.cursor);
-    bool bad = cursor < 0;
+    bool bad = cursor < 0 || cursor > p.n_free;
     for (int b = tid; b < p.B; b += kThreads) {
         const int len = p.kv_lens[b];
         const bool fits = len >= 0 && len <= (long)M * ps;
