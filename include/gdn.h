@@ -670,7 +670,7 @@ GDN_API size_t gdn_attention_paged_workspace_bytes(int B, int N, int H, int HKV,
  * [page_size, D/2], the even channel in the low half of a byte, then the
  * scales, [page_size, D/16].  A scale byte of 0x7f counts as 480 and 0xff too,
  * so no byte is a NaN.  D is a multiple of 16 up to 256, page_size a multiple
- * of 16 (GDN_ERR_UNSUPPORTED otherwise).
+ * of 16 (GDN_ERR_UNSUPPORTED otherwise) up to 2^20.
  */
 
 /*

@@ -110,6 +110,13 @@ def test_page_copy_refusals(lib, kw, status):
     assert lib.gdn_page_copy(ptrs, sizes, a["count"], a["copies"], a["n"], a["pages"], None) == status
 
 
+@pytest.mark.parametrize("D", [16, 256])
+def test_kv4_pages_past_32_bit_places_are_refused(lib, D):
+    for ps, status in ((1 << 20, 0), ((1 << 20) + 16, 3), (1 << 24, 3)):
+        assert _call(lib.gdn_kv4_write, WRITE, dict(ps=ps, pages=1, D=D, ks=512, vs=512, N=0)) == status
+        assert _call(lib.gdn_attention_paged_kv4, ATTN, dict(ps=ps, pages=1, M=1, D=D, qs=1024, N=0)) == status
+
+
 def test_workspace_queries(lib):
     attn, beam = gdn.gdn_attention_paged_kv4_workspace_bytes, gdn.gdn_beam_select_workspace_bytes
     assert attn(64, 64, 32, 8, 128, 1) > 0

@@ -54,6 +54,8 @@ int check_kv4(int N, int HKV, int D, int page_size, int num_pages, const char *w
         return set_error(GDN_ERR_SHAPE, "%s: page_size=%d and num_pages=%d must be positive", what, page_size, num_pages);
     if (page_size % 16 != 0)
         return set_error(GDN_ERR_UNSUPPORTED, "%s: page_size=%d is not a multiple of 16", what, page_size);
+    // (places within a page's block of a head fit 32 bits)
+    if (page_size > 1 << 20) return set_error(GDN_ERR_OVERFLOW, "%s: page_size=%d exceeds 2^20", what, page_size);
     if (N > INT_MAX - 1024 || HKV > 32767 || (long)page_size * num_pages > INT_MAX - 1024 ||
         (long)N * HKV > (1L << 40) / (D * 2))
         return set_error(GDN_ERR_OVERFLOW, "%s: N, HKV or page_size * num_pages out of range", what);
