@@ -912,7 +912,11 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : WARPS * 32) kv4_join_kernel
     const int tid = threadIdx.x, lane = tid & 31, warp = WARPS == 1 ? 0 : tid >> 5;
     const int h = blockIdx.x % p.a.HKV, block = blockIdx.x / p.a.HKV % p.blocks, b = blockIdx.x / p.a.HKV / p.blocks;
     int start, len, kv;
-    if (block >= seq_blocks(p, rows, b, start, len, kv)) return;
+    if (block >= seq_blocks(p, rows, b, start, len, kv)) {
+        // (a grid none of whose blocks waits could end before the first kernel, and let the next call begin beside that)
+        if (blockIdx.x == 0 && blockIdx.y == 0) pdl_wait_primary();
+        return;
+    }
     const float vs = head_scale(p.vs, h);
     pdl_wait_primary();
     const int2 span = p.spans[blockIdx.x];
