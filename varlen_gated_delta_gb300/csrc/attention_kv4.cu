@@ -16,12 +16,12 @@
 // list, of which every CTA takes an equal run; a CTA whose run begins or ends inside a triple leaves m, l and an
 // unscaled o for a second kernel that joins the parts.  Which parts exist follows from the lengths alone.
 //
-// 64 requests with histories of U[1, 8192] tokens, one token each, 32 heads of 128 on 8: 71 us, 3.8 TB/s.  Longer ones add 55 us
+// 64 requests with histories of U[1, 8192] tokens, one token each, 32 heads of 128 on 8: 68 us, 3.9 TB/s.  Longer ones add 55 us
 // for 302 MB (5.5 TB/s, 0.81 of the measured copy), on top of some 15 us for launches, first dependent loads, the first tile
-// and the join (one request: 16384 tokens 17 us, 131072 43, 524288 125).  What bounds the rest is issue and latency: 336
+// and the join (one request: 16384 tokens 16 us, 131072 41, 524288 123).  What bounds the rest is issue and latency: 336
 // instructions a warp for 16 keys of 128 channels, of which 128 convert and interleave, 64 scale and 16 multiply; 12 warps an SM
-// issue 2.1 a clock.  32 and 48 keys a warp at a time with 16 warps an SM gave 45 and 46 us for the request of 131072 tokens,
-// scoring two or four blocks of keys in turn 43 and 44.
+// issue 2.2 a clock.  Before the join took its present form (43 us for the request of 131072 tokens), 32 and 48 keys a warp at a
+// time with 16 warps an SM gave 45 and 46 us, scoring two or four blocks of keys in turn 43 and 44.
 #include <algorithm>
 #include <cmath>
 
@@ -111,7 +111,8 @@ __device__ __forceinline__ int seq_blocks(const Kv4Params &p, int rows, int b, i
     return (int)(((long)len * p.G + rows - 1) / rows);
 }
 // What beginning and ending a triple costs stands in the list as places before its first tile: without them a CTA with a
-// run of short histories would take far longer than the others (64 x U[1, 8192] keys: 80 us without, 71 with one place, 72 with two).
+// run of short histories would take far longer than the others (64 x U[1, 8192] keys: 80 us without, 71 with one place, 72 with two;
+// the join has since taken 3 us from each).
 struct List {
     int rows, keys, ahead;  // rows of a block, keys of a tile, places before a triple's first tile
 };
@@ -453,7 +454,7 @@ __global__ void __launch_bounds__(128) kv4_wide_kernel(const Kv4Params p) {
 
 // ---------------------------------------------------------------- rows by the block of 8 or 16
 
-// 16 x 5 drafts over 4096 keys, 16 heads of 256 on 2 (40 rows in three blocks): 38 us, against 80 for a tile of 64 rows.
+// 16 x 5 drafts over 4096 keys, 16 heads of 256 on 2 (40 rows in three blocks): 37 us, against 80 for a tile of 64 rows.
 //
 // Rows are the columns of the products, keys and channels their rows: S^T = K Q^T and O^T = V^T P^T with 16 keys or 16
 // channels to a tile, so that a cached value is converted into the registers of one product and no row

@@ -49,9 +49,11 @@
 //
 // Over a 4-bit cache (KV4) the load warp copies codes and scales to a ring of two tiles, and a fourth warpgroup turns them, and
 // the queries, into fp16 tiles where the other instance's loads put bf16 ones.  4 x 512 tokens over 8192, 32 heads of
-// 128 on 8: 286 us, 930 TFLOP/s; 256 items on 152 SMs leave a sixth of the time to the second round.  Loading codes into
-// registers a tile ahead instead took 1393 us (page lookups and divisions in the converting warps); 176, 192 and 200 registers
-// to a softmax thread instead of 184 took 291, 300 and 328.
+// 128 on 8: 224 us, 1190 TFLOP/s (tensor pipe 60% active); 256 items on 152 SMs leave a sixth of the time to the second round.  Steps:
+// codes go to registers before the first is converted, which frees their place in the ring for the next copy, and a lane's
+// places lie in different banks (286 -> 253 us); whole tiles take loads and stores at fixed offsets (253 -> 224).  Loading codes
+// into registers a tile ahead from global memory took 1393 (page lookups and divisions in the converting warps).  176 and 192 registers
+// to a softmax thread instead of 184: 239 us against 224, and 275 against 253 a step earlier.
 #include <algorithm>
 #include <cmath>
 #include <exception>
