@@ -32,7 +32,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kMaxCtas = 4 * 160;
+constexpr int kMaxSms = 160;
 constexpr float kShift = 14.f;  // log2 of the probabilities' factor
 
 struct Kv4Params {
@@ -216,6 +216,7 @@ struct Wide {
     static constexpr int QBYTES = ROWS * DP * 2;
     static constexpr int SMEM = STAGES * 2 * RAW + 2 * TILE + Q * QBYTES;
     static constexpr int PART = ROWS * (3 + DP);  // floats of a part: m, l, the rows' factors, o
+    static constexpr int PER_SM = 220 * 1024 / (SMEM + 1024);
 };
 
 template <int DP, typename T>
@@ -1000,6 +1001,8 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : WARPS * 32) kv4_join_kernel
 int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 // (the most that any of the kernels asks for: blocks of 8 rows)
 size_t span_bytes(int B, int HKV, long blocks) { return ((size_t)B * blocks * HKV * 8 + 255) & ~size_t(255); }
+// Rows of the parts of one SM's CTAs, at most.
+constexpr int part_rows(int DP) { return 64 * 256 / DP; }
 long row_blocks(int H, int HKV, int max_q, int rows) { return ((long)max_q * (H / HKV) + rows - 1) / rows; }
 
 // Sequences of up to so many rows run in blocks of 8 or 16, which convert the cache anew; the tcgen05 kernel takes more
@@ -1017,7 +1020,8 @@ int narrow_rows(const Attn &a, int dtype) {
 
 // A kernel over the sequences of its rows (C: its sizes), then the join of what several CTAs shared.
 template <int DP, typename T, typename C>
-cudaError_t launch_kernels(void (*kernel)(Kv4Params), int per_sm, Kv4Params p, void *ws, cudaStream_t s) {
+cudaError_t launch_kernels(void (*kernel)(Kv4Params), Kv4Params p, void *ws, cudaStream_t s) {
+    static_assert(C::PER_SM * C::ROWS <= part_rows(DP), "parts of an SM's CTAs");
     p.blocks = (int)((std::min((long)p.a.max_q * p.G, (long)p.max_rows) + C::ROWS - 1) / C::ROWS);
     p.spans = static_cast<int2 *>(ws);
     p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + span_bytes(p.a.B, p.a.HKV, p.blocks));
@@ -1027,7 +1031,7 @@ cudaError_t launch_kernels(void (*kernel)(Kv4Params), int per_sm, Kv4Params p, v
     const long triples = (long)p.a.B * p.blocks * p.a.HKV;
     if (triples > INT32_MAX) return cudaErrorInvalidConfiguration;
     const long most = triples * (((long)p.a.max_pages * p.a.page_size + C::KEYS - 1) / C::KEYS);
-    const long grid = std::min(std::min((long)per_sm * sms, (long)kMaxCtas), most);
+    const long grid = std::min((long)C::PER_SM * std::min(sms, kMaxSms), most);
     cudaError_t e = launch_kernel(kernel, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, s, true, p);
     note_launch();
     if (e != cudaSuccess) return e;
@@ -1050,7 +1054,7 @@ cudaError_t launch_wide(Kv4Params p, int min_rows, void *ws, cudaStream_t s) {
     });
     if (e != cudaSuccess) return e;
     p.min_rows = min_rows, p.max_rows = INT32_MAX;
-    return launch_kernels<DP, T, C>(kv4_wide_kernel<DP, T>, std::max(1, 220 * 1024 / (C::SMEM + 1024)), p, ws, s);
+    return launch_kernels<DP, T, C>(kv4_wide_kernel<DP, T>, p, ws, s);
 }
 
 template <int DP, int NT, typename T, bool FULL>
@@ -1062,7 +1066,7 @@ cudaError_t launch_narrow(Kv4Params p, void *ws, cudaStream_t s) {
     });
     if (e != cudaSuccess) return e;
     p.min_rows = 0, p.max_rows = narrow_rows(p.a, sizeof(T) == 2 ? GDN_BF16 : GDN_F32);
-    return launch_kernels<DP, T, C>(kv4_narrow_kernel<DP, NT, T, FULL>, C::PER_SM, p, ws, s);
+    return launch_kernels<DP, T, C>(kv4_narrow_kernel<DP, NT, T, FULL>, p, ws, s);
 }
 
 template <int DP, typename T>
@@ -1104,7 +1108,7 @@ cudaError_t launch(const Kv4Params &p, void *ws, cudaStream_t s) {
 
 size_t attention_kv4_workspace(int B, int N, int H, int HKV, int D, int max_q) {
     const long blocks = std::max(row_blocks(H, HKV, max_q, 64), row_blocks(H, HKV, std::min(max_q, kNarrowRows), 8));
-    const size_t parts = span_bytes(B, HKV, blocks) + 2 * (size_t)kMaxCtas * 64 * (3 + padded(D)) * 4;
+    const size_t parts = span_bytes(B, HKV, blocks) + 2 * (size_t)kMaxSms * part_rows(padded(D)) * (3 + padded(D)) * 4;
     Attn a{};
     a.B = B, a.HKV = HKV, a.D = D;
     const bool slices = (long)max_q * (H / HKV) > narrow_rows(a, GDN_BF16);
