@@ -329,3 +329,24 @@ def test_reruns_and_graphs_give_the_same_bits(n):
     graph.replay()
     assert torch.equal(out, gdn.gdn_attention_paged_kv4(*a, max_q=n))
     assert n > 1 or bool((out[2] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n", [1, 2, 40])
+def test_nothing_past_the_workspace_and_the_rows(n, D, dtype):
+    """Every CTA has parts of two sequences to leave; the words behind the workspace and the output keep their values."""
+    H, HKV, ps, pages, B = 8, 1, 64, 2000, 7
+    gen = torch.Generator(device="cuda").manual_seed(D)
+    cache = torch.randint(0, 120, (pages, HKV, gdn.kv4_page_bytes(ps, D)), dtype=torch.uint8, generator=gen, device="cuda")
+    table = torch.randint(0, pages, (B, 500), dtype=I32, generator=gen, device="cuda")
+    kv = _i32([31000 - 1700 * b for b in range(B)])
+    q = torch.randn(B * n, H, D, generator=gen, device="cuda").to(dtype)
+    need = gdn.gdn_attention_paged_kv4_workspace_bytes(B, B * n, H, HKV, D, n)
+    room = torch.full((need + 65536,), 77, dtype=torch.uint8, device="cuda")
+    out = torch.full((B * n + 5, H, D), 3.0, dtype=dtype, device="cuda")
+    gdn.gdn_attention_paged_kv4(q, cache, cache, table, kv, _i32([n * b for b in range(B + 1)]), max_q=n, workspace=room[:need],
+                                out=out[:B * n])
+    assert bool((room[need:] == 77).all()) and bool((out[B * n:] == 3.0).all())
+    want = gdn.gdn_attention_paged_kv4(q, cache, cache, table, kv, _i32([n * b for b in range(B + 1)]), max_q=n)
+    assert torch.equal(out[:B * n], want) and bool(torch.isfinite(want).all())
