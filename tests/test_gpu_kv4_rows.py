@@ -1,0 +1,28 @@
+"""Rows of 4-bit attention where it can go wrong: without keys, infinite, of extreme sizes, of malformed sequences."""
+import pytest
+import torch
+
+import test_gpu_kv4 as kv4
+import varlen_gated_delta_gb300 as gdn
+
+pytestmark = pytest.mark.gpu
+BF16, F32, I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+@pytest.mark.parametrize("H,HKV,D", [(32, 8, 128), (8, 8, 64), (16, 4, 256)])
+def test_hundreds_of_slices_without_keys(H, HKV, D):
+    """Slices of sequences with no keys, or whose first rows see none, between ones that have some."""
+    gen = torch.Generator().manual_seed(D)
+    B = 400
+    new = [int(x) for x in torch.randint(70, 90, (B,), generator=gen)]
+    kv = [0 if b % 25 else new[b] + 60 for b in range(B)]
+    kv[3], kv[200] = 5, 30  # fewer keys than rows
+    p = kv4._problem(D, new, kv, H, HKV, D, 16, BF16)
+    for _ in range(3):
+        out = torch.full(p["q"].shape, 7.0, dtype=BF16, device="cuda")
+        kv4._run(p, out=out)
+        gdn.gdn_attention_status()
+        for b in range(B):
+            if kv[b] == 0:
+                assert bool((out[p["offsets"][b]:p["offsets"][b + 1]] == 0).all())
+    kv4._check(p, out)

@@ -530,12 +530,15 @@ __global__ void __launch_bounds__(Cfg<DP, KV4>::THREADS, 1)
     it.n[1] = 0;
     // Items come from the load warp through a ring of four; false past the last one.
     uint32_t n_item = 0;
-    auto next_item = [&]() {
+    auto release_item = [&](uint32_t k) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(item_empty + k);
+    };
+    auto next_item = [&](bool release = true) {
         const uint32_t k = n_item & 3;
         if (!wait_or_abort(item_full + k, (n_item >> 2) & 1, abort)) return false;
         it = s_item[k];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(item_empty + k);
+        if (release || it.b < 0) release_item(k);
         ++n_item;
         return it.b >= 0;
     };
@@ -799,7 +802,7 @@ __global__ void __launch_bounds__(Cfg<DP, KV4>::THREADS, 1)
         uint32_t s_phase = 0, turn_phase = 0;
         uint32_t o_phase = 0;  // a bit for each score buffer: products with its P so far, mod 2
         if (NQ == 2 && t == 1) mbar_arrive(turn + 0);  // query tile 0 goes first
-        while (next_item()) {
+        while (next_item(!KV4)) {
             const int shift = it.kv - it.len, first = it.row0 + (p.pair ? 0 : t * (128 >> p.packed)),
                       r = first + (row >> p.packed);
             const int n = NQ == 2 && t ? it.n[1] : it.n[0];
@@ -810,6 +813,9 @@ __global__ void __launch_bounds__(Cfg<DP, KV4>::THREADS, 1)
                 const uint32_t k = (n_item - 1) & 3;
                 if (!wait_or_abort(f_full + k, ((n_item - 1) >> 2) & 1, abort)) goto done;
                 pc = n > 0 ? factors[(k * 2 + t) * 128 + row] : 1.f;
+                // (not before: items without keys hold nobody up, and the factors of the fourth item after this one may be
+                // ready before a late warp has looked at these)
+                release_item(k);
             }
             for (int j = 0; j < it.tiles; ++j) {
                 if (j >= n) {  // only the other query tile sees these keys
