@@ -9,6 +9,27 @@ pytestmark = pytest.mark.gpu
 BF16, F32, I32 = torch.bfloat16, torch.float32, torch.int32
 
 
+@pytest.mark.parametrize("size", [1e-36, 1e-30, 1e-22, 1e25, 1e36])
+@pytest.mark.parametrize("n", [1, 20, 70])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_queries_and_scales_of_extreme_sizes(dtype, n, size):
+    """Small factors with large queries, and the other way round, give ordinary scores."""
+    p = kv4._problem(2, [n], [100], 4, 2, 64, 16, dtype)
+    p["q"] = (p["q"].float() * size).to(dtype)
+    scale = 0.3 / size
+    kv4._check(p, kv4._run(p, scale=scale), scale)
+
+
+@pytest.mark.parametrize("size", [1e-25, 1e25])
+@pytest.mark.parametrize("n", [1, 70])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_head_scales_of_extreme_sizes(dtype, n, size):
+    p = kv4._problem(3, [n], [100], 4, 2, 64, 16, dtype)
+    p["q"] = (p["q"].float() * size).to(dtype)
+    p["ts"][0] = torch.tensor([1.0 / size, 0.5 / size])
+    kv4._check(p, kv4._run(p, scale=0.2), 0.2)
+
+
 @pytest.mark.parametrize("H,HKV,D", [(32, 8, 128), (8, 8, 64), (16, 4, 256)])
 def test_hundreds_of_slices_without_keys(H, HKV, D):
     """Slices of sequences with no keys, or whose first rows see none, between ones that have some."""

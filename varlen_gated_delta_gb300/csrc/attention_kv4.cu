@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(128) kv4_wide_kernel(const Kv4Params p) {
             fresh = false;
             first_tile = cur.tile;
             // this warp's 16 rows of Q
-            const float c = fmaxf(p.c * head_scale(p.ks, cur.h), 1e-18f);
+            const float ks = head_scale(p.ks, cur.h);
             __syncwarp();
             for (int r = warp * 16; r < warp * 16 + 16; ++r) {
                 const bool real = r < rows;
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(128) kv4_wide_kernel(const Kv4Params p) {
                     if constexpr (F32)
                         *reinterpret_cast<__half *>(q_rows + C::QBYTES + at) = __float2half_rn(x[i] * power - __half2float(hi));
                 }
-                if (lane == 0) s_c[r] = c * back;
+                if (lane == 0) s_c[r] = kv4_row_factor(p.c, back, ks);
             }
             __syncwarp();
             cr[0] = s_c[warp * 16 + g], cr[1] = s_c[warp * 16 + g + 8];
@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(128, Narrow<DP, NT, T>::PER_SM) kv4_narrow_ker
     constexpr int MT = DP / 16;                // tiles of channels, and steps of 16 channels
     constexpr bool F32 = sizeof(T) == 4;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ float s_m[4][C::ROWS], s_l[4][C::ROWS], s_back[C::ROWS];
+    __shared__ float s_m[4][C::ROWS], s_l[4][C::ROWS], s_c[C::ROWS];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     unsigned char *ring = smem + warp * STAGES * 2 * RAW;
     const uint32_t ring_at = sm100::smem_u32(ring);
@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(128, Narrow<DP, NT, T>::PER_SM) kv4_narrow_ker
         if (fresh) {
             fresh = false;
             first_tile = cur.tile;
-            const float c = fmaxf(p.c * head_scale(p.ks, cur.h), 1e-18f);
+            const float ks = head_scale(p.ks, cur.h);
             const auto load_rows = [&](int nt, auto put) {  // rows nt 8 + g, DP / 4 channels of each a thread
                 const int r = nt * 8 + g;
                 const T *src = static_cast<const T *>(p.a.q);
@@ -667,16 +667,17 @@ __global__ void __launch_bounds__(128, Narrow<DP, NT, T>::PER_SM) kv4_narrow_ker
                 for (int nt = 0; nt < NT; ++nt) {
                     const float back = load_rows(nt, [&](int z, int ks, uint32_t a, uint32_t b) { q[z][nt][ks][0] = a, q[z][nt][ks][1] = b; });
                     // this thread's columns are rows 2 t4 and 2 t4 + 1
-                    cr[nt][0] = c * __shfl_sync(0xffffffffu, back, t4 * 8), cr[nt][1] = c * __shfl_sync(0xffffffffu, back, t4 * 8 + 4);
+                    const float factor = kv4_row_factor(p.c, back, ks);
+                    cr[nt][0] = __shfl_sync(0xffffffffu, factor, t4 * 8), cr[nt][1] = __shfl_sync(0xffffffffu, factor, t4 * 8 + 4);
                 }
             } else {
                 if (warp < NT) {
                     const float back = load_rows(warp, [&](int z, int ks, uint32_t a, uint32_t b) { s_q[((z * NT + warp) * MT + ks) * 32 + lane] = make_uint2(a, b); });
-                    if (t4 == 0) s_back[warp * 8 + g] = back;
+                    if (t4 == 0) s_c[warp * 8 + g] = kv4_row_factor(p.c, back, ks);
                 }
                 __syncthreads();
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) cr[nt][0] = c * s_back[nt * 8 + t4 * 2], cr[nt][1] = c * s_back[nt * 8 + t4 * 2 + 1];
+                for (int nt = 0; nt < NT; ++nt) cr[nt][0] = s_c[nt * 8 + t4 * 2], cr[nt][1] = s_c[nt * 8 + t4 * 2 + 1];
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {

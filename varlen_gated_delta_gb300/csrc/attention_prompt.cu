@@ -108,7 +108,7 @@ struct Cfg {
     static constexpr int REGS_IO = !KV4 ? 96 : NQ == 2 ? 72 : 128;
     static constexpr int REGS_SOFTMAX = !SPLIT_REGS ? REGS : !KV4 ? 200 : NQ == 2 ? 184 : 248;
     static_assert(NQ * REGS_SOFTMAX + IO * REGS_IO <= (NQ + IO) * REGS, "more registers than the CTA was launched with");
-    // KV4: codes and scales of a tile of keys (or values), and how many of those there are; softmax factors of the rows
+    // KV4: codes and scales of a tile of keys (or values), and how many of those there are; inverse powers of the rows
     // of four items; the barriers of both, and which tokens of a raw tile are there
     static constexpr int RAW = BN * DP / 16 * 9, RAWS = 2;
     static constexpr int EXTRA = KV4 ? RAWS * RAW + 4 * 2 * 128 * 4 + 4 * 8 + RAWS * (2 * 8 + 8) : 0;
@@ -353,12 +353,11 @@ __device__ __forceinline__ bool masked_non_finite(const PromptParams &p, int b, 
 // ---------------------------------------------------------------- the converting warpgroup (KV4)
 
 // Rows of a query tile to fp16, each by the power of two that puts its largest value into [1, 2) (and the sign of the scale);
-// the softmax factor of each row takes that back.  tid: of the warpgroup.
+// the softmax factor of each row takes that back (its inverse).  tid: of the warpgroup.
 template <int DP>
-__device__ __forceinline__ void convert_queries(const PromptParams &p, const Item &it, int t, unsigned char *tile, float *factors, int tid) {
+__device__ __forceinline__ void convert_queries(const PromptParams &p, const Item &it, int t, unsigned char *tile, float *inverses, int tid) {
     constexpr int LANES = DP / 8, STEP = 128 / LANES, BATCH = 4;  // lanes to a row, rows at a time, loads in flight
     const int c = tid % LANES;
-    const float factor = fmaxf(p.c * (p.ks ? __ldg(p.ks + it.h / p.G) : 1.f), 1e-18f);
 #pragma unroll 1
     for (int r0 = tid / LANES; r0 < 128; r0 += STEP * BATCH) {
         Vec16<__nv_bfloat16> x[BATCH];
@@ -393,7 +392,7 @@ __device__ __forceinline__ void convert_queries(const PromptParams &p, const Ite
                 w[i] = *reinterpret_cast<const uint32_t *>(&h);
             }
             *reinterpret_cast<uint4 *>(tile + (c >> 3) * 128 * 128 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-            if (c == 0) factors[row] = factor * back;
+            if (c == 0) inverses[row] = back;
         }
     }
 }
@@ -457,8 +456,8 @@ __global__ void __launch_bounds__(Cfg<DP, KV4>::THREADS, 1)
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     unsigned char *sq = smem, *ring = smem + NQ * C::QBYTES;
     unsigned char *raws = ring + SLOTS * C::SLOT;  // (this and the next three: KV4)
-    float *factors = reinterpret_cast<float *>(raws + C::RAWS * C::RAW);  // [4 items][2 query tiles][128 rows]
-    uint64_t *f_full = reinterpret_cast<uint64_t *>(factors + 4 * 2 * 128), *raw_full = f_full + 4, *raw_empty = raw_full + C::RAWS;
+    float *inverses = reinterpret_cast<float *>(raws + C::RAWS * C::RAW);  // [4 items][2 query tiles][128 rows]
+    uint64_t *f_full = reinterpret_cast<uint64_t *>(inverses + 4 * 2 * 128), *raw_full = f_full + 4, *raw_empty = raw_full + C::RAWS;
     volatile uint32_t *s_there = reinterpret_cast<uint32_t *>(raw_empty + C::RAWS);
     uint64_t *bars = reinterpret_cast<uint64_t *>(ring + SLOTS * C::SLOT + C::EXTRA);
     uint64_t *full = bars, *empty = full + SLOTS, *q_full = empty + SLOTS, *q_empty = q_full + 2,
@@ -560,7 +559,7 @@ __global__ void __launch_bounds__(Cfg<DP, KV4>::THREADS, 1)
                         if ((t ? it.n[1] : it.n[0]) == 0) continue;
                         if (!wait_or_abort(q_empty + t, ((q_phase >> t) & 1) ^ 1, abort)) goto done;
                         q_phase ^= 1u << t;
-                        convert_queries<DP>(p, it, t, sq + t * C::QBYTES, factors + (k * 2 + t) * 128, ctid);
+                        convert_queries<DP>(p, it, t, sq + t * C::QBYTES, inverses + (k * 2 + t) * 128, ctid);
                         fence_async_smem();
                         mbar_arrive(q_full + t);
                     }
@@ -812,8 +811,8 @@ __global__ void __launch_bounds__(Cfg<DP, KV4>::THREADS, 1)
             if constexpr (KV4) {
                 const uint32_t k = (n_item - 1) & 3;
                 if (!wait_or_abort(f_full + k, ((n_item - 1) >> 2) & 1, abort)) goto done;
-                pc = n > 0 ? factors[(k * 2 + t) * 128 + row] : 1.f;
-                // (not before: items without keys hold nobody up, and the factors of the fourth item after this one may be
+                pc = n > 0 ? kv4_row_factor(p.c, inverses[(k * 2 + t) * 128 + row], p.ks ? __ldg(p.ks + it.h / p.G) : 1.f) : 1.f;
+                // (not before: items without keys hold nobody up, and the inverses of the fourth item after this one may be
                 // ready before a late warp has looked at these)
                 release_item(k);
             }
@@ -1087,7 +1086,7 @@ cudaError_t launch(const Attn &a, int min_rows, int splits, cudaStream_t s, cons
     p.q_wide = rows_aligned(a.q, a.qs, a.D, 2);
     p.G = a.H / a.HKV;
     p.min_rows = min_rows;
-    p.c = std::fmax(std::fabs(a.scale) * kLog2e, 1e-30f);
+    p.c = std::fmax(std::fabs(a.scale) * kLog2e, KV4 ? 0.f : 1e-30f);  // (KV4: kv4_row_factor)
     p.negate = a.scale < 0.f;
     p.out32 = ((uintptr_t)a.out & 31) == 0 && a.D % 16 == 0;
     const bool paged = a.block_table != nullptr;

@@ -58,12 +58,20 @@ __device__ __forceinline__ uint32_t kv4_encode(const float (&t)[8]) {
     return r;
 }
 
-// The power of two that brings a row's largest magnitude into [1, 2), and its inverse (for rows below 2^-63, nothing
-// but zeros among them, 2^63, so that the inverse stays far from zero).
+// The power of two that brings a row's largest magnitude into [1, 2), and its inverse (both normal numbers; for rows below
+// 2^-126, nothing but zeros among them, 2^126).
 __device__ __forceinline__ float kv4_row_power(float amax, float &inverse) {
-    const int e = max(64, min((int)(__float_as_uint(amax) >> 23 & 255u), 253));  // (biased)
+    const int e = max(1, min((int)(__float_as_uint(amax) >> 23 & 255u), 253));  // (biased)
     inverse = __uint_as_float((uint32_t)e << 23);
     return __uint_as_float((uint32_t)(254 - e) << 23);
+}
+
+// A row's softmax factor c inverse ks, in an order that leaves the range only if the product does, and then kept
+// from 0 and infinity: a masked score stays -inf and a difference of 0 stays 0 under it.
+__device__ __forceinline__ float kv4_row_factor(float c, float inverse, float ks) {
+    const float lo = fminf(fminf(c, inverse), ks), hi = fmaxf(fmaxf(c, inverse), ks);
+    const float mid = fmaxf(fminf(fmaxf(c, inverse), ks), fminf(c, inverse));
+    return fminf(fmaxf(lo * hi * mid, 1e-30f), 1e30f);
 }
 
 }  // namespace gdn
