@@ -2,6 +2,8 @@
 import pytest
 import torch
 
+import beam_ref
+import serving_ref
 import test_gpu_kv4 as kv4
 import varlen_gated_delta_gb300 as gdn
 
@@ -28,6 +30,28 @@ def test_head_scales_of_extreme_sizes(dtype, n, size):
     p["q"] = (p["q"].float() * size).to(dtype)
     p["ts"][0] = torch.tensor([1.0 / size, 0.5 / size])
     kv4._check(p, kv4._run(p, scale=0.2), 0.2)
+
+
+@pytest.mark.parametrize("size", [1e9, 1e20, 1e35])
+@pytest.mark.parametrize("n,kv", [(1, 100), (20, 100), (70, 300), (40, 5000)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_scores_of_any_size_choose_one_key(dtype, n, kv, size):
+    """With scores of 1e9 and more a row is the value of its best key."""
+    p = kv4._problem(6, [n], [kv], 4, 2, 64, 16, dtype)
+    p["q"] = (p["q"].float() * size).to(dtype)
+    out = kv4._run(p).cpu().double()
+    k, v = (serving_ref.cached_rows(beam_ref.kv4_values(c, 16, 64), p["table"][0], kv) for c in p["caches"])
+    q, k, v = p["q"].double() / size, k.repeat_interleave(2, 1), v.repeat_interleave(2, 1)
+    x = torch.einsum("nhd,khd->nhk", q, k)
+    x.masked_fill_(torch.ones(n, kv, dtype=torch.bool).triu(kv - n + 1)[:, None], -float("inf"))
+    best = x.topk(2, -1)
+    # a score is a sum of 64 products in fp32, each sum within 2^-23 of the largest: 2^-17 of sum |q k| covers it
+    clear = best.values[..., 0] - best.values[..., 1] > 2.0 ** -16 * torch.einsum("nhd,khd->nhk", q.abs(), k.abs()).amax(-1)
+    assert float(clear.float().mean()) > 0.9
+    want = torch.gather(v.transpose(0, 1)[None].expand(n, -1, -1, -1), 2, best.indices[..., :1, None].expand(-1, -1, -1, 64))[:, :, 0]
+    # the probability is a power of two: one rounding to the output's type, and one of the quotient
+    tol = (torch.finfo(dtype).eps / 2 + 2.0 ** -23) * want.abs()
+    assert bool(((out - want).abs() <= tol)[clear].all())
 
 
 @pytest.mark.parametrize("H,HKV,D", [(32, 8, 128), (8, 8, 64), (16, 4, 256)])

@@ -876,7 +876,9 @@ __global__ void __launch_bounds__(Cfg<DP, KV4>::THREADS, 1)
                     }
                     tmem_wait_st();
                 }
-                const float mc = (m == -INFINITY ? 0.f : -m * pc) + (KV4 ? kKv4Shift : 0.f);
+                // KV4 takes the reference off first: all exponents of a row share the rounding of m pc, and where that is large
+                // (scores from 2^24 on) fp16 has no room for it (223 -> 226 us)
+                const float mc = KV4 ? kKv4Shift : m == -INFINITY ? 0.f : -m * pc, base = m == -INFINITY ? 0.f : -m;
                 float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int c = 0; c < BN / 64; ++c) {
@@ -885,7 +887,8 @@ __global__ void __launch_bounds__(Cfg<DP, KV4>::THREADS, 1)
                     for (int i = 0; i < 32; ++i) {
                         const float2 s2 = make_float2(__uint_as_float(x[2 * c + (i >> 4)][(2 * i) & 31]),
                                                       __uint_as_float(x[2 * c + (i >> 4)][(2 * i + 1) & 31]));
-                        float2 e = __ffma2_rn(s2, make_float2(pc, pc), make_float2(mc, mc));
+                        float2 e = __ffma2_rn(KV4 ? __fadd2_rn(s2, make_float2(base, base)) : s2, make_float2(pc, pc),
+                                              make_float2(mc, mc));
                         e.x = exp2_fast(e.x), e.y = exp2_fast(e.y);
                         sum = __fadd2_rn(sum, e);
                         if constexpr (KV4) {
