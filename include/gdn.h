@@ -695,7 +695,9 @@ GDN_API int gdn_kv4_write(const void *k, const void *v, int64_t k_stride, int64_
  * rows, masks, offsets, max_q and workspace rules.  out is 16-byte aligned.
  * The cache's values are used as they are (exact in the products); fp32
  * queries and probabilities as sums of two fp16 values, bf16 queries exactly,
- * their probabilities rounded to 11 bits; scores, sums and outputs in fp32.
+ * their probabilities rounded to 11 bits; scores, sums and outputs in fp32.  A
+ * (token, head) row with a NaN or an infinity among its queries is NaN if it
+ * sees a key.
  */
 GDN_API int gdn_attention_paged_kv4(const void *q, const void *k_cache, const void *v_cache,
                                     const float *k_scale, const float *v_scale,

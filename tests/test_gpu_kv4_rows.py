@@ -54,6 +54,28 @@ def test_scores_of_any_size_choose_one_key(dtype, n, kv, size):
     assert bool(((out - want).abs() <= tol)[clear].all())
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,kv", [(1, 90), (5, 90), (70, 90), (40, 5000)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_rows_of_infinite_queries_are_nan(dtype, n, kv, D):
+    """Also where every score is -inf; a row that sees no key stays 0."""
+    p = kv4._problem(n, [n, n], [kv, n - n // 2], 4, 2, D, 16, dtype)
+    keys = p["caches"][0]
+    keys[:, :, :16 * D // 2], keys[:, :, 16 * D // 2:] = 0x22, 0x38  # every key is a row of ones
+    clean = kv4._run(p)
+    odd = torch.zeros(clean.shape[:2], dtype=torch.bool, device="cuda")
+    for row, h, d, x in ((0, 1, 3, "-inf"), (n - 1, 2, D - 1, "inf"), (2 * n - 1, 0, 0, "-inf")):
+        p["q"][row, h, d] = float(x)
+        odd[row, h] = True
+    if n > 1:
+        p["q"][n, 3, 1] = -float("inf")  # a row before the first key
+    for scale in (0.0, -0.1):
+        clean = kv4._run(dict(p, q=p["q"].nan_to_num(posinf=0, neginf=0)), scale=scale)
+        out = kv4._run(p, scale=scale)
+        assert bool(out[odd].isnan().all()) and torch.equal(out[~odd], clean[~odd])
+        assert n == 1 or bool((out[n] == 0).all())
+
+
 @pytest.mark.parametrize("H,HKV,D", [(32, 8, 128), (8, 8, 64), (16, 4, 256)])
 def test_hundreds_of_slices_without_keys(H, HKV, D):
     """Slices of sequences with no keys, or whose first rows see none, between ones that have some."""

@@ -59,11 +59,12 @@ __device__ __forceinline__ uint32_t kv4_encode(const float (&t)[8]) {
 }
 
 // The power of two that brings a row's largest magnitude into [1, 2), and its inverse (both normal numbers; for rows below
-// 2^-126, nothing but zeros among them, 2^126).
+// 2^-126, nothing but zeros among them, 2^126).  With an infinity in the row the power is NaN, which makes all of its scores
+// NaN, as the definition has it: each is infinite or NaN, and a softmax over those has no value.
 __device__ __forceinline__ float kv4_row_power(float amax, float &inverse) {
     const int e = max(1, min((int)(__float_as_uint(amax) >> 23 & 255u), 253));  // (biased)
     inverse = __uint_as_float((uint32_t)e << 23);
-    return __uint_as_float((uint32_t)(254 - e) << 23);
+    return fmaf(amax, 0.f, __uint_as_float((uint32_t)(254 - e) << 23));  // (infinity times 0)
 }
 
 // A row's softmax factor c inverse ks, in an order that leaves the range only if the product does, and then kept
