@@ -76,6 +76,16 @@ def test_rows_of_infinite_queries_are_nan(dtype, n, kv, D):
         assert n == 1 or bool((out[n] == 0).all())
 
 
+@pytest.mark.parametrize("n", [1, 24, 40])
+def test_a_malformed_offset_leaves_the_others_alone(n):
+    p = kv4._problem(5, [n, n, n], [40, 50, 60], 4, 2, 64, 16, BF16)
+    out = torch.full(p["q"].shape, 3.0, dtype=BF16, device="cuda")
+    kv4._run(dict(p, offsets=[0, -1, n, 2 * n]), out=out, max_q=n)  # the third sequence has rows n to 2 n
+    alone = kv4._run(dict(p, q=p["q"][n:2 * n], table=p["table"][2:], kv=p["kv"][2:], offsets=[0, n]), max_q=n)
+    assert torch.equal(out[n:2 * n], alone)
+    assert bool((out[:n] == 3).all()) and bool((out[2 * n:] == 3).all())
+
+
 @pytest.mark.parametrize("H,HKV,D", [(32, 8, 128), (8, 8, 64), (16, 4, 256)])
 def test_hundreds_of_slices_without_keys(H, HKV, D):
     """Slices of sequences with no keys, or whose first rows see none, between ones that have some."""
