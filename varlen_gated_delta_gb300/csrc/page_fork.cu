@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kThreads) page_fork_kernel(const PageFork p, F
     for (long i = t0 * 16; i < p.num_pages; i += step * 16)  // (the marks' rooms are multiples of 16)
         *reinterpret_cast<uint4 *>(w.was + i) = *reinterpret_cast<uint4 *>(w.is + i) = make_uint4(0, 0, 0, 0);
     if (tid == 0) s_bad = 0;
-    const int cursor = __ldg(p.cursor);
+    const int cursor = *p.cursor;  // (not as read-only data: cursor_out may be the same word)
     bool bad = cursor < 0 || cursor > p.n_free;
     for (int b = tid; b < p.B; b += kThreads) {
         const int len = p.kv_lens[b];

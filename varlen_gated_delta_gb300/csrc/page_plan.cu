@@ -75,13 +75,13 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const PagePlan p) {
 
     if (tid == 0) s_bad = 0;
     __syncthreads();
-    const int cursor = __ldg(p.cursor);
+    const int cursor = *p.cursor;  // (this and the cached lengths not as read-only data: outputs may be the same words)
     const int per = (p.B + kThreads - 1) / kThreads;
     const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
     long long tok = 0, pages = 0;
     int bad = 0;  // the most severe finding: shape, then capacity
     for (int b = b0; b < b1; ++b) {
-        int n = __ldg(p.new_lens + b), c = __ldg(p.cached_lens + b);
+        int n = __ldg(p.new_lens + b), c = p.cached_lens[b];
         if (n < 0 || c < 0) {
             bad = GDN_ERR_SHAPE;
             n = 0, c = max(c, 0);
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const PagePlan p) {
     for (int b = t0; b <= p.B; b += step) {
         p.offsets[b] = ok ? s_ofs[b] : 0;
         if (b < p.B && (ok || p.kv_lens != p.cached_lens))
-            p.kv_lens[b] = ok ? s_cached[b] + s_ofs[b + 1] - s_ofs[b] : __ldg(p.cached_lens + b);
+            p.kv_lens[b] = ok ? s_cached[b] + s_ofs[b + 1] - s_ofs[b] : p.cached_lens[b];
     }
     if (t0 == 0) {
         *p.cursor_out = cursor + fresh;
