@@ -18,10 +18,11 @@
 // 64 x 8 beams of 131072 bf16 logits, a tenth of the beams at their end: 45 us, 2.7 TB/s.  Reading is not what bounds it: 20
 // million warp instructions at two a clock (two fifths of them exponentials and the conversions before them), and warps that wait
 // for a piece's ranking.  One launch's pieces without the next one's loads in flight: 55 us; one piece to a CTA: 57.
-// One group of 4 x 32768: 10 us, two launches and chains of dependent steps.
+// One group of 4 x 32768: 9 us, two launches and chains of dependent steps.
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
 #include "serving.h"
@@ -117,13 +118,20 @@ __device__ __forceinline__ float of_key(uint32_t high) {
     return __uint_as_float(high & 0x80000000u ? high & 0x7fffffffu : ~high);
 }
 
-template <typename T, int ELEMS>
+// Vectors of a warp in a row of its stage.  SKEWED: some rows do not begin on 16-byte boundaries, and values are shifted
+// into their places when they come from the stage (64 x 8 beams of 131071: 55 us; 51 with sums in the order of
+// addresses, which differ from row to row).
+constexpr int warp_row(bool skewed) { return skewed ? 33 : 32; }
+
+template <typename T, int ELEMS, bool SKEWED>
 __global__ void __launch_bounds__(kThreads, ELEMS <= 8 ? 6 : 3)
     beam_spans_kernel(const T *__restrict__ logits, long stride, const uint8_t *__restrict__ finished, Spans out, int V,
                       int n, int spans, int pieces) {
     constexpr int VEC = 16 / sizeof(T), VECS = ELEMS / VEC;
     using Key = unsigned long long;
-    extern __shared__ uint4 s_data[];  // [2 stages][VECS][kThreads]: each thread's own vectors of a piece and of the next
+    // [2 stages][VECS][8 warps][32 or 33]: each warp's vectors of a piece and of the next (SKEWED: and the one behind them)
+    extern __shared__ uint4 s_data[];
+    constexpr int kWarp = warp_row(SKEWED), kRow = kThreads / 32 * kWarp, kStage = VECS * kRow;
     __shared__ __align__(16) float s_all[kThreads];
     __shared__ Key s_list[kList], s_top[kThreads / 32], s_best[2][kBeamMaxN];
     __shared__ float2 s_nth[kThreads / 32];
@@ -135,9 +143,10 @@ __global__ void __launch_bounds__(kThreads, ELEMS <= 8 ? 6 : 3)
     pdl_launch_dependents();
     if (finished != nullptr && __ldg(finished + row) != 0) return;  // (nothing of it is looked at)
     const T *x = logits + row * stride;
-    // Vectors lie on 16-byte boundaries: the first may begin before the row.  (Places up to a piece past V fit: beam_select_fits)
-    const int skew = (int)(((uintptr_t)x / sizeof(T)) % VEC);
-    const int from = span * pieces * (ELEMS * kThreads) - skew;
+    // Copied vectors lie on 16-byte boundaries, which a row may begin `skew` values behind.  A thread's values are the same wherever
+    // a row begins, so that equal rows have equal sums.  (Places up to a piece past V fit: beam_select_fits)
+    const int skew = SKEWED ? (int)(((uintptr_t)x / sizeof(T)) % VEC) : 0;
+    const int from = span * pieces * (ELEMS * kThreads);
     if (tid < 3) s_n[tid] = 0;
 
     constexpr float kL = 1.4426950408889634f;
@@ -148,21 +157,23 @@ __global__ void __launch_bounds__(kThreads, ELEMS <= 8 ? 6 : 3)
     const auto fetch = [&](int piece) {
         const int first = from + piece * (ELEMS * kThreads);
         if (piece < pieces && first < V) {
-            uint4 *stage = s_data + (piece & 1) * VECS * kThreads + tid;
-#pragma unroll
-            for (int j = 0; j < VECS; ++j) {
-                const int at = first + (j * kThreads + tid) * VEC;
+            uint4 *stage = s_data + (piece & 1) * kStage + warp * kWarp;
+            const auto copy = [&](int j, int i) {  // the warp's vector i of row j
+                const int at = first - skew + (j * kThreads + warp * 32 + i) * VEC;
                 if (at >= 0 && at <= V - VEC) {
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(stage + j * kThreads)),
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(stage + j * kRow + i)),
                                  "l"(x + at)
                                  : "memory");
                 } else {
                     Vec16<T> w;
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) w.v[i] = at + i >= 0 && at + i < V ? x[at + i] : from_f32<T>(-INFINITY);
-                    stage[j * kThreads] = w.u;
+                    for (int k = 0; k < VEC; ++k) w.v[k] = at + k >= 0 && at + k < V ? x[at + k] : from_f32<T>(-INFINITY);
+                    stage[j * kRow + i] = w.u;
                 }
-            }
+            };
+#pragma unroll
+            for (int j = 0; j < VECS; ++j) copy(j, lane);
+            if (SKEWED && lane < VECS) copy(lane, 32);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -173,11 +184,33 @@ __global__ void __launch_bounds__(kThreads, ELEMS <= 8 ? 6 : 3)
         if (first >= V) break;
         fetch(piece + 1);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
-        __syncwarp();  // (the warp's vectors are here: its lanes read each other's below)
-        const uint4 *stage = s_data + (piece & 1) * VECS * kThreads;
+        __syncwarp();  // (the warp's vectors are here: its lanes read each other's, also below)
+        const uint4 *stage = s_data + (piece & 1) * kStage + warp * kWarp;
+        // value i of a lane
+        const auto held = [&](int lane, int i) { return to_f32(reinterpret_cast<const T *>(stage + i / VEC * kRow + lane)[skew + i % VEC]); };
         Vec16<T> w[VECS];
+        if constexpr (!SKEWED) {
 #pragma unroll
-        for (int j = 0; j < VECS; ++j) w[j].u = stage[j * kThreads + tid];
+            for (int j = 0; j < VECS; ++j) w[j].u = stage[j * kRow + lane];
+        } else {
+            const auto shifted = [&](auto words) {  // by so many words, and half a one
+                constexpr int k = decltype(words)::value;
+                const int bits = sizeof(T) == 2 && (skew & 1) ? 16 : 0;
+#pragma unroll
+                for (int j = 0; j < VECS; ++j) {
+                    const uint4 a = stage[j * kRow + lane], b = stage[j * kRow + lane + 1];
+                    const uint32_t c[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                    w[j].u = make_uint4(__funnelshift_r(c[k], c[k + 1], bits), __funnelshift_r(c[k + 1], c[k + 2], bits),
+                                        __funnelshift_r(c[k + 2], c[k + 3], bits), __funnelshift_r(c[k + 3], c[k + 4], bits));
+                }
+            };
+            switch (skew * (int)sizeof(T) / 4) {
+            case 0: shifted(std::integral_constant<int, 0>()); break;
+            case 1: shifted(std::integral_constant<int, 1>()); break;
+            case 2: shifted(std::integral_constant<int, 2>()); break;
+            default: shifted(std::integral_constant<int, 3>());
+            }
+        }
         const auto value = [&](int i) { return to_f32(w[i / VEC].v[i % VEC]); };
         const auto token = [&](int i) { return first + (i / VEC * kThreads + tid) * VEC + i % VEC; };
         // (NaN is passed over: it is no candidate)
@@ -210,8 +243,8 @@ __global__ void __launch_bounds__(kThreads, ELEMS <= 8 ? 6 : 3)
         for (unsigned left = __ballot_sync(0xffffffffu, some); left != 0; left &= left - 1)
 #pragma unroll
             for (int e = lane; e < ELEMS; e += 32) {
-                const int place = e / VEC * kThreads + warp * 32 + __ffs(left) - 1, at = first + place * VEC + e % VEC;
-                const float v = fmaxf(to_f32(reinterpret_cast<const T *>(stage + place)[e % VEC]), -INFINITY);
+                const int of = __ffs(left) - 1, at = first + (e / VEC * kThreads + warp * 32 + of) * VEC + e % VEC;
+                const float v = fmaxf(held(of, e), -INFINITY);
                 if (v >= reach && v != -INFINITY) {
                     const int k = atomicAdd(&s_n[piece % 3], 1);
                     if (k < kList) s_list[k] = key_of(v, at);
@@ -240,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, ELEMS <= 8 ? 6 : 3)
                     Key top = tid < have && best[tid] < last ? best[tid] : 0;
 #pragma unroll 4
                     for (int i = 0; i < ELEMS; ++i) {
-                        const float v = fmaxf(to_f32(reinterpret_cast<const T *>(stage + i / VEC * kThreads + tid)[i % VEC]), -INFINITY);
+                        const float v = fmaxf(held(lane, i), -INFINITY);
                         const Key key = key_of(v, token(i));
                         if (v != -INFINITY && key < last && key > top) top = key;
                     }
@@ -509,7 +542,7 @@ struct Cut {
     int elems, spans, pieces;  // of a thread; of a row; of a span
 };
 Cut cut_rows(int rows, int V, int dtype) {
-    const auto pieces = [&](int elems) { return (int)(((long)V + 7 + elems * kThreads - 1) / (elems * kThreads)); };  // (7: the skew)
+    const auto pieces = [&](int elems) { return (int)(((long)V + elems * kThreads - 1) / (elems * kThreads)); };
     Cut c;
     c.elems = dtype == GDN_BF16 ? 64 : 32;
     int all = pieces(c.elems);
@@ -521,18 +554,23 @@ Cut cut_rows(int rows, int V, int dtype) {
 }
 int most_spans(int rows, int V) { return std::max(cut_rows(rows, V, GDN_BF16).spans, cut_rows(rows, V, GDN_F32).spans); }
 
-template <typename T, int ELEMS>
+template <typename T, int ELEMS, bool SKEWED>
 cudaError_t launch_spans(const BeamSelect &p, const Spans &w, const Cut &c, cudaStream_t s) {
-    constexpr int kBytes = 2 * ELEMS * kThreads * sizeof(T);
+    constexpr int kBytes = 2 * (ELEMS * sizeof(T)) * (kThreads / 32 * warp_row(SKEWED));
     static std::atomic<uint64_t> attr_set{0};
     cudaError_t e = once_per_device(attr_set, [] {
-        return cudaFuncSetAttribute(beam_spans_kernel<T, ELEMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+        return cudaFuncSetAttribute(beam_spans_kernel<T, ELEMS, SKEWED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     });
     if (e != cudaSuccess) return e;
-    e = launch_kernel(beam_spans_kernel<T, ELEMS>, dim3((unsigned)(p.G * p.K * c.spans)), dim3(kThreads), kBytes, s, true,
+    e = launch_kernel(beam_spans_kernel<T, ELEMS, SKEWED>, dim3((unsigned)(p.G * p.K * c.spans)), dim3(kThreads), kBytes, s, true,
                       static_cast<const T *>(p.logits), p.stride, p.finished, w, p.V, p.n, c.spans, c.pieces);
     note_launch();
     return e;
+}
+template <typename T, int ELEMS>
+cudaError_t launch_spans(const BeamSelect &p, const Spans &w, const Cut &c, cudaStream_t s) {
+    const bool aligned = (uintptr_t)p.logits % 16 == 0 && (p.G * p.K == 1 || p.stride * sizeof(T) % 16 == 0);
+    return aligned ? launch_spans<T, ELEMS, false>(p, w, c, s) : launch_spans<T, ELEMS, true>(p, w, c, s);
 }
 
 }  // namespace
