@@ -724,7 +724,9 @@ GDN_API size_t gdn_attention_paged_kv4_workspace_bytes(int B, int N, int H, int 
 /*
  * gdn_beam_select - of each group's K V continuations the n with the largest
  *   scores[g, k] + x[g K + k, t] - log sum_t' exp x[g K + k, t'],
- * descending, ties to the lowest k V + t.
+ * descending.  Of equal totals the lowest k comes first, within a beam the
+ * largest logit (a score of -1e30 takes the logits' differences away), then the
+ * lowest t.
  *   logits       G K rows of V values T, row_stride elements apart (>= V)
  *   scores       [G, K] f32: log probabilities so far
  *   finished     [G, K] bytes or NULL: a beam whose flag is not 0 has one

@@ -49,3 +49,31 @@ def test_equal_rows_stay_in_order(V, dtype):
         assert tokens[g].tolist() == [f[2] for f in found]
         same = [f[0] == found[0][0] for f in found]
         assert len({x for x, s in zip(totals[g].tolist(), same) if s}) == 1
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dead", [-1e4, -1e9, -3.4e38, torch.finfo(F32).min])
+@pytest.mark.parametrize("V", [40, 3001, 140001])
+def test_dead_beams_with_finite_scores(V, dead, dtype):
+    """The first step of a search whose dead beams have a large negative score instead of -inf."""
+    gen = torch.Generator(device="cuda").manual_seed(V)
+    K, n = 8, 16
+    logits = (torch.randn(2 * K, V, generator=gen, device="cuda") * 3).to(dtype)
+    scores = torch.full((2, K), dead, device="cuda")
+    scores[0, 0] = scores[1, 3] = 0.0
+    logits[K + 3, 5:] = -float("inf")  # the live beam of the second group has five continuations
+    tokens, parents, totals, _ = gdn.gdn_beam_select(logits, scores, n=n)
+    # the definition: by total, then the lowest beam; within a beam by logit, then the lowest token
+    for g in range(2):
+        found = []
+        for k in range(K):
+            row = logits[g * K + k].double()
+            total = float(scores[g, k]) + (row - torch.logsumexp(row, 0))
+            best = torch.sort(row, descending=True, stable=True).indices[:n].tolist()
+            found += [(-float(total[t]), k, i, t) for i, t in enumerate(best) if row[t] > -float("inf")]
+        found = sorted(found)[:n]
+        assert parents[g].tolist() == [g * K + f[1] for f in found]
+        assert tokens[g].tolist() == [f[3] for f in found]
+        want = torch.tensor([-f[0] for f in found], dtype=torch.float64)
+        # one rounding to fp32, and a sum of fp32 exponentials that is 2^-20 off at most
+        assert bool(((totals[g].cpu().double() - want).abs() <= want.abs() * 2.0 ** -24 + 2.0 ** -20).all())

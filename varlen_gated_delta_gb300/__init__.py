@@ -809,10 +809,11 @@ def gdn_beam_select(logits, scores, *, n=None, finished=None, end_token=-1, keep
 
     ``logits`` [G * K, V] (any row stride), ``scores`` [G, K] f32 log probabilities so far.
     A beam whose ``finished`` [G, K] flag (bool or uint8) is set goes on as it is, with
-    ``end_token``.  Ordered by score, ties to the lowest beam and token; with ``keep_rows``
-    (n == K) a beam's best continuation takes the beam's own place instead, the others take
-    the places that are left.  ``scores_out`` may be ``scores`` and ``finished_out``
-    ``finished``.  Returns (tokens, parents, scores, finished) [G, n]; parents are rows
+    ``end_token``.  Ordered by score; of equal ones the lowest beam comes first, in it the
+    largest logit, then the lowest token.  With ``keep_rows`` (n == K) a beam's best
+    continuation takes the beam's own place instead, the others take the places that are left.
+    ``scores_out`` may be ``scores`` and ``finished_out`` ``finished``.  Returns (tokens,
+    parents, scores, finished) [G, n]; parents are rows
     g * K + k; finished is None unless flags were given or asked for."""
     return (_marshal_module or _marshal()).beam_select(logits, scores, n, finished, end_token, keep_rows, tokens,
                                                        parents, scores_out, finished_out, workspace)

@@ -1,8 +1,8 @@
 // beam_select.cu - gdn_beam_select: the best continuations of each group of beams.
 //
 //   total[g, k, t] = score[g, k] + x[g, k, t] - log sum_t' exp x[g, k, t'],
-// and of a group's K V totals the n largest, ties to the lowest k V + t.  The logits are read once, in two
-// launches.
+// and of a group's K V totals the n largest.  Of equal ones the lowest beam comes first, within a beam the largest logit (a
+// score of -1e30 leaves nothing of the logits in 64 bits), then the lowest token.  The logits are read once, in two launches.
 //
 // The first gives a CTA a span of a row, which it goes through in pieces that fit its registers, with a reference m, the
 // sum of exp(x - m), and the n largest logits so far.  In a first piece (with at least n values above -inf, else in the next too) the threads form groups whose maxima are at hand: at
@@ -377,12 +377,14 @@ __global__ void __launch_bounds__(kThreads, ELEMS <= 8 ? 6 : 3)
     }
 }
 
+// A continuation: the larger key comes first, of equal totals the larger place (the lowest beam, in it the largest logit, of
+// equal ones the lowest token).
 struct Pick {
     unsigned long long total;  // key_of
-    int at;                    // k V + t
+    unsigned long long place;  // K - 1 - k; the logit's key; 2^bits - 1 - t
 };
-__device__ __forceinline__ bool before(unsigned long long a, int ia, unsigned long long b, int ib) {
-    return a > b || (a == b && ia < ib);
+__device__ __forceinline__ bool before(unsigned long long a, unsigned long long ia, unsigned long long b, unsigned long long ib) {
+    return a > b || (a == b && ia > ib);
 }
 
 __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamSelect p, Spans in, int spans) {
@@ -393,7 +395,8 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamSelect p,
     __shared__ float2 s_sum[kBeamMaxK];
     __shared__ uint8_t s_done[kBeamMaxK];
     __shared__ unsigned long long s_total[kList];
-    __shared__ int s_at[kList], s_place[kBeamMaxN], s_rest[kBeamMaxN];
+    __shared__ unsigned long long s_key[kList];
+    __shared__ int s_first[kBeamMaxN], s_place[kBeamMaxN], s_rest[kBeamMaxN];
     __shared__ Pick s_pick[kBeamMaxN], s_top[kThreads / 32];
     __shared__ float s_x[kNear];
     __shared__ int s_token[kNear];
@@ -449,82 +452,78 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamSelect p,
     auto total = [&](int c, int k, float x) {
         return key_of(s_done[k] ? (double)s_score[k] : (double)s_score[k] + ((double)x - s_lse[k]));
     };
-    auto place = [&](int c, int k) { return k * p.V + (s_done[k] ? p.end_token : c < kNear ? s_token[c] : __ldcg(in.token + (long)g * all + c)); };
-    float mine = -INFINITY, size = 0.f;
+    // How far that may be off: the row's term, the two sums and this bound's own are rounded to 2^-24 of these sizes each.
+    auto off = [&](float x, int k) { return (fabsf(x) + (s_done[k] ? 0.f : fabsf(s_lse32[k])) + fabsf(s_score[k])) * 0x1p-21f; };
+    const int bits = p.V > 1 ? 32 - __clz(p.V - 1) : 0;  // of a token (bits of K and V together: at most 32)
+    const uint32_t mask = (1u << bits) - 1u;
+    auto place = [&](int c, int k, float x) {
+        const uint32_t t = s_done[k] ? p.end_token : c < kNear ? s_token[c] : __ldcg(in.token + (long)g * all + c);
+        return (unsigned long long)(K - 1 - k) << (32 + bits) | (key_of(x, 0) >> 32) << bits | (mask - t);
+    };
+    auto beam_of = [&](const Pick &b) { return K - 1 - (int)(b.place >> (32 + bits)); };
+    auto token_of = [&](const Pick &b) { return (int)(mask - ((uint32_t)b.place & mask)); };
+    float mine = -INFINITY;
     for (int c = tid; c < all; c += kThreads) {
         const int k = c / per_beam;
         const float x = logit(c, k), t = about(x, k);
-        if (x != -INFINITY && t > -INFINITY)
-            mine = fmaxf(mine, t), size = fmaxf(size, fabsf(x) + (s_done[k] ? 0.f : fabsf(s_lse32[k])) + fabsf(s_score[k]));
+        if (x != -INFINITY && t > -INFINITY) mine = fmaxf(mine, t - off(x, k));  // (passes over inf - inf)
     }
-    // The row's term and two sums are rounded, each to 2^-24 of these sizes: 2^-21 is more than two totals can be off.
-    // (Infinite scores leave everything in.)
-    size = warp_max(size);
-    if (lane == 0) s_m[warp] = size;  // (K <= 128 >= 8 places; the maxima have been used)
     float best;  // (barriers)
     const float reach = nth_maximum(mine, n, kThreads, s_all, s_least, best);
-    size = s_m[0];
-#pragma unroll
-    for (int w = 1; w < kThreads / 32; ++w) size = fmaxf(size, s_m[w]);
-    const float least = size < 1e30f ? reach - size * 0x1p-21f : -INFINITY;
     for (int c = tid; c < all; c += kThreads) {
         const int k = c / per_beam;
         const float x = logit(c, k), t = about(x, k);
-        if (x != -INFINITY && t >= least && t > -INFINITY) {
+        if (x != -INFINITY && t > -INFINITY && t + off(x, k) >= reach) {
             const int i = atomicAdd(&s_n, 1);
-            if (i < kList) s_total[i] = total(c, k, x), s_at[i] = place(c, k);
+            if (i < kList) s_total[i] = total(c, k, x), s_key[i] = place(c, k, x);
         }
     }
     __syncthreads();
     int found = s_n;
     if (found <= kList) {
         for (int i = tid; i < found; i += kThreads) {
-            const unsigned long long t = s_total[i];
-            const int at = s_at[i];
+            const unsigned long long t = s_total[i], at = s_key[i];
             int rank = 0;
 #pragma unroll 8
-            for (int j = 0; j < found; ++j) rank += before(s_total[j], s_at[j], t, at);
+            for (int j = 0; j < found; ++j) rank += before(s_total[j], s_key[j], t, at);
             if (rank < n) s_pick[rank] = Pick{t, at};
         }
     } else {
-        unsigned long long lt = ~0ull;
-        int la = -1;
+        Pick last{~0ull, ~0ull};
         for (found = 0; found < n; ++found) {
-            unsigned long long bt = 0;
-            int ba = INT_MAX;
+            Pick top{0, 0};
             for (int c = tid; c < all; c += kThreads) {
                 const int k = c / per_beam;
                 const float x = logit(c, k);
                 if (x == -INFINITY || !(about(x, k) > -INFINITY)) continue;
-                const unsigned long long t = total(c, k, x);
-                const int at = place(c, k);
-                if (before(lt, la, t, at) && before(t, at, bt, ba)) bt = t, ba = at;
+                const unsigned long long t = total(c, k, x), at = place(c, k, x);
+                if (before(last.total, last.place, t, at) && before(t, at, top.total, top.place)) top = Pick{t, at};
             }
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) {
-                const unsigned long long t = __shfl_xor_sync(0xffffffffu, bt, d);
-                const int at = __shfl_xor_sync(0xffffffffu, ba, d);
-                if (before(t, at, bt, ba)) bt = t, ba = at;
+                const unsigned long long t = __shfl_xor_sync(0xffffffffu, top.total, d), at = __shfl_xor_sync(0xffffffffu, top.place, d);
+                if (before(t, at, top.total, top.place)) top = Pick{t, at};
             }
-            if (lane == 0) s_top[warp] = Pick{bt, ba};
+            if (lane == 0) s_top[warp] = top;
             __syncthreads();
 #pragma unroll
             for (int w = 0; w < kThreads / 32; ++w)
-                if (before(s_top[w].total, s_top[w].at, bt, ba)) bt = s_top[w].total, ba = s_top[w].at;
+                if (before(s_top[w].total, s_top[w].place, top.total, top.place)) top = s_top[w];
             __syncthreads();
-            if (ba == INT_MAX) break;
-            if (tid == 0) s_pick[found] = Pick{bt, ba};
-            lt = bt, la = ba;
+            if (top.total == 0) break;
+            if (tid == 0) s_pick[found] = top;
+            last = top;
         }
     }
     found = min(found, n);
     __syncthreads();
     if (tid == 0 && found < n) {
         // too few: the lowest places of those that are left, all of them at -inf
-        for (int at = 0; found < n; ++at) {
+        const int had = found;
+        for (int k = 0, t = 0; found < n; t + 1 < p.V ? ++t : (t = 0, ++k)) {
             bool have = false;
-            for (int i = 0; i < found; ++i) have |= s_pick[i].at == at;
-            if (!have) s_pick[found++] = Pick{key_of(-(double)INFINITY), at};
+            for (int i = 0; i < had; ++i) have |= beam_of(s_pick[i]) == k && token_of(s_pick[i]) == t;
+            if (!have) s_pick[found++] = Pick{key_of(-(double)INFINITY), (unsigned long long)(K - 1 - k) << (32 + bits) | (mask - t)};
         }
     }
     __syncthreads();
@@ -533,18 +532,18 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamSelect p,
         for (int i = tid; i < n; i += kThreads) s_rest[i] = -1;
         __syncthreads();
         for (int i = tid; i < n; i += kThreads) {
-            const int k = s_pick[i].at / p.V;
+            const int k = beam_of(s_pick[i]);
             bool best = true;
-            for (int j = 0; j < i; ++j) best &= s_pick[j].at / p.V != k;
-            s_at[i] = best ? k : -1;
+            for (int j = 0; j < i; ++j) best &= beam_of(s_pick[j]) != k;
+            s_first[i] = best ? k : -1;
             if (best) s_rest[k] = i;
         }
         __syncthreads();
         for (int i = tid; i < n; i += kThreads) {
             if (s_rest[i] >= 0) s_place[i] = s_rest[i];
-            if (s_at[i] >= 0) continue;
+            if (s_first[i] >= 0) continue;
             int others = 0, row = -1;  // the others before this one, and the row that many are left before
-            for (int j = 0; j < i; ++j) others += s_at[j] < 0;
+            for (int j = 0; j < i; ++j) others += s_first[j] < 0;
             while (others >= 0) others -= s_rest[++row] < 0;
             s_place[row] = i;
         }
@@ -552,7 +551,7 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamSelect p,
     }
     for (int i = tid; i < n; i += kThreads) {
         const Pick b = s_pick[p.keep_rows ? s_place[i] : i];
-        const int k = b.at / p.V, token = b.at % p.V;
+        const int k = beam_of(b), token = token_of(b);
         const long o = (long)g * n + i;
         p.tokens[o] = token;
         p.parents[o] = g * K + k;
