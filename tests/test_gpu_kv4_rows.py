@@ -54,6 +54,19 @@ def test_scores_of_any_size_choose_one_key(dtype, n, kv, size):
     assert bool(((out - want).abs() <= tol)[clear].all())
 
 
+@pytest.mark.parametrize("factor", [2.0 ** -116, 2.0 ** 100])
+@pytest.mark.parametrize("n,kv", [(1, 100), (1, 5000), (20, 100), (70, 300), (40, 5000)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_value_scales_of_extreme_sizes(dtype, n, kv, factor):
+    """A power of two as the values' scale moves the exponent of the outputs and nothing else."""
+    p = kv4._problem(8, [n], [kv], 4, 2, 64, 16, dtype)
+    want = kv4._run(p).double() * factor
+    p["ts"][1] = torch.full((2,), factor)
+    got = kv4._run(p).double()
+    normal = want.abs() >= 2.0 ** -125
+    assert float(normal.double().mean()) > 0.9 and torch.equal(got[normal], want[normal])
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("n,kv", [(1, 90), (5, 90), (70, 90), (40, 5000)])
 @pytest.mark.parametrize("dtype", [BF16, F32])

@@ -426,6 +426,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const Attn a, int splits
     for (int s = lane; s < splits; s += 32) l += first.ml[2 * s + 1] * exp2_fast(first.ml[2 * s] - ref);
     l = group_sum<32>(l);
     const float inv = l > 0.f ? 1.f / l : l;  // (0 gives 0, NaN stays)
+    const float scale = a.out_scale ? __ldg(a.out_scale + row % a.H / (a.H / a.HKV)) : 1.f;
     T *out = static_cast<T *>(a.out) + row * D;
     for (int d = lane; d < D; d += 32) {
         float o = 0.f;
@@ -434,7 +435,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const Attn a, int splits
             const float c = exp2_fast(first.ml[2 * s] - ref), v = first.o[(size_t)s * D + d];
             o += c > 0.f ? v * c : 0.f;  // (a split that counts for nothing may hold inf)
         }
-        out[d] = from_f32<T>(l != 0.f ? o * inv : 0.f);
+        out[d] = from_f32<T>(l != 0.f ? o * inv * scale : 0.f);
     }
 }
 

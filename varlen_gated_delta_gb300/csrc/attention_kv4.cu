@@ -433,11 +433,11 @@ __global__ void __launch_bounds__(128) kv4_wide_kernel(const Kv4Params p) {
                 const int r = warp * 16 + g + 8 * z;
                 if (r >= rows) continue;
                 if (whole) {
-                    const float inv = l[z] > 0.f ? vs / l[z] : l[z];  // (0 gives 0, NaN stays)
+                    const float inv = l[z] > 0.f ? 1.f / l[z] : l[z];  // (0 gives 0, NaN stays)
                     T *out = static_cast<T *>(p.a.out) + ((size_t)(cur.start + (row0 + r) / G) * p.a.H + cur.h * G + (row0 + r) % G) * D;
 #pragma unroll
                     for (int i = 0; i < DP / 8; ++i)
-                        if (i * 8 < D) store2(out + i * 8 + t4 * 2, o[i][2 * z] * inv, o[i][2 * z + 1] * inv);
+                        if (i * 8 < D) store2(out + i * 8 + t4 * 2, o[i][2 * z] * inv * vs, o[i][2 * z + 1] * inv * vs);
                 } else {
                     // a part that begins its triple is the CTA's last, any other its first
                     float *part = p.part + (2 * cta + (first_tile == 0)) * C::PART;
@@ -876,7 +876,7 @@ __global__ void __launch_bounds__(128, Narrow<DP, NT, T>::PER_SM) kv4_narrow_ker
                         M = __shfl_sync(0xffffffffu, m[nt][y], from), L = __shfl_sync(0xffffffffu, l[nt][y], from);
                         c = __shfl_sync(0xffffffffu, cr[nt][y], from);
                     }
-                    const float inv = L > 0.f ? vs / L : L;  // (0 gives 0, NaN stays)
+                    const float inv = L > 0.f ? 1.f / L : L;  // (0 gives 0, NaN stays)
                     float *part = p.part + (2 * cta + (first_tile == 0)) * C::PART;
                     T *out = static_cast<T *>(p.a.out) + ((size_t)(cur.start + (row0 + r) / G) * p.a.H + cur.h * G + (row0 + r) % G) * D;
                     if (!whole && lane == 0) part[r] = M, part[C::ROWS + r] = L, part[2 * C::ROWS + r] = c;
@@ -889,7 +889,7 @@ __global__ void __launch_bounds__(128, Narrow<DP, NT, T>::PER_SM) kv4_narrow_ker
                             x.x += v.x, x.y += v.y;
                         }
                         if (!whole) *reinterpret_cast<float2 *>(part + 3 * C::ROWS + r * DP + d) = x;
-                        else if (FULL || d < D) store2(out + d, x.x * inv, x.y * inv);
+                        else if (FULL || d < D) store2(out + d, x.x * inv * vs, x.y * inv * vs);
                     }
                 }
                 __syncthreads();  // read, before the next column tile's or the copies to come
@@ -967,10 +967,10 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : WARPS * 32) kv4_join_kernel
         }
         T *out = static_cast<T *>(p.a.out) + ((size_t)(start + row / p.G) * p.a.H + h * p.G + row % p.G) * p.a.D;
         if constexpr (WARPS == 1) {
-            const float inv = l > 0.f ? vs / l : l;  // (0 gives 0, NaN stays)
+            const float inv = l > 0.f ? 1.f / l : l;  // (0 gives 0, NaN stays)
             if (lane * E < p.a.D)
 #pragma unroll
-                for (int i = 0; i < E; i += 2) store2(out + lane * E + i, o[i] * inv, o[i + 1] * inv);
+                for (int i = 0; i < E; i += 2) store2(out + lane * E + i, o[i] * inv * vs, o[i + 1] * inv * vs);
         } else {
             if (lane == 0) s_m[warp] = m;
             __syncthreads();
@@ -985,12 +985,12 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : WARPS * 32) kv4_join_kernel
             float L = 0.f;
 #pragma unroll
             for (int w = 0; w < WARPS; ++w) L += s_l[w];
-            const float inv = L > 0.f ? vs / L : L;  // (0 gives 0, NaN stays)
+            const float inv = L > 0.f ? 1.f / L : L;  // (0 gives 0, NaN stays)
             for (int d = tid; d < p.a.D; d += WARPS * 32) {
                 float x = 0.f;
 #pragma unroll
                 for (int w = 0; w < WARPS; ++w) x += s_o[w][d];
-                out[d] = from_f32<T>(x * inv);
+                out[d] = from_f32<T>(x * inv * vs);
             }
             __syncthreads();  // the sums have been read
         }
@@ -1091,8 +1091,8 @@ cudaError_t launch_rows(const Kv4Params &p, void *ws, cudaStream_t s) {
         return launch_wide<DP, T>(p, most, ws, s);
     } else {
         Attn a = p.a;
-        a.part = static_cast<float *>(ws);
-        return launch_attention_prompt_kv4(a, p.ks, p.vs, most, s);
+        a.part = static_cast<float *>(ws), a.out_scale = p.vs;
+        return launch_attention_prompt_kv4(a, p.ks, most, s);
     }
 }
 

@@ -133,7 +133,7 @@ struct PromptParams {
     int negate;     // scale < 0
     int out32;      // output rows lie on 32-byte boundaries
     int splits;     // of the key tiles of an item; more than one: parts for a second kernel
-    const float *ks, *vs;  // KV4: scales of the key-value heads, or NULL
+    const float *ks;  // KV4: scales of the key heads, or NULL (the value heads' are a.out_scale)
     int q_wide;            // KV4: query rows lie on 16-byte boundaries
 };
 
@@ -921,8 +921,8 @@ __global__ void __launch_bounds__(Cfg<DP, KV4>::THREADS, 1)
                 tc_fence_after();
             }
             const bool whole = p.splits == 1;
-            const float vs = KV4 && p.vs ? __ldg(p.vs + it.h / p.G) : 1.f;
-            const float inv = !whole ? vs : l > 0.f ? vs / l : l;  // (0 gives 0, NaN stays)
+            const float vs = KV4 && p.a.out_scale ? __ldg(p.a.out_scale + it.h / p.G) : 1.f;
+            const float inv = !whole ? 1.f : l > 0.f ? 1.f / l : l;  // (0 gives 0, NaN stays)
             const int head = it.h + (p.pair ? t : row & ((1 << p.packed) - 1));
             const size_t out_row = (size_t)(it.start + r) * p.a.H + head;
             __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) + out_row * p.a.D;
@@ -953,8 +953,9 @@ __global__ void __launch_bounds__(Cfg<DP, KV4>::THREADS, 1)
                     uint32_t w[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const float2 f = __fmul2_rn(make_float2(__uint_as_float(o[k][2 * i]), __uint_as_float(o[k][2 * i + 1])),
+                        float2 f = __fmul2_rn(make_float2(__uint_as_float(o[k][2 * i]), __uint_as_float(o[k][2 * i + 1])),
                                                     make_float2(inv, inv));
+                        if constexpr (KV4) f = __fmul2_rn(f, make_float2(vs, vs));
                         finite[i & 1] = __ffma2_rn(f, make_float2(0.f, 0.f), finite[i & 1]);
                         const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
                         w[i] = *reinterpret_cast<const uint32_t *>(&h);
@@ -962,9 +963,6 @@ __global__ void __launch_bounds__(Cfg<DP, KV4>::THREADS, 1)
                     if (finite[0].x + finite[0].y + finite[1].x + finite[1].y != 0.f) odd |= 1u << (c >> 5);
                     if (r >= it.len) continue;
                     if (!whole) {
-                        if constexpr (KV4)
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) o[k][i] = __float_as_uint(__uint_as_float(o[k][i]) * inv);
 #pragma unroll
                         for (int i = 0; i < 32; i += 8)
                             if (c + i < p.a.D) store32(part.o + c + i, &o[k][i]);
@@ -1081,11 +1079,11 @@ int packed_heads(int G, int max_q) {
 bool paired_heads(int G, int D, int packed) { return packed == 0 && D <= 128 && G % 2 == 0; }
 
 template <int DP, bool KV4>
-cudaError_t launch(const Attn &a, int min_rows, int splits, cudaStream_t s, const float *ks = nullptr, const float *vs = nullptr) {
+cudaError_t launch(const Attn &a, int min_rows, int splits, cudaStream_t s, const float *ks = nullptr) {
     using C = Cfg<DP, KV4>;
     PromptParams p{};
     p.a = a;
-    p.ks = ks, p.vs = vs;
+    p.ks = ks;
     p.q_wide = rows_aligned(a.q, a.qs, a.D, 2);
     p.G = a.H / a.HKV;
     p.min_rows = min_rows;
@@ -1192,11 +1190,11 @@ cudaError_t launch_attention_prompt(const Attn &a, int min_rows, cudaStream_t s)
     return launch<256, false>(a, min_rows, splits, s);
 }
 
-cudaError_t launch_attention_prompt_kv4(const Attn &a, const float *ks, const float *vs, int min_rows, cudaStream_t s) {
+cudaError_t launch_attention_prompt_kv4(const Attn &a, const float *ks, int min_rows, cudaStream_t s) {
     const int splits = prompt_splits(a.B, a.N, a.H, a.HKV, a.D, a.max_q, min_rows);
-    if (a.D <= 64) return launch<64, true>(a, min_rows, splits, s, ks, vs);
-    if (a.D <= 128) return launch<128, true>(a, min_rows, splits, s, ks, vs);
-    return launch<256, true>(a, min_rows, splits, s, ks, vs);
+    if (a.D <= 64) return launch<64, true>(a, min_rows, splits, s, ks);
+    if (a.D <= 128) return launch<128, true>(a, min_rows, splits, s, ks);
+    return launch<256, true>(a, min_rows, splits, s, ks);
 }
 
 }  // namespace gdn

@@ -47,6 +47,7 @@ struct Attn {
     float scale;
     float *part;  // parts of key splits (paged only): [N][H][splits][D], then [N][H][splits][2]
     size_t part_floats;
+    const float *out_scale;  // of the joined outputs of each key-value head, or NULL
 };
 
 // Whether base and row stride suit 16-byte accesses of every head's row.
@@ -95,7 +96,7 @@ struct Kv4Write {
 cudaError_t launch_kv4_write(const Kv4Write &p, int dtype, cudaStream_t s);
 
 // bf16 sequences of more than min_rows rows over a 4-bit cache.
-cudaError_t launch_attention_prompt_kv4(const Attn &a, const float *ks, const float *vs, int min_rows, cudaStream_t s);
+cudaError_t launch_attention_prompt_kv4(const Attn &a, const float *ks, int min_rows, cudaStream_t s);
 
 // Any rows; a.k and a.v are the 4-bit caches.
 size_t attention_kv4_workspace(int B, int N, int H, int HKV, int D, int max_q);
