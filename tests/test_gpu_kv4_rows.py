@@ -116,3 +116,18 @@ def test_hundreds_of_slices_without_keys(H, HKV, D):
             if kv[b] == 0:
                 assert bool((out[p["offsets"][b]:p["offsets"][b + 1]] == 0).all())
     kv4._check(p, out)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_write_keeps_zeros_where_units_are_denormal(dtype):
+    """Units below 2^-128, whose reciprocal leaves the range: zeros stay zeros, and values their nearest codes."""
+    x = torch.zeros(1, 1, 32, dtype=dtype)
+    x[0, 0, :3] = torch.tensor([2.0 ** -127, -2.0 ** -128, 2.0 ** -133])  # scale 2^-9, unit 2^-129
+    x[0, 0, 16:18] = torch.tensor([2.0 ** -118, -2.0 ** -125])            # an ordinary group: scale 0.6875
+    ts = torch.full((1,), 2.0 ** -120, device="cuda")
+    cache = [torch.zeros(1, 1, gdn.kv4_page_bytes(16, 32), dtype=torch.uint8, device="cuda") for _ in "kv"]
+    held, _ = gdn.gdn_kv4_write(x.cuda(), x.cuda(), torch.zeros(1, dtype=I32, device="cuda"), *cache, k_scale=ts, v_scale=ts, values=True)
+    held = held.cpu().double()
+    # 2^-127 and -2^-128 are 4 and -2 units, 2^-133 is nearest to none; of the other group 5.8 units and a 22nd of one
+    assert held[0, 0, :16].tolist() == [2.0 ** -127, -2.0 ** -128] + [0.0] * 14
+    assert held[0, 0, 16:].tolist() == [6 * 0.6875 * 2.0 ** -120] + [0.0] * 15

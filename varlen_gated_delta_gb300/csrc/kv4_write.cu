@@ -49,13 +49,15 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const Kv4Write p) {
     for (int j = 0; j < 16; ++j) amax = fmaxf(amax, fabsf(x[j]));  // (passes over NaN)
     float unit;
     const uint32_t byte = kv4_unit(amax, ts, unit);
-    const float r = unit > 0.f ? __fdiv_rn(1.f, unit) : 0.f;
+    // (the reciprocal of a unit below 2^-128 leaves the range: both factors of the quotient are moved by a power of two, which
+    // changes none of its bits otherwise)
+    const float up = unit < 0x1p-64f ? 0x1p64f : 1.f, r = unit > 0.f ? __fdiv_rn(1.f, unit * up) : 0.f;
     uint32_t code[2];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         float t[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) t[j] = __fmul_rn(x[half * 8 + j], r);
+        for (int j = 0; j < 8; ++j) t[j] = __fmul_rn(x[half * 8 + j] * up, r);
         code[half] = kv4_encode(t);
     }
     if (held) {
