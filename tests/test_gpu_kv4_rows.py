@@ -131,3 +131,24 @@ def test_write_keeps_zeros_where_units_are_denormal(dtype):
     # 2^-127 and -2^-128 are 4 and -2 units, 2^-133 is nearest to none; of the other group 5.8 units and a 22nd of one
     assert held[0, 0, :16].tolist() == [2.0 ** -127, -2.0 ** -128] + [0.0] * 14
     assert held[0, 0, 16:].tolist() == [6 * 0.6875 * 2.0 ** -120] + [0.0] * 15
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D", [48, 64, 128, 256])
+@pytest.mark.parametrize("M", [5, 400])
+def test_slices_give_the_same_bits_every_time(M, D, dtype):
+    """Short slices, a tile or two each, some without keys: what a CTA reads is not overwritten by its next item."""
+    H, HKV, ps, pages = 32, 1, 32, 200
+    new, kv = [67, 14, 83, 91, 128, 122, 94, 145, 79], [62, 14, 98, 91, 128, 0, 94, 145, 79]
+    gen = torch.Generator(device="cuda").manual_seed(D)
+    offsets = [0] + [sum(new[:i + 1]) for i in range(len(new))]
+    # scales from 2^-9 to 240: mostly one key of a row counts, and a wrong value of it shows
+    caches = [torch.randint(0, 120, (pages, HKV, gdn.kv4_page_bytes(ps, D)), dtype=torch.uint8, generator=gen, device="cuda") for _ in "kv"]
+    table = torch.randint(0, pages, (len(new), M), dtype=I32, generator=gen, device="cuda")
+    q = torch.randn(offsets[-1], H, D, generator=gen, device="cuda").to(dtype)
+    a = (q, *caches, table, torch.tensor(kv, dtype=I32, device="cuda"), torch.tensor(offsets, dtype=I32, device="cuda"))
+    want = gdn.gdn_attention_paged_kv4(*a, max_q=145)
+    differs = torch.zeros((), dtype=torch.bool, device="cuda")
+    for _ in range(300):
+        differs |= (gdn.gdn_attention_paged_kv4(*a, max_q=145) != want).any()
+    assert not bool(differs)

@@ -154,6 +154,14 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// A warp's one arrival that frees what its lanes have read from shared memory; `read` holds bits of all that a lane has read.
+// The lane that arrives follows from everybody's bits, so that the values have to be in registers before.  Behind a
+// __syncwarp alone loads were seen to come after the arrival, when the next copy had begun to overwrite the place.
+__device__ __forceinline__ void mbar_arrive_after(uint64_t *bar, uint32_t read) {
+    const unsigned who = __ballot_sync(0xffffffffu, read & 1) & 31;
+    if ((threadIdx.x & 31) == who) mbar_arrive(bar);
+}
+
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int x,
                                             int y, int z) {
     asm volatile(
@@ -205,6 +213,9 @@ struct Item {
     int end;      // rows of the last key tile that hold keys; a second pass adds kMend
     // Keys from here on are hidden from the item's first row.
     __device__ __forceinline__ int masked() const { return kv - len + row0 + 1; }
+    __device__ __forceinline__ uint32_t bits() const {
+        return (uint32_t)(b ^ h ^ start ^ len ^ kv ^ row0 ^ split ^ lo ^ n[0] ^ n[1] ^ tiles ^ end);
+    }
     // Whether V tile j has rows to change before they are used: past the last key, and in a second pass
     // those that are hidden from some row.
     __device__ __forceinline__ bool changes_v(int j, int BN) const {
@@ -423,6 +434,12 @@ struct RawTile {
             }
         }
     }
+    __device__ __forceinline__ uint32_t bits() const {
+        uint32_t x = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) x ^= codes[i].x ^ codes[i].y ^ scale[i];
+        return x;
+    }
     // To fp16.  Groups of the upper 64 channels of 128 begin with their second half: 16 bytes of eight lanes then lie in different
     // banks.
     __device__ __forceinline__ void store(unsigned char *slot, int tid) const {
@@ -529,15 +546,11 @@ __global__ void __launch_bounds__(Cfg<DP, KV4>::THREADS, 1)
     it.n[1] = 0;
     // Items come from the load warp through a ring of four; false past the last one.
     uint32_t n_item = 0;
-    auto release_item = [&](uint32_t k) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(item_empty + k);
-    };
     auto next_item = [&](bool release = true) {
         const uint32_t k = n_item & 3;
         if (!wait_or_abort(item_full + k, (n_item >> 2) & 1, abort)) return false;
         it = s_item[k];
-        if (release || it.b < 0) release_item(k);
+        if (release || it.b < 0) mbar_arrive_after(item_empty + k, it.bits());
         ++n_item;
         return it.b >= 0;
     };
@@ -570,8 +583,7 @@ __global__ void __launch_bounds__(Cfg<DP, KV4>::THREADS, 1)
                         if (!wait_or_abort(raw_full + r, (seq / C::RAWS) & 1, abort)) goto done;
                         RawTile<DP> raw;
                         raw.load(p.a.D, raws + r * C::RAW, s_there[r], ctid);
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(raw_empty + r);
+                        mbar_arrive_after(raw_empty + r, raw.bits());
                         if (!wait_or_abort(empty + slot, phase_of(seq) ^ 1, abort)) goto done;
                         raw.store(ring + slot * C::SLOT, ctid);
                         fence_async_smem();
@@ -811,10 +823,11 @@ __global__ void __launch_bounds__(Cfg<DP, KV4>::THREADS, 1)
             if constexpr (KV4) {
                 const uint32_t k = (n_item - 1) & 3;
                 if (!wait_or_abort(f_full + k, ((n_item - 1) >> 2) & 1, abort)) goto done;
-                pc = n > 0 ? kv4_row_factor(p.c, inverses[(k * 2 + t) * 128 + row], p.ks ? __ldg(p.ks + it.h / p.G) : 1.f) : 1.f;
+                const float inverse = inverses[(k * 2 + t) * 128 + row];
+                pc = n > 0 ? kv4_row_factor(p.c, inverse, p.ks ? __ldg(p.ks + it.h / p.G) : 1.f) : 1.f;
                 // (not before: items without keys hold nobody up, and the inverses of the fourth item after this one may be
                 // ready before a late warp has looked at these)
-                release_item(k);
+                mbar_arrive_after(item_empty + k, it.bits() ^ __float_as_uint(inverse) >> 23);
             }
             for (int j = 0; j < it.tiles; ++j) {
                 if (j >= n) {  // only the other query tile sees these keys
