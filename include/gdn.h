@@ -762,7 +762,9 @@ GDN_API size_t gdn_beam_select_workspace_bytes(int G, int K, int V, int n);
  *   row_bytes  their rows' bytes (a host array)
  *   parents    [B] int32 on the device; a row whose parent lies outside [0, B)
  *              keeps its content
- * Requires count <= 64 and B <= 4096; the states do not overlap.
+ * Requires count <= 64 and B <= 4096; the states do not overlap.  Rows that take
+ * another's content while theirs goes elsewhere move in strips of 64 KB / B:
+ * beyond some 1000 rows that is well below the memory's rate.
  */
 GDN_API int gdn_state_reorder(void *const *states, const int64_t *row_bytes, int count,
                               const int32_t *parents, int B, void *stream);
@@ -831,7 +833,7 @@ GDN_API size_t gdn_page_compact_workspace_bytes(int num_pages);
  *   page_bytes  bytes of a page of each (a host array)
  *   copies      [n, 2] int32 on the device: (from, to); pairs outside the pool
  *               (-1) are skipped.  No page is written that another pair reads or
- *               writes.
+ *               writes, and the caches do not overlap.
  * Requires count <= 128, page_bytes <= 2^32.
  */
 GDN_API int gdn_page_copy(void *const *caches, const int64_t *page_bytes, int count,

@@ -47,13 +47,15 @@
 // slots 44%), they wait for tensor memory and for each other.  32 x U[1, 512], 32 heads on
 // 8: 54 us, bound by the chain of one or two key tiles an item.
 //
-// Over a 4-bit cache (KV4) the load warp copies codes and scales to a ring of two tiles, and a fourth warpgroup turns them, and
-// the queries, into fp16 tiles where the other instance's loads put bf16 ones.  4 x 512 tokens over 8192, 32 heads of
-// 128 on 8: 224 us, 1190 TFLOP/s (tensor pipe 60% active); 256 items on 152 SMs leave a sixth of the time to the second round.  Steps:
-// codes go to registers before the first is converted, which frees their place in the ring for the next copy, and a lane's
-// places lie in different banks (286 -> 253 us); whole tiles take loads and stores at fixed offsets (253 -> 224).  Loading codes
-// into registers a tile ahead from global memory took 1393 (page lookups and divisions in the converting warps).  176 and 192 registers
-// to a softmax thread instead of 184: 239 us against 224, and 275 against 253 a step earlier.
+// Over a 4-bit cache (KV4) the load warp copies codes and scales to a ring of two tiles, and a fourth warpgroup turns them,
+// and the queries, into fp16 tiles where the other instance's loads put bf16 ones.  4 x 512 tokens over 8192, 32 heads of
+// 128 on 8: 231 us, 1150 TFLOP/s (tensor pipe 58% active); 256 items on 152 SMs leave a sixth of the time to the second
+// round.  Steps: codes go to registers before the first is converted, which frees their place in the ring for the next copy,
+// and a lane's places lie in different banks (286 -> 253 us); whole tiles take loads and stores at fixed offsets (253 -> 224).
+// Loading codes into registers a tile ahead from global memory took 1393 (page lookups and divisions in the converting warps).
+// 176 and 192 registers to a softmax thread instead of 184: 239 us against 224, and 275 against 253 a step earlier.  Taking the
+// row's reference off the scores before the product with their factor costs 2 us, arrivals that follow from what was
+// read (mbar_arrive_after) 5.
 #include <algorithm>
 #include <cmath>
 #include <exception>
@@ -890,7 +892,7 @@ __global__ void __launch_bounds__(Cfg<DP, KV4>::THREADS, 1)
                     tmem_wait_st();
                 }
                 // KV4 takes the reference off first: all exponents of a row share the rounding of m pc, and where that is large
-                // (scores from 2^24 on) fp16 has no room for it (223 -> 226 us)
+                // (scores from 2^24 on) fp16 has no room for it
                 const float mc = KV4 ? kKv4Shift : m == -INFINITY ? 0.f : -m * pc, base = m == -INFINITY ? 0.f : -m;
                 float2 sum = make_float2(0.f, 0.f);
 #pragma unroll

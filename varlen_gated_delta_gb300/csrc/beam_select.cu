@@ -4,12 +4,12 @@
 // and of a group's K V totals the n largest.  Of equal ones the lowest beam comes first, within a beam the largest logit (a
 // score of -1e30 leaves nothing of the logits in 64 bits), then the lowest token.  The logits are read once, in two launches.
 //
-// The first gives a CTA a span of a row, which it goes through in pieces that fit its registers, with a reference m, the
-// sum of exp(x - m), and the n largest logits so far.  In a first piece (with at least n values above -inf, else in the next too) the threads form groups whose maxima are at hand: at
-// least n values reach the n-th largest of them, and few more do (n = 8 of 32 groups: some 9 of 16384 values).  Later
-// pieces have few values above the n-th largest so far.  Those go into a list and are ranked by counting, together with
-// the ones before.  A list that overflows (equal or rising logits) is left for n rounds of the CTA-wide largest value
-// below the last one.
+// The first gives a CTA a span of a row, which it goes through in pieces that fit its registers, with the largest logit m, the
+// sum of exp(x - m), and the n largest logits so far.  In a first piece (with at least n values above -inf, else in the
+// next too) the threads form groups whose maxima are at hand: at least n values reach the n-th largest of them, and few
+// more do (n = 8 of 32 groups: some 9 of 16384 values).  Later pieces have few values above the n-th largest so far.  Those
+// go into a list and are ranked by counting, together with the ones before.  A list that overflows (equal or rising
+// logits) is left for n rounds of the CTA-wide largest value below the last one.
 //
 // The second, a CTA to a group of beams, joins the spans' sums, and takes the n best of their candidates the
 // same way.  Totals and their comparison are in 64 bits: only the error of the row's sum (fp32 terms, a thread's of a
@@ -17,7 +17,7 @@
 // the sum is off by at most 4e-8 where no few terms dominate (normal logits of deviation 0.5 and 1, 1000 to 200000 of
 // them; most of it the same for all rows), and by at most 4.9e-7 where one does.
 //
-// 64 x 8 beams of 131072 bf16 logits, a tenth of the beams at their end: 45 us, 2.7 TB/s.  Reading is not what bounds it: 20
+// 64 x 8 beams of 131072 bf16 logits, a tenth of the beams at their end: 46 us, 2.6 TB/s.  Reading is not what bounds it: 20
 // million warp instructions at two a clock (two fifths of them exponentials and the conversions before them), and warps that wait
 // for a piece's ranking.  One launch's pieces without the next one's loads in flight: 55 us; one piece to a CTA: 57.
 // One group of 4 x 32768: 9 us, two launches and chains of dependent steps.

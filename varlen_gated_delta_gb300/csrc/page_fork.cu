@@ -8,9 +8,9 @@
 // each: a thread-block cluster, whose barrier parts the steps (one CTA for small pools).  Order comes from
 // page numbers and row numbers alone, so results do not depend on timing.
 //
-// 64 x 4 rows of up to 4096 tokens in pages of 64: the plan of a fork takes some 16 us (launch, four cluster barriers, ten dependent
-// loads; 28 with a cluster of four, 48 in one CTA, copies included), the copies of its last pages 8; a compaction's plan
-// 19, its copies 51 (350 MB at 6.8 TB/s, the measured copy's rate).
+// 64 x 4 rows of up to 4096 tokens in pages of 64: the plan of a fork takes some 15 us (launch, four cluster barriers, ten
+// dependent loads; 28 with a cluster of four, 48 in one CTA, copies included), the copies of its last pages 8; a compaction's
+// plan 15 (19 before its copies), its copies 51 (350 MB at 6.8 TB/s, the measured copy's rate).
 #include <cooperative_groups.h>
 
 #include <algorithm>
