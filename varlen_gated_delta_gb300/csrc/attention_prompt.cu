@@ -552,7 +552,9 @@ __global__ void __launch_bounds__(Cfg<DP, KV4>::THREADS, 1)
         const uint32_t k = n_item & 3;
         if (!wait_or_abort(item_full + k, (n_item >> 2) & 1, abort)) return false;
         it = s_item[k];
-        if (release || it.b < 0) mbar_arrive_after(item_empty + k, it.bits());
+        __syncwarp();
+        // (all lanes have read the same words)
+        if ((release || it.b < 0) && lane == (int)(it.bits() & 31)) mbar_arrive(item_empty + k);
         ++n_item;
         return it.b >= 0;
     };
